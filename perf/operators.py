@@ -192,7 +192,7 @@ def _codes(x):
     g = x.reshape(*x.shape[:-1], -1, GROUP)
     low, high = g.amin(-1, keepdim=True), g.amax(-1, keepdim=True)
     m = low.bfloat16().float()
-    s = ((high - m) / torch.full_like(m, 15.0)).bfloat16().float()
+    s = ((high - m).clamp(min=0) / torch.full_like(m, 15.0)).bfloat16().float()
     bad = ~(torch.isfinite(s) & torch.isfinite(m))
     c = torch.where(bad | (s == 0), torch.zeros_like(g), ((g - m) / s).round().clamp(0, 15))
     nan = torch.full_like(s, math.nan)
@@ -460,7 +460,7 @@ def _exact_quantised(x):
     for a in range(0, dim, GROUP):
         part = x[:, :, a:a + GROUP]
         m = part.min(2, keepdim=True).values.to(torch.bfloat16).double()
-        s = ((part.max(2, keepdim=True).values - m) / 15).to(torch.bfloat16).double()
+        s = ((part.max(2, keepdim=True).values - m).clamp(min=0) / 15).to(torch.bfloat16).double()
         step = torch.where(s > 0, s, torch.ones_like(s))
         y[:, :, a:a + GROUP] = m + s * torch.round((part - m) / step).clamp(0, 15)
     return y
