@@ -50,7 +50,8 @@ typedef enum clef_status {
     CLEF_ERR_UNSUPPORTED_CONFIG = 3, /* shape outside what the kernels handle (see clef_config) */
     CLEF_ERR_CUDA = 4,               /* a CUDA runtime call or launch failed */
     CLEF_ERR_DEVICE_BOUNDS = 5,      /* a kernel met an out-of-range index (a token id) and skipped it */
-    CLEF_ERR_DEVICE_TIMEOUT = 6      /* a kernel's bounded wait ran out; it stopped and returned */
+    CLEF_ERR_DEVICE_TIMEOUT = 6,     /* a kernel's bounded wait ran out; it stopped and returned */
+    CLEF_ERR_NO_PAGES = 7            /* a cache plan asked for more pages than are free (clef_cache.h) */
 } clef_status;
 
 /* Head hyper-parameters: the joint_head_config.json fields of "Dissecting the

@@ -15,15 +15,19 @@ CLEF_OK = 0
 STATUS = {
     0: "CLEF_OK", 1: "CLEF_ERR_INVALID_ARGUMENT", 2: "CLEF_ERR_WORKSPACE_TOO_SMALL",
     3: "CLEF_ERR_UNSUPPORTED_CONFIG", 4: "CLEF_ERR_CUDA", 5: "CLEF_ERR_DEVICE_BOUNDS",
-    6: "CLEF_ERR_DEVICE_TIMEOUT",
+    6: "CLEF_ERR_DEVICE_TIMEOUT", 7: "CLEF_ERR_NO_PAGES",
 }
 EXPORTED = [
     "clef_weight_count", "clef_prepared_size", "clef_prepare_weights", "clef_workspace_size",
     "clef_head_forward", "clef_device_status", "clef_span_sums", "clef_gemm_bf16",
     "clef_kernel_launches", "clef_status_string", "clef_span_sums_noalloc", "clef_stream_begin",
     "clef_stream_rows", "clef_stream_finish", "clef_selftest_wait_timeout", "clef_stream_rows_f16",
-    "clef_stream_finish_f16",
+    "clef_stream_finish_f16", "clef_cache_size", "clef_cache_plan", "clef_cache_append", "clef_cache_read",
+    "clef_cache_attend_workspace", "clef_cache_attend", "clef_cache_status", "clef_memory_store",
+    "clef_stream_finish_memory",
 ]
+BF16, FP16, FP32 = 0, 1, 2   # clef_dtype
+CACHE_MAX_REQUESTS = 1024
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
@@ -50,6 +54,10 @@ class ClefDebugOutputs(ctypes.Structure):
                 ("option_final", _vp), ("field_final", _vp), ("events", _vp * 8), ("timeline", _vp),
                 ("timeline_len", _i32), ("timeline_count", _vp), ("tail_mode", _i32), ("row_mu", _vp),
                 ("row_rstd", _vp)]
+
+
+class ClefCache(ctypes.Structure):
+    _fields_ = [("data", _vp), ("n_pages", _i32), ("page", _i32), ("heads", _i32), ("head_dim", _i32)]
 
 
 _lib = None
@@ -88,6 +96,21 @@ def load():
     lib.clef_kernel_launches.restype = ctypes.c_uint64
     lib.clef_status_string.argtypes = [ctypes.c_int]
     lib.clef_status_string.restype = ctypes.c_char_p
+    cache = ctypes.POINTER(ClefCache)
+    lib.clef_cache_size.argtypes = [cache, ctypes.POINTER(_sz)]
+    lib.clef_cache_plan.argtypes = [cache, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp]
+    lib.clef_cache_append.argtypes = [cache, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp]
+    lib.clef_cache_read.argtypes = [cache, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
+    lib.clef_cache_attend_workspace.argtypes = [cache, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]
+    lib.clef_cache_attend.argtypes = [cache, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i32,
+                                      _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.clef_cache_status.argtypes = [_vp, _vp]
+    lib.clef_memory_store.argtypes = [ctypes.POINTER(ClefConfig), ctypes.POINTER(ClefSchema), _i32, _i32, _i32, _vp, _sz,
+                                      cache, _vp, _vp, _vp]
+    lib.clef_stream_finish_memory.argtypes = [ctypes.POINTER(ClefConfig), ctypes.POINTER(_vp), _vp,
+                                              ctypes.POINTER(ClefSchema), _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _vp, _vp, _sz, cache, _vp, _i32, _vp, _vp, _sz,
+                                              ctypes.POINTER(ClefDebugOutputs), _vp]
     for name in EXPORTED:
         if name not in ("clef_weight_count", "clef_status_string", "clef_kernel_launches"):
             getattr(lib, name).restype = ctypes.c_int
@@ -237,3 +260,70 @@ def clef_span_sums_noalloc(cfg, schema: Schema, hidden_ptr, token_ids_ptr, lexic
 def clef_gemm_bf16(A_ptr, lda, B_ptr, ldb, bias_ptr, C_ptr, ldc, M, N, K, flags_ptr, stream=0):
     _check(load().clef_gemm_bf16(A_ptr, lda, B_ptr, ldb, bias_ptr, C_ptr, ldc, M, N, K, flags_ptr, stream),
            "clef_gemm_bf16")
+
+
+def clef_cache_size(cache: ClefCache):
+    out = _sz(0)
+    _check(load().clef_cache_size(ctypes.byref(cache), ctypes.byref(out)), "clef_cache_size")
+    return out.value
+
+
+def clef_cache_plan(cache: ClefCache, B, lengths_ptr, want_ptr, block_table_ptr, table_stride, free_pages_ptr,
+                    free_count_ptr, cu_new_ptr, slots_ptr, n_slots, flags_ptr, stream=0):
+    _check(load().clef_cache_plan(cache, B, lengths_ptr, want_ptr, block_table_ptr, table_stride, free_pages_ptr,
+                                  free_count_ptr, cu_new_ptr, slots_ptr, n_slots, flags_ptr, stream), "clef_cache_plan")
+
+
+def clef_cache_append(cache: ClefCache, n_tokens, head0, n_heads, dtype, k_ptr, k_row_stride, k_head_stride, v_ptr,
+                      v_row_stride, v_head_stride, slots_ptr, flags_ptr, stream=0):
+    _check(load().clef_cache_append(cache, n_tokens, head0, n_heads, dtype, k_ptr, k_row_stride, k_head_stride, v_ptr,
+                                    v_row_stride, v_head_stride, slots_ptr, flags_ptr, stream), "clef_cache_append")
+
+
+def clef_cache_read(cache: ClefCache, n_tokens, head0, n_heads, dtype, slots_ptr, k_ptr, v_ptr, flags_ptr, stream=0):
+    _check(load().clef_cache_read(cache, n_tokens, head0, n_heads, dtype, slots_ptr, k_ptr, v_ptr, flags_ptr, stream),
+           "clef_cache_read")
+
+
+def clef_cache_attend_workspace(cache: ClefCache, B, total_q, q_heads, max_length):
+    out = _sz(0)
+    _check(load().clef_cache_attend_workspace(cache, B, total_q, q_heads, max_length, ctypes.byref(out)),
+           "clef_cache_attend_workspace")
+    return out.value
+
+
+def clef_cache_attend(cache: ClefCache, B, total_q, max_q, q_heads, head0, kv_heads, dtype, q_ptr, q_row_stride,
+                      q_head_stride, cu_q_ptr, block_table_ptr, table_stride, lengths_ptr, scale, causal, out_ptr,
+                      lse_ptr, flags_ptr, workspace_ptr, workspace_bytes, stream=0):
+    _check(load().clef_cache_attend(cache, B, total_q, max_q, q_heads, head0, kv_heads, dtype, q_ptr, q_row_stride,
+                                    q_head_stride, cu_q_ptr, block_table_ptr, table_stride, lengths_ptr, scale, causal,
+                                    out_ptr, lse_ptr, flags_ptr, workspace_ptr, workspace_bytes, stream),
+           "clef_cache_attend")
+
+
+def clef_cache_status(flags_ptr, stream=0):
+    return load().clef_cache_status(flags_ptr, stream)
+
+
+def clef_memory_store(cfg, schema: Schema, record, row0, n_rows, workspace_ptr, workspace_bytes, cache: ClefCache,
+                      slots_ptr, flags_ptr, stream=0):
+    _check(load().clef_memory_store(ctypes.byref(cfg), ctypes.byref(schema.struct), record, row0, n_rows, workspace_ptr,
+                                    workspace_bytes, ctypes.byref(cache), slots_ptr, flags_ptr, stream),
+           "clef_memory_store")
+
+
+def clef_stream_finish_memory(cfg, weight_ptrs, prepared_ptr, schema: Schema, first_row, hidden_ptr, hidden_dtype,
+                              token_ids_ptr, lexical_ptr, logits_ptr, probs_ptr, q_value_ptr, q_conf_ptr, q_argmax_ptr,
+                              workspace_ptr, workspace_bytes, cache: ClefCache, block_table_ptr, table_stride, flags_ptr,
+                              attend_workspace_ptr, attend_workspace_bytes, debug=None, stream=0):
+    arr = (_vp * len(weight_ptrs))(*weight_ptrs)
+    dbg = ctypes.byref(debug) if debug is not None else None
+    first = np.ascontiguousarray(first_row, dtype=np.int32)
+    if first.shape != (schema.B,):
+        raise ClefError(1, "clef_stream_finish_memory")
+    _check(load().clef_stream_finish_memory(ctypes.byref(cfg), arr, prepared_ptr, ctypes.byref(schema.struct),
+                                            first.ctypes.data, hidden_ptr, hidden_dtype, token_ids_ptr, lexical_ptr,
+                                            logits_ptr, probs_ptr, q_value_ptr, q_conf_ptr, q_argmax_ptr, workspace_ptr,
+                                            workspace_bytes, ctypes.byref(cache), block_table_ptr, table_stride,
+                                            flags_ptr, attend_workspace_ptr, attend_workspace_bytes, dbg, stream),
+           "clef_stream_finish_memory")

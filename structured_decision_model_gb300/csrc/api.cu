@@ -6,6 +6,7 @@
 #include <mutex>
 #include <vector>
 
+#include "../../include/clef_cache.h"
 #include "../../include/clef_head.h"
 #include "common.cuh"
 #include "head_kernels.h"
@@ -503,6 +504,7 @@ const char* clef_status_string(int s) {
         case CLEF_ERR_CUDA: return "CUDA error";
         case CLEF_ERR_DEVICE_BOUNDS: return "device-side index out of range";
         case CLEF_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
+        case CLEF_ERR_NO_PAGES: return "no free cache pages left";
         default: return "unknown status";
     }
 }
@@ -585,7 +587,17 @@ int clef_workspace_size(const clef_config* cfg, const clef_schema* schema, size_
 
 namespace {
 
-enum ForwardMode { kForwardFull = 0, kForwardAfterStream = 1 };
+enum ForwardMode { kForwardFull = 0, kForwardAfterStream = 1, kForwardMemory = 2 };
+
+// Kept memory of kForwardMemory: the routing attention reads it instead of the workspace's K/V.
+struct MemoryArgs {
+    const clef_cache* cache;
+    const int32_t* block_table;
+    int32_t table_stride;
+    int32_t* flags;
+    void* ws;
+    size_t ws_bytes;
+};
 
 // The per-record tail (option LayerNorm to softmax) has two implementations.  The
 // batched chain runs every projection as one GEMM over the whole batch, so each weight
@@ -625,13 +637,15 @@ int finish_debug(const clef_debug_outputs* debug, int n_launch, int Q, int O, in
 // The forward pass.  kForwardFull uploads the plan and computes the memory statistics
 // and K/V itself; kForwardAfterStream finds both already in the workspace (put there by
 // clef_stream_begin / clef_stream_rows) and only zeroes the records' round-up slack rows.
+// kForwardMemory finds the plan and the statistics of the pooled rows there and reads K/V
+// from the 4-bit cache.
 int forward_impl(const clef_config* cfg, const void* const* weights, const void* prepared,
                  const clef_schema* schema, const uint16_t* hidden, const int32_t* token_ids,
                  const uint16_t* lexical, float* logits, float* probs, float* q_value, float* q_conf,
                  int32_t* q_argmax, void* workspace, size_t workspace_bytes, const clef_debug_outputs* debug,
-                 void* stream, int mode, bool hidden_f16 = false) {
+                 void* stream, int mode, bool hidden_f16 = false, const MemoryArgs* mem = nullptr) {
     if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
-    if (hidden_f16 && mode != kForwardAfterStream) return CLEF_ERR_INVALID_ARGUMENT;
+    if (hidden_f16 && mode == kForwardFull) return CLEF_ERR_INVALID_ARGUMENT;
     if (!weights || !prepared || !hidden || !token_ids || !lexical || !logits || !probs || !q_value || !q_conf ||
         !q_argmax || !workspace)
         return CLEF_ERR_INVALID_ARGUMENT;
@@ -704,7 +718,9 @@ int forward_impl(const clef_config* cfg, const void* const* weights, const void*
     // 1. memory K/V of every routing layer (LayerNorm folded), real rows only; the
     // projection also writes the memory row statistics that pooling applies the memory
     // LayerNorm through
-    if (mode == kForwardAfterStream) {
+    if (mode == kForwardMemory) {
+        // nothing to project: the streamed rows' statistics are in place, K/V in the cache
+    } else if (mode == kForwardAfterStream) {
         // K/V rows and statistics came in chunk by chunk; the round-up slack rows of each
         // record were never written, and attention reads whole tiles, so they are zeroed here
         CK(launch_zero_slack(kv, NKV, T(p.rec_row_off), T(p.lengths), B, st)); CK(tick());
@@ -766,9 +782,19 @@ int forward_impl(const clef_config* cfg, const void* const* weights, const void*
         ra.k_col = 2 * l * D;
         ra.v_col = (2 * l + 1) * D;
         if (l == 0) CK(mark(debug, 2, st));
-        CK(launch_route_attn_partial(ra, O, st)); CK(tick());
-        if (l == 0) CK(mark(debug, 3, st));
-        CK(launch_route_attn_merge(ra, O, st)); CK(tick());
+        if (mem) {
+            const int s = clef_cache_attend(mem->cache, B, O, p.max_rec_options, cfg->heads, l * cfg->heads, cfg->heads,
+                                            CLEF_BF16, q_buf, D, 64, T(p.rec_o_off), mem->block_table,
+                                            mem->table_stride, T(p.lengths), 0.125f, 0, attn_buf, nullptr, mem->flags,
+                                            mem->ws, mem->ws_bytes, stream);
+            if (s != CLEF_OK) return s;
+            CK(tick());
+            if (l == 0) CK(mark(debug, 3, st));
+        } else {
+            CK(launch_route_attn_partial(ra, O, st)); CK(tick());
+            if (l == 0) CK(mark(debug, 3, st));
+            CK(launch_route_attn_merge(ra, O, st)); CK(tick());
+        }
         CK(dense_partial(attn_buf, D, O, W(weights, wi.route(l, 8)), D, D, part, flags, st, &splits)); CK(tick());
         CK(ln_acc(o_res, O, splits, W(weights, wi.route(l, 9)), true, W(weights, wi.route(l, 10)),
                   W(weights, wi.route(l, 11)), ln_buf, nullptr)); CK(tick());
@@ -981,6 +1007,78 @@ int clef_stream_finish_f16(const clef_config* cfg, const void* const* weights, c
                            const clef_debug_outputs* debug, void* stream) {
     return forward_impl(cfg, weights, prepared, schema, hidden, token_ids, lexical, logits, probs, q_value, q_conf,
                         q_argmax, workspace, workspace_bytes, debug, stream, kForwardAfterStream, true);
+}
+
+namespace {
+
+// A cache that holds this head's memory: every routing layer's heads side by side.
+bool memory_cache_fits(const clef_config* cfg, const clef_cache* c) {
+    return c && c->head_dim == 64 && c->heads == cfg->n_route * cfg->heads;
+}
+
+}  // namespace
+
+int clef_memory_store(const clef_config* cfg, const clef_schema* schema, int32_t record, int32_t row0, int32_t n_rows,
+                      const void* workspace, size_t workspace_bytes, const clef_cache* cache, const int32_t* slots,
+                      int32_t* flags, void* stream) {
+    if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || !memory_cache_fits(cfg, cache) || !slots || !flags)
+        return CLEF_ERR_INVALID_ARGUMENT;
+    const Plan* pp = nullptr;
+    const WsLayout* lp = nullptr;
+    const int v = cached_plan(cfg, schema, &pp, &lp);
+    if (v != CLEF_OK) return v;
+    if (record < 0 || record >= schema->B || row0 < 0 || n_rows < 1 ||
+        int64_t(row0) + n_rows > schema->lengths[record])
+        return CLEF_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < lp->total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+    const int64_t D = cfg->width, NKV = 2 * cfg->n_route * D;
+    const int64_t row = pp->blob[pp->rec_row_off + record] + int64_t(row0);
+    const uint16_t* kv = reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(workspace) + lp->kv) + row * NKV;
+    for (int l = 0; l < cfg->n_route; ++l) {
+        const int s = clef_cache_append(cache, n_rows, l * cfg->heads, cfg->heads, CLEF_BF16, kv + 2 * l * D, NKV, 64,
+                                        kv + (2 * l + 1) * D, NKV, 64, slots, flags, stream);
+        if (s != CLEF_OK) return s;
+    }
+    return CLEF_OK;
+}
+
+int clef_stream_finish_memory(const clef_config* cfg, const void* const* weights, const void* prepared,
+                              const clef_schema* schema, const int32_t* first_row, const void* hidden,
+                              int32_t hidden_dtype, const int32_t* token_ids, const uint16_t* lexical, float* logits,
+                              float* probs, float* q_value, float* q_conf, int32_t* q_argmax, void* workspace,
+                              size_t workspace_bytes, const clef_cache* cache, const int32_t* block_table,
+                              int32_t table_stride, int32_t* flags, void* attend_workspace,
+                              size_t attend_workspace_bytes, const clef_debug_outputs* debug, void* stream) {
+    if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    if (!first_row || (hidden_dtype != CLEF_BF16 && hidden_dtype != CLEF_FP16) || !memory_cache_fits(cfg, cache) ||
+        !cache->data || (reinterpret_cast<uintptr_t>(cache->data) & 255) || !block_table || !flags || table_stride < 1 ||
+        (reinterpret_cast<uintptr_t>(attend_workspace) & 255))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    const Plan* pp = nullptr;
+    const WsLayout* lp = nullptr;
+    int v = cached_plan(cfg, schema, &pp, &lp);
+    if (v != CLEF_OK) return v;
+    if (schema->B > CLEF_CACHE_MAX_REQUESTS) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    for (int b = 0; b < schema->B; ++b)
+        if (first_row[b] < 0 || first_row[b] >= schema->lengths[b] ||
+            schema->lengths[b] > int64_t(table_stride) * cache->page)
+            return CLEF_ERR_INVALID_ARGUMENT;
+    for (int q = 0; q < schema->Q; ++q) {
+        const int from = first_row[schema->q_rec[q]];
+        if (schema->q_span[2 * q] < from) return CLEF_ERR_INVALID_ARGUMENT;
+        for (int j = schema->q_opt_off[q]; j < schema->q_opt_off[q + 1]; ++j)
+            if (schema->o_span[2 * j] < from) return CLEF_ERR_INVALID_ARGUMENT;
+    }
+    size_t need = 0;
+    v = clef_cache_attend_workspace(cache, schema->B, pp->O, cfg->heads, table_stride * cache->page, &need);
+    if (v != CLEF_OK) return v;
+    if (need > 0 && !attend_workspace) return CLEF_ERR_INVALID_ARGUMENT;
+    if (attend_workspace_bytes < need) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+    const MemoryArgs mem{cache, block_table, table_stride, flags, attend_workspace, attend_workspace_bytes};
+    return forward_impl(cfg, weights, prepared, schema, static_cast<const uint16_t*>(hidden), token_ids, lexical, logits,
+                        probs, q_value, q_conf, q_argmax, workspace, workspace_bytes, debug, stream, kForwardMemory,
+                        hidden_dtype == CLEF_FP16, &mem);
 }
 
 int clef_device_status(void* workspace, void* stream) {

@@ -1,0 +1,66 @@
+// Launchers of the 4-bit memory cache's kernels (internal to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace clef {
+
+constexpr int kCacheMaxRequests = 1024;
+constexpr int kFlagPages = 1 << 2;  // flags bit beside those of common.cuh: the free pages ran out
+constexpr int kPiece = 1152;  // bytes of 16 tokens, 64 values: key codes, value codes, scales and minima
+
+// A cache as the kernels see it.
+struct CacheView {
+    uint8_t* data;
+    int n_pages, page, page_shift;  // tokens a page and its logarithm
+    int heads, groups;              // head size / 64
+};
+
+struct CachePlanArgs {
+    int B, n_pages, page_shift, width, n_slots;
+    int32_t* lengths; const int32_t* want; int32_t* table; int32_t* free_pages; int32_t* free_count;
+    int32_t* cu; int32_t* slots; int32_t* flags;
+};
+
+struct CacheRowsArgs {
+    CacheView c;
+    int n_tokens, head0, n_heads, dtype;
+    const void* k; int64_t k_row, k_head;  // strides in elements
+    const void* v; int64_t v_row, v_head;
+    void* out_k; void* out_v;              // read back
+    const int32_t* slots; int32_t* flags;
+};
+
+struct CacheAttendArgs {
+    CacheView c;
+    int B, total_q, max_q, q_heads, head0, kv_heads, share, dtype, width, causal;
+    const void* q; int64_t q_row, q_head;
+    const int32_t* cu_q; const int32_t* table; const int32_t* lengths;
+    float scale_log2;
+    void* out; float* lse; int32_t* flags;
+    float* part_o; float* part_lse; int32_t* part_off;  // split partials, their row offset per request
+    int64_t part_rows;  // partial rows that the workspace holds
+    int max_chunks;
+};
+
+// Keys of one split of a request's memory: a function of the request's length alone, so that
+// a row's result does not depend on the batch.
+__host__ __device__ inline int attend_chunk(int len) {
+    const int c = (len / 64 + 15) & ~15;
+    return c < 256 ? 256 : c > 1024 ? 1024 : c;
+}
+// Upper bound of the splits of any request of at most max_len keys.
+inline int64_t attend_max_chunks(int64_t max_len) {
+    const int64_t short_chunks = (max_len + 255) / 256, long_chunks = (max_len + 1023) / 1024;
+    return short_chunks <= 66 ? short_chunks : long_chunks > 66 ? long_chunks : 66;
+}
+
+cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t s);
+cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s);
+
+
+}  // namespace clef

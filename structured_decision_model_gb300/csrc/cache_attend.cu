@@ -1,0 +1,546 @@
+// Attention over the paged 4-bit memory cache (clef_cache_attend).
+//
+// A warp takes one item: a split of a request's keys, one key/value head, and up to 8 NT
+// query rows of the heads that share it.  The products run transposed on mma.sync, the keys
+// as the M dimension: S^T = K Q^T (16 keys x 8 queries an instruction, so that a single
+// token wastes 7 of 8 columns rather than 15 of 16 rows) and O^T += V^T P^T.  The A operand
+// of both is made in registers from the codes: the stored order gives each lane its own 16
+// bytes of a 16-token piece.
+//   Keys: a 4-bit code in bits 0-3 of an fp16 word is the subnormal c 2^-24, exact, and in
+// bits 4-7 c 2^-20, so one AND makes two operand values; the 2^4 between the two halves of
+// a run of 16 is taken out of the queries instead.  The score is then, in fp32,
+//   s_t (q . c_t) + m_t (sum q),  with s_t and m_t the key's scale and minimum.
+// Queries are scaled by a power of two per row to fill fp16's range (exact).
+//   Values: o = sum_t p_t (s_t c_t + m_t) = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t).
+// The weights p_t s_t 2^E are rounded to fp16 (11 bits, E keeps them at the top of its
+// range), the second sum is fp32; centring the codes keeps the first sum, whose terms carry
+// the rounding, from cancelling against the second.
+// The softmax reference of a row moves only when a score exceeds it by 2^8 (then all sums
+// of the warp are rescaled), so that a step needs no reduction between lanes: each lane sums
+// the keys that it holds, and the lanes are added once at the end of the item.
+//
+// Requests longer than one split leave normalised partials with their log-sum, which the
+// merge kernel weighs; the split length depends on the request's length alone.
+#include <algorithm>
+#include <mutex>
+
+#include "cache.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace clef {
+
+namespace {
+
+constexpr int kAttendWarps = 4;
+constexpr int kAttendThreads = 32 * kAttendWarps;
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 block of 16-bit values held one row a group of four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 2^e, e clamped to the normal range.
+__device__ __forceinline__ float pow2i(int e) {
+    return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23);
+}
+
+// The two elements of a 32-bit word as fp32.
+__device__ __forceinline__ float2 unpack2(uint32_t w, int dtype) {
+    if (dtype == 0) return make_float2(bf16_lo(w), bf16_hi(w));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// What a CTA needs to know of every request: the ends of its work items and of its partial
+// rows, as running sums.
+struct Requests {
+    int items[kCacheMaxRequests];   // work items of requests 0 .. b
+    int parts[kCacheMaxRequests];   // partial rows of requests 0 .. b
+    int tmp[2][kAttendWarps];
+};
+
+struct Request {
+    int len, q0, nq, chunk, chunks;
+};
+
+__device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, bool report) {
+    Request r;
+    r.len = a.lengths[b];
+    r.q0 = a.cu_q[b];
+    int q1 = a.cu_q[b + 1];
+    const int cap = int(min(int64_t(a.width) << a.c.page_shift, int64_t(0x7fffffff)));
+    const bool bad = r.len < 0 || r.len > cap || r.q0 < 0 || q1 < r.q0 || q1 > a.total_q || q1 - r.q0 > a.max_q;
+    if (bad) {
+        if (report) atomicOr(a.flags, kFlagBounds);
+        r.len = min(max(r.len, 0), cap);
+        r.q0 = min(max(r.q0, 0), a.total_q);
+        q1 = min(max(q1, r.q0), a.total_q);
+    }
+    r.nq = min(q1 - r.q0, a.max_q);
+    r.chunk = attend_chunk(r.len);
+    r.chunks = max(1, (r.len + r.chunk - 1) / r.chunk);
+    return r;
+}
+
+// Fills the running sums; every thread of the CTA takes a run of neighbouring requests.
+__device__ __forceinline__ void scan_requests(const CacheAttendArgs& a, Requests& s, int rows_per_item) {
+    const int per = (a.B + kAttendThreads - 1) / kAttendThreads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b0 = threadIdx.x * per, b1 = min(b0 + per, a.B);
+    int items = 0, parts = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request_of(a, b, blockIdx.x == 0);
+        items += r.chunks * ((r.nq * a.share + rows_per_item - 1) / rows_per_item) * a.kv_heads;
+        parts += r.chunks > 1 ? r.chunks * r.nq * a.q_heads : 0;
+        s.items[b] = items;
+        s.parts[b] = parts;
+    }
+    int ei = items, ep = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int yi = __shfl_up_sync(0xffffffffu, ei, o), yp = __shfl_up_sync(0xffffffffu, ep, o);
+        if (lane >= o) {
+            ei += yi;
+            ep += yp;
+        }
+    }
+    if (lane == 31) {
+        s.tmp[0][warp] = ei;
+        s.tmp[1][warp] = ep;
+    }
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+        ei += s.tmp[0][w];
+        ep += s.tmp[1][w];
+    }
+    for (int b = b0; b < b1; ++b) {
+        s.items[b] += ei - items;
+        s.parts[b] += ep - parts;
+    }
+    __syncthreads();
+}
+
+}  // namespace
+
+template <int G, int NT>
+__global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const CacheAttendArgs a) {
+    griddep_wait();
+    griddep_launch();
+    __shared__ Requests s_req;
+    scan_requests(a, s_req, 8 * NT);
+    if (blockIdx.x == 0 && a.part_off)
+        for (int b = threadIdx.x; b < a.B; b += kAttendThreads) a.part_off[b] = b ? s_req.parts[b - 1] : 0;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, tq = lane & 3;
+    const int n_items = s_req.items[a.B - 1];
+    const int64_t piece_bytes = kPiece * G;
+    const int64_t page_pieces = a.c.page >> 4;
+
+    for (int w = blockIdx.x * kAttendWarps + warp; w < n_items; w += gridDim.x * kAttendWarps) {
+        // ---- the item: request b, split, key/value head, block of query rows
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_req.items[mid] <= w)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        const int b = lo;
+        const Request rq = request_of(a, b, false);
+        int it = w - (b ? s_req.items[b - 1] : 0);
+        const int n_rows = rq.nq * a.share;
+        const int n_blocks = (n_rows + 8 * NT - 1) / (8 * NT);
+        const int qb = it % n_blocks;
+        it /= n_blocks;
+        const int h = it % a.kv_heads, split = it / a.kv_heads;
+        const int row0 = qb * 8 * NT;
+        const int last_row = min(row0 + 8 * NT, n_rows) - 1;
+        const int t0 = split * rq.chunk;
+        int t1 = min(t0 + rq.chunk, rq.len);
+        const int ahead = rq.len - rq.nq;  // causal: query i sees keys 0 .. ahead + i
+        if (a.causal) t1 = min(t1, ahead + last_row / a.share + 1);
+
+        // ---- queries: B operand of S^T, one row a group of four lanes
+        uint32_t qf[G][NT][8];
+        float qscale[NT][2], qsum[G][NT][2];  // of rows 2 tq, 2 tq + 1 of each block of 8
+        int vis[NT][2];                       // keys that those rows see: 0 .. vis - 1
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = row0 + n * 8 + g;
+            const bool live = r < n_rows;
+            const int qi = live ? r / a.share : 0, qh = h * a.share + (live ? r % a.share : 0);
+            const uint16_t* q = static_cast<const uint16_t*>(a.q) + (rq.q0 + qi) * a.q_row + qh * a.q_head;
+            float2 x[G][8];
+            float top = 0.f, sum[G];
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                sum[gr] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t word = live ? *reinterpret_cast<const uint32_t*>(q + gr * 64 + i * 8 + 2 * tq) : 0u;
+                    x[gr][i] = unpack2(word, a.dtype);
+                    sum[gr] += x[gr][i].x + x[gr][i].y;
+                    top = fmaxf(top, fmaxf(fabsf(x[gr][i].x), fabsf(x[gr][i].y)));
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], o);
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // the row's largest value goes to [2^14, 2^15)
+            const int e = top > 0.f ? 14 - (int(__float_as_uint(top) >> 23) - 127) : 0;
+            const float up = pow2i(min(e, 120));
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = (i & 1) ? up * 0.0625f : up;
+                    qf[gr][n][i] = pack_f16(x[gr][i].x * f, x[gr][i].y * f);
+                }
+            const float back = a.scale_log2 * pow2i(24 - min(e, 120));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int from = (2 * tq + c) * 4;
+                qscale[n][c] = __shfl_sync(0xffffffffu, back, from);
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+                    qsum[gr][n][c] = __shfl_sync(0xffffffffu, sum[gr], from) * a.scale_log2;
+                const int rc = row0 + n * 8 + 2 * tq + c;
+                vis[n][c] = a.causal ? min(t1, ahead + rc / a.share + 1) : t1;
+            }
+        }
+
+        float acc[G][4][NT][4];  // O^T: 4 blocks of 16 values of each group
+        float l[NT][2], z[G][NT][2], ref[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                l[n][c] = 0.f;
+                ref[n][c] = -1e30f;
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) z[gr][n][c] = 0.f;
+            }
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[gr][mt][n][c] = 0.f;
+        int vexp = 120;  // value scales are multiplied by 2^vexp, at most 2^7
+
+        for (int t = t0; t < t1; t += 16) {
+            const int col = t >> a.c.page_shift;
+            const int id = a.table[int64_t(b) * a.width + col];
+            if (id < 0 || id >= a.c.n_pages) {  // no such page: its tokens are not there
+                if (lane == 0) atomicOr(a.flags, kFlagBounds);
+                continue;
+            }
+            const uint8_t* piece = a.c.data + ((int64_t(id) * a.c.heads + a.head0 + h) * page_pieces +
+                                               ((t & (a.c.page - 1)) >> 4)) * piece_bytes;
+            uint4 kw[G], vw[G];
+            uint2 sm[G][2];
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                kw[gr] = __ldg(reinterpret_cast<const uint4*>(piece + gr * 512) + lane);
+                vw[gr] = __ldg(reinterpret_cast<const uint4*>(piece + (G + gr) * 512) + lane);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    sm[gr][r] = __ldg(reinterpret_cast<const uint2*>(piece + G * 1024 + ((g + 8 * r) * G + gr) * 8));
+            }
+            const bool tail = t + 16 > t1;
+            if (tail) {  // tokens behind the last one hold anything
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (t + g + 8 * r >= t1)
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) sm[gr][r] = make_uint2(0u, 0u);
+            }
+            // ---- scores
+            float s[NT][4];
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                float part[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) part[n][c] = 0.f;
+                const uint32_t words[4] = {kw[gr].x, kw[gr].y, kw[gr].z, kw[gr].w};
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint32_t x = words[ks], y = x >> 8;
+                    const uint32_t A[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16_16816(part[n], A, qf[gr][n][2 * ks], qf[gr][n][2 * ks + 1]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t ksm = sm[gr][c >> 1].x;
+                        const float y = fmaf(part[n][c] * qscale[n][c & 1], bf16_lo(ksm),
+                                             qsum[gr][n][c & 1] * bf16_hi(ksm));
+                        s[n][c] = gr == 0 ? y : s[n][c] + y;
+                    }
+            }
+            if (tail || (a.causal && t + 15 > ahead)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (t + g + 8 * (c >> 1) >= vis[n][c & 1]) s[n][c] = -INFINITY;
+            }
+            // ---- references
+            const float vtop = pow2i(vexp);
+            bool need = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) need |= fmaxf(s[n][c], s[n][c + 2]) > ref[n][c] + 8.f;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) need |= bf16_lo(sm[gr][r].y) * vtop > 128.f;
+            if (__any_sync(0xffffffffu, need)) {
+                float vs = 0.f;
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) vs = fmaxf(vs, bf16_lo(sm[gr][r].y));
+                vs = warp_max(vs);
+                int e = vexp;
+                if (vs * vtop > 128.f) e = max(6 - (int(__float_as_uint(vs) >> 23) - 127), -120);
+                const float vcorr = pow2i(max(e - vexp, -126));
+                vexp = e;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(s[n][c], s[n][c + 2]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        float corr = 1.f;
+                        if (mx > ref[n][c] + 8.f) {
+                            corr = ex2_approx(ref[n][c] - mx);
+                            ref[n][c] = mx;
+                        }
+                        l[n][c] *= corr;
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            z[gr][n][c] *= corr;
+#pragma unroll
+                            for (int mt = 0; mt < 4; ++mt) {
+                                acc[gr][mt][n][c] *= corr * vcorr;
+                                acc[gr][mt][n][c + 2] *= corr * vcorr;
+                            }
+                        }
+                    }
+            }
+            // ---- weights
+            float p[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    p[n][c] = ex2_approx(s[n][c] - ref[n][c & 1]);
+                    l[n][c & 1] += p[n][c];
+                }
+            const float vmul = pow2i(vexp);
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                float vs[2], vm[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float sc = bf16_lo(sm[gr][r].y);
+                    vs[r] = sc * vmul;
+                    vm[r] = fmaf(8.f, sc, bf16_hi(sm[gr][r].y));
+                }
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        // a key that a row does not see adds nothing, whatever its value is
+                        const float w0 = p[n][2 * r], w1 = p[n][2 * r + 1];
+                        pf[n][r] = transpose8(pack_f16(w0 == 0.f ? 0.f : w0 * vs[r], w1 == 0.f ? 0.f : w1 * vs[r]));
+                        z[gr][n][0] += w0 == 0.f ? 0.f : w0 * vm[r];
+                        z[gr][n][1] += w1 == 0.f ? 0.f : w1 * vm[r];
+                    }
+                }
+                const uint32_t words[4] = {vw[gr].x, vw[gr].y, vw[gr].z, vw[gr].w};
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    // 1024 + c and 64 + c in fp16, less 1032 and 72: c - 8, exact
+                    const uint32_t x = words[mt], y = x >> 8;
+                    uint32_t A[4] = {(x & 0x000F000Fu) | 0x64006400u, (x & 0x00F000F0u) | 0x54005400u,
+                                     (y & 0x000F000Fu) | 0x64006400u, (y & 0x00F000F0u) | 0x54005400u};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __half2 off = __float2half2_rn((i & 1) ? 72.f : 1032.f);
+                        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&A[i]), off);
+                        A[i] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16_16816(acc[gr][mt][n], A, pf[n][0], pf[n][1]);
+                }
+            }
+        }
+
+        // ---- the item's result: normalised, with the logarithm (base 2) of its sum
+        const float vback = pow2i(-vexp);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float sum = l[n][c], zs[G];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    zs[gr] = z[gr][n][c];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) zs[gr] += __shfl_xor_sync(0xffffffffu, zs[gr], o);
+                }
+                const int r = row0 + n * 8 + 2 * tq + c;
+                if (r >= n_rows) continue;
+                const int qi = r / a.share, qh = h * a.share + r % a.share;
+                // (query rows of requests that overlap, which cu_q must not have, could
+                // make more partial rows than the workspace holds)
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float lse2 = sum == 0.f ? -INFINITY : ref[n][c] + log2f(sum);
+                const bool whole = rq.chunks == 1;
+                const int64_t row = whole ? int64_t(rq.q0 + qi) * a.q_heads + qh
+                                          : (b ? s_req.parts[b - 1] : 0) + (int64_t(split) * rq.nq + qi) * a.q_heads + qh;
+                if (!whole && (row < 0 || row >= a.part_rows)) {
+                    if (g == 0) atomicOr(a.flags, kFlagBounds);
+                    continue;
+                }
+                if (g == 0) {
+                    if (!whole)
+                        a.part_lse[row] = lse2;
+                    else if (a.lse)
+                        a.lse[row] = lse2 * 0.6931471805599453f;
+                }
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const float o = fmaf(acc[gr][mt][n][c + 2 * half], vback, zs[gr]) * inv;
+                            const int64_t at = row * (64 * G) + gr * 64 + mt * 16 + half * 8 + g;
+                            if (!whole)
+                                a.part_o[at] = o;
+                            else if (a.dtype == 0)
+                                static_cast<uint16_t*>(a.out)[at] = float_to_bf16(o);
+                            else
+                                static_cast<__half*>(a.out)[at] = __float2half_rn(o);
+                        }
+            }
+    }
+}
+
+// Weighs the splits of one (query row, head): one warp, two (or four) values a lane.
+template <int G>
+__global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs a) {
+    griddep_wait();
+    griddep_launch();
+    const int lane = threadIdx.x & 31;
+    const int b = blockIdx.y;
+    const int64_t item = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const Request r = request_of(a, b, false);
+    if (r.chunks == 1 || item >= int64_t(r.nq) * a.q_heads) return;
+    const int64_t p0 = a.part_off[b] + item, stride = int64_t(r.nq) * a.q_heads;
+    if (p0 < 0 || p0 + (r.chunks - 1) * stride >= a.part_rows) return;  // reported by the attention kernel
+    float top = -INFINITY, sum = 0.f, o[2 * G] = {};
+    for (int k0 = 0; k0 < r.chunks; k0 += 32) {
+        const int k = k0 + lane;
+        const float x = k < r.chunks ? a.part_lse[p0 + k * stride] : -INFINITY;
+        const float mx = fmaxf(top, warp_max(x));
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float corr = exp2f(top - ref);
+        const float w = exp2f(x - ref);
+        sum = sum * corr + warp_sum(w);
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) o[i] *= corr;
+        const int n = min(32, r.chunks - k0);
+        for (int j = 0; j < n; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            if (wj == 0.f) continue;  // a split that sees nothing, or weighs nothing
+            const float* src = a.part_o + (p0 + (k0 + j) * stride) * (64 * G) + lane * 2 * G;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const float2 v = *reinterpret_cast<const float2*>(src + 2 * i);
+                o[2 * i] = fmaf(v.x, wj, o[2 * i]);
+                o[2 * i + 1] = fmaf(v.y, wj, o[2 * i + 1]);
+            }
+        }
+        top = mx;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = int64_t(r.q0) * a.q_heads + item;
+    if (lane == 0 && a.lse)
+        a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * (64 * G) + lane * 2 * G);
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+        out[i] = a.dtype == 0 ? pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv) : pack_f16(o[2 * i] * inv, o[2 * i + 1] * inv);
+}
+
+namespace {
+
+template <int G, int NT>
+cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    static int resident = 0;
+    std::call_once(once, [] {
+        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_kernel<G, NT>, kAttendThreads, 0);
+    });
+    if (err != cudaSuccess) return err;
+    return launch_pdl(cache_attend_kernel<G, NT>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
+                      0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s) {
+    if (a.total_q <= 0 || a.max_q <= 0) return cudaSuccess;
+    // query rows an item: as few blocks of rows as fit the registers (8 NT rows; 32 of 64
+    // values, 16 of 128), shared out evenly
+    const int64_t tiles = (int64_t(a.max_q) * a.share + 7) / 8;
+    const int most = a.c.groups == 1 ? 4 : 2;
+    const int64_t blocks = (tiles + most - 1) / most;
+    const int nt = int((tiles + blocks - 1) / blocks);
+    cudaError_t e;
+    if (a.c.groups == 1)
+        e = nt == 1 ? launch_attend<1, 1>(a, s) : nt == 2 ? launch_attend<1, 2>(a, s)
+            : nt == 3 ? launch_attend<1, 3>(a, s) : launch_attend<1, 4>(a, s);
+    else
+        e = nt == 1 ? launch_attend<2, 1>(a, s) : launch_attend<2, 2>(a, s);
+    if (e != cudaSuccess || a.max_chunks <= 1) return e;
+    const dim3 grid(unsigned((int64_t(a.max_q) * a.q_heads + 7) / 8), unsigned(a.B));
+    if (a.c.groups == 1) return launch_pdl(cache_merge_kernel<1>, grid, dim3(256), 0, s, a);
+    return launch_pdl(cache_merge_kernel<2>, grid, dim3(256), 0, s, a);
+}
+
+}  // namespace clef

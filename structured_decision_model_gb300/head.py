@@ -11,6 +11,7 @@ import numpy as np
 import torch
 
 from . import binding as B
+from .memory import MemoryCache, stream_handle
 
 
 def weight_order(H, D, heads, F, n_route, n_joint):
@@ -38,11 +39,6 @@ def to_device_bf16(a: np.ndarray, device="cuda") -> torch.Tensor:
     """uint16 bf16 bit patterns -> a torch bfloat16 tensor on ``device``."""
     t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.uint16).view(np.int16))
     return t.to(device).view(torch.bfloat16)
-
-
-def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
 
 
 @dataclass
@@ -115,6 +111,44 @@ class ClefHead:
            lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(), out.q_value.data_ptr(),
            out.q_conf.data_ptr(), out.q_argmax.data_ptr(), ws.data_ptr(), ws.numel(), debug=debug,
            stream=stream_handle(stream))
+        return out
+
+    def memory_cache(self, n_pages, requests, max_len, page=64) -> MemoryCache:
+        """A 4-bit cache that keeps this head's memory (every routing layer's heads side by side)."""
+        return MemoryCache(n_pages, page=page, heads=self.cfg.n_route * self.heads, head_dim=64, requests=requests,
+                           max_len=max_len, device=self.device)
+
+    def memory_store(self, schema: B.Schema, record: int, row0: int, n_rows: int, cache: MemoryCache,
+                     slots: torch.Tensor, stream=None):
+        """Keep the K/V of rows [row0, row0 + n_rows) of ``record``, which ``stream_rows`` or
+        ``forward`` left in the workspace, in the cache's ``slots`` (int32 [n_rows])."""
+        slots = cache.checked_slots(slots)
+        if slots.numel() != n_rows:
+            raise B.ClefError(1, "memory_store: one slot a row")
+        ws = self.workspace(schema)
+        B.clef_memory_store(self.cfg, schema, record, row0, n_rows, ws.data_ptr(), ws.numel(), cache.struct,
+                            slots.data_ptr(), cache.flags.data_ptr(), stream_handle(stream))
+
+    def stream_finish_memory(self, schema: B.Schema, first_row, hidden: torch.Tensor, token_ids: torch.Tensor,
+                             lexical: torch.Tensor, cache: MemoryCache, block_table: Optional[torch.Tensor] = None,
+                             out: Optional[Outputs] = None, debug=None, stream=None) -> Outputs:
+        """``stream_finish`` with the whole memory read from the cache: row b of ``block_table``
+        (the cache's own by default) holds record b.  Rows before ``first_row[b]`` need not
+        have been streamed for this schema; spans must start at or behind it."""
+        ws = self._ws
+        out = out if out is not None else self.alloc_outputs(schema)
+        table = cache.checked_table(block_table, schema.B)
+        s = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.stream(s):
+            n = B.clef_cache_attend_workspace(cache.struct, schema.B, schema.O, self.heads, table.shape[1] * cache.page)
+            space = torch.empty(n, dtype=torch.uint8, device=self.device)
+        dtype = B.FP16 if hidden.dtype == torch.float16 else B.BF16
+        B.clef_stream_finish_memory(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), schema, first_row,
+                                    hidden.data_ptr(), dtype, token_ids.data_ptr(), lexical.data_ptr(),
+                                    out.logits.data_ptr(), out.probs.data_ptr(), out.q_value.data_ptr(),
+                                    out.q_conf.data_ptr(), out.q_argmax.data_ptr(), ws.data_ptr(), ws.numel(),
+                                    cache.struct, table.data_ptr(), table.shape[1], cache.flags.data_ptr(),
+                                    space.data_ptr(), n, debug=debug, stream=stream_handle(s))
         return out
 
     def device_status(self, stream=None) -> int:

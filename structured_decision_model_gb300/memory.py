@@ -1,0 +1,201 @@
+"""PyTorch-side helper around the 4-bit memory cache: device buffers and streams only.
+
+``MemoryCache`` owns (or is given) the page buffer and the page accounts, and calls the
+``clef_cache_*`` entry points on torch's current stream.  All arithmetic happens in
+libclef_head.so.  A serving step is
+
+    slots, cu = cache.plan(want, n_slots)        # pages and slots of the new tokens
+    cache.append(k, v, slots)                    # their keys and values, into 4 bits
+    out, lse = cache.attend(q, cu, max_q)        # their attention over the whole memory
+
+and ``plan`` with smaller lengths gives pages back.  Nothing here waits for the GPU;
+``device_status`` does, and reports what the kernels met (a bad slot, pages that ran out).
+The cache holds numbers, not gradients: tensors that require one are refused while grad
+mode is on.
+"""
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import binding as B
+
+_DTYPES = {torch.bfloat16: B.BF16, torch.float16: B.FP16, torch.float32: B.FP32}
+
+
+def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
+    s = stream if stream is not None else torch.cuda.current_stream()
+    return int(s.cuda_stream)
+
+
+def _refuse(why):
+    raise B.ClefError(1, why)
+
+
+class MemoryCache:
+    """Pages of 4-bit keys and values, and who holds them.
+
+    ``n_pages`` pages of ``page`` tokens (16 .. 256, a power of two) of ``heads`` heads of
+    ``head_dim`` 64 or 128; page accounts for ``requests`` requests of at most ``max_len``
+    tokens.  ``data`` (uint8, of ``size_bytes``) and ``state`` (int32, of ``state_size``: the free
+    count, the lengths, the free pages and the block table, one after the other) may be
+    buffers of the caller, taken as they are; otherwise they are made here, empty.
+    """
+
+    def __init__(self, n_pages: int, page: int = 64, heads: int = 16, head_dim: int = 64, requests: int = 1,
+                 max_len: int = 16384, device="cuda", data: Optional[torch.Tensor] = None,
+                 state: Optional[torch.Tensor] = None):
+        self.n_pages, self.page, self.heads, self.head_dim = int(n_pages), int(page), int(heads), int(head_dim)
+        self.requests, self.max_len = int(requests), int(max_len)
+        self.struct = B.ClefCache(0, self.n_pages, self.page, self.heads, self.head_dim)
+        self.size_bytes = B.clef_cache_size(self.struct)
+        if not 1 <= self.requests <= B.CACHE_MAX_REQUESTS or self.max_len < 1:
+            _refuse("MemoryCache: requests or max_len out of range")
+        self.width = -(-self.max_len // self.page)
+        n, p = self.requests, self.n_pages
+        self.state_size = 1 + n + p + n * self.width
+        # index 0 where no number is given, so that the current device may differ from the cache's
+        self.device = torch.empty(0, device=device).device
+        if data is None:
+            data = torch.zeros(self.size_bytes, dtype=torch.uint8, device=self.device)
+        elif data.dtype != torch.uint8 or data.numel() != self.size_bytes or not data.is_contiguous() or \
+                data.device != self.device:
+            _refuse("MemoryCache: data is not a contiguous uint8 tensor of size_bytes on the device")
+        if state is None:
+            state = torch.full((self.state_size,), -1, dtype=torch.int32, device=self.device)
+            state[0] = p
+            state[1:1 + n] = 0
+            state[1 + n:1 + n + p] = torch.arange(p - 1, -1, -1, dtype=torch.int32, device=self.device)
+        elif state.dtype != torch.int32 or state.numel() != self.state_size or not state.is_contiguous() or \
+                state.device != self.device:
+            _refuse("MemoryCache: state is not a contiguous int32 tensor of state_size on the device")
+        self.data, self.state = data, state
+        self.struct.data = data.data_ptr()
+        self.free_count, self.lengths = state[:1], state[1:1 + n]
+        self.free_pages, self.block_table = state[1 + n:1 + n + p], state[1 + n + p:].view(n, self.width)
+        self.flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    # ------------------------------------------------------------- checks
+
+    def _on_device(self, t, what):
+        if t.device != self.device:
+            _refuse(f"{what} is on {t.device}, the cache on {self.device}")
+
+    def checked_slots(self, slots: torch.Tensor) -> torch.Tensor:
+        self._on_device(slots, "slots")
+        if slots.dtype != torch.int32 or slots.dim() != 1 or not slots.is_contiguous():
+            _refuse("slots: a contiguous int32 vector")
+        return slots
+
+    def checked_table(self, table: Optional[torch.Tensor], n: int) -> torch.Tensor:
+        if table is None:
+            table = self.block_table
+        self._on_device(table, "block_table")
+        if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] < n or not table.is_contiguous():
+            _refuse("block_table: contiguous int32 [requests, pages]")
+        return table
+
+    def _rows(self, t, what):
+        self._on_device(t, what)
+        if t.dim() != 3 or t.shape[2] != self.head_dim or t.stride(2) != 1 or t.dtype not in (torch.bfloat16, torch.float16):
+            _refuse(f"{what}: bf16 or fp16 [tokens, heads, {self.head_dim}], values contiguous")
+        if t.requires_grad and torch.is_grad_enabled():
+            _refuse(f"{what} requires a gradient, which a 4-bit cache does not pass on")
+        return _DTYPES[t.dtype]
+
+    # ---------------------------------------------------------- operators
+
+    def plan(self, want: torch.Tensor, n_slots: int, slots: Optional[torch.Tensor] = None,
+             cu: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Take the requests' lengths to ``want`` (int32 [requests]): the slots of the tokens
+        gained, request by request, -1 behind them (int32 [n_slots]), and their running sum
+        (int32 [requests + 1])."""
+        self._on_device(want, "want")
+        if want.dtype != torch.int32 or want.shape != (self.requests,) or not want.is_contiguous():
+            _refuse("want: contiguous int32 [requests]")
+        with torch.cuda.device(self.device):
+            if slots is None:
+                slots = torch.empty(n_slots, dtype=torch.int32, device=self.device)
+            elif self.checked_slots(slots).numel() != n_slots:
+                _refuse("slots: int32 [n_slots]")
+            if cu is None:
+                cu = torch.empty(self.requests + 1, dtype=torch.int32, device=self.device)
+            elif self.checked_slots(cu).numel() != self.requests + 1:
+                _refuse("cu: int32 [requests + 1]")
+            B.clef_cache_plan(self.struct, self.requests, self.lengths.data_ptr(), want.data_ptr(),
+                              self.block_table.data_ptr(), self.width, self.free_pages.data_ptr(),
+                              self.free_count.data_ptr(), cu.data_ptr(), slots.data_ptr(), n_slots,
+                              self.flags.data_ptr(), stream_handle())
+        return slots, cu
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, head0: int = 0):
+        """Store key and value rows [tokens, heads, head_dim] (bf16 or fp16, any row and head
+        strides) in ``slots``, as cache heads ``head0`` on.  Negative slots skip their row."""
+        dtype = self._rows(k, "k")
+        if self._rows(v, "v") != dtype or v.shape != k.shape:
+            _refuse("k and v: one shape and type")
+        if self.checked_slots(slots).numel() != k.shape[0]:
+            _refuse("slots: one a row")
+        with torch.cuda.device(self.device):
+            B.clef_cache_append(self.struct, k.shape[0], head0, k.shape[1], dtype, k.data_ptr(), k.stride(0), k.stride(1),
+                                v.data_ptr(), v.stride(0), v.stride(1), slots.data_ptr(), self.flags.data_ptr(),
+                                stream_handle())
+
+    def read(self, slots: torch.Tensor, dtype=torch.bfloat16, head0: int = 0,
+             heads: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """What the rows of ``slots`` stand for: k, v [tokens, heads, head_dim] in ``dtype``
+        (bf16, fp16 or fp32); zeros for negative slots."""
+        if dtype not in _DTYPES:
+            _refuse("read: bf16, fp16 or fp32")
+        heads = self.heads - head0 if heads is None else heads
+        n = self.checked_slots(slots).numel()
+        if heads < 1:
+            _refuse("read: no heads")
+        with torch.cuda.device(self.device):
+            k = torch.empty((n, heads, self.head_dim), dtype=dtype, device=self.device)
+            v = torch.empty_like(k)
+            B.clef_cache_read(self.struct, n, head0, heads, _DTYPES[dtype], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+                              self.flags.data_ptr(), stream_handle())
+        return k, v
+
+    def attend(self, q: torch.Tensor, cu_q: torch.Tensor, max_q: int, scale: Optional[float] = None,
+               causal: bool = True, head0: int = 0, kv_heads: Optional[int] = None,
+               block_table: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Attention of query rows [total, q_heads, head_dim] over their requests' memory: the
+        output in q's type and the scores' log-sum (fp32 [total, q_heads]).
+
+        ``cu_q`` (int32 [B + 1]) holds each request's first row, ``max_q`` bounds the rows of
+        one request.  With ``causal`` the queries are the request's last tokens, otherwise
+        each sees the whole memory.  Query heads share the ``kv_heads`` cache heads from
+        ``head0`` on evenly (all of the cache's by default).  ``block_table`` and ``lengths``
+        default to the cache's own.  A row that sees nothing gives 0 and -inf; rows behind
+        the last request are not written (not set at all without ``out``)."""
+        dtype = self._rows(q, "q")
+        kv_heads = self.heads - head0 if kv_heads is None else kv_heads
+        n = self.checked_slots(cu_q).numel() - 1
+        lengths = self.lengths if lengths is None else self.checked_slots(lengths)
+        table = self.checked_table(block_table, n)
+        if n < 1 or lengths.numel() < n:
+            _refuse("cu_q, lengths: one entry a request")
+        total, q_heads = q.shape[0], q.shape[1]
+        scale = self.head_dim ** -0.5 if scale is None else scale
+        with torch.cuda.device(self.device):
+            if out is None:
+                out = torch.empty((total, q_heads, self.head_dim), dtype=q.dtype, device=self.device)
+            elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != self.device:
+                _refuse("out: contiguous, of q's shape and type")
+            lse = torch.empty((total, q_heads), dtype=torch.float32, device=self.device)
+            # a buffer of the call's own: overlapping calls and captured graphs never share one
+            n_bytes = B.clef_cache_attend_workspace(self.struct, n, total, max(q_heads, 1), table.shape[1] * self.page)
+            space = torch.empty(n_bytes, dtype=torch.uint8, device=self.device)
+            B.clef_cache_attend(self.struct, n, total, max_q, q_heads, head0, kv_heads, dtype, q.data_ptr(), q.stride(0),
+                                q.stride(1), cu_q.data_ptr(), table.data_ptr(), table.shape[1], lengths.data_ptr(),
+                                scale, int(causal), out.data_ptr(), lse.data_ptr(), self.flags.data_ptr(),
+                                space.data_ptr() if n_bytes else None, n_bytes, stream_handle())
+        return out, lse
+
+    def device_status(self) -> int:
+        """Waits for the current stream, reads and clears what the kernels reported."""
+        with torch.cuda.device(self.device):
+            return B.clef_cache_status(self.flags.data_ptr(), stream_handle())
