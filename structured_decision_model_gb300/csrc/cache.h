@@ -45,17 +45,9 @@ struct CacheAttendArgs {
     int max_chunks;
 };
 
-// Keys of one split of a request's memory: a function of the request's length alone, so that
-// a row's result does not depend on the batch.
-__host__ __device__ inline int attend_chunk(int len) {
-    const int c = (len / 64 + 15) & ~15;
-    return c < 256 ? 256 : c > 1024 ? 1024 : c;
-}
-// Upper bound of the splits of any request of at most max_len keys.
-inline int64_t attend_max_chunks(int64_t max_len) {
-    const int64_t short_chunks = (max_len + 255) / 256, long_chunks = (max_len + 1023) / 1024;
-    return short_chunks <= 66 ? short_chunks : long_chunks > 66 ? long_chunks : 66;
-}
+// Keys of one split of a request's memory: one size for all requests, so that a row's result
+// does not depend on the batch.
+constexpr int kAttendChunk = 1024;
 
 cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t s);

@@ -43,7 +43,7 @@ bool bad_table(const clef_cache* c, int B, int stride) {
 struct AttendSpace {
     int64_t rows = 0, lse = 0, off = 0, bytes = 0;  // partial rows; byte offsets; total
     AttendSpace(int64_t B, int64_t total_q, int64_t q_heads, int64_t dim, int64_t max_len) {
-        const int64_t chunks = attend_max_chunks(max_len);
+        const int64_t chunks = (max_len + kAttendChunk - 1) / kAttendChunk;
         if (chunks <= 1 || total_q < 1) return;
         rows = total_q * q_heads * chunks;
         lse = rows * dim * 4;
@@ -157,7 +157,7 @@ int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32
     const int64_t max_len = int64_t(table_stride) * cache->page;
     const AttendSpace sp(B, total_q, q_heads, cache->head_dim, max_len);
     // items and partial rows are counted in 32 bits on the GPU
-    const int64_t chunks = attend_max_chunks(max_len);
+    const int64_t chunks = (max_len + kAttendChunk - 1) / kAttendChunk;
     if (sp.rows >= kInt32 || chunks * (int64_t(max_q) * (q_heads / kv_heads) / 8 + 1) * kv_heads * B >= kInt32 ||
         (int64_t(max_q) * q_heads + 7) / 8 >= kInt32)
         return CLEF_ERR_UNSUPPORTED_CONFIG;

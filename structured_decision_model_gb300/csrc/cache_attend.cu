@@ -1,7 +1,10 @@
 // Attention over the paged 4-bit memory cache (clef_cache_attend).
 //
-// A warp takes one item: a split of a request's keys, one key/value head, and up to 8 NT
-// query rows of the heads that share it.  The products run transposed on mma.sync, the keys
+// A CTA of four warps takes one item: a split of a request's keys, one key/value head, and up
+// to 8 NT query rows of the heads that share it.  Its warps take the 16-token pieces of the
+// split in turn, each through a ring of its own that cp.async fills several pieces ahead
+// (no barrier, nothing to wait for but the warp's own copies), and meet once, at the end of
+// the item, to weigh their results.  The products run transposed on mma.sync, the keys
 // as the M dimension: S^T = K Q^T (16 keys x 8 queries an instruction, so that a single
 // token wastes 7 of 8 columns rather than 15 of 16 rows) and O^T += V^T P^T.  The A operand
 // of both is made in registers from the codes: the stored order gives each lane its own 16
@@ -12,15 +15,15 @@
 //   s_t (q . c_t) + m_t (sum q),  with s_t and m_t the key's scale and minimum.
 // Queries are scaled by a power of two per row to fill fp16's range (exact).
 //   Values: o = sum_t p_t (s_t c_t + m_t) = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t).
-// The weights p_t s_t 2^E are rounded to fp16 (11 bits, E keeps them at the top of its
-// range), the second sum is fp32; centring the codes keeps the first sum, whose terms carry
+// The weights p_t s_t 2^E are rounded to fp16 (11 bits, E keeps the largest s_t 2^E in [4, 8)
+// or the weights within 2^11), the second sum is fp32; centring the codes keeps the first sum, whose terms carry
 // the rounding, from cancelling against the second.
 // The softmax reference of a row moves only when a score exceeds it by 2^8 (then all sums
 // of the warp are rescaled), so that a step needs no reduction between lanes: each lane sums
 // the keys that it holds, and the lanes are added once at the end of the item.
 //
 // Requests longer than one split leave normalised partials with their log-sum, which the
-// merge kernel weighs; the split length depends on the request's length alone.
+// merge kernel weighs.
 #include <algorithm>
 #include <mutex>
 
@@ -75,7 +78,7 @@ struct Requests {
 };
 
 struct Request {
-    int len, q0, nq, chunk, chunks;
+    int len, q0, nq, chunks;
 };
 
 __device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, bool report) {
@@ -92,8 +95,7 @@ __device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, b
         q1 = min(max(q1, r.q0), a.total_q);
     }
     r.nq = min(q1 - r.q0, a.max_q);
-    r.chunk = attend_chunk(r.len);
-    r.chunks = max(1, (r.len + r.chunk - 1) / r.chunk);
+    r.chunks = max(1, int((int64_t(r.len) + kAttendChunk - 1) / kAttendChunk));
     return r;
 }
 
@@ -138,10 +140,28 @@ __device__ __forceinline__ void scan_requests(const CacheAttendArgs& a, Requests
 }  // namespace
 
 template <int G, int NT>
+struct AttendSmem {
+    // 16-token pieces a step: two where the registers allow, which halves the cost of a step's
+    // waits, votes and addresses
+    static constexpr int kPieces = 2;
+    // steps in flight a warp; the same bytes then hold the warps' results
+    static constexpr int kStages = G == 2 ? 2 : NT <= 2 ? 3 : 4;
+    static constexpr int kRing = kAttendWarps * kStages * kPieces * kPiece * G;
+    static constexpr int kResults = kAttendWarps * 8 * NT * 64 * G * 4;
+    static constexpr int kBytes = kRing > kResults ? kRing : kResults;
+};
+
+template <int G, int NT>
 __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const CacheAttendArgs a) {
+    using Smem = AttendSmem<G, NT>;
+    constexpr int ST = Smem::kStages, KP = Smem::kPieces;
+    constexpr int kBytes = kPiece * G;
     griddep_wait();
     griddep_launch();
     __shared__ Requests s_req;
+    __shared__ __align__(16) uint8_t s_ring[Smem::kBytes];
+    __shared__ float s_ref[kAttendWarps][8 * NT], s_sum[kAttendWarps][8 * NT];
+    __shared__ const uint8_t* s_page[kAttendChunk / 16];  // the split's pages, null where there is none
     scan_requests(a, s_req, 8 * NT);
     if (blockIdx.x == 0 && a.part_off)
         for (int b = threadIdx.x; b < a.B; b += kAttendThreads) a.part_off[b] = b ? s_req.parts[b - 1] : 0;
@@ -149,10 +169,10 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tq = lane & 3;
     const int n_items = s_req.items[a.B - 1];
-    const int64_t piece_bytes = kPiece * G;
-    const int64_t page_pieces = a.c.page >> 4;
+    const int page_mask = a.c.page - 1;
+    uint8_t* ring = s_ring + warp * (ST * KP * kBytes);
 
-    for (int w = blockIdx.x * kAttendWarps + warp; w < n_items; w += gridDim.x * kAttendWarps) {
+    for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
         // ---- the item: request b, split, key/value head, block of query rows
         int lo = 0, hi = a.B - 1;
         while (lo < hi) {
@@ -172,10 +192,49 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
         const int h = it % a.kv_heads, split = it / a.kv_heads;
         const int row0 = qb * 8 * NT;
         const int last_row = min(row0 + 8 * NT, n_rows) - 1;
-        const int t0 = split * rq.chunk;
-        int t1 = min(t0 + rq.chunk, rq.len);
+        const int t0 = split * kAttendChunk;
+        int t1 = min(t0 + kAttendChunk, rq.len);
         const int ahead = rq.len - rq.nq;  // causal: query i sees keys 0 .. ahead + i
         if (a.causal) t1 = min(t1, ahead + last_row / a.share + 1);
+
+        // ---- pages of the split and the first pieces: warp w takes steps w, w + 4, ...
+        const int p0 = t0 >> a.c.page_shift;
+        bool hole = false;
+        if (threadIdx.x < kAttendChunk / 16) {
+            const int p = p0 + threadIdx.x;
+            const uint8_t* at = nullptr;
+            if ((int64_t(p) << a.c.page_shift) < t1) {
+                const int id = a.table[int64_t(b) * a.width + p];
+                hole = id < 0 || id >= a.c.n_pages;
+                if (hole)
+                    atomicOr(a.flags, kFlagBounds);
+                else
+                    at = a.c.data + ((int64_t(id) * a.c.heads + a.head0 + h) << (a.c.page_shift - 4)) * kBytes;
+            }
+            s_page[threadIdx.x] = at;
+        }
+        const bool holes = __syncthreads_or(hole);
+        auto request_step = [&](int t, int stage) {
+            uint8_t* dst = ring + stage * (KP * kBytes);
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const int tk = t + 16 * k;
+                if (tk < t1) {
+                    const uint8_t* page = s_page[(tk >> a.c.page_shift) - p0];
+                    const uint8_t* src = page + ((tk & page_mask) >> 4) * kBytes;
+                    if (page)
+#pragma unroll
+                        for (int i = 0; i < kBytes; i += 512)
+                            if (i + lane * 16 < kBytes) cp_async16(dst + k * kBytes + i + lane * 16, src + i + lane * 16, true);
+                }
+            }
+            cp_async_commit();
+        };
+        constexpr int kStride = 16 * KP * kAttendWarps;
+        const int t_first = t0 + warp * 16 * KP;
+        int t_next = t_first;
+#pragma unroll
+        for (int s = 0; s < ST - 1; ++s, t_next += kStride) request_step(t_next, s);
 
         // ---- queries: B operand of S^T, one row a group of four lanes
         uint32_t qf[G][NT][8];
@@ -246,96 +305,153 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) acc[gr][mt][n][c] = 0.f;
-        int vexp = 120;  // value scales are multiplied by 2^vexp, at most 2^7
+        float vmul = pow2i(120);  // value scales are multiplied by a power of two, to at most 8
 
-        for (int t = t0; t < t1; t += 16) {
-            const int col = t >> a.c.page_shift;
-            const int id = a.table[int64_t(b) * a.width + col];
-            if (id < 0 || id >= a.c.n_pages) {  // no such page: its tokens are not there
-                if (lane == 0) atomicOr(a.flags, kFlagBounds);
-                continue;
-            }
-            const uint8_t* piece = a.c.data + ((int64_t(id) * a.c.heads + a.head0 + h) * page_pieces +
-                                               ((t & (a.c.page - 1)) >> 4)) * piece_bytes;
-            uint4 kw[G], vw[G];
-            uint2 sm[G][2];
+        int stage = 0;
+        for (int t = t_first; t < t1; t += kStride, t_next += kStride) {
+            cp_async_wait<ST - 2>();
+            __syncwarp();  // this step's pieces are there, and every lane is done with those before
+            request_step(t_next, stage == 0 ? ST - 1 : stage - 1);
+            const uint8_t* pieces = ring + stage * (KP * kBytes);
+            stage = stage == ST - 1 ? 0 : stage + 1;
+
+            // ---- key products, scales and minima (keys g and g + 8 of each piece)
+            float part[KP][G][NT][4];
+            float ks[KP][G][2], km[KP][G][2], vs[KP][G][2], vm[KP][G][2];
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                kw[gr] = __ldg(reinterpret_cast<const uint4*>(piece + gr * 512) + lane);
-                vw[gr] = __ldg(reinterpret_cast<const uint4*>(piece + (G + gr) * 512) + lane);
+            for (int k = 0; k < KP; ++k)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    sm[gr][r] = __ldg(reinterpret_cast<const uint2*>(piece + G * 1024 + ((g + 8 * r) * G + gr) * 8));
-            }
-            const bool tail = t + 16 > t1;
-            if (tail) {  // tokens behind the last one hold anything
+                for (int gr = 0; gr < G; ++gr) {
+                    const uint8_t* piece = pieces + k * kBytes;
+                    const uint4 kw = reinterpret_cast<const uint4*>(piece + gr * 512)[lane];
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    if (t + g + 8 * r >= t1)
+                    for (int r = 0; r < 2; ++r) {
+                        const uint2 sm = *reinterpret_cast<const uint2*>(piece + G * 1024 + ((g + 8 * r) * G + gr) * 8);
+                        ks[k][gr][r] = bf16_lo(sm.x);
+                        km[k][gr][r] = bf16_hi(sm.x);
+                        vs[k][gr][r] = bf16_lo(sm.y);
+                        vm[k][gr][r] = bf16_hi(sm.y);
+                    }
 #pragma unroll
-                        for (int gr = 0; gr < G; ++gr) sm[gr][r] = make_uint2(0u, 0u);
-            }
-            // ---- scores
-            float s[NT][4];
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                float part[NT][4];
+                        for (int c = 0; c < 4; ++c) part[k][gr][n][c] = 0.f;
+                    const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t x = words[i], y = x >> 8;
+                        const uint32_t A[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16_16816(part[k][gr][n], A, qf[gr][n][2 * i], qf[gr][n][2 * i + 1]);
+                    }
+                }
+            // ---- scores (base 2) less their row's reference
+            auto score = [&](int k, int n, int c, float less) {
+                float y = less;
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    y = fmaf(qsum[gr][n][c & 1], km[k][gr][c >> 1], y);
+                    y = fmaf(part[k][gr][n][c] * qscale[n][c & 1], ks[k][gr][c >> 1], y);
+                }
+                return y;
+            };
+            float p[KP][NT][4], top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) part[n][c] = 0.f;
-                const uint32_t words[4] = {kw[gr].x, kw[gr].y, kw[gr].z, kw[gr].w};
+                    for (int c = 0; c < 4; ++c) p[k][n][c] = score(k, n, c, -ref[n][c & 1]);
+            // tokens behind the last one hold anything, causal rows see a part, pages may lack
+            if (t + 16 * KP > t1 || (a.causal && t + 16 * KP - 1 > ahead) || holes) {
+                bool odd = false;  // a value scale that is no number
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const uint32_t x = words[ks], y = x >> 8;
-                    const uint32_t A[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+                for (int k = 0; k < KP; ++k) {
+                    const int tk = t + 16 * k;
+                    const int end = tk < t1 && s_page[(tk >> a.c.page_shift) - p0] ? t1 : 0;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16_16816(part[n], A, qf[gr][n][2 * ks], qf[gr][n][2 * ks + 1]);
+                    for (int r = 0; r < 2; ++r)
+                        if (tk + g + 8 * r >= end)
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr) vs[k][gr][r] = vm[k][gr][r] = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (tk + g + 8 * (c >> 1) >= min(vis[n][c & 1], end)) p[k][n][c] = -INFINITY;
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) odd |= !(fabsf(vs[k][gr][r]) < INFINITY);
+                }
+                if (odd) {  // it makes the rows that see it no number, and is nothing to the others
+#pragma unroll
+                    for (int k = 0; k < KP; ++k)
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                if (!(fabsf(vs[k][gr][r]) < INFINITY)) {
+                                    vs[k][gr][r] = vm[k][gr][r] = 0.f;
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                        for (int c = 0; c < 2; ++c)
+                                            if (!(p[k][n][c + 2 * r] == -INFINITY)) z[gr][n][c] = NAN;
+                                }
+                }
+            }
+            float vw[KP][G][2];  // the value scales as weights take them
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        vm[k][gr][r] = fmaf(8.f, vs[k][gr][r], vm[k][gr][r]);
+                        vw[k][gr][r] = vs[k][gr][r] * vmul;
+                        top = fmaxf(top, vw[k][gr][r]);
+                    }
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    top = fmax3(top, p[k][n][0], p[k][n][1]);
+                    top = fmax3(top, p[k][n][2], p[k][n][3]);
+                }
+            if (__any_sync(0xffffffffu, top > 8.f)) {  // new references: the first step, and rarely after
+                float vtop = 0.f;
+#pragma unroll
+                for (int k = 0; k < KP; ++k)
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) vtop = fmax3(vtop, vs[k][gr][0], vs[k][gr][1]);
+                vtop = warp_max(vtop);
+                float vcorr = 1.f;
+                if (vtop * vmul > 8.f) {  // the largest scale goes to [4, 8)
+                    const float to = pow2i(2 - (int(__float_as_uint(vtop) >> 23) - 127));
+                    vcorr = to / vmul;
+                    vmul = to;
+#pragma unroll
+                    for (int k = 0; k < KP; ++k)
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) vw[k][gr][r] = vs[k][gr][r] * vmul;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t ksm = sm[gr][c >> 1].x;
-                        const float y = fmaf(part[n][c] * qscale[n][c & 1], bf16_lo(ksm),
-                                             qsum[gr][n][c & 1] * bf16_hi(ksm));
-                        s[n][c] = gr == 0 ? y : s[n][c] + y;
-                    }
-            }
-            if (tail || (a.causal && t + 15 > ahead)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (t + g + 8 * (c >> 1) >= vis[n][c & 1]) s[n][c] = -INFINITY;
-            }
-            // ---- references
-            const float vtop = pow2i(vexp);
-            bool need = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) need |= fmaxf(s[n][c], s[n][c + 2]) > ref[n][c] + 8.f;
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) need |= bf16_lo(sm[gr][r].y) * vtop > 128.f;
-            if (__any_sync(0xffffffffu, need)) {
-                float vs = 0.f;
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) vs = fmaxf(vs, bf16_lo(sm[gr][r].y));
-                vs = warp_max(vs);
-                int e = vexp;
-                if (vs * vtop > 128.f) e = max(6 - (int(__float_as_uint(vs) >> 23) - 127), -120);
-                const float vcorr = pow2i(max(e - vexp, -126));
-                vexp = e;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float mx = fmaxf(s[n][c], s[n][c + 2]);
+                        float s[KP][2], mx = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < KP; ++k)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float seen = p[k][n][c + 2 * r];
+                                s[k][r] = seen == -INFINITY ? seen : score(k, n, c + 2 * r, 0.f);
+                                mx = fmaxf(mx, s[k][r]);
+                            }
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                         float corr = 1.f;
@@ -343,6 +459,10 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                             corr = ex2_approx(ref[n][c] - mx);
                             ref[n][c] = mx;
                         }
+#pragma unroll
+                        for (int k = 0; k < KP; ++k)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) p[k][n][c + 2 * r] = s[k][r] - ref[n][c];
                         l[n][c] *= corr;
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
@@ -355,58 +475,55 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                         }
                     }
             }
-            // ---- weights
-            float p[NT][4];
+            // ---- weights and value products
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int k = 0; k < KP; ++k) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    p[n][c] = ex2_approx(s[n][c] - ref[n][c & 1]);
-                    l[n][c & 1] += p[n][c];
-                }
-            const float vmul = pow2i(vexp);
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                float vs[2], vm[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float sc = bf16_lo(sm[gr][r].y);
-                    vs[r] = sc * vmul;
-                    vm[r] = fmaf(8.f, sc, bf16_hi(sm[gr][r].y));
-                }
-                uint32_t pf[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        // a key that a row does not see adds nothing, whatever its value is
-                        const float w0 = p[n][2 * r], w1 = p[n][2 * r + 1];
-                        pf[n][r] = transpose8(pack_f16(w0 == 0.f ? 0.f : w0 * vs[r], w1 == 0.f ? 0.f : w1 * vs[r]));
-                        z[gr][n][0] += w0 == 0.f ? 0.f : w0 * vm[r];
-                        z[gr][n][1] += w1 == 0.f ? 0.f : w1 * vm[r];
-                    }
-                }
-                const uint32_t words[4] = {vw[gr].x, vw[gr].y, vw[gr].z, vw[gr].w};
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
-                    // 1024 + c and 64 + c in fp16, less 1032 and 72: c - 8, exact
-                    const uint32_t x = words[mt], y = x >> 8;
-                    uint32_t A[4] = {(x & 0x000F000Fu) | 0x64006400u, (x & 0x00F000F0u) | 0x54005400u,
-                                     (y & 0x000F000Fu) | 0x64006400u, (y & 0x00F000F0u) | 0x54005400u};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __half2 off = __float2half2_rn((i & 1) ? 72.f : 1032.f);
-                        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&A[i]), off);
-                        A[i] = *reinterpret_cast<const uint32_t*>(&v);
+                    for (int c = 0; c < 4; ++c) {
+                        p[k][n][c] = ex2_approx(p[k][n][c]);
+                        l[n][c & 1] += p[k][n][c];
                     }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16_16816(acc[gr][mt][n], A, pf[n][0], pf[n][1]);
+                for (int gr = 0; gr < G; ++gr) {
+                    const uint4 codes = reinterpret_cast<const uint4*>(pieces + k * kBytes + (G + gr) * 512)[lane];
+                    uint32_t pf[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float w0 = p[k][n][2 * r], w1 = p[k][n][2 * r + 1];
+                            pf[n][r] = transpose8(pack_f16(w0 * vw[k][gr][r], w1 * vw[k][gr][r]));
+                            z[gr][n][0] = fmaf(w0, vm[k][gr][r], z[gr][n][0]);
+                            z[gr][n][1] = fmaf(w1, vm[k][gr][r], z[gr][n][1]);
+                        }
+                    const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) {
+                        // 1024 + c and 64 + c in fp16, less 1032 and 72: c - 8, exact
+                        const uint32_t x = words[mt], y = x >> 8;
+                        uint32_t A[4] = {(x & 0x000F000Fu) | 0x64006400u, (x & 0x00F000F0u) | 0x54005400u,
+                                         (y & 0x000F000Fu) | 0x64006400u, (y & 0x00F000F0u) | 0x54005400u};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __half2 off = __float2half2_rn((i & 1) ? 72.f : 1032.f);
+                            const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&A[i]), off);
+                            A[i] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16_16816(acc[gr][mt][n], A, pf[n][0], pf[n][1]);
+                    }
                 }
             }
         }
+        cp_async_wait<0>();
 
-        // ---- the item's result: normalised, with the logarithm (base 2) of its sum
-        const float vback = pow2i(-vexp);
+        // ---- the warps' results side by side in shared memory, then weighed: normalised, with
+        // the logarithm (base 2) of the sum
+        __syncthreads();  // no warp needs its pieces any more
+        float* results = reinterpret_cast<float*>(s_ring);  // [warp][row][value]
+        const float vback = 1.f / vmul;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -420,90 +537,149 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) zs[gr] += __shfl_xor_sync(0xffffffffu, zs[gr], o);
                 }
-                const int r = row0 + n * 8 + 2 * tq + c;
-                if (r >= n_rows) continue;
-                const int qi = r / a.share, qh = h * a.share + r % a.share;
-                // (query rows of requests that overlap, which cu_q must not have, could
-                // make more partial rows than the workspace holds)
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const float lse2 = sum == 0.f ? -INFINITY : ref[n][c] + log2f(sum);
-                const bool whole = rq.chunks == 1;
-                const int64_t row = whole ? int64_t(rq.q0 + qi) * a.q_heads + qh
-                                          : (b ? s_req.parts[b - 1] : 0) + (int64_t(split) * rq.nq + qi) * a.q_heads + qh;
-                if (!whole && (row < 0 || row >= a.part_rows)) {
-                    if (g == 0) atomicOr(a.flags, kFlagBounds);
-                    continue;
-                }
+                const int r = n * 8 + 2 * tq + c;
                 if (g == 0) {
-                    if (!whole)
-                        a.part_lse[row] = lse2;
-                    else if (a.lse)
-                        a.lse[row] = lse2 * 0.6931471805599453f;
+                    s_ref[warp][r] = ref[n][c];
+                    s_sum[warp][r] = sum;
                 }
+                float* dst = results + (warp * 8 * NT + r) * (64 * G);
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr)
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const float o = fmaf(acc[gr][mt][n][c + 2 * half], vback, zs[gr]) * inv;
-                            const int64_t at = row * (64 * G) + gr * 64 + mt * 16 + half * 8 + g;
-                            if (!whole)
-                                a.part_o[at] = o;
-                            else if (a.dtype == 0)
-                                static_cast<uint16_t*>(a.out)[at] = float_to_bf16(o);
-                            else
-                                static_cast<__half*>(a.out)[at] = __float2half_rn(o);
-                        }
+                        for (int half = 0; half < 2; ++half)
+                            dst[gr * 64 + mt * 16 + half * 8 + g] = fmaf(acc[gr][mt][n][c + 2 * half], vback, zs[gr]);
             }
+        __syncthreads();
+        const int rows = last_row - row0 + 1;
+        const bool whole = rq.chunks == 1;
+        for (int r = warp; r < rows; r += kAttendWarps) {
+            float wgt[kAttendWarps], top = -1e30f, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kAttendWarps; ++i) top = fmaxf(top, s_ref[i][r]);
+#pragma unroll
+            for (int i = 0; i < kAttendWarps; ++i) {
+                wgt[i] = ex2_approx(s_ref[i][r] - top);
+                sum = fmaf(s_sum[i][r], wgt[i], sum);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+            const int qi = (row0 + r) / a.share, qh = h * a.share + (row0 + r) % a.share;
+            // (query rows of requests that overlap, which cu_q must not have, could make more
+            // partial rows than the workspace holds)
+            const int64_t row = whole ? int64_t(rq.q0 + qi) * a.q_heads + qh
+                                      : (b ? s_req.parts[b - 1] : 0) + (int64_t(split) * rq.nq + qi) * a.q_heads + qh;
+            if (!whole && (row < 0 || row >= a.part_rows)) {
+                if (lane == 0) atomicOr(a.flags, kFlagBounds);
+                continue;
+            }
+            if (lane == 0) {
+                if (!whole)
+                    a.part_lse[row] = lse2;
+                else if (a.lse)
+                    a.lse[row] = lse2 * 0.6931471805599453f;
+            }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kAttendWarps; ++i) {
+                    const float2 x = *reinterpret_cast<const float2*>(results + (i * 8 * NT + r) * (64 * G) + gr * 64 + lane * 2);
+                    o.x = fmaf(x.x, wgt[i], o.x);
+                    o.y = fmaf(x.y, wgt[i], o.y);
+                }
+                o.x *= inv;
+                o.y *= inv;
+                const int64_t at = row * (64 * G) + gr * 64 + lane * 2;
+                if (!whole)
+                    *reinterpret_cast<float2*>(a.part_o + at) = o;
+                else
+                    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
+                        a.dtype == 0 ? pack_bf16(o.x, o.y) : pack_f16(o.x, o.y);
+            }
+        }
+        __syncthreads();  // the results make room for the next item's pieces
     }
 }
 
-// Weighs the splits of one (query row, head): one warp, two (or four) values a lane.
-template <int G>
+// Weighs the splits of one (query row, head): W warps, which share out the splits eight at a
+// time (all loads of eight splits are under way at once) and meet in shared memory; two values
+// of each group a lane.
+template <int G, int W>
 __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs a) {
     griddep_wait();
     griddep_launch();
-    const int lane = threadIdx.x & 31;
+    __shared__ float s_top[8], s_sum[8], s_o[8][64 * G];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
     const int b = blockIdx.y;
-    const int64_t item = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t item = int64_t(blockIdx.x) * (8 / W) + warp / W;
     const Request r = request_of(a, b, false);
-    if (r.chunks == 1 || item >= int64_t(r.nq) * a.q_heads) return;
     const int64_t p0 = a.part_off[b] + item, stride = int64_t(r.nq) * a.q_heads;
-    if (p0 < 0 || p0 + (r.chunks - 1) * stride >= a.part_rows) return;  // reported by the attention kernel
-    float top = -INFINITY, sum = 0.f, o[2 * G] = {};
-    for (int k0 = 0; k0 < r.chunks; k0 += 32) {
-        const int k = k0 + lane;
-        const float x = k < r.chunks ? a.part_lse[p0 + k * stride] : -INFINITY;
-        const float mx = fmaxf(top, warp_max(x));
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        const float corr = exp2f(top - ref);
-        const float w = exp2f(x - ref);
-        sum = sum * corr + warp_sum(w);
+    // a row of a request of one split is finished; one outside the workspace has been reported
+    const bool live = r.chunks > 1 && item < stride && p0 >= 0 && p0 + (r.chunks - 1) * stride < a.part_rows;
+    float top = -1e30f, sum = 0.f, o[2 * G] = {};
+    if (live)
+        for (int k0 = part * 8; k0 < r.chunks; k0 += 8 * W) {
+            const int n = min(8, r.chunks - k0);
+            const float x = lane < n ? a.part_lse[p0 + (k0 + lane) * stride] : -INFINITY;
+            float2 v[8][G];
 #pragma unroll
-        for (int i = 0; i < 2 * G; ++i) o[i] *= corr;
-        const int n = min(32, r.chunks - k0);
-        for (int j = 0; j < n; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            if (wj == 0.f) continue;  // a split that sees nothing, or weighs nothing
-            const float* src = a.part_o + (p0 + (k0 + j) * stride) * (64 * G) + lane * 2 * G;
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    v[j][i] = j < n ? *reinterpret_cast<const float2*>(a.part_o + (p0 + (k0 + j) * stride) * (64 * G) + i * 64 + lane * 2)
+                                    : make_float2(0.f, 0.f);
+            const float mx = fmaxf(top, warp_max(x));
+            const float corr = ex2_approx(top - mx), w = ex2_approx(x - mx);
+            sum = sum * corr + warp_sum(w);
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i) o[i] *= corr;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    o[2 * i] = fmaf(v[j][i].x, wj, o[2 * i]);
+                    o[2 * i + 1] = fmaf(v[j][i].y, wj, o[2 * i + 1]);
+                }
+            }
+            top = mx;
+        }
+    if (W > 1) {
+        if (lane == 0) {
+            s_top[warp] = top;
+            s_sum[warp] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) *reinterpret_cast<float2*>(&s_o[warp][i * 64 + lane * 2]) = make_float2(o[2 * i], o[2 * i + 1]);
+        __syncthreads();
+        if (part != 0) return;
+        float all = -1e30f;
+        for (int j = 0; j < W; ++j) all = fmaxf(all, s_top[warp + j]);
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) o[i] = 0.f;
+        for (int j = 0; j < W; ++j) {
+            const float w = ex2_approx(s_top[warp + j] - all);
+            sum = fmaf(s_sum[warp + j], w, sum);
 #pragma unroll
             for (int i = 0; i < G; ++i) {
-                const float2 v = *reinterpret_cast<const float2*>(src + 2 * i);
-                o[2 * i] = fmaf(v.x, wj, o[2 * i]);
-                o[2 * i + 1] = fmaf(v.y, wj, o[2 * i + 1]);
+                const float2 v = *reinterpret_cast<const float2*>(&s_o[warp + j][i * 64 + lane * 2]);
+                o[2 * i] = fmaf(v.x, w, o[2 * i]);
+                o[2 * i + 1] = fmaf(v.y, w, o[2 * i + 1]);
             }
         }
-        top = mx;
+        top = all;
     }
+    if (!live) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t row = int64_t(r.q0) * a.q_heads + item;
-    if (lane == 0 && a.lse)
-        a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * (64 * G) + lane * 2 * G);
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * (64 * G)) + lane;
 #pragma unroll
     for (int i = 0; i < G; ++i)
-        out[i] = a.dtype == 0 ? pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv) : pack_f16(o[2 * i] * inv, o[2 * i + 1] * inv);
+        out[i * 32] = a.dtype == 0 ? pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv) : pack_f16(o[2 * i] * inv, o[2 * i + 1] * inv);
 }
 
 namespace {
@@ -538,9 +714,13 @@ cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s) {
     else
         e = nt == 1 ? launch_attend<2, 1>(a, s) : launch_attend<2, 2>(a, s);
     if (e != cudaSuccess || a.max_chunks <= 1) return e;
-    const dim3 grid(unsigned((int64_t(a.max_q) * a.q_heads + 7) / 8), unsigned(a.B));
-    if (a.c.groups == 1) return launch_pdl(cache_merge_kernel<1>, grid, dim3(256), 0, s, a);
-    return launch_pdl(cache_merge_kernel<2>, grid, dim3(256), 0, s, a);
+    // long memories: a row's splits are shared out among the eight warps of a CTA
+    const bool wide = a.max_chunks > 16;
+    const int per = wide ? 1 : 8;
+    const dim3 grid(unsigned((int64_t(a.max_q) * a.q_heads + per - 1) / per), unsigned(a.B));
+    auto merge = a.c.groups == 1 ? (wide ? cache_merge_kernel<1, 8> : cache_merge_kernel<1, 1>)
+                                 : (wide ? cache_merge_kernel<2, 8> : cache_merge_kernel<2, 1>);
+    return launch_pdl(merge, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace clef

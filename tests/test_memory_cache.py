@@ -83,10 +83,10 @@ def test_read_refusals():
 
 def test_attend_refusals():
     c = cache()
-    n = B.clef_cache_attend_workspace(c, 2, 6, 8, 16 * 64)
+    n = B.clef_cache_attend_workspace(c, 2, 6, 8, 40 * 64)
     assert n > 0 and B.clef_cache_attend_workspace(c, 2, 6, 8, 256) == 0
     #       0  1  2  3  4  5  6  7       8  9        10  11 12 13  14 15   16 17 18 19 20 21
-    good = [c, 2, 6, 4, 8, 0, 4, B.BF16, P, 8 * 64, 64, P, P, 16, P, 0.125, 1, P, P, P, P, n]
+    good = [c, 2, 6, 4, 8, 0, 4, B.BF16, P, 8 * 64, 64, P, P, 40, P, 0.125, 1, P, P, P, P, n]
     for at in (8, 11, 12, 14, 17, 19, 20):
         refused(1, B.clef_cache_attend, *changed(good, at, 0))
     for at, value in ((0, cache(data=0)), (1, 0), (2, -1), (3, -1), (3, 7), (4, 0), (4, 6), (5, 1), (6, 0), (6, 5),
@@ -129,12 +129,12 @@ def test_stream_finish_memory_refusals():
     bt, cfg, sch = _head_args()
     ws = B.clef_workspace_size(cfg, sch)
     c = cache(heads=32)
-    space = B.clef_cache_attend_workspace(c, 2, sch.O, 16, 7 * 64)
+    space = B.clef_cache_attend_workspace(c, 2, sch.O, 16, 40 * 64)
     weights = [P] * B.clef_weight_count(cfg)
     first = [min(int(sch.q_span.reshape(-1, 2)[sch.q_rec == b].min()), int(min(
         sch.o_span.reshape(-1, 2)[sch.q_opt_off[q]:sch.q_opt_off[q + 1]].min() for q in range(sch.Q) if sch.q_rec[q] == b)))
         for b in range(2)]
-    good = [cfg, weights, P, sch, first, P, B.BF16, P, P, P, P, P, P, P, P, ws, c, P, 7, P, P, space]
+    good = [cfg, weights, P, sch, first, P, B.BF16, P, P, P, P, P, P, P, P, ws, c, P, 40, P, P, space]
     for at in (2, 5, 7, 8, 9, 10, 11, 12, 13, 14, 17, 19, 20):
         refused(1, B.clef_stream_finish_memory, *changed(good, at, 0))
     for at, value in ((4, [first[0] + 1, first[1]]), (4, [first[0], int(bt.lengths[1])]), (4, [-1, 0]), (4, [0]),
