@@ -38,6 +38,7 @@ struct CacheAttendArgs {
     int B, total_q, max_q, q_heads, head0, kv_heads, share, dtype, width, causal;
     const void* q; int64_t q_row, q_head;
     const int32_t* cu_q; const int32_t* table; const int32_t* lengths;
+    uint64_t share_inv;  // ceil(2^40 / share)
     float scale_log2;
     void* out; float* lse; int32_t* flags;
     float* part_o; float* part_lse; int32_t* part_off;  // split partials, their row offset per request

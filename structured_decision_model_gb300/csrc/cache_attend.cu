@@ -46,6 +46,15 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same with nothing added.
+__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Transpose of an 8 x 8 block of 16-bit values held one row a group of four lanes.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -76,6 +85,11 @@ struct Requests {
     int parts[kCacheMaxRequests];   // partial rows of requests 0 .. b
     int tmp[2][kAttendWarps];
 };
+
+// r / share for query rows: share_inv = ceil(2^40 / share), exact while r * share < 2^40.
+__device__ __forceinline__ int by_share(const CacheAttendArgs& a, int r) {
+    return int((uint64_t(uint32_t(r)) * a.share_inv) >> 40);
+}
 
 struct Request {
     int len, q0, nq, chunks;
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
         const int t0 = split * kAttendChunk;
         int t1 = min(t0 + kAttendChunk, rq.len);
         const int ahead = rq.len - rq.nq;  // causal: query i sees keys 0 .. ahead + i
-        if (a.causal) t1 = min(t1, ahead + last_row / a.share + 1);
+        if (a.causal) t1 = min(t1, ahead + by_share(a, last_row) + 1);
 
         // ---- pages of the split and the first pieces: warp w takes steps w, w + 4, ...
         const int p0 = t0 >> a.c.page_shift;
@@ -214,18 +228,28 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
             s_page[threadIdx.x] = at;
         }
         const bool holes = __syncthreads_or(hole);
+        // pages of 32 tokens and more hold a step's pieces side by side (what lies behind the
+        // last token is never used)
         auto request_step = [&](int t, int stage) {
-            uint8_t* dst = ring + stage * (KP * kBytes);
-#pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const int tk = t + 16 * k;
-                if (tk < t1) {
-                    const uint8_t* page = s_page[(tk >> a.c.page_shift) - p0];
-                    const uint8_t* src = page + ((tk & page_mask) >> 4) * kBytes;
+            if (t < t1) {
+                uint8_t* dst = ring + stage * (KP * kBytes) + lane * 16;
+                const int col = (t >> a.c.page_shift) - p0;
+                if (a.c.page_shift > 4) {
+                    const uint8_t* page = s_page[col];
+                    const uint8_t* src = page + ((t & page_mask) >> 4) * kBytes + lane * 16;
                     if (page)
 #pragma unroll
-                        for (int i = 0; i < kBytes; i += 512)
-                            if (i + lane * 16 < kBytes) cp_async16(dst + k * kBytes + i + lane * 16, src + i + lane * 16, true);
+                        for (int i = 0; i < KP * kBytes; i += 512)
+                            if (i + lane * 16 < KP * kBytes) cp_async16(dst + i, src + i, true);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < KP; ++k) {
+                        const uint8_t* src = t + 16 * k < t1 ? s_page[col + k] : nullptr;
+                        if (src)
+#pragma unroll
+                            for (int i = 0; i < kBytes; i += 512)
+                                if (i + lane * 16 < kBytes) cp_async16(dst + k * kBytes + i, src + lane * 16 + i, true);
+                    }
                 }
             }
             cp_async_commit();
@@ -244,7 +268,7 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
         for (int n = 0; n < NT; ++n) {
             const int r = row0 + n * 8 + g;
             const bool live = r < n_rows;
-            const int qi = live ? r / a.share : 0, qh = h * a.share + (live ? r % a.share : 0);
+            const int qi = live ? by_share(a, r) : 0, qh = h * a.share + (live ? r - qi * a.share : 0);
             const uint16_t* q = static_cast<const uint16_t*>(a.q) + (rq.q0 + qi) * a.q_row + qh * a.q_head;
             float2 x[G][8];
             float top = 0.f, sum[G];
@@ -282,7 +306,7 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                 for (int gr = 0; gr < G; ++gr)
                     qsum[gr][n][c] = __shfl_sync(0xffffffffu, sum[gr], from) * a.scale_log2;
                 const int rc = row0 + n * 8 + 2 * tq + c;
-                vis[n][c] = a.causal ? min(t1, ahead + rc / a.share + 1) : t1;
+                vis[n][c] = a.causal ? min(t1, ahead + by_share(a, rc) + 1) : t1;
             }
         }
 
@@ -332,18 +356,18 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                         vs[k][gr][r] = bf16_lo(sm.y);
                         vm[k][gr][r] = bf16_hi(sm.y);
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) part[k][gr][n][c] = 0.f;
                     const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t x = words[i], y = x >> 8;
                         const uint32_t A[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma_f16_16816(part[k][gr][n], A, qf[gr][n][2 * i], qf[gr][n][2 * i + 1]);
+                        for (int n = 0; n < NT; ++n) {
+                            if (i == 0)
+                                mma_f16_16816_first(part[k][gr][n], A, qf[gr][n][0], qf[gr][n][1]);
+                            else
+                                mma_f16_16816(part[k][gr][n], A, qf[gr][n][2 * i], qf[gr][n][2 * i + 1]);
+                        }
                     }
                 }
             // ---- scores (base 2) less their row's reference
@@ -554,8 +578,12 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
         __syncthreads();
         const int rows = last_row - row0 + 1;
         const bool whole = rq.chunks == 1;
-        for (int r = warp; r < rows; r += kAttendWarps) {
-            float wgt[kAttendWarps], top = -1e30f, sum = 0.f;
+        // warp w finishes rows w, w + 4, ...: lane i weighs the i-th of them, then all lanes its values
+        float wgt[kAttendWarps];
+        int64_t row = -1;
+        if (lane < 2 * NT) {
+            const int r = warp + kAttendWarps * lane;
+            float top = -1e30f, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) top = fmaxf(top, s_ref[i][r]);
 #pragma unroll
@@ -564,34 +592,41 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                 sum = fmaf(s_sum[i][r], wgt[i], sum);
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-            const int qi = (row0 + r) / a.share, qh = h * a.share + (row0 + r) % a.share;
-            // (query rows of requests that overlap, which cu_q must not have, could make more
-            // partial rows than the workspace holds)
-            const int64_t row = whole ? int64_t(rq.q0 + qi) * a.q_heads + qh
-                                      : (b ? s_req.parts[b - 1] : 0) + (int64_t(split) * rq.nq + qi) * a.q_heads + qh;
-            if (!whole && (row < 0 || row >= a.part_rows)) {
-                if (lane == 0) atomicOr(a.flags, kFlagBounds);
-                continue;
+#pragma unroll
+            for (int i = 0; i < kAttendWarps; ++i) wgt[i] *= inv;
+            if (r < rows) {
+                const int qi = by_share(a, row0 + r), qh = h * a.share + (row0 + r) - qi * a.share;
+                row = whole ? int64_t(rq.q0 + qi) * a.q_heads + qh
+                            : (b ? s_req.parts[b - 1] : 0) + (int64_t(split) * rq.nq + qi) * a.q_heads + qh;
+                // (query rows of requests that overlap, which cu_q must not have, could make
+                // more partial rows than the workspace holds)
+                if (!whole && (row < 0 || row >= a.part_rows)) {
+                    atomicOr(a.flags, kFlagBounds);
+                    row = -1;
+                }
+                const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+                if (row >= 0 && !whole) a.part_lse[row] = lse2;
+                if (whole && a.lse) a.lse[row] = lse2 * 0.6931471805599453f;
             }
-            if (lane == 0) {
-                if (!whole)
-                    a.part_lse[row] = lse2;
-                else if (a.lse)
-                    a.lse[row] = lse2 * 0.6931471805599453f;
-            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * NT; ++j) {
+            const int64_t to = __shfl_sync(0xffffffffu, row, j);
+            float wj[kAttendWarps];
+#pragma unroll
+            for (int i = 0; i < kAttendWarps; ++i) wj[i] = __shfl_sync(0xffffffffu, wgt[i], j);
+            if (to < 0) continue;
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 float2 o = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kAttendWarps; ++i) {
-                    const float2 x = *reinterpret_cast<const float2*>(results + (i * 8 * NT + r) * (64 * G) + gr * 64 + lane * 2);
-                    o.x = fmaf(x.x, wgt[i], o.x);
-                    o.y = fmaf(x.y, wgt[i], o.y);
+                    const float2 x = *reinterpret_cast<const float2*>(results + (i * 8 * NT + warp + kAttendWarps * j) * (64 * G) +
+                                                                      gr * 64 + lane * 2);
+                    o.x = fmaf(x.x, wj[i], o.x);
+                    o.y = fmaf(x.y, wj[i], o.y);
                 }
-                o.x *= inv;
-                o.y *= inv;
-                const int64_t at = row * (64 * G) + gr * 64 + lane * 2;
+                const int64_t at = to * (64 * G) + gr * 64 + lane * 2;
                 if (!whole)
                     *reinterpret_cast<float2*>(a.part_o + at) = o;
                 else
@@ -599,7 +634,7 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                         a.dtype == 0 ? pack_bf16(o.x, o.y) : pack_f16(o.x, o.y);
             }
         }
-        __syncthreads();  // the results make room for the next item's pieces
+        // (the barrier that publishes the next item's pages makes room for its pieces)
     }
 }
 
