@@ -78,12 +78,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, int dtype) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// What a CTA needs to know of every request: the ends of its work items and of its partial
-// rows, as running sums.
+// What a CTA needs to know of every request, in shared memory: the ends of its work items and
+// of its partial rows as running sums, its keys, its first query row and its query rows.
 struct Requests {
-    int items[kCacheMaxRequests];   // work items of requests 0 .. b
-    int parts[kCacheMaxRequests];   // partial rows of requests 0 .. b
-    int tmp[2][kAttendWarps];
+    int *items, *parts, *len, *q0, *nq;
+    __device__ Requests(int* base, int n) : items(base), parts(base + n), len(base + 2 * n), q0(base + 3 * n), nq(base + 4 * n) {}
 };
 
 // r / share for query rows: share_inv = ceil(2^40 / share), exact while r * share < 2^40.
@@ -113,8 +112,9 @@ __device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, b
     return r;
 }
 
-// Fills the running sums; every thread of the CTA takes a run of neighbouring requests.
-__device__ __forceinline__ void scan_requests(const CacheAttendArgs& a, Requests& s, int rows_per_item) {
+// Fills the tables; every thread of the CTA takes a run of neighbouring requests.
+__device__ __forceinline__ void scan_requests(const CacheAttendArgs& a, const Requests& s, int rows_per_item) {
+    __shared__ int tmp[2][kAttendWarps];
     const int per = (a.B + kAttendThreads - 1) / kAttendThreads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b0 = threadIdx.x * per, b1 = min(b0 + per, a.B);
@@ -125,6 +125,9 @@ __device__ __forceinline__ void scan_requests(const CacheAttendArgs& a, Requests
         parts += r.chunks > 1 ? r.chunks * r.nq * a.q_heads : 0;
         s.items[b] = items;
         s.parts[b] = parts;
+        s.len[b] = r.len;
+        s.q0[b] = r.q0;
+        s.nq[b] = r.nq;
     }
     int ei = items, ep = parts;
 #pragma unroll
@@ -136,19 +139,58 @@ __device__ __forceinline__ void scan_requests(const CacheAttendArgs& a, Requests
         }
     }
     if (lane == 31) {
-        s.tmp[0][warp] = ei;
-        s.tmp[1][warp] = ep;
+        tmp[0][warp] = ei;
+        tmp[1][warp] = ep;
     }
     __syncthreads();
     for (int w = 0; w < warp; ++w) {
-        ei += s.tmp[0][w];
-        ep += s.tmp[1][w];
+        ei += tmp[0][w];
+        ep += tmp[1][w];
     }
     for (int b = b0; b < b1; ++b) {
         s.items[b] += ei - items;
         s.parts[b] += ep - parts;
     }
     __syncthreads();
+}
+
+// A work item: a split of request b's keys, key/value head h, a block of its query rows.
+struct Item {
+    int b, h, split, row0, rows, t0, t1, ahead, p0;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Item item_of(const CacheAttendArgs& a, const Requests& s, int w) {
+    Item k;
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s.items[mid] <= w)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    k.b = lo;
+    const int it = w - (lo ? s.items[lo - 1] : 0);
+    const int len = s.len[lo], nq = s.nq[lo];
+    const int n_rows = nq * a.share;
+    const int n_blocks = (n_rows + ROWS - 1) / ROWS;
+    const int rest = n_blocks == 1 ? it : it / n_blocks;
+    k.row0 = (it - rest * n_blocks) * ROWS;
+    k.split = rest / a.kv_heads;
+    k.h = rest - k.split * a.kv_heads;
+    k.rows = min(ROWS, n_rows - k.row0);
+    k.t0 = k.split * kAttendChunk;
+    k.t1 = min(k.t0 + kAttendChunk, len);
+    k.ahead = len - nq;  // causal: query i sees keys 0 .. ahead + i
+    if (a.causal) k.t1 = min(k.t1, k.ahead + by_share(a, k.row0 + k.rows - 1) + 1);
+    k.p0 = k.t0 >> a.c.page_shift;
+    return k;
+}
+
+// One 4-byte word to shared memory, asynchronously.
+__device__ __forceinline__ void cp_async4(void* smem_dst, const void* gsrc) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gsrc) : "memory");
 }
 
 }  // namespace
@@ -158,11 +200,11 @@ struct AttendSmem {
     // 16-token pieces a step: two where the registers allow, which halves the cost of a step's
     // waits, votes and addresses
     static constexpr int kPieces = 2;
-    // steps in flight a warp; the same bytes then hold the warps' results
+    // steps in flight a warp
     static constexpr int kStages = G == 2 ? 2 : NT <= 2 ? 3 : 4;
     static constexpr int kRing = kAttendWarps * kStages * kPieces * kPiece * G;
-    static constexpr int kResults = kAttendWarps * 8 * NT * 64 * G * 4;
-    static constexpr int kBytes = kRing > kResults ? kRing : kResults;
+    static constexpr int kResults = kAttendWarps * 8 * NT * 64 * G * 4;  // the warps' sums of values
+    static constexpr int kBytes = kRing + kResults + 2 * kAttendWarps * 8 * NT * 4;
 };
 
 template <int G, int NT>
@@ -170,12 +212,15 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
     using Smem = AttendSmem<G, NT>;
     constexpr int ST = Smem::kStages, KP = Smem::kPieces;
     constexpr int kBytes = kPiece * G;
+    constexpr int kMaxPages = kAttendChunk / 16;
     griddep_wait();
     griddep_launch();
-    __shared__ Requests s_req;
-    __shared__ __align__(16) uint8_t s_ring[Smem::kBytes];
-    __shared__ float s_ref[kAttendWarps][8 * NT], s_sum[kAttendWarps][8 * NT];
-    __shared__ const uint8_t* s_page[kAttendChunk / 16];  // the split's pages, null where there is none
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* results = reinterpret_cast<float*>(smem + Smem::kRing);  // [warp][row][value]
+    float* s_ref = results + Smem::kResults / 4;                     // [warp][row]
+    float* s_sum = s_ref + kAttendWarps * 8 * NT;
+    const Requests s_req(reinterpret_cast<int*>(smem + Smem::kBytes), a.B);
+    __shared__ int s_page[2][kMaxPages];  // page numbers of the split at hand and of the next one
     scan_requests(a, s_req, 8 * NT);
     if (blockIdx.x == 0 && a.part_off)
         for (int b = threadIdx.x; b < a.B; b += kAttendThreads) a.part_off[b] = b ? s_req.parts[b - 1] : 0;
@@ -184,92 +229,96 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
     const int g = lane >> 2, tq = lane & 3;
     const int n_items = s_req.items[a.B - 1];
     const int page_mask = a.c.page - 1;
-    uint8_t* ring = s_ring + warp * (ST * KP * kBytes);
+    uint8_t* ring = smem + warp * (ST * KP * kBytes);
+    constexpr int kStride = 16 * KP * kAttendWarps;
 
-    for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
-        // ---- the item: request b, split, key/value head, block of query rows
-        int lo = 0, hi = a.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_req.items[mid] <= w)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        const int b = lo;
-        const Request rq = request_of(a, b, false);
-        int it = w - (b ? s_req.items[b - 1] : 0);
-        const int n_rows = rq.nq * a.share;
-        const int n_blocks = (n_rows + 8 * NT - 1) / (8 * NT);
-        const int qb = it % n_blocks;
-        it /= n_blocks;
-        const int h = it % a.kv_heads, split = it / a.kv_heads;
-        const int row0 = qb * 8 * NT;
-        const int last_row = min(row0 + 8 * NT, n_rows) - 1;
-        const int t0 = split * kAttendChunk;
-        int t1 = min(t0 + kAttendChunk, rq.len);
-        const int ahead = rq.len - rq.nq;  // causal: query i sees keys 0 .. ahead + i
-        if (a.causal) t1 = min(t1, ahead + by_share(a, last_row) + 1);
-
-        // ---- pages of the split and the first pieces: warp w takes steps w, w + 4, ...
-        const int p0 = t0 >> a.c.page_shift;
-        bool hole = false;
-        if (threadIdx.x < kAttendChunk / 16) {
-            const int p = p0 + threadIdx.x;
-            const uint8_t* at = nullptr;
-            if ((int64_t(p) << a.c.page_shift) < t1) {
-                const int id = a.table[int64_t(b) * a.width + p];
-                hole = id < 0 || id >= a.c.n_pages;
-                if (hole)
-                    atomicOr(a.flags, kFlagBounds);
-                else
-                    at = a.c.data + ((int64_t(id) * a.c.heads + a.head0 + h) << (a.c.page_shift - 4)) * kBytes;
-            }
-            s_page[threadIdx.x] = at;
-        }
-        const bool holes = __syncthreads_or(hole);
-        // pages of 32 tokens and more hold a step's pieces side by side (what lies behind the
-        // last token is never used)
-        auto request_step = [&](int t, int stage) {
-            if (t < t1) {
-                uint8_t* dst = ring + stage * (KP * kBytes) + lane * 16;
-                const int col = (t >> a.c.page_shift) - p0;
-                if (a.c.page_shift > 4) {
-                    const uint8_t* page = s_page[col];
-                    const uint8_t* src = page + ((t & page_mask) >> 4) * kBytes + lane * 16;
-                    if (page)
+    // Items run into one another: while the pieces of one are worked off, the next one's page
+    // numbers arrive; its first pieces and queries are requested before the results of the
+    // first are weighed.
+    auto request_pages = [&](const Item& k, int* to) {
+        if (threadIdx.x < kMaxPages && (int64_t(k.p0 + threadIdx.x) << a.c.page_shift) < k.t1)
+            cp_async4(to + threadIdx.x, a.table + int64_t(k.b) * a.width + k.p0 + threadIdx.x);
+    };
+    // does the item lack a page? (all lanes of the warp get the answer)
+    auto lacks_pages = [&](const Item& k, const int* pages) {
+        bool bad = false;
 #pragma unroll
-                        for (int i = 0; i < KP * kBytes; i += 512)
-                            if (i + lane * 16 < KP * kBytes) cp_async16(dst + i, src + i, true);
-                } else {
+        for (int i = lane; i < kMaxPages; i += 32)
+            if ((int64_t(k.p0 + i) << a.c.page_shift) < k.t1) bad |= pages[i] < 0 || pages[i] >= a.c.n_pages;
+        if (bad) atomicOr(a.flags, kFlagBounds);
+        return bool(__any_sync(0xffffffffu, bad));
+    };
+    auto piece_at = [&](const Item& k, const int* pages, int t) -> const uint8_t* {
+        const int id = pages[(t >> a.c.page_shift) - k.p0];
+        if (id < 0 || id >= a.c.n_pages) return nullptr;
+        return a.c.data + (((int64_t(id) * a.c.heads + a.head0 + k.h) << (a.c.page_shift - 4)) + ((t & page_mask) >> 4)) * kBytes;
+    };
+    // pages of 32 tokens and more hold a step's pieces side by side (what lies behind the
+    // last token is never used)
+    auto request_step = [&](const Item& k, const int* pages, int t, int stage) {
+        if (t < k.t1) {
+            uint8_t* dst = ring + stage * (KP * kBytes) + lane * 16;
+            if (a.c.page_shift > 4) {
+                const uint8_t* src = piece_at(k, pages, t);
+                if (src)
 #pragma unroll
-                    for (int k = 0; k < KP; ++k) {
-                        const uint8_t* src = t + 16 * k < t1 ? s_page[col + k] : nullptr;
-                        if (src)
+                    for (int i = 0; i < KP * kBytes; i += 512)
+                        if (i + lane * 16 < KP * kBytes) cp_async16(dst + i, src + lane * 16 + i, true);
+            } else {
 #pragma unroll
-                            for (int i = 0; i < kBytes; i += 512)
-                                if (i + lane * 16 < kBytes) cp_async16(dst + k * kBytes + i, src + lane * 16 + i, true);
-                    }
+                for (int j = 0; j < KP; ++j) {
+                    const uint8_t* src = t + 16 * j < k.t1 ? piece_at(k, pages, t + 16 * j) : nullptr;
+                    if (src)
+#pragma unroll
+                        for (int i = 0; i < kBytes; i += 512)
+                            if (i + lane * 16 < kBytes) cp_async16(dst + j * kBytes + i, src + lane * 16 + i, true);
                 }
             }
-            cp_async_commit();
-        };
-        constexpr int kStride = 16 * KP * kAttendWarps;
-        const int t_first = t0 + warp * 16 * KP;
-        int t_next = t_first;
+        }
+        cp_async_commit();
+    };
+    auto request_first = [&](const Item& k, const int* pages) {
 #pragma unroll
-        for (int s = 0; s < ST - 1; ++s, t_next += kStride) request_step(t_next, s);
+        for (int s = 0; s < ST - 1; ++s) request_step(k, pages, k.t0 + warp * 16 * KP + s * kStride, s);
+    };
+    // a lane's query words: rows g of each block of 8, values 2 tq, 2 tq + 1 of each run of 8
+    auto load_queries = [&](const Item& k, uint32_t (&qw)[NT][G][8]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = n * 8 + g;
+            const bool live = r < k.rows;
+            const int qi = live ? by_share(a, k.row0 + r) : 0;
+            const int qh = k.h * a.share + (live ? k.row0 + r - qi * a.share : 0);
+            const uint16_t* q = static_cast<const uint16_t*>(a.q) + (s_req.q0[k.b] + qi) * a.q_row + qh * a.q_head + 2 * tq;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    qw[n][gr][i] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + gr * 64 + i * 8)) : 0u;
+        }
+    };
+
+    int w = blockIdx.x;
+    if (w >= n_items) return;
+    Item me = item_of<8 * NT>(a, s_req, w);
+    request_pages(me, s_page[0]);
+    cp_async_commit();
+    uint32_t qw[NT][G][8];
+    load_queries(me, qw);
+    cp_async_wait<0>();
+    __syncthreads();
+    request_first(me, s_page[0]);
+
+    for (int turn = 0;; turn ^= 1) {
+        const int* pages = s_page[turn];
+        const int t0 = me.t0, t1 = me.t1, ahead = me.ahead;
+        const bool holes = lacks_pages(me, pages);
 
         // ---- queries: B operand of S^T, one row a group of four lanes
         uint32_t qf[G][NT][8];
         float qscale[NT][2], qsum[G][NT][2];  // of rows 2 tq, 2 tq + 1 of each block of 8
-        int vis[NT][2];                       // keys that those rows see: 0 .. vis - 1
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = row0 + n * 8 + g;
-            const bool live = r < n_rows;
-            const int qi = live ? by_share(a, r) : 0, qh = h * a.share + (live ? r - qi * a.share : 0);
-            const uint16_t* q = static_cast<const uint16_t*>(a.q) + (rq.q0 + qi) * a.q_row + qh * a.q_head;
             float2 x[G][8];
             float top = 0.f, sum[G];
 #pragma unroll
@@ -277,8 +326,7 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                 sum[gr] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint32_t word = live ? *reinterpret_cast<const uint32_t*>(q + gr * 64 + i * 8 + 2 * tq) : 0u;
-                    x[gr][i] = unpack2(word, a.dtype);
+                    x[gr][i] = unpack2(qw[n][gr][i], a.dtype);
                     sum[gr] += x[gr][i].x + x[gr][i].y;
                     top = fmaxf(top, fmaxf(fabsf(x[gr][i].x), fabsf(x[gr][i].y)));
                 }
@@ -305,8 +353,6 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr)
                     qsum[gr][n][c] = __shfl_sync(0xffffffffu, sum[gr], from) * a.scale_log2;
-                const int rc = row0 + n * 8 + 2 * tq + c;
-                vis[n][c] = a.causal ? min(t1, ahead + by_share(a, rc) + 1) : t1;
             }
         }
 
@@ -331,11 +377,20 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                     for (int c = 0; c < 4; ++c) acc[gr][mt][n][c] = 0.f;
         float vmul = pow2i(120);  // value scales are multiplied by a power of two, to at most 8
 
+        // the next item's page numbers come in with the pieces of this one
+        const int w_next = w + gridDim.x;
+        const bool more = w_next < n_items;
+        Item next = me;
+        if (more) {
+            next = item_of<8 * NT>(a, s_req, w_next);
+            request_pages(next, s_page[turn ^ 1]);
+        }
+
         int stage = 0;
-        for (int t = t_first; t < t1; t += kStride, t_next += kStride) {
+        for (int t = t0 + warp * 16 * KP; t < t1; t += kStride) {
             cp_async_wait<ST - 2>();
             __syncwarp();  // this step's pieces are there, and every lane is done with those before
-            request_step(t_next, stage == 0 ? ST - 1 : stage - 1);
+            request_step(me, pages, t + (ST - 1) * kStride, stage == 0 ? ST - 1 : stage - 1);
             const uint8_t* pieces = ring + stage * (KP * kBytes);
             stage = stage == ST - 1 ? 0 : stage + 1;
 
@@ -393,7 +448,7 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
 #pragma unroll
                 for (int k = 0; k < KP; ++k) {
                     const int tk = t + 16 * k;
-                    const int end = tk < t1 && s_page[(tk >> a.c.page_shift) - p0] ? t1 : 0;
+                    const int end = tk < t1 && piece_at(me, pages, tk) ? t1 : 0;
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
                         if (tk + g + 8 * r >= end)
@@ -402,8 +457,10 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (tk + g + 8 * (c >> 1) >= min(vis[n][c & 1], end)) p[k][n][c] = -INFINITY;
+                        for (int c = 0; c < 4; ++c) {
+                            const int sees = a.causal ? ahead + by_share(a, me.row0 + n * 8 + 2 * tq + (c & 1)) + 1 : end;
+                            if (tk + g + 8 * (c >> 1) >= min(sees, end)) p[k][n][c] = -INFINITY;
+                        }
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr)
 #pragma unroll
@@ -541,12 +598,12 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                 }
             }
         }
+        cp_async_commit();  // page numbers, where the warp had no step
         cp_async_wait<0>();
 
         // ---- the warps' results side by side in shared memory, then weighed: normalised, with
         // the logarithm (base 2) of the sum
-        __syncthreads();  // no warp needs its pieces any more
-        float* results = reinterpret_cast<float*>(s_ring);  // [warp][row][value]
+        __syncthreads();  // the results of the item before this one are no longer read
         const float vback = 1.f / vmul;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -563,8 +620,8 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                 }
                 const int r = n * 8 + 2 * tq + c;
                 if (g == 0) {
-                    s_ref[warp][r] = ref[n][c];
-                    s_sum[warp][r] = sum;
+                    s_ref[warp * 8 * NT + r] = ref[n][c];
+                    s_sum[warp * 8 * NT + r] = sum;
                 }
                 float* dst = results + (warp * 8 * NT + r) * (64 * G);
 #pragma unroll
@@ -575,9 +632,12 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                         for (int half = 0; half < 2; ++half)
                             dst[gr * 64 + mt * 16 + half * 8 + g] = fmaf(acc[gr][mt][n][c + 2 * half], vback, zs[gr]);
             }
-        __syncthreads();
-        const int rows = last_row - row0 + 1;
-        const bool whole = rq.chunks == 1;
+        __syncthreads();  // the results and the next item's page numbers are there
+        if (more) {
+            request_first(next, s_page[turn ^ 1]);
+            load_queries(next, qw);
+        }
+        const bool whole = s_req.len[me.b] <= kAttendChunk;
         // warp w finishes rows w, w + 4, ...: lane i weighs the i-th of them, then all lanes its values
         float wgt[kAttendWarps];
         int64_t row = -1;
@@ -585,19 +645,19 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
             const int r = warp + kAttendWarps * lane;
             float top = -1e30f, sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kAttendWarps; ++i) top = fmaxf(top, s_ref[i][r]);
+            for (int i = 0; i < kAttendWarps; ++i) top = fmaxf(top, s_ref[i * 8 * NT + r]);
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) {
-                wgt[i] = ex2_approx(s_ref[i][r] - top);
-                sum = fmaf(s_sum[i][r], wgt[i], sum);
+                wgt[i] = ex2_approx(s_ref[i * 8 * NT + r] - top);
+                sum = fmaf(s_sum[i * 8 * NT + r], wgt[i], sum);
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) wgt[i] *= inv;
-            if (r < rows) {
-                const int qi = by_share(a, row0 + r), qh = h * a.share + (row0 + r) - qi * a.share;
-                row = whole ? int64_t(rq.q0 + qi) * a.q_heads + qh
-                            : (b ? s_req.parts[b - 1] : 0) + (int64_t(split) * rq.nq + qi) * a.q_heads + qh;
+            if (r < me.rows) {
+                const int qi = by_share(a, me.row0 + r), qh = me.h * a.share + me.row0 + r - qi * a.share;
+                row = whole ? int64_t(s_req.q0[me.b] + qi) * a.q_heads + qh
+                            : (me.b ? s_req.parts[me.b - 1] : 0) + (int64_t(me.split) * s_req.nq[me.b] + qi) * a.q_heads + qh;
                 // (query rows of requests that overlap, which cu_q must not have, could make
                 // more partial rows than the workspace holds)
                 if (!whole && (row < 0 || row >= a.part_rows)) {
@@ -634,7 +694,9 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
                         a.dtype == 0 ? pack_bf16(o.x, o.y) : pack_f16(o.x, o.y);
             }
         }
-        // (the barrier that publishes the next item's pages makes room for its pieces)
+        if (!more) return;
+        me = next;
+        w = w_next;
     }
 }
 
@@ -721,15 +783,20 @@ namespace {
 
 template <int G, int NT>
 cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
+    constexpr int kMost = AttendSmem<G, NT>::kBytes + kCacheMaxRequests * 20;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
-    static int resident = 0;
+    static int resident = 0;  // CTAs an SM for few requests
+    const int bytes = AttendSmem<G, NT>::kBytes + a.B * 20;
     std::call_once(once, [] {
-        err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_kernel<G, NT>, kAttendThreads, 0);
+        err = cudaFuncSetAttribute(cache_attend_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (err == cudaSuccess)
+            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_kernel<G, NT>, kAttendThreads,
+                                                                AttendSmem<G, NT>::kBytes + 64 * 20);
     });
     if (err != cudaSuccess) return err;
     return launch_pdl(cache_attend_kernel<G, NT>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
-                      0, s, a);
+                      bytes, s, a);
 }
 
 }  // namespace
