@@ -43,7 +43,8 @@ bool bad_table(const clef_cache* c, int B, int stride) {
 struct AttendSpace {
     int64_t rows = 0, lse = 0, off = 0, bytes = 0;  // partial rows; byte offsets; total
     AttendSpace(int64_t B, int64_t total_q, int64_t q_heads, int64_t dim, int64_t max_len) {
-        const int64_t chunks = (max_len + kAttendChunk - 1) / kAttendChunk;
+        const int64_t chunk = attend_chunk(1);  // the shortest splits of any call
+        const int64_t chunks = (max_len + chunk - 1) / chunk;
         if (chunks <= 1 || total_q < 1) return;
         rows = total_q * q_heads * chunks;
         lse = rows * dim * 4;
@@ -104,6 +105,7 @@ int clef_cache_append(const clef_cache* cache, int32_t n_tokens, int32_t head0, 
     a.n_tokens = n_tokens; a.head0 = head0; a.n_heads = n_heads; a.dtype = dtype;
     a.k = k; a.k_row = k_row_stride; a.k_head = k_head_stride;
     a.v = v; a.v_row = v_row_stride; a.v_head = v_head_stride;
+    a.aligned = !misaligned(k, 16) && !misaligned(v, 16) && (k_row_stride | k_head_stride | v_row_stride | v_head_stride) % 8 == 0;
     a.slots = slots; a.flags = flags;
     CKC(launch_cache_append(a, static_cast<cudaStream_t>(stream)));
     return CLEF_OK;
@@ -157,7 +159,8 @@ int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32
     const int64_t max_len = int64_t(table_stride) * cache->page;
     const AttendSpace sp(B, total_q, q_heads, cache->head_dim, max_len);
     // items and partial rows are counted in 32 bits on the GPU
-    const int64_t chunks = (max_len + kAttendChunk - 1) / kAttendChunk;
+    a.chunk = attend_chunk(kv_heads);
+    const int64_t chunks = (max_len + a.chunk - 1) / a.chunk;
     if (sp.rows >= kInt32 || chunks * (int64_t(max_q) * (q_heads / kv_heads) / 8 + 1) * kv_heads * B >= kInt32 ||
         int64_t(max_q) * q_heads >= kInt32 ||
         int64_t(max_q) * (q_heads / kv_heads) >= (int64_t(1) << 40) / (q_heads / kv_heads))

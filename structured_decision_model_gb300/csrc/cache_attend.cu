@@ -39,7 +39,7 @@ constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -48,7 +48,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
 
 // The same with nothing added.
 __device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -58,7 +58,7 @@ __device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], const uint32_
 // Transpose of an 8 x 8 block of 16-bit values held one row a group of four lanes.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, b
         q1 = min(max(q1, r.q0), a.total_q);
     }
     r.nq = min(q1 - r.q0, a.max_q);
-    r.chunks = max(1, int((int64_t(r.len) + kAttendChunk - 1) / kAttendChunk));
+    r.chunks = max(1, int((int64_t(r.len) + a.chunk - 1) / a.chunk));
     return r;
 }
 
@@ -180,8 +180,8 @@ __device__ __forceinline__ Item item_of(const CacheAttendArgs& a, const Requests
     k.split = rest / a.kv_heads;
     k.h = rest - k.split * a.kv_heads;
     k.rows = min(ROWS, n_rows - k.row0);
-    k.t0 = k.split * kAttendChunk;
-    k.t1 = min(k.t0 + kAttendChunk, len);
+    k.t0 = k.split * a.chunk;
+    k.t1 = min(k.t0 + a.chunk, len);
     k.ahead = len - nq;  // causal: query i sees keys 0 .. ahead + i
     if (a.causal) k.t1 = min(k.t1, k.ahead + by_share(a, k.row0 + k.rows - 1) + 1);
     k.p0 = k.t0 >> a.c.page_shift;
@@ -208,11 +208,11 @@ struct AttendSmem {
 };
 
 template <int G, int NT>
-__global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const CacheAttendArgs a) {
+__global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : NT == 2 ? 3 : 2) cache_attend_kernel(const CacheAttendArgs a) {
     using Smem = AttendSmem<G, NT>;
     constexpr int ST = Smem::kStages, KP = Smem::kPieces;
     constexpr int kBytes = kPiece * G;
-    constexpr int kMaxPages = kAttendChunk / 16;
+    constexpr int kMaxPages = kAttendMaxChunk / 16;
     griddep_wait();
     griddep_launch();
     extern __shared__ __align__(16) uint8_t smem[];
@@ -236,8 +236,9 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
     // numbers arrive; its first pieces and queries are requested before the results of the
     // first are weighed.
     auto request_pages = [&](const Item& k, int* to) {
-        if (threadIdx.x < kMaxPages && (int64_t(k.p0 + threadIdx.x) << a.c.page_shift) < k.t1)
-            cp_async4(to + threadIdx.x, a.table + int64_t(k.b) * a.width + k.p0 + threadIdx.x);
+        for (int i = threadIdx.x; i < kMaxPages; i += kAttendThreads)
+            if ((int64_t(k.p0 + i) << a.c.page_shift) < k.t1)
+                cp_async4(to + i, a.table + int64_t(k.b) * a.width + k.p0 + i);
     };
     // does the item lack a page? (all lanes of the warp get the answer)
     auto lacks_pages = [&](const Item& k, const int* pages) {
@@ -637,7 +638,7 @@ __global__ void __launch_bounds__(kAttendThreads) cache_attend_kernel(const Cach
             request_first(next, s_page[turn ^ 1]);
             load_queries(next, qw);
         }
-        const bool whole = s_req.len[me.b] <= kAttendChunk;
+        const bool whole = s_req.len[me.b] <= a.chunk;
         // warp w finishes rows w, w + 4, ...: lane i weighs the i-th of them, then all lanes its values
         float wgt[kAttendWarps];
         int64_t row = -1;
