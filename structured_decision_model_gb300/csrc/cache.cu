@@ -9,27 +9,37 @@ namespace clef {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanFused = 8 * kPlanThreads;  // slots that the plan kernel itself fills
+constexpr int kPlanCtas = 8;  // CTAs of a large step's cluster
 
-// Inclusive sum over the block's threads (1024), in thread order; `tmp` holds 32 values.
-__device__ __forceinline__ int block_scan(int x, int* tmp) {
+// Inclusive sums of two numbers over the block's threads (1024), in thread order; `tmp` holds
+// 2 x 32 values.
+__device__ __forceinline__ int2 block_scan(int x, int y, int (*tmp)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) {
+            x += u;
+            y += v;
+        }
     }
     __syncthreads();  // tmp may still be read by the previous scan
-    if (lane == 31) tmp[warp] = x;
+    if (lane == 31) {
+        tmp[0][warp] = x;
+        tmp[1][warp] = y;
+    }
     __syncthreads();
-    int t = tmp[lane];
+    int s = tmp[0][lane], t = tmp[1][lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, t, o);
-        if (lane >= o) t += y;
+        const int u = __shfl_up_sync(0xffffffffu, s, o), v = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) {
+            s += u;
+            t += v;
+        }
     }
-    const int before = __shfl_sync(0xffffffffu, t, warp > 0 ? warp - 1 : 0);
-    return x + (warp > 0 ? before : 0);
+    const int bx = __shfl_sync(0xffffffffu, s, max(warp - 1, 0)), by = __shfl_sync(0xffffffffu, t, max(warp - 1, 0));
+    return warp > 0 ? make_int2(x + bx, y + by) : make_int2(x, y);
 }
 
 // Number of entries of the non-decreasing `ends` (n of them) that are <= i.
@@ -45,48 +55,40 @@ __device__ __forceinline__ int upper(const int* ends, int n, int i) {
     return lo;
 }
 
-// Slots of gained tokens [first, end) in steps of `step`; `cu` holds the B + 1 running sums
-// and `lengths` the new lengths, so that token t of request b is at position
-// lengths[b] - (cu[b + 1] - cu[b]) + t - cu[b].
-__device__ __forceinline__ void fill_slots(const CachePlanArgs& a, const int* cu, int first, int end, int step) {
-    const int total = cu[a.B];
-    for (int t = first; t < end; t += step) {
-        int slot = -1;
-        if (t < total) {
-            const int b = min(upper(cu + 1, a.B, t), a.B - 1);
-            const int pos = a.lengths[b] - cu[b + 1] + t;
-            const int col = pos >> a.page_shift;
-            const int id = pos >= 0 && col < a.width ? a.table[int64_t(b) * a.width + col] : -1;
-            if (id < 0 || id >= a.n_pages)
-                atomicOr(a.flags, kFlagBounds);
-            else
-                slot = (id << a.page_shift) | (pos & ((1 << a.page_shift) - 1));
-        }
-        a.slots[t] = slot;
-    }
-}
-
 }  // namespace
 
-// One CTA, one thread a request: what each request gives back and needs, three scans over
-// the requests, then the page moves spread evenly over the threads (a search in the scans
-// finds the request of each page).  Bound by its chain of dependent steps, not by bytes.
-__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePlanArgs a, int fill) {
+// Page accounts: one CTA, or a cluster of them that share out the page moves and the slots
+// (each CTA works out what every request gives back, needs and gains by itself, one thread a
+// request, in three scans; a search in the sums finds the request of a page or slot).  Three
+// phases with the cluster's barrier between them: pages come back, pages are granted, slots
+// are written.  Bound by the latency of these dependent steps, not by bytes; each thread has
+// four moves under way at a time.
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePlanArgs a) {
     griddep_wait();
     griddep_launch();
-    __shared__ int tmp[32];
-    __shared__ int s_rel[kPlanThreads], s_more[kPlanThreads], s_have[kPlanThreads], s_cu[kPlanThreads + 1];
+    __shared__ int tmp[2][32];
+    __shared__ int s_rel[kPlanThreads], s_more[kPlanThreads], s_have[kPlanThreads], s_old[kPlanThreads];
+    __shared__ int s_cu[kPlanThreads + 1];
     __shared__ int s_grant;
     const int t = threadIdx.x;
+    const bool alone = gridDim.x == 1;
+    const int first = blockIdx.x * kPlanThreads + t, step = gridDim.x * kPlanThreads;
     const int page = 1 << a.page_shift;
     const int64_t cap = int64_t(a.width) << a.page_shift;
+    const bool lead = blockIdx.x == 0;  // reports, and writes what there is one of
+    auto meet = [&] {
+        if (alone)
+            __syncthreads();
+        else
+            cluster_sync();
+    };
     int old = 0, want = 0, have = 0, need = 0;
     if (t < a.B) {
         old = a.lengths[t];
         want = a.want[t];
         const bool bad_old = old < 0 || old > cap;
         if (bad_old || want < 0 || want > cap) {
-            atomicOr(a.flags, kFlagBounds);
+            if (lead) atomicOr(a.flags, kFlagBounds);
             want = old;  // left as it is
         }
         if (!bad_old) {
@@ -96,81 +98,137 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePla
     }
     int count = *a.free_count;
     if (count < 0 || count > a.n_pages) {
-        if (t == 0) atomicOr(a.flags, kFlagBounds);
+        if (lead && t == 0) atomicOr(a.flags, kFlagBounds);
         count = count < 0 ? 0 : a.n_pages;
     }
-    const int rel = max(have - need, 0), more = max(need - have, 0);
-    const int rel_end = block_scan(rel, tmp);
-    const int more_end = block_scan(more, tmp);
-    s_rel[t] = rel_end;
-    s_more[t] = more_end;
+    if (t == 0) s_grant = 0;
+    const int more = max(need - have, 0);
+    const int2 ends = block_scan(max(have - need, 0), more, tmp);
+    s_rel[t] = ends.x;
+    s_more[t] = ends.y;
     s_have[t] = have;
+    s_old[t] = old;
     __syncthreads();
     const int n_rel = s_rel[kPlanThreads - 1];
-    // give back: ascending index i of (request, page) pairs; the stack takes them in descending order
-    for (int i = t; i < n_rel; i += kPlanThreads) {
-        const int b = upper(s_rel, a.B, i);
-        const int last = s_have[b] - 1, j = s_rel[b] - 1 - i;  // j-th page from the request's end
-        const int64_t at = int64_t(b) * a.width + last - j;
-        const int pos = count + n_rel - 1 - i;
-        const int id = a.table[at];
-        a.table[at] = -1;
-        if (pos < a.n_pages)
-            a.free_pages[pos] = id;
-        else
-            atomicOr(a.flags, kFlagBounds);  // more pages came back than there are
-    }
     const int top = min(count + n_rel, a.n_pages);
-    const bool fits = more == 0 || more_end <= top;
-    if (t == 0) s_grant = 0;
-    __syncthreads();
-    if (fits && more > 0) atomicMax(&s_grant, more_end);
-    const int gain_end = block_scan(fits ? max(want - old, 0) : 0, tmp);
-    s_cu[t + 1] = gain_end;
+    const bool fits = more == 0 || ends.y <= top;
+    if (fits && more > 0) atomicMax(&s_grant, ends.y);
+    s_cu[t + 1] = block_scan(fits ? max(want - old, 0) : 0, 0, tmp).x;
     if (t == 0) s_cu[0] = 0;
     __syncthreads();
+    // give back: ascending index i of (request, page) pairs; the stack takes them in descending order
+    for (int i0 = first; i0 < n_rel; i0 += 4 * step) {
+        int id[4];
+        int64_t at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * step;
+            if (i >= n_rel) continue;
+            const int b = upper(s_rel, a.B, i);
+            at[u] = int64_t(b) * a.width + s_have[b] - (s_rel[b] - i);
+            id[u] = a.table[at[u]];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * step, pos = count + n_rel - 1 - i;
+            if (i >= n_rel) continue;
+            a.table[at[u]] = -1;
+            if (pos < a.n_pages)
+                a.free_pages[pos] = id[u];
+            else
+                atomicOr(a.flags, kFlagBounds);  // more pages came back than there are
+        }
+    }
+    meet();  // everyone has read the old lengths and count; the pages that came back are on the stack
     const int grant = s_grant;  // requests fit in order, so the granted pages are the first ones
-    for (int i = t; i < grant; i += kPlanThreads) {
-        const int b = upper(s_more, a.B, i);
-        const int first = b > 0 ? s_more[b - 1] : 0;
-        const int pos = top - 1 - i;
-        a.table[int64_t(b) * a.width + s_have[b] + i - first] = a.free_pages[pos];
-        a.free_pages[pos] = -1;
+    for (int i0 = first; i0 < grant; i0 += 4 * step) {
+        int id[4];
+        int64_t at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * step;
+            if (i >= grant) continue;
+            const int b = upper(s_more, a.B, i);
+            at[u] = int64_t(b) * a.width + s_have[b] + i - (b > 0 ? s_more[b - 1] : 0);
+            id[u] = a.free_pages[top - 1 - i];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * step;
+            if (i >= grant) continue;
+            a.table[at[u]] = id[u];
+            a.free_pages[top - 1 - i] = -1;
+        }
     }
-    if (t < a.B) {
-        if (fits)
-            a.lengths[t] = want;
-        else
-            atomicOr(a.flags, kFlagPages);
+    if (lead) {
+        if (t < a.B) {
+            if (fits)
+                a.lengths[t] = want;
+            else
+                atomicOr(a.flags, kFlagPages);
+            a.cu[t] = s_cu[t];
+        }
+        if (t == 0) {
+            a.cu[a.B] = s_cu[a.B];
+            *a.free_count = top - grant;
+            if (s_cu[a.B] > a.n_slots) atomicOr(a.flags, kFlagBounds);
+        }
     }
-    if (t <= a.B) a.cu[t] = s_cu[t];
-    if (t == 0) {
-        if (a.B == kPlanThreads) a.cu[a.B] = s_cu[a.B];
-        *a.free_count = top - grant;
-        if (s_cu[a.B] > a.n_slots) atomicOr(a.flags, kFlagBounds);
+    meet();  // the tables are as they will be
+    // one slot a thread, or four neighbouring ones: one search, and one page number where they
+    // share a page
+    const int total = s_cu[a.B], per = a.n_slots <= step ? 1 : 4;
+    for (int64_t i0 = per * int64_t(first); i0 < a.n_slots; i0 += per * int64_t(step)) {
+        int slot[4] = {-1, -1, -1, -1};
+        if (i0 < total) {
+            int b = min(upper(s_cu + 1, a.B, int(i0)), a.B - 1), at = -1, id = -1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = int(i0) + u;
+                if (u >= per || i >= total || i >= a.n_slots) break;
+                while (b < a.B - 1 && i >= s_cu[b + 1]) {
+                    ++b;
+                    at = -1;
+                }
+                const int pos = s_old[b] + i - s_cu[b], col = pos >> a.page_shift;
+                if (col != at) {
+                    at = col;
+                    id = pos >= 0 && col < a.width ? a.table[int64_t(b) * a.width + col] : -1;
+                    if (id < 0 || id >= a.n_pages) {
+                        atomicOr(a.flags, kFlagBounds);
+                        id = -1;
+                    }
+                }
+                if (id >= 0) slot[u] = (id << a.page_shift) | (pos & (page - 1));
+            }
+        }
+        if (per == 4 && i0 + 4 <= a.n_slots && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
+            *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (u < per && i0 + u < a.n_slots) a.slots[i0 + u] = slot[u];
+        }
     }
-    if (fill) {
-        __syncthreads();
-        fill_slots(a, s_cu, t, a.n_slots, kPlanThreads);
-    }
-}
-
-// Slots of a large step, after the plan kernel.
-__global__ void __launch_bounds__(256) cache_slots_kernel(const CachePlanArgs a) {
-    griddep_wait();
-    griddep_launch();
-    __shared__ int s_cu[kCacheMaxRequests + 1];
-    for (int i = threadIdx.x; i <= a.B; i += 256) s_cu[i] = a.cu[i];
-    __syncthreads();
-    const int64_t first = int64_t(blockIdx.x) * 1024;
-    fill_slots(a, s_cu, int(first) + threadIdx.x, int(min(int64_t(a.n_slots), first + 1024)), 256);
 }
 
 cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t s) {
-    const bool fused = a.n_slots <= kPlanFused;
-    cudaError_t e = launch_pdl(cache_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, fused ? 1 : 0);
-    if (e != cudaSuccess || fused) return e;
-    return launch_pdl(cache_slots_kernel, dim3(unsigned((a.n_slots + 1023) / 1024)), dim3(256), 0, s, a);
+    // A cluster pays from a few thousand slots on (its barriers take about a microsecond).
+    const unsigned ctas = a.n_slots > 4 * kPlanThreads ? kPlanCtas : 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return counted(cudaLaunchKernelEx(&cfg, cache_plan_kernel, a));
 }
 
 // ------------------------------------------------------------------- rows
@@ -313,22 +371,29 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[8], uint2* code
     const float lo = half_of<T>(lo2, 0), hi = half_of<T>(hi2, 0);
     const uint16_t mb = float_to_bf16(lo);
     const float m = bf16_to_float(mb), range = fmaxf(hi - m, 0.f);
-    const uint16_t sb = float_to_bf16(__fdiv_rn(range, 15.f));
+    // range / 15 by the same correction; tiny ranges, where the residual would lose bits, are divided
+    const float third = range * (1.f / 15.f);
+    float width = fmaf(fmaf(-third, 15.f, range), 1.f / 15.f, third);
+    if (!(range > 0x1p-90f && range < INFINITY)) width = __fdiv_rn(range, 15.f);
+    const uint16_t sb = float_to_bf16(width);
     const float s = bf16_to_float(sb);
     const bool bad = !(s < INFINITY && fabsf(m) < INFINITY);
     const bool flat = bad || s == 0.f;
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a small number added to it is rounded to an integer
     uint32_t t[16];
-    // tiny scales, and ranges that rounding took out of [0, 15 s], go the plain way
-    if (!flat && (s < 0x1p-100f || lo < m || range > 15.4f * s)) {
+    // tiny scales, and ranges that rounding took past 15 s, go the plain way
+    if (!flat && (s < 0x1p-90f || range > 15.4f * s)) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             t[i] = uint32_t(fminf(fmaxf(rintf(__fdiv_rn(less<T>(x[i >> 1], i & 1, m), s)), 0.f), 15.f));
     } else {
-        const float r = flat ? 0.f : __frcp_rn(s);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // within an ulp
+        if (flat) r = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float a = less<T>(x[i >> 1], i & 1, m);
+            float a = less<T>(x[i >> 1], i & 1, m);
+            if (T == 1) a = fmaxf(a, 0.f);  // m may have been rounded up past an fp16 minimum
             const float q = a * r;
             t[i] = __float_as_uint(fmaf(fmaf(-q, s, a), r, q) + kMagic);
         }
@@ -344,16 +409,15 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[8], uint2* code
 
 }  // namespace
 
-template <int T>
-__global__ void __launch_bounds__(32 * kRowsWarps) cache_append_kernel(const CacheRowsArgs a) {
+template <int T, int G>
+__global__ void __launch_bounds__(32 * kRowsWarps, 4) cache_append_kernel(const CacheRowsArgs a) {
     griddep_wait();
     griddep_launch();
-    __shared__ __align__(16) uint32_t s_piece[kRowsWarps][2 * kPiece / 4];
+    __shared__ __align__(16) uint32_t s_piece[kRowsWarps][G * kPiece / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.y * kRowsWarps + warp;
     if (head >= a.n_heads) return;
     const int64_t i0 = int64_t(blockIdx.x) * 16;
-    const int G = a.c.groups;
     const Window win = window_of(a.slots, i0, a.n_tokens, a.c.n_pages << a.c.page_shift, a.flags);
     const int r8 = lane >> 2, run = lane & 3;
     const uint16_t* k0 = static_cast<const uint16_t*>(a.k) + head * a.k_head + run * 16;
@@ -366,6 +430,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) cache_append_kernel(const Cac
         const int at = __ffs(start) - 1;
         uint32_t* piece = s_piece[warp];
         const int64_t row = i0 + at + r8;
+#pragma unroll
         for (int gr = 0; gr < G; ++gr) {
             uint32_t x[4][8];  // keys of rows r8 and r8 + 8, values of the same
 #pragma unroll
@@ -439,90 +504,135 @@ __global__ void __launch_bounds__(32 * kRowsWarps) cache_append_kernel(const Cac
 
 namespace {
 
-// The lane's 16 values from its eight bytes, scale and minimum, to a row of `T`.
+// Two codes as bf16 numbers (bits 0-3 and 16-19 of x): 128 + c, less 128, exact.
+__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+    const uint32_t w = (x & 0x000F000Fu) | 0x43004300u, off = 0x43004300u;
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&off));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// scale * c + minimum with c and the scale in bf16, in one fp32 rounding.
+__device__ __forceinline__ float stands_for(uint32_t c2, int hi, uint16_t scale, float m) {
+    const uint16_t c = uint16_t(hi ? c2 >> 16 : c2 & 0xffffu);
+    float d;
+    asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(c), "h"(scale), "f"(m));
+    return d;
+}
+
+// The lane's 16 values from its eight bytes, scale and minimum, to row `i` of `T` (i rows from
+// base, `live` where there is one).  Lanes 16 apart hold rows four apart: they swap halves, so
+// that a store instruction writes whole 32-byte sectors (half a sector at a time costs 1.3
+// times the time).  All lanes of the warp come here.
 template <int T>
-__device__ __forceinline__ void write16(void* base, int64_t at, uint2 code, uint32_t sm) {
-    const float s = bf16_lo(sm), m = bf16_hi(sm);
+__device__ __forceinline__ void write16(void* base, int64_t at, int64_t row_stride, bool live, bool other_live, uint2 code,
+                                        uint32_t sm) {
+    const uint16_t s = uint16_t(sm & 0xffffu);
+    const float m = bf16_hi(sm);
     float x[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t byte = (j < 4 ? code.x : code.y) >> (8 * (j & 3));
-        // 2^23 + c as bits, less 2^23
-        x[j] = fmaf(s, __uint_as_float((byte & 15u) | 0x4B000000u) - 8388608.f, m);
-        x[j + 8] = fmaf(s, __uint_as_float((byte >> 4 & 15u) | 0x4B000000u) - 8388608.f, m);
-    }
-    if (T == 2) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t w = h ? code.y : code.x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    } else {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (T == 0) {
-                w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-            } else {
-                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+        for (int e = 0; e < 4; ++e) {
+            // bits 4 e of bytes 0 and 2 (e < 2), of bytes 1 and 3 (e >= 2)
+            const uint32_t c = codes2(w >> (4 * (e & 1) + 8 * (e >> 1)));
+            const int j = 4 * h + (e >> 1) + 8 * (e & 1);
+            x[j] = stands_for(c, 0, s, m);
+            x[j + 2] = stands_for(c, 1, s, m);
         }
-        uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at);
-        p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    constexpr int kWords = T == 2 ? 16 : 8;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (T == 0) {
+            w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        } else if (T == 1) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            w[2 * i] = __float_as_uint(x[2 * i]);
+            w[2 * i + 1] = __float_as_uint(x[2 * i + 1]);
+        }
+    }
+    // 32 bytes at a time: the lower lane writes the first half of its own row and of the upper
+    // lane's, the upper lane the second halves
+    const bool upper_lane = threadIdx.x & 16;
+    uint32_t* p = static_cast<uint32_t*>(base) + at * (T == 2 ? 4 : 2) / 4;
+    const int64_t to_other = (upper_lane ? -4 : 4) * row_stride * (T == 2 ? 4 : 2) / 4;
+#pragma unroll
+    for (int i = 0; i < kWords; i += 8) {
+        uint32_t got[4], own[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            got[j] = __shfl_xor_sync(0xffffffffu, upper_lane ? w[i + j] : w[i + 4 + j], 16);
+            own[j] = upper_lane ? w[i + 4 + j] : w[i + j];
+        }
+        uint32_t* q = p + i + (upper_lane ? 4 : 0);
+        uint4* first = reinterpret_cast<uint4*>(upper_lane ? q + to_other : q);
+        uint4* second = reinterpret_cast<uint4*>(upper_lane ? q : q + to_other);
+        // rows of the lower lanes, then rows of the upper ones
+        if (upper_lane ? other_live : live)
+            *first = upper_lane ? make_uint4(got[0], got[1], got[2], got[3]) : make_uint4(own[0], own[1], own[2], own[3]);
+        if (upper_lane ? live : other_live)
+            *second = upper_lane ? make_uint4(own[0], own[1], own[2], own[3]) : make_uint4(got[0], got[1], got[2], got[3]);
     }
 }
 
 }  // namespace
 
-template <int T>
+template <int T, int G>
 __global__ void __launch_bounds__(32 * kRowsWarps) cache_read_kernel(const CacheRowsArgs a) {
     griddep_wait();
     griddep_launch();
+    // eight rows a warp; the warp beside it takes the next eight, which share its words
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = blockIdx.y * kRowsWarps + warp;
+    const int head = blockIdx.y * (kRowsWarps / 2) + (warp >> 1);
+    const int64_t i = int64_t(blockIdx.x) * 16 + (warp & 1) * 8 + (lane >> 2);
     if (head >= a.n_heads) return;
-    const int total = a.c.n_pages << a.c.page_shift, G = a.c.groups;
-    const int r8 = lane >> 2, run = lane & 3;
-    for (int half = 0; half < 2; ++half) {
-        const int64_t i = int64_t(blockIdx.x) * 16 + half * 8 + r8;
-        if (i >= a.n_tokens) continue;
-        const int slot = a.slots[i];
-        if (slot >= total && run == 0) atomicOr(a.flags, kFlagBounds);
-        const bool live = slot >= 0 && slot < total;
-        const int r = slot & 15, hi = r >> 3;
-        const uint8_t* piece = piece_of(a.c, live ? slot : 0, a.head0 + head);
-        for (int gr = 0; gr < G; ++gr) {
-            const int64_t at = (i * a.n_heads + head) * (64 * G) + gr * 64 + run * 16;
-            uint2 sm = make_uint2(0u, 0u), kc = make_uint2(0u, 0u), vc = make_uint2(0u, 0u);
-            if (live) {
-                sm = *reinterpret_cast<const uint2*>(piece + G * 1024 + (r * G + gr) * 8);
-                // words that hold the row's bytes beside those of its neighbours
-                const uint32_t* kw = reinterpret_cast<const uint32_t*>(piece + gr * 512) + (r & 7) * 16 + run;
-                const uint32_t* vw = reinterpret_cast<const uint32_t*>(piece + (G + gr) * 512) + ((r & 7) >> 1) * 4 + run;
-                const int ks = hi ? 0x7531 : 0x6420, vs = (r & 1) * 2 + hi;  // byte selectors
-                const uint32_t b0 = __byte_perm(kw[0], kw[4], ks), b1 = __byte_perm(kw[8], kw[12], ks);
-                kc = make_uint2(b0, b1);
-                const int pick = vs | (4 + vs) << 4;
-                vc.x = __byte_perm(__byte_perm(vw[0], vw[16], pick), __byte_perm(vw[32], vw[48], pick), 0x5410);
-                vc.y = __byte_perm(__byte_perm(vw[64], vw[80], pick), __byte_perm(vw[96], vw[112], pick), 0x5410);
-            }
-            write16<T>(a.out_k, at, kc, sm.x);
-            write16<T>(a.out_v, at, vc, sm.y);
+    const int run = lane & 3;
+    const bool there = i < a.n_tokens, other = (lane & 16 ? i - 4 : i + 4) < a.n_tokens;
+    const int slot = there ? a.slots[i] : -1, total = a.c.n_pages << a.c.page_shift;
+    if (slot >= total && run == 0) atomicOr(a.flags, kFlagBounds);
+    const bool live = slot >= 0 && slot < total;
+    const int r = slot & 15, hi = r >> 3;
+    const uint8_t* piece = piece_of(a.c, live ? slot : 0, a.head0 + head);
+    uint2 sm[G], kc[G], vc[G];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+        sm[gr] = kc[gr] = vc[gr] = make_uint2(0u, 0u);
+        if (live) {
+            sm[gr] = *reinterpret_cast<const uint2*>(piece + G * 1024 + (r * G + gr) * 8);
+            // words that hold the row's bytes beside those of its neighbours
+            const uint32_t* kw = reinterpret_cast<const uint32_t*>(piece + gr * 512) + (r & 7) * 16 + run;
+            const uint32_t* vw = reinterpret_cast<const uint32_t*>(piece + (G + gr) * 512) + ((r & 7) >> 1) * 4 + run;
+            const int ks = hi ? 0x7531 : 0x6420, at = (r & 1) * 2 + hi, vs = at | (4 + at) << 4;  // byte selectors
+            kc[gr] = make_uint2(__byte_perm(kw[0], kw[4], ks), __byte_perm(kw[8], kw[12], ks));
+            vc[gr].x = __byte_perm(__byte_perm(vw[0], vw[16], vs), __byte_perm(vw[32], vw[48], vs), 0x5410);
+            vc[gr].y = __byte_perm(__byte_perm(vw[64], vw[80], vs), __byte_perm(vw[96], vw[112], vs), 0x5410);
         }
+    }
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+        const int64_t row = int64_t(a.n_heads) * (64 * G), at = i * row + head * (64 * G) + gr * 64 + run * 16;
+        write16<T>(a.out_k, at, row, there, other, kc[gr], sm[gr].x);
+        write16<T>(a.out_v, at, row, there, other, vc[gr], sm[gr].y);
     }
 }
 
 cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t s) {
     if (a.n_tokens <= 0) return cudaSuccess;
     const dim3 grid(unsigned((int64_t(a.n_tokens) + 15) / 16), unsigned((a.n_heads + kRowsWarps - 1) / kRowsWarps));
-    auto kernel = a.dtype == 0 ? cache_append_kernel<0> : cache_append_kernel<1>;
+    auto kernel = a.c.groups == 1 ? (a.dtype == 0 ? cache_append_kernel<0, 1> : cache_append_kernel<1, 1>)
+                                  : (a.dtype == 0 ? cache_append_kernel<0, 2> : cache_append_kernel<1, 2>);
     return launch_pdl(kernel, grid, dim3(32 * kRowsWarps), 0, s, a);
 }
 
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t s) {
     if (a.n_tokens <= 0) return cudaSuccess;
-    const dim3 grid(unsigned((int64_t(a.n_tokens) + 15) / 16), unsigned((a.n_heads + kRowsWarps - 1) / kRowsWarps));
-    auto kernel = a.dtype == 0 ? cache_read_kernel<0> : a.dtype == 1 ? cache_read_kernel<1> : cache_read_kernel<2>;
+    const dim3 grid(unsigned((int64_t(a.n_tokens) + 15) / 16), unsigned((a.n_heads + kRowsWarps / 2 - 1) / (kRowsWarps / 2)));
+    auto kernel = a.c.groups == 1
+                      ? (a.dtype == 0 ? cache_read_kernel<0, 1> : a.dtype == 1 ? cache_read_kernel<1, 1> : cache_read_kernel<2, 1>)
+                      : (a.dtype == 0 ? cache_read_kernel<0, 2> : a.dtype == 1 ? cache_read_kernel<1, 2> : cache_read_kernel<2, 2>);
     return launch_pdl(kernel, grid, dim3(32 * kRowsWarps), 0, s, a);
 }
 

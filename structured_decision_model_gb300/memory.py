@@ -13,7 +13,6 @@ and ``plan`` with smaller lengths gives pages back.  Nothing here waits for the 
 The cache holds numbers, not gradients: tensors that require one are refused while grad
 mode is on.
 """
-import ctypes
 from typing import Optional, Tuple
 
 import torch
@@ -26,6 +25,27 @@ _DTYPES = {torch.bfloat16: B.BF16, torch.float16: B.FP16, torch.float32: B.FP32}
 def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
+
+
+class _On:
+    """The launches of one call: its device made current where it is not, and the handle of
+    that device's current stream.  (A decoding step calls this layer a few times per layer of
+    a model; the calls of an idle host are a few microseconds.)"""
+
+    __slots__ = ("index", "back")
+
+    def __init__(self, index):
+        self.index, self.back = index, None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
 
 
 def _refuse(why):
@@ -74,6 +94,10 @@ class MemoryCache:
         self.free_count, self.lengths = state[:1], state[1:1 + n]
         self.free_pages, self.block_table = state[1 + n:1 + n + p], state[1 + n + p:].view(n, self.width)
         self.flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._index = self.device.index if self.device.type == "cuda" else None
+        self._flags = self.flags.data_ptr()
+        self._accounts = [x.data_ptr() for x in (self.lengths, self.block_table, self.free_pages, self.free_count)]
+        self._lib = B.load()
 
     # ------------------------------------------------------------- checks
 
@@ -95,6 +119,15 @@ class MemoryCache:
             _refuse("block_table: contiguous int32 [requests, pages]")
         return table
 
+    def _on(self):
+        if self._index is None:
+            _refuse("the cache is not on a GPU")
+        return _On(self._index)
+
+    def _check(self, status, where):
+        if status != B.CLEF_OK:
+            raise B.ClefError(status, where)
+
     def _rows(self, t, what):
         self._on_device(t, what)
         if t.dim() != 3 or t.shape[2] != self.head_dim or t.stride(2) != 1 or t.dtype not in (torch.bfloat16, torch.float16):
@@ -113,19 +146,19 @@ class MemoryCache:
         self._on_device(want, "want")
         if want.dtype != torch.int32 or want.shape != (self.requests,) or not want.is_contiguous():
             _refuse("want: contiguous int32 [requests]")
-        with torch.cuda.device(self.device):
+        if slots is not None and self.checked_slots(slots).numel() != n_slots:
+            _refuse("slots: int32 [n_slots]")
+        if cu is not None and self.checked_slots(cu).numel() != self.requests + 1:
+            _refuse("cu: int32 [requests + 1]")
+        with self._on() as stream:
             if slots is None:
                 slots = torch.empty(n_slots, dtype=torch.int32, device=self.device)
-            elif self.checked_slots(slots).numel() != n_slots:
-                _refuse("slots: int32 [n_slots]")
             if cu is None:
                 cu = torch.empty(self.requests + 1, dtype=torch.int32, device=self.device)
-            elif self.checked_slots(cu).numel() != self.requests + 1:
-                _refuse("cu: int32 [requests + 1]")
-            B.clef_cache_plan(self.struct, self.requests, self.lengths.data_ptr(), want.data_ptr(),
-                              self.block_table.data_ptr(), self.width, self.free_pages.data_ptr(),
-                              self.free_count.data_ptr(), cu.data_ptr(), slots.data_ptr(), n_slots,
-                              self.flags.data_ptr(), stream_handle())
+            lengths, table, free_pages, free_count = self._accounts
+            self._check(self._lib.clef_cache_plan(self.struct, self.requests, lengths, want.data_ptr(), table, self.width,
+                                                  free_pages, free_count, cu.data_ptr(), slots.data_ptr(), n_slots,
+                                                  self._flags, stream), "clef_cache_plan")
         return slots, cu
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, head0: int = 0):
@@ -136,10 +169,12 @@ class MemoryCache:
             _refuse("k and v: one shape and type")
         if self.checked_slots(slots).numel() != k.shape[0]:
             _refuse("slots: one a row")
-        with torch.cuda.device(self.device):
-            B.clef_cache_append(self.struct, k.shape[0], head0, k.shape[1], dtype, k.data_ptr(), k.stride(0), k.stride(1),
-                                v.data_ptr(), v.stride(0), v.stride(1), slots.data_ptr(), self.flags.data_ptr(),
-                                stream_handle())
+        n, heads, _ = k.shape
+        ks, vs = k.stride(), v.stride()
+        with self._on() as stream:
+            self._check(self._lib.clef_cache_append(self.struct, n, head0, heads, dtype, k.data_ptr(), ks[0], ks[1],
+                                                    v.data_ptr(), vs[0], vs[1], slots.data_ptr(), self._flags, stream),
+                        "clef_cache_append")
 
     def read(self, slots: torch.Tensor, dtype=torch.bfloat16, head0: int = 0,
              heads: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -151,11 +186,11 @@ class MemoryCache:
         n = self.checked_slots(slots).numel()
         if heads < 1:
             _refuse("read: no heads")
-        with torch.cuda.device(self.device):
+        with self._on() as stream:
             k = torch.empty((n, heads, self.head_dim), dtype=dtype, device=self.device)
             v = torch.empty_like(k)
-            B.clef_cache_read(self.struct, n, head0, heads, _DTYPES[dtype], slots.data_ptr(), k.data_ptr(), v.data_ptr(),
-                              self.flags.data_ptr(), stream_handle())
+            self._check(self._lib.clef_cache_read(self.struct, n, head0, heads, _DTYPES[dtype], slots.data_ptr(),
+                                                  k.data_ptr(), v.data_ptr(), self._flags, stream), "clef_cache_read")
         return k, v
 
     def attend(self, q: torch.Tensor, cu_q: torch.Tensor, max_q: int, scale: Optional[float] = None,
@@ -178,24 +213,28 @@ class MemoryCache:
         table = self.checked_table(block_table, n)
         if n < 1 or lengths.numel() < n:
             _refuse("cu_q, lengths: one entry a request")
-        total, q_heads = q.shape[0], q.shape[1]
+        total, q_heads, _ = q.shape
+        strides = q.stride()
         scale = self.head_dim ** -0.5 if scale is None else scale
-        with torch.cuda.device(self.device):
+        if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or
+                                out.device != self.device):
+            _refuse("out: contiguous, of q's shape and type")
+        with self._on() as stream:
             if out is None:
                 out = torch.empty((total, q_heads, self.head_dim), dtype=q.dtype, device=self.device)
-            elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != self.device:
-                _refuse("out: contiguous, of q's shape and type")
             lse = torch.empty((total, q_heads), dtype=torch.float32, device=self.device)
             # a buffer of the call's own: overlapping calls and captured graphs never share one
             n_bytes = B.clef_cache_attend_workspace(self.struct, n, total, max(q_heads, 1), table.shape[1] * self.page)
-            space = torch.empty(n_bytes, dtype=torch.uint8, device=self.device)
-            B.clef_cache_attend(self.struct, n, total, max_q, q_heads, head0, kv_heads, dtype, q.data_ptr(), q.stride(0),
-                                q.stride(1), cu_q.data_ptr(), table.data_ptr(), table.shape[1], lengths.data_ptr(),
-                                scale, int(causal), out.data_ptr(), lse.data_ptr(), self.flags.data_ptr(),
-                                space.data_ptr() if n_bytes else None, n_bytes, stream_handle())
+            space = torch.empty(n_bytes, dtype=torch.uint8, device=self.device) if n_bytes else None
+            self._check(self._lib.clef_cache_attend(self.struct, n, total, max_q, q_heads, head0, kv_heads, dtype,
+                                                    q.data_ptr(), strides[0], strides[1], cu_q.data_ptr(),
+                                                    table.data_ptr(), table.shape[1], lengths.data_ptr(), scale,
+                                                    int(causal), out.data_ptr(), lse.data_ptr(), self._flags,
+                                                    space.data_ptr() if n_bytes else None, n_bytes, stream),
+                        "clef_cache_attend")
         return out, lse
 
     def device_status(self) -> int:
         """Waits for the current stream, reads and clears what the kernels reported."""
-        with torch.cuda.device(self.device):
-            return B.clef_cache_status(self.flags.data_ptr(), stream_handle())
+        with self._on() as stream:
+            return B.clef_cache_status(self._flags, stream)
