@@ -59,6 +59,7 @@ cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t s);
 cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_attend_rows(const CacheAttendArgs& a, cudaStream_t s);  // its requests of many query rows
 
 
 }  // namespace clef

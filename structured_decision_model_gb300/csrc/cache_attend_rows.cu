@@ -1,0 +1,511 @@
+// Attention over the paged 4-bit memory cache for requests of many query rows: options over a
+// record's memory, prompts in chunks.  (cache_attend.cu has the few-rows kernel, the formulas
+// of the codes and the launch.)
+//
+// A CTA of four warps takes a split of a request's keys, one key/value head and 64 query rows,
+// 16 a warp.  Here the queries are the M dimension, S = Q K^T and O += P V, and what the codes
+// cost is paid once for 64 rows: in a step of 64 keys each warp turns one 16-token piece into
+// fp16 operands in shared memory, in the order in which the lanes take them as the B operand,
+// and then all four pieces meet all rows.  Two buffers: a step's pieces are expanded while the
+// step before is multiplied, one barrier a step.
+//   Keys stay exact: codes as fp16 subnormals, and scores s_t (q . c_t) + m_t (sum q) in fp32,
+// where s_t comes with the scale of the softmax and of the queries' power of two on it.
+//   Values are rounded to fp16 once, (c - 8) s' + m' with s' = s 2^E and m' = (m + 8 s) 2^E:
+// half a step of 11 bits, as the weights (which then need no value scale, and sum to the
+// softmax's denominator themselves).  E is a multiple of 8 for each piece that puts its largest
+// value between 1 and 2^8, so neighbouring pieces hardly ever differ; where they do, the
+// weights of a piece are multiplied by the power of two between them.
+// The softmax reference of a row moves only when a score exceeds it by 2^8.
+#include <algorithm>
+#include <mutex>
+
+#include "cache_attend.cuh"
+
+namespace clef {
+
+namespace {
+
+constexpr int kRowsItem = 16 * kAttendWarps;  // query rows of an item
+constexpr int kRowsStep = 16 * kAttendWarps;  // keys of a step
+
+// Of an expanded piece: its exponent E, the tokens whose values are no numbers (a bit each, by
+// group of 64 values), and whether it is there at all.
+struct PieceInfo {
+    int exponent, bad0, bad1, absent;
+};
+
+template <int G>
+struct RowsSmem {
+    static constexpr int kStages = 3;                               // raw pieces a warp
+    static constexpr int kRaw = kAttendWarps * kStages * kPiece * G;
+    static constexpr int kOperand = 2048 * G;                       // 16 tokens x 64 G values in fp16
+    static constexpr int kScales = 16 * 8 * G;                      // scale and minimum of 16 keys in fp32
+    static constexpr int kExpanded = 2 * kOperand + kScales;
+    static constexpr int kBytes = kRaw + 2 * kAttendWarps * kExpanded;
+};
+
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                              *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, float b) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(b));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+}  // namespace
+
+template <int G>
+__global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_rows_kernel(const CacheAttendArgs a) {
+    using Smem = RowsSmem<G>;
+    constexpr int ST = Smem::kStages;
+    constexpr int kBytes = kPiece * G;
+    constexpr int kMaxPages = kAttendMaxChunk / 16;
+    griddep_wait();
+    griddep_launch();
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* expanded = smem + Smem::kRaw;  // [buffer][piece]{keys, values, scales}
+    const Requests s_req(reinterpret_cast<int*>(smem + Smem::kBytes), a.B);
+    __shared__ const uint8_t* s_page[kMaxPages];
+    __shared__ __align__(16) PieceInfo s_info[2][kAttendWarps];
+    __shared__ int s_exp[kAttendWarps];
+    scan_requests<true>(a, s_req, kRowsItem);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, tq = lane & 3;
+    const int n_items = s_req.items[a.B - 1];
+    const int page_mask = a.c.page - 1;
+    uint8_t* raw = smem + warp * (ST * kBytes);
+
+    for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
+        const Item me = item_of<kRowsItem>(a, s_req, w);
+        const int t0 = me.t0, t1 = me.t1, ahead = me.ahead;
+        // ---- the split's pages, and the queries of the warp's rows g and g + 8
+        for (int i = threadIdx.x; i < kMaxPages; i += kAttendThreads) {
+            const uint8_t* at = nullptr;
+            if ((int64_t(me.p0 + i) << a.c.page_shift) < t1) {
+                const int id = a.table[int64_t(me.b) * a.width + me.p0 + i];
+                if (id < 0 || id >= a.c.n_pages)
+                    atomicOr(a.flags, kFlagBounds);
+                else
+                    at = a.c.data + ((int64_t(id) * a.c.heads + a.head0 + me.h) << (a.c.page_shift - 4)) * kBytes;
+            }
+            s_page[i] = at;
+        }
+        uint32_t qw[2][G][8];
+        float top[2], qsum[2][G];
+        const int r0 = warp * 16 + g;  // the lane's rows of the item: r0 and r0 + 8
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const bool live = r0 + 8 * r < me.rows;
+            const int row = live ? me.row0 + r0 + 8 * r : 0, qi = by_share(a, row), qh = me.h * a.share + row - qi * a.share;
+            const uint16_t* q = static_cast<const uint16_t*>(a.q) + (s_req.q0[me.b] + qi) * a.q_row + qh * a.q_head + 2 * tq;
+            top[r] = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    qw[r][gr][i] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + gr * 64 + i * 8)) : 0u;
+                    const float2 x = unpack2(qw[r][gr][i], a.dtype);
+                    sum += x.x + x.y;
+                    top[r] = fmaxf(top[r], fmaxf(fabsf(x.x), fabsf(x.y)));
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                qsum[r][gr] = sum;
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
+        }
+        // One power of two for all rows of the item puts the largest value in [2^14, 2^15); rows
+        // that are far smaller (or no numbers) are scaled by themselves, and their scores by
+        // what is between.
+        int e[2], least = 1000;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int field = int(__float_as_uint(top[r]) >> 23);
+            e[r] = top[r] > 0.f ? min(14 - (field - 127), 120) : 120;
+            if (top[r] > 0.f && field < 255) least = min(least, e[r]);
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        __syncthreads();  // nothing of the item before this one is needed any more
+        if (lane == 0) s_exp[warp] = least;
+        __syncthreads();
+        int common = 1000;
+#pragma unroll
+        for (int i = 0; i < kAttendWarps; ++i) common = min(common, s_exp[i]);
+        if (common == 1000) common = 0;
+        float rowmul[2];
+        bool apart = false;
+        uint32_t qa[G][4][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const bool own = top[r] > 0.f && (e[r] - common > 10 || e[r] < common);
+            const int mine = own ? e[r] : common;
+            rowmul[r] = pow2i(common - mine);
+            apart |= own;
+            const float up = pow2i(mine);
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = (i & 1) ? up * 0.0625f : up;
+                    const float2 x = unpack2(qw[r][gr][i], a.dtype);
+                    qa[gr][i >> 1][(i & 1) * 2 + r] = pack_f16(x.x * f, x.y * f);
+                }
+        }
+        apart = __any_sync(0xffffffffu, apart);
+        const float score_mul = a.scale_log2 * pow2i(24 - common);
+
+        float acc[G][8][4];  // O: rows g (0, 1) and g + 8 (2, 3), values 8 n + 2 tq, + 1
+        float l[2] = {0.f, 0.f}, ref[2] = {0.f, 0.f}, none[2][G];
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+            none[0][gr] = none[1][gr] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) acc[gr][n][0] = acc[gr][n][1] = acc[gr][n][2] = acc[gr][n][3] = 0.f;
+        }
+        int scale_exp = 120;  // acc holds values times 2^scale_exp
+        bool first = true;
+
+        auto page_at = [&](int t) { return t < t1 ? s_page[(t >> a.c.page_shift) - me.p0] : nullptr; };
+        auto request = [&](int t, int stage) {  // the warp's piece of the step at t
+            const uint8_t* page = page_at(t + 16 * warp);
+            if (page) {
+                const uint8_t* src = page + (((t + 16 * warp) & page_mask) >> 4) * kBytes + lane * 16;
+                uint8_t* dst = raw + stage * kBytes + lane * 16;
+#pragma unroll
+                for (int i = 0; i < kBytes; i += 512)
+                    if (i + lane * 16 < kBytes) cp_async16(dst + i, src + i, true);
+            }
+            cp_async_commit();
+        };
+        // The warp's raw piece of the step at t becomes operands in buffer `buf`.
+        auto expand = [&](int t, int stage, int buf) {
+            const int tk = t + 16 * warp;
+            const uint8_t* src = raw + stage * kBytes;
+            uint8_t* dst = expanded + (buf * kAttendWarps + warp) * Smem::kExpanded;
+            const bool there = page_at(tk) != nullptr;
+            // scales: lane i looks after key i (and i + 16 again)
+            const int key = lane & 15;
+            const bool real = there && tk + key < t1;
+            float most = 0.f;
+            uint32_t bad[2] = {0u, 0u};
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                uint2 sm = *reinterpret_cast<const uint2*>(src + G * 1024 + (key * G + gr) * 8);
+                if (!real) sm = make_uint2(0u, 0u);
+                if (lane < 16)
+                    *reinterpret_cast<float2*>(dst + 2 * Smem::kOperand + (gr * 16 + key) * 8) =
+                        make_float2(bf16_lo(sm.x) * score_mul, bf16_hi(sm.x) * a.scale_log2);
+                const float s = bf16_lo(sm.y), m = bf16_hi(sm.y);
+                const bool odd = !(fabsf(s) < INFINITY && fabsf(m) < INFINITY);
+                bad[gr] = __ballot_sync(0xffffffffu, odd) & 0xffffu;
+                if (!odd) most = fmaxf(most, fmaxf(fabsf(m), fabsf(fmaf(15.f, s, m))));
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const int field = min(int(__float_as_uint(most) >> 23) - 127, 127);
+            const int ex = most > 0.f ? max(min(((7 - field) >> 3) * 8, 120), -120) : 120;
+            const float up = pow2i(ex);
+            if (lane == 0) s_info[buf][warp] = PieceInfo{ex, int(bad[0]), int(bad[1]), there ? 0 : 1};
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                const uint4 kw = reinterpret_cast<const uint4*>(src + gr * 512)[lane];
+                const uint4 vw = reinterpret_cast<const uint4*>(src + (G + gr) * 512)[lane];
+                const uint32_t kws[4] = {kw.x, kw.y, kw.z, kw.w}, vws[4] = {vw.x, vw.y, vw.z, vw.w};
+                // value scales and middles of keys 2 tq, 2 tq + 1 (low, high half) and of both + 8
+                uint32_t s2[2], m2[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float sv[2], mv[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int k = 8 * h + 2 * tq + c;
+                        uint32_t sm = *reinterpret_cast<const uint32_t*>(src + G * 1024 + (k * G + gr) * 8 + 4);
+                        if (!there || tk + k >= t1 || (bad[gr] >> k & 1)) sm = 0u;
+                        const float s = bf16_lo(sm);
+                        sv[c] = s * up;
+                        mv[c] = fmaf(8.f, s, bf16_hi(sm)) * up;
+                    }
+                    s2[h] = pack_f16(sv[0], sv[1]);
+                    m2[h] = pack_f16(mv[0], mv[1]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = kws[i], y = x >> 8;
+                    reinterpret_cast<uint4*>(dst + gr * 2048)[i * 32 + lane] =
+                        make_uint4(x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = vws[i], y = x >> 8;
+                    const uint32_t a0 = fma_f16x2(sub_f16x2((x & 0x000F000Fu) | 0x64006400u, 1032.f), s2[0], m2[0]);
+                    const uint32_t a1 = fma_f16x2(sub_f16x2((x & 0x00F000F0u) | 0x54005400u, 72.f), s2[0], m2[0]);
+                    const uint32_t a2 = fma_f16x2(sub_f16x2((y & 0x000F000Fu) | 0x64006400u, 1032.f), s2[1], m2[1]);
+                    const uint32_t a3 = fma_f16x2(sub_f16x2((y & 0x00F000F0u) | 0x54005400u, 72.f), s2[1], m2[1]);
+                    reinterpret_cast<uint4*>(dst + Smem::kOperand + gr * 2048)[i * 32 + lane] = make_uint4(a0, a1, a2, a3);
+                }
+            }
+        };
+        const int see0 = ahead + by_share(a, me.row0 + r0) + 1, see1 = ahead + by_share(a, me.row0 + r0 + 8) + 1;
+        const int full = a.causal ? ahead + by_share(a, me.row0) + 1 : t1;  // keys that every row sees
+
+        // The step at t, expanded in buffer `buf`, meets the warp's rows.
+        auto multiply = [&](int t, int buf) {
+            const uint8_t* base = expanded + buf * kAttendWarps * Smem::kExpanded;
+            float p[kAttendWarps][2][4];  // piece, keys 0-7 / 8-15: (row g: key 2 tq, + 1; row g + 8: the same)
+            bool odd = t + kRowsStep > t1 || t + kRowsStep > full;
+            int ex = scale_exp;
+#pragma unroll
+            for (int i = 0; i < kAttendWarps; ++i) {
+                const PieceInfo info = s_info[buf][i];
+                ex = min(ex, info.exponent);
+                odd |= (info.bad0 | info.bad1 | info.absent) != 0;
+            }
+            if (ex < scale_exp) {  // larger values than any before
+                const float f = pow2i(ex - scale_exp);
+                scale_exp = ex;
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[gr][n][c] *= f;
+            }
+            float most = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kAttendWarps; ++i) {
+                const uint8_t* piece = base + i * Smem::kExpanded;
+                float s[G][2][4];
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint4 f = reinterpret_cast<const uint4*>(piece + gr * 2048)[ks * 32 + lane];
+                        if (ks == 0) {
+                            mma_f16_16816_first(s[gr][0], qa[gr][ks], f.x, f.z);
+                            mma_f16_16816_first(s[gr][1], qa[gr][ks], f.y, f.w);
+                        } else {
+                            mma_f16_16816(s[gr][0], qa[gr][ks], f.x, f.z);
+                            mma_f16_16816(s[gr][1], qa[gr][ks], f.y, f.w);
+                        }
+                    }
+                if (apart) {
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) s[gr][n][c] *= rowmul[c >> 1];
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) p[i][n][c] = -ref[c >> 1];
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        // {scale, minimum} of keys 2 tq and 2 tq + 1
+                        const float4 k = *reinterpret_cast<const float4*>(piece + 2 * Smem::kOperand + (gr * 16 + n * 8 + 2 * tq) * 8);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            p[i][n][c] = fmaf(s[gr][n][c], (c & 1) ? k.z : k.x,
+                                              fmaf(qsum[c >> 1][gr], (c & 1) ? k.w : k.y, p[i][n][c]));
+                    }
+                    most = fmax3(most, p[i][n][0], p[i][n][1]);
+                    most = fmax3(most, p[i][n][2], p[i][n][3]);
+                }
+            }
+            if (odd) {  // keys that are not there or that a causal row does not see, values that are no numbers
+                most = -INFINITY;
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < kAttendWarps; ++i) {
+                    const PieceInfo info = s_info[buf][i];
+                    const int end = info.absent ? 0 : t1;
+                    any |= !info.absent;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int key = n * 8 + 2 * tq + (c & 1), at = t + 16 * i + key;
+                            const int sees = a.causal ? min(end, c < 2 ? see0 : see1) : end;
+                            if (at >= sees) {
+                                p[i][n][c] = -INFINITY;
+                            } else {
+                                if (info.bad0 >> key & 1) none[c >> 1][0] = NAN;
+                                if (G == 2 && (info.bad1 >> key & 1)) none[c >> 1][G - 1] = NAN;
+                            }
+                            most = fmaxf(most, p[i][n][c]);
+                        }
+                }
+                if (first && !any) return;  // nothing there: the references are still to be set
+            }
+            if (__any_sync(0xffffffffu, first || most > 8.f)) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < kAttendWarps; ++i)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mx = fmax3(mx, p[i][n][2 * r], p[i][n][2 * r + 1]);
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // mx is relative to the reference (0 in the first step, whatever is seen)
+                    if (first ? mx > -INFINITY : mx > 8.f) {
+                        const float corr = first ? 0.f : ex2_approx(-mx);
+                        ref[r] += mx;
+                        l[r] *= corr;
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                acc[gr][n][2 * r] *= corr;
+                                acc[gr][n][2 * r + 1] *= corr;
+                            }
+#pragma unroll
+                        for (int i = 0; i < kAttendWarps; ++i)
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                p[i][n][2 * r] -= mx;
+                                p[i][n][2 * r + 1] -= mx;
+                            }
+                    }
+                }
+                first = false;
+            }
+#pragma unroll
+            for (int i = 0; i < kAttendWarps; ++i) {
+                const uint8_t* piece = base + i * Smem::kExpanded;
+                uint32_t pa[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        p[i][n][c] = ex2_approx(p[i][n][c]);
+                        l[c >> 1] += p[i][n][c];
+                    }
+                }
+                const int apart_by = s_info[buf][i].exponent - scale_exp;  // >= 0
+                if (apart_by) {
+                    const float f = pow2i(-apart_by);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) p[i][n][c] *= f;
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    pa[2 * n] = pack_f16(p[i][n][0], p[i][n][1]);
+                    pa[2 * n + 1] = pack_f16(p[i][n][2], p[i][n][3]);
+                }
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) {
+                        const uint4 f = reinterpret_cast<const uint4*>(piece + Smem::kOperand + gr * 2048)[mt * 32 + lane];
+                        mma_f16_16816(acc[gr][2 * mt], pa, f.x, f.z);
+                        mma_f16_16816(acc[gr][2 * mt + 1], pa, f.y, f.w);
+                    }
+            }
+        };
+
+#pragma unroll
+        for (int s = 0; s < ST - 1; ++s) request(t0 + s * kRowsStep, s);
+        cp_async_wait<ST - 2>();
+        __syncwarp();
+        expand(t0, 0, 0);
+        __syncthreads();
+        const bool busy = warp * 16 < me.rows;  // the warp has rows
+        int stage = 0, buf = 0;
+        for (int t = t0; t < t1; t += kRowsStep) {
+            // the raw piece at `stage` has been expanded; the one after it is about to be
+            const int next = stage == ST - 1 ? 0 : stage + 1, free_stage = stage == 0 ? ST - 1 : stage - 1;
+            request(t + (ST - 1) * kRowsStep, free_stage);
+            cp_async_wait<ST - 2>();
+            __syncwarp();
+            if (t + kRowsStep < t1) expand(t + kRowsStep, next, buf ^ 1);
+            if (busy) multiply(t, buf);
+            __syncthreads();
+            stage = next;
+            buf ^= 1;
+        }
+        cp_async_wait<0>();
+
+        // ---- the warp's rows: normalised, with the logarithm (base 2) of the sum
+        const bool whole = s_req.len[me.b] <= a.chunk;
+        const float back = pow2i(-scale_exp);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float sum = l[r];
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) none[r][gr] += __shfl_xor_sync(0xffffffffu, none[r][gr], o);
+            const int rr = r0 + 8 * r;
+            if (rr >= me.rows) continue;
+            const int qi = by_share(a, me.row0 + rr), qh = me.h * a.share + me.row0 + rr - qi * a.share;
+            const int64_t row = whole ? int64_t(s_req.q0[me.b] + qi) * a.q_heads + qh
+                                      : (me.b ? s_req.parts[me.b - 1] : 0) +
+                                            (int64_t(me.split) * s_req.nq[me.b] + qi) * a.q_heads + qh;
+            // (query rows of requests that overlap, which cu_q must not have, could make more
+            // partial rows than the workspace holds)
+            if (!whole && (row < 0 || row >= a.part_rows)) {
+                if (tq == 0) atomicOr(a.flags, kFlagBounds);
+                continue;
+            }
+            const float inv = sum == 0.f ? 0.f : back / sum;
+            if (tq == 0) {
+                const float lse2 = sum == 0.f ? -INFINITY : ref[r] + log2f(sum);
+                if (!whole)
+                    a.part_lse[row] = lse2;
+                else if (a.lse)
+                    a.lse[row] = lse2 * 0.6931471805599453f;
+            }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float x = fmaf(acc[gr][n][2 * r], inv, none[r][gr]), y = fmaf(acc[gr][n][2 * r + 1], inv, none[r][gr]);
+                    const int64_t at = row * (64 * G) + gr * 64 + n * 8 + 2 * tq;
+                    if (!whole)
+                        *reinterpret_cast<float2*>(a.part_o + at) = make_float2(x, y);
+                    else
+                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
+                            a.dtype == 0 ? pack_bf16(x, y) : pack_f16(x, y);
+                }
+        }
+    }
+}
+
+namespace {
+
+template <int G>
+cudaError_t launch_rows(const CacheAttendArgs& a, cudaStream_t s) {
+    constexpr int kMost = RowsSmem<G>::kBytes + kCacheMaxRequests * 20;
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    static int resident = 0;  // CTAs an SM for few requests
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(cache_attend_rows_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (err == cudaSuccess)
+            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_rows_kernel<G>, kAttendThreads,
+                                                                RowsSmem<G>::kBytes + 64 * 20);
+    });
+    if (err != cudaSuccess) return err;
+    return launch_pdl(cache_attend_rows_kernel<G>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
+                      size_t(RowsSmem<G>::kBytes + a.B * 20), s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attend_rows(const CacheAttendArgs& a, cudaStream_t s) {
+    return a.c.groups == 1 ? launch_rows<1>(a, s) : launch_rows<2>(a, s);
+}
+
+}  // namespace clef
