@@ -37,14 +37,14 @@ struct AttendSmem {
     // waits, votes and addresses
     static constexpr int kPieces = 2;
     // steps in flight a warp
-    static constexpr int kStages = G == 2 ? 2 : 3;
+    static constexpr int kStages = G == 2 ? 2 : NT <= 2 ? 3 : 4;
     static constexpr int kRing = kAttendWarps * kStages * kPieces * kPiece * G;
     static constexpr int kResults = kAttendWarps * 8 * NT * 64 * G * 4;  // the warps' sums of values
     static constexpr int kBytes = kRing + kResults + 2 * kAttendWarps * 8 * NT * 4;
 };
 
 template <int G, int NT>
-__global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : NT == 2 ? 3 : 2)
     cache_attend_kernel(const CacheAttendArgs a) {
     using Smem = AttendSmem<G, NT>;
     constexpr int ST = Smem::kStages, KP = Smem::kPieces;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
     float* s_sum = s_ref + kAttendWarps * 8 * NT;
     const Requests s_req(reinterpret_cast<int*>(smem + Smem::kBytes), a.B);
     __shared__ int s_page[2][kMaxPages];  // page numbers of the split at hand and of the next one
-    scan_requests<false>(a, s_req, 8 * NT);
+    scan_requests<G, false>(a, s_req, 8 * NT);
     if (blockIdx.x == 0 && a.part_off)
         for (int b = threadIdx.x; b < a.B; b += kAttendThreads) a.part_off[b] = b ? s_req.parts[b - 1] : 0;
 
@@ -641,10 +641,17 @@ cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s) {
     if (a.total_q <= 0 || a.max_q <= 0) return cudaSuccess;
+    // blocks of 8 query rows a warp: as few as the requests that come here can have
     const int64_t most = int64_t(a.max_q) * a.share;  // query rows of any request
-    cudaError_t e = a.c.groups == 1 ? (most <= 8 ? launch_attend<1, 1>(a, s) : launch_attend<1, 2>(a, s))
-                                    : (most <= 8 ? launch_attend<2, 1>(a, s) : launch_attend<2, 2>(a, s));
-    if (e == cudaSuccess && most > kFewRows) e = launch_cache_attend_rows(a, s);
+    cudaError_t e;
+    if (a.c.groups == 1)
+        e = most <= 8    ? launch_attend<1, 1>(a, s)
+            : most <= 16 ? launch_attend<1, 2>(a, s)
+            : most <= 24 ? launch_attend<1, 3>(a, s)
+                         : launch_attend<1, 4>(a, s);
+    else
+        e = most <= 8 ? launch_attend<2, 1>(a, s) : launch_attend<2, 2>(a, s);
+    if (e == cudaSuccess && most > few_rows(a.c.groups)) e = launch_cache_attend_rows(a, s);
     if (e != cudaSuccess || a.max_chunks <= 1) return e;
     // long memories: a row's splits are shared out among the eight warps of a CTA
     const bool wide = a.max_chunks > 16;

@@ -3,11 +3,13 @@
 // of the codes and the launch.)
 //
 // A CTA of four warps takes a split of a request's keys, one key/value head and 64 query rows,
-// 16 a warp.  Here the queries are the M dimension, S = Q K^T and O += P V, and what the codes
-// cost is paid once for 64 rows: in a step of 64 keys each warp turns one 16-token piece into
-// fp16 operands in shared memory, in the order in which the lanes take them as the B operand,
-// and then all four pieces meet all rows.  Two buffers: a step's pieces are expanded while the
-// step before is multiplied, one barrier a step.
+// 16 a warp.  Here the queries are the M dimension, S = Q K^T and O += P V, and most of what the
+// codes cost is paid once for 64 rows: in a step of 64 keys each warp turns the values of one
+// 16-token piece into fp16 operands in shared memory, in the order in which the lanes take them
+// as the B operand, and its keys' scales into fp32; then all four pieces meet all rows.  The key
+// codes stay packed and each warp splits them itself (20 instructions a piece, while operands
+// of four times the bytes would run into shared memory's rate).  Two buffers: a step's pieces
+// are expanded while the step before is multiplied, one barrier a step.
 //   Keys stay exact: codes as fp16 subnormals, and scores s_t (q . c_t) + m_t (sum q) in fp32,
 // where s_t comes with the scale of the softmax and of the queries' power of two on it.
 //   Values are rounded to fp16 once, (c - 8) s' + m' with s' = s 2^E and m' = (m + 8 s) 2^E:
@@ -38,9 +40,10 @@ template <int G>
 struct RowsSmem {
     static constexpr int kStages = 3;                               // raw pieces a warp
     static constexpr int kRaw = kAttendWarps * kStages * kPiece * G;
-    static constexpr int kOperand = 2048 * G;                       // 16 tokens x 64 G values in fp16
-    static constexpr int kScales = 16 * 8 * G;                      // scale and minimum of 16 keys in fp32
-    static constexpr int kExpanded = 2 * kOperand + kScales;
+    // an expanded piece: key codes, values in fp16, scale and minimum of its keys in fp32
+    static constexpr int kValuesAt = 512 * G;
+    static constexpr int kScalesAt = kValuesAt + 2048 * G;
+    static constexpr int kExpanded = kScalesAt + 16 * 8 * G;
     static constexpr int kBytes = kRaw + 2 * kAttendWarps * kExpanded;
 };
 
@@ -70,7 +73,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
     __shared__ const uint8_t* s_page[kMaxPages];
     __shared__ __align__(16) PieceInfo s_info[2][kAttendWarps];
     __shared__ int s_exp[kAttendWarps];
-    scan_requests<true>(a, s_req, kRowsItem);
+    scan_requests<G, true>(a, s_req, kRowsItem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tq = lane & 3;
@@ -189,22 +192,24 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
             const uint8_t* src = raw + stage * kBytes;
             uint8_t* dst = expanded + (buf * kAttendWarps + warp) * Smem::kExpanded;
             const bool there = page_at(tk) != nullptr;
-            // scales: lane i looks after key i (and i + 16 again)
+            // scales: lane i looks after key i (lane i + 16 too)
             const int key = lane & 15;
             const bool real = there && tk + key < t1;
-            float most = 0.f;
+            float vs[G], vm[G], most = 0.f;
             uint32_t bad[2] = {0u, 0u};
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 uint2 sm = *reinterpret_cast<const uint2*>(src + G * 1024 + (key * G + gr) * 8);
                 if (!real) sm = make_uint2(0u, 0u);
                 if (lane < 16)
-                    *reinterpret_cast<float2*>(dst + 2 * Smem::kOperand + (gr * 16 + key) * 8) =
+                    *reinterpret_cast<float2*>(dst + Smem::kScalesAt + (gr * 16 + key) * 8) =
                         make_float2(bf16_lo(sm.x) * score_mul, bf16_hi(sm.x) * a.scale_log2);
-                const float s = bf16_lo(sm.y), m = bf16_hi(sm.y);
-                const bool odd = !(fabsf(s) < INFINITY && fabsf(m) < INFINITY);
+                vs[gr] = bf16_lo(sm.y);
+                vm[gr] = bf16_hi(sm.y);
+                const bool odd = !(fabsf(vs[gr]) < INFINITY && fabsf(vm[gr]) < INFINITY);
                 bad[gr] = __ballot_sync(0xffffffffu, odd) & 0xffffu;
-                if (!odd) most = fmaxf(most, fmaxf(fabsf(m), fabsf(fmaf(15.f, s, m))));
+                if (odd) vs[gr] = vm[gr] = 0.f;
+                most = fmax3(most, fabsf(vm[gr]), fabsf(fmaf(15.f, vs[gr], vm[gr])));
             }
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -216,30 +221,19 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
             for (int gr = 0; gr < G; ++gr) {
                 const uint4 kw = reinterpret_cast<const uint4*>(src + gr * 512)[lane];
                 const uint4 vw = reinterpret_cast<const uint4*>(src + (G + gr) * 512)[lane];
-                const uint32_t kws[4] = {kw.x, kw.y, kw.z, kw.w}, vws[4] = {vw.x, vw.y, vw.z, vw.w};
-                // value scales and middles of keys 2 tq, 2 tq + 1 (low, high half) and of both + 8
+                const uint32_t vws[4] = {vw.x, vw.y, vw.z, vw.w};
+                // value scale and middle of the lane's key, then those of keys 2 tq, 2 tq + 1 (low,
+                // high half) and of both + 8
+                const uint32_t own = pack_f16(vs[gr] * up, fmaf(8.f, vs[gr], vm[gr]) * up);
                 uint32_t s2[2], m2[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float sv[2], mv[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int k = 8 * h + 2 * tq + c;
-                        uint32_t sm = *reinterpret_cast<const uint32_t*>(src + G * 1024 + (k * G + gr) * 8 + 4);
-                        if (!there || tk + k >= t1 || (bad[gr] >> k & 1)) sm = 0u;
-                        const float s = bf16_lo(sm);
-                        sv[c] = s * up;
-                        mv[c] = fmaf(8.f, s, bf16_hi(sm)) * up;
-                    }
-                    s2[h] = pack_f16(sv[0], sv[1]);
-                    m2[h] = pack_f16(mv[0], mv[1]);
+                    const uint32_t x = __shfl_sync(0xffffffffu, own, 8 * h + 2 * tq);
+                    const uint32_t y = __shfl_sync(0xffffffffu, own, 8 * h + 2 * tq + 1);
+                    s2[h] = __byte_perm(x, y, 0x5410);
+                    m2[h] = __byte_perm(x, y, 0x7632);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x = kws[i], y = x >> 8;
-                    reinterpret_cast<uint4*>(dst + gr * 2048)[i * 32 + lane] =
-                        make_uint4(x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u);
-                }
+                reinterpret_cast<uint4*>(dst + gr * 512)[lane] = kw;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t x = vws[i], y = x >> 8;
@@ -247,7 +241,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                     const uint32_t a1 = fma_f16x2(sub_f16x2((x & 0x00F000F0u) | 0x54005400u, 72.f), s2[0], m2[0]);
                     const uint32_t a2 = fma_f16x2(sub_f16x2((y & 0x000F000Fu) | 0x64006400u, 1032.f), s2[1], m2[1]);
                     const uint32_t a3 = fma_f16x2(sub_f16x2((y & 0x00F000F0u) | 0x54005400u, 72.f), s2[1], m2[1]);
-                    reinterpret_cast<uint4*>(dst + Smem::kOperand + gr * 2048)[i * 32 + lane] = make_uint4(a0, a1, a2, a3);
+                    reinterpret_cast<uint4*>(dst + Smem::kValuesAt + gr * 2048)[i * 32 + lane] = make_uint4(a0, a2, a1, a3);
                 }
             }
         };
@@ -282,18 +276,21 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 const uint8_t* piece = base + i * Smem::kExpanded;
                 float s[G][2][4];
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr)
+                for (int gr = 0; gr < G; ++gr) {
+                    const uint4 kq = reinterpret_cast<const uint4*>(piece + gr * 512)[lane];
+                    const uint32_t words[4] = {kq.x, kq.y, kq.z, kq.w};
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
-                        const uint4 f = reinterpret_cast<const uint4*>(piece + gr * 2048)[ks * 32 + lane];
+                        const uint32_t x = words[ks], y = x >> 8;
                         if (ks == 0) {
-                            mma_f16_16816_first(s[gr][0], qa[gr][ks], f.x, f.z);
-                            mma_f16_16816_first(s[gr][1], qa[gr][ks], f.y, f.w);
+                            mma_f16_16816_first(s[gr][0], qa[gr][ks], x & 0x000F000Fu, x & 0x00F000F0u);
+                            mma_f16_16816_first(s[gr][1], qa[gr][ks], y & 0x000F000Fu, y & 0x00F000F0u);
                         } else {
-                            mma_f16_16816(s[gr][0], qa[gr][ks], f.x, f.z);
-                            mma_f16_16816(s[gr][1], qa[gr][ks], f.y, f.w);
+                            mma_f16_16816(s[gr][0], qa[gr][ks], x & 0x000F000Fu, x & 0x00F000F0u);
+                            mma_f16_16816(s[gr][1], qa[gr][ks], y & 0x000F000Fu, y & 0x00F000F0u);
                         }
                     }
+                }
                 if (apart) {
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr)
@@ -309,7 +306,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
                         // {scale, minimum} of keys 2 tq and 2 tq + 1
-                        const float4 k = *reinterpret_cast<const float4*>(piece + 2 * Smem::kOperand + (gr * 16 + n * 8 + 2 * tq) * 8);
+                        const float4 k = *reinterpret_cast<const float4*>(piece + Smem::kScalesAt + (gr * 16 + n * 8 + 2 * tq) * 8);
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             p[i][n][c] = fmaf(s[gr][n][c], (c & 1) ? k.z : k.x,
@@ -406,9 +403,9 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 for (int gr = 0; gr < G; ++gr)
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt) {
-                        const uint4 f = reinterpret_cast<const uint4*>(piece + Smem::kOperand + gr * 2048)[mt * 32 + lane];
-                        mma_f16_16816(acc[gr][2 * mt], pa, f.x, f.z);
-                        mma_f16_16816(acc[gr][2 * mt + 1], pa, f.y, f.w);
+                        const uint4 f = reinterpret_cast<const uint4*>(piece + Smem::kValuesAt + gr * 2048)[mt * 32 + lane];
+                        mma_f16_16816(acc[gr][2 * mt], pa, f.x, f.y);
+                        mma_f16_16816(acc[gr][2 * mt + 1], pa, f.z, f.w);
                     }
             }
         };

@@ -84,6 +84,9 @@ def attention_tolerance(q, k, v, scale, dtype):
     Output: those relative errors times max |v|, the weights' fp16 rounding (half a step,
     2^-11 relative to the weight, floored at 2^-24 of the largest) on codes centred to
     |c - 8| <= 8, so on 8 s <= max - min <= 2 max |v|, and the output's own rounding.
+    Requests of many query rows instead round the values themselves to fp16, their middle
+    m + 8 s and the value, half a step each of at most max |v|, and the weights on them: three
+    half steps of max |v|.  The larger of the two is taken for all.
     """
     dim = q.shape[-1]
     span = (v.amax() - v.amin()).item() if v.numel() else 0.0
@@ -92,5 +95,5 @@ def attention_tolerance(q, k, v, scale, dtype):
     err_s = 160 * 2.0 ** -24 * amp
     sums = 2.0 ** -24 * (k.shape[0] / 8 + 100)
     rel = 2 * err_s + 2.0 ** -22 + sums
-    out = rel * 2 * reach + (2.0 ** -11 + 2.0 ** -20) * span
+    out = rel * 2 * reach + max((2.0 ** -11 + 2.0 ** -20) * span, (3 * 2.0 ** -11 + 2.0 ** -20) * reach)
     return out, err_s + 2.0 ** -22 + sums + 2.0 ** -20

@@ -258,7 +258,9 @@ CASES = [  # lens, new, kv heads, share, dim, page
     ([255, 256, 257, 512, 513], [1, 1, 0, 1, 1], 3, 1, 128, 64), ([33, 700, 5], [5, 9, 7], 2, 8, 64, 32),
     ([3, 100, 0, 64], [10, 100, 4, 3], 4, 1, 64, 64), ([1000], [33], 1, 1, 64, 256), ([777, 1200], [17, 1], 2, 5, 128, 16),
     ([4096, 100], [16, 2], 1, 7, 64, 128), ([5000], [1], 16, 1, 64, 64), ([20000, 300], [2, 2], 2, 2, 128, 256),
-    ([70001], [1], 1, 8, 64, 64), ([2100], [100], 2, 1, 64, 64), ([40, 2000, 1, 90, 333], [25, 0, 1, 24, 9], 1, 1, 64, 16)]
+    ([600, 600, 90], [32, 33, 90], 1, 1, 64, 32), ([2500, 100, 0, 7], [40, 64, 65, 7], 2, 1, 64, 16),
+    ([300, 3000, 40], [16, 17, 1], 2, 1, 128, 64), ([5000, 64], [13, 20], 1, 8, 64, 128),
+    ([2049, 130, 1], [50, 70, 2], 1, 3, 128, 16), ([70001], [1], 1, 8, 64, 64), ([2100], [100], 2, 1, 64, 64), ([40, 2000, 1, 90, 333], [25, 0, 1, 24, 9], 1, 1, 64, 16)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -294,16 +296,17 @@ def test_strided_queries_layers_and_given_tables():
 
 
 @pytest.mark.parametrize("size", [2.0 ** -40, 2.0 ** -10, 64.0, 2.0 ** 30])
-def test_query_sizes(size):
+@pytest.mark.parametrize("n", [8, 50])
+def test_query_sizes(size, n):
     """Scores from nearly equal to one-hot; rows of very different size side by side."""
     g = gen(8)
     c, memory = filled([600], 2, 64, 64, g)
-    q = torch.randn(8, 2, 64, generator=g, device=DEV)
+    q = torch.randn(n, 2, 64, generator=g, device=DEV)
     q[::2] *= size
     q[3] = 0
     q = q.bfloat16()
-    out, lse = c.attend(q, ints([0, 8]), 8, causal=False)
-    for i in range(8):
+    out, lse = c.attend(q, ints([0, n]), n, causal=False)
+    for i in range(n):
         scale = 64 ** -0.5
         want, want_lse = attention(q[i:i + 1], *memory[0], scale, False)
         if size < 2.0 ** 20 or i % 2 or i == 3:
@@ -317,70 +320,78 @@ def test_query_sizes(size):
             assert ((out[i] - want[0]).abs().amax(-1)[sure] <= 2 ** -7 * memory[0][1].abs().max()).all()
 
 
-def test_equal_weights_give_the_mean_value():
+@pytest.mark.parametrize("n", [1, 40])
+def test_equal_weights_give_the_mean_value(n):
     """Zero queries over 20000 keys: 1 / n weights, a mean far smaller than the values it is made of."""
     g = gen(9)
     c, memory = filled([20000], 2, 64, 64, g)
-    q = torch.zeros(1, 2, 64, dtype=torch.float16, device=DEV)
-    out, lse = c.attend(q, ints([0, 1]), 1, causal=False)
+    q = torch.zeros(n, 2, 64, dtype=torch.float16, device=DEV)
+    out, lse = c.attend(q, ints([0, n]), n, causal=False)
     v = memory[0][1].double()
-    # every weight is rounded by at most 2^-11 of itself, independently of the sign of its value:
-    # |error| <= 2^-11 sqrt(sum v^2) / n times 6 deviations, and the bias of equal weights of equal
-    # scales 2^-11 |mean|; the output's own rounding 2^-11 |mean|
-    bound = 6 * 2 ** -11 * v.square().sum(0).sqrt() / 20000 + 2 ** -10 * v.mean(0).abs() + 2 ** -24
-    assert ((out[0].double() - v.mean(0)).abs() <= bound).all()
+    # every weight (many rows: and value, and its middle) is rounded by at most 2^-11 of itself,
+    # independently of the sign of its value: |error| <= 3 x 2^-11 sqrt(sum v^2) / n times 6
+    # deviations, and the bias of equal weights of equal scales 2^-11 |mean|; the output's own
+    # rounding 2^-11 |mean|
+    bound = (6 if n == 1 else 18) * 2 ** -11 * v.square().sum(0).sqrt() / 20000 + 2 ** -10 * v.mean(0).abs() + 2 ** -24
+    assert ((out.double() - v.mean(0)).abs() <= bound).all()
     assert (lse.double() - math.log(20000)).abs().max() < 2 ** -20
 
 
-def test_what_is_masked_may_hold_anything():
+@pytest.mark.parametrize("n0,n1", [(4, 3), (19, 18), (36, 40)])
+def test_what_is_masked_may_hold_anything(n0, n1):
     """NaN and infinite values behind the last token, in tokens that a causal row does not see, and in
     another request leave a row alone; a NaN that it does see makes it NaN."""
     g = gen(10)
     lens = [37, 50]
     c, memory = filled(lens, 2, 128, 16, g)
-    clean_q = torch.randn(7, 2, 128, generator=g, device=DEV).bfloat16()
-    cu = ints([0, 4, 7])
-    clean, _ = c.attend(clean_q, cu, 4)
+    clean_q = torch.randn(n0 + n1, 2, 128, generator=g, device=DEV).bfloat16()
+    cu, most = ints([0, n0, n0 + n1]), max(n0, n1)
+    clean, clean_lse = c.attend(clean_q, cu, most)
     bad = torch.full((1, 2, 128), math.nan, device=DEV).bfloat16()
     slot = lambda b, p: ints([c.block_table[b, p // 16].item() * 16 + p % 16])
     for p in range(37, 48):                       # behind the last token of request 0, in its last page
         c.append(bad, bad, slot(0, p))
-    out, lse = c.attend(clean_q, cu, 4)
-    assert torch.equal(out, clean)
+    out, lse = c.attend(clean_q, cu, most)
+    assert torch.equal(out, clean) and torch.equal(lse, clean_lse)
     c.append(bad, bad, slot(0, 36))               # its last token: only the last causal row sees it
-    out, lse = c.attend(clean_q, cu, 4)
-    assert torch.equal(out[:3], clean[:3]) and torch.equal(out[4:], clean[4:])
-    assert torch.isnan(out[3]).all() and torch.isnan(lse[3]).all() and not torch.isnan(lse[:3]).any()
+    out, lse = c.attend(clean_q, cu, most)
+    assert torch.equal(out[:n0 - 1], clean[:n0 - 1]) and torch.equal(out[n0:], clean[n0:])
+    assert torch.isnan(out[n0 - 1]).all() and torch.isnan(lse[n0 - 1]).all() and not torch.isnan(lse[:n0 - 1]).any()
     k, v = memory[1]
-    c.append(k[49:50].bfloat16(), bad, slot(1, 49))  # a value alone
-    out, lse = c.attend(clean_q, cu, 4)
-    assert torch.equal(out[4:6], clean[4:6]) and torch.isnan(out[6]).all() and not torch.isnan(lse[4:]).any()
+    some = v[49:50].bfloat16()
+    some[:, :, 64:] = math.nan
+    c.append(k[49:50].bfloat16(), some, slot(1, 49))  # half of a value alone
+    out, lse = c.attend(clean_q, cu, most)
+    last = n0 + n1 - 1
+    assert torch.equal(out[n0:last], clean[n0:last]) and not torch.isnan(lse[n0:]).any()
+    assert torch.isnan(out[last, :, 64:]).all() and not torch.isnan(out[last, :, :64]).any()
 
 
-def test_a_bad_query_row_stays_alone():
+@pytest.mark.parametrize("n", [9, 30, 70])
+def test_a_bad_query_row_stays_alone(n):
     g = gen(11)
     c, _ = filled([400], 1, 64, 64, g)
-    q = torch.randn(9, 1, 64, generator=g, device=DEV).bfloat16()
-    clean, clean_lse = c.attend(q, ints([0, 9]), 9, causal=False)
+    q = torch.randn(n, 1, 64, generator=g, device=DEV).bfloat16()
+    clean, clean_lse = c.attend(q, ints([0, n]), n, causal=False)
     q[2, 0, 5], q[4, 0, 6] = math.nan, math.inf
-    out, lse = c.attend(q, ints([0, 9]), 9, causal=False)
-    keep = [0, 1, 3, 5, 6, 7, 8]
+    out, lse = c.attend(q, ints([0, n]), n, causal=False)
+    keep = [i for i in range(n) if i not in (2, 4)]
     assert torch.equal(out[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
     assert torch.isnan(out[2]).all()
 
 
 def test_a_row_does_not_depend_on_the_batch():
     g = gen(12)
-    lens, new = [3000, 17, 900, 0, 2048], [1, 3, 1, 1, 2]
+    lens, new = [3000, 17, 900, 0, 2048, 2500, 1100, 5000], [1, 3, 1, 1, 2, 40, 12, 7]
     c, _ = filled(lens, 2, 64, 32, g)
     q = torch.randn(sum(new), 4, 64, generator=g, device=DEV).bfloat16()
-    cu = [sum(new[:i]) for i in range(6)]
-    out, lse = c.attend(q, ints(cu), 3)
-    for b in range(5):
+    cu = [sum(new[:i]) for i in range(9)]
+    out, lse = c.attend(q, ints(cu), 40)
+    for b in range(8):
         one, one_lse = c.attend(q[cu[b]:cu[b + 1]], ints([0, new[b]]), new[b], block_table=c.block_table[b:b + 1],
                                 lengths=c.lengths[b:b + 1])
         assert torch.equal(one, out[cu[b]:cu[b + 1]]) and torch.equal(one_lse, lse[cu[b]:cu[b + 1]])
-    again, _ = c.attend(q, ints(cu), 3)
+    again, _ = c.attend(q, ints(cu), sum(new))
     assert torch.equal(again, out)
 
 
@@ -391,6 +402,47 @@ def test_rows_behind_the_last_request_are_left():
     out = torch.full_like(q, 7.0)
     c.attend(q, ints([0, 2, 5]), 5, out=out)
     assert (out[5:] == 7).all() and not (out[:5] == 7).all(-1).any()
+
+
+@pytest.mark.parametrize("page,n", [(16, 2), (32, 2), (16, 40), (32, 40)])
+def test_missing_pages(page, n):
+    """Tokens of pages that are not there are hidden, the first ones among them; a request with none is empty."""
+    g = gen(18)
+    c, memory = filled([2300, 100, 70], 2, 64, page, g)
+    table = c.block_table.clone()
+    gone = {0: [0, 1, 2, 3, 4, 5, 9, 64, 70], 1: [1], 2: list(range(5))}
+    for b, cols in gone.items():
+        table[b, cols] = -1
+    table[0, 9] = c.n_pages
+    q = torch.randn(3 * n, 2, 64, generator=g, device=DEV).bfloat16()
+    cu = ints([0, n, 2 * n, 3 * n])
+    out, lse = c.attend(q, cu, n, causal=False, block_table=table)
+    assert c.device_status() == 5
+    left = []
+    for b, (k, v) in enumerate(memory):
+        keep = torch.tensor([i // page not in gone[b] for i in range(k.shape[0])], device=DEV)
+        left.append((k[keep], v[keep]))
+    assert left[2][0].shape[0] == 0
+    check(c, left, q, [n] * 3, out, lse, 0.125, False, torch.bfloat16)
+
+
+@pytest.mark.parametrize("n", [1, 6, 50])
+@pytest.mark.parametrize("order", [1, -1])
+def test_values_of_every_size(n, order):
+    """Values whose size grows or falls by 2^60 along the memory: the powers of two that keep weights
+    and values in fp16's range move with them."""
+    g = gen(19)
+    c, _ = filled([3000], 1, 128, 64, g)
+    grow = torch.exp2((torch.arange(3000, device=DEV) / 3000 * 60 - 30) * order)[:, None, None]
+    k = torch.randn(3000, 1, 128, generator=g, device=DEV).bfloat16()
+    v = (torch.randn(3000, 1, 128, generator=g, device=DEV) * grow).bfloat16()
+    pos = torch.arange(3000, device=DEV)
+    slots = (c.block_table[0, pos // 64] * 64 + pos % 64).int()
+    c.append(k, v, slots)
+    memory = c.read(slots, torch.float32)
+    q = torch.randn(n, 1, 128, generator=g, device=DEV).bfloat16()
+    out, lse = c.attend(q, ints([0, n]), n, causal=True)
+    check(c, [memory], q, [n], out, lse, 128 ** -0.5, True, torch.bfloat16)
 
 
 def test_bad_tables_lengths_and_query_offsets_are_reported():
@@ -416,12 +468,13 @@ def test_bad_tables_lengths_and_query_offsets_are_reported():
     assert c.device_status() == 0 and torch.equal(out, clean)
 
 
-def test_overlapping_query_ranges_stay_in_the_workspace():
+@pytest.mark.parametrize("n", [4, 40])
+def test_overlapping_query_ranges_stay_in_the_workspace(n):
     """cu_q that goes back makes more partial rows than there are: reported, nothing written outside."""
     g = gen(15)
     c, _ = filled([2000] * 8, 1, 64, 64, g)
-    q = torch.randn(4, 1, 64, generator=g, device=DEV).bfloat16()
-    c.attend(q, ints([0, 4, 0, 4, 0, 4, 0, 4, 4]), 4, causal=False)
+    q = torch.randn(n, 1, 64, generator=g, device=DEV).bfloat16()
+    c.attend(q, ints([0, n, 0, n, 0, n, 0, n, n]), n, causal=False)
     assert c.device_status() == 5
 
 
