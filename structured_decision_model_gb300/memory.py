@@ -27,25 +27,11 @@ def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
     return int(s.cuda_stream)
 
 
-class _On:
-    """The launches of one call: its device made current where it is not, and the handle of
-    that device's current stream.  (A decoding step calls this layer a few times per layer of
-    a model; the calls of an idle host are a few microseconds.)"""
-
-    __slots__ = ("index", "back")
-
-    def __init__(self, index):
-        self.index, self.back = index, None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+# A decoding step calls this layer a few times for every layer of a model, so the host's share of
+# a call matters: no device guard and no Stream object where the current device is the cache's.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _refuse(why):
@@ -98,6 +84,7 @@ class MemoryCache:
         self._flags = self.flags.data_ptr()
         self._accounts = [x.data_ptr() for x in (self.lengths, self.block_table, self.free_pages, self.free_count)]
         self._lib = B.load()
+        self._space = {}  # workspace bytes of the sizes that attend has met
 
     # ------------------------------------------------------------- checks
 
@@ -106,7 +93,8 @@ class MemoryCache:
             _refuse(f"{what} is on {t.device}, the cache on {self.device}")
 
     def checked_slots(self, slots: torch.Tensor) -> torch.Tensor:
-        self._on_device(slots, "slots")
+        if slots.device != self.device:
+            self._on_device(slots, "slots")
         if slots.dtype != torch.int32 or slots.dim() != 1 or not slots.is_contiguous():
             _refuse("slots: a contiguous int32 vector")
         return slots
@@ -119,10 +107,11 @@ class MemoryCache:
             _refuse("block_table: contiguous int32 [requests, pages]")
         return table
 
-    def _on(self):
+    def _elsewhere(self):
+        """Whether another device than the cache's is current (the call is then made inside a guard)."""
         if self._index is None:
             _refuse("the cache is not on a GPU")
-        return _On(self._index)
+        return _current_device() != self._index
 
     def _check(self, status, where):
         if status != B.CLEF_OK:
@@ -150,15 +139,17 @@ class MemoryCache:
             _refuse("slots: int32 [n_slots]")
         if cu is not None and self.checked_slots(cu).numel() != self.requests + 1:
             _refuse("cu: int32 [requests + 1]")
-        with self._on() as stream:
-            if slots is None:
-                slots = torch.empty(n_slots, dtype=torch.int32, device=self.device)
-            if cu is None:
-                cu = torch.empty(self.requests + 1, dtype=torch.int32, device=self.device)
-            lengths, table, free_pages, free_count = self._accounts
-            self._check(self._lib.clef_cache_plan(self.struct, self.requests, lengths, want.data_ptr(), table, self.width,
-                                                  free_pages, free_count, cu.data_ptr(), slots.data_ptr(), n_slots,
-                                                  self._flags, stream), "clef_cache_plan")
+        if self._elsewhere():
+            with torch.cuda.device(self._index):
+                return self.plan(want, n_slots, slots, cu)
+        if slots is None:
+            slots = torch.empty(n_slots, dtype=torch.int32, device=self.device)
+        if cu is None:
+            cu = torch.empty(self.requests + 1, dtype=torch.int32, device=self.device)
+        lengths, table, free_pages, free_count = self._accounts
+        self._check(self._lib.clef_cache_plan(self.struct, self.requests, lengths, want.data_ptr(), table, self.width,
+                                              free_pages, free_count, cu.data_ptr(), slots.data_ptr(), n_slots,
+                                              self._flags, _raw_stream(self._index)), "clef_cache_plan")
         return slots, cu
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, head0: int = 0):
@@ -171,10 +162,12 @@ class MemoryCache:
             _refuse("slots: one a row")
         n, heads, _ = k.shape
         ks, vs = k.stride(), v.stride()
-        with self._on() as stream:
-            self._check(self._lib.clef_cache_append(self.struct, n, head0, heads, dtype, k.data_ptr(), ks[0], ks[1],
-                                                    v.data_ptr(), vs[0], vs[1], slots.data_ptr(), self._flags, stream),
-                        "clef_cache_append")
+        if self._elsewhere():
+            with torch.cuda.device(self._index):
+                return self.append(k, v, slots, head0)
+        self._check(self._lib.clef_cache_append(self.struct, n, head0, heads, dtype, k.data_ptr(), ks[0], ks[1],
+                                                v.data_ptr(), vs[0], vs[1], slots.data_ptr(), self._flags,
+                                                _raw_stream(self._index)), "clef_cache_append")
 
     def read(self, slots: torch.Tensor, dtype=torch.bfloat16, head0: int = 0,
              heads: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -186,11 +179,14 @@ class MemoryCache:
         n = self.checked_slots(slots).numel()
         if heads < 1:
             _refuse("read: no heads")
-        with self._on() as stream:
-            k = torch.empty((n, heads, self.head_dim), dtype=dtype, device=self.device)
-            v = torch.empty_like(k)
-            self._check(self._lib.clef_cache_read(self.struct, n, head0, heads, _DTYPES[dtype], slots.data_ptr(),
-                                                  k.data_ptr(), v.data_ptr(), self._flags, stream), "clef_cache_read")
+        if self._elsewhere():
+            with torch.cuda.device(self._index):
+                return self.read(slots, dtype, head0, heads)
+        k = torch.empty((n, heads, self.head_dim), dtype=dtype, device=self.device)
+        v = torch.empty_like(k)
+        self._check(self._lib.clef_cache_read(self.struct, n, head0, heads, _DTYPES[dtype], slots.data_ptr(),
+                                              k.data_ptr(), v.data_ptr(), self._flags, _raw_stream(self._index)),
+                    "clef_cache_read")
         return k, v
 
     def attend(self, q: torch.Tensor, cu_q: torch.Tensor, max_q: int, scale: Optional[float] = None,
@@ -219,22 +215,32 @@ class MemoryCache:
         if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or
                                 out.device != self.device):
             _refuse("out: contiguous, of q's shape and type")
-        with self._on() as stream:
-            if out is None:
-                out = torch.empty((total, q_heads, self.head_dim), dtype=q.dtype, device=self.device)
-            lse = torch.empty((total, q_heads), dtype=torch.float32, device=self.device)
-            # a buffer of the call's own: overlapping calls and captured graphs never share one
+        if self._elsewhere():
+            with torch.cuda.device(self._index):
+                return self.attend(q, cu_q, max_q, scale, causal, head0, kv_heads, table, lengths, out)
+        if out is None:
+            out = torch.empty((total, q_heads, self.head_dim), dtype=q.dtype, device=self.device)
+        lse = torch.empty((total, q_heads), dtype=torch.float32, device=self.device)
+        # a buffer of the call's own: overlapping calls and captured graphs never share one
+        sizes = (n, total, q_heads, table.shape[1])
+        n_bytes = self._space.get(sizes)
+        if n_bytes is None:
+            if len(self._space) >= 4096:
+                self._space.clear()
             n_bytes = B.clef_cache_attend_workspace(self.struct, n, total, max(q_heads, 1), table.shape[1] * self.page)
-            space = torch.empty(n_bytes, dtype=torch.uint8, device=self.device) if n_bytes else None
-            self._check(self._lib.clef_cache_attend(self.struct, n, total, max_q, q_heads, head0, kv_heads, dtype,
-                                                    q.data_ptr(), strides[0], strides[1], cu_q.data_ptr(),
-                                                    table.data_ptr(), table.shape[1], lengths.data_ptr(), scale,
-                                                    int(causal), out.data_ptr(), lse.data_ptr(), self._flags,
-                                                    space.data_ptr() if n_bytes else None, n_bytes, stream),
-                        "clef_cache_attend")
+            self._space[sizes] = n_bytes
+        space = torch.empty(n_bytes, dtype=torch.uint8, device=self.device) if n_bytes else None
+        self._check(self._lib.clef_cache_attend(self.struct, n, total, max_q, q_heads, head0, kv_heads, dtype,
+                                                q.data_ptr(), strides[0], strides[1], cu_q.data_ptr(),
+                                                table.data_ptr(), table.shape[1], lengths.data_ptr(), scale,
+                                                int(causal), out.data_ptr(), lse.data_ptr(), self._flags,
+                                                space.data_ptr() if n_bytes else None, n_bytes,
+                                                _raw_stream(self._index)), "clef_cache_attend")
         return out, lse
 
     def device_status(self) -> int:
         """Waits for the current stream, reads and clears what the kernels reported."""
-        with self._on() as stream:
-            return B.clef_cache_status(self._flags, stream)
+        if self._elsewhere():
+            with torch.cuda.device(self._index):
+                return self.device_status()
+        return B.clef_cache_status(self._flags, _raw_stream(self._index))
