@@ -409,65 +409,68 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[8], uint2* code
 
 }  // namespace
 
-template <int T, int G>
-__global__ void __launch_bounds__(32 * kRowsWarps, G == 1 ? 4 : 3) cache_append_kernel(const CacheRowsArgs a) {
+template <int T>
+__global__ void __launch_bounds__(32 * kRowsWarps, 4) cache_append_kernel(const CacheRowsArgs a) {
     griddep_wait();
     griddep_launch();
-    __shared__ __align__(16) uint32_t s_piece[kRowsWarps][G * kPiece / 4];
+    __shared__ __align__(16) uint32_t s_codes[kRowsWarps][256];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r8 = lane >> 2, run = lane & 3;
+    const int r8 = lane >> 2, run = lane & 3, G = a.c.groups;
     for (int64_t i0 = int64_t(blockIdx.x) * 16; i0 < a.n_tokens; i0 += int64_t(gridDim.x) * 16) {
         const Window win = window_of(a.slots, i0, a.n_tokens, a.c.n_pages << a.c.page_shift, a.flags);
-        for (int head = blockIdx.y * kRowsWarps + warp; head < a.n_heads; head += gridDim.y * kRowsWarps) {
-            const uint16_t* k0 = static_cast<const uint16_t*>(a.k) + head * a.k_head + run * 16;
-            const uint16_t* v0 = static_cast<const uint16_t*>(a.v) + head * a.v_head + run * 16;
+        // a warp takes one group of 64 values of one head at a time
+        for (int part = blockIdx.y * kRowsWarps + warp; part < a.n_heads * G; part += gridDim.y * kRowsWarps) {
+            const int head = part >> (G - 1), gr = part & (G - 1);
+            const uint16_t* k0 = static_cast<const uint16_t*>(a.k) + head * a.k_head + gr * 64 + run * 16;
+            const uint16_t* v0 = static_cast<const uint16_t*>(a.v) + head * a.v_head + gr * 64 + run * 16;
 
             const uint32_t start = uint32_t(win.runs >> 16) & 0xffffu;
             if (start) {
                 // a whole piece (a window holds the start of one at most): codes laid out in shared
                 // memory, then 16 bytes a lane
                 const int at = __ffs(start) - 1;
-                uint32_t* piece = s_piece[warp];
                 const int64_t row = i0 + at + r8;
+                uint32_t x[4][8];  // keys of rows r8 and r8 + 8, values of the same
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr) {
-                    uint32_t x[4][8];  // keys of rows r8 and r8 + 8, values of the same
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        load16(x[half], k0 + (row + 8 * half) * a.k_row + gr * 64, a.aligned);
-                        load16(x[2 + half], v0 + (row + 8 * half) * a.v_row + gr * 64, a.aligned);
-                    }
-                    uint2 c[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t sm = quantise<T>(x[i], &c[i]);
-                        if (run == 0) piece[G * 256 + ((r8 + 8 * (i & 1)) * G + gr) * 2 + (i >> 1)] = sm;
-                    }
-                    // keys: word 16 g + 4 t + run holds bytes 2 t, 2 t + 1 of rows g and g + 8
-                    uint32_t* kc = piece + gr * 128 + r8 * 16 + run;
-                    kc[0] = __byte_perm(c[0].x, c[1].x, 0x5140);
-                    kc[4] = __byte_perm(c[0].x, c[1].x, 0x7362);
-                    kc[8] = __byte_perm(c[0].y, c[1].y, 0x5140);
-                    kc[12] = __byte_perm(c[0].y, c[1].y, 0x7362);
-                    // values: word 16 j + 4 (row / 2) + run holds byte j of rows 2 (row / 2), + 1, and both + 8;
-                    // even rows write bytes 0 .. 3, odd ones bytes 4 .. 7
-                    const bool odd = r8 & 1;
-                    const uint32_t send0 = odd ? c[2].x : c[2].y, send1 = odd ? c[3].x : c[3].y;
-                    const uint32_t got0 = __shfl_xor_sync(0xffffffffu, send0, 4), got1 = __shfl_xor_sync(0xffffffffu, send1, 4);
-                    const uint32_t e0 = odd ? got0 : c[2].x, e1 = odd ? got1 : c[3].x;  // even row, low and high half
-                    const uint32_t o0 = odd ? c[2].y : got0, o1 = odd ? c[3].y : got1;
-                    uint32_t* vc = piece + (G + gr) * 128 + (odd ? 64 : 0) + (r8 >> 1) * 4 + run;
-                    const uint32_t ea = __byte_perm(e0, e1, 0x5140), eb = __byte_perm(e0, e1, 0x7362);
-                    const uint32_t oa = __byte_perm(o0, o1, 0x5140), ob = __byte_perm(o0, o1, 0x7362);
-                    vc[0] = __byte_perm(ea, oa, 0x5410);
-                    vc[16] = __byte_perm(ea, oa, 0x7632);
-                    vc[32] = __byte_perm(eb, ob, 0x5410);
-                    vc[48] = __byte_perm(eb, ob, 0x7632);
+                for (int half = 0; half < 2; ++half) {
+                    load16(x[half], k0 + (row + 8 * half) * a.k_row, a.aligned);
+                    load16(x[2 + half], v0 + (row + 8 * half) * a.v_row, a.aligned);
                 }
+                uint8_t* piece = piece_of(a.c, __shfl_sync(0xffffffffu, win.slot, at), a.head0 + head);
+                uint2 c[4];
+                uint32_t sm[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sm[i] = quantise<T>(x[i], &c[i]);
+                if (run == 0) {
+                    uint2* scales = reinterpret_cast<uint2*>(piece + G * 1024) + r8 * G + gr;
+                    scales[0] = make_uint2(sm[0], sm[2]);
+                    scales[8 * G] = make_uint2(sm[1], sm[3]);
+                }
+                // keys: word 16 g + 4 t + run holds bytes 2 t, 2 t + 1 of rows g and g + 8
+                uint32_t* kc = s_codes[warp] + r8 * 16 + run;
+                kc[0] = __byte_perm(c[0].x, c[1].x, 0x5140);
+                kc[4] = __byte_perm(c[0].x, c[1].x, 0x7362);
+                kc[8] = __byte_perm(c[0].y, c[1].y, 0x5140);
+                kc[12] = __byte_perm(c[0].y, c[1].y, 0x7362);
+                // values: word 16 j + 4 (row / 2) + run holds byte j of rows 2 (row / 2), + 1, and both + 8;
+                // even rows write bytes 0 .. 3, odd ones bytes 4 .. 7
+                const bool odd = r8 & 1;
+                const uint32_t send0 = odd ? c[2].x : c[2].y, send1 = odd ? c[3].x : c[3].y;
+                const uint32_t got0 = __shfl_xor_sync(0xffffffffu, send0, 4), got1 = __shfl_xor_sync(0xffffffffu, send1, 4);
+                const uint32_t e0 = odd ? got0 : c[2].x, e1 = odd ? got1 : c[3].x;  // even row, low and high half
+                const uint32_t o0 = odd ? c[2].y : got0, o1 = odd ? c[3].y : got1;
+                uint32_t* vc = s_codes[warp] + 128 + (odd ? 64 : 0) + (r8 >> 1) * 4 + run;
+                const uint32_t ea = __byte_perm(e0, e1, 0x5140), eb = __byte_perm(e0, e1, 0x7362);
+                const uint32_t oa = __byte_perm(o0, o1, 0x5140), ob = __byte_perm(o0, o1, 0x7362);
+                vc[0] = __byte_perm(ea, oa, 0x5410);
+                vc[16] = __byte_perm(ea, oa, 0x7632);
+                vc[32] = __byte_perm(eb, ob, 0x5410);
+                vc[48] = __byte_perm(eb, ob, 0x7632);
                 __syncwarp();
-                uint4* dst = reinterpret_cast<uint4*>(piece_of(a.c, __shfl_sync(0xffffffffu, win.slot, at), a.head0 + head));
-                const uint4* src = reinterpret_cast<const uint4*>(piece);
-                for (int i = lane; i < G * kPiece / 16; i += 32) dst[i] = src[i];
+                const uint4* src = reinterpret_cast<const uint4*>(s_codes[warp]) + lane;
+                reinterpret_cast<uint4*>(piece + gr * 512)[lane] = src[0];
+                reinterpret_cast<uint4*>(piece + (G + gr) * 512)[lane] = src[32];
+                __syncwarp();  // the codes are out before the next ones
             }
             // rows by themselves: their bytes go where they belong
             for (uint32_t left = win.alone; left;) {
@@ -480,26 +483,23 @@ __global__ void __launch_bounds__(32 * kRowsWarps, G == 1 ? 4 : 3) cache_append_
                 const int64_t row = mine >= 0 ? i0 + mine : 0;
                 uint8_t* piece = piece_of(a.c, mine >= 0 ? slot : 0, a.head0 + head);
                 const int r = slot & 15;
-                for (int gr = 0; gr < G; ++gr) {
-                    uint32_t x[2][8];
-                    load16(x[0], k0 + row * a.k_row + gr * 64, a.aligned);
-                    load16(x[1], v0 + row * a.v_row + gr * 64, a.aligned);
+                uint32_t x[2][8];
+                load16(x[0], k0 + row * a.k_row, a.aligned);
+                load16(x[1], v0 + row * a.v_row, a.aligned);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint2 c;
-                        const uint32_t sm = quantise<T>(x[i], &c);
-                        if (mine >= 0) {
-                            uint8_t* codes = piece + (i * G + gr) * 512;
+                for (int i = 0; i < 2; ++i) {
+                    uint2 c;
+                    const uint32_t sm = quantise<T>(x[i], &c);
+                    if (mine >= 0) {
+                        uint8_t* codes = piece + (i * G + gr) * 512;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                codes[i ? value_byte(r, run * 8 + j) : key_byte(r, run * 8 + j)] =
-                                    uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
-                            if (run == 0) *reinterpret_cast<uint32_t*>(piece + G * 1024 + (r * G + gr) * 8 + i * 4) = sm;
-                        }
+                        for (int j = 0; j < 8; ++j)
+                            codes[i ? value_byte(r, run * 8 + j) : key_byte(r, run * 8 + j)] =
+                                uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+                        if (run == 0) *reinterpret_cast<uint32_t*>(piece + G * 1024 + (r * G + gr) * 8 + i * 4) = sm;
                     }
                 }
             }
-            __syncwarp();  // the staged piece is out before the next head's
         }
     }
 }
@@ -582,13 +582,14 @@ __device__ __forceinline__ void write16(void* base, int64_t at, int64_t row_stri
 
 }  // namespace
 
-template <int T, int G>
+template <int T>
 __global__ void __launch_bounds__(32 * kRowsWarps) cache_read_kernel(const CacheRowsArgs a) {
     griddep_wait();
     griddep_launch();
     // eight rows a warp; the warp beside it takes the next eight, which share its words
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int run = lane & 3;
+    const int run = lane & 3, G = a.c.groups;
+    const int64_t row_stride = int64_t(a.n_heads) * (64 * G);
     for (int64_t i0 = int64_t(blockIdx.x) * 16; i0 < a.n_tokens; i0 += int64_t(gridDim.x) * 16) {
         const int64_t i = i0 + (warp & 1) * 8 + (lane >> 2);
         const bool there = i < a.n_tokens, other = (lane & 16 ? i - 4 : i + 4) < a.n_tokens;
@@ -596,59 +597,50 @@ __global__ void __launch_bounds__(32 * kRowsWarps) cache_read_kernel(const Cache
         if (slot >= total && run == 0) atomicOr(a.flags, kFlagBounds);
         const bool live = slot >= 0 && slot < total;
         const int r = slot & 15, hi = r >> 3;
-        for (int head = blockIdx.y * (kRowsWarps / 2) + (warp >> 1); head < a.n_heads; head += gridDim.y * (kRowsWarps / 2)) {
+        for (int part = blockIdx.y * (kRowsWarps / 2) + (warp >> 1); part < a.n_heads * G; part += gridDim.y * (kRowsWarps / 2)) {
+            const int head = part >> (G - 1), gr = part & (G - 1);
             const uint8_t* piece = piece_of(a.c, live ? slot : 0, a.head0 + head);
-            uint2 sm[G], kc[G], vc[G];
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                sm[gr] = kc[gr] = vc[gr] = make_uint2(0u, 0u);
-                if (live) {
-                    sm[gr] = *reinterpret_cast<const uint2*>(piece + G * 1024 + (r * G + gr) * 8);
-                    // words that hold the row's bytes beside those of its neighbours
-                    const uint32_t* kw = reinterpret_cast<const uint32_t*>(piece + gr * 512) + (r & 7) * 16 + run;
-                    const uint32_t* vw = reinterpret_cast<const uint32_t*>(piece + (G + gr) * 512) + ((r & 7) >> 1) * 4 + run;
-                    const int ks = hi ? 0x7531 : 0x6420, at = (r & 1) * 2 + hi, vs = at | (4 + at) << 4;  // byte selectors
-                    kc[gr] = make_uint2(__byte_perm(kw[0], kw[4], ks), __byte_perm(kw[8], kw[12], ks));
-                    vc[gr].x = __byte_perm(__byte_perm(vw[0], vw[16], vs), __byte_perm(vw[32], vw[48], vs), 0x5410);
-                    vc[gr].y = __byte_perm(__byte_perm(vw[64], vw[80], vs), __byte_perm(vw[96], vw[112], vs), 0x5410);
-                }
+            uint2 sm = make_uint2(0u, 0u), kc = make_uint2(0u, 0u), vc = make_uint2(0u, 0u);
+            if (live) {
+                sm = *reinterpret_cast<const uint2*>(piece + G * 1024 + (r * G + gr) * 8);
+                // words that hold the row's bytes beside those of its neighbours
+                const uint32_t* kw = reinterpret_cast<const uint32_t*>(piece + gr * 512) + (r & 7) * 16 + run;
+                const uint32_t* vw = reinterpret_cast<const uint32_t*>(piece + (G + gr) * 512) + ((r & 7) >> 1) * 4 + run;
+                const int ks = hi ? 0x7531 : 0x6420, at = (r & 1) * 2 + hi, vs = at | (4 + at) << 4;  // byte selectors
+                kc = make_uint2(__byte_perm(kw[0], kw[4], ks), __byte_perm(kw[8], kw[12], ks));
+                vc.x = __byte_perm(__byte_perm(vw[0], vw[16], vs), __byte_perm(vw[32], vw[48], vs), 0x5410);
+                vc.y = __byte_perm(__byte_perm(vw[64], vw[80], vs), __byte_perm(vw[96], vw[112], vs), 0x5410);
             }
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                const int64_t row = int64_t(a.n_heads) * (64 * G), at = i * row + head * (64 * G) + gr * 64 + run * 16;
-                write16<T>(a.out_k, at, row, there, other, kc[gr], sm[gr].x);
-                write16<T>(a.out_v, at, row, there, other, vc[gr], sm[gr].y);
-            }
+            const int64_t at = i * row_stride + part * 64 + run * 16;
+            write16<T>(a.out_k, at, row_stride, there, other, kc, sm.x);
+            write16<T>(a.out_v, at, row_stride, there, other, vc, sm.y);
         }
     }
 }
 
 namespace {
 
-// CTAs over the 16-row windows and, where there are few of those, over the heads that
+// CTAs over the 16-row windows and, where there are few of those, over the heads' groups that
 // `per_cta` warps or pairs of warps leave; each CTA walks several windows of a large call.
 // (Store and read back of 131072 rows x 16 heads: 265 us with a CTA for each window and eight
 // heads, 245 us with 32 CTAs an SM that walk, 270 with 4.)
 dim3 rows_grid(const CacheRowsArgs& a, int per_cta) {
-    const int64_t windows = (int64_t(a.n_tokens) + 15) / 16, heads = (a.n_heads + per_cta - 1) / per_cta;
+    const int64_t windows = (int64_t(a.n_tokens) + 15) / 16, parts = (a.n_heads * a.c.groups + per_cta - 1) / per_cta;
     const int64_t most = int64_t(num_sms()) * 32;
-    return windows * heads <= most ? dim3(unsigned(windows), unsigned(heads)) : dim3(unsigned(windows < most ? windows : most), 1);
+    return windows * parts <= most ? dim3(unsigned(windows), unsigned(parts)) : dim3(unsigned(windows < most ? windows : most), 1);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t s) {
     if (a.n_tokens <= 0) return cudaSuccess;
-    auto kernel = a.c.groups == 1 ? (a.dtype == 0 ? cache_append_kernel<0, 1> : cache_append_kernel<1, 1>)
-                                  : (a.dtype == 0 ? cache_append_kernel<0, 2> : cache_append_kernel<1, 2>);
+    auto kernel = a.dtype == 0 ? cache_append_kernel<0> : cache_append_kernel<1>;
     return launch_pdl(kernel, rows_grid(a, kRowsWarps), dim3(32 * kRowsWarps), 0, s, a);
 }
 
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t s) {
     if (a.n_tokens <= 0) return cudaSuccess;
-    auto kernel = a.c.groups == 1
-                      ? (a.dtype == 0 ? cache_read_kernel<0, 1> : a.dtype == 1 ? cache_read_kernel<1, 1> : cache_read_kernel<2, 1>)
-                      : (a.dtype == 0 ? cache_read_kernel<0, 2> : a.dtype == 1 ? cache_read_kernel<1, 2> : cache_read_kernel<2, 2>);
+    auto kernel = a.dtype == 0 ? cache_read_kernel<0> : a.dtype == 1 ? cache_read_kernel<1> : cache_read_kernel<2>;
     return launch_pdl(kernel, rows_grid(a, kRowsWarps / 2), dim3(32 * kRowsWarps), 0, s, a);
 }
 
