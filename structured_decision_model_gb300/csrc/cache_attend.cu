@@ -58,13 +58,12 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
     float* s_sum = s_ref + kAttendWarps * 8 * NT;
     const Requests s_req(reinterpret_cast<int*>(smem + Smem::kBytes), a.B);
     __shared__ int s_page[2][kMaxPages];  // page numbers of the split at hand and of the next one
-    scan_requests<G, false>(a, s_req, 8 * NT);
+    const int n_items = scan_requests<G, false>(a, s_req, 8 * NT);
     if (blockIdx.x == 0 && a.part_off)
         for (int b = threadIdx.x; b < a.B; b += kAttendThreads) a.part_off[b] = b ? s_req.parts[b - 1] : 0;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tq = lane & 3;
-    const int n_items = s_req.items[a.B - 1];
     const int page_mask = a.c.page - 1;
     uint8_t* ring = smem + warp * (ST * KP * kBytes);
     constexpr int kStride = 16 * KP * kAttendWarps;
@@ -136,9 +135,8 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         }
     };
 
-    int w = blockIdx.x;
-    if (w >= n_items) return;
-    Item me = item_of<8 * NT>(a, s_req, w);
+    if (item_of_turn(0) >= n_items) return;
+    Item me = item_of<8 * NT>(a, s_req, item_of_turn(0));
     request_pages(me, s_page[0]);
     cp_async_commit();
     uint32_t qw[NT][G][8];
@@ -147,8 +145,8 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
     __syncthreads();
     request_first(me, s_page[0]);
 
-    for (int turn = 0;; turn ^= 1) {
-        const int* pages = s_page[turn];
+    for (int turn = 0;; ++turn) {
+        const int* pages = s_page[turn & 1];
         const int t0 = me.t0, t1 = me.t1, ahead = me.ahead;
         const bool holes = lacks_pages(me, pages);
 
@@ -195,15 +193,16 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         }
 
         float acc[G][4][NT][4];  // O^T: 4 blocks of 16 values of each group
+        float mid[G][NT][4];     // eight times the sum of the weights, as acc counts
         float l[NT][2], z[G][NT][2], ref[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 l[n][c] = 0.f;
-                ref[n][c] = -1e30f;
+                ref[n][c] = 0.f;
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr) z[gr][n][c] = 0.f;
+                for (int gr = 0; gr < G; ++gr) z[gr][n][c] = mid[gr][n][c] = mid[gr][n][c + 2] = 0.f;
             }
 #pragma unroll
         for (int gr = 0; gr < G; ++gr)
@@ -214,14 +213,15 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                     for (int c = 0; c < 4; ++c) acc[gr][mt][n][c] = 0.f;
         float vmul = pow2i(120);  // value scales are multiplied by a power of two, to at most 8
+        bool first = true;        // no step yet: the references are still to be set
 
         // the next item's page numbers come in with the pieces of this one
-        const int w_next = w + gridDim.x;
+        const int w_next = item_of_turn(turn + 1);
         const bool more = w_next < n_items;
         Item next = me;
         if (more) {
             next = item_of<8 * NT>(a, s_req, w_next);
-            request_pages(next, s_page[turn ^ 1]);
+            request_pages(next, s_page[~turn & 1]);
         }
 
         int stage = 0;
@@ -264,29 +264,29 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     }
                 }
             // ---- scores (base 2) less their row's reference
-            auto score = [&](int k, int n, int c, float less) {
-                float y = less;
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr) {
-                    y = fmaf(qsum[gr][n][c & 1], km[k][gr][c >> 1], y);
-                    y = fmaf(part[k][gr][n][c] * qscale[n][c & 1], ks[k][gr][c >> 1], y);
-                }
-                return y;
-            };
             float p[KP][NT][4], top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < KP; ++k)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) p[k][n][c] = score(k, n, c, -ref[n][c & 1]);
+                    for (int c = 0; c < 4; ++c) {
+                        float y = -ref[n][c & 1];
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            y = fmaf(qsum[gr][n][c & 1], km[k][gr][c >> 1], y);
+                            y = fmaf(part[k][gr][n][c] * qscale[n][c & 1], ks[k][gr][c >> 1], y);
+                        }
+                        p[k][n][c] = y;
+                    }
             // tokens behind the last one hold anything, causal rows see a part, pages may lack
             if (t + 16 * KP > t1 || (a.causal && t + 16 * KP - 1 > ahead) || holes) {
-                bool odd = false;  // a value scale that is no number
+                bool odd = false, any = false;  // a value scale that is no number; a token that is there
 #pragma unroll
                 for (int k = 0; k < KP; ++k) {
                     const int tk = t + 16 * k;
                     const int end = tk < t1 && piece_at(me, pages, tk) ? t1 : 0;
+                    any |= tk < end;
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
                         if (tk + g + 8 * r >= end)
@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                         for (int r = 0; r < 2; ++r) odd |= !(fabsf(vs[k][gr][r]) < INFINITY);
                 }
+                if (first && !any) continue;
                 if (odd) {  // it makes the rows that see it no number, and is nothing to the others
 #pragma unroll
                     for (int k = 0; k < KP; ++k)
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     top = fmax3(top, p[k][n][0], p[k][n][1]);
                     top = fmax3(top, p[k][n][2], p[k][n][3]);
                 }
-            if (__any_sync(0xffffffffu, top > 8.f)) {  // new references: the first step, and rarely after
+            if (__any_sync(0xffffffffu, first || top > 8.f)) {  // new references: the first step, and rarely after
                 float vtop = 0.f;
 #pragma unroll
                 for (int k = 0; k < KP; ++k)
@@ -362,30 +363,27 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float s[KP][2], mx = -INFINITY;
+                        float mx = -INFINITY;  // relative to the reference (0 in the first step)
 #pragma unroll
-                        for (int k = 0; k < KP; ++k)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const float seen = p[k][n][c + 2 * r];
-                                s[k][r] = seen == -INFINITY ? seen : score(k, n, c + 2 * r, 0.f);
-                                mx = fmaxf(mx, s[k][r]);
-                            }
+                        for (int k = 0; k < KP; ++k) mx = fmax3(mx, p[k][n][c], p[k][n][c + 2]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                         float corr = 1.f;
-                        if (mx > ref[n][c] + 8.f) {
-                            corr = ex2_approx(ref[n][c] - mx);
-                            ref[n][c] = mx;
+                        if (first ? mx > -INFINITY : mx > 8.f) {
+                            corr = first ? 0.f : ex2_approx(-mx);
+                            ref[n][c] += mx;
+#pragma unroll
+                            for (int k = 0; k < KP; ++k) {
+                                p[k][n][c] -= mx;
+                                p[k][n][c + 2] -= mx;
+                            }
                         }
-#pragma unroll
-                        for (int k = 0; k < KP; ++k)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) p[k][n][c + 2 * r] = s[k][r] - ref[n][c];
                         l[n][c] *= corr;
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
                             z[gr][n][c] *= corr;
+                            mid[gr][n][c] *= corr * vcorr;
+                            mid[gr][n][c + 2] *= corr * vcorr;
 #pragma unroll
                             for (int mt = 0; mt < 4; ++mt) {
                                 acc[gr][mt][n][c] *= corr * vcorr;
@@ -393,6 +391,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                             }
                         }
                     }
+                first = false;
             }
             // ---- weights and value products
 #pragma unroll
@@ -420,19 +419,14 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt) {
-                        // 1024 + c and 64 + c in fp16, less 1032 and 72: c - 8, exact
                         const uint32_t x = words[mt], y = x >> 8;
-                        uint32_t A[4] = {(x & 0x000F000Fu) | 0x64006400u, (x & 0x00F000F0u) | 0x54005400u,
-                                         (y & 0x000F000Fu) | 0x64006400u, (y & 0x00F000F0u) | 0x54005400u};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __half2 off = __float2half2_rn((i & 1) ? 72.f : 1032.f);
-                            const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&A[i]), off);
-                            A[i] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
+                        const uint32_t A[4] = {x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u};
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma_f16_16816(acc[gr][mt][n], A, pf[n][0], pf[n][1]);
                     }
+                    constexpr uint32_t kEights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16_16816(mid[gr][n], kEights, pf[n][0], pf[n][1]);
                 }
             }
         }
@@ -442,7 +436,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         // ---- the warps' results side by side in shared memory, then weighed: normalised, with
         // the logarithm (base 2) of the sum
         __syncthreads();  // the results of the item before this one are no longer read
-        const float vback = 1.f / vmul;
+        const float vback = 0x1p24f / vmul;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -458,7 +452,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                 }
                 const int r = n * 8 + 2 * tq + c;
                 if (g == 0) {
-                    s_ref[warp * 8 * NT + r] = ref[n][c];
+                    s_ref[warp * 8 * NT + r] = sum == 0.f ? -1e30f : ref[n][c];
                     s_sum[warp * 8 * NT + r] = sum;
                 }
                 float* dst = results + (warp * 8 * NT + r) * (64 * G);
@@ -468,11 +462,11 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
-                            dst[gr * 64 + mt * 16 + half * 8 + g] = fmaf(acc[gr][mt][n][c + 2 * half], vback, zs[gr]);
+                            dst[gr * 64 + mt * 16 + half * 8 + g] = fmaf(fmaf(acc[gr][mt][n][c + 2 * half], half ? 0.0625f : 1.f, -mid[gr][n][c + 2 * half]), vback, zs[gr]);
             }
         __syncthreads();  // the results and the next item's page numbers are there
         if (more) {
-            request_first(next, s_page[turn ^ 1]);
+            request_first(next, s_page[~turn & 1]);
             load_queries(next, qw);
         }
         const bool whole = s_req.len[me.b] <= a.chunk;
@@ -534,7 +528,6 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         }
         if (!more) return;
         me = next;
-        w = w_next;
     }
 }
 
@@ -621,16 +614,16 @@ namespace {
 
 template <int G, int NT>
 cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
-    constexpr int kMost = AttendSmem<G, NT>::kBytes + kCacheMaxRequests * 20;
+    constexpr int kMost = AttendSmem<G, NT>::kBytes + kCacheMaxRequests * Requests::kInts * 4;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     static int resident = 0;  // CTAs an SM for few requests
-    const int bytes = AttendSmem<G, NT>::kBytes + a.B * 20;
+    const int bytes = AttendSmem<G, NT>::kBytes + a.B * Requests::kInts * 4;
     std::call_once(once, [] {
         err = cudaFuncSetAttribute(cache_attend_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (err == cudaSuccess)
             err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_kernel<G, NT>, kAttendThreads,
-                                                                AttendSmem<G, NT>::kBytes + 64 * 20);
+                                                                AttendSmem<G, NT>::kBytes + 64 * Requests::kInts * 4);
     });
     if (err != cudaSuccess) return err;
     return launch_pdl(cache_attend_kernel<G, NT>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),

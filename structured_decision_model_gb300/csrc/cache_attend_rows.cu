@@ -73,16 +73,19 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
     __shared__ const uint8_t* s_page[kMaxPages];
     __shared__ __align__(16) PieceInfo s_info[2][kAttendWarps];
     __shared__ int s_exp[kAttendWarps];
-    scan_requests<G, true>(a, s_req, kRowsItem);
+    __shared__ Item s_item;
+    const int n_items = scan_requests<G, true>(a, s_req, kRowsItem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tq = lane & 3;
-    const int n_items = s_req.items[a.B - 1];
     const int page_mask = a.c.page - 1;
     uint8_t* raw = smem + warp * (ST * kBytes);
 
-    for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
-        const Item me = item_of<kRowsItem>(a, s_req, w);
+    for (int turn = 0; item_of_turn(turn) < n_items; ++turn) {
+        __syncthreads();  // nothing of the item before this one is needed any more
+        if (threadIdx.x == 0) s_item = item_of<kRowsItem>(a, s_req, item_of_turn(turn));
+        __syncthreads();
+        const Item& me = s_item;
         const int t0 = me.t0, t1 = me.t1, ahead = me.ahead;
         // ---- the split's pages, and the queries of the warp's rows g and g + 8
         for (int i = threadIdx.x; i < kMaxPages; i += kAttendThreads) {
@@ -134,7 +137,6 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-        __syncthreads();  // nothing of the item before this one is needed any more
         if (lane == 0) s_exp[warp] = least;
         __syncthreads();
         int common = 1000;
@@ -484,7 +486,7 @@ namespace {
 
 template <int G>
 cudaError_t launch_rows(const CacheAttendArgs& a, cudaStream_t s) {
-    constexpr int kMost = RowsSmem<G>::kBytes + kCacheMaxRequests * 20;
+    constexpr int kMost = RowsSmem<G>::kBytes + kCacheMaxRequests * Requests::kInts * 4;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     static int resident = 0;  // CTAs an SM for few requests
@@ -492,11 +494,11 @@ cudaError_t launch_rows(const CacheAttendArgs& a, cudaStream_t s) {
         err = cudaFuncSetAttribute(cache_attend_rows_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (err == cudaSuccess)
             err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_rows_kernel<G>, kAttendThreads,
-                                                                RowsSmem<G>::kBytes + 64 * 20);
+                                                                RowsSmem<G>::kBytes + 64 * Requests::kInts * 4);
     });
     if (err != cudaSuccess) return err;
     return launch_pdl(cache_attend_rows_kernel<G>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
-                      size_t(RowsSmem<G>::kBytes + a.B * 20), s, a);
+                      size_t(RowsSmem<G>::kBytes + a.B * Requests::kInts * 4), s, a);
 }
 
 }  // namespace
