@@ -86,8 +86,9 @@ CLEF_API int clef_cache_size(const clef_cache* cache, size_t* bytes);
  * their old length (they gain no token), and the status is CLEF_ERR_NO_PAGES.  A length out
  * of range leaves its request as it is, and gained tokens past n_slots get no slot: both are
  * CLEF_ERR_DEVICE_BOUNDS.  One page must not be held twice; the kernels' accesses stay in
- * bounds whatever the tables hold.  The arrays must not overlap.  1 <= B <=
- * CLEF_CACHE_MAX_REQUESTS, 1 <= table_stride, table_stride * page < 2^31, 0 <= n_slots. */
+ * bounds whatever the tables hold.  The arrays must not overlap, and each starts on 4 bytes.
+ * 1 <= B <= CLEF_CACHE_MAX_REQUESTS, 1 <= table_stride, table_stride * page <= 2^31 - 65536,
+ * B * table_stride and n_slots at most 2^30. */
 CLEF_API int clef_cache_plan(const clef_cache* cache, int32_t B, int32_t* lengths, const int32_t* want,
                              int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* free_count,
                              int32_t* cu_new, int32_t* slots, int32_t n_slots, int32_t* flags, void* stream);
@@ -132,12 +133,14 @@ CLEF_API int clef_cache_attend_workspace(const clef_cache* cache, int32_t B, int
  *                0 .. lengths[b] - 1.
  *   causal       0: every query sees all keys of its request.  1: the queries are the last
  *                tokens of the request; query i of n sees keys 0 .. lengths[b] - n + i.
- *   out          [total_q][q_heads][head_dim] of `dtype`, contiguous, 4-byte aligned; lse
- *                fp32 [total_q][q_heads], or NULL.
+ *   out          [total_q][q_heads][head_dim] of `dtype`, contiguous, 4-byte aligned, apart
+ *                from q; lse fp32 [total_q][q_heads], or NULL.
  * A query that sees no key (an empty request, or one with fewer keys than queries) gets
  * out = 0, lse = -inf.  Rows at and behind cu_q[B] are left as they were.
  * Scores, softmax and sums are fp32; softmax weights are rounded to fp16 (11 bits) for the
- * product with the codes; the output is rounded once.  A row's result depends on nothing
+ * product with the values, and so are the values themselves for requests of many query rows
+ * (queries x query heads a key/value head: over 32 at head_dim 64, over 16 at 128); the output
+ * is rounded once.  A row's result depends on nothing
  * but its own request: not on the batch, and bit for bit the same from call to call.
  * A table entry outside the cache hides its tokens, a length or cu_q out of range is cut
  * to it, each with CLEF_ERR_DEVICE_BOUNDS.

@@ -1022,7 +1022,8 @@ int clef_memory_store(const clef_config* cfg, const clef_schema* schema, int32_t
                       const void* workspace, size_t workspace_bytes, const clef_cache* cache, const int32_t* slots,
                       int32_t* flags, void* stream) {
     if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || !memory_cache_fits(cfg, cache) || !slots || !flags)
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || !memory_cache_fits(cfg, cache) || !slots ||
+        !flags || ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(flags)) & 3))
         return CLEF_ERR_INVALID_ARGUMENT;
     const Plan* pp = nullptr;
     const WsLayout* lp = nullptr;
@@ -1053,6 +1054,7 @@ int clef_stream_finish_memory(const clef_config* cfg, const void* const* weights
     if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
     if (!first_row || (hidden_dtype != CLEF_BF16 && hidden_dtype != CLEF_FP16) || !memory_cache_fits(cfg, cache) ||
         !cache->data || (reinterpret_cast<uintptr_t>(cache->data) & 255) || !block_table || !flags || table_stride < 1 ||
+        ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(flags)) & 3) ||
         (reinterpret_cast<uintptr_t>(attend_workspace) & 255))
         return CLEF_ERR_INVALID_ARGUMENT;
     const Plan* pp = nullptr;
@@ -1070,6 +1072,7 @@ int clef_stream_finish_memory(const clef_config* cfg, const void* const* weights
         for (int j = schema->q_opt_off[q]; j < schema->q_opt_off[q + 1]; ++j)
             if (schema->o_span[2 * j] < from) return CLEF_ERR_INVALID_ARGUMENT;
     }
+    if (int64_t(table_stride) * cache->page >= (int64_t(1) << 31)) return CLEF_ERR_INVALID_ARGUMENT;
     size_t need = 0;
     v = clef_cache_attend_workspace(cache, schema->B, pp->O, cfg->heads, table_stride * cache->page, &need);
     if (v != CLEF_OK) return v;

@@ -1,5 +1,6 @@
 // C ABI of the paged 4-bit memory cache: argument checks and launches.
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/clef_cache.h"
 #include "cache.h"
@@ -36,8 +37,12 @@ int check_data(const clef_cache* c) {
 
 bool bad_heads(const clef_cache* c, int head0, int n) { return head0 < 0 || n < 1 || n > c->heads || head0 > c->heads - n; }
 
+// The kernels count tokens, table entries and slots in 32 bits, and step past the last one.
+constexpr int64_t kMaxLength = kInt32 - 65536;
+constexpr int64_t kMaxEntries = kInt32 / 2;
+
 bool bad_table(const clef_cache* c, int B, int stride) {
-    return B < 1 || stride < 1 || int64_t(stride) * c->page >= kInt32 || int64_t(B) * stride >= kInt32;
+    return B < 1 || stride < 1 || int64_t(stride) * c->page > kMaxLength || int64_t(B) * stride > kMaxEntries;
 }
 
 struct AttendSpace {
@@ -78,8 +83,13 @@ int clef_cache_plan(const clef_cache* cache, int32_t B, int32_t* lengths, const 
     const int st = check_cache(cache, &v);
     if (st != CLEF_OK) return st;
     if (!lengths || !want || !block_table || !free_pages || !free_count || !cu_new || !flags || n_slots < 0 ||
-        (n_slots > 0 && !slots) || bad_table(cache, B, table_stride))
+        n_slots > kMaxEntries || (n_slots > 0 && !slots) || bad_table(cache, B, table_stride))
         return CLEF_ERR_INVALID_ARGUMENT;
+    for (const void* p : {static_cast<const void*>(lengths), static_cast<const void*>(want),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_count), static_cast<const void*>(cu_new),
+                          static_cast<const void*>(slots), static_cast<const void*>(flags)})
+        if (misaligned(p, 4)) return CLEF_ERR_INVALID_ARGUMENT;
     if (B > CLEF_CACHE_MAX_REQUESTS) return CLEF_ERR_UNSUPPORTED_CONFIG;
     CachePlanArgs a{};
     a.B = B; a.n_pages = v.n_pages; a.page_shift = v.page_shift; a.width = table_stride; a.n_slots = n_slots;
@@ -99,7 +109,7 @@ int clef_cache_append(const clef_cache* cache, int32_t n_tokens, int32_t head0, 
     if (n_tokens < 0 || bad_heads(cache, head0, n_heads) || (dtype != CLEF_BF16 && dtype != CLEF_FP16) || !flags)
         return CLEF_ERR_INVALID_ARGUMENT;
     if (n_tokens == 0) return CLEF_OK;
-    if (!k || !v || !slots || misaligned(k, 2) || misaligned(v, 2) || k_row_stride < 0 || k_head_stride < 0 ||
+    if (!k || !v || !slots || misaligned(k, 2) || misaligned(v, 2) || misaligned(slots, 4) || misaligned(flags, 4) || k_row_stride < 0 || k_head_stride < 0 ||
         v_row_stride < 0 || v_head_stride < 0)
         return CLEF_ERR_INVALID_ARGUMENT;
     a.n_tokens = n_tokens; a.head0 = head0; a.n_heads = n_heads; a.dtype = dtype;
@@ -120,7 +130,8 @@ int clef_cache_read(const clef_cache* cache, int32_t n_tokens, int32_t head0, in
     if (n_tokens < 0 || bad_heads(cache, head0, n_heads) || dtype < CLEF_BF16 || dtype > CLEF_FP32 || !flags)
         return CLEF_ERR_INVALID_ARGUMENT;
     if (n_tokens == 0) return CLEF_OK;
-    if (!k || !v || !slots || misaligned(k, 16) || misaligned(v, 16)) return CLEF_ERR_INVALID_ARGUMENT;
+    if (!k || !v || !slots || misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 4) || misaligned(flags, 4))
+        return CLEF_ERR_INVALID_ARGUMENT;
     a.n_tokens = n_tokens; a.head0 = head0; a.n_heads = n_heads; a.dtype = dtype;
     a.out_k = k; a.out_v = v; a.slots = slots; a.flags = flags;
     CKC(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
@@ -133,7 +144,7 @@ int clef_cache_attend_workspace(const clef_cache* cache, int32_t B, int32_t tota
     CacheView v;
     const int st = check_cache(cache, &v);
     if (st != CLEF_OK) return st;
-    if (B < 1 || total_q < 0 || q_heads < 1 || max_length < 1) return CLEF_ERR_INVALID_ARGUMENT;
+    if (B < 1 || total_q < 0 || q_heads < 1 || max_length < 1 || max_length > kMaxLength) return CLEF_ERR_INVALID_ARGUMENT;
     *bytes = size_t(AttendSpace(B, total_q, q_heads, cache->head_dim, max_length).bytes);
     return CLEF_OK;
 }
@@ -154,7 +165,8 @@ int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32
     if (B > CLEF_CACHE_MAX_REQUESTS) return CLEF_ERR_UNSUPPORTED_CONFIG;
     if (max_q == 0) return CLEF_OK;
     if (!q || !cu_q || !block_table || !lengths || !out || misaligned(q, 4) || misaligned(out, 4) || q_row_stride < 0 ||
-        q_head_stride < 0 || q_row_stride % 2 || q_head_stride % 2 || misaligned(workspace, 256))
+        q_head_stride < 0 || q_row_stride % 2 || q_head_stride % 2 || misaligned(workspace, 256) || misaligned(cu_q, 4) ||
+        misaligned(block_table, 4) || misaligned(lengths, 4) || misaligned(lse, 4) || misaligned(flags, 4))
         return CLEF_ERR_INVALID_ARGUMENT;
     const int64_t max_len = int64_t(table_stride) * cache->page;
     const AttendSpace sp(B, total_q, q_heads, cache->head_dim, max_len);
@@ -186,7 +198,7 @@ int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32
 }
 
 int clef_cache_status(int32_t* flags, void* stream) {
-    if (!flags) return CLEF_ERR_INVALID_ARGUMENT;
+    if (!flags || misaligned(flags, 4)) return CLEF_ERR_INVALID_ARGUMENT;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int h = 0;
     CKC(cudaMemcpyAsync(&h, flags, 4, cudaMemcpyDeviceToHost, st));

@@ -88,7 +88,7 @@ __device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, b
         q1 = min(max(q1, r.q0), a.total_q);
     }
     r.nq = min(q1 - r.q0, a.max_q);
-    r.chunks = max(1, int((int64_t(r.len) + a.chunk - 1) / a.chunk));
+    r.chunks = (r.len - 1) / a.chunk + 1;  // 1 for no keys too
     return r;
 }
 
@@ -227,7 +227,7 @@ __device__ __forceinline__ int scan_requests(const CacheAttendArgs& a, const Req
     for (int i = 0; i < kSizes - 1; ++i) sorted += total[i];
     int parts = 0, whole = 0, last = 0;
     for (int b = b0; b < b1; ++b) {
-        const int chunks = max(1, (s.len[b] + a.chunk - 1) / a.chunk);
+        const int chunks = (s.len[b] - 1) / a.chunk + 1;
         parts += chunks > 1 ? chunks * s.nq[b] * a.q_heads : 0;
         whole += s.len[b] / a.chunk * items_of_split<G, MANY>(a, s.nq[b], rows_per_item);
         last += b < sorted ? items_of_split<G, MANY>(a, s.nq[s.order[b]], rows_per_item) : 0;

@@ -595,6 +595,56 @@ def test_captured_steps_follow_their_buffers():
     assert torch.equal(c.state, eager.state)
 
 
+def test_large_plan_from_a_graph():
+    """A step of many slots (a cluster launch) captured and replayed: prompts in, then out again."""
+    r = random.Random(5)
+    lens = [r.randint(1, 400) for _ in range(60)]
+    c = MemoryCache(2000, page=16, heads=1, requests=60, max_len=400, device=DEV)
+    plain = Pages(2000, 16, 60, c.width)
+    want, n = ints(lens), sum(lens)
+    assert n > 8192
+    slots, cu = c.plan(want, n)          # the ordinary first call
+    c.plan(ints([0] * 60), 0)
+    start = c.state.clone()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            c.plan(want, n, slots=slots, cu=cu)
+        for _ in range(3):
+            c.state.copy_(start)
+            slots.fill_(-7)
+            graph.replay()
+            stream.synchronize()
+            plain = Pages(2000, 16, 60, c.width)
+            plain.free = start[61:61 + 2000].tolist()
+            ref, ref_cu, _ = plain.plan(lens)
+            assert slots.tolist() == ref and cu.tolist() == ref_cu and c.block_table.tolist() == plain.table()
+    assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 20, 50])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_scales_and_one_row_for_all(scale, n):
+    """Any finite scale; one query row expanded over the request (a row stride of zero)."""
+    g = gen(24)
+    c, memory = filled([900], 2, 64, 32, g)
+    q = torch.randn(1, 4, 64, generator=g, device=DEV).bfloat16().expand(n, 4, 64)
+    out, lse = c.attend(q, ints([0, n]), n, scale=scale, causal=True)
+    check(c, memory, q, [n], out, lse, scale, True, torch.bfloat16)
+
+
+def test_one_row_stored_in_many_slots():
+    g = gen(25)
+    c = MemoryCache(4, page=16, heads=3, head_dim=128, device=DEV)
+    k = torch.randn(1, 3, 128, generator=g, device=DEV).half()
+    slots = torch.randperm(64, generator=g, device=DEV)[:40].int()
+    c.append(k.expand(40, 3, 128), -k.expand(40, 3, 128), slots)
+    gk, gv = c.read(slots, torch.float32)
+    assert torch.equal(gk, quantised(k).float().expand(40, 3, 128)) and torch.equal(gv, quantised(-k).float().expand(40, 3, 128))
+
+
 def test_two_calls_at_once():
     """Attention of two streams over one cache at the same time, each with its own workspace."""
     g = gen(23)

@@ -56,7 +56,9 @@ def test_plan_refusals():
     good = [cache(), 4, P, P, P, 8, P, P, P, P, 16, P]
     for at in (2, 3, 4, 6, 7, 8, 9, 11):                       # every pointer
         refused(1, B.clef_cache_plan, *changed(good, at, 0))
-    for at, value in ((1, 0), (1, -1), (5, 0), (10, -1), (5, 1 << 25)):
+    for at in (2, 3, 4, 6, 7, 8, 9, 11):                       # and each on 4 bytes
+        refused(1, B.clef_cache_plan, *changed(good, at, P + 2))
+    for at, value in ((1, 0), (1, -1), (5, 0), (10, -1), (10, (1 << 30) + 1), (5, 1 << 25), (5, (1 << 25) - 1)):
         refused(1, B.clef_cache_plan, *changed(good, at, value))
     refused(3, B.clef_cache_plan, *changed(good, 1, 1025))
     refused(3, B.clef_cache_plan, *changed(good, 0, cache(page=24)))
@@ -67,7 +69,7 @@ def test_append_refusals():
     for at in (5, 8, 11, 12):
         refused(1, B.clef_cache_append, *changed(good, at, 0))
     for at, value in ((0, cache(data=0)), (0, cache(data=P + 128)), (1, -1), (2, -1), (2, 1), (3, 0), (3, 5), (4, B.FP32),
-                      (4, -1), (5, P + 1), (8, P + 1), (6, -256), (7, -1), (9, -1), (10, -64)):
+                      (4, -1), (5, P + 1), (8, P + 1), (11, P + 2), (12, P + 1), (6, -256), (7, -1), (9, -1), (10, -64)):
         refused(1, B.clef_cache_append, *changed(good, at, value))
     B.clef_cache_append(*changed(good, 1, 0))                  # nothing to do: no launch
 
@@ -76,7 +78,7 @@ def test_read_refusals():
     good = [cache(), 5, 0, 4, B.FP32, P, P, P, P]
     for at in (5, 6, 7, 8):
         refused(1, B.clef_cache_read, *changed(good, at, 0))
-    for at, value in ((0, cache(data=0)), (1, -1), (2, 4), (3, 0), (4, 3), (6, P + 8), (7, P + 8)):
+    for at, value in ((0, cache(data=0)), (1, -1), (2, 4), (3, 0), (4, 3), (5, P + 2), (6, P + 8), (7, P + 8), (8, P + 2)):
         refused(1, B.clef_cache_read, *changed(good, at, value))
     B.clef_cache_read(*changed(good, 1, 0))
 
@@ -90,18 +92,19 @@ def test_attend_refusals():
     for at in (8, 11, 12, 14, 17, 19, 20):
         refused(1, B.clef_cache_attend, *changed(good, at, 0))
     for at, value in ((0, cache(data=0)), (1, 0), (2, -1), (3, -1), (3, 7), (4, 0), (4, 6), (5, 1), (6, 0), (6, 5),
-                      (7, B.FP32), (8, P + 2), (9, 511), (10, 63), (9, -512), (13, 0), (13, 1 << 25),
+                      (7, B.FP32), (8, P + 2), (9, 511), (10, 63), (9, -512), (11, P + 2), (12, P + 1), (13, 0),
+                      (13, 1 << 25), (13, (1 << 25) - 1), (14, P + 2), (18, P + 2), (19, P + 3),
                       (15, float("nan")), (15, float("inf")), (16, 2), (17, P + 2), (20, P + 16)):
         refused(1, B.clef_cache_attend, *changed(good, at, value))
     refused(2, B.clef_cache_attend, *changed(good, 21, n - 1))
     refused(3, B.clef_cache_attend, *changed(good, 1, 1025))
     B.clef_cache_attend(*changed(good, 3, 0))                  # no queries: no launch
     # a table so wide that the partial rows cannot be counted in 32 bits
-    refused(3, B.clef_cache_attend, *changed(changed(changed(good, 13, (1 << 25) - 1), 2, 1 << 20), 21, 1 << 62))
+    refused(3, B.clef_cache_attend, *changed(changed(changed(good, 13, (1 << 25) - 1024), 2, 1 << 20), 21, 1 << 62))
 
 
 def test_status_of_nothing_is_refused():
-    assert B.load().clef_cache_status(0, None) == 1
+    assert B.load().clef_cache_status(0, None) == 1 and B.load().clef_cache_status(P + 2, None) == 1
     assert B.clef_status_string(7) == "no free cache pages left"
 
 
@@ -120,7 +123,7 @@ def test_memory_store_refusals():
     good = [cfg, sch, 0, 0, 10, P, ws, cache(heads=32), P, P]
     length = int(bt.lengths[0])
     for at, value in ((2, -1), (2, 2), (3, -1), (4, 0), (4, length + 1), (5, 0), (5, P + 16), (7, cache(heads=16)),
-                      (7, cache(heads=32, head_dim=128)), (7, cache(data=0, heads=32)), (8, 0), (9, 0)):
+                      (7, cache(heads=32, head_dim=128)), (7, cache(data=0, heads=32)), (8, 0), (8, P + 2), (9, 0), (9, P + 1)):
         refused(1, B.clef_memory_store, *changed(good, at, value))
     refused(2, B.clef_memory_store, *changed(good, 6, ws - 1))
 
@@ -138,7 +141,7 @@ def test_stream_finish_memory_refusals():
     for at in (2, 5, 7, 8, 9, 10, 11, 12, 13, 14, 17, 19, 20):
         refused(1, B.clef_stream_finish_memory, *changed(good, at, 0))
     for at, value in ((4, [first[0] + 1, first[1]]), (4, [first[0], int(bt.lengths[1])]), (4, [-1, 0]), (4, [0]),
-                      (6, B.FP32), (16, cache(heads=16)), (18, 0), (18, 4), (20, P + 16)):
+                      (6, B.FP32), (16, cache(heads=16)), (17, P + 2), (18, 0), (18, 4), (18, 1 << 25), (18, 1 << 30), (19, P + 2), (20, P + 16)):
         refused(1, B.clef_stream_finish_memory, *changed(good, at, value))
     refused(2, B.clef_stream_finish_memory, *changed(good, 21, space - 1))
     refused(2, B.clef_stream_finish_memory, *changed(good, 15, ws - 1))
