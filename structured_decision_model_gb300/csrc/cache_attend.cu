@@ -31,7 +31,7 @@
 
 namespace clef {
 
-template <int G, int NT>
+template <int G, int NT, int C>
 struct AttendSmem {
     // 16-token pieces a step: two where the registers allow, which halves the cost of a step's
     // waits, votes and addresses
@@ -39,26 +39,29 @@ struct AttendSmem {
     // steps in flight a warp
     static constexpr int kStages = G == 2 ? 2 : NT <= 2 ? 3 : 4;
     static constexpr int kRing = kAttendWarps * kStages * kPieces * kPiece * G;
-    static constexpr int kResults = kAttendWarps * 8 * NT * 64 * G * 4;  // the warps' sums of values
-    static constexpr int kBytes = kRing + kResults + 2 * kAttendWarps * 8 * NT * 4;
+    static constexpr int kRows = 4 * C * NT;  // query rows of an item
+    static constexpr int kResults = kAttendWarps * kRows * 64 * G * 4;  // the warps' sums of values
+    static constexpr int kBytes = kRing + kResults + 2 * kAttendWarps * kRows * 4;
 };
 
-template <int G, int NT>
+template <int G, int NT, int C>
 __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : NT == 2 ? 3 : 2)
     cache_attend_kernel(const CacheAttendArgs a) {
-    using Smem = AttendSmem<G, NT>;
+    using Smem = AttendSmem<G, NT, C>;
     constexpr int ST = Smem::kStages, KP = Smem::kPieces;
-    constexpr int kBytes = kPiece * G;
+    constexpr int kBytes = kPiece * G, R = Smem::kRows;
+    // column c of a lane's in block n is row `row_of(n, c)` of the item
+    auto row_of = [&](int n, int c) { return C == 2 ? n * 8 + 2 * (int(threadIdx.x) & 3) + c : int(threadIdx.x) & 3; };
     constexpr int kMaxPages = kAttendMaxChunk / 16;
     griddep_wait();
     griddep_launch();
     extern __shared__ __align__(16) uint8_t smem[];
     float* results = reinterpret_cast<float*>(smem + Smem::kRing);  // [warp][row][value]
     float* s_ref = results + Smem::kResults / 4;                     // [warp][row]
-    float* s_sum = s_ref + kAttendWarps * 8 * NT;
+    float* s_sum = s_ref + kAttendWarps * R;
     const Requests s_req(reinterpret_cast<int*>(smem + Smem::kBytes), a.B);
     __shared__ int s_page[2][kMaxPages];  // page numbers of the split at hand and of the next one
-    const int n_items = scan_requests<G, false>(a, s_req, 8 * NT);
+    const int n_items = scan_requests<G, false>(a, s_req, R);
     if (blockIdx.x == 0 && a.part_off)
         for (int b = threadIdx.x; b < a.B; b += kAttendThreads) a.part_off[b] = b ? s_req.parts[b - 1] : 0;
 
@@ -122,8 +125,8 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
     auto load_queries = [&](const Item& k, uint32_t (&qw)[NT][G][8]) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = n * 8 + g;
-            const bool live = r < k.rows;
+            const int r = C == 2 ? n * 8 + g : g >> 1;
+            const bool live = r < k.rows && (C == 2 || !(g & 1));
             const int qi = live ? by_share(a, k.row0 + r) : 0;
             const int qh = k.h * a.share + (live ? k.row0 + r - qi * a.share : 0);
             const uint16_t* q = static_cast<const uint16_t*>(a.q) + (s_req.q0[k.b] + qi) * a.q_row + qh * a.q_head + 2 * tq;
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
     };
 
     if (item_of_turn(0) >= n_items) return;
-    Item me = item_of<8 * NT>(a, s_req, item_of_turn(0));
+    Item me = item_of<R>(a, s_req, item_of_turn(0));
     request_pages(me, s_page[0]);
     cp_async_commit();
     uint32_t qw[NT][G][8];
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                 }
             const float back = a.scale_log2 * pow2i(24 - min(e, 120));
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < C; ++c) {
                 const int from = (2 * tq + c) * 4;
                 qscale[n][c] = __shfl_sync(0xffffffffu, back, from);
 #pragma unroll
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         const bool more = w_next < n_items;
         Item next = me;
         if (more) {
-            next = item_of<8 * NT>(a, s_req, w_next);
+            next = item_of<R>(a, s_req, w_next);
             request_pages(next, s_page[~turn & 1]);
         }
 
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 4; c += 3 - C) {
                         float y = -ref[n][c & 1];
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
@@ -295,8 +298,8 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int sees = a.causal ? ahead + by_share(a, me.row0 + n * 8 + 2 * tq + (c & 1)) + 1 : end;
+                        for (int c = 0; c < 4; c += 3 - C) {
+                            const int sees = a.causal ? ahead + by_share(a, me.row0 + row_of(n, c & 1)) + 1 : end;
                             if (tk + g + 8 * (c >> 1) >= min(sees, end)) p[k][n][c] = -INFINITY;
                         }
 #pragma unroll
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                                        for (int c = 0; c < 2; ++c)
+                                        for (int c = 0; c < C; ++c)
                                             if (!(p[k][n][c + 2 * r] == -INFINITY)) z[gr][n][c] = NAN;
                                 }
                 }
@@ -337,8 +340,12 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
             for (int k = 0; k < KP; ++k)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    top = fmax3(top, p[k][n][0], p[k][n][1]);
-                    top = fmax3(top, p[k][n][2], p[k][n][3]);
+                    if (C == 2) {
+                        top = fmax3(top, p[k][n][0], p[k][n][1]);
+                        top = fmax3(top, p[k][n][2], p[k][n][3]);
+                    } else {
+                        top = fmax3(top, p[k][n][0], p[k][n][2]);
+                    }
                 }
             if (__any_sync(0xffffffffu, first || top > 8.f)) {  // new references: the first step, and rarely after
                 float vtop = 0.f;
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < C; ++c) {
                         float mx = -INFINITY;  // relative to the reference (0 in the first step)
 #pragma unroll
                         for (int k = 0; k < KP; ++k) mx = fmax3(mx, p[k][n][c], p[k][n][c + 2]);
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 4; c += 3 - C) {
                         p[k][n][c] = ex2_approx(p[k][n][c]);
                         l[n][c & 1] += p[k][n][c];
                     }
@@ -411,10 +418,10 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float w0 = p[k][n][2 * r], w1 = p[k][n][2 * r + 1];
-                            pf[n][r] = transpose8(pack_f16(w0 * vw[k][gr][r], w1 * vw[k][gr][r]));
+                            const float w0 = p[k][n][2 * r], w1 = C == 2 ? p[k][n][2 * r + 1] : 0.f;
+                            pf[n][r] = transpose8(pack_f16(w0 * vw[k][gr][r], C == 2 ? w1 * vw[k][gr][r] : 0.f));
                             z[gr][n][0] = fmaf(w0, vm[k][gr][r], z[gr][n][0]);
-                            z[gr][n][1] = fmaf(w1, vm[k][gr][r], z[gr][n][1]);
+                            if (C == 2) z[gr][n][1] = fmaf(w1, vm[k][gr][r], z[gr][n][1]);
                         }
                     const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < C; ++c) {
                 float sum = l[n][c], zs[G];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -450,12 +457,12 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) zs[gr] += __shfl_xor_sync(0xffffffffu, zs[gr], o);
                 }
-                const int r = n * 8 + 2 * tq + c;
+                const int r = row_of(n, c);
                 if (g == 0) {
-                    s_ref[warp * 8 * NT + r] = sum == 0.f ? -1e30f : ref[n][c];
-                    s_sum[warp * 8 * NT + r] = sum;
+                    s_ref[warp * R + r] = sum == 0.f ? -1e30f : ref[n][c];
+                    s_sum[warp * R + r] = sum;
                 }
-                float* dst = results + (warp * 8 * NT + r) * (64 * G);
+                float* dst = results + (warp * R + r) * (64 * G);
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr)
 #pragma unroll
@@ -473,15 +480,15 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         // warp w finishes rows w, w + 4, ...: lane i weighs the i-th of them, then all lanes its values
         float wgt[kAttendWarps];
         int64_t row = -1;
-        if (lane < 2 * NT) {
+        if (lane < C * NT) {
             const int r = warp + kAttendWarps * lane;
             float top = -1e30f, sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kAttendWarps; ++i) top = fmaxf(top, s_ref[i * 8 * NT + r]);
+            for (int i = 0; i < kAttendWarps; ++i) top = fmaxf(top, s_ref[i * R + r]);
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) {
-                wgt[i] = ex2_approx(s_ref[i * 8 * NT + r] - top);
-                sum = fmaf(s_sum[i * 8 * NT + r], wgt[i], sum);
+                wgt[i] = ex2_approx(s_ref[i * R + r] - top);
+                sum = fmaf(s_sum[i * R + r], wgt[i], sum);
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
             }
         }
 #pragma unroll
-        for (int j = 0; j < 2 * NT; ++j) {
+        for (int j = 0; j < C * NT; ++j) {
             const int64_t to = __shfl_sync(0xffffffffu, row, j);
             float wj[kAttendWarps];
 #pragma unroll
@@ -513,7 +520,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                 float2 o = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kAttendWarps; ++i) {
-                    const float2 x = *reinterpret_cast<const float2*>(results + (i * 8 * NT + warp + kAttendWarps * j) * (64 * G) +
+                    const float2 x = *reinterpret_cast<const float2*>(results + (i * R + warp + kAttendWarps * j) * (64 * G) +
                                                                       gr * 64 + lane * 2);
                     o.x = fmaf(x.x, wj[i], o.x);
                     o.y = fmaf(x.y, wj[i], o.y);
@@ -612,21 +619,21 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs 
 
 namespace {
 
-template <int G, int NT>
+template <int G, int NT, int C>
 cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
-    constexpr int kMost = AttendSmem<G, NT>::kBytes + kCacheMaxRequests * Requests::kInts * 4;
+    constexpr int kMost = AttendSmem<G, NT, C>::kBytes + kCacheMaxRequests * Requests::kInts * 4;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     static int resident = 0;  // CTAs an SM for few requests
-    const int bytes = AttendSmem<G, NT>::kBytes + a.B * Requests::kInts * 4;
+    const int bytes = AttendSmem<G, NT, C>::kBytes + a.B * Requests::kInts * 4;
     std::call_once(once, [] {
-        err = cudaFuncSetAttribute(cache_attend_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        err = cudaFuncSetAttribute(cache_attend_kernel<G, NT, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (err == cudaSuccess)
-            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_kernel<G, NT>, kAttendThreads,
-                                                                AttendSmem<G, NT>::kBytes + 64 * Requests::kInts * 4);
+            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_kernel<G, NT, C>, kAttendThreads,
+                                                                AttendSmem<G, NT, C>::kBytes + 64 * Requests::kInts * 4);
     });
     if (err != cudaSuccess) return err;
-    return launch_pdl(cache_attend_kernel<G, NT>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
+    return launch_pdl(cache_attend_kernel<G, NT, C>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
                       bytes, s, a);
 }
 
@@ -638,12 +645,15 @@ cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s) {
     const int64_t most = int64_t(a.max_q) * a.share;  // query rows of any request
     cudaError_t e;
     if (a.c.groups == 1)
-        e = most <= 8    ? launch_attend<1, 1>(a, s)
-            : most <= 16 ? launch_attend<1, 2>(a, s)
-            : most <= 24 ? launch_attend<1, 3>(a, s)
-                         : launch_attend<1, 4>(a, s);
+        e = most <= 4    ? launch_attend<1, 1, 1>(a, s)
+            : most <= 8  ? launch_attend<1, 1, 2>(a, s)
+            : most <= 16 ? launch_attend<1, 2, 2>(a, s)
+            : most <= 24 ? launch_attend<1, 3, 2>(a, s)
+                         : launch_attend<1, 4, 2>(a, s);
     else
-        e = most <= 8 ? launch_attend<2, 1>(a, s) : launch_attend<2, 2>(a, s);
+        e = most <= 4   ? launch_attend<2, 1, 1>(a, s)
+            : most <= 8 ? launch_attend<2, 1, 2>(a, s)
+                        : launch_attend<2, 2, 2>(a, s);
     if (e == cudaSuccess && most > few_rows(a.c.groups)) e = launch_cache_attend_rows(a, s);
     if (e != cudaSuccess || a.max_chunks <= 1) return e;
     // long memories: a row's splits are shared out among the eight warps of a CTA
