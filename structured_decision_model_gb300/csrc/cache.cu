@@ -233,9 +233,15 @@ cudaError_t launch_cache_plan(const CachePlanArgs& a, cudaStream_t s) {
 
 // ------------------------------------------------------------------- rows
 //
-// A warp takes 16 consecutive rows of one head.  Four lanes hold the 64 values of a row's
-// group, 16 each (lane / 4 is the row of eight, lane % 4 the run of 16 values): a lane owns
-// the eight code bytes of its run, and a row's minimum and maximum cost two exchanges.
+// Store: a warp takes a window of 16 consecutive rows, one group of 64 values of one head at a
+// time.  Four lanes hold a row's group, 16 values each (lane / 4 is the row of eight, lane % 4
+// the run of 16 values): a lane owns the eight code bytes of its run, and a row's minimum and
+// maximum cost two exchanges.  Where 16 rows fill a whole piece, wherever in the window they
+// start, their codes go through shared memory and out as 16 bytes a lane; other rows write the
+// bytes that are their own.  Read back: eight rows a warp, words straight from the piece.
+//   131072 rows x 16 heads of 64 in bf16: store 136 us (689 MB, 75 % of the measured copy rate;
+// 860 instructions a window and head's group, five of them for each quotient, fill 69 % of the
+// issue slots), read back 110 us (92 %).
 
 namespace {
 
@@ -509,7 +515,8 @@ namespace {
 // Two codes as bf16 numbers (bits 0-3 and 16-19 of x): 128 + c, less 128, exact.
 __device__ __forceinline__ uint32_t codes2(uint32_t x) {
     const uint32_t w = (x & 0x000F000Fu) | 0x43004300u, off = 0x43004300u;
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&off));
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&w),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&off));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 // scale * c + minimum with c and the scale in bf16, in one fp32 rounding.
@@ -627,7 +634,8 @@ namespace {
 dim3 rows_grid(const CacheRowsArgs& a, int per_cta) {
     const int64_t windows = (int64_t(a.n_tokens) + 15) / 16, parts = (a.n_heads * a.c.groups + per_cta - 1) / per_cta;
     const int64_t most = int64_t(num_sms()) * 32;
-    return windows * parts <= most ? dim3(unsigned(windows), unsigned(parts)) : dim3(unsigned(windows < most ? windows : most), 1);
+    if (windows * parts <= most) return dim3(unsigned(windows), unsigned(parts));
+    return dim3(unsigned(windows < most ? windows : most), 1);
 }
 
 }  // namespace

@@ -109,13 +109,14 @@ int clef_cache_append(const clef_cache* cache, int32_t n_tokens, int32_t head0, 
     if (n_tokens < 0 || bad_heads(cache, head0, n_heads) || (dtype != CLEF_BF16 && dtype != CLEF_FP16) || !flags)
         return CLEF_ERR_INVALID_ARGUMENT;
     if (n_tokens == 0) return CLEF_OK;
-    if (!k || !v || !slots || misaligned(k, 2) || misaligned(v, 2) || misaligned(slots, 4) || misaligned(flags, 4) || k_row_stride < 0 || k_head_stride < 0 ||
-        v_row_stride < 0 || v_head_stride < 0)
+    if (!k || !v || !slots || misaligned(k, 2) || misaligned(v, 2) || misaligned(slots, 4) || misaligned(flags, 4) ||
+        k_row_stride < 0 || k_head_stride < 0 || v_row_stride < 0 || v_head_stride < 0)
         return CLEF_ERR_INVALID_ARGUMENT;
     a.n_tokens = n_tokens; a.head0 = head0; a.n_heads = n_heads; a.dtype = dtype;
     a.k = k; a.k_row = k_row_stride; a.k_head = k_head_stride;
     a.v = v; a.v_row = v_row_stride; a.v_head = v_head_stride;
-    a.aligned = !misaligned(k, 16) && !misaligned(v, 16) && (k_row_stride | k_head_stride | v_row_stride | v_head_stride) % 8 == 0;
+    a.aligned = !misaligned(k, 16) && !misaligned(v, 16) &&
+                (k_row_stride | k_head_stride | v_row_stride | v_head_stride) % 8 == 0;
     a.slots = slots; a.flags = flags;
     CKC(launch_cache_append(a, static_cast<cudaStream_t>(stream)));
     return CLEF_OK;
@@ -180,7 +181,8 @@ int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32
     if (sp.bytes > 0 && !workspace) return CLEF_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < size_t(sp.bytes)) return CLEF_ERR_WORKSPACE_TOO_SMALL;
     a.B = B; a.total_q = total_q; a.max_q = max_q; a.q_heads = q_heads; a.head0 = head0; a.kv_heads = kv_heads;
-    a.share = q_heads / kv_heads; a.share_inv = ((uint64_t(1) << 40) + a.share - 1) / a.share; a.dtype = dtype; a.width = table_stride; a.causal = causal;
+    a.share = q_heads / kv_heads; a.share_inv = ((uint64_t(1) << 40) + a.share - 1) / a.share;
+    a.dtype = dtype; a.width = table_stride; a.causal = causal;
     a.q = q; a.q_row = q_row_stride; a.q_head = q_head_stride;
     a.cu_q = cu_q; a.table = block_table; a.lengths = lengths;
     a.scale_log2 = float(double(scale) * 1.4426950408889634);

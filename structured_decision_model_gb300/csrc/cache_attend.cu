@@ -1,29 +1,42 @@
 // Attention over the paged 4-bit memory cache (clef_cache_attend).
 //
+// The few-rows kernel, and the merge of both kernels' splits; cache_attend_rows.cu has the
+// kernel for requests of many query rows.
+//
 // A CTA of four warps takes one item: a split of a request's keys, one key/value head, and up
-// to 8 NT query rows of the heads that share it.  Its warps take the 16-token pieces of the
-// split in turn, each through a ring of its own that cp.async fills several pieces ahead
-// (no barrier, nothing to wait for but the warp's own copies), and meet once, at the end of
-// the item, to weigh their results.  The products run transposed on mma.sync, the keys
-// as the M dimension: S^T = K Q^T (16 keys x 8 queries an instruction, so that a single
-// token wastes 7 of 8 columns rather than 15 of 16 rows) and O^T += V^T P^T.  The A operand
-// of both is made in registers from the codes: the stored order gives each lane its own 16
-// bytes of a 16-token piece.
+// to 4 C NT query rows of the heads that share it.  Its warps take the split in steps of 32
+// keys (two 16-token pieces) in turn, each through a ring of its own that cp.async fills
+// several steps ahead (no barrier, nothing to wait for but the warp's own copies), and meet at
+// the end of the item to weigh their results; the next item's pages, pieces and queries are
+// under way by then.  The products run transposed on mma.sync, the keys as the M dimension:
+// S^T = K Q^T (16 keys x 8 queries an instruction, so that a single token wastes 7 of 8 columns
+// rather than 15 of 16 rows) and O^T += V^T P^T.  The A operand of both is made in registers
+// from the codes: the stored order gives each lane its own 16 bytes of a 16-token piece.
 //   Keys: a 4-bit code in bits 0-3 of an fp16 word is the subnormal c 2^-24, exact, and in
 // bits 4-7 c 2^-20, so one AND makes two operand values; the 2^4 between the two halves of
 // a run of 16 is taken out of the queries instead.  The score is then, in fp32,
 //   s_t (q . c_t) + m_t (sum q),  with s_t and m_t the key's scale and minimum.
 // Queries are scaled by a power of two per row to fill fp16's range (exact).
-//   Values: o = sum_t p_t (s_t c_t + m_t) = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t).
-// The weights p_t s_t 2^E are rounded to fp16 (11 bits, E keeps the largest s_t 2^E in [4, 8)
-// or the weights within 2^11), the second sum is fp32; centring the codes keeps the first sum, whose terms carry
-// the rounding, from cancelling against the second.
+//   Values: with w_t = p_t s_t,
+//   o = sum_t p_t (s_t c_t + m_t) = sum_t w_t c_t - sum_t 8 w_t + sum_t p_t (m_t + 8 s_t).
+// The weights w_t 2^E are rounded to fp16 (11 bits; E puts the largest s_t 2^E met so far in
+// [4, 8), so that the weights stay under 2^11), once for the first two sums, which are products
+// of the matrix unit with the codes and with eights: their difference is that of centred codes
+// |c - 8| <= 8, and what the rounding costs is relative to it, not to the whole range of the
+// codes.  The third sum is fp32.  (Centring the codes themselves takes 16 more instructions a
+// piece and 10 % more time.)
 // The softmax reference of a row moves only when a score exceeds it by 2^8 (then all sums
 // of the warp are rescaled), so that a step needs no reduction between lanes: each lane sums
 // the keys that it holds, and the lanes are added once at the end of the item.
 //
 // Requests longer than one split leave normalised partials with their log-sum, which the
 // merge kernel weighs.
+//
+// What bounds it: instruction issue, the integer pipe above all (about 130 instructions for 16
+// keys, 56 of them to split codes; 51 % of the issue slots and 57 % of the memory rate in a
+// decoding step of 64 requests of 400 to 16000 keys with 8 heads of 128: 219 MB in 51 us), and
+// the unequal ends of a call; 256 requests of 4096 keys (1.2 GB) take 213 us, 84 % of the
+// memory's measured copy rate.
 #include <algorithm>
 #include <mutex>
 
@@ -33,8 +46,8 @@ namespace clef {
 
 template <int G, int NT, int C>
 struct AttendSmem {
-    // 16-token pieces a step: two where the registers allow, which halves the cost of a step's
-    // waits, votes and addresses
+    // 16-token pieces a step: two halve the cost of a step's waits, votes and addresses; the same
+    // for all, so that a row's sums do not depend on the other requests' rows
     static constexpr int kPieces = 2;
     // steps in flight a warp
     static constexpr int kStages = G == 2 ? 2 : NT <= 2 ? 3 : 4;
@@ -469,7 +482,10 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
-                            dst[gr * 64 + mt * 16 + half * 8 + g] = fmaf(fmaf(acc[gr][mt][n][c + 2 * half], half ? 0.0625f : 1.f, -mid[gr][n][c + 2 * half]), vback, zs[gr]);
+                            // (codes of the upper half of a run count 2^4)
+                            dst[gr * 64 + mt * 16 + half * 8 + g] =
+                                fmaf(fmaf(acc[gr][mt][n][c + 2 * half], half ? 0.0625f : 1.f, -mid[gr][n][c + 2 * half]),
+                                     vback, zs[gr]);
             }
         __syncthreads();  // the results and the next item's page numbers are there
         if (more) {
@@ -563,7 +579,8 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs 
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int i = 0; i < G; ++i)
-                    v[j][i] = j < n ? *reinterpret_cast<const float2*>(a.part_o + (p0 + (k0 + j) * stride) * (64 * G) + i * 64 + lane * 2)
+                    v[j][i] = j < n ? *reinterpret_cast<const float2*>(a.part_o + (p0 + (k0 + j) * stride) * (64 * G) +
+                                                                       i * 64 + lane * 2)
                                     : make_float2(0.f, 0.f);
             const float mx = fmaxf(top, warp_max(x));
             const float corr = ex2_approx(top - mx), w = ex2_approx(x - mx);
@@ -587,7 +604,8 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs 
             s_sum[warp] = sum;
         }
 #pragma unroll
-        for (int i = 0; i < G; ++i) *reinterpret_cast<float2*>(&s_o[warp][i * 64 + lane * 2]) = make_float2(o[2 * i], o[2 * i + 1]);
+        for (int i = 0; i < G; ++i)
+            *reinterpret_cast<float2*>(&s_o[warp][i * 64 + lane * 2]) = make_float2(o[2 * i], o[2 * i + 1]);
         __syncthreads();
         if (part != 0) return;
         float all = -1e30f;
@@ -641,7 +659,9 @@ cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s) {
     if (a.total_q <= 0 || a.max_q <= 0) return cudaSuccess;
-    // blocks of 8 query rows a warp: as few as the requests that come here can have
+    // Columns of the matrix instruction: as few as the requests that come here can have rows.  Up to
+    // four rows sit in every other column, so that each lane has one column of scores, not two
+    // (64 requests, 4 rows of 128 values each: 51 us, and 55 us with all columns).
     const int64_t most = int64_t(a.max_q) * a.share;  // query rows of any request
     cudaError_t e;
     if (a.c.groups == 1)

@@ -95,7 +95,7 @@ __device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, b
 // Requests of up to so many query rows (queries x the query heads that share a key head) are
 // the few-rows kernel's, the others the many-rows kernel's: by the request alone, so that a
 // row's result does not depend on the batch.  128 requests x 1024 keys x 16 heads of 64: 24 rows
-// take 89 us there and 137 here, 64 rows 219 there and 180 here.
+// take 96 us in the first and 137 in the second, 64 rows 219 and 190.
 __host__ __device__ constexpr int few_rows(int groups) { return groups == 1 ? 32 : 16; }
 
 // Inclusive sums of two numbers over the CTA's threads.
@@ -247,8 +247,8 @@ __device__ __forceinline__ int scan_requests(const CacheAttendArgs& a, const Req
 }
 
 // The item of a CTA's n-th turn: items, largest first, are dealt out in rows that run forward
-// and back, so that the sums of their sizes come out nearly even (a decoding step of 64 requests of
-// 400 to 16000 keys takes 50 us, and 64 us where they are dealt in the requests' order).
+// and back, so that the sums of their sizes come out nearly even (a decoding step of 64 requests
+// of 400 to 16000 keys, 8 heads of 128: 55 us, and 64 us dealt in the requests' order).
 __device__ __forceinline__ int item_of_turn(int n) {
     return n * int(gridDim.x) + ((n & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
 }
