@@ -20,6 +20,8 @@ import torch
 from . import binding as B
 
 _DTYPES = {torch.bfloat16: B.BF16, torch.float16: B.FP16, torch.float32: B.FP32}
+_ROW_DTYPES = {torch.bfloat16: B.BF16, torch.float16: B.FP16}
+_INT32 = torch.int32
 
 
 def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -88,23 +90,17 @@ class MemoryCache:
 
     # ------------------------------------------------------------- checks
 
-    def _on_device(self, t, what):
-        if t.device != self.device:
-            _refuse(f"{what} is on {t.device}, the cache on {self.device}")
-
     def checked_slots(self, slots: torch.Tensor) -> torch.Tensor:
-        if slots.device != self.device:
-            self._on_device(slots, "slots")
-        if slots.dtype != torch.int32 or slots.dim() != 1 or not slots.is_contiguous():
-            _refuse("slots: a contiguous int32 vector")
+        if slots.dtype is not _INT32 or slots.dim() != 1 or not slots.is_contiguous() or slots.device != self.device:
+            _refuse(f"slots and offsets: a contiguous int32 vector on {self.device}")
         return slots
 
     def checked_table(self, table: Optional[torch.Tensor], n: int) -> torch.Tensor:
         if table is None:
             table = self.block_table
-        self._on_device(table, "block_table")
-        if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] < n or not table.is_contiguous():
-            _refuse("block_table: contiguous int32 [requests, pages]")
+        if table.dtype is not _INT32 or table.dim() != 2 or table.shape[0] < n or not table.is_contiguous() or \
+                table.device != self.device:
+            _refuse(f"block_table: contiguous int32 [requests, pages] on {self.device}")
         return table
 
     def _elsewhere(self):
@@ -113,17 +109,14 @@ class MemoryCache:
             _refuse("the cache is not on a GPU")
         return _current_device() != self._index
 
-    def _check(self, status, where):
-        if status != B.CLEF_OK:
-            raise B.ClefError(status, where)
-
     def _rows(self, t, what):
-        self._on_device(t, what)
-        if t.dim() != 3 or t.shape[2] != self.head_dim or t.stride(2) != 1 or t.dtype not in (torch.bfloat16, torch.float16):
-            _refuse(f"{what}: bf16 or fp16 [tokens, heads, {self.head_dim}], values contiguous")
+        """The type, shape and strides of rows [tokens, heads, head_dim]."""
+        dtype, shape, strides = _ROW_DTYPES.get(t.dtype), t.shape, t.stride()
+        if dtype is None or len(shape) != 3 or shape[2] != self.head_dim or strides[2] != 1 or t.device != self.device:
+            _refuse(f"{what}: bf16 or fp16 [tokens, heads, {self.head_dim}], values contiguous, on {self.device}")
         if t.requires_grad and torch.is_grad_enabled():
             _refuse(f"{what} requires a gradient, which a 4-bit cache does not pass on")
-        return _DTYPES[t.dtype]
+        return dtype, shape, strides
 
     # ---------------------------------------------------------- operators
 
@@ -132,9 +125,9 @@ class MemoryCache:
         """Take the requests' lengths to ``want`` (int32 [requests]): the slots of the tokens
         gained, request by request, -1 behind them (int32 [n_slots]), and their running sum
         (int32 [requests + 1])."""
-        self._on_device(want, "want")
-        if want.dtype != torch.int32 or want.shape != (self.requests,) or not want.is_contiguous():
-            _refuse("want: contiguous int32 [requests]")
+        if want.dtype is not _INT32 or want.dim() != 1 or want.numel() != self.requests or \
+                not want.is_contiguous() or want.device != self.device:
+            _refuse(f"want: contiguous int32 [requests] on {self.device}")
         if slots is not None and self.checked_slots(slots).numel() != n_slots:
             _refuse("slots: int32 [n_slots]")
         if cu is not None and self.checked_slots(cu).numel() != self.requests + 1:
@@ -143,31 +136,34 @@ class MemoryCache:
             with torch.cuda.device(self._index):
                 return self.plan(want, n_slots, slots, cu)
         if slots is None:
-            slots = torch.empty(n_slots, dtype=torch.int32, device=self.device)
+            slots = torch.empty(n_slots, dtype=_INT32, device=self.device)
         if cu is None:
-            cu = torch.empty(self.requests + 1, dtype=torch.int32, device=self.device)
+            cu = torch.empty(self.requests + 1, dtype=_INT32, device=self.device)
         lengths, table, free_pages, free_count = self._accounts
-        self._check(self._lib.clef_cache_plan(self.struct, self.requests, lengths, want.data_ptr(), table, self.width,
-                                              free_pages, free_count, cu.data_ptr(), slots.data_ptr(), n_slots,
-                                              self._flags, _raw_stream(self._index)), "clef_cache_plan")
+        status = self._lib.clef_cache_plan(self.struct, self.requests, lengths, want.data_ptr(), table, self.width,
+                                           free_pages, free_count, cu.data_ptr(), slots.data_ptr(), n_slots,
+                                           self._flags, _raw_stream(self._index))
+        if status:
+            raise B.ClefError(status, "clef_cache_plan")
         return slots, cu
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, head0: int = 0):
         """Store key and value rows [tokens, heads, head_dim] (bf16 or fp16, any row and head
         strides) in ``slots``, as cache heads ``head0`` on.  Negative slots skip their row."""
-        dtype = self._rows(k, "k")
-        if self._rows(v, "v") != dtype or v.shape != k.shape:
+        dtype, (n, heads, _), ks = self._rows(k, "k")
+        v_dtype, v_shape, vs = self._rows(v, "v")
+        if v_dtype != dtype or v_shape[0] != n or v_shape[1] != heads:
             _refuse("k and v: one shape and type")
-        if self.checked_slots(slots).numel() != k.shape[0]:
+        if self.checked_slots(slots).numel() != n:
             _refuse("slots: one a row")
-        n, heads, _ = k.shape
-        ks, vs = k.stride(), v.stride()
         if self._elsewhere():
             with torch.cuda.device(self._index):
                 return self.append(k, v, slots, head0)
-        self._check(self._lib.clef_cache_append(self.struct, n, head0, heads, dtype, k.data_ptr(), ks[0], ks[1],
-                                                v.data_ptr(), vs[0], vs[1], slots.data_ptr(), self._flags,
-                                                _raw_stream(self._index)), "clef_cache_append")
+        status = self._lib.clef_cache_append(self.struct, n, head0, heads, dtype, k.data_ptr(), ks[0], ks[1],
+                                             v.data_ptr(), vs[0], vs[1], slots.data_ptr(), self._flags,
+                                             _raw_stream(self._index))
+        if status:
+            raise B.ClefError(status, "clef_cache_append")
 
     def read(self, slots: torch.Tensor, dtype=torch.bfloat16, head0: int = 0,
              heads: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -184,9 +180,10 @@ class MemoryCache:
                 return self.read(slots, dtype, head0, heads)
         k = torch.empty((n, heads, self.head_dim), dtype=dtype, device=self.device)
         v = torch.empty_like(k)
-        self._check(self._lib.clef_cache_read(self.struct, n, head0, heads, _DTYPES[dtype], slots.data_ptr(),
-                                              k.data_ptr(), v.data_ptr(), self._flags, _raw_stream(self._index)),
-                    "clef_cache_read")
+        status = self._lib.clef_cache_read(self.struct, n, head0, heads, _DTYPES[dtype], slots.data_ptr(),
+                                           k.data_ptr(), v.data_ptr(), self._flags, _raw_stream(self._index))
+        if status:
+            raise B.ClefError(status, "clef_cache_read")
         return k, v
 
     def attend(self, q: torch.Tensor, cu_q: torch.Tensor, max_q: int, scale: Optional[float] = None,
@@ -202,16 +199,17 @@ class MemoryCache:
         ``head0`` on evenly (all of the cache's by default).  ``block_table`` and ``lengths``
         default to the cache's own.  A row that sees nothing gives 0 and -inf; rows behind
         the last request are not written (not set at all without ``out``)."""
-        dtype = self._rows(q, "q")
-        kv_heads = self.heads - head0 if kv_heads is None else kv_heads
+        dtype, (total, q_heads, _), strides = self._rows(q, "q")
         n = self.checked_slots(cu_q).numel() - 1
         lengths = self.lengths if lengths is None else self.checked_slots(lengths)
         table = self.checked_table(block_table, n)
+        pages = table.shape[1]
         if n < 1 or lengths.numel() < n:
             _refuse("cu_q, lengths: one entry a request")
-        total, q_heads, _ = q.shape
-        strides = q.stride()
-        scale = self.head_dim ** -0.5 if scale is None else scale
+        if kv_heads is None:
+            kv_heads = self.heads - head0
+        if scale is None:
+            scale = self.head_dim ** -0.5
         if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or
                                 out.device != self.device):
             _refuse("out: contiguous, of q's shape and type")
@@ -222,20 +220,20 @@ class MemoryCache:
             out = torch.empty((total, q_heads, self.head_dim), dtype=q.dtype, device=self.device)
         lse = torch.empty((total, q_heads), dtype=torch.float32, device=self.device)
         # a buffer of the call's own: overlapping calls and captured graphs never share one
-        sizes = (n, total, q_heads, table.shape[1])
-        n_bytes = self._space.get(sizes)
+        n_bytes = self._space.get((n, total, q_heads, pages))
         if n_bytes is None:
             if len(self._space) >= 4096:
                 self._space.clear()
-            n_bytes = B.clef_cache_attend_workspace(self.struct, n, total, max(q_heads, 1), table.shape[1] * self.page)
-            self._space[sizes] = n_bytes
+            n_bytes = B.clef_cache_attend_workspace(self.struct, n, total, max(q_heads, 1), pages * self.page)
+            self._space[n, total, q_heads, pages] = n_bytes
         space = torch.empty(n_bytes, dtype=torch.uint8, device=self.device) if n_bytes else None
-        self._check(self._lib.clef_cache_attend(self.struct, n, total, max_q, q_heads, head0, kv_heads, dtype,
-                                                q.data_ptr(), strides[0], strides[1], cu_q.data_ptr(),
-                                                table.data_ptr(), table.shape[1], lengths.data_ptr(), scale,
-                                                int(causal), out.data_ptr(), lse.data_ptr(), self._flags,
-                                                space.data_ptr() if n_bytes else None, n_bytes,
-                                                _raw_stream(self._index)), "clef_cache_attend")
+        status = self._lib.clef_cache_attend(self.struct, n, total, max_q, q_heads, head0, kv_heads, dtype, q.data_ptr(),
+                                             strides[0], strides[1], cu_q.data_ptr(), table.data_ptr(), pages,
+                                             lengths.data_ptr(), scale, 1 if causal else 0, out.data_ptr(),
+                                             lse.data_ptr(), self._flags, space.data_ptr() if n_bytes else None, n_bytes,
+                                             _raw_stream(self._index))
+        if status:
+            raise B.ClefError(status, "clef_cache_attend")
         return out, lse
 
     def device_status(self) -> int:
