@@ -198,7 +198,8 @@ class MemoryCache:
         each sees the whole memory.  Query heads share the ``kv_heads`` cache heads from
         ``head0`` on evenly (all of the cache's by default).  ``block_table`` and ``lengths``
         default to the cache's own.  A row that sees nothing gives 0 and -inf; rows behind
-        the last request are not written (not set at all without ``out``)."""
+        the last request are not written (not set at all without ``out``, which must lie apart
+        from ``q``)."""
         dtype, (total, q_heads, _), strides = self._rows(q, "q")
         n = self.checked_slots(cu_q).numel() - 1
         lengths = self.lengths if lengths is None else self.checked_slots(lengths)
@@ -211,8 +212,8 @@ class MemoryCache:
         if scale is None:
             scale = self.head_dim ** -0.5
         if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or
-                                out.device != self.device):
-            _refuse("out: contiguous, of q's shape and type")
+                                out.device != self.device or out.data_ptr() == q.data_ptr() and q.numel()):
+            _refuse("out: contiguous, of q's shape and type, apart from q")
         if self._elsewhere():
             with torch.cuda.device(self._index):
                 return self.attend(q, cu_q, max_q, scale, causal, head0, kv_heads, table, lengths, out)

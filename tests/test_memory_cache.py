@@ -173,3 +173,12 @@ def test_python_refusals_without_a_gpu():
         with pytest.raises(B.ClefError):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_output_in_place_of_the_queries_is_refused():
+    """Rows of a request are read by several blocks: the output cannot go over them."""
+    from structured_decision_model_gb300.memory import MemoryCache
+    c = MemoryCache(4, page=16, heads=2, head_dim=64, requests=3, max_len=40, device="cpu")
+    q = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(B.ClefError, match="apart from q"):
+        c.attend(q, torch.zeros(4, dtype=torch.int32), 1, out=q)
