@@ -32,9 +32,9 @@
 // Requests longer than one split leave normalised partials with their log-sum, which the
 // merge kernel weighs.
 //
-// What bounds it: instruction issue, the integer pipe above all (about 130 instructions for 16
-// keys, 56 of them to split codes; 51 % of the issue slots and 57 % of the memory rate in a
-// decoding step of 64 requests of 400 to 16000 keys with 8 heads of 128: 219 MB in 51 us), and
+// What bounds it: instruction issue, the integer pipe above all (about 140 instructions for 16
+// keys of 64 values, 40 of them to split codes; 51 % of the issue slots and 57 % of the memory rate in a
+// decoding step of 64 requests of 156 to 16384 keys with 8 heads of 128: 219 MB in 51 us), and
 // the unequal ends of a call; 256 requests of 4096 keys (1.2 GB) take 213 us, 84 % of the
 // memory's measured copy rate.
 #include <algorithm>

@@ -248,7 +248,7 @@ __device__ __forceinline__ int scan_requests(const CacheAttendArgs& a, const Req
 
 // The item of a CTA's n-th turn: items, largest first, are dealt out in rows that run forward
 // and back, so that the sums of their sizes come out nearly even (a decoding step of 64 requests
-// of 400 to 16000 keys, 8 heads of 128: 55 us, and 64 us dealt in the requests' order).
+// of 156 to 16384 keys, 8 heads of 128: 55 us, and 64 us dealt in the requests' order).
 __device__ __forceinline__ int item_of_turn(int n) {
     return n * int(gridDim.x) + ((n & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
 }

@@ -19,7 +19,7 @@
 // weights of a piece are multiplied by the power of two between them.
 // The softmax reference of a row moves only when a score exceeds it by 2^8.
 //   64 queries x 8 requests x 16384 keys x 16 heads of 64: 183 us with the merge, 188 TFLOP/s.
-// What bounds it: the instructions around the products (about 170 for 16 keys x 16 rows, 16 of
+// What bounds it: the instructions around the products (about 180 for 16 keys x 16 rows, 16 of
 // them matrix instructions) at half of the issue slots; the matrix pipe is 37 % busy, shared
 // memory 55 %.  Tried and slower: 32 rows a warp (265 us, out of registers), key operands
 // expanded in shared memory (188), products of two or four pieces side by side (same), the next
