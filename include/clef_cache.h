@@ -146,7 +146,8 @@ CLEF_API int clef_cache_attend_workspace(const clef_cache* cache, int32_t B, int
  * to it, each with CLEF_ERR_DEVICE_BOUNDS.
  * workspace: clef_cache_attend_workspace bytes, 256-byte aligned (may be NULL when 0);
  * calls that overlap on the GPU need one each, captured graphs included.
- * 1 <= B <= CLEF_CACHE_MAX_REQUESTS; 0 <= max_q <= total_q; scale finite. */
+ * 1 <= B <= CLEF_CACHE_MAX_REQUESTS; 0 <= max_q <= total_q, max_q * q_heads at most 2^31 - 65536 (and
+ * so are the work items and partial rows of a call, else CLEF_ERR_UNSUPPORTED_CONFIG); scale finite. */
 CLEF_API int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32_t max_q, int32_t q_heads,
                                int32_t head0, int32_t kv_heads, int32_t dtype, const void* q, int64_t q_row_stride,
                                int64_t q_head_stride, const int32_t* cu_q, const int32_t* block_table,

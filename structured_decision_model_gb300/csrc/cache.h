@@ -34,12 +34,26 @@ struct CacheRowsArgs {
     const int32_t* slots; int32_t* flags;
 };
 
+// Division of query rows by the query heads that share a key head: r / share = r mul >> shift, exact
+// for every 0 <= r < 2^31.  With 2^(l - 1) < share <= 2^l, mul = ceil(2^(31 + l) / share) is over by
+// less than share / share <= 2^l / share, so r mul / 2^(31 + l) is over by less than 1 / share; mul is
+// below 2^32 and the product below 2^63.
+struct RowDivider {
+    uint32_t mul, shift;
+    __host__ __device__ int operator()(int r) const { return int((uint64_t(uint32_t(r)) * mul) >> shift); }
+};
+inline RowDivider row_divider(int share) {
+    uint32_t l = 0;
+    while ((int64_t(1) << l) < share) ++l;
+    return {uint32_t(((uint64_t(1) << (31 + l)) + share - 1) / share), 31 + l};
+}
+
 struct CacheAttendArgs {
     CacheView c;
     int B, total_q, max_q, q_heads, head0, kv_heads, share, dtype, width, causal;
     const void* q; int64_t q_row, q_head;
     const int32_t* cu_q; const int32_t* table; const int32_t* lengths;
-    uint64_t share_inv;  // ceil(2^40 / share)
+    RowDivider by_share;
     float scale_log2;
     void* out; float* lse; int32_t* flags;
     float* part_o; float* part_lse; int32_t* part_off;  // split partials, their row offset per request

@@ -171,17 +171,17 @@ int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32
         return CLEF_ERR_INVALID_ARGUMENT;
     const int64_t max_len = int64_t(table_stride) * cache->page;
     const AttendSpace sp(B, total_q, q_heads, cache->head_dim, max_len);
-    // items and partial rows are counted in 32 bits on the GPU
+    // items, query rows x heads and partial rows are counted in 32 bits on the GPU, which rounds them up
+    // to blocks of rows and looks a grid of items ahead
     a.chunk = attend_chunk(kv_heads);
     const int64_t chunks = (max_len + a.chunk - 1) / a.chunk;
-    if (sp.rows >= kInt32 || chunks * (int64_t(max_q) * (q_heads / kv_heads) / 8 + 1) * kv_heads * B >= kInt32 ||
-        int64_t(max_q) * q_heads >= kInt32 ||
-        int64_t(max_q) * (q_heads / kv_heads) >= (int64_t(1) << 40) / (q_heads / kv_heads))
+    if (sp.rows >= kInt32 || chunks * (int64_t(max_q) * (q_heads / kv_heads) / 8 + 1) * kv_heads * B > kMaxLength ||
+        int64_t(max_q) * q_heads > kMaxLength)
         return CLEF_ERR_UNSUPPORTED_CONFIG;
     if (sp.bytes > 0 && !workspace) return CLEF_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < size_t(sp.bytes)) return CLEF_ERR_WORKSPACE_TOO_SMALL;
     a.B = B; a.total_q = total_q; a.max_q = max_q; a.q_heads = q_heads; a.head0 = head0; a.kv_heads = kv_heads;
-    a.share = q_heads / kv_heads; a.share_inv = ((uint64_t(1) << 40) + a.share - 1) / a.share;
+    a.share = q_heads / kv_heads; a.by_share = row_divider(a.share);
     a.dtype = dtype; a.width = table_stride; a.causal = causal;
     a.q = q; a.q_row = q_row_stride; a.q_head = q_head_stride;
     a.cu_q = cu_q; a.table = block_table; a.lengths = lengths;

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         for (int n = 0; n < NT; ++n) {
             const int r = C == 2 ? n * 8 + g : g >> 1;
             const bool live = r < k.rows && (C == 2 || !(g & 1));
-            const int qi = live ? by_share(a, k.row0 + r) : 0;
+            const int qi = live ? a.by_share(k.row0 + r) : 0;
             const int qh = k.h * a.share + (live ? k.row0 + r - qi * a.share : 0);
             const uint16_t* q = static_cast<const uint16_t*>(a.q) + (s_req.q0[k.b] + qi) * a.q_row + qh * a.q_head + 2 * tq;
 #pragma unroll
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int c = 0; c < 4; c += 3 - C) {
-                            const int sees = a.causal ? ahead + by_share(a, me.row0 + row_of(n, c & 1)) + 1 : end;
+                            const int sees = a.causal ? ahead + a.by_share(me.row0 + row_of(n, c & 1)) + 1 : end;
                             if (tk + g + 8 * (c >> 1) >= min(sees, end)) p[k][n][c] = -INFINITY;
                         }
 #pragma unroll
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) wgt[i] *= inv;
             if (r < me.rows) {
-                const int qi = by_share(a, me.row0 + r), qh = me.h * a.share + me.row0 + r - qi * a.share;
+                const int qi = a.by_share(me.row0 + r), qh = me.h * a.share + me.row0 + r - qi * a.share;
                 row = whole ? int64_t(s_req.q0[me.b] + qi) * a.q_heads + qh
                             : (me.b ? s_req.parts[me.b - 1] : 0) + (int64_t(me.split) * s_req.nq[me.b] + qi) * a.q_heads + qh;
                 // (query rows of requests that overlap, which cu_q must not have, could make

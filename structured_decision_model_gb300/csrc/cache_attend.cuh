@@ -65,11 +65,6 @@ struct Requests {
           last(base + 6 * n) {}
 };
 
-// r / share for query rows: share_inv = ceil(2^40 / share), exact while r * share < 2^40.
-__device__ __forceinline__ int by_share(const CacheAttendArgs& a, int r) {
-    return int((uint64_t(uint32_t(r)) * a.share_inv) >> 40);
-}
-
 struct Request {
     int len, q0, nq, chunks;
 };
@@ -293,7 +288,7 @@ __device__ __forceinline__ Item item_of(const CacheAttendArgs& a, const Requests
     k.t0 = k.split * a.chunk;
     k.t1 = min(k.t0 + a.chunk, len);
     k.ahead = len - nq;  // causal: query i sees keys 0 .. ahead + i
-    if (a.causal) k.t1 = min(k.t1, k.ahead + by_share(a, k.row0 + k.rows - 1) + 1);
+    if (a.causal) k.t1 = min(k.t1, k.ahead + a.by_share(k.row0 + k.rows - 1) + 1);
     k.p0 = k.t0 >> a.c.page_shift;
     return k;
 }

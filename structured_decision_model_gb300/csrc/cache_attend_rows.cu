@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const bool live = r0 + 8 * r < me.rows;
-            const int row = live ? me.row0 + r0 + 8 * r : 0, qi = by_share(a, row), qh = me.h * a.share + row - qi * a.share;
+            const int row = live ? me.row0 + r0 + 8 * r : 0, qi = a.by_share(row), qh = me.h * a.share + row - qi * a.share;
             const uint16_t* q = static_cast<const uint16_t*>(a.q) + (s_req.q0[me.b] + qi) * a.q_row + qh * a.q_head + 2 * tq;
             top[r] = 0.f;
 #pragma unroll
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 }
             }
         };
-        const int see0 = ahead + by_share(a, me.row0 + r0) + 1, see1 = ahead + by_share(a, me.row0 + r0 + 8) + 1;
-        const int full = a.causal ? ahead + by_share(a, me.row0) + 1 : t1;  // keys that every row sees
+        const int see0 = ahead + a.by_share(me.row0 + r0) + 1, see1 = ahead + a.by_share(me.row0 + r0 + 8) + 1;
+        const int full = a.causal ? ahead + a.by_share(me.row0) + 1 : t1;  // keys that every row sees
 
         // The step at t, expanded in buffer `buf`, meets the warp's rows.
         auto multiply = [&](int t, int buf) {
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 for (int o = 1; o < 4; o <<= 1) none[r][gr] += __shfl_xor_sync(0xffffffffu, none[r][gr], o);
             const int rr = r0 + 8 * r;
             if (rr >= me.rows) continue;
-            const int qi = by_share(a, me.row0 + rr), qh = me.h * a.share + me.row0 + rr - qi * a.share;
+            const int qi = a.by_share(me.row0 + rr), qh = me.h * a.share + me.row0 + rr - qi * a.share;
             const int64_t row = whole ? int64_t(s_req.q0[me.b] + qi) * a.q_heads + qh
                                       : (me.b ? s_req.parts[me.b - 1] : 0) +
                                             (int64_t(me.split) * s_req.nq[me.b] + qi) * a.q_heads + qh;

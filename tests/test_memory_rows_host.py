@@ -1,0 +1,55 @@
+"""Index arithmetic of the 4-bit cache's attention, on the host (no GPU)."""
+import os
+import subprocess
+
+from structured_decision_model_gb300 import binding as B
+from structured_decision_model_gb300 import build
+from test_memory_cache import P, cache, changed, lib, refused  # noqa: F401
+
+DIVIDE = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "cache.h"
+
+int main() {
+    const int64_t top = (int64_t(1) << 31) - 1;
+    long bad = 0, n = 0;
+    auto check = [&](const clef::RowDivider& d, int share, int64_t r) {
+        if (r < 0 || r > top) return;
+        ++n;
+        bad += d(int(r)) != int(r / share);
+    };
+    for (int64_t base : {int64_t(1), int64_t(1) << 10, int64_t(1) << 20, int64_t(1) << 24, int64_t(1) << 30, top - 300})
+        for (int64_t share = base; share < base + 300 && share <= top; ++share) {
+            const clef::RowDivider d = clef::row_divider(int(share));
+            for (int64_t r = 0; r < 40; ++r) {
+                check(d, int(share), r);
+                check(d, int(share), top - r);
+                check(d, int(share), (int64_t(1) << 24) + r - 20);
+                check(d, int(share), (share << 24) + r - 20);
+            }
+            for (int64_t q = 1; q <= top / share; q = q * 3 / 2 + 1)  // both sides of a multiple
+                for (int64_t e = -1; e <= 1; ++e) check(d, int(share), q * share + e);
+        }
+    std::printf("%ld of %ld\n", bad, n);
+    return bad != 0;
+}
+"""
+
+
+def test_rows_are_divided_exactly(tmp_path):
+    """r / share for every r that the call admits: both sides of multiples, of 2^24 and of 2^31."""
+    src, exe = tmp_path / "divide.cpp", tmp_path / "divide"
+    src.write_text(DIVIDE)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build._nvcc())) or "/usr/local/cuda", "include")
+    subprocess.run(["g++", "-std=c++17", "-O1", f"-I{build.CSRC}", f"-I{cuda}", str(src), "-o", str(exe)], check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout
+
+
+def test_more_rows_than_32_bits_hold_are_refused():
+    c = cache()
+    good = [c, 2, 1 << 24, 1 << 24, 127, 0, 1, B.BF16, P, 127 * 64, 64, P, P, 4, P, 0.125, 1, P, P, P, 0, 0]
+    refused(1, B.clef_cache_attend, *changed(good, 18, P + 2))              # the size is fine
+    refused(3, B.clef_cache_attend, *changed(good, 4, 128))                 # 2^31 rows
+    refused(3, B.clef_cache_attend, *changed(changed(changed(good, 4, 1), 2, (1 << 31) - 65535), 3, (1 << 31) - 65535))
