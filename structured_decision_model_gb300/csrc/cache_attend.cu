@@ -19,8 +19,8 @@
 // Queries are scaled by a power of two per row to fill fp16's range (exact).
 //   Values: with w_t = p_t s_t,
 //   o = sum_t p_t (s_t c_t + m_t) = sum_t w_t c_t - sum_t 8 w_t + sum_t p_t (m_t + 8 s_t).
-// The weights w_t 2^E are rounded to fp16 (11 bits; E puts the largest s_t 2^E met so far in
-// [4, 8), so that the weights stay under 2^11), once for the first two sums, which are products
+// The weights w_t are rounded to fp16 (11 bits; after a power of two of the row's own, see
+// move_weights in cache_attend.cuh), once for the first two sums, which are products
 // of the matrix unit with the codes and with eights: their difference is that of centred codes
 // |c - 8| <= 8, and what the rounding costs is relative to it, not to the whole range of the
 // codes.  The third sum is fp32.  (Centring the codes themselves takes 16 more instructions a
@@ -228,8 +228,12 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) acc[gr][mt][n][c] = 0.f;
-        float vmul = pow2i(120);  // value scales are multiplied by a power of two, to at most 8
-        bool first = true;        // no step yet: the references are still to be set
+        float mul[G][NT][2];  // the weights' powers of two
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mul[gr][n][0] = mul[gr][n][1] = 1.f;
+        bool first = true;  // no step yet: the references are still to be set
 
         // the next item's page numbers come in with the pieces of this one
         const int w_next = item_of_turn(turn + 1);
@@ -338,17 +342,6 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                                 }
                 }
             }
-            float vw[KP][G][2];  // the value scales as weights take them
-#pragma unroll
-            for (int k = 0; k < KP; ++k)
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        vm[k][gr][r] = fmaf(8.f, vs[k][gr][r], vm[k][gr][r]);
-                        vw[k][gr][r] = vs[k][gr][r] * vmul;
-                        top = fmaxf(top, vw[k][gr][r]);
-                    }
 #pragma unroll
             for (int k = 0; k < KP; ++k)
 #pragma unroll
@@ -361,24 +354,6 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     }
                 }
             if (__any_sync(0xffffffffu, first || top > 8.f)) {  // new references: the first step, and rarely after
-                float vtop = 0.f;
-#pragma unroll
-                for (int k = 0; k < KP; ++k)
-#pragma unroll
-                    for (int gr = 0; gr < G; ++gr) vtop = fmax3(vtop, vs[k][gr][0], vs[k][gr][1]);
-                vtop = warp_max(vtop);
-                float vcorr = 1.f;
-                if (vtop * vmul > 8.f) {  // the largest scale goes to [4, 8)
-                    const float to = pow2i(2 - (int(__float_as_uint(vtop) >> 23) - 127));
-                    vcorr = to / vmul;
-                    vmul = to;
-#pragma unroll
-                    for (int k = 0; k < KP; ++k)
-#pragma unroll
-                        for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) vw[k][gr][r] = vs[k][gr][r] * vmul;
-                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -388,67 +363,131 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                         for (int k = 0; k < KP; ++k) mx = fmax3(mx, p[k][n][c], p[k][n][c + 2]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        float corr = 1.f;
-                        if (first ? mx > -INFINITY : mx > 8.f) {
-                            corr = first ? 0.f : ex2_approx(-mx);
+                        const bool moved = first ? mx > -INFINITY : mx > 8.f;
+                        Decay d;
+                        if (moved) {
+                            if (!first) d.set(mx);
                             ref[n][c] += mx;
+                            l[n][c] *= d.corr;
 #pragma unroll
                             for (int k = 0; k < KP; ++k) {
                                 p[k][n][c] -= mx;
                                 p[k][n][c + 2] -= mx;
                             }
                         }
-                        l[n][c] *= corr;
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
-                            z[gr][n][c] *= corr;
-                            mid[gr][n][c] *= corr * vcorr;
-                            mid[gr][n][c + 2] *= corr * vcorr;
+                            float x = 0.f, big = 0.f;
 #pragma unroll
-                            for (int mt = 0; mt < 4; ++mt) {
-                                acc[gr][mt][n][c] *= corr * vcorr;
-                                acc[gr][mt][n][c + 2] *= corr * vcorr;
+                            for (int k = 0; k < KP; ++k)
+                                x = fmax3(x, ex2_approx(p[k][n][c]) * vs[k][gr][0], ex2_approx(p[k][n][c + 2]) * vs[k][gr][1]);
+#pragma unroll
+                            for (int mt = 0; mt < 4; ++mt)
+                                big = fmax3(big, fabsf(acc[gr][mt][n][c]), fabsf(acc[gr][mt][n][c + 2]));
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) {
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            }
+                            if (moved) {
+                                const float f = move_weights(mul[gr][n][c], x, big, d);
+                                z[gr][n][c] *= d.corr;
+                                mid[gr][n][c] *= f;
+                                mid[gr][n][c + 2] *= f;
+#pragma unroll
+                                for (int mt = 0; mt < 4; ++mt) {
+                                    acc[gr][mt][n][c] *= f;
+                                    acc[gr][mt][n][c + 2] *= f;
+                                }
                             }
                         }
                     }
                 first = false;
             }
-            // ---- weights and value products
+            // ---- weights
+            uint32_t pf[KP][G][NT][2];
+            float most = 0.f;
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
+            for (int k = 0; k < KP; ++k)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int c = 0; c < 4; c += 3 - C) {
                         p[k][n][c] = ex2_approx(p[k][n][c]);
                         l[n][c & 1] += p[k][n][c];
                     }
 #pragma unroll
+                    for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float mid_value = fmaf(8.f, vs[k][gr][r], vm[k][gr][r]);
+                            float w[2] = {0.f, 0.f};
+#pragma unroll
+                            for (int c = 0; c < C; ++c) {
+                                w[c] = p[k][n][2 * r + c] * mul[gr][n][c] * vs[k][gr][r];
+                                z[gr][n][c] = fmaf(p[k][n][2 * r + c], mid_value, z[gr][n][c]);
+                            }
+                            most = C == 2 ? fmax3(most, w[0], w[1]) : fmaxf(most, w[0]);
+                            pf[k][gr][n][r] = pack_f16(w[0], w[1]);
+                        }
+                }
+            if (__any_sync(0xffffffffu, most > kMostWeight)) {  // larger values than the rows have used before
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            float x = 0.f;
+#pragma unroll
+                            for (int k = 0; k < KP; ++k)
+                                x = fmax3(x, p[k][n][c] * vs[k][gr][0], p[k][n][c + 2] * vs[k][gr][1]);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                            if (x * mul[gr][n][c] > kMostWeight) {
+                                const float f = move_weights(mul[gr][n][c], x, 0.f, Decay());
+                                mid[gr][n][c] *= f;
+                                mid[gr][n][c + 2] *= f;
+#pragma unroll
+                                for (int mt = 0; mt < 4; ++mt) {
+                                    acc[gr][mt][n][c] *= f;
+                                    acc[gr][mt][n][c + 2] *= f;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < KP; ++k)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                float w[2] = {0.f, 0.f};
+#pragma unroll
+                                for (int c = 0; c < C; ++c) w[c] = p[k][n][2 * r + c] * mul[gr][n][c] * vs[k][gr][r];
+                                pf[k][gr][n][r] = pack_f16(w[0], w[1]);
+                            }
+                    }
+            }
+            // ---- value products
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+#pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     const uint4 codes = reinterpret_cast<const uint4*>(pieces + k * kBytes + (G + gr) * 512)[lane];
-                    uint32_t pf[NT][2];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float w0 = p[k][n][2 * r], w1 = C == 2 ? p[k][n][2 * r + 1] : 0.f;
-                            pf[n][r] = transpose8(pack_f16(w0 * vw[k][gr][r], C == 2 ? w1 * vw[k][gr][r] : 0.f));
-                            z[gr][n][0] = fmaf(w0, vm[k][gr][r], z[gr][n][0]);
-                            if (C == 2) z[gr][n][1] = fmaf(w1, vm[k][gr][r], z[gr][n][1]);
-                        }
+                        for (int r = 0; r < 2; ++r) pf[k][gr][n][r] = transpose8(pf[k][gr][n][r]);
                     const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt) {
                         const uint32_t x = words[mt], y = x >> 8;
                         const uint32_t A[4] = {x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u};
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16_16816(acc[gr][mt][n], A, pf[n][0], pf[n][1]);
+                        for (int n = 0; n < NT; ++n) mma_f16_16816(acc[gr][mt][n], A, pf[k][gr][n][0], pf[k][gr][n][1]);
                     }
                     constexpr uint32_t kEights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16_16816(mid[gr][n], kEights, pf[n][0], pf[n][1]);
+                    for (int n = 0; n < NT; ++n) mma_f16_16816(mid[gr][n], kEights, pf[k][gr][n][0], pf[k][gr][n][1]);
                 }
-            }
         }
         cp_async_commit();  // page numbers, where the warp had no step
         cp_async_wait<0>();
@@ -456,7 +495,6 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
         // ---- the warps' results side by side in shared memory, then weighed: normalised, with
         // the logarithm (base 2) of the sum
         __syncthreads();  // the results of the item before this one are no longer read
-        const float vback = 0x1p24f / vmul;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -484,8 +522,9 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                         for (int half = 0; half < 2; ++half)
                             // (codes of the upper half of a run count 2^4)
                             dst[gr * 64 + mt * 16 + half * 8 + g] =
-                                fmaf(fmaf(acc[gr][mt][n][c + 2 * half], half ? 0.0625f : 1.f, -mid[gr][n][c + 2 * half]),
-                                     vback, zs[gr]);
+                                fmaf(0x1p24f * fmaf(acc[gr][mt][n][c + 2 * half], half ? 0.0625f : 1.f,
+                                                    -mid[gr][n][c + 2 * half]),
+                                     1.f / mul[gr][n][c], zs[gr]);
             }
         __syncthreads();  // the results and the next item's page numbers are there
         if (more) {

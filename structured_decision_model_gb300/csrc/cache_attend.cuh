@@ -47,6 +47,40 @@ __device__ __forceinline__ float pow2i(int e) {
     return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23);
 }
 
+// A row's softmax weights meet the matrix unit in fp16, multiplied by the size of the token's values
+// (its scale, or the power of two below its largest value) and by a power of two `mul` of the row's own.  It
+// moves when the row's reference does, to put the largest product of the step in [4, 8), and down when a
+// product exceeds kMostWeight.  Between two moves the products only add, so the largest weight
+// that a row has used is 4 at least and the floor of fp16's subnormals 2^-27 of it: a row is as exact as the
+// tokens that it gives weight to, whatever others, or tokens that it does not see, hold.
+constexpr float kMostWeight = 16384.f;
+
+__device__ __forceinline__ int exponent_of(float x) { return int(__float_as_uint(x) >> 23) - 127; }  // of x >= 0
+
+// The softmax weights of a row are multiplied by 2^-mx (mx > 0): frac 2^-k, with frac in [0.7, 1.5).
+struct Decay {
+    float frac = 1.f, corr = 1.f;  // corr: the whole factor, 0 where it is below 2^-126
+    int k = 0;
+    __device__ void set(float mx) {
+        const float kf = rintf(fminf(mx, 300.f));
+        frac = ex2_approx(kf - mx);
+        k = int(kf);
+        corr = k > 126 ? 0.f : frac * pow2i(-k);
+    }
+};
+
+// Moves a row's `mul` for products p * size of at most x, and returns the factor of its sums, whose
+// largest is `big` (they stay under 2^102, and give way to no smaller products beyond that).
+__device__ __forceinline__ float move_weights(float& mul, float x, float big, const Decay& d) {
+    const int old = exponent_of(mul);
+    int to = x > 0.f ? 2 - exponent_of(fminf(x, 0x1.fffffep127f)) : old;
+    if (big > 0.f) to = min(to, old + d.k + 100 - exponent_of(big));
+    to = min(max(to, -126), 119);  // (p mul stays finite)
+    mul = pow2i(to);
+    const int by = to - old - d.k;
+    return by < -126 ? 0.f : d.frac * pow2i(by);
+}
+
 // The two elements of a 32-bit word as fp32.
 __device__ __forceinline__ float2 unpack2(uint32_t w, int dtype) {
     if (dtype == 0) return make_float2(bf16_lo(w), bf16_hi(w));

@@ -12,11 +12,12 @@
 // are expanded while the step before is multiplied, one barrier a step.
 //   Keys stay exact: codes as fp16 subnormals, and scores s_t (q . c_t) + m_t (sum q) in fp32,
 // where s_t comes with the scale of the softmax and of the queries' power of two on it.
-//   Values are rounded to fp16 once, (c - 8) s' + m' with s' = s 2^E and m' = (m + 8 s) 2^E:
-// half a step of 11 bits, as the weights (which then need no value scale, and sum to the
-// softmax's denominator themselves).  E is a multiple of 8 for each piece that puts its largest
-// value between 1 and 2^8, so neighbouring pieces hardly ever differ; where they do, the
-// weights of a piece are multiplied by the power of two between them.
+//   Values are rounded to fp16, (c - 8) s' + m' with s' = s 2^-e and m' = (m + 8 s) 2^-e, where 2^e
+// is the size of the token's group: its largest magnitude comes to [1, 2).  The middle m' and
+// the value are rounded by half a step of 11 bits each.  The size goes to the weights, p_t 2^e_t,
+// which are rounded to 11 bits too, after the row's power of two (move_weights in
+// cache_attend.cuh); the denominator sums p_t in fp32.  A token's values and a row's weights
+// are thus scaled by themselves, whatever their neighbours hold.
 // The softmax reference of a row moves only when a score exceeds it by 2^8.
 //   64 queries x 8 requests x 16384 keys x 16 heads of 64: 183 us with the merge, 188 TFLOP/s.
 // What bounds it: the instructions around the products (about 180 for 16 keys x 16 rows, 16 of
@@ -36,20 +37,22 @@ namespace {
 constexpr int kRowsItem = 16 * kAttendWarps;  // query rows of an item
 constexpr int kRowsStep = 16 * kAttendWarps;  // keys of a step
 
-// Of an expanded piece: its exponent E, the tokens whose values are no numbers (a bit each, by
-// group of 64 values), and whether it is there at all.
+// Of an expanded piece: the tokens whose values are no numbers (a bit each, by group of 64
+// values), and whether it is there at all.
 struct PieceInfo {
-    int exponent, bad0, bad1, absent;
+    int bad0, bad1, absent;
 };
 
 template <int G>
 struct RowsSmem {
     static constexpr int kStages = 3;                               // raw pieces a warp
     static constexpr int kRaw = kAttendWarps * kStages * kPiece * G;
-    // an expanded piece: key codes, values in fp16, scale and minimum of its keys in fp32
+    // an expanded piece: key codes, values in fp16, scale and minimum of its keys and the sizes of its
+    // values in fp32
     static constexpr int kValuesAt = 512 * G;
     static constexpr int kScalesAt = kValuesAt + 2048 * G;
-    static constexpr int kExpanded = kScalesAt + 16 * 8 * G;
+    static constexpr int kSizesAt = kScalesAt + 16 * 8 * G;
+    static constexpr int kExpanded = kSizesAt + 16 * 4 * G;
     static constexpr int kBytes = kRaw + 2 * kAttendWarps * kExpanded;
 };
 
@@ -77,7 +80,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
     uint8_t* expanded = smem + Smem::kRaw;  // [buffer][piece]{keys, values, scales}
     const Requests s_req(reinterpret_cast<int*>(smem + Smem::kBytes), a.B);
     __shared__ const uint8_t* s_page[kMaxPages];
-    __shared__ __align__(16) PieceInfo s_info[2][kAttendWarps];
+    __shared__ PieceInfo s_info[2][kAttendWarps];
     __shared__ int s_exp[kAttendWarps];
     __shared__ Item s_item;
     const int n_items = scan_requests<G, true>(a, s_req, kRowsItem);
@@ -179,7 +182,9 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 #pragma unroll
             for (int n = 0; n < 8; ++n) acc[gr][n][0] = acc[gr][n][1] = acc[gr][n][2] = acc[gr][n][3] = 0.f;
         }
-        int scale_exp = 120;  // acc holds values times 2^scale_exp
+        float mul[2][G];  // the weights' powers of two
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) mul[0][gr] = mul[1][gr] = 1.f;
         bool first = true;
 
         auto page_at = [&](int t) { return t < t1 ? s_page[(t >> a.c.page_shift) - me.p0] : nullptr; };
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
             // scales: lane i looks after key i (lane i + 16 too)
             const int key = lane & 15;
             const bool real = there && tk + key < t1;
-            float vs[G], vm[G], most = 0.f;
+            float vs[G], vm[G], up[G];
             uint32_t bad[2] = {0u, 0u};
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
@@ -217,14 +222,14 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 const bool odd = !(fabsf(vs[gr]) < INFINITY && fabsf(vm[gr]) < INFINITY);
                 bad[gr] = __ballot_sync(0xffffffffu, odd) & 0xffffu;
                 if (odd) vs[gr] = vm[gr] = 0.f;
-                most = fmax3(most, fabsf(vm[gr]), fabsf(fmaf(15.f, vs[gr], vm[gr])));
+                // 2^e, the size of the token's values: its largest is put in [1, 2)
+                const int e = min(max(exponent_of(fmaxf(fabsf(vm[gr]), fabsf(fmaf(15.f, vs[gr], vm[gr])))), -126), 119);
+                up[gr] = pow2i(-e);
+                if (lane < 16)
+                    *reinterpret_cast<float*>(dst + Smem::kSizesAt + (gr * 16 + key) * 4) =
+                        vs[gr] == 0.f && vm[gr] == 0.f ? 0.f : pow2i(e);
             }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const int field = min(int(__float_as_uint(most) >> 23) - 127, 127);
-            const int ex = most > 0.f ? max(min(((7 - field) >> 3) * 8, 120), -120) : 120;
-            const float up = pow2i(ex);
-            if (lane == 0) s_info[buf][warp] = PieceInfo{ex, int(bad[0]), int(bad[1]), there ? 0 : 1};
+            if (lane == 0) s_info[buf][warp] = PieceInfo{int(bad[0]), int(bad[1]), there ? 0 : 1};
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 const uint4 kw = reinterpret_cast<const uint4*>(src + gr * 512)[lane];
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 const uint32_t vws[4] = {vw.x, vw.y, vw.z, vw.w};
                 // value scale and middle of the lane's key, then those of keys 2 tq, 2 tq + 1 (low,
                 // high half) and of both + 8
-                const uint32_t own = pack_f16(vs[gr] * up, fmaf(8.f, vs[gr], vm[gr]) * up);
+                const uint32_t own = pack_f16(vs[gr] * up[gr], fmaf(8.f, vs[gr], vm[gr]) * up[gr]);
                 uint32_t s2[2], m2[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -261,23 +266,16 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
             const uint8_t* base = expanded + buf * kAttendWarps * Smem::kExpanded;
             float p[kAttendWarps][2][4];  // piece, keys 0-7 / 8-15: (row g: key 2 tq, + 1; row g + 8: the same)
             bool odd = t + kRowsStep > t1 || t + kRowsStep > full;
-            int ex = scale_exp;
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) {
                 const PieceInfo info = s_info[buf][i];
-                ex = min(ex, info.exponent);
                 odd |= (info.bad0 | info.bad1 | info.absent) != 0;
             }
-            if (ex < scale_exp) {  // larger values than any before
-                const float f = pow2i(ex - scale_exp);
-                scale_exp = ex;
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-                    for (int n = 0; n < 8; ++n)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[gr][n][c] *= f;
-            }
+            // sizes of the values of keys 2 tq and 2 tq + 1 (n = 1: + 8) of piece i
+            auto sizes_of = [&](int i, int gr, int n) {
+                return *reinterpret_cast<const float2*>(base + i * Smem::kExpanded + Smem::kSizesAt +
+                                                        (gr * 16 + n * 8 + 2 * tq) * 4);
+            };
             float most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) {
@@ -361,17 +359,12 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 #pragma unroll
                     for (int o = 1; o < 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     // mx is relative to the reference (0 in the first step, whatever is seen)
-                    if (first ? mx > -INFINITY : mx > 8.f) {
-                        const float corr = first ? 0.f : ex2_approx(-mx);
+                    const bool moved = first ? mx > -INFINITY : mx > 8.f;
+                    Decay d;
+                    if (moved) {
+                        if (!first) d.set(mx);
                         ref[r] += mx;
-                        l[r] *= corr;
-#pragma unroll
-                        for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-                            for (int n = 0; n < 8; ++n) {
-                                acc[gr][n][2 * r] *= corr;
-                                acc[gr][n][2 * r + 1] *= corr;
-                            }
+                        l[r] *= d.corr;
 #pragma unroll
                         for (int i = 0; i < kAttendWarps; ++i)
 #pragma unroll
@@ -380,42 +373,90 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                                 p[i][n][2 * r + 1] -= mx;
                             }
                     }
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        float x = 0.f, big = 0.f;
+#pragma unroll
+                        for (int i = 0; i < kAttendWarps; ++i)
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                const float2 f = sizes_of(i, gr, n);
+                                x = fmax3(x, ex2_approx(p[i][n][2 * r]) * f.x, ex2_approx(p[i][n][2 * r + 1]) * f.y);
+                            }
+#pragma unroll
+                        for (int n = 0; n < 8; ++n)
+                            big = fmax3(big, fabsf(acc[gr][n][2 * r]), fabsf(acc[gr][n][2 * r + 1]));
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) {
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        }
+                        if (moved) {
+                            const float f = move_weights(mul[r][gr], x, big, d);
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                acc[gr][n][2 * r] *= f;
+                                acc[gr][n][2 * r + 1] *= f;
+                            }
+                        }
+                    }
                 }
                 first = false;
             }
 #pragma unroll
-            for (int i = 0; i < kAttendWarps; ++i) {
-                const uint8_t* piece = base + i * Smem::kExpanded;
-                uint32_t pa[4];
+            for (int i = 0; i < kAttendWarps; ++i)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         p[i][n][c] = ex2_approx(p[i][n][c]);
                         l[c >> 1] += p[i][n][c];
                     }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                float w[kAttendWarps][2][4], x[2] = {0.f, 0.f};  // weights, still without the row's factor
+#pragma unroll
+                for (int i = 0; i < kAttendWarps; ++i)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float2 f = sizes_of(i, gr, n);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[i][n][c] = p[i][n][c] * ((c & 1) ? f.y : f.x);
+                        x[0] = fmax3(x[0], w[i][n][0], w[i][n][1]);
+                        x[1] = fmax3(x[1], w[i][n][2], w[i][n][3]);
+                    }
+                // larger values than the rows have used before
+                if (__any_sync(0xffffffffu, fmaxf(x[0] * mul[0][gr], x[1] * mul[1][gr]) > kMostWeight)) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) x[r] = fmaxf(x[r], __shfl_xor_sync(0xffffffffu, x[r], o));
+                        if (x[r] * mul[r][gr] > kMostWeight) {
+                            const float f = move_weights(mul[r][gr], x[r], 0.f, Decay());
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                acc[gr][n][2 * r] *= f;
+                                acc[gr][n][2 * r + 1] *= f;
+                            }
+                        }
+                    }
                 }
-                const int apart_by = s_info[buf][i].exponent - scale_exp;  // >= 0
-                if (apart_by) {
-                    const float f = pow2i(-apart_by);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                for (int i = 0; i < kAttendWarps; ++i) {
+                    uint32_t pa[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) p[i][n][c] *= f;
-                }
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    pa[2 * n] = pack_f16(p[i][n][0], p[i][n][1]);
-                    pa[2 * n + 1] = pack_f16(p[i][n][2], p[i][n][3]);
-                }
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr)
+                    for (int n = 0; n < 2; ++n) {
+                        pa[2 * n] = pack_f16(w[i][n][0] * mul[0][gr], w[i][n][1] * mul[0][gr]);
+                        pa[2 * n + 1] = pack_f16(w[i][n][2] * mul[1][gr], w[i][n][3] * mul[1][gr]);
+                    }
+                    const uint8_t* values = base + i * Smem::kExpanded + Smem::kValuesAt + gr * 2048;
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt) {
-                        const uint4 f = reinterpret_cast<const uint4*>(piece + Smem::kValuesAt + gr * 2048)[mt * 32 + lane];
+                        const uint4 f = reinterpret_cast<const uint4*>(values)[mt * 32 + lane];
                         mma_f16_16816(acc[gr][2 * mt], pa, f.x, f.y);
                         mma_f16_16816(acc[gr][2 * mt + 1], pa, f.z, f.w);
                     }
+                }
             }
         };
 
@@ -443,7 +484,6 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 
         // ---- the warp's rows: normalised, with the logarithm (base 2) of the sum
         const bool whole = s_req.len[me.b] <= a.chunk;
-        const float back = pow2i(-scale_exp);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float sum = l[r];
@@ -465,7 +505,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 if (tq == 0) atomicOr(a.flags, kFlagBounds);
                 continue;
             }
-            const float inv = sum == 0.f ? 0.f : back / sum;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             if (tq == 0) {
                 const float lse2 = sum == 0.f ? -INFINITY : ref[r] + log2f(sum);
                 if (!whole)
@@ -474,10 +514,12 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                     a.lse[row] = lse2 * 0.6931471805599453f;
             }
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr)
+            for (int gr = 0; gr < G; ++gr) {
+                const float back = 1.f / mul[r][gr];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                    const float x = fmaf(acc[gr][n][2 * r], inv, none[r][gr]), y = fmaf(acc[gr][n][2 * r + 1], inv, none[r][gr]);
+                    const float x = fmaf(acc[gr][n][2 * r] * back, inv, none[r][gr]);
+                    const float y = fmaf(acc[gr][n][2 * r + 1] * back, inv, none[r][gr]);
                     const int64_t at = row * (64 * G) + gr * 64 + n * 8 + 2 * tq;
                     if (!whole)
                         *reinterpret_cast<float2*>(a.part_o + at) = make_float2(x, y);
@@ -485,6 +527,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
                             a.dtype == 0 ? pack_bf16(x, y) : pack_f16(x, y);
                 }
+            }
         }
     }
 }
