@@ -593,78 +593,101 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
     }
 }
 
-// Weighs the splits of one (query row, head): W warps, which share out the splits eight at a
-// time (all loads of eight splits are under way at once) and meet in shared memory; two values
-// of each group a lane.
-template <int G, int W>
+// Some splits of a row, weighed: the largest log-sum, the sum of weights and values relative to it.
+template <int G>
+struct Weighed {
+    float top, sum, o[2 * G];
+    __device__ void clear() {
+        top = -1e30f;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) o[i] = 0.f;
+    }
+};
+
+// Splits k0 .. k0 + 7 of the n of a row (all their loads under way at once), added to `x`.
+template <int G>
+__device__ __forceinline__ void weigh_eight(const CacheAttendArgs& a, int64_t p0, int64_t stride, int k0, int n, Weighed<G>& x) {
+    const int lane = threadIdx.x & 31;
+    n = min(8, n - k0);
+    const float y = lane < n ? a.part_lse[p0 + (k0 + lane) * stride] : -INFINITY;
+    float2 v[8][G];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            v[j][i] = j < n ? *reinterpret_cast<const float2*>(a.part_o + (p0 + (k0 + j) * stride) * (64 * G) + i * 64 + lane * 2)
+                            : make_float2(0.f, 0.f);
+    const float mx = fmaxf(x.top, warp_max(y));
+    const float corr = ex2_approx(x.top - mx), w = ex2_approx(y - mx);
+    x.sum = fmaf(x.sum, corr, warp_sum(w));
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) x.o[i] *= corr;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            x.o[2 * i] = fmaf(v[j][i].x, wj, x.o[2 * i]);
+            x.o[2 * i + 1] = fmaf(v[j][i].y, wj, x.o[2 * i + 1]);
+        }
+    }
+    x.top = mx;
+}
+
+// `x` added to `all`, whose top is the largest of all that are added.
+template <int G>
+__device__ __forceinline__ void add_weighed(Weighed<G>& all, const Weighed<G>& x) {
+    const float w = ex2_approx(x.top - all.top);
+    all.sum = fmaf(x.sum, w, all.sum);
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) all.o[i] = fmaf(x.o[i], w, all.o[i]);
+}
+
+// Weighs the splits of one (query row, head), two values of each group a lane.  The splits form
+// eight parts, eight splits in turn each (0-7 and 64-71 are the first part's), and the parts are
+// added in their order: the same sums in both forms, whatever the other requests' lengths are.  WIDE:
+// a CTA's eight warps take a part each and meet in shared memory; otherwise (16 splits at most, so two
+// parts) each warp has a row of its own.
+template <int G, bool WIDE>
 __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs a) {
     griddep_wait();
     griddep_launch();
-    __shared__ float s_top[8], s_sum[8], s_o[8][64 * G];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
+    __shared__ Weighed<G> s_part[8][WIDE ? 32 : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.y;
-    const int64_t item = int64_t(blockIdx.x) * (8 / W) + warp / W;
+    const int64_t item = WIDE ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + warp;
     const Request r = request_of(a, b, false);
     const int64_t p0 = a.part_off[b] + item, stride = int64_t(r.nq) * a.q_heads;
     // a row of a request of one split is finished; one outside the workspace has been reported
     const bool live = r.chunks > 1 && item < stride && p0 >= 0 && p0 + (r.chunks - 1) * stride < a.part_rows;
-    float top = -1e30f, sum = 0.f, o[2 * G] = {};
-    if (live)
-        for (int k0 = part * 8; k0 < r.chunks; k0 += 8 * W) {
-            const int n = min(8, r.chunks - k0);
-            const float x = lane < n ? a.part_lse[p0 + (k0 + lane) * stride] : -INFINITY;
-            float2 v[8][G];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int i = 0; i < G; ++i)
-                    v[j][i] = j < n ? *reinterpret_cast<const float2*>(a.part_o + (p0 + (k0 + j) * stride) * (64 * G) +
-                                                                       i * 64 + lane * 2)
-                                    : make_float2(0.f, 0.f);
-            const float mx = fmaxf(top, warp_max(x));
-            const float corr = ex2_approx(top - mx), w = ex2_approx(x - mx);
-            sum = sum * corr + warp_sum(w);
-#pragma unroll
-            for (int i = 0; i < 2 * G; ++i) o[i] *= corr;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, w, j);
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    o[2 * i] = fmaf(v[j][i].x, wj, o[2 * i]);
-                    o[2 * i + 1] = fmaf(v[j][i].y, wj, o[2 * i + 1]);
-                }
-            }
-            top = mx;
+    const int chunks = live ? r.chunks : 0;
+    Weighed<G> all;
+    all.clear();
+    if (WIDE) {  // (a CTA without a row goes through it empty)
+        const int n_parts = min(8, (chunks + 7) / 8);
+        if (warp < n_parts) {
+            Weighed<G> mine;
+            mine.clear();
+            for (int k0 = warp * 8; k0 < chunks; k0 += 64) weigh_eight<G>(a, p0, stride, k0, chunks, mine);
+            s_part[warp][lane] = mine;
         }
-    if (W > 1) {
-        if (lane == 0) {
-            s_top[warp] = top;
-            s_sum[warp] = sum;
-        }
-#pragma unroll
-        for (int i = 0; i < G; ++i)
-            *reinterpret_cast<float2*>(&s_o[warp][i * 64 + lane * 2]) = make_float2(o[2 * i], o[2 * i + 1]);
         __syncthreads();
-        if (part != 0) return;
-        float all = -1e30f;
-        for (int j = 0; j < W; ++j) all = fmaxf(all, s_top[warp + j]);
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * G; ++i) o[i] = 0.f;
-        for (int j = 0; j < W; ++j) {
-            const float w = ex2_approx(s_top[warp + j] - all);
-            sum = fmaf(s_sum[warp + j], w, sum);
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                const float2 v = *reinterpret_cast<const float2*>(&s_o[warp + j][i * 64 + lane * 2]);
-                o[2 * i] = fmaf(v.x, w, o[2 * i]);
-                o[2 * i + 1] = fmaf(v.y, w, o[2 * i + 1]);
-            }
-        }
-        top = all;
+        if (warp != 0) return;
+        for (int j = 0; j < n_parts; ++j) all.top = fmaxf(all.top, s_part[j][lane].top);
+        for (int j = 0; j < n_parts; ++j) add_weighed<G>(all, s_part[j][lane]);
+    } else {
+        Weighed<G> part[2];
+        part[0].clear();
+        part[1].clear();
+        if (chunks > 0) weigh_eight<G>(a, p0, stride, 0, chunks, part[0]);
+        if (chunks > 8) weigh_eight<G>(a, p0, stride, 8, chunks, part[1]);
+        all.top = fmaxf(part[0].top, part[1].top);
+        add_weighed<G>(all, part[0]);
+        if (chunks > 8) add_weighed<G>(all, part[1]);
     }
-    if (!live) return;
+    if (!live) return;  // (at the end: warps that leave at once made the call of 64 single tokens 65 us, not 51)
+    const float top = all.top, sum = all.sum, (&o)[2 * G] = all.o;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t row = int64_t(r.q0) * a.q_heads + item;
     if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
@@ -719,8 +742,8 @@ cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s) {
     const bool wide = a.max_chunks > 16;
     const int per = wide ? 1 : 8;
     const dim3 grid(unsigned((int64_t(a.max_q) * a.q_heads + per - 1) / per), unsigned(a.B));
-    auto merge = a.c.groups == 1 ? (wide ? cache_merge_kernel<1, 8> : cache_merge_kernel<1, 1>)
-                                 : (wide ? cache_merge_kernel<2, 8> : cache_merge_kernel<2, 1>);
+    auto merge = a.c.groups == 1 ? (wide ? cache_merge_kernel<1, true> : cache_merge_kernel<1, false>)
+                                 : (wide ? cache_merge_kernel<2, true> : cache_merge_kernel<2, false>);
     return launch_pdl(merge, grid, dim3(256), 0, s, a);
 }
 

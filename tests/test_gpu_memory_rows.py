@@ -167,3 +167,19 @@ def test_values_near_the_ends_of_the_range(n, dim):
         c, (gk, gv) = stored(k, v, 16)
         out, lse = c.attend(q, ints([0, n]), n)
         check_rows(q, gk, gv, out, lse, dim ** -0.5, True, torch.bfloat16)
+
+
+@pytest.mark.parametrize("heads,length", [(2, 8300), (2, 12000), (2, 16384), (8, 20000), (2, 5000), (2, 17500), (1, 70000)])
+@pytest.mark.parametrize("n,dim", [(1, 64), (2, 128), (40, 64), (20, 128)])
+def test_a_row_does_not_depend_on_the_width_of_the_table(heads, length, n, dim):
+    """The same request under tables of different widths, and beside a longer one: bit for bit the same."""
+    g = gen(length + n)
+    c, _ = filled([length, 300], heads, dim, 64, g)
+    q = torch.randn(n + 1, heads, dim, generator=g, device=DEV).bfloat16()
+    out, lse = c.attend(q, ints([0, n, n + 1]), n)
+    for pages in (c.width + 1, 20 * 1024 // 64, 64 * 1024 // 64, 200 * 1024 // 64):
+        if pages > c.width:
+            wide = torch.cat([c.block_table, c.block_table.new_full((2, pages - c.width), -1)], 1)
+            again, again_lse = c.attend(q, ints([0, n, n + 1]), n, block_table=wide)
+            assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    assert c.device_status() == 0
