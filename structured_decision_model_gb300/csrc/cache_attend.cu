@@ -37,9 +37,6 @@
 // decoding step of 64 requests of 156 to 16384 keys with 8 heads of 128: 219 MB in 51 us), and
 // the unequal ends of a call; 256 requests of 4096 keys (1.2 GB) take 213 us, 84 % of the
 // memory's measured copy rate.
-#include <algorithm>
-#include <mutex>
-
 #include "cache_attend.cuh"
 
 namespace clef {
@@ -701,20 +698,14 @@ namespace {
 
 template <int G, int NT, int C>
 cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
-    constexpr int kMost = AttendSmem<G, NT, C>::kBytes + kCacheMaxRequests * Requests::kInts * 4;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int resident = 0;  // CTAs an SM for few requests
-    const int bytes = AttendSmem<G, NT, C>::kBytes + a.B * Requests::kInts * 4;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(cache_attend_kernel<G, NT, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-        if (err == cudaSuccess)
-            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_kernel<G, NT, C>, kAttendThreads,
-                                                                AttendSmem<G, NT, C>::kBytes + 64 * Requests::kInts * 4);
-    });
-    if (err != cudaSuccess) return err;
-    return launch_pdl(cache_attend_kernel<G, NT, C>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
-                      bytes, s, a);
+    constexpr int kBytes = AttendSmem<G, NT, C>::kBytes, kEach = Requests::kInts * 4;
+    static PerDevice<int> state;
+    int ctas = 0;
+    const cudaError_t e =
+        resident_ctas(state, cache_attend_kernel<G, NT, C>, kBytes + kCacheMaxRequests * kEach, kBytes + 64 * kEach, &ctas);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_attend_kernel<G, NT, C>, dim3(unsigned(ctas)), dim3(kAttendThreads), size_t(kBytes + a.B * kEach), s,
+                      a);
 }
 
 }  // namespace

@@ -2,9 +2,12 @@
 // work items, and small matrix helpers.
 #pragma once
 
+#include <algorithm>
+
 #include "cache.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "per_device.h"
 
 namespace clef {
 
@@ -330,6 +333,22 @@ __device__ __forceinline__ Item item_of(const CacheAttendArgs& a, const Requests
 // One 4-byte word to shared memory, asynchronously.
 __device__ __forceinline__ void cp_async4(void* smem_dst, const void* gsrc) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gsrc) : "memory");
+}
+
+// CTAs of `kernel` that the current device holds when requests are few, its shared-memory limit
+// (`most` bytes) raised at the device's first call; `state` is the kernel's own.
+template <typename Kernel>
+cudaError_t resident_ctas(PerDevice<int>& state, Kernel kernel, int most, int usual, int* ctas) {
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return cudaError_t(state.get(device, ctas, [&](int* n) -> int {
+        int resident = 0;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, kAttendThreads, usual);
+        *n = std::max(resident, 1) * num_sms();
+        return e;
+    }));
 }
 
 }  // namespace

@@ -25,9 +25,6 @@
 // memory 55 %.  Tried and slower: 32 rows a warp (265 us, out of registers), key operands
 // expanded in shared memory (188), products of two or four pieces side by side (same), the next
 // item requested ahead (191, out of registers).
-#include <algorithm>
-#include <mutex>
-
 #include "cache_attend.cuh"
 
 namespace clef {
@@ -536,19 +533,13 @@ namespace {
 
 template <int G>
 cudaError_t launch_rows(const CacheAttendArgs& a, cudaStream_t s) {
-    constexpr int kMost = RowsSmem<G>::kBytes + kCacheMaxRequests * Requests::kInts * 4;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int resident = 0;  // CTAs an SM for few requests
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(cache_attend_rows_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-        if (err == cudaSuccess)
-            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, cache_attend_rows_kernel<G>, kAttendThreads,
-                                                                RowsSmem<G>::kBytes + 64 * Requests::kInts * 4);
-    });
-    if (err != cudaSuccess) return err;
-    return launch_pdl(cache_attend_rows_kernel<G>, dim3(unsigned(std::max(resident, 1) * num_sms())), dim3(kAttendThreads),
-                      size_t(RowsSmem<G>::kBytes + a.B * Requests::kInts * 4), s, a);
+    constexpr int kBytes = RowsSmem<G>::kBytes, kEach = Requests::kInts * 4;
+    static PerDevice<int> state;
+    int ctas = 0;
+    const cudaError_t e =
+        resident_ctas(state, cache_attend_rows_kernel<G>, kBytes + kCacheMaxRequests * kEach, kBytes + 64 * kEach, &ctas);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_attend_rows_kernel<G>, dim3(unsigned(ctas)), dim3(kAttendThreads), size_t(kBytes + a.B * kEach), s, a);
 }
 
 }  // namespace

@@ -53,3 +53,59 @@ def test_more_rows_than_32_bits_hold_are_refused():
     refused(1, B.clef_cache_attend, *changed(good, 18, P + 2))              # the size is fine
     refused(3, B.clef_cache_attend, *changed(good, 4, 128))                 # 2^31 rows
     refused(3, B.clef_cache_attend, *changed(changed(changed(good, 4, 1), 2, (1 << 31) - 65535), 3, (1 << 31) - 65535))
+
+
+ONCE = r"""
+#include <cstdio>
+#include <thread>
+#include <vector>
+#include "per_device.h"
+
+static clef::PerDevice<int> state;
+static std::atomic<int> made[200], broken;
+
+static int get(int device, int error = 0) {
+    int value = -1;
+    const int e = state.get(device, &value, [&](int* v) {
+        ++made[device];
+        *v = device * 10;
+        return error;
+    });
+    broken += e != error || (e == 0 && value != device * 10);
+    return e;
+}
+
+int main() {
+    get(3, 7);                                   // a failure is passed on ...
+    get(3);                                      // ... and not kept
+    std::vector<std::thread> threads;
+    for (int t = 0; t < 8; ++t)
+        threads.emplace_back([] {
+            for (int i = 0; i < 20000; ++i) get(i % 5);
+        });
+    for (auto& t : threads) t.join();
+    for (int device = 0; device < 5; ++device) broken += made[device] != (device == 3 ? 2 : 1);
+    get(150);                                    // more devices than are kept
+    get(150);
+    broken += made[150] != 2;
+    std::printf("%d\n", broken.load());
+    return broken != 0;
+}
+"""
+
+
+def test_every_device_is_prepared_once(tmp_path):
+    """What attention sets up at its first call is set up for each device, and a failure is not kept."""
+    src, exe = tmp_path / "once.cpp", tmp_path / "once"
+    src.write_text(ONCE)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", f"-I{build.CSRC}", str(src), "-o", str(exe)], check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout
+
+
+def test_attention_keeps_nothing_for_one_device_alone():
+    """No kernel of the cache is set up once a process (a second device would be left out)."""
+    for name in sorted(os.listdir(build.CSRC)):
+        if name.startswith("cache"):
+            with open(os.path.join(build.CSRC, name)) as f:
+                assert "call_once" not in f.read(), name
