@@ -133,8 +133,9 @@ CLEF_API int clef_cache_attend_workspace(const clef_cache* cache, int32_t B, int
  *                0 .. lengths[b] - 1.
  *   causal       0: every query sees all keys of its request.  1: the queries are the last
  *                tokens of the request; query i of n sees keys 0 .. lengths[b] - n + i.
- *   out          [total_q][q_heads][head_dim] of `dtype`, contiguous, 4-byte aligned, apart
- *                from q; lse fp32 [total_q][q_heads], or NULL.
+ *   out          [total_q][q_heads][head_dim] of `dtype`, contiguous, 4-byte aligned; lse
+ *                fp32 [total_q][q_heads], or NULL.  Both lie apart from each other and from q,
+ *                from its first value to its last.
  * A query that sees no key (an empty request, or one with fewer keys than queries) gets
  * out = 0, lse = -inf.  Rows at and behind cu_q[B] are left as they were.
  * Scores, softmax and sums are fp32; softmax weights are rounded to fp16 (11 bits) for the

@@ -1,4 +1,5 @@
 // C ABI of the paged 4-bit memory cache: argument checks and launches.
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 
@@ -43,6 +44,12 @@ constexpr int64_t kMaxEntries = kInt32 / 2;
 
 bool bad_table(const clef_cache* c, int B, int stride) {
     return B < 1 || stride < 1 || int64_t(stride) * c->page > kMaxLength || int64_t(B) * stride > kMaxEntries;
+}
+
+// Whether two runs of bytes share one.
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return n > 0 && m > 0 && (a <= b ? b - a < uintptr_t(n) : a - b < uintptr_t(m));
 }
 
 struct AttendSpace {
@@ -180,6 +187,13 @@ int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total_q, int32
         return CLEF_ERR_UNSUPPORTED_CONFIG;
     if (sp.bytes > 0 && !workspace) return CLEF_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < size_t(sp.bytes)) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+    // several CTAs read a row of queries, and at different times
+    const int64_t n_rows = int64_t(total_q) * q_heads, out_bytes = 2 * n_rows * cache->head_dim;
+    const __int128 q_span = 2 * (__int128(total_q - 1) * q_row_stride + __int128(q_heads - 1) * q_head_stride + cache->head_dim);
+    const int64_t q_bytes = int64_t(std::min(q_span, __int128(INT64_MAX)));
+    if (overlap(q, q_bytes, out, out_bytes) ||
+        (lse && (overlap(lse, 4 * n_rows, q, q_bytes) || overlap(lse, 4 * n_rows, out, out_bytes))))
+        return CLEF_ERR_INVALID_ARGUMENT;
     a.B = B; a.total_q = total_q; a.max_q = max_q; a.q_heads = q_heads; a.head0 = head0; a.kv_heads = kv_heads;
     a.share = q_heads / kv_heads; a.by_share = row_divider(a.share);
     a.dtype = dtype; a.width = table_stride; a.causal = causal;

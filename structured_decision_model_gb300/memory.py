@@ -40,6 +40,15 @@ def _refuse(why):
     raise B.ClefError(1, why)
 
 
+def _overlap(a, b):
+    """Whether the memory of two tensors, from the first value to the last, has bytes in common."""
+    if not a.numel() or not b.numel():
+        return False
+    (a0, a1), (b0, b1) = ((t.data_ptr(), t.data_ptr() + t.element_size() *
+                           (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))) for t in (a, b))
+    return a0 < b1 and b0 < a1
+
+
 class MemoryCache:
     """Pages of 4-bit keys and values, and who holds them.
 
@@ -212,7 +221,7 @@ class MemoryCache:
         if scale is None:
             scale = self.head_dim ** -0.5
         if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or
-                                out.device != self.device or out.data_ptr() == q.data_ptr() and q.numel()):
+                                out.device != self.device or _overlap(out, q)):
             _refuse("out: contiguous, of q's shape and type, apart from q")
         if self._elsewhere():
             with torch.cuda.device(self._index):

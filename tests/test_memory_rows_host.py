@@ -2,6 +2,9 @@
 import os
 import subprocess
 
+import pytest
+import torch
+
 from structured_decision_model_gb300 import binding as B
 from structured_decision_model_gb300 import build
 from test_memory_cache import P, cache, changed, lib, refused  # noqa: F401
@@ -109,3 +112,36 @@ def test_attention_keeps_nothing_for_one_device_alone():
         if name.startswith("cache"):
             with open(os.path.join(build.CSRC, name)) as f:
                 assert "call_once" not in f.read(), name
+
+
+def test_outputs_that_overlap_the_queries_are_refused():
+    """The C entry point goes by the bytes of q, out and lse, whatever their starts and strides."""
+    c = cache()
+    rows, heads, row, head = 6, 8, 8 * 64 + 32, 64
+    q_bytes = 2 * ((rows - 1) * row + (heads - 1) * head + 64)
+    out_bytes, lse_bytes = 2 * rows * heads * 64, 4 * rows * heads
+    far = P + (1 << 16)
+    good = [c, 2, rows, 4, heads, 0, 4, B.BF16, P, row, head, P, P, 4, P, 0.125, 1, far, far << 1, P, 0, 0]
+    for at in (P, P + 4, P + q_bytes - 4, P - out_bytes + 4):
+        refused(1, B.clef_cache_attend, *changed(good, 17, at))
+    for at in (P, P + q_bytes - 4, P - lse_bytes + 4, far, far + out_bytes - 4, far - lse_bytes + 4):
+        refused(1, B.clef_cache_attend, *changed(good, 18, at))
+    heads_first = changed(changed(good, 9, 64), 10, rows * 64)               # the same bytes, other strides
+    refused(1, B.clef_cache_attend, *changed(heads_first, 17, P + 2 * rows * heads * 64 - 4))
+
+
+def test_torch_outputs_that_overlap_the_queries_are_refused():
+    from structured_decision_model_gb300.memory import MemoryCache
+    c = MemoryCache(4, page=16, heads=2, head_dim=64, requests=3, max_len=40, device="cpu")
+    cu = torch.zeros(4, dtype=torch.int32)
+    x = torch.zeros(3000, dtype=torch.bfloat16)
+    plain, size = (lambda at: x[at:at + 640].view(5, 2, 64)), 640
+    wide = x[:5 * 200].view(5, 200)[:, :128].view(5, 2, 64)                  # rows 200 apart
+    turned = x[:640].view(2, 5, 64).transpose(0, 1)                          # heads first
+    for q, out in ((plain(0), plain(0)), (plain(64), plain(0)), (plain(0), plain(size - 2)), (wide, plain(100)),
+                   (wide, plain(800 + 126)), (turned, plain(600)), (plain(2), turned.contiguous().set_(x, 0, (5, 2, 64)))):
+        with pytest.raises(B.ClefError, match="apart from q"):
+            c.attend(q, cu, 1, out=out)
+    for q, out in ((plain(0), plain(size)), (wide, plain(1000)), (turned, plain(640))):
+        with pytest.raises(B.ClefError, match="not on a GPU"):               # accepted so far
+            c.attend(q, cu, 1, out=out)
