@@ -125,7 +125,9 @@ class ClefHead:
         slots = cache.checked_slots(slots)
         if slots.numel() != n_rows:
             raise B.ClefError(1, "memory_store: one slot a row")
-        ws = self.workspace(schema)
+        ws = self._ws   # never a new one: the rows are in this
+        if ws is None:
+            raise B.ClefError(1, "memory_store: no rows have been streamed")
         B.clef_memory_store(self.cfg, schema, record, row0, n_rows, ws.data_ptr(), ws.numel(), cache.struct,
                             slots.data_ptr(), cache.flags.data_ptr(), stream_handle(stream))
 
