@@ -73,10 +73,11 @@ struct Decay {
 };
 
 // Moves a row's `mul` for products p * size of at most x, and returns the factor of its sums, whose
-// largest is `big` (they stay under 2^102, and give way to no smaller products beyond that).
+// largest is `big` (they stay under 2^102, and give way to no smaller products beyond that).  With no product at
+// all (values of zero) the power goes as high as the sums let it: the next products may have any size.
 __device__ __forceinline__ float move_weights(float& mul, float x, float big, const Decay& d) {
     const int old = exponent_of(mul);
-    int to = x > 0.f ? 2 - exponent_of(fminf(x, 0x1.fffffep127f)) : old;
+    int to = x > 0.f ? 2 - exponent_of(fminf(x, 0x1.fffffep127f)) : 119;
     if (big > 0.f) to = min(to, old + d.k + 100 - exponent_of(big));
     to = min(max(to, -126), 119);  // (p mul stays finite)
     mul = pow2i(to);

@@ -183,3 +183,21 @@ def test_a_row_does_not_depend_on_the_width_of_the_table(heads, length, n, dim):
             again, again_lse = c.attend(q, ints([0, n, n + 1]), n, block_table=wide)
             assert torch.equal(again, out) and torch.equal(again_lse, lse)
     assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("n,dim", ROWS)
+def test_zero_values_that_take_the_reference(n, dim):
+    """A run of zero values (no size at all) outweighs what came before; what comes after has its weight and is
+    2^30 times smaller than the first tokens: it is all that the rows are made of."""
+    g = gen(n * 7 + dim)
+    length, u = 900, torch.ones(dim, device=DEV)
+    for score in (30.0, 80.0):
+        k = 0.1 * torch.randn(length, 2, dim, generator=g, device=DEV)
+        k[300:] += score * dim ** 0.5 / (4 * dim) * u
+        v = torch.randn(length, 2, dim, generator=g, device=DEV)
+        v[300:600] = 0
+        v[600:] *= 2.0 ** -30
+        q = (4 * u + 0.1 * torch.randn(n, 2, dim, generator=g, device=DEV)).bfloat16()
+        c, (gk, gv) = stored(k.bfloat16(), v.bfloat16(), 32)
+        out, lse = c.attend(q, ints([0, n]), n, causal=False)
+        check_rows(q, gk, gv, out, lse, dim ** -0.5, False, torch.bfloat16)
