@@ -138,11 +138,15 @@ CLEF_API int clef_cache_attend_workspace(const clef_cache* cache, int32_t B, int
  *                from its first value to its last.
  * A query that sees no key (an empty request, or one with fewer keys than queries) gets
  * out = 0, lse = -inf.  Rows at and behind cu_q[B] are left as they were.
- * Scores, softmax and sums are fp32; softmax weights are rounded to fp16 (11 bits) for the
- * product with the values, and so are the values themselves for requests of many query rows
- * (queries x query heads a key/value head: over 32 at head_dim 64, over 16 at 128); the output
- * is rounded once.  A row's result depends on nothing
- * but its own request: not on the batch, and bit for bit the same from call to call.
+ * Scores, softmax and sums are fp32.  For the product with the values, softmax weights are
+ * rounded to 11 bits for bf16 queries and to 22 for fp16 ones, relative to the row's own
+ * largest product of weight and value scale; for bf16 queries of requests of many rows (queries x
+ * query heads a key/value head: over 32 at head_dim 64, over 16 at 128) the values are rounded to
+ * 11 bits too, twice.  The output is rounded once.  A row's result depends on nothing but its
+ * own request and the keys that it sees: not on the batch, nor on the width of the table, and
+ * bit for bit the same from call to call.  Query values are below 2^118 in magnitude (larger
+ * ones give scores that are too small), stored values below 2^108 (sums of larger ones may
+ * overflow fp32).
  * A table entry outside the cache hides its tokens, a length or cu_q out of range is cut
  * to it, each with CLEF_ERR_DEVICE_BOUNDS.
  * workspace: clef_cache_attend_workspace bytes, 256-byte aligned (may be NULL when 0);

@@ -23,8 +23,12 @@
 // move_weights in cache_attend.cuh), once for the first two sums, which are products
 // of the matrix unit with the codes and with eights: their difference is that of centred codes
 // |c - 8| <= 8, and what the rounding costs is relative to it, not to the whole range of the
-// codes.  The third sum is fp32.  (Centring the codes themselves takes 16 more instructions a
-// piece and 10 % more time.)
+// codes.  The third sum is fp32.  An fp16 output keeps as many digits as the weights, so for fp16
+// (FINE) what the rounding leaves of a weight is rounded to fp16 too and multiplied after it: 22 bits.
+// There the codes are centred: the matrix unit's additions round towards zero, so a difference of
+// two large sums would be off by 2^-19 of them, always to the same side.  (Centring the codes
+// takes 16 more instructions a piece; that and the second product make fp16 17 % slower: 61 us
+// against 52 for a decoding step of 64 requests with 8 heads of 128.)
 // The softmax reference of a row moves only when a score exceeds it by 2^8 (then all sums
 // of the warp are rescaled), so that a step needs no reduction between lanes: each lane sums
 // the keys that it holds, and the lanes are added once at the end of the item.
@@ -54,7 +58,7 @@ struct AttendSmem {
     static constexpr int kBytes = kRing + kResults + 2 * kAttendWarps * kRows * 4;
 };
 
-template <int G, int NT, int C>
+template <int G, int NT, int C, bool FINE>
 __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : NT == 2 ? 3 : 2)
     cache_attend_kernel(const CacheAttendArgs a) {
     using Smem = AttendSmem<G, NT, C>;
@@ -402,8 +406,16 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                 first = false;
             }
             // ---- weights
-            uint32_t pf[KP][G][NT][2];
+            uint32_t pf[KP][G][NT][2], pl[KP][G][NT][2];  // FINE: pl holds what rounding left of pf
             float most = 0.f;
+            auto weigh = [&](int k, int gr, int n, int r) {
+                float w[2] = {0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < C; ++c) w[c] = p[k][n][2 * r + c] * mul[gr][n][c] * vs[k][gr][r];
+                pf[k][gr][n][r] = pack_f16(w[0], w[1]);
+                if (FINE) pl[k][gr][n][r] = rest_f16(pf[k][gr][n][r], w[0], w[1]);
+                return C == 2 ? fmaxf(w[0], w[1]) : w[0];
+            };
 #pragma unroll
             for (int k = 0; k < KP; ++k)
 #pragma unroll
@@ -418,14 +430,9 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const float mid_value = fmaf(8.f, vs[k][gr][r], vm[k][gr][r]);
-                            float w[2] = {0.f, 0.f};
 #pragma unroll
-                            for (int c = 0; c < C; ++c) {
-                                w[c] = p[k][n][2 * r + c] * mul[gr][n][c] * vs[k][gr][r];
-                                z[gr][n][c] = fmaf(p[k][n][2 * r + c], mid_value, z[gr][n][c]);
-                            }
-                            most = C == 2 ? fmax3(most, w[0], w[1]) : fmaxf(most, w[0]);
-                            pf[k][gr][n][r] = pack_f16(w[0], w[1]);
+                            for (int c = 0; c < C; ++c) z[gr][n][c] = fmaf(p[k][n][2 * r + c], mid_value, z[gr][n][c]);
+                            most = fmaxf(most, weigh(k, gr, n, r));
                         }
                 }
             if (__any_sync(0xffffffffu, most > kMostWeight)) {  // larger values than the rows have used before
@@ -455,12 +462,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                         for (int k = 0; k < KP; ++k)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                float w[2] = {0.f, 0.f};
-#pragma unroll
-                                for (int c = 0; c < C; ++c) w[c] = p[k][n][2 * r + c] * mul[gr][n][c] * vs[k][gr][r];
-                                pf[k][gr][n][r] = pack_f16(w[0], w[1]);
-                            }
+                            for (int r = 0; r < 2; ++r) weigh(k, gr, n, r);
                     }
             }
             // ---- value products
@@ -472,15 +474,23 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) pf[k][gr][n][r] = transpose8(pf[k][gr][n][r]);
+                        for (int r = 0; r < 2; ++r) {
+                            pf[k][gr][n][r] = transpose8(pf[k][gr][n][r]);
+                            if (FINE) pl[k][gr][n][r] = transpose8(pl[k][gr][n][r]);
+                        }
                     const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt) {
                         const uint32_t x = words[mt], y = x >> 8;
-                        const uint32_t A[4] = {x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u};
+                        const uint32_t A[4] = {FINE ? centred_low(x) : x & 0x000F000Fu, FINE ? centred_high(x) : x & 0x00F000F0u,
+                                               FINE ? centred_low(y) : y & 0x000F000Fu, FINE ? centred_high(y) : y & 0x00F000F0u};
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16_16816(acc[gr][mt][n], A, pf[k][gr][n][0], pf[k][gr][n][1]);
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16_16816(acc[gr][mt][n], A, pf[k][gr][n][0], pf[k][gr][n][1]);
+                            if (FINE) mma_f16_16816(acc[gr][mt][n], A, pl[k][gr][n][0], pl[k][gr][n][1]);
+                        }
                     }
+                    if (FINE) continue;
                     constexpr uint32_t kEights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma_f16_16816(mid[gr][n], kEights, pf[k][gr][n][0], pf[k][gr][n][1]);
@@ -517,8 +527,9 @@ __global__ void __launch_bounds__(kAttendThreads, G == 2 ? (NT == 1 ? 3 : 2) : N
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
-                            // (codes of the upper half of a run count 2^4)
+                            // (codes of the upper half of a run count 2^4, and all 2^-24)
                             dst[gr * 64 + mt * 16 + half * 8 + g] =
+                                FINE ? fmaf(acc[gr][mt][n][c + 2 * half], 1.f / mul[gr][n][c], zs[gr]) :
                                 fmaf(0x1p24f * fmaf(acc[gr][mt][n][c + 2 * half], half ? 0.0625f : 1.f,
                                                     -mid[gr][n][c + 2 * half]),
                                      1.f / mul[gr][n][c], zs[gr]);
@@ -696,16 +707,21 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs 
 
 namespace {
 
-template <int G, int NT, int C>
-cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
+template <int G, int NT, int C, bool FINE>
+cudaError_t launch_attend_as(const CacheAttendArgs& a, cudaStream_t s) {
     constexpr int kBytes = AttendSmem<G, NT, C>::kBytes, kEach = Requests::kInts * 4;
     static PerDevice<int> state;
     int ctas = 0;
     const cudaError_t e =
-        resident_ctas(state, cache_attend_kernel<G, NT, C>, kBytes + kCacheMaxRequests * kEach, kBytes + 64 * kEach, &ctas);
+        resident_ctas(state, cache_attend_kernel<G, NT, C, FINE>, kBytes + kCacheMaxRequests * kEach, kBytes + 64 * kEach, &ctas);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_attend_kernel<G, NT, C>, dim3(unsigned(ctas)), dim3(kAttendThreads), size_t(kBytes + a.B * kEach), s,
-                      a);
+    return launch_pdl(cache_attend_kernel<G, NT, C, FINE>, dim3(unsigned(ctas)), dim3(kAttendThreads),
+                      size_t(kBytes + a.B * kEach), s, a);
+}
+
+template <int G, int NT, int C>
+cudaError_t launch_attend(const CacheAttendArgs& a, cudaStream_t s) {
+    return a.dtype == 1 ? launch_attend_as<G, NT, C, true>(a, s) : launch_attend_as<G, NT, C, false>(a, s);
 }
 
 }  // namespace

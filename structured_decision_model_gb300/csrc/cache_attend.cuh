@@ -45,6 +45,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Value codes of two tokens (bits 0-3 and 16-19 of x; bits 4-7 and 20-23) less 8, in fp16, exact.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, float b) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(b));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t centred_low(uint32_t x) { return sub_f16x2((x & 0x000F000Fu) | 0x64006400u, 1032.f); }
+__device__ __forceinline__ uint32_t centred_high(uint32_t x) { return sub_f16x2((x & 0x00F000F0u) | 0x54005400u, 72.f); }
+
+// What a packed pair of fp16 numbers leaves of the two that it was rounded from, in fp16.
+__device__ __forceinline__ uint32_t rest_f16(uint32_t w, float lo, float hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pack_f16(lo - f.x, hi - f.y);
+}
+
 // 2^e, e clamped to the normal range.
 __device__ __forceinline__ float pow2i(int e) {
     return __uint_as_float(uint32_t(min(max(e, -126), 127) + 127) << 23);

@@ -18,6 +18,9 @@
 // which are rounded to 11 bits too, after the row's power of two (move_weights in
 // cache_attend.cuh); the denominator sums p_t in fp32.  A token's values and a row's weights
 // are thus scaled by themselves, whatever their neighbours hold.
+//   fp16 outputs (FINE) keep as many digits as that, so for them the value operand is the centred code
+// c - 8, exact; the weights p_t s_t are multiplied in two fp16 parts (22 bits), and the middles' sum
+// p_t (m_t + 8 s_t) goes by itself in fp32 (options of 8 records of 16384 rows: 252 us, bf16 193).
 // The softmax reference of a row moves only when a score exceeds it by 2^8.
 //   64 queries x 8 requests x 16384 keys x 16 heads of 64: 183 us with the merge, 188 TFLOP/s.
 // What bounds it: the instructions around the products (about 180 for 16 keys x 16 rows, 16 of
@@ -40,7 +43,7 @@ struct PieceInfo {
     int bad0, bad1, absent;
 };
 
-template <int G>
+template <int G, bool FINE>
 struct RowsSmem {
     static constexpr int kStages = 3;                               // raw pieces a warp
     static constexpr int kRaw = kAttendWarps * kStages * kPiece * G;
@@ -49,7 +52,8 @@ struct RowsSmem {
     static constexpr int kValuesAt = 512 * G;
     static constexpr int kScalesAt = kValuesAt + 2048 * G;
     static constexpr int kSizesAt = kScalesAt + 16 * 8 * G;
-    static constexpr int kExpanded = kSizesAt + 16 * 4 * G;
+    static constexpr int kMiddlesAt = kSizesAt + 16 * 4 * G;  // FINE
+    static constexpr int kExpanded = kMiddlesAt + (FINE ? 16 * 4 * G : 0);
     static constexpr int kBytes = kRaw + 2 * kAttendWarps * kExpanded;
 };
 
@@ -58,16 +62,12 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
                               *reinterpret_cast<const __half2*>(&c));
     return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, float b) {
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(b));
-    return *reinterpret_cast<const uint32_t*>(&d);
-}
 
 }  // namespace
 
-template <int G>
-__global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_rows_kernel(const CacheAttendArgs a) {
-    using Smem = RowsSmem<G>;
+template <int G, bool FINE>
+__global__ void __launch_bounds__(kAttendThreads, G == 1 ? (FINE ? 3 : 4) : 2) cache_attend_rows_kernel(const CacheAttendArgs a) {
+    using Smem = RowsSmem<G, FINE>;
     constexpr int ST = Smem::kStages;
     constexpr int kBytes = kPiece * G;
     constexpr int kMaxPages = kAttendMaxChunk / 16;
@@ -180,8 +180,12 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
             for (int n = 0; n < 8; ++n) acc[gr][n][0] = acc[gr][n][1] = acc[gr][n][2] = acc[gr][n][3] = 0.f;
         }
         float mul[2][G];  // the weights' powers of two
+        float z[2][G];    // FINE: sum of p (m + 8 s)
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) mul[0][gr] = mul[1][gr] = 1.f;
+        for (int gr = 0; gr < G; ++gr) {
+            mul[0][gr] = mul[1][gr] = 1.f;
+            z[0][gr] = z[1][gr] = 0.f;
+        }
         bool first = true;
 
         auto page_at = [&](int t) { return t < t1 ? s_page[(t >> a.c.page_shift) - me.p0] : nullptr; };
@@ -219,6 +223,14 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 const bool odd = !(fabsf(vs[gr]) < INFINITY && fabsf(vm[gr]) < INFINITY);
                 bad[gr] = __ballot_sync(0xffffffffu, odd) & 0xffffu;
                 if (odd) vs[gr] = vm[gr] = 0.f;
+                if (FINE) {
+                    // the size is the scale itself (2^119 and more gives no fp16 number), the middle goes by itself
+                    if (lane < 16) {
+                        *reinterpret_cast<float*>(dst + Smem::kSizesAt + (gr * 16 + key) * 4) = fminf(vs[gr], 0x1p119f);
+                        *reinterpret_cast<float*>(dst + Smem::kMiddlesAt + (gr * 16 + key) * 4) = fmaf(8.f, vs[gr], vm[gr]);
+                    }
+                    continue;
+                }
                 // 2^e, the size of the token's values: its largest is put in [1, 2)
                 const int e = min(max(exponent_of(fmaxf(fabsf(vm[gr]), fabsf(fmaf(15.f, vs[gr], vm[gr])))), -126), 119);
                 up[gr] = pow2i(-e);
@@ -234,10 +246,10 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 const uint32_t vws[4] = {vw.x, vw.y, vw.z, vw.w};
                 // value scale and middle of the lane's key, then those of keys 2 tq, 2 tq + 1 (low,
                 // high half) and of both + 8
-                const uint32_t own = pack_f16(vs[gr] * up[gr], fmaf(8.f, vs[gr], vm[gr]) * up[gr]);
+                const uint32_t own = FINE ? 0u : pack_f16(vs[gr] * up[gr], fmaf(8.f, vs[gr], vm[gr]) * up[gr]);
                 uint32_t s2[2], m2[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < (FINE ? 0 : 2); ++h) {
                     const uint32_t x = __shfl_sync(0xffffffffu, own, 8 * h + 2 * tq);
                     const uint32_t y = __shfl_sync(0xffffffffu, own, 8 * h + 2 * tq + 1);
                     s2[h] = __byte_perm(x, y, 0x5410);
@@ -247,10 +259,17 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t x = vws[i], y = x >> 8;
-                    const uint32_t a0 = fma_f16x2(sub_f16x2((x & 0x000F000Fu) | 0x64006400u, 1032.f), s2[0], m2[0]);
-                    const uint32_t a1 = fma_f16x2(sub_f16x2((x & 0x00F000F0u) | 0x54005400u, 72.f), s2[0], m2[0]);
-                    const uint32_t a2 = fma_f16x2(sub_f16x2((y & 0x000F000Fu) | 0x64006400u, 1032.f), s2[1], m2[1]);
-                    const uint32_t a3 = fma_f16x2(sub_f16x2((y & 0x00F000F0u) | 0x54005400u, 72.f), s2[1], m2[1]);
+                    // c - 8 of keys 2 tq, 2 tq + 1, and of both + 8: values d, then d + 8
+                    uint32_t a0 = centred_low(x);
+                    uint32_t a1 = centred_high(x);
+                    uint32_t a2 = centred_low(y);
+                    uint32_t a3 = centred_high(y);
+                    if (!FINE) {
+                        a0 = fma_f16x2(a0, s2[0], m2[0]);
+                        a1 = fma_f16x2(a1, s2[0], m2[0]);
+                        a2 = fma_f16x2(a2, s2[1], m2[1]);
+                        a3 = fma_f16x2(a3, s2[1], m2[1]);
+                    }
                     reinterpret_cast<uint4*>(dst + Smem::kValuesAt + gr * 2048)[i * 32 + lane] = make_uint4(a0, a2, a1, a3);
                 }
             }
@@ -268,11 +287,11 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 const PieceInfo info = s_info[buf][i];
                 odd |= (info.bad0 | info.bad1 | info.absent) != 0;
             }
-            // sizes of the values of keys 2 tq and 2 tq + 1 (n = 1: + 8) of piece i
-            auto sizes_of = [&](int i, int gr, int n) {
-                return *reinterpret_cast<const float2*>(base + i * Smem::kExpanded + Smem::kSizesAt +
-                                                        (gr * 16 + n * 8 + 2 * tq) * 4);
+            // of keys 2 tq and 2 tq + 1 (n = 1: + 8) of piece i: the sizes of their values, their middles
+            auto pair_at = [&](int i, int at, int gr, int n) {
+                return *reinterpret_cast<const float2*>(base + i * Smem::kExpanded + at + (gr * 16 + n * 8 + 2 * tq) * 4);
             };
+            auto sizes_of = [&](int i, int gr, int n) { return pair_at(i, Smem::kSizesAt, gr, n); };
             float most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < kAttendWarps; ++i) {
@@ -390,6 +409,7 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                         }
                         if (moved) {
                             const float f = move_weights(mul[r][gr], x, big, d);
+                            if (FINE) z[r][gr] *= d.corr;
 #pragma unroll
                             for (int n = 0; n < 8; ++n) {
                                 acc[gr][n][2 * r] *= f;
@@ -419,6 +439,11 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                         const float2 f = sizes_of(i, gr, n);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) w[i][n][c] = p[i][n][c] * ((c & 1) ? f.y : f.x);
+                        if (FINE) {
+                            const float2 m = pair_at(i, Smem::kMiddlesAt, gr, n);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) z[c >> 1][gr] = fmaf(p[i][n][c], (c & 1) ? m.y : m.x, z[c >> 1][gr]);
+                        }
                         x[0] = fmax3(x[0], w[i][n][0], w[i][n][1]);
                         x[1] = fmax3(x[1], w[i][n][2], w[i][n][3]);
                     }
@@ -440,18 +465,25 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 }
 #pragma unroll
                 for (int i = 0; i < kAttendWarps; ++i) {
-                    uint32_t pa[4];
+                    uint32_t pa[4], pl[4];  // FINE: pl holds what rounding left of pa
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        pa[2 * n] = pack_f16(w[i][n][0] * mul[0][gr], w[i][n][1] * mul[0][gr]);
-                        pa[2 * n + 1] = pack_f16(w[i][n][2] * mul[1][gr], w[i][n][3] * mul[1][gr]);
-                    }
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float w0 = w[i][n][2 * r] * mul[r][gr], w1 = w[i][n][2 * r + 1] * mul[r][gr];
+                            pa[2 * n + r] = pack_f16(w0, w1);
+                            if (FINE) pl[2 * n + r] = rest_f16(pa[2 * n + r], w0, w1);
+                        }
                     const uint8_t* values = base + i * Smem::kExpanded + Smem::kValuesAt + gr * 2048;
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt) {
                         const uint4 f = reinterpret_cast<const uint4*>(values)[mt * 32 + lane];
                         mma_f16_16816(acc[gr][2 * mt], pa, f.x, f.y);
                         mma_f16_16816(acc[gr][2 * mt + 1], pa, f.z, f.w);
+                        if (FINE) {
+                            mma_f16_16816(acc[gr][2 * mt], pl, f.x, f.y);
+                            mma_f16_16816(acc[gr][2 * mt + 1], pl, f.z, f.w);
+                        }
                     }
                 }
             }
@@ -489,7 +521,10 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 #pragma unroll
             for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-                for (int o = 1; o < 4; o <<= 1) none[r][gr] += __shfl_xor_sync(0xffffffffu, none[r][gr], o);
+                for (int o = 1; o < 4; o <<= 1) {
+                    none[r][gr] += __shfl_xor_sync(0xffffffffu, none[r][gr], o);
+                    if (FINE) z[r][gr] += __shfl_xor_sync(0xffffffffu, z[r][gr], o);
+                }
             const int rr = r0 + 8 * r;
             if (rr >= me.rows) continue;
             const int qi = a.by_share(me.row0 + rr), qh = me.h * a.share + me.row0 + rr - qi * a.share;
@@ -515,8 +550,8 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
                 const float back = 1.f / mul[r][gr];
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                    const float x = fmaf(acc[gr][n][2 * r] * back, inv, none[r][gr]);
-                    const float y = fmaf(acc[gr][n][2 * r + 1] * back, inv, none[r][gr]);
+                    const float x = fmaf(fmaf(acc[gr][n][2 * r], back, z[r][gr]), inv, none[r][gr]);
+                    const float y = fmaf(fmaf(acc[gr][n][2 * r + 1], back, z[r][gr]), inv, none[r][gr]);
                     const int64_t at = row * (64 * G) + gr * 64 + n * 8 + 2 * tq;
                     if (!whole)
                         *reinterpret_cast<float2*>(a.part_o + at) = make_float2(x, y);
@@ -531,21 +566,22 @@ __global__ void __launch_bounds__(kAttendThreads, G == 1 ? 4 : 2) cache_attend_r
 
 namespace {
 
-template <int G>
+template <int G, bool FINE>
 cudaError_t launch_rows(const CacheAttendArgs& a, cudaStream_t s) {
-    constexpr int kBytes = RowsSmem<G>::kBytes, kEach = Requests::kInts * 4;
+    constexpr int kBytes = RowsSmem<G, FINE>::kBytes, kEach = Requests::kInts * 4;
     static PerDevice<int> state;
     int ctas = 0;
     const cudaError_t e =
-        resident_ctas(state, cache_attend_rows_kernel<G>, kBytes + kCacheMaxRequests * kEach, kBytes + 64 * kEach, &ctas);
+        resident_ctas(state, cache_attend_rows_kernel<G, FINE>, kBytes + kCacheMaxRequests * kEach, kBytes + 64 * kEach, &ctas);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_attend_rows_kernel<G>, dim3(unsigned(ctas)), dim3(kAttendThreads), size_t(kBytes + a.B * kEach), s, a);
+    return launch_pdl(cache_attend_rows_kernel<G, FINE>, dim3(unsigned(ctas)), dim3(kAttendThreads), size_t(kBytes + a.B * kEach), s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attend_rows(const CacheAttendArgs& a, cudaStream_t s) {
-    return a.c.groups == 1 ? launch_rows<1>(a, s) : launch_rows<2>(a, s);
+    if (a.dtype == 1) return a.c.groups == 1 ? launch_rows<1, true>(a, s) : launch_rows<2, true>(a, s);
+    return a.c.groups == 1 ? launch_rows<1, false>(a, s) : launch_rows<2, false>(a, s);
 }
 
 }  // namespace clef

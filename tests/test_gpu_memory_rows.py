@@ -201,3 +201,62 @@ def test_zero_values_that_take_the_reference(n, dim):
         c, (gk, gv) = stored(k.bfloat16(), v.bfloat16(), 32)
         out, lse = c.attend(q, ints([0, n]), n, causal=False)
         check_rows(q, gk, gv, out, lse, dim ** -0.5, False, torch.bfloat16)
+
+
+# ---- fp16: the output keeps 11 bits, so what comes before it is held to more
+
+FINE = [(1, 64), (8, 64), (20, 64), (32, 64), (33, 64), (90, 64), (4, 128), (8, 128), (16, 128), (17, 128), (70, 128)]
+
+
+@pytest.mark.parametrize("n,dim", FINE)
+@pytest.mark.parametrize("length", [2, 7, 40, 300, 2500])
+def test_fp16_rows_are_exact_up_to_their_rounding(n, dim, length):
+    """Nearly even weights (small queries, so that the scores' own error is small: 160 x 2^-24 of their size).
+    Before the output's rounding: weights in two fp16 parts (2^-22 of p span, the second part's floor
+    len 2^-27), scores, exponentials and sums as at the top of this file."""
+    g = gen(n * 11 + dim + length)
+    k = torch.randn(length, 2, dim, generator=g, device=DEV).half()
+    v = (torch.randn(length, 2, dim, generator=g, device=DEV) * torch.exp(torch.randn(length, 1, 1, generator=g, device=DEV))).half()
+    q = (0.002 * torch.randn(n, 4, dim, generator=g, device=DEV)).half()
+    c, (gk, gv) = stored(k, v, 16)
+    scale = dim ** -0.5
+    out, _ = c.attend(q, ints([0, n]), n, causal=False)
+    want, want_lse = attention(q, gk, gv, scale, False)
+    groups = gv.double().reshape(length, 2, dim // 64, 64).repeat_interleave(2, 1)
+    size = torch.maximum(groups.amax(-1) - groups.amin(-1), groups.abs().amax(-1))
+    s = torch.einsum("nhd,lhd->hnl", q.double(), gk.double().repeat_interleave(2, 1)) * scale
+    used = torch.einsum("hnl,lhg->nhg", torch.exp(s - want_lse.T[..., None]), size).repeat_interleave(64, -1)
+    amp = q.double().abs().sum(-1).amax().item() * gk.double().abs().amax().item() * 4 * scale
+    rel = 2 * (2 * 160 * 2.0 ** -24 * amp + 2.0 ** -22 + 2.0 ** -24 * (length / 8 + 100)) + 2.0 ** -22 + length * 2.0 ** -27
+    bound = rel * used * (1 + 2.0 ** -10) + 2.0 ** -11 * want.abs() * (1 + 2.0 ** -10) + 2.0 ** -25
+    error = (out.double() - want).abs()
+    assert (error <= bound).all(), (error / bound).amax()
+
+
+@pytest.mark.parametrize("n,dim", FINE)
+def test_fp16_rows_have_the_error_of_their_rounding(n, dim):
+    """Ordinary scores: the mean square error is that of rounding the exact result once (errors in front of it
+    that are a fraction r of it raise its root by r^2 / 2; 5 % allows r = 0.3, and 2^-22 is 2^-10 of it)."""
+    g = gen(n * 13 + dim)
+    k = torch.randn(2500, 2, dim, generator=g, device=DEV).half()
+    v = (torch.randn(2500, 2, dim, generator=g, device=DEV) * torch.exp(0.4 * torch.randn(2500, 1, 1, generator=g, device=DEV))).half()
+    q = torch.randn(n, 4, dim, generator=g, device=DEV).half()
+    c, (gk, gv) = stored(k, v, 64)
+    out, _ = c.attend(q, ints([0, n]), n)
+    want, _ = attention(q, gk, gv, dim ** -0.5, True)
+    rms = lambda x: x.square().mean().sqrt().item()
+    assert rms(out.double() - want) <= 1.05 * rms(want.half().double() - want)
+
+
+@pytest.mark.parametrize("n,share", [(1, 8), (1, 1), (2, 8), (8, 8)])
+def test_fp16_rows_of_a_long_memory_have_the_error_of_their_rounding(n, share):
+    """The mean of 100000 values is far smaller than they are: errors of one sign would show."""
+    g = gen(n * 17 + share)
+    k = torch.randn(100003, 2, 64, generator=g, device=DEV).half()
+    v = torch.randn(100003, 2, 64, generator=g, device=DEV).half()
+    q = torch.randn(n, 2 * share, 64, generator=g, device=DEV).half()
+    c, (gk, gv) = stored(k, v, 64)
+    out, _ = c.attend(q, ints([0, n]), n)
+    want, _ = attention(q, gk, gv, 0.125, True)
+    rms = lambda x: x.square().mean().sqrt().item()
+    assert rms(out.double() - want) <= 1.05 * rms(want.half().double() - want)
