@@ -63,9 +63,13 @@ struct CacheAttendArgs {
 
 // Keys of one split of a request's memory.  It goes by the key/value heads of the call alone,
 // so that a row's result does not depend on the batch.  Long splits spend less on their ends,
-// short ones spread a lone request over the GPU: 64 queries x 8 requests x 16384 keys x 16
-// heads take 221 us with 1024 keys a split, 181 with 2048 and 169 with 4096; one token over
-// 131001 keys x 2 heads takes 16.0, 18.0 and 22.1 us.
+// short ones spread a lone request over the GPU.  With 1024, 2048 and 4096 keys a split, bf16:
+//   one token of 64 requests of 156-16384 keys, 8 heads of 128     54, 52 and 49 us
+//   one token over 131072 keys, 16 heads of 64                     43, 40 and 38 us
+//   64 queries x 8 requests x 16384 keys, 16 heads of 64          205, 193 and 182 us
+//   96 queries x 4 requests x 8192 keys, 8 heads of 128, causal   287, 268 and 334 us
+// so 2048 from 8 heads on.  One token over 131001 keys x 2 heads takes 16.5, 15.3 and 18.0 us
+// with 512, 1024 and 2048: 1024 below 8 heads.
 constexpr int kAttendMaxChunk = 2048;
 __host__ __device__ inline int attend_chunk(int kv_heads) { return kv_heads >= 8 ? kAttendMaxChunk : 1024; }
 

@@ -36,10 +36,10 @@
 // Requests longer than one split leave normalised partials with their log-sum, which the
 // merge kernel weighs.
 //
-// What bounds it: instruction issue, the integer pipe above all (about 140 instructions for 16
-// keys of 64 values, 40 of them to split codes; 51 % of the issue slots and 57 % of the memory rate in a
-// decoding step of 64 requests of 156 to 16384 keys with 8 heads of 128: 219 MB in 51 us), and
-// the unequal ends of a call; 256 requests of 4096 keys (1.2 GB) take 213 us, 84 % of the
+// What bounds it: instruction issue, the integer pipe above all (about 142 instructions for 16
+// keys of 64 values, 40 of them to split codes; 52 % of the issue slots and 57 % of the memory rate
+// in a decoding step of 64 requests of 156 to 16384 keys with 8 heads of 128: 218 MB in 52 us),
+// and the unequal ends of a call; 256 requests of 4096 keys (1.2 GB) take 216 us, 83 % of the
 // memory's measured copy rate.
 #include "cache_attend.cuh"
 
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const CacheAttendArgs 
         add_weighed<G>(all, part[0]);
         if (chunks > 8) add_weighed<G>(all, part[1]);
     }
-    if (!live) return;  // (at the end: warps that leave at once made the call of 64 single tokens 65 us, not 51)
+    if (!live) return;  // (at the end: warps that leave at once made the call of 64 single tokens 65 us, not 52)
     const float top = all.top, sum = all.sum, (&o)[2 * G] = all.o;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t row = int64_t(r.q0) * a.q_heads + item;
@@ -730,7 +730,7 @@ cudaError_t launch_cache_attend(const CacheAttendArgs& a, cudaStream_t s) {
     if (a.total_q <= 0 || a.max_q <= 0) return cudaSuccess;
     // Columns of the matrix instruction: as few as the requests that come here can have rows.  Up to
     // four rows sit in every other column, so that each lane has one column of scores, not two
-    // (64 requests, 4 rows of 128 values each: 51 us, and 55 us with all columns).
+    // (64 requests, 4 rows of 128 values each: 52 us, and 55 us with all columns).
     const int64_t most = int64_t(a.max_q) * a.share;  // query rows of any request
     cudaError_t e;
     if (a.c.groups == 1)

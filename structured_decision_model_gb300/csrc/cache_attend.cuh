@@ -141,8 +141,12 @@ __device__ __forceinline__ Request request_of(const CacheAttendArgs& a, int b, b
 
 // Requests of up to so many query rows (queries x the query heads that share a key head) are
 // the few-rows kernel's, the others the many-rows kernel's: by the request alone, so that a
-// row's result does not depend on the batch.  128 requests x 1024 keys x 16 heads of 64: 24 rows
-// take 96 us in the first and 137 in the second, 64 rows 219 and 190.
+// row's result does not depend on the batch.  An item of the first holds up to 32 rows at head size
+// 64 and 16 at 128, and these are the borders.  128 requests x 1024 keys in the first and the second, bf16:
+//   16 heads of 64:   16 rows 73 and 131 us, 24 rows 105 and 152, 32 rows 146 and 154,
+//                     33 rows 269 and 177, 64 rows 283 and 204
+//   8 heads of 128:   8 rows 44 and 158 us, 16 rows 73 and 162, 64 rows 252 and 202;
+//                     17 to 32 rows, in two items, would take 126-131 us in the first (second: 192)
 __host__ __device__ constexpr int few_rows(int groups) { return groups == 1 ? 32 : 16; }
 
 // Inclusive sums of two numbers over the CTA's threads.
@@ -295,7 +299,7 @@ __device__ __forceinline__ int scan_requests(const CacheAttendArgs& a, const Req
 
 // The item of a CTA's n-th turn: items, largest first, are dealt out in rows that run forward
 // and back, so that the sums of their sizes come out nearly even (a decoding step of 64 requests
-// of 156 to 16384 keys, 8 heads of 128: 55 us, and 64 us dealt in the requests' order).
+// of 156 to 16384 keys, 8 heads of 128: 52 us, and 58 us dealt in the requests' order).
 __device__ __forceinline__ int item_of_turn(int n) {
     return n * int(gridDim.x) + ((n & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
 }

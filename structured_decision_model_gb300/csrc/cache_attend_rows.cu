@@ -22,10 +22,11 @@
 // c - 8, exact; the weights p_t s_t are multiplied in two fp16 parts (22 bits), and the middles' sum
 // p_t (m_t + 8 s_t) goes by itself in fp32 (options of 8 records of 16384 rows: 252 us, bf16 193).
 // The softmax reference of a row moves only when a score exceeds it by 2^8.
-//   64 queries x 8 requests x 16384 keys x 16 heads of 64: 183 us with the merge, 188 TFLOP/s.
-// What bounds it: the instructions around the products (about 180 for 16 keys x 16 rows, 16 of
-// them matrix instructions) at half of the issue slots; the matrix pipe is 37 % busy, shared
-// memory 55 %.  Tried and slower: 32 rows a warp (265 us, out of registers), key operands
+//   64 queries x 8 requests x 16384 keys x 16 heads of 64: 193 us with the merge, 178 TFLOP/s.
+// What bounds it: the instructions around the products (about 197 for 16 keys x 16 rows, 16 of
+// them matrix instructions) at half of the issue slots; the matrix pipe is 35 % busy, shared
+// memory 57 %.  Scaling each token's values by itself costs 20 of them and 10 us.  Before that, at
+// 183 us, these were tried and slower: 32 rows a warp (265 us, out of registers), key operands
 // expanded in shared memory (188), products of two or four pieces side by side (same), the next
 // item requested ahead (191, out of registers).
 #include "cache_attend.cuh"
