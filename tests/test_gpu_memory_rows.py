@@ -260,3 +260,57 @@ def test_fp16_rows_of_a_long_memory_have_the_error_of_their_rounding(n, share):
     want, _ = attention(q, gk, gv, 0.125, True)
     rms = lambda x: x.square().mean().sqrt().item()
     assert rms(out.double() - want) <= 1.05 * rms(want.half().double() - want)
+
+
+@pytest.mark.parametrize("jump", [18, 40, 120])
+@pytest.mark.parametrize("n,dim", ROWS)
+def test_fp16_rows_beside_large_values(n, dim, jump):
+    """fp16 queries over a memory stored in bf16: tokens of no weight and tokens that a row does not see are 2^jump
+    times larger than the others (past fp16), or no numbers."""
+    g = gen(jump * 10 + n + dim)
+    length, u = 700, torch.ones(dim, device=DEV)
+    u[::2] = -1
+    k = torch.randn(length, 2, dim, generator=g, device=DEV)
+    v = torch.randn(length, 2, dim, generator=g, device=DEV)
+    far = torch.rand(length, generator=g, device=DEV) < 0.1
+    far[:3] = True
+    far[length - n - 2:] = False
+    k[far] = -8 * u
+    v[far] *= 2.0 ** jump
+    q = (4 * u + torch.randn(n, 2, dim, generator=g, device=DEV)).half()
+    k, v = k.bfloat16(), v.bfloat16()
+    c, (gk, gv) = stored(k, v, 32)
+    out, lse = c.attend(q, ints([0, n]), n)
+    check_rows(q, gk, gv, out, lse, dim ** -0.5, True, torch.float16)
+    hidden = n // 2                               # the last tokens: rows before them keep their bits
+    for value in (2.0 ** jump, math.nan):
+        if hidden:
+            v[length - hidden:] = value * torch.randn(hidden, 2, dim, generator=g, device=DEV).bfloat16()
+            c.append(k[length - hidden:], v[length - hidden:], slots_of(c, 0, torch.arange(length - hidden, length, device=DEV)))
+            again, again_lse = c.attend(q, ints([0, n]), n)
+            assert torch.equal(again[:n - hidden], out[:n - hidden]) and torch.equal(again_lse, lse)
+    if hidden:
+        assert torch.isnan(again[n - hidden:]).all()
+    assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,dim", [(2, 64), (40, 64), (2, 128), (40, 128)])
+def test_half_of_a_value_that_is_no_number(n, dim, dtype):
+    """A group of 64 values that is no number stays alone, and missing pages hide their tokens, in both types."""
+    g = gen(n + dim)
+    k = torch.randn(2100, 1, dim, generator=g, device=DEV).to(dtype)
+    v = torch.randn(2100, 1, dim, generator=g, device=DEV).to(dtype)
+    q = torch.randn(n, 1, dim, generator=g, device=DEV).to(dtype)
+    c, (gk, gv) = stored(k, v, 32)
+    clean, _ = c.attend(q, ints([0, n]), n, causal=False)
+    check_rows(q, gk, gv, clean, _, dim ** -0.5, False, dtype)
+    v[7, :, :64] = math.nan
+    c.append(k[7:8], v[7:8], slots_of(c, 0, torch.tensor([7], device=DEV)))
+    out, lse = c.attend(q, ints([0, n]), n, causal=False)
+    assert torch.isnan(out[..., :64]).all() and torch.equal(out[..., 64:], clean[..., 64:]) and not torch.isnan(lse).any()
+    table = c.block_table.clone()
+    table[0, 0] = -1                              # the token is hidden with its page
+    out, lse = c.attend(q, ints([0, n]), n, causal=False, block_table=table)
+    assert c.device_status() == 5
+    check_rows(q, gk[32:], gv[32:], out, lse, dim ** -0.5, False, dtype)
