@@ -1,0 +1,86 @@
+/*
+ * clef_fp4.h — C ABI of the microscaled 4-bit operators on GB300 (sm_103a).
+ *
+ * The memory K/V projection is four fifths of the head's time (clef_head.h).  Its rows and
+ * weights can be kept in 4 bits with a scale for every few values, which the tensor cores
+ * multiply at several times their bf16 rate and which take a quarter of the memory: rows
+ * quantised (with the statistics that the memory LayerNorm needs, in the same pass), read
+ * back, multiplied with the LayerNorm folded in, and the head's streamed rows over them
+ * (clef_stream_rows_fp4).
+ *
+ * A row of `cols` values is cut into blocks (the last may be short).  A value is an e2m1
+ * number (0, 0.5, 1, 1.5, 2, 3, 4, 6, signed) times its block's scale, nearest, ties to the
+ * even code; the decisions are exact, so equal values give equal codes on any path.
+ *   CLEF_MXFP4  blocks of 32, scale 2^(floor(log2 amax) - 2), not below 2^-127 (e8m0);
+ *               quotients above 6 become 6
+ *   CLEF_NVFP4  blocks of 16, scale r * e4m3(amax / (6 r)), where r = 2^(floor(log2 a) - 10),
+ *               not below 2^-126, a the row's largest finite size: a row stands by itself,
+ *               whatever other rows hold
+ * A block that holds an infinity or a NaN reads as NaN, and so does every product of its row;
+ * other rows and blocks are as without it.
+ *
+ * Layout.  codes: row-major, ceil(cols / 32) * 16 bytes a row; byte j holds value 2j in its
+ * low four bits and 2j + 1 in the high ones (bit 3 the sign); values behind `cols` are 0.
+ * scales: one byte a block, rows in groups of 128 and blocks in groups of 4; a group of both
+ * is 512 contiguous bytes (byte (row % 32) * 16 + row % 128 / 32 * 4 + block % 4), the groups
+ * of 128 rows lie one after the other with cols rounded up to 256; blocks behind `cols` are 0.
+ * row_scale: r of every row (fp32; unused for CLEF_MXFP4).
+ *
+ * Conventions are those of clef_head.h: caller-owned device memory, host-side validation
+ * before any launch, a clef_status from every entry point, all work asynchronous on
+ * `stream` of the current device, nothing allocated, every call capturable into a CUDA
+ * graph.  `flags` is a device int32 that the caller clears; kernels only set bits in it
+ * (clef_cache_status reads and clears it).
+ */
+#ifndef CLEF_FP4_H
+#define CLEF_FP4_H
+
+#include "clef_cache.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum clef_fp4_format { CLEF_MXFP4 = 0, CLEF_NVFP4 = 1 } clef_fp4_format;
+
+#define CLEF_FP4_MAX_COLS 16384
+
+/* A matrix of rows kept in 4 bits.  codes and scales: 256-byte aligned device memory of the
+ * sizes that clef_fp4_size gives; row_scale: [rows] fp32, NULL for CLEF_MXFP4.
+ * 1 <= rows < 2^31 - 256, 1 <= cols <= CLEF_FP4_MAX_COLS. */
+typedef struct clef_fp4 {
+    void* codes;
+    void* scales;
+    float* row_scale;
+    int32_t rows;
+    int32_t cols;
+    int32_t format;
+} clef_fp4;
+
+/* Bytes of codes and scales of a rows x cols matrix. */
+CLEF_API int clef_fp4_size(int32_t format, int32_t rows, int32_t cols, size_t* codes_bytes, size_t* scales_bytes);
+
+/* Rows x (dtype bf16, fp16 or fp32, `row_stride` elements apart, the values of a row
+ * contiguous) into q.  Optional outputs ([rows] fp32, NULL: not wanted): mean and rstd, the
+ * row's mean and 1 / sqrt(variance + 1e-5) of x itself; sums, the sum of what the row
+ * stands for once kept. */
+CLEF_API int clef_fp4_quantize(const clef_fp4* q, int32_t dtype, const void* x, int64_t row_stride, float* mean,
+                               float* rstd, float* sums, void* stream);
+
+/* What the rows of q stand for, rounded once to dtype (bf16, fp16 or fp32), into out. */
+CLEF_API int clef_fp4_dequantize(const clef_fp4* q, int32_t dtype, void* out, int64_t row_stride, void* stream);
+
+/* out[m, n] = sum over k of x[m, k] w[n, k] + bias[n], sums in fp32, rounded once to dtype
+ * (bf16, fp16 or fp32).  x and w: of one format and one number of columns; bias: [w.rows]
+ * fp32 or NULL.  With mean, rstd (of x's rows) and sums (of w's rows) all given, x's rows
+ * are taken less their means and times their rstd: rstd[m] (x w^T - mean[m] sums[n]) + bias[n],
+ * the layer behind a LayerNorm whose weight w holds already.  out's rows are
+ * `row_stride` elements apart (at least w.rows) and out lies apart from all inputs. */
+CLEF_API int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, const float* mean,
+                              const float* rstd, const float* sums, int32_t dtype, void* out, int64_t row_stride,
+                              int32_t* flags, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* CLEF_FP4_H */

@@ -24,10 +24,12 @@ EXPORTED = [
     "clef_stream_rows", "clef_stream_finish", "clef_selftest_wait_timeout", "clef_stream_rows_f16",
     "clef_stream_finish_f16", "clef_cache_size", "clef_cache_plan", "clef_cache_append", "clef_cache_read",
     "clef_cache_attend_workspace", "clef_cache_attend", "clef_cache_status", "clef_memory_store",
-    "clef_stream_finish_memory",
+    "clef_stream_finish_memory", "clef_fp4_size", "clef_fp4_quantize", "clef_fp4_dequantize", "clef_fp4_product",
 ]
 BF16, FP16, FP32 = 0, 1, 2   # clef_dtype
 CACHE_MAX_REQUESTS = 1024
+MXFP4, NVFP4 = 0, 1          # clef_fp4_format
+FP4_MAX_COLS = 16384
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
@@ -58,6 +60,10 @@ class ClefDebugOutputs(ctypes.Structure):
 
 class ClefCache(ctypes.Structure):
     _fields_ = [("data", _vp), ("n_pages", _i32), ("page", _i32), ("heads", _i32), ("head_dim", _i32)]
+
+
+class ClefFp4(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("row_scale", _vp), ("rows", _i32), ("cols", _i32), ("format", _i32)]
 
 
 _lib = None
@@ -111,6 +117,11 @@ def load():
                                               ctypes.POINTER(ClefSchema), _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                               _vp, _vp, _sz, cache, _vp, _i32, _vp, _vp, _sz,
                                               ctypes.POINTER(ClefDebugOutputs), _vp]
+    fp4 = ctypes.POINTER(ClefFp4)
+    lib.clef_fp4_size.argtypes = [_i32, _i32, _i32, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
+    lib.clef_fp4_quantize.argtypes = [fp4, _i32, _vp, _i64, _vp, _vp, _vp, _vp]
+    lib.clef_fp4_dequantize.argtypes = [fp4, _i32, _vp, _i64, _vp]
+    lib.clef_fp4_product.argtypes = [fp4, fp4, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
     for name in EXPORTED:
         if name not in ("clef_weight_count", "clef_status_string", "clef_kernel_launches"):
             getattr(lib, name).restype = ctypes.c_int
@@ -327,3 +338,25 @@ def clef_stream_finish_memory(cfg, weight_ptrs, prepared_ptr, schema: Schema, fi
                                             workspace_bytes, ctypes.byref(cache), block_table_ptr, table_stride,
                                             flags_ptr, attend_workspace_ptr, attend_workspace_bytes, dbg, stream),
            "clef_stream_finish_memory")
+
+
+def clef_fp4_size(format, rows, cols):
+    """Bytes of the codes and of the scales."""
+    codes, scales = _sz(0), _sz(0)
+    _check(load().clef_fp4_size(format, rows, cols, ctypes.byref(codes), ctypes.byref(scales)), "clef_fp4_size")
+    return codes.value, scales.value
+
+
+def clef_fp4_quantize(q: ClefFp4, dtype, x_ptr, row_stride, mean_ptr=None, rstd_ptr=None, sums_ptr=None, stream=0):
+    _check(load().clef_fp4_quantize(q, dtype, x_ptr, row_stride, mean_ptr, rstd_ptr, sums_ptr, stream),
+           "clef_fp4_quantize")
+
+
+def clef_fp4_dequantize(q: ClefFp4, dtype, out_ptr, row_stride, stream=0):
+    _check(load().clef_fp4_dequantize(q, dtype, out_ptr, row_stride, stream), "clef_fp4_dequantize")
+
+
+def clef_fp4_product(x: ClefFp4, w: ClefFp4, bias_ptr, mean_ptr, rstd_ptr, sums_ptr, dtype, out_ptr, row_stride,
+                     flags_ptr, stream=0):
+    _check(load().clef_fp4_product(x, w, bias_ptr, mean_ptr, rstd_ptr, sums_ptr, dtype, out_ptr, row_stride, flags_ptr,
+                                   stream), "clef_fp4_product")

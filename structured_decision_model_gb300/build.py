@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libclef_head.so")
 SOURCES = ["gemm.cu", "attention.cu", "head_kernels.cu", "record_tail.cu", "api.cu", "cache.cu", "cache_attend.cu",
-           "cache_attend_rows.cu", "cache_api.cu"]
+           "cache_attend_rows.cu", "cache_api.cu", "fp4.cu", "fp4_product.cu", "fp4_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
@@ -28,7 +28,7 @@ def _nvcc():
 
 def _newest_input():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(HERE, "..", "include", f) for f in ("clef_head.h", "clef_cache.h")]
+    files += [os.path.join(HERE, "..", "include", f) for f in ("clef_head.h", "clef_cache.h", "clef_fp4.h")]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files if os.path.exists(f))
 

@@ -1,0 +1,63 @@
+// Host-side launchers of the microscaled 4-bit kernels (internal to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/clef_fp4.h"
+
+namespace clef {
+
+constexpr int kFp4Tile = 256;       // columns of one K tile: 128 bytes of codes
+constexpr int kFp4RowGroup = 128;   // rows of one group of scales
+constexpr int kFp4ScaleGroup = 512; // bytes of 128 rows x 4 scales
+
+inline int fp4_block(int format) { return format == CLEF_MXFP4 ? 32 : 16; }
+inline int64_t fp4_code_stride(int cols) { return int64_t(cols + 31) / 32 * 16; }
+inline int fp4_ktiles(int cols) { return (cols + kFp4Tile - 1) / kFp4Tile; }
+// 512-byte groups of scales of 128 rows: 2 (mxfp4) or 4 (nvfp4) a K tile
+inline int fp4_kgroups(int format, int cols) { return fp4_ktiles(cols) * (format == CLEF_MXFP4 ? 2 : 4); }
+inline int64_t fp4_row_groups(int64_t rows) { return (rows + kFp4RowGroup - 1) / kFp4RowGroup; }
+
+struct Fp4QuantizeArgs {
+    const void* x;
+    int64_t row_stride;  // elements
+    uint8_t* codes;
+    uint8_t* scales;
+    float* row_scale;    // NVFP4
+    float* mean;         // optional
+    float* rstd;         // with mean
+    float* sums;         // optional
+    int rows, cols;
+};
+cudaError_t launch_fp4_quantize(const Fp4QuantizeArgs& a, int format, int dtype, cudaStream_t s);
+
+struct Fp4DequantizeArgs {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const float* row_scale;
+    void* out;
+    int64_t row_stride;
+    int rows, cols;
+};
+cudaError_t launch_fp4_dequantize(const Fp4DequantizeArgs& a, int format, int dtype, cudaStream_t s);
+
+struct Fp4ProductArgs {
+    const float* x_scale;  // [M], null: 1
+    const float* w_scale;  // [N], null: 1
+    const float* bias;     // [N], null: 0
+    const float* mean;     // [M], with rstd and sums: the LayerNorm fold
+    const float* rstd;     // [M]
+    const float* sums;     // [N]
+    void* out;
+    int64_t ldo;
+    int* flags;
+    int M, N;              // rows of x and of w
+    int k64;               // columns in steps of 64 (one MMA)
+    int kgroups;           // scale groups of a row group
+    int splits;            // K parts of a tile (a cluster)
+};
+cudaError_t launch_fp4_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, int dtype,
+                               cudaStream_t s);
+
+}  // namespace clef

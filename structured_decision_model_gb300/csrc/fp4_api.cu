@@ -1,0 +1,149 @@
+// C ABI of the microscaled 4-bit operators: argument checks and launches.
+#include <initializer_list>
+
+#include "common.cuh"
+#include "fp4.h"
+
+using namespace clef;
+
+namespace {
+
+constexpr int64_t kInt32 = int64_t(1) << 31;
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+bool bad_type(int dtype) { return dtype != CLEF_BF16 && dtype != CLEF_FP16 && dtype != CLEF_FP32; }
+
+int64_t size_of(int dtype) { return dtype == CLEF_FP32 ? 4 : 2; }
+
+// A run of bytes that a call reads or writes (empty where the pointer is null).
+struct Run {
+    uintptr_t at;
+    uint64_t n;
+    Run(const void* p, int64_t bytes) : at(reinterpret_cast<uintptr_t>(p)), n(p && bytes > 0 ? uint64_t(bytes) : 0) {}
+    bool meets(const Run& o) const { return n && o.n && (at <= o.at ? o.at - at < n : at - o.at < o.n); }
+};
+
+// From the first value to the last of rows `stride` elements apart.
+Run rows_run(const void* p, int64_t rows, int64_t stride, int64_t cols, int64_t size) {
+    return Run(p, ((rows - 1) * stride + cols) * size);
+}
+
+int check_size(int32_t format, int32_t rows, int32_t cols) {
+    if (format != CLEF_MXFP4 && format != CLEF_NVFP4) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    if (rows < 1 || rows >= kInt32 - 256 || cols < 1 || cols > CLEF_FP4_MAX_COLS) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    // scale groups are counted in 32 bits
+    if (fp4_row_groups(rows) * fp4_kgroups(format, cols) >= kInt32) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    return CLEF_OK;
+}
+
+int64_t codes_bytes(const clef_fp4& q) { return q.rows * fp4_code_stride(q.cols); }
+int64_t scales_bytes(const clef_fp4& q) {
+    return fp4_row_groups(q.rows) * fp4_kgroups(q.format, q.cols) * kFp4ScaleGroup;
+}
+
+int check_matrix(const clef_fp4* q) {
+    if (!q) return CLEF_ERR_INVALID_ARGUMENT;
+    const int st = check_size(q->format, q->rows, q->cols);
+    if (st != CLEF_OK) return st;
+    if (!q->codes || !q->scales || misaligned(q->codes, 256) || misaligned(q->scales, 256) ||
+        misaligned(q->row_scale, 4) || (q->format == CLEF_NVFP4 && !q->row_scale))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    return CLEF_OK;
+}
+
+Run codes_run(const clef_fp4& q) { return Run(q.codes, codes_bytes(q)); }
+Run scales_run(const clef_fp4& q) { return Run(q.scales, scales_bytes(q)); }
+Run row_scale_run(const clef_fp4& q) { return Run(q.format == CLEF_NVFP4 ? q.row_scale : nullptr, int64_t(q.rows) * 4); }
+
+// Rows of `cols` elements at `stride`: aligned to the element, and offsets that 64 bits hold.
+bool bad_rows(const void* p, int dtype, int64_t stride, int64_t least) {
+    return !p || misaligned(p, uintptr_t(size_of(dtype))) || stride < least || stride > (int64_t(1) << 31);
+}
+
+}  // namespace
+
+extern "C" {
+
+int clef_fp4_size(int32_t format, int32_t rows, int32_t cols, size_t* codes, size_t* scales) {
+    if (!codes || !scales) return CLEF_ERR_INVALID_ARGUMENT;
+    const int st = check_size(format, rows, cols);
+    if (st != CLEF_OK) return st;
+    const clef_fp4 q{nullptr, nullptr, nullptr, rows, cols, format};
+    *codes = size_t(codes_bytes(q));
+    *scales = size_t(scales_bytes(q));
+    return CLEF_OK;
+}
+
+int clef_fp4_quantize(const clef_fp4* q, int32_t dtype, const void* x, int64_t row_stride, float* mean, float* rstd,
+                      float* sums, void* stream) {
+    const int st = check_matrix(q);
+    if (st != CLEF_OK) return st;
+    if (bad_type(dtype) || bad_rows(x, dtype, row_stride, 0) || !mean != !rstd || misaligned(mean, 4) ||
+        misaligned(rstd, 4) || misaligned(sums, 4))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    const int64_t each = int64_t(q->rows) * 4;
+    const Run out[] = {codes_run(*q), scales_run(*q), row_scale_run(*q), Run(mean, each), Run(rstd, each), Run(sums, each)};
+    const Run in = rows_run(x, q->rows, row_stride, q->cols, size_of(dtype));
+    for (int i = 0; i < 6; ++i) {
+        if (out[i].meets(in)) return CLEF_ERR_INVALID_ARGUMENT;
+        for (int j = 0; j < i; ++j)
+            if (out[i].meets(out[j])) return CLEF_ERR_INVALID_ARGUMENT;
+    }
+    const Fp4QuantizeArgs a{x, row_stride, static_cast<uint8_t*>(q->codes), static_cast<uint8_t*>(q->scales),
+                            q->row_scale, mean, rstd, sums, q->rows, q->cols};
+    return launch_fp4_quantize(a, q->format, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
+                                                                                                      : CLEF_ERR_CUDA;
+}
+
+int clef_fp4_dequantize(const clef_fp4* q, int32_t dtype, void* out, int64_t row_stride, void* stream) {
+    const int st = check_matrix(q);
+    if (st != CLEF_OK) return st;
+    if (bad_type(dtype) || bad_rows(out, dtype, row_stride, q->cols)) return CLEF_ERR_INVALID_ARGUMENT;
+    const Run to = rows_run(out, q->rows, row_stride, q->cols, size_of(dtype));
+    if (to.meets(codes_run(*q)) || to.meets(scales_run(*q)) || to.meets(row_scale_run(*q)))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    const Fp4DequantizeArgs a{static_cast<const uint8_t*>(q->codes), static_cast<const uint8_t*>(q->scales),
+                              q->row_scale, out, row_stride, q->rows, q->cols};
+    return launch_fp4_dequantize(a, q->format, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
+                                                                                                        : CLEF_ERR_CUDA;
+}
+
+int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, const float* mean, const float* rstd,
+                     const float* sums, int32_t dtype, void* out, int64_t row_stride, int32_t* flags, void* stream) {
+    int st = check_matrix(x);
+    if (st == CLEF_OK) st = check_matrix(w);
+    if (st != CLEF_OK) return st;
+    if (x->format != w->format || x->cols != w->cols || bad_type(dtype) || bad_rows(out, dtype, row_stride, w->rows) ||
+        !mean != !rstd || !mean != !sums || !flags)
+        return CLEF_ERR_INVALID_ARGUMENT;
+    for (const void* p : {static_cast<const void*>(bias), static_cast<const void*>(mean), static_cast<const void*>(rstd),
+                          static_cast<const void*>(sums), static_cast<const void*>(flags)})
+        if (misaligned(p, 4)) return CLEF_ERR_INVALID_ARGUMENT;
+    // output tiles are counted in 32 bits
+    if ((int64_t(x->rows) + 31) / 32 * ((int64_t(w->rows) + 127) / 128) >= kInt32 / 16) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    const int64_t m4 = int64_t(x->rows) * 4, n4 = int64_t(w->rows) * 4;
+    const Run to = rows_run(out, x->rows, row_stride, w->rows, size_of(dtype));
+    for (const Run& r : {codes_run(*x), scales_run(*x), row_scale_run(*x), codes_run(*w), scales_run(*w),
+                         row_scale_run(*w), Run(bias, n4), Run(mean, m4), Run(rstd, m4), Run(sums, n4), Run(flags, 4)})
+        if (to.meets(r)) return CLEF_ERR_INVALID_ARGUMENT;
+    Fp4ProductArgs a{};
+    a.x_scale = x->format == CLEF_NVFP4 ? x->row_scale : nullptr;
+    a.w_scale = w->format == CLEF_NVFP4 ? w->row_scale : nullptr;
+    a.bias = bias;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.sums = sums;
+    a.out = out;
+    a.ldo = row_stride;
+    a.flags = flags;
+    a.M = x->rows;
+    a.N = w->rows;
+    a.k64 = (x->cols + 63) / 64;
+    a.kgroups = fp4_kgroups(x->format, x->cols);
+    a.splits = 1;
+    return launch_fp4_product(*x, *w, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
+                                                                                                  : CLEF_ERR_CUDA;
+}
+
+}  // extern "C"

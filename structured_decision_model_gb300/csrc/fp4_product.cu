@@ -1,0 +1,411 @@
+// Products of microscaled 4-bit matrices on the 5th-generation tensor cores
+// (tcgen05.mma kind::mxf4nvf4, block-scaled): y = x w^T with fp32 sums in TMEM, the blocks'
+// scales applied by the tensor cores, the rows' scales, the bias and the LayerNorm fold in
+// the epilogue.
+//
+// w's rows are the MMA's M side (TMEM lanes) and x's rows its N side (columns): a thread of
+// the epilogue then holds one column of the output, with its scale, bias and sum in
+// registers, and a warp stores 32 neighbouring values of an output row, whatever the
+// output's width, stride and alignment are.
+//
+// A K tile is 256 columns: 128 bytes of codes a row (one 128-byte swizzle atom, four MMAs of
+// 64 columns) and 2 (mxfp4) or 4 (nvfp4) 512-byte groups of scales for every 128 rows,
+// which tcgen05.cp spreads over 4 TMEM columns each.  The tensor cores take the copies and
+// the products of one thread in order, so one set of scale columns serves every K tile.
+//
+// Every wait is bounded: on a timeout the CTA sets the timeout flag, waits (bounded) for its
+// own copies and MMAs in flight, frees TMEM and returns.
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp4.h"
+#include "kernels.h"
+#include "per_device.h"
+
+namespace clef {
+
+namespace {
+
+constexpr int kAtomBytes = 128;             // codes of one row of a K tile
+constexpr int kWRows = 128;                 // rows of w in a CTA's tile
+constexpr int kWBytes = kWRows * kAtomBytes;
+
+constexpr int groups_of(int fmt) { return fmt == CLEF_MXFP4 ? 2 : 4; }  // scale groups of a K tile
+
+// Descriptor of the 32 x 16-byte rows of a scale group: four 8-row core matrices, 128 bytes
+// apart, no swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3FFFu);
+    d |= uint64_t(128 >> 4) << 32;  // stride byte offset
+    d |= uint64_t(1) << 46;         // descriptor version
+    return d;
+}
+
+// Instruction descriptor: e2m1 A and B, K-major, M x N tile, K = 64; scales e8m0 or e4m3,
+// `part` the byte of a scale word that the MMA's scales start at (mxfp4: 0 or 2).
+__host__ __device__ constexpr uint32_t idesc_fp4(int fmt, int M, int N, int part) {
+    return (uint32_t(part) << 4)                              // B's scales
+           | (1u << 7)                                        // A format e2m1
+           | (1u << 10)                                       // B format e2m1
+           | (uint32_t(N >> 3) << 17)                         // N / 8
+           | ((fmt == CLEF_MXFP4 ? 1u : 0u) << 23)            // scale format: e8m0 or e4m3
+           | (uint32_t(M >> 4) << 24)                         // M / 16
+           | (uint32_t(part) << 29);                          // A's scales
+}
+
+template <int FMT, bool PAIR>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        uint32_t accumulate) {
+#define CLEF_FP4_MMA(GROUP, VEC)                                                                        \
+    asm volatile(                                                                                       \
+        "{\n\t.reg .pred p;\n\t"                                                                        \
+        "setp.ne.b32 p, %6, 0;\n\t"                                                                     \
+        "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                   \
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                              \
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)                                   \
+        : "memory")
+    if constexpr (FMT == CLEF_MXFP4) {
+        if constexpr (PAIR) CLEF_FP4_MMA("2", "2X");
+        else CLEF_FP4_MMA("1", "2X");
+    } else {
+        if constexpr (PAIR) CLEF_FP4_MMA("2", "4X");
+        else CLEF_FP4_MMA("1", "4X");
+    }
+#undef CLEF_FP4_MMA
+}
+
+// 32 rows x 16 bytes of shared memory to 4 TMEM columns, repeated in all four lane quarters.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <int OUT>
+__device__ __forceinline__ void store_value(void* out, int64_t at, float v) {
+    if constexpr (OUT == CLEF_FP32) static_cast<float*>(out)[at] = v;
+    else if constexpr (OUT == CLEF_BF16) static_cast<uint16_t*>(out)[at] = float_to_bf16(v);
+    else static_cast<uint16_t*>(out)[at] = __half_as_ushort(__float2half_rn(v));
+}
+
+// What an output column (a row of w) brings: y = acc * scale * f[m] + (h[m] * sum + bias).
+struct ColumnTerms {
+    float scale, sum, bias;
+};
+__device__ __forceinline__ ColumnTerms column_terms(const Fp4ProductArgs& a, int n) {
+    ColumnTerms t{1.f, 0.f, 0.f};
+    if (n < a.N) {
+        if (a.w_scale) t.scale = a.w_scale[n];
+        if (a.sums) t.sum = a.sums[n];
+        if (a.bias) t.bias = a.bias[n];
+    }
+    return t;
+}
+
+// What an output row (a row of x) brings: f and h of the formula above.
+__device__ __forceinline__ float2 row_terms(const Fp4ProductArgs& a, int m) {
+    float2 t = make_float2(1.f, 0.f);
+    if (m < a.M) {
+        if (a.x_scale) t.x = a.x_scale[m];
+        if (a.rstd) {
+            const float rs = a.rstd[m];
+            t.x *= rs;
+            t.y = -a.mean[m] * rs;
+        }
+    }
+    return t;
+}
+
+__device__ __forceinline__ float finish(float acc, const ColumnTerms& c, float2 r) {
+    return fmaf(acc * c.scale, r.x, fmaf(r.y, c.sum, c.bias));
+}
+
+// --------------------------------------------------------- one CTA, one tile
+// 128 rows of w x BN rows of x.  Few rows of x leave few tiles, so the K range of a tile is
+// cut among the CTAs of a cluster, which stage their fp32 tiles in their own shared memory
+// and add them in order through distributed shared memory.
+template <int FMT, int BN>
+struct TileCfg {
+    static constexpr int GROUPS = groups_of(FMT);
+    static constexpr int X_BYTES = BN * kAtomBytes;
+    static constexpr int S_BYTES = GROUPS * kFp4ScaleGroup;  // of 128 rows of one side
+    static constexpr int STAGE = kWBytes + X_BYTES + 2 * S_BYTES;
+    static constexpr int STAGES = BN == 32 ? 4 : 3;  // two CTAs an SM
+    static constexpr int SMEM = STAGES * STAGE + 1024 /*align*/ + BN * 8 /*row terms*/ + 128 /*barriers*/;
+    static constexpr uint32_t S_COLS = 4 * GROUPS;  // TMEM columns of one side's scales
+    static constexpr uint32_t TMEM_COLS = BN == 32 ? 64 : 2 * BN;
+    static constexpr int LD = kWRows + 4;  // row stride (floats) of a staged tile [BN][128]
+    static_assert(BN + 2 * S_COLS <= TMEM_COLS, "accumulator and scales fit");
+    static_assert(BN * LD * 4 <= STAGES * STAGE, "a staged tile fits the operand stages");
+    static_assert(STAGE % 1024 == 0 && X_BYTES % 1024 == 0, "swizzle atoms start on 1024 bytes");
+};
+constexpr int kTileThreads = 192;  // TMA, MMA, four epilogue warps
+constexpr int kMaxSplits = 8;
+
+template <int FMT, int BN, int OUT>
+__global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                                const __grid_constant__ CUtensorMap tmX,
+                                                                const __grid_constant__ CUtensorMap tmSW,
+                                                                const __grid_constant__ CUtensorMap tmSX,
+                                                                const Fp4ProductArgs args) {
+    using C = TileCfg<FMT, BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float2* terms = reinterpret_cast<float2*>(smem + C::STAGES * C::STAGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(terms + BN);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* done = empty + C::STAGES;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmSW);
+        prefetch_tensormap(&tmSX);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int S = args.splits;
+    const int sp = int(blockIdx.x) % S, tile = int(blockIdx.x) / S;
+    const int n_wt = (args.N + kWRows - 1) / kWRows;
+    const int wt = tile % n_wt, xt = tile / n_wt;  // w's tiles next to each other share x's rows
+    const int ktiles = (args.k64 + 3) / 4;
+    const int kt0 = int(int64_t(sp) * ktiles / S), kt1 = int(int64_t(sp + 1) * ktiles / S);
+    griddep_wait();
+    griddep_launch();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int i = 0;
+            for (int kt = kt0; kt < kt1; ++kt, ++i) {
+                const int s = i % C::STAGES;
+                if (!mbar_wait_bounded(&empty[s], uint32_t(i / C::STAGES & 1) ^ 1u, abort_flag, args.flags)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* st = smem + s * C::STAGE;
+                mbar_arrive_expect_tx(&full[s], C::STAGE);
+                tma_load_2d(st, &tmW, kt * kAtomBytes, wt * kWRows, &full[s]);
+                tma_load_2d(st + kWBytes, &tmX, kt * kAtomBytes, xt * BN, &full[s]);
+                tma_load_2d(st + kWBytes + C::X_BYTES, &tmSW, 0, wt * args.kgroups + kt * C::GROUPS, &full[s]);
+                // x's scales of the 128-row group that the tile lies in (tiles of fewer rows: the first)
+                tma_load_2d(st + kWBytes + C::X_BYTES + C::S_BYTES, &tmSX, 0,
+                            xt * BN / kFp4RowGroup * args.kgroups + kt * C::GROUPS, &full[s]);
+            }
+            if (!ok) {  // let every copy that was asked for land before the CTA goes
+                for (int j = i < C::STAGES ? 0 : i - C::STAGES; j < i; ++j)
+                    mbar_wait_bounded(&full[j % C::STAGES], uint32_t(j / C::STAGES & 1), nullptr, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            int i = 0;
+            for (int kt = kt0; kt < kt1; ++kt, ++i) {
+                const int s = i % C::STAGES;
+                if (!mbar_wait_bounded(&full[s], uint32_t(i / C::STAGES & 1), abort_flag, args.flags)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * C::STAGE);
+                const uint32_t sw = tmem + BN, sx = sw + C::S_COLS;
+#pragma unroll
+                for (int g = 0; g < C::GROUPS; ++g) {
+                    copy_scales<false>(sw + 4 * g, scale_desc(st + kWBytes + C::X_BYTES + g * kFp4ScaleGroup));
+                    copy_scales<false>(sx + 4 * g, scale_desc(st + kWBytes + C::X_BYTES + C::S_BYTES + g * kFp4ScaleGroup));
+                }
+                const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + kWBytes);
+                const int nk = min(4, args.k64 - 4 * kt);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= nk) break;
+                    constexpr bool MX = FMT == CLEF_MXFP4;
+                    const uint32_t g = 4 * (MX ? k / 2 : k);  // mxfp4: a word holds two MMAs' scales
+                    mma_fp4<FMT, false>(tmem, da + uint64_t(2 * k), db + uint64_t(2 * k),
+                                        idesc_fp4(FMT, kWRows, BN, MX ? (k & 1) * 2 : 0), sw + g, sx + g,
+                                        i > 0 || k > 0 ? 1u : 0u);
+                }
+                tc_commit(&empty[s]);
+            }
+            tc_commit(done);
+            // on every path: what was issued completes before TMEM is freed
+            if (!mbar_wait_bounded(done, 0, nullptr, args.flags) || !ok) *abort_flag = 1;
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3;  // TMEM lanes that this warp may read
+        const int row = quarter * 32 + lane, n = wt * kWRows + row;
+        const ColumnTerms col = column_terms(args, n);
+        for (int j = int(threadIdx.x) - 64; j < BN; j += 128) terms[j] = row_terms(args, xt * BN + j);
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // the epilogue's warps
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait_bounded(done, 0, abort_flag, args.flags) && !*abort_flag ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        tc_fence_after();
+        const int rows = min(BN, args.M - xt * BN);
+        if (ok && S == 1) {
+#pragma unroll 1
+            for (int c = 0; c < rows; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
+                tmem_ld_wait();
+                if (n < args.N) {
+                    int64_t at = int64_t(xt * BN + c) * args.ldo + n;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, at += args.ldo)
+                        if (c + j < rows) store_value<OUT>(args.out, at, finish(__uint_as_float(r[j]), col, terms[c + j]));
+                }
+            }
+        } else if (ok) {  // the operand stages are idle: every MMA that read them is done
+            float* red = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+            for (int c = 0; c < rows; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) red[(c + j) * C::LD + row] = __uint_as_float(r[j]);
+            }
+        }
+        tc_fence_before();
+    }
+    if (S > 1) {
+        cluster_sync();  // every thread of every CTA of the cluster, on every path
+        if (warp >= 2 && !*abort_flag) {
+            const int row = (warp & 3) * 32 + lane, n = wt * kWRows + row;
+            const ColumnTerms col = column_terms(args, n);
+            const int rows = min(BN, args.M - xt * BN);
+            const uint32_t red0 = smem_u32(smem);
+            for (int j = sp; j < rows; j += S) {  // CTA sp finishes rows sp, sp + S, ...
+                const uint32_t at = red0 + uint32_t((j * C::LD + row) * 4);
+                float v[kMaxSplits];
+#pragma unroll
+                for (int i = 0; i < kMaxSplits; ++i) {
+                    if (i < S)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[i]) : "r"(cluster_map(at, uint32_t(i))));
+                }
+                float acc = 0.f;
+#pragma unroll
+                for (int i = 0; i < kMaxSplits; ++i)
+                    if (i < S) acc += v[i];
+                if (n < args.N)
+                    store_value<OUT>(args.out, int64_t(xt * BN + j) * args.ldo + n, finish(acc, col, terms[j]));
+            }
+        }
+        cluster_sync();  // no CTA leaves while another may still read its shared memory
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// ----------------------------------------------------------------- host side
+
+// Codes [rows][stride bytes], boxes of 128 bytes x `box` rows, 128-byte swizzle; what lies
+// outside reads as zeros.
+bool codes_map(CUtensorMap* map, const clef_fp4& q, int box) {
+    const uint64_t stride = uint64_t(fp4_code_stride(q.cols));
+    return make_tma_2d(map, q.codes, 1, stride, uint64_t(q.rows), stride, kAtomBytes, uint32_t(box), true);
+}
+
+// Scale groups [groups][512 bytes, as words], boxes of the groups of one K tile.
+bool scales_map(CUtensorMap* map, const clef_fp4& q) {
+    const uint64_t groups = uint64_t(fp4_row_groups(q.rows)) * uint64_t(fp4_kgroups(q.format, q.cols));
+    return make_tma_2d(map, q.scales, 4, kFp4ScaleGroup / 4, groups, kFp4ScaleGroup, kFp4ScaleGroup / 4,
+                       uint32_t(groups_of(q.format)), false);
+}
+
+// The kernel's shared memory, opted into once for every device.
+template <typename K>
+cudaError_t set_up(PerDevice<int>* ready, K kernel, int bytes) {
+    int device = 0, set = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return cudaError_t(ready->get(device, &set, [&](int* v) {
+        *v = 1;
+        return int(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    }));
+}
+
+template <typename K>
+cudaError_t launch_clusters(K kernel, int grid, int cluster, int threads, size_t smem, cudaStream_t s,
+                            const CUtensorMap (&maps)[4], const Fp4ProductArgs& a) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return counted(cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], a));
+}
+
+template <int FMT, int BN, int OUT>
+cudaError_t launch_tile(const clef_fp4& x, const clef_fp4& w, Fp4ProductArgs a, cudaStream_t s) {
+    using C = TileCfg<FMT, BN>;
+    static PerDevice<int> ready;
+    const cudaError_t e = set_up(&ready, fp4_tile_kernel<FMT, BN, OUT>, C::SMEM);
+    if (e != cudaSuccess) return e;
+    CUtensorMap maps[4];
+    if (!codes_map(&maps[0], w, kWRows) || !codes_map(&maps[1], x, BN) || !scales_map(&maps[2], w) ||
+        !scales_map(&maps[3], x))
+        return cudaErrorInvalidValue;
+    const int tiles = (a.N + kWRows - 1) / kWRows * ((a.M + BN - 1) / BN);
+    // as many K parts as fill the SMs twice, each with a K tile at least
+    a.splits = 1;
+    const int ktiles = fp4_ktiles(x.cols);
+    while (a.splits < kMaxSplits && 2 * a.splits <= ktiles && tiles * a.splits * 2 <= 2 * num_sms()) a.splits *= 2;
+    return launch_clusters(fp4_tile_kernel<FMT, BN, OUT>, tiles * a.splits, a.splits, kTileThreads, C::SMEM, s, maps, a);
+}
+
+template <int FMT, int OUT>
+cudaError_t launch_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, cudaStream_t s) {
+    if (a.M <= 32) return launch_tile<FMT, 32, OUT>(x, w, a, s);
+    if (a.M <= 64) return launch_tile<FMT, 64, OUT>(x, w, a, s);
+    return launch_tile<FMT, 128, OUT>(x, w, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, int dtype,
+                               cudaStream_t s) {
+    if (x.format == CLEF_MXFP4) {
+        if (dtype == CLEF_BF16) return launch_product<CLEF_MXFP4, CLEF_BF16>(x, w, a, s);
+        if (dtype == CLEF_FP16) return launch_product<CLEF_MXFP4, CLEF_FP16>(x, w, a, s);
+        return launch_product<CLEF_MXFP4, CLEF_FP32>(x, w, a, s);
+    }
+    if (dtype == CLEF_BF16) return launch_product<CLEF_NVFP4, CLEF_BF16>(x, w, a, s);
+    if (dtype == CLEF_FP16) return launch_product<CLEF_NVFP4, CLEF_FP16>(x, w, a, s);
+    return launch_product<CLEF_NVFP4, CLEF_FP32>(x, w, a, s);
+}
+
+}  // namespace clef

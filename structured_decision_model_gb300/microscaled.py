@@ -1,0 +1,223 @@
+"""PyTorch-side helper around the microscaled 4-bit operators: device buffers and streams only.
+
+    w = Fp4Linear(weight, bias)                  # weights laid out once, in 4 bits
+    y = w(x)                                     # rows quantised and multiplied
+    y, mean, rstd = w.normalized(x)              # the layer behind a LayerNorm whose weight it holds
+
+and by single steps: ``quantize`` (an ``Fp4Matrix``), ``Fp4Matrix.dequantize`` and ``product``.
+All arithmetic happens in libclef_head.so, on torch's current stream.  Nothing here waits
+for the GPU; ``device_status`` does, and reports what the kernels met.  A value is kept as
+the nearest of 16 numbers times its block's scale: "mxfp4" (blocks of 32, a power of two)
+or "nvfp4" (blocks of 16, three bits behind the point, and a power of two for each row).
+Nothing here passes gradients on: tensors that require one are refused while grad mode is on.
+"""
+from typing import Optional, Tuple
+
+import torch
+
+from . import binding as B
+from .memory import _DTYPES, _current_device, _overlap, _raw_stream, _refuse
+
+FORMATS = {"mxfp4": B.MXFP4, "nvfp4": B.NVFP4}
+BLOCK = {"mxfp4": 32, "nvfp4": 16}
+_FP32 = torch.float32
+
+
+def _sizes(format: int, rows: int, cols: int) -> Tuple[int, int]:
+    """Bytes of codes and scales (clef_fp4_size, without a call into the library)."""
+    return rows * ((cols + 31) // 32 * 16), (rows + 127) // 128 * ((cols + 255) // 256 * (2048 if format else 1024))
+
+
+def _up(n: int) -> int:
+    return (n + 255) // 256 * 256
+
+
+class Fp4Matrix:
+    """Rows kept in 4 bits: codes, block scales and row scales, one after the other in ``data``.
+
+    ``data`` (uint8, contiguous, of ``size_bytes``) may be a buffer of the caller, taken as it is: what an earlier
+    matrix of the same shape and format held, for instance.  ``mean``, ``rstd`` and ``sums`` (fp32 [rows])
+    are there where ``quantize`` was asked for them.
+    """
+
+    __slots__ = ("rows", "cols", "format", "data", "struct", "device", "mean", "rstd", "sums", "_flags", "_index")
+
+    def __init__(self, rows: int, cols: int, format: str = "nvfp4", device="cuda", data: Optional[torch.Tensor] = None):
+        code = FORMATS.get(format)
+        if code is None:
+            _refuse(f"format: one of {sorted(FORMATS)}")
+        if not 1 <= rows < 2 ** 31 - 256 or not 1 <= cols <= B.FP4_MAX_COLS:
+            _refuse(f"an Fp4Matrix has 1 to 2^31 - 257 rows of 1 to {B.FP4_MAX_COLS} values")
+        codes, scales = _sizes(code, rows, cols)
+        at = _up(codes)
+        size = at + _up(scales) + (4 * rows if code == B.NVFP4 else 0)
+        if data is None:
+            data = torch.empty(size, dtype=torch.uint8, device=device)
+        elif data.dtype != torch.uint8 or data.dim() != 1 or data.numel() != size or not data.is_contiguous() or \
+                data.data_ptr() % 256:
+            _refuse("Fp4Matrix: data is not a contiguous uint8 vector of size_bytes on 256 bytes")
+        if data.device.type != "cuda":
+            _refuse("Fp4Matrix: data is not on a GPU")
+        base = data.data_ptr()
+        self.rows, self.cols, self.format, self.data = rows, cols, format, data
+        self.struct = B.ClefFp4(base, base + at, base + at + _up(scales) if code == B.NVFP4 else None, rows, cols, code)
+        self.device = data.device
+        self._index = data.device.index
+        self.mean = self.rstd = self.sums = self._flags = None
+
+    @property
+    def size_bytes(self) -> int:
+        return self.data.numel()
+
+    @property
+    def flags(self) -> torch.Tensor:
+        """What the products with these weights report (int32 [1]); made at the first one."""
+        if self._flags is None:
+            self._flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+        return self._flags
+
+    def dequantize(self, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """What the rows stand for, [rows, cols] in ``dtype`` (bf16, fp16 or fp32), rounded once."""
+        out = _out(out, self.rows, self.cols, dtype, self.device)
+        if _overlap(out, self.data):
+            _refuse("out lies apart from what is read")
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.dequantize(dtype, out)
+        B.clef_fp4_dequantize(self.struct, _DTYPES[dtype], out.data_ptr(), out.stride(0), _raw_stream(self._index))
+        return out
+
+    def device_status(self) -> int:
+        """Waits for the current stream, reads and clears what the products with these weights reported."""
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.device_status()
+        return B.clef_cache_status(self.flags.data_ptr(), _raw_stream(self._index))
+
+
+def _out(out, rows, cols, dtype, device):
+    if dtype not in _DTYPES:
+        _refuse("outputs: bf16, fp16 or fp32")
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    if out.dtype != dtype or out.shape != (rows, cols) or out.device != device or \
+            (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
+        _refuse(f"out: {dtype} [{rows}, {cols}], values of a row contiguous, rows apart, on {device}")
+    if out.requires_grad and torch.is_grad_enabled():
+        _refuse("out requires a gradient")
+    return out
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def quantize(x: torch.Tensor, format: str = "nvfp4", stats: bool = False, sums: bool = False,
+             out: Optional[Fp4Matrix] = None) -> Fp4Matrix:
+    """Rows x [rows, cols] (bf16, fp16 or fp32, any row stride, values contiguous) in 4 bits.
+
+    ``stats``: also the rows' ``mean`` and ``rstd`` = 1 / sqrt(variance + 1e-5); ``sums``: also the
+    sums of what the rows stand for once kept."""
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or x.device.type != "cuda":
+        _refuse("x: bf16, fp16 or fp32 [rows, cols], values of a row contiguous, on a GPU")
+    if x.requires_grad and torch.is_grad_enabled():
+        _refuse("x requires a gradient, which 4-bit rows do not pass on")
+    rows, cols = x.shape
+    if out is None:
+        out = Fp4Matrix(rows, cols, format, x.device)
+    elif (out.rows, out.cols, out.format, out.device) != (rows, cols, format, x.device):
+        _refuse("out: an Fp4Matrix of x's shape and device and of the format")
+    if _current_device() != out._index:
+        with torch.cuda.device(out._index):
+            return quantize(x, format, stats, sums, out)
+    out.mean = out.rstd = out.sums = None
+    mean = rstd = total = None
+    if stats:
+        out.mean, out.rstd = torch.empty((2, rows), dtype=_FP32, device=x.device).unbind(0)
+        mean, rstd = out.mean.data_ptr(), out.rstd.data_ptr()
+    if sums:
+        out.sums = torch.empty(rows, dtype=_FP32, device=x.device)
+        total = out.sums.data_ptr()
+    B.clef_fp4_quantize(out.struct, dtype, x.data_ptr(), _row_stride(x), mean, rstd, total, _raw_stream(out._index))
+    return out
+
+
+def product(x: Fp4Matrix, w: Fp4Matrix, bias: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
+            normalized: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x w^T + bias: [x.rows, w.rows] in ``dtype`` (bf16, fp16 or fp32), sums in fp32, rounded once.
+
+    ``normalized``: x's rows less their means and times their rstd (x quantised with ``stats``, w
+    with ``sums``).  ``bias``: fp32 [w.rows]."""
+    if x.format != w.format or x.cols != w.cols or x.device != w.device:
+        _refuse("product: one format, number of columns and device")
+    if bias is not None and (bias.dtype is not _FP32 or bias.shape != (w.rows,) or not bias.is_contiguous() or
+                             bias.device != w.device or (bias.requires_grad and torch.is_grad_enabled())):
+        _refuse("bias: contiguous fp32 [w.rows], without a gradient, on the matrices' device")
+    if normalized and (x.mean is None or w.sums is None):
+        _refuse("normalized: x quantised with stats=True, w with sums=True")
+    given = out is not None
+    out = _out(out, x.rows, w.rows, dtype, w.device)
+    if given and any(_overlap(out, t) for t in (x.data, w.data, bias, x.mean, x.rstd, w.sums) if t is not None):
+        _refuse("out lies apart from what is read")
+    if _current_device() != w._index:
+        with torch.cuda.device(w._index):
+            return product(x, w, bias, dtype, normalized, out)
+    B.clef_fp4_product(x.struct, w.struct, None if bias is None else bias.data_ptr(),
+                       x.mean.data_ptr() if normalized else None, x.rstd.data_ptr() if normalized else None,
+                       w.sums.data_ptr() if normalized else None, _DTYPES[dtype], out.data_ptr(), max(_row_stride(out), w.rows),
+                       w.flags.data_ptr(), _raw_stream(w._index))
+    return out
+
+
+class Fp4Linear:
+    """A linear layer of 4-bit weights: its inputs are quantised row by row as they come.
+
+    ``weight`` [outs, cols] (bf16, fp16 or fp32; or an ``Fp4Matrix``, quantised with ``sums`` where
+    ``normalized`` is to be called) and ``bias`` [outs] are laid out once.  For ``normalized`` the weight
+    holds the LayerNorm's weight (its columns times it) and the bias what the LayerNorm's bias brings."""
+
+    def __init__(self, weight, bias: Optional[torch.Tensor] = None, format: str = "nvfp4"):
+        if not isinstance(weight, Fp4Matrix):
+            weight = quantize(weight.detach(), format, sums=True)
+        elif weight.format != format:
+            _refuse("weight: an Fp4Matrix of the format")
+        self.weight, self.format = weight, format
+        self.cols, self.outs = weight.cols, weight.rows
+        if bias is not None:
+            if bias.shape != (self.outs,) or bias.device != weight.device:
+                _refuse("bias: [outs] on the weight's device")
+            bias = bias.detach().to(_FP32).contiguous()
+        self.bias = bias
+        weight.flags  # made here, outside of any later capture
+
+    def _run(self, x, dtype, normalized):
+        dtype = x.dtype if dtype is None else dtype
+        if x.dim() < 1 or x.shape[-1] != self.cols or x.device != self.weight.device:
+            _refuse(f"x: [..., {self.cols}] on the weight's device")
+        lead = x.shape[:-1]
+        rows = x if x.dim() == 2 else x.reshape(-1, self.cols)
+        if rows.shape[0] == 0:
+            if dtype not in _DTYPES or x.dtype not in _DTYPES:
+                _refuse("inputs and outputs: bf16, fp16 or fp32")
+            q, y = None, torch.empty((0, self.outs), dtype=dtype, device=x.device)
+        else:
+            q = quantize(rows, self.format, stats=normalized)
+            y = product(q, self.weight, self.bias, dtype, normalized)
+        return q, y if x.dim() == 2 else y.view(*lead, self.outs)
+
+    def __call__(self, x: torch.Tensor, dtype=None) -> torch.Tensor:
+        """x [..., cols] through the layer: [..., outs] in ``dtype`` (x's own by default)."""
+        return self._run(x, dtype, False)[1]
+
+    def normalized(self, x: torch.Tensor, dtype=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """The layer behind a LayerNorm: outputs, and the rows' mean and 1 / sqrt(variance + 1e-5) (fp32 [...])."""
+        q, y = self._run(x, dtype, True)
+        if q is None:
+            mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=_FP32, device=x.device).unbind(0)
+            return y, mean, rstd
+        return y, q.mean.view(x.shape[:-1]), q.rstd.view(x.shape[:-1])
+
+    def device_status(self) -> int:
+        """Waits for the current stream, reads and clears what the layer's products reported."""
+        return self.weight.device_status()

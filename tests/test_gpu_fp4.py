@@ -1,0 +1,180 @@
+"""The microscaled 4-bit operators on the GPU against their definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from fp4_support import BLOCK, EPS, kept, stored
+from structured_decision_model_gb300.binding import ClefError
+from structured_decision_model_gb300.microscaled import Fp4Linear, Fp4Matrix, product, quantize
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+FORMATS = ["mxfp4", "nvfp4"]
+
+
+def rows_of(rows, cols, dtype, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(spread * torch.randn(rows, 1, generator=g))
+    x *= torch.exp(spread * torch.randn(rows, cols, generator=g))
+    return x.to(dtype).cuda()
+
+
+def check_kept(x, form, m):
+    codes, byte, r, values = kept(x.double().cpu().numpy(), form)
+    got, scales, row_scale = stored(m)
+    cols, blocks = x.shape[1], byte.shape[1]
+    np.testing.assert_array_equal(scales[:, :blocks], byte)
+    assert not scales[:, blocks:].any()
+    # a value of zero may carry either sign
+    same = (got[:, :cols] == codes) | ((got[:, :cols] & 7) + (codes & 7) == 0)
+    assert same.all(), np.argwhere(~same)[:5]
+    assert not got[:, cols:].any()
+    if form == "nvfp4":
+        np.testing.assert_array_equal(row_scale, r.astype(np.float32))
+    return values
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 16), (3, 33), (130, 256), (5, 300), (64, 1111), (300, 4096), (7, 8192),
+                                       (2, 16384), (1, 5121)])
+def test_rows_are_kept_exactly(form, dtype, rows, cols):
+    x = rows_of(rows, cols, TYPES[dtype], rows * 7 + cols)
+    m = quantize(x, form)
+    values = check_kept(x, form, m)
+    for out in TYPES.values():
+        want = torch.from_numpy(values).to(torch.float32).to(out)  # fp32 holds every value
+        assert torch.equal(m.dequantize(out).cpu(), want)
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quotients_next_to_the_borders(form, dtype):
+    """Every midpoint times scales of every size, and the numbers of the type next to it on both sides."""
+    t = TYPES[dtype]
+    n = BLOCK[form]
+    out = []
+    for top in (6.0, 5.25, 4.125, 6.75, 3.1875, 7.5):
+        for power in (-9, -3, 0, 5):
+            head = torch.tensor([top * 2.0 ** power], dtype=t)
+            scale = kept(head[None].double().numpy(), form)[3][0, 0]  # what the largest stands for
+            scale = scale / 6 if form == "nvfp4" else 2.0 ** np.floor(np.log2(top * 2.0 ** power)) / 4
+            mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64) * scale
+            mids = mids.to(t)
+            inf = torch.tensor(float("inf"), dtype=t)
+            near = torch.cat([mids, torch.nextafter(mids.cuda(), inf.cuda()).cpu() if t == torch.float32 else mids * (1 + 2.0 ** -7),
+                              torch.nextafter(mids.cuda(), -inf.cuda()).cpu() if t == torch.float32 else mids * (1 - 2.0 ** -7)])
+            for a in range(0, len(near), n - 1):
+                block = torch.zeros(n, dtype=t)
+                block[0] = head[0]
+                part = near[a:a + n - 1].clamp(max=float(head[0]))
+                block[1:1 + len(part)] = part
+                out.append(block)
+                out.append(-block)
+    x = torch.cat(out)
+    x = torch.nn.functional.pad(x, (0, -len(x) % (4 * n))).view(-1, 4 * n).cuda()
+    check_kept(x, form, quantize(x, form))
+
+
+@pytest.mark.parametrize("form", FORMATS)
+def test_sizes_at_the_ends_of_fp32(form):
+    x = torch.tensor([[1e-38, -3e-40, 0, 5e-39] * 16, [3e38, 1, 1e30, -2e38] * 16, [0.0] * 64, [1e-45, 0, -1e-44, 0] * 16,
+                      [-0.0] * 64, [2.0 ** 127, 2.0 ** 115, -2.0 ** 110, 2.0 ** 100] * 16], dtype=torch.float32, device="cuda")
+    check_kept(x, form, quantize(x, form))
+    y = x.bfloat16()
+    check_kept(y, form, quantize(y, form))
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_that_are_no_numbers_stay_in_their_block(form, dtype):
+    x = rows_of(5, 200, TYPES[dtype], 3)
+    x[0, 17], x[1, 40], x[1, 199], x[3, 0] = float("nan"), float("inf"), float("-inf"), float("nan")
+    m = quantize(x, form)
+    values = check_kept(x, form, m)
+    back = m.dequantize(torch.float32).cpu().double().numpy()
+    np.testing.assert_array_equal(back, values)
+    assert np.isnan(back[0]).sum() == BLOCK[form] and not np.isnan(back[2]).any() and not np.isnan(back[4]).any()
+
+
+def test_strided_and_unaligned_rows():
+    base = rows_of(40, 700, torch.bfloat16, 4)
+    for x in (base[:, 1:301], base[::3, :256], base[:, 8:264], base[:1].expand(6, 700)):
+        check_kept(x, "nvfp4", quantize(x, "nvfp4"))
+    m = quantize(base, "mxfp4")
+    wide = torch.full((40, 801), 7.0, dtype=torch.float16, device="cuda")
+    m.dequantize(torch.float16, wide[:, 3:703])
+    assert torch.equal(wide[:, 3:703], m.dequantize(torch.float16))
+    assert (wide[:, :3] == 7).all() and (wide[:, 703:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 33), (9, 1000), (300, 4096), (2, 16384)])
+def test_statistics_and_sums(dtype, rows, cols):
+    x = rows_of(rows, cols, TYPES[dtype], 5, spread=0.3) + 2.0
+    m = quantize(x, "nvfp4", stats=True, sums=True)
+    v = x.double()
+    mean = v.mean(1)
+    var = (v - mean[:, None]).square().mean(1)
+    size = v.abs().mean(1)
+    # fp32 sums in a tree of at most 2^5 terms in line and 10 levels: 42 roundings of 2^-24, of the sizes' mean
+    assert ((m.mean.double() - mean).abs() <= 42 * 2.0 ** -24 * size).all()
+    # the same for the variance (each term rounded three times), halved by the root, the root and the quotient
+    # rounded once each; the mean's own error enters squared
+    assert ((m.rstd.double() * (var + EPS).sqrt() - 1).abs() <= 30 * 2.0 ** -24).all()
+    kept_rows = m.dequantize(torch.float32).double()
+    assert ((m.sums.double() - kept_rows.sum(1)).abs() <= 42 * 2.0 ** -24 * kept_rows.abs().sum(1)).all()
+
+
+def check_product(x, w, form, out, bias=None, normalized=False, y=None):
+    """The product against 64 bits of what both sides stand for."""
+    a, b = (torch.from_numpy(kept(t.double().cpu().numpy(), form)[3]).cuda() for t in (x, w))
+    want = a @ b.T
+    room = a.abs() @ b.abs().T  # the sum of the terms' sizes
+    if normalized:
+        v = x.double()
+        mean = v.mean(1, keepdim=True)
+        rstd = ((v - mean).square().mean(1, keepdim=True) + EPS).rsqrt()
+        shift = mean * b.sum(1)
+        want = rstd * (want - shift)
+        room = rstd * (room + v.abs().mean(1, keepdim=True) * b.abs().sum(1))
+    if bias is not None:
+        want = want + bias.double()
+        room = room + bias.double().abs()
+    # sums in fp32 on the tensor cores, which may cut off instead of rounding: 2^-23 of the terms' sizes for each MMA
+    # of 64 columns; 50 roundings of 2^-24 for statistics, sums, factors and joined parts; the output's own
+    steps = -(-x.shape[1] // 64)
+    tol = room * (steps * 2.0 ** -23 + 50 * 2.0 ** -24) + want.abs() * torch.finfo(out).eps / 2
+    tol = tol + torch.finfo(out).tiny
+    off = (y.double() - want).abs()
+    assert (off <= tol).all(), (float((off / tol).max()), int((off > tol).sum()))
+
+
+SHAPES = [(1, 1, 1), (1, 128, 256), (3, 40, 32), (32, 256, 512), (33, 129, 300), (64, 512, 4096), (65, 700, 1000),
+          (128, 128, 64), (200, 384, 5000), (511, 1024, 1024), (1000, 777, 515)]
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_product(form, out, m, n, k):
+    x = rows_of(m, k, torch.bfloat16, m + n, 0.5)
+    w = rows_of(n, k, torch.bfloat16, m + k, 0.5)
+    bias = torch.randn(n, device="cuda") * 3
+    layer = Fp4Linear(w, bias, form)
+    y = layer(x, TYPES[out])
+    check_product(x, w, form, TYPES[out], bias, y=y)
+    assert layer.device_status() == 0
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_normalized_product(form, m, n, k):
+    x = rows_of(m, k, torch.float16, m + n, 0.3) + 0.5
+    w = rows_of(n, k, torch.bfloat16, m + k, 0.5)
+    layer = Fp4Linear(w, None, form)
+    y, mean, rstd = layer.normalized(x, torch.float32)
+    check_product(x, w, form, torch.float32, None, True, y)
+    m_ = quantize(x, form, stats=True)
+    assert torch.equal(m_.mean, mean) and torch.equal(m_.rstd, rstd)
