@@ -142,6 +142,7 @@ int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, co
     a.k64 = (x->cols + 63) / 64;
     a.kgroups = fp4_kgroups(x->format, x->cols);
     a.splits = 1;
+    a.paired = dtype != CLEF_FP32 && row_stride % 2 == 0 && w->rows % 2 == 0 && !misaligned(out, 4);
     return launch_fp4_product(*x, *w, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
                                                                                                   : CLEF_ERR_CUDA;
 }

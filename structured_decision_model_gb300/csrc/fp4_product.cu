@@ -123,6 +123,60 @@ __device__ __forceinline__ float finish(float acc, const ColumnTerms& c, float2 
     return fmaf(acc * c.scale, r.x, fmaf(r.y, c.sum, c.bias));
 }
 
+// A barrier of the four epilogue warps, behind which all of them know whether all may go on.
+__device__ __forceinline__ bool epilogue_agrees(int ok) {
+    int all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(ok)
+        : "memory");
+    return all != 0;
+}
+
+// 32 accumulator columns (rows m0 .. m0 + 31 of x; `rows` of them exist) of one TMEM lane
+// (column n) out.  Stores of 16-bit values go out two a lane where PAIRED says that they may:
+// neighbouring lanes swap halves, so that an even lane has columns n, n + 1 of an even row and the
+// odd one those of the row behind it.  Measured at 16384 x 4096 x 4096, bf16: see fp4_pair_kernel.
+template <int OUT, bool PAIRED>
+__device__ __forceinline__ void emit32(const Fp4ProductArgs& a, const uint32_t (&r)[32], const ColumnTerms& col,
+                                       const float2* terms, int m0, int rows, int n, int lane) {
+    float v[32];
+    const float4* t4 = reinterpret_cast<const float4*>(terms);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float4 t = t4[j];
+        v[2 * j] = finish(__uint_as_float(r[2 * j]), col, make_float2(t.x, t.y));
+        v[2 * j + 1] = finish(__uint_as_float(r[2 * j + 1]), col, make_float2(t.z, t.w));
+    }
+    if constexpr (PAIRED && OUT != CLEF_FP32) {
+        const int odd = lane & 1;
+        const uint32_t pick = odd ? 0x3276u : 0x5410u;  // odd: (other's high, own high); even: (own low, other's low)
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + int64_t(m0 + odd) * a.ldo + (n - odd));
+        const int64_t step = a.ldo;  // two rows, in words
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            uint32_t w;
+            if constexpr (OUT == CLEF_BF16) w = pack_bf16(v[2 * j], v[2 * j + 1]);
+            else {
+                const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+                w = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
+            if (n < a.N && 2 * j + odd < rows) *out = __byte_perm(w, other, pick);
+            out += step;
+        }
+    } else {
+        int64_t at = int64_t(m0) * a.ldo + n;
+#pragma unroll
+        for (int j = 0; j < 32; ++j, at += a.ldo)
+            if (n < a.N && j < rows) store_value<OUT>(a.out, at, v[j]);
+    }
+}
+
 // --------------------------------------------------------- one CTA, one tile
 // 128 rows of w x BN rows of x.  Few rows of x leave few tiles, so the K range of a tile is
 // cut among the CTAs of a cluster, which stage their fp32 tiles in their own shared memory
@@ -257,24 +311,19 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
         const int row = quarter * 32 + lane, n = wt * kWRows + row;
         const ColumnTerms col = column_terms(args, n);
         for (int j = int(threadIdx.x) - 64; j < BN; j += 128) terms[j] = row_terms(args, xt * BN + j);
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // the epilogue's warps
         int ok = 1;
         if (lane == 0) ok = mbar_wait_bounded(done, 0, abort_flag, args.flags) && !*abort_flag ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = epilogue_agrees(__shfl_sync(0xffffffffu, ok, 0));
         tc_fence_after();
         const int rows = min(BN, args.M - xt * BN);
         if (ok && S == 1) {
 #pragma unroll 1
-            for (int c = 0; c < rows; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
+            for (int c = 0; c < rows; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
                 tmem_ld_wait();
-                if (n < args.N) {
-                    int64_t at = int64_t(xt * BN + c) * args.ldo + n;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j, at += args.ldo)
-                        if (c + j < rows) store_value<OUT>(args.out, at, finish(__uint_as_float(r[j]), col, terms[c + j]));
-                }
+                if (args.paired) emit32<OUT, true>(args, r, col, terms + c, xt * BN + c, rows - c, n, lane);
+                else emit32<OUT, false>(args, r, col, terms + c, xt * BN + c, rows - c, n, lane);
             }
         } else if (ok) {  // the operand stages are idle: every MMA that read them is done
             float* red = reinterpret_cast<float*>(smem);
@@ -318,6 +367,213 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------- CTA pairs, 256 x 256 tiles, persistent
+// Many rows: two CTAs (cta_group::2) compute 256 rows of w x 256 rows of x, each loading its
+// own 128 rows of w and half of x's rows (scales: of its rows of w, and of all rows of x), and
+// walk the tiles until none is left.  Two 256-column accumulators and the scales do not fit
+// 512 TMEM columns, so the accumulators share 64: [0, 256) and [192, 448), scales from 448 on.
+// The epilogue takes the shared columns first and hands them back at once; from then on the next
+// tile's products run beside the rest of it.
+template <int FMT>
+struct PairCfg {
+    static constexpr int GROUPS = groups_of(FMT);
+    static constexpr int ROWS = 256;                          // rows of x in a tile
+    static constexpr int X_BYTES = ROWS / 2 * kAtomBytes;     // a CTA's half
+    static constexpr int S_BYTES = GROUPS * kFp4ScaleGroup;
+    static constexpr int STAGE = kWBytes + X_BYTES + 3 * S_BYTES;
+    static constexpr int STAGE_STRIDE = (STAGE + 1023) / 1024 * 1024;
+    static constexpr int STAGES = 5;
+    static constexpr int SMEM = STAGES * STAGE_STRIDE + 1024 + 2 * ROWS * 8 + 256;
+    static constexpr uint32_t ACC1 = 192, SHARED = 64, S_AT = 448;
+    static_assert(4 * GROUPS + 8 * GROUPS <= 64, "scales fit the last columns");
+};
+
+template <int FMT, int OUT>
+__global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                                   const __grid_constant__ CUtensorMap tmX,
+                                                                   const __grid_constant__ CUtensorMap tmSW,
+                                                                   const __grid_constant__ CUtensorMap tmSX,
+                                                                   const Fp4ProductArgs args) {
+    using C = PairCfg<FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float2* terms = reinterpret_cast<float2*>(smem + C::STAGES * C::STAGE_STRIDE);  // [2][256]
+    uint64_t* full = reinterpret_cast<uint64_t*>(terms + 2 * C::ROWS);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* tfull = empty + C::STAGES;
+    uint64_t* handed = tfull + 2;  // the shared columns of a tile have been taken
+    uint64_t* drain = handed + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&tfull[0], 1);
+        mbar_init(&tfull[1], 1);
+        mbar_init(handed, 2 * 4);  // the epilogue warps of both CTAs
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmSW);
+        prefetch_tensormap(&tmSX);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tc_fence_before();
+    }
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are initialised before either arrives on the other's
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int n_wt = (args.N + 2 * kWRows - 1) / (2 * kWRows);
+    const int n_tiles = n_wt * ((args.M + C::ROWS - 1) / C::ROWS);
+    const int first = int(blockIdx.x) / 2, stride = int(gridDim.x) / 2;
+    const int ktiles = (args.k64 + 3) / 4;
+    griddep_wait();
+    griddep_launch();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t leader_full = cluster_map(smem_u32(full), 0);
+            bool ok = true;
+            int i = 0;  // stages filled so far
+            for (int t = first; ok && t < n_tiles; t += stride) {
+                const int w0 = (t % n_wt) * 2 + int(rank);  // 128-row groups: own rows of w,
+                const int x0 = (t / n_wt) * 2;              // the first of x's two
+                for (int kt = 0; kt < ktiles; ++kt, ++i) {
+                    const int s = i % C::STAGES;
+                    if (!mbar_wait_bounded(&empty[s], uint32_t(i / C::STAGES & 1) ^ 1u, abort_flag, args.flags)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = smem + s * C::STAGE_STRIDE;
+                    // rank 0's barrier counts the bytes of both CTAs
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
+                    const uint32_t bar = leader_full + 8u * uint32_t(s);
+                    uint8_t* sc = st + kWBytes + C::X_BYTES;
+                    tma_load_2d_pair(st, &tmW, kt * kAtomBytes, w0 * kWRows, bar);
+                    tma_load_2d_pair(st + kWBytes, &tmX, kt * kAtomBytes, (x0 + int(rank)) * kFp4RowGroup, bar);
+                    tma_load_2d_pair(sc, &tmSW, 0, w0 * args.kgroups + kt * C::GROUPS, bar);
+                    tma_load_2d_pair(sc + C::S_BYTES, &tmSX, 0, x0 * args.kgroups + kt * C::GROUPS, bar);
+                    tma_load_2d_pair(sc + 2 * C::S_BYTES, &tmSX, 0, (x0 + 1) * args.kgroups + kt * C::GROUPS, bar);
+                }
+            }
+            if (!ok && rank == 0) {  // let every copy that this CTA's barriers count land before it goes
+                for (int j = i < C::STAGES ? 0 : i - C::STAGES; j < i; ++j)
+                    mbar_wait_bounded(&full[j % C::STAGES], uint32_t(j / C::STAGES & 1), nullptr, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t peer_empty = cluster_map(smem_u32(empty), 1), peer_tfull = cluster_map(smem_u32(tfull), 1);
+            const uint32_t sw = tmem + C::S_AT, sx = sw + 4 * C::GROUPS;
+            bool ok = true;
+            int i = 0, j = 0;
+            for (int t = first; ok && t < n_tiles; t += stride, ++j) {
+                // the last tile's shared columns: whatever came before it has been read too
+                if (j > 0 && !mbar_wait_bounded(handed, uint32_t(j - 1) & 1u, abort_flag, args.flags, kWaitLimitNs, true))
+                    break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (j & 1 ? C::ACC1 : 0);
+                for (int kt = 0; kt < ktiles; ++kt, ++i) {
+                    const int s = i % C::STAGES;
+                    if (!mbar_wait_bounded(&full[s], uint32_t(i / C::STAGES & 1), abort_flag, args.flags)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * C::STAGE_STRIDE), sc = st + kWBytes + C::X_BYTES;
+#pragma unroll
+                    for (int g = 0; g < C::GROUPS; ++g) {
+                        copy_scales<true>(sw + 4 * g, scale_desc(sc + g * kFp4ScaleGroup));
+                        copy_scales<true>(sx + 8 * g, scale_desc(sc + C::S_BYTES + g * kFp4ScaleGroup));
+                        copy_scales<true>(sx + 8 * g + 4, scale_desc(sc + 2 * C::S_BYTES + g * kFp4ScaleGroup));
+                    }
+                    const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + kWBytes);
+                    const int nk = min(4, args.k64 - 4 * kt);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= nk) break;
+                        constexpr bool MX = FMT == CLEF_MXFP4;
+                        const uint32_t g = MX ? k / 2 : k;
+                        mma_fp4<FMT, true>(acc, da + uint64_t(2 * k), db + uint64_t(2 * k),
+                                           idesc_fp4(FMT, 2 * kWRows, C::ROWS, MX ? (k & 1) * 2 : 0), sw + 4 * g,
+                                           sx + 8 * g, kt > 0 || k > 0 ? 1u : 0u);
+                    }
+                    tc_commit_pair(smem_u32(&empty[s]));  // the stage is free in both CTAs
+                    tc_commit_pair(peer_empty + 8u * uint32_t(s));
+                }
+                if (ok) {
+                    tc_commit_pair(smem_u32(&tfull[j & 1]));
+                    tc_commit_pair(peer_tfull + 8u * uint32_t(j & 1));
+                }
+            }
+            // every MMA completes before TMEM is freed
+            tc_commit_pair(smem_u32(drain));
+            mbar_wait_bounded(drain, 0, nullptr, args.flags);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+        const uint32_t leader_handed = cluster_map(smem_u32(handed), 0);
+        int j = 0;
+        for (int t = first; t < n_tiles; t += stride, ++j) {
+            const int m0 = t / n_wt * C::ROWS, n = (t % n_wt) * 2 * kWRows + int(rank) * kWRows + quarter * 32 + lane;
+            float2* mine = terms + (j & 1) * C::ROWS;
+            for (int c = int(threadIdx.x) - 64; c < C::ROWS; c += 128) mine[c] = row_terms(args, m0 + c);
+            const ColumnTerms col = column_terms(args, n);
+            int ok = 1;
+            if (lane == 0) ok = mbar_wait_bounded(&tfull[j & 1], uint32_t(j >> 1) & 1u, abort_flag, args.flags) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!epilogue_agrees(ok)) break;  // all four warps, or none
+            tc_fence_after();
+            const uint32_t acc = lanes + (j & 1 ? C::ACC1 : 0);
+            const int shared0 = j & 1 ? 0 : int(C::ACC1);  // this tile's columns that the other accumulator has too
+            const int rows = min(C::ROWS, args.M - m0);
+            uint32_t r[2][32];
+            tmem_ld32(acc + uint32_t(shared0), r[0]);
+            tmem_ld32(acc + uint32_t(shared0 + 32), r[1]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_handed);
+#pragma unroll 1
+            for (int c = 0; c < C::ROWS; c += 64) {
+                const int c0 = (shared0 + c) % C::ROWS;  // the shared columns first
+                if (c > 0) {
+                    tmem_ld32(acc + uint32_t(c0), r[0]);
+                    tmem_ld32(acc + uint32_t(c0 + 32), r[1]);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = c0 + 32 * h;
+                    if (at >= rows) continue;
+                    if (args.paired) emit32<OUT, true>(args, r[h], col, mine + at, m0 + at, rows - at, n, lane);
+                    else emit32<OUT, false>(args, r[h], col, mine + at, m0 + at, rows - at, n, lane);
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    // no CTA leaves (or frees TMEM) while the other's MMAs, copies or arrivals may still touch it
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -387,8 +643,50 @@ cudaError_t launch_tile(const clef_fp4& x, const clef_fp4& w, Fp4ProductArgs a, 
     return launch_clusters(fp4_tile_kernel<FMT, BN, OUT>, tiles * a.splits, a.splits, kTileThreads, C::SMEM, s, maps, a);
 }
 
+// Pairs that the current device holds at once, found out once for every device.
+template <int FMT, int OUT>
+cudaError_t pairs_at_once(int* n) {
+    using C = PairCfg<FMT>;
+    static PerDevice<int> known;
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return cudaError_t(known.get(device, n, [](int* v) {
+        cudaError_t f = cudaFuncSetAttribute(fp4_pair_kernel<FMT, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (f != cudaSuccess) return int(f);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kTileThreads);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        f = cudaOccupancyMaxActiveClusters(v, fp4_pair_kernel<FMT, OUT>, &cfg);
+        return f != cudaSuccess ? int(f) : *v < 1 ? int(cudaErrorInvalidConfiguration) : 0;
+    }));
+}
+
+template <int FMT, int OUT>
+cudaError_t launch_pair(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, cudaStream_t s) {
+    using C = PairCfg<FMT>;
+    int pairs = 0;
+    const cudaError_t e = pairs_at_once<FMT, OUT>(&pairs);
+    if (e != cudaSuccess) return e;
+    CUtensorMap maps[4];
+    if (!codes_map(&maps[0], w, kWRows) || !codes_map(&maps[1], x, C::ROWS / 2) || !scales_map(&maps[2], w) ||
+        !scales_map(&maps[3], x))
+        return cudaErrorInvalidValue;
+    const int tiles = (a.N + 2 * kWRows - 1) / (2 * kWRows) * ((a.M + C::ROWS - 1) / C::ROWS);
+    return launch_clusters(fp4_pair_kernel<FMT, OUT>, 2 * std::min(tiles, pairs), 2, kTileThreads, C::SMEM, s, maps, a);
+}
+
 template <int FMT, int OUT>
 cudaError_t launch_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, cudaStream_t s) {
+    if (a.M > 256) return launch_pair<FMT, OUT>(x, w, a, s);
     if (a.M <= 32) return launch_tile<FMT, 32, OUT>(x, w, a, s);
     if (a.M <= 64) return launch_tile<FMT, 64, OUT>(x, w, a, s);
     return launch_tile<FMT, 128, OUT>(x, w, a, s);
