@@ -123,6 +123,19 @@ __device__ __forceinline__ float finish(float acc, const ColumnTerms& c, float2 
     return fmaf(acc * c.scale, r.x, fmaf(r.y, c.sum, c.bias));
 }
 
+// True in one thread of a converged warp.  The MMA warps stay converged and pick the issuing thread
+// around each batch of tcgen05 instructions: addresses and descriptors then stay in uniform
+// registers, where the instructions want them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // A barrier of the four epilogue warps, behind which all of them know whether all may go on.
 __device__ __forceinline__ bool epilogue_agrees(int ok) {
     int all;
@@ -387,7 +400,7 @@ struct PairCfg {
     static constexpr int STAGE_STRIDE = (STAGE + 1023) / 1024 * 1024;
     static constexpr int STAGES = 5;
     static constexpr int SMEM = STAGES * STAGE_STRIDE + 1024 + 2 * ROWS * 8 + 256;
-    static constexpr uint32_t ACC1 = 192, SHARED = 64, S_AT = 448;
+    static constexpr uint32_t ACC1 = 192, S_AT = 448;
     static_assert(4 * GROUPS + 8 * GROUPS <= 64, "scales fit the last columns");
 };
 
@@ -446,13 +459,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_
         if (lane == 0) {
             const uint32_t leader_full = cluster_map(smem_u32(full), 0);
             bool ok = true;
-            int i = 0;  // stages filled so far
+            int i = 0, s = 0;  // stages filled so far, and the next one
+            uint32_t phase = 1;
             for (int t = first; ok && t < n_tiles; t += stride) {
                 const int w0 = (t % n_wt) * 2 + int(rank);  // 128-row groups: own rows of w,
                 const int x0 = (t / n_wt) * 2;              // the first of x's two
                 for (int kt = 0; kt < ktiles; ++kt, ++i) {
-                    const int s = i % C::STAGES;
-                    if (!mbar_wait_bounded(&empty[s], uint32_t(i / C::STAGES & 1) ^ 1u, abort_flag, args.flags)) {
+                    if (!mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags)) {
                         ok = false;
                         break;
                     }
@@ -466,6 +479,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_
                     tma_load_2d_pair(sc, &tmSW, 0, w0 * args.kgroups + kt * C::GROUPS, bar);
                     tma_load_2d_pair(sc + C::S_BYTES, &tmSX, 0, x0 * args.kgroups + kt * C::GROUPS, bar);
                     tma_load_2d_pair(sc + 2 * C::S_BYTES, &tmSX, 0, (x0 + 1) * args.kgroups + kt * C::GROUPS, bar);
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
             if (!ok && rank == 0) {  // let every copy that this CTA's barriers count land before it goes
@@ -475,52 +492,62 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             const uint32_t peer_empty = cluster_map(smem_u32(empty), 1), peer_tfull = cluster_map(smem_u32(tfull), 1);
             const uint32_t sw = tmem + C::S_AT, sx = sw + 4 * C::GROUPS;
+            const uint64_t d0 = smem_desc_sw128(smem_u32(smem)), c0 = scale_desc(smem_u32(smem) + kWBytes + C::X_BYTES);
             bool ok = true;
-            int i = 0, j = 0;
+            int s = 0, j = 0;
+            uint32_t phase = 0;
             for (int t = first; ok && t < n_tiles; t += stride, ++j) {
                 // the last tile's shared columns: whatever came before it has been read too
                 if (j > 0 && !mbar_wait_bounded(handed, uint32_t(j - 1) & 1u, abort_flag, args.flags, kWaitLimitNs, true))
-                    break;
+                    ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + (j & 1 ? C::ACC1 : 0);
-                for (int kt = 0; kt < ktiles; ++kt, ++i) {
-                    const int s = i % C::STAGES;
-                    if (!mbar_wait_bounded(&full[s], uint32_t(i / C::STAGES & 1), abort_flag, args.flags)) {
-                        ok = false;
-                        break;
-                    }
+                for (int kt = 0; kt < ktiles; ++kt) {
+                    ok = mbar_wait_bounded(&full[s], phase, abort_flag, args.flags);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * C::STAGE_STRIDE), sc = st + kWBytes + C::X_BYTES;
-#pragma unroll
-                    for (int g = 0; g < C::GROUPS; ++g) {
-                        copy_scales<true>(sw + 4 * g, scale_desc(sc + g * kFp4ScaleGroup));
-                        copy_scales<true>(sx + 8 * g, scale_desc(sc + C::S_BYTES + g * kFp4ScaleGroup));
-                        copy_scales<true>(sx + 8 * g + 4, scale_desc(sc + 2 * C::S_BYTES + g * kFp4ScaleGroup));
-                    }
-                    const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + kWBytes);
+                    const uint64_t da = d0 + uint64_t(s * (C::STAGE_STRIDE >> 4)), db = da + (kWBytes >> 4);
+                    const uint64_t dc = c0 + uint64_t(s * (C::STAGE_STRIDE >> 4));
                     const int nk = min(4, args.k64 - 4 * kt);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k >= nk) break;
-                        constexpr bool MX = FMT == CLEF_MXFP4;
-                        const uint32_t g = MX ? k / 2 : k;
-                        mma_fp4<FMT, true>(acc, da + uint64_t(2 * k), db + uint64_t(2 * k),
-                                           idesc_fp4(FMT, 2 * kWRows, C::ROWS, MX ? (k & 1) * 2 : 0), sw + 4 * g,
-                                           sx + 8 * g, kt > 0 || k > 0 ? 1u : 0u);
+                        for (int g = 0; g < C::GROUPS; ++g) {
+                            copy_scales<true>(sw + 4 * g, dc + g * (kFp4ScaleGroup >> 4));
+                            copy_scales<true>(sx + 8 * g, dc + (C::GROUPS + g) * (kFp4ScaleGroup >> 4));
+                            copy_scales<true>(sx + 8 * g + 4, dc + (2 * C::GROUPS + g) * (kFp4ScaleGroup >> 4));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k >= nk) break;
+                            constexpr bool MX = FMT == CLEF_MXFP4;
+                            const uint32_t g = MX ? k / 2 : k;
+                            mma_fp4<FMT, true>(acc, da + uint64_t(2 * k), db + uint64_t(2 * k),
+                                               idesc_fp4(FMT, 2 * kWRows, C::ROWS, MX ? (k & 1) * 2 : 0), sw + 4 * g,
+                                               sx + 8 * g, kt > 0 || k > 0 ? 1u : 0u);
+                        }
+                        tc_commit_pair(smem_u32(&empty[s]));  // the stage is free in both CTAs
+                        tc_commit_pair(peer_empty + 8u * uint32_t(s));
+                        if (kt == ktiles - 1) {
+                            tc_commit_pair(smem_u32(&tfull[j & 1]));
+                            tc_commit_pair(peer_tfull + 8u * uint32_t(j & 1));
+                        }
                     }
-                    tc_commit_pair(smem_u32(&empty[s]));  // the stage is free in both CTAs
-                    tc_commit_pair(peer_empty + 8u * uint32_t(s));
-                }
-                if (ok) {
-                    tc_commit_pair(smem_u32(&tfull[j & 1]));
-                    tc_commit_pair(peer_tfull + 8u * uint32_t(j & 1));
+                    __syncwarp();
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
             // every MMA completes before TMEM is freed
-            tc_commit_pair(smem_u32(drain));
+            if (elect_one()) tc_commit_pair(smem_u32(drain));
+            __syncwarp();
             mbar_wait_bounded(drain, 0, nullptr, args.flags);
         }
         __syncwarp();
