@@ -143,6 +143,7 @@ int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, co
     a.kgroups = fp4_kgroups(x->format, x->cols);
     a.splits = 1;
     a.paired = dtype != CLEF_FP32 && row_stride % 2 == 0 && w->rows % 2 == 0 && !misaligned(out, 4);
+    a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && !misaligned(out, 16);
     return launch_fp4_product(*x, *w, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
                                                                                                   : CLEF_ERR_CUDA;
 }

@@ -105,7 +105,8 @@ __device__ __forceinline__ ColumnTerms column_terms(const Fp4ProductArgs& a, int
     return t;
 }
 
-// What an output row (a row of x) brings: f and h of the formula above.
+// What an output row (a row of x) brings: f and h of the formula above, kept in shared memory as
+// (f, f, h, h) of two rows, so that one read serves two columns of an accumulator.
 __device__ __forceinline__ float2 row_terms(const Fp4ProductArgs& a, int m) {
     float2 t = make_float2(1.f, 0.f);
     if (m < a.M) {
@@ -118,9 +119,39 @@ __device__ __forceinline__ float2 row_terms(const Fp4ProductArgs& a, int m) {
     }
     return t;
 }
+__device__ __forceinline__ void put_row_terms(float* terms, int j, float2 t) {
+    float* p = terms + (j >> 1) * 4 + (j & 1);
+    p[0] = t.x;
+    p[2] = t.y;
+}
 
-__device__ __forceinline__ float finish(float acc, const ColumnTerms& c, float2 r) {
-    return fmaf(acc * c.scale, r.x, fmaf(r.y, c.sum, c.bias));
+// Two fp32 numbers in one register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 both_of(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Outputs of one column and two rows from their accumulators.
+__device__ __forceinline__ float2 finish2(float acc0, float acc1, const ColumnTerms& c, const float4& t) {
+    const uint64_t acc = mul2(pair_of(acc0, acc1), pair_of(c.scale, c.scale));
+    const uint64_t add = fma2(pair_of(t.z, t.w), pair_of(c.sum, c.sum), pair_of(c.bias, c.bias));
+    return both_of(fma2(acc, pair_of(t.x, t.y), add));
 }
 
 // True in one thread of a converged warp.  The MMA warps stay converged and pick the issuing thread
@@ -136,13 +167,13 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// A barrier of the four epilogue warps, behind which all of them know whether all may go on.
+// A barrier of the epilogue warps, behind which all of them know whether all may go on.
 __device__ __forceinline__ bool epilogue_agrees(int ok) {
     int all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.s32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
         "selp.s32 %0, 1, 0, q;\n\t}"
         : "=r"(all)
         : "r"(ok)
@@ -150,45 +181,81 @@ __device__ __forceinline__ bool epilogue_agrees(int ok) {
     return all != 0;
 }
 
-// 32 accumulator columns (rows m0 .. m0 + 31 of x; `rows` of them exist) of one TMEM lane
-// (column n) out.  Stores of 16-bit values go out two a lane where PAIRED says that they may:
+// NC accumulator columns (rows m0 .. of x, of which `rows` exist) of one TMEM lane (column n) out;
+// `terms` at row m0.  16-bit values go out two a lane where a.paired says that they may:
 // neighbouring lanes swap halves, so that an even lane has columns n, n + 1 of an even row and the
-// odd one those of the row behind it.  Measured at 16384 x 4096 x 4096, bf16: see fp4_pair_kernel.
-template <int OUT, bool PAIRED>
-__device__ __forceinline__ void emit32(const Fp4ProductArgs& a, const uint32_t (&r)[32], const ColumnTerms& col,
-                                       const float2* terms, int m0, int rows, int n, int lane) {
-    float v[32];
+// odd one those of the row behind it.
+template <int OUT, int NC>
+__device__ __forceinline__ void emit(const Fp4ProductArgs& a, const uint32_t (&r)[NC], const ColumnTerms& col,
+                                     const float* terms, int m0, int rows, int n, int lane) {
     const float4* t4 = reinterpret_cast<const float4*>(terms);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float4 t = t4[j];
-        v[2 * j] = finish(__uint_as_float(r[2 * j]), col, make_float2(t.x, t.y));
-        v[2 * j + 1] = finish(__uint_as_float(r[2 * j + 1]), col, make_float2(t.z, t.w));
-    }
-    if constexpr (PAIRED && OUT != CLEF_FP32) {
+    if (OUT != CLEF_FP32 && a.paired) {
         const int odd = lane & 1;
         const uint32_t pick = odd ? 0x3276u : 0x5410u;  // odd: (other's high, own high); even: (own low, other's low)
         uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + int64_t(m0 + odd) * a.ldo + (n - odd));
         const int64_t step = a.ldo;  // two rows, in words
+        // rows of this lane, as a count of pairs: all of them in every tile but the last
+        const int most = n < a.N ? (min(rows, NC) + 1 - odd) >> 1 : 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < NC / 2; ++j) {
+            const float2 v = finish2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), col, t4[j]);
             uint32_t w;
-            if constexpr (OUT == CLEF_BF16) w = pack_bf16(v[2 * j], v[2 * j + 1]);
-            else {
-                const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+            if constexpr (OUT == CLEF_FP16) {
+                const __half2 h = __floats2half2_rn(v.x, v.y);
                 w = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                w = pack_bf16(v.x, v.y);
             }
             const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
-            if (n < a.N && 2 * j + odd < rows) *out = __byte_perm(w, other, pick);
+            if (j < most) *out = __byte_perm(w, other, pick);
             out += step;
         }
     } else {
+        const int most = n < a.N ? rows : 0;
         int64_t at = int64_t(m0) * a.ldo + n;
 #pragma unroll
-        for (int j = 0; j < 32; ++j, at += a.ldo)
-            if (n < a.N && j < rows) store_value<OUT>(a.out, at, v[j]);
+        for (int j = 0; j < NC / 2; ++j) {
+            const float2 v = finish2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), col, t4[j]);
+            if (2 * j < most) store_value<OUT>(a.out, at, v.x);
+            at += a.ldo;
+            if (2 * j + 1 < most) store_value<OUT>(a.out, at, v.y);
+            at += a.ldo;
+        }
     }
 }
+
+// 16 columns of one TMEM lane as 16-bit values into a staged tile [16 rows of x][128 columns].
+template <int OUT, int FROM>
+__device__ __forceinline__ void stage16(uint16_t* to, const uint32_t (&r)[32], const ColumnTerms& col, const float* terms) {
+    const float4* t4 = reinterpret_cast<const float4*>(terms);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 v = finish2(__uint_as_float(r[FROM + 2 * j]), __uint_as_float(r[FROM + 2 * j + 1]), col, t4[j]);
+        uint32_t w;
+        if constexpr (OUT == CLEF_FP16) {
+            const __half2 h = __floats2half2_rn(v.x, v.y);
+            w = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            w = pack_bf16(v.x, v.y);
+        }
+        to[(2 * j) * kWRows] = uint16_t(w);
+        to[(2 * j + 1) * kWRows] = uint16_t(w >> 16);
+    }
+}
+
+// A barrier of the four warps of one half of the epilogue.
+__device__ __forceinline__ void half_sync(int half) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + half) : "memory");
+}
+
+template <int NC>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[NC]) {
+    if constexpr (NC == 16) tmem_ld16(taddr, r);
+    else tmem_ld32(taddr, r);
+}
+
+constexpr int kEpilogue = 256;               // threads of the epilogue: two warps for every 32 TMEM lanes
+constexpr int kThreads = 64 + kEpilogue;     // and one warp each for TMA and MMA
 
 // --------------------------------------------------------- one CTA, one tile
 // 128 rows of w x BN rows of x.  Few rows of x leave few tiles, so the K range of a tile is
@@ -209,11 +276,11 @@ struct TileCfg {
     static_assert(BN * LD * 4 <= STAGES * STAGE, "a staged tile fits the operand stages");
     static_assert(STAGE % 1024 == 0 && X_BYTES % 1024 == 0, "swizzle atoms start on 1024 bytes");
 };
-constexpr int kTileThreads = 192;  // TMA, MMA, four epilogue warps
+
 constexpr int kMaxSplits = 8;
 
 template <int FMT, int BN, int OUT>
-__global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_constant__ CUtensorMap tmW,
+__global__ void __launch_bounds__(kThreads) fp4_tile_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                 const __grid_constant__ CUtensorMap tmX,
                                                                 const __grid_constant__ CUtensorMap tmSW,
                                                                 const __grid_constant__ CUtensorMap tmSX,
@@ -221,8 +288,8 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
     using C = TileCfg<FMT, BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float2* terms = reinterpret_cast<float2*>(smem + C::STAGES * C::STAGE);
-    uint64_t* full = reinterpret_cast<uint64_t*>(terms + BN);
+    float* terms = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(terms + 2 * BN);
     uint64_t* empty = full + C::STAGES;
     uint64_t* done = empty + C::STAGES;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -261,10 +328,10 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
-            int i = 0;
+            int i = 0, s = 0;  // stages filled so far, and the next one
+            uint32_t phase = 1;
             for (int kt = kt0; kt < kt1; ++kt, ++i) {
-                const int s = i % C::STAGES;
-                if (!mbar_wait_bounded(&empty[s], uint32_t(i / C::STAGES & 1) ^ 1u, abort_flag, args.flags)) {
+                if (!mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags)) {
                     ok = false;
                     break;
                 }
@@ -276,6 +343,10 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
                 // x's scales of the 128-row group that the tile lies in (tiles of fewer rows: the first)
                 tma_load_2d(st + kWBytes + C::X_BYTES + C::S_BYTES, &tmSX, 0,
                             xt * BN / kFp4RowGroup * args.kgroups + kt * C::GROUPS, &full[s]);
+                if (++s == C::STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
             if (!ok) {  // let every copy that was asked for land before the CTA goes
                 for (int j = i < C::STAGES ? 0 : i - C::STAGES; j < i; ++j)
@@ -284,25 +355,24 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            int i = 0;
-            for (int kt = kt0; kt < kt1; ++kt, ++i) {
-                const int s = i % C::STAGES;
-                if (!mbar_wait_bounded(&full[s], uint32_t(i / C::STAGES & 1), abort_flag, args.flags)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * C::STAGE);
-                const uint32_t sw = tmem + BN, sx = sw + C::S_COLS;
+        const uint32_t sw = tmem + BN, sx = sw + C::S_COLS;
+        const uint64_t d0 = smem_desc_sw128(smem_u32(smem)), c0 = scale_desc(smem_u32(smem) + kWBytes + C::X_BYTES);
+        bool ok = true;
+        int s = 0;
+        uint32_t phase = 0;
+        for (int kt = kt0; kt < kt1; ++kt) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], phase, abort_flag, args.flags));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = d0 + uint64_t(s * (C::STAGE >> 4)), db = da + (kWBytes >> 4);
+            const uint64_t dc = c0 + uint64_t(s * (C::STAGE >> 4));
+            const int nk = min(4, args.k64 - 4 * kt);
+            if (elect_one()) {
 #pragma unroll
                 for (int g = 0; g < C::GROUPS; ++g) {
-                    copy_scales<false>(sw + 4 * g, scale_desc(st + kWBytes + C::X_BYTES + g * kFp4ScaleGroup));
-                    copy_scales<false>(sx + 4 * g, scale_desc(st + kWBytes + C::X_BYTES + C::S_BYTES + g * kFp4ScaleGroup));
+                    copy_scales<false>(sw + 4 * g, dc + g * (kFp4ScaleGroup >> 4));
+                    copy_scales<false>(sx + 4 * g, dc + (C::GROUPS + g) * (kFp4ScaleGroup >> 4));
                 }
-                const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + kWBytes);
-                const int nk = min(4, args.k64 - 4 * kt);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (k >= nk) break;
@@ -310,43 +380,45 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
                     const uint32_t g = 4 * (MX ? k / 2 : k);  // mxfp4: a word holds two MMAs' scales
                     mma_fp4<FMT, false>(tmem, da + uint64_t(2 * k), db + uint64_t(2 * k),
                                         idesc_fp4(FMT, kWRows, BN, MX ? (k & 1) * 2 : 0), sw + g, sx + g,
-                                        i > 0 || k > 0 ? 1u : 0u);
+                                        kt > kt0 || k > 0 ? 1u : 0u);
                 }
                 tc_commit(&empty[s]);
             }
-            tc_commit(done);
-            // on every path: what was issued completes before TMEM is freed
-            if (!mbar_wait_bounded(done, 0, nullptr, args.flags) || !ok) *abort_flag = 1;
+            __syncwarp();
+            if (++s == C::STAGES) {
+                s = 0;
+                phase ^= 1u;
+            }
         }
+        // on every path: what was issued completes before TMEM is freed
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+        if (!mbar_wait_bounded(done, 0, nullptr, args.flags) || !ok) *abort_flag = 1;
         __syncwarp();
     } else {
-        const int quarter = warp & 3;  // TMEM lanes that this warp may read
+        const int t = int(threadIdx.x) - 64;
+        const int quarter = warp & 3, half = t >> 7;  // TMEM lanes that this warp may read; its half of the columns
         const int row = quarter * 32 + lane, n = wt * kWRows + row;
         const ColumnTerms col = column_terms(args, n);
-        for (int j = int(threadIdx.x) - 64; j < BN; j += 128) terms[j] = row_terms(args, xt * BN + j);
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait_bounded(done, 0, abort_flag, args.flags) && !*abort_flag ? 1 : 0;
-        ok = epilogue_agrees(__shfl_sync(0xffffffffu, ok, 0));
+        if (t < BN) put_row_terms(terms, t, row_terms(args, xt * BN + t));
+        bool ok = mbar_wait_bounded(done, 0, abort_flag, args.flags) && !*abort_flag;
+        ok = epilogue_agrees(ok);  // the row terms are there too
         tc_fence_after();
         const int rows = min(BN, args.M - xt * BN);
-        if (ok && S == 1) {
+        constexpr int NC = BN == 32 ? 16 : 32;
+        if (ok) {
+            float* red = reinterpret_cast<float*>(smem);  // idle: every MMA that read the stages is done
 #pragma unroll 1
-            for (int c = 0; c < rows; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
+            for (int c = half * (BN / 2); c < min(rows, (half + 1) * (BN / 2)); c += NC) {
+                uint32_t r[NC];
+                tmem_load<NC>(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
                 tmem_ld_wait();
-                if (args.paired) emit32<OUT, true>(args, r, col, terms + c, xt * BN + c, rows - c, n, lane);
-                else emit32<OUT, false>(args, r, col, terms + c, xt * BN + c, rows - c, n, lane);
-            }
-        } else if (ok) {  // the operand stages are idle: every MMA that read them is done
-            float* red = reinterpret_cast<float*>(smem);
-#pragma unroll 1
-            for (int c = 0; c < rows; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tmem + uint32_t(c) + (uint32_t(quarter * 32) << 16), r);
-                tmem_ld_wait();
+                if (S == 1) {
+                    emit<OUT, NC>(args, r, col, terms + 2 * c, xt * BN + c, rows - c, n, lane);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) red[(c + j) * C::LD + row] = __uint_as_float(r[j]);
+                    for (int j = 0; j < NC; ++j) red[(c + j) * C::LD + row] = __uint_as_float(r[j]);
+                }
             }
         }
         tc_fence_before();
@@ -354,11 +426,13 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
     if (S > 1) {
         cluster_sync();  // every thread of every CTA of the cluster, on every path
         if (warp >= 2 && !*abort_flag) {
-            const int row = (warp & 3) * 32 + lane, n = wt * kWRows + row;
+            const int t = int(threadIdx.x) - 64;
+            const int row = t & (kWRows - 1), n = wt * kWRows + row;
             const ColumnTerms col = column_terms(args, n);
             const int rows = min(BN, args.M - xt * BN);
             const uint32_t red0 = smem_u32(smem);
-            for (int j = sp; j < rows; j += S) {  // CTA sp finishes rows sp, sp + S, ...
+            // row j of the tile is added up by CTA j % S, each row by 128 neighbouring threads
+            for (int j = sp + S * (t / kWRows); j < rows; j += S * (kEpilogue / kWRows)) {
                 const uint32_t at = red0 + uint32_t((j * C::LD + row) * 4);
                 float v[kMaxSplits];
 #pragma unroll
@@ -370,8 +444,10 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < kMaxSplits; ++i)
                     if (i < S) acc += v[i];
+                const float4 pair = reinterpret_cast<const float4*>(terms)[j >> 1];
+                const float2 y = finish2(acc, acc, col, pair);
                 if (n < args.N)
-                    store_value<OUT>(args.out, int64_t(xt * BN + j) * args.ldo + n, finish(acc, col, terms[j]));
+                    store_value<OUT>(args.out, int64_t(xt * BN + j) * args.ldo + n, j & 1 ? y.y : y.x);
             }
         }
         cluster_sync();  // no CTA leaves while another may still read its shared memory
@@ -399,22 +475,25 @@ struct PairCfg {
     static constexpr int STAGE = kWBytes + X_BYTES + 3 * S_BYTES;
     static constexpr int STAGE_STRIDE = (STAGE + 1023) / 1024 * 1024;
     static constexpr int STAGES = 5;
-    static constexpr int SMEM = STAGES * STAGE_STRIDE + 1024 + 2 * ROWS * 8 + 256;
+    static constexpr int OUT_BYTES = 16 * kWRows * 2;         // a staged piece of the output: 16 rows x 128 columns
+    static constexpr int SMEM = STAGES * STAGE_STRIDE + 4 * OUT_BYTES + 1024 + 2 * ROWS * 8 + 256;
     static constexpr uint32_t ACC1 = 192, S_AT = 448;
     static_assert(4 * GROUPS + 8 * GROUPS <= 64, "scales fit the last columns");
 };
 
 template <int FMT, int OUT>
-__global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW,
+__global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                    const __grid_constant__ CUtensorMap tmX,
                                                                    const __grid_constant__ CUtensorMap tmSW,
                                                                    const __grid_constant__ CUtensorMap tmSX,
+                                                                   const __grid_constant__ CUtensorMap tmOut,
                                                                    const Fp4ProductArgs args) {
     using C = PairCfg<FMT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float2* terms = reinterpret_cast<float2*>(smem + C::STAGES * C::STAGE_STRIDE);  // [2][256]
-    uint64_t* full = reinterpret_cast<uint64_t*>(terms + 2 * C::ROWS);
+    uint8_t* staged = smem + C::STAGES * C::STAGE_STRIDE;  // [half][2] pieces of the output
+    float* terms = reinterpret_cast<float*>(staged + 4 * C::OUT_BYTES);  // of two tiles
+    uint64_t* full = reinterpret_cast<uint64_t*>(terms + 4 * C::ROWS);
     uint64_t* empty = full + C::STAGES;
     uint64_t* tfull = empty + C::STAGES;
     uint64_t* handed = tfull + 2;  // the shared columns of a tile have been taken
@@ -431,7 +510,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_
         }
         mbar_init(&tfull[0], 1);
         mbar_init(&tfull[1], 1);
-        mbar_init(handed, 2 * 4);  // the epilogue warps of both CTAs
+        mbar_init(handed, 2 * kEpilogue / 32);  // the epilogue warps of both CTAs
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -500,12 +579,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_
             int s = 0, j = 0;
             uint32_t phase = 0;
             for (int t = first; ok && t < n_tiles; t += stride, ++j) {
-                // the last tile's shared columns: whatever came before it has been read too
-                if (j > 0 && !mbar_wait_bounded(handed, uint32_t(j - 1) & 1u, abort_flag, args.flags, kWaitLimitNs, true))
-                    ok = false;
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t acc = tmem + (j & 1 ? C::ACC1 : 0);
                 for (int kt = 0; kt < ktiles; ++kt) {
                     ok = mbar_wait_bounded(&full[s], phase, abort_flag, args.flags);
@@ -522,6 +595,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_
                             copy_scales<true>(sx + 8 * g, dc + (C::GROUPS + g) * (kFp4ScaleGroup >> 4));
                             copy_scales<true>(sx + 8 * g + 4, dc + (2 * C::GROUPS + g) * (kFp4ScaleGroup >> 4));
                         }
+                    }
+                    __syncwarp();
+                    if (kt == 0 && j > 0) {
+                        // the last tile's shared columns: whatever came before it has been read too
+                        ok = mbar_wait_bounded(handed, uint32_t(j - 1) & 1u, abort_flag, args.flags, kWaitLimitNs, true);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             if (k >= nk) break;
@@ -552,48 +635,78 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_pair_kernel(const __grid_
         }
         __syncwarp();
     } else {
-        const int quarter = warp & 3;
+        const int tid = int(threadIdx.x) - 64;
+        const int quarter = warp & 3, half = tid >> 7;  // TMEM lanes that this warp may read; its half of the columns
         const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
         const uint32_t leader_handed = cluster_map(smem_u32(handed), 0);
+        const int lane_n = int(rank) * kWRows + quarter * 32 + lane;
+        // a tile's terms are read while the tile before it is written out
+        float2 row = row_terms(args, first / n_wt * C::ROWS + tid);  // kEpilogue == ROWS
+        ColumnTerms col = column_terms(args, first % n_wt * 2 * kWRows + lane_n);
         int j = 0;
         for (int t = first; t < n_tiles; t += stride, ++j) {
-            const int m0 = t / n_wt * C::ROWS, n = (t % n_wt) * 2 * kWRows + int(rank) * kWRows + quarter * 32 + lane;
-            float2* mine = terms + (j & 1) * C::ROWS;
-            for (int c = int(threadIdx.x) - 64; c < C::ROWS; c += 128) mine[c] = row_terms(args, m0 + c);
-            const ColumnTerms col = column_terms(args, n);
-            int ok = 1;
-            if (lane == 0) ok = mbar_wait_bounded(&tfull[j & 1], uint32_t(j >> 1) & 1u, abort_flag, args.flags) ? 1 : 0;
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!epilogue_agrees(ok)) break;  // all four warps, or none
+            const int m0 = t / n_wt * C::ROWS, n = t % n_wt * 2 * kWRows + lane_n;
+            float* mine = terms + (j & 1) * 2 * C::ROWS;
+            put_row_terms(mine, tid, row);
+            const bool got = mbar_wait_bounded(&tfull[j & 1], uint32_t(j >> 1) & 1u, abort_flag, args.flags);
             tc_fence_after();
+            // The accumulators share the last 64 columns of the first and the first 64 of the second: the
+            // warps whose half they lie in take them and say so, the others only that they are done with the
+            // tile before.
             const uint32_t acc = lanes + (j & 1 ? C::ACC1 : 0);
-            const int shared0 = j & 1 ? 0 : int(C::ACC1);  // this tile's columns that the other accumulator has too
-            const int rows = min(C::ROWS, args.M - m0);
+            const int c0 = half * 128, turn = half == 1 ? 64 : 0;  // half 1 takes its upper 64 columns first
             uint32_t r[2][32];
-            tmem_ld32(acc + uint32_t(shared0), r[0]);
-            tmem_ld32(acc + uint32_t(shared0 + 32), r[1]);
-            tmem_ld_wait();
-            tc_fence_before();
+            if (half != (j & 1)) {
+                tmem_ld32(acc + uint32_t(c0 + turn), r[0]);
+                tmem_ld32(acc + uint32_t(c0 + turn + 32), r[1]);
+                tmem_ld_wait();
+                tc_fence_before();
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_handed);
+            if (lane == 0) mbar_arrive_cluster_relaxed(leader_handed);
+            if (!epilogue_agrees(got)) break;  // all warps or none; the row terms are there too
+            const ColumnTerms next_col = column_terms(args, (t + stride) % n_wt * 2 * kWRows + lane_n);
+            row = row_terms(args, (t + stride) / n_wt * C::ROWS + tid);
+            const int rows = min(C::ROWS, args.M - m0);
 #pragma unroll 1
-            for (int c = 0; c < C::ROWS; c += 64) {
-                const int c0 = (shared0 + c) % C::ROWS;  // the shared columns first
-                if (c > 0) {
-                    tmem_ld32(acc + uint32_t(c0), r[0]);
-                    tmem_ld32(acc + uint32_t(c0 + 32), r[1]);
+            for (int c = 0; c < 128; c += 64) {
+                const int at = c0 + (c ^ turn);
+                if (c > 0 || half == (j & 1)) {
+                    tmem_ld32(acc + uint32_t(at), r[0]);
+                    tmem_ld32(acc + uint32_t(at + 32), r[1]);
                     tmem_ld_wait();
                 }
+                if (OUT != CLEF_FP32 && args.bulk) {
+                    const bool issuer = (tid & 127) == 0;
+                    const int col0 = n - lane - quarter * 32;
+                    uint8_t* to = staged + half * 2 * C::OUT_BYTES;
+                    uint16_t* own = reinterpret_cast<uint16_t*>(to) + quarter * 32 + lane;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int at = c0 + 32 * h;
-                    if (at >= rows) continue;
-                    if (args.paired) emit32<OUT, true>(args, r[h], col, mine + at, m0 + at, rows - at, n, lane);
-                    else emit32<OUT, false>(args, r[h], col, mine + at, m0 + at, rows - at, n, lane);
+                    for (int q = 0; q < 4; ++q) {
+                        // two pieces in turn: before the barrier of one, the other has been read
+                        uint16_t* piece = own + (q & 1) * (C::OUT_BYTES / 2);
+                        const float* tq = mine + 2 * (at + 16 * q);
+                        if (q == 0) stage16<OUT, 0>(piece, r[0], col, tq);
+                        if (q == 1) stage16<OUT, 16>(piece, r[0], col, tq);
+                        if (q == 2) stage16<OUT, 0>(piece, r[1], col, tq);
+                        if (q == 3) stage16<OUT, 16>(piece, r[1], col, tq);
+                        fence_proxy_async_smem();
+                        if (issuer) bulk_wait_read<0>();
+                        half_sync(half);
+                        if (issuer && at + 16 * q < rows && col0 < args.N) {
+                            tma_store_2d(&tmOut, to + (q & 1) * C::OUT_BYTES, col0, m0 + at + 16 * q);
+                            bulk_commit();
+                        }
+                    }
+                } else {
+                    if (at < rows) emit<OUT, 32>(args, r[0], col, mine + 2 * at, m0 + at, rows - at, n, lane);
+                    if (at + 32 < rows) emit<OUT, 32>(args, r[1], col, mine + 2 * at + 64, m0 + at + 32, rows - at - 32, n, lane);
                 }
             }
+            col = next_col;
             tc_fence_before();
         }
+        if ((tid & 127) == 0) bulk_wait_all();
     }
     __syncthreads();
     // no CTA leaves (or frees TMEM) while the other's MMAs, copies or arrivals may still touch it
@@ -632,9 +745,9 @@ cudaError_t set_up(PerDevice<int>* ready, K kernel, int bytes) {
     }));
 }
 
-template <typename K>
+template <int N, typename K>
 cudaError_t launch_clusters(K kernel, int grid, int cluster, int threads, size_t smem, cudaStream_t s,
-                            const CUtensorMap (&maps)[4], const Fp4ProductArgs& a) {
+                            const CUtensorMap (&maps)[N], const Fp4ProductArgs& a) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -649,7 +762,8 @@ cudaError_t launch_clusters(K kernel, int grid, int cluster, int threads, size_t
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return counted(cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], a));
+    if constexpr (N == 5) return counted(cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], a));
+    else return counted(cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], a));
 }
 
 template <int FMT, int BN, int OUT>
@@ -667,7 +781,7 @@ cudaError_t launch_tile(const clef_fp4& x, const clef_fp4& w, Fp4ProductArgs a, 
     a.splits = 1;
     const int ktiles = fp4_ktiles(x.cols);
     while (a.splits < kMaxSplits && 2 * a.splits <= ktiles && tiles * a.splits * 2 <= 2 * num_sms()) a.splits *= 2;
-    return launch_clusters(fp4_tile_kernel<FMT, BN, OUT>, tiles * a.splits, a.splits, kTileThreads, C::SMEM, s, maps, a);
+    return launch_clusters(fp4_tile_kernel<FMT, BN, OUT>, tiles * a.splits, a.splits, kThreads, C::SMEM, s, maps, a);
 }
 
 // Pairs that the current device holds at once, found out once for every device.
@@ -688,7 +802,7 @@ cudaError_t pairs_at_once(int* n) {
         attr[0].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kTileThreads);
+        cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = C::SMEM;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -703,12 +817,15 @@ cudaError_t launch_pair(const clef_fp4& x, const clef_fp4& w, const Fp4ProductAr
     int pairs = 0;
     const cudaError_t e = pairs_at_once<FMT, OUT>(&pairs);
     if (e != cudaSuccess) return e;
-    CUtensorMap maps[4];
+    CUtensorMap maps[5];
     if (!codes_map(&maps[0], w, kWRows) || !codes_map(&maps[1], x, C::ROWS / 2) || !scales_map(&maps[2], w) ||
         !scales_map(&maps[3], x))
         return cudaErrorInvalidValue;
+    maps[4] = maps[0];  // a map that is never used where the output is not stored by TMA
+    if (a.bulk && !make_tma_2d(&maps[4], a.out, 2, uint64_t(a.N), uint64_t(a.M), uint64_t(a.ldo) * 2, kWRows, 16, false))
+        return cudaErrorInvalidValue;
     const int tiles = (a.N + 2 * kWRows - 1) / (2 * kWRows) * ((a.M + C::ROWS - 1) / C::ROWS);
-    return launch_clusters(fp4_pair_kernel<FMT, OUT>, 2 * std::min(tiles, pairs), 2, kTileThreads, C::SMEM, s, maps, a);
+    return launch_clusters(fp4_pair_kernel<FMT, OUT>, 2 * std::min(tiles, pairs), 2, kThreads, C::SMEM, s, maps, a);
 }
 
 template <int FMT, int OUT>

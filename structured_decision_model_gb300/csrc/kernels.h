@@ -105,7 +105,7 @@ void partial_split_config(int n_mtiles, int N, int K, int* bn, int* splits);
 bool make_tma_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t row_stride_elems,
                       uint32_t box_rows);
 
-// The same of rows of 1- or 4-byte elements, box_inner x box_rows box, with the 128-byte swizzle or none.
+// The same of rows of 1-, 2- or 4-byte elements, box_inner x box_rows box, with the 128-byte swizzle or none.
 bool make_tma_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t rows,
                  uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128);
 cudaError_t launch_gemm(const GemmProblem& p, const GemmEpilogue& e, int* dev_flags, cudaStream_t s,
