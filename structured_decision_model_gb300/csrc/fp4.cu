@@ -14,6 +14,8 @@
 // the rounded quotient is on the true side, and a midpoint comes out as itself.  An fp32
 // value may lie closer: what it has left over, x - q * scale, is exact in one fused
 // multiply-add, and its sign moves the quotient off the midpoint to the true side.
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4.h"
 #include "kernels.h"
@@ -34,7 +36,7 @@ __device__ __forceinline__ float pow2(int e) {  // e in [-126, 127]
 __device__ __forceinline__ int exponent_of(float x) { return int(__float_as_uint(x) >> 23) - 127; }
 
 // Eight codes, the first in the lowest four bits.
-__device__ __forceinline__ uint32_t pack_e2m1(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t pack_e2m1(const float* v) {
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -48,7 +50,7 @@ __device__ __forceinline__ uint32_t pack_e2m1(const float (&v)[8]) {
 }
 
 // Eight codes to their numbers, as four fp16 pairs.
-__device__ __forceinline__ void unpack_e2m1(uint32_t codes, uint32_t (&h)[4]) {
+__device__ __forceinline__ void unpack_e2m1(uint32_t codes, uint32_t* h) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "mov.b32 {a, b, c, d}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
@@ -71,321 +73,353 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
     return __half2float(__ushort_as_half(uint16_t(h & 0xFFFFu)));
 }
 
-// t / 6 so that rounding it to few bits gives what rounding the true quotient gives: cut off,
-// with the last bit set where something was cut (a number next to a border stays off it).
+// t / 6 so that rounding it to few bits gives what rounding the true quotient gives.  One residual
+// correction gives the nearest fp32 number, which is the quotient itself where that is a border of
+// e4m3; for 16-bit values (t has 11 bits at most) a quotient that is none is far from one.  An fp32
+// value's may round to a border: it is cut off instead, with the last bit set where something was cut.
+template <bool WIDE>
 __device__ __forceinline__ float sixth(float t) {
-    const float q = __fdiv_rz(t, 6.f);
-    return fmaf(-q, 6.f, t) != 0.f ? __uint_as_float(__float_as_uint(q) | 1u) : q;
+    constexpr float kSixth = 1.f / 6.f;
+    const float q0 = t * kSixth;
+    const float q = fmaf(fmaf(-q0, 6.f, t), kSixth, q0);
+    if constexpr (!WIDE) return q;
+    const float rest = fmaf(-q, 6.f, t);
+    const uint32_t b = __float_as_uint(q) - (rest < 0.f ? 1u : 0u);
+    return __uint_as_float(rest != 0.f ? b | 1u : b);
 }
 
-// The eight values of a lane as they lie in memory: 4 words of two, or 8 fp32.
+__device__ __forceinline__ float reciprocal(float x) {  // to 1 ulp
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The larger size of each half of two words of 16-bit floats, NaN if one is; the signs are of no use.
+template <int DT>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    if constexpr (DT == CLEF_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+
+// The 16 values of a lane as they lie in memory: 8 words of two, or 16 fp32.
 template <int DT>
 struct Raw {
-    uint32_t w[DT == CLEF_FP32 ? 8 : 4];
-    __device__ __forceinline__ float at(int j) const {
-        if constexpr (DT == CLEF_FP32) return __uint_as_float(w[j]);
-        else if constexpr (DT == CLEF_BF16) return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+    static constexpr int kWords = DT == CLEF_FP32 ? 16 : 8;
+    uint32_t w[kWords];
+    // values 2j and 2j + 1 as an fp32 pair
+    __device__ __forceinline__ uint64_t two(int j) const {
+        if constexpr (DT == CLEF_FP32) return pair_of(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+        else if constexpr (DT == CLEF_BF16) return pair_of(bf16_lo(w[j]), bf16_hi(w[j]));
         else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j >> 1]));
-            return j & 1 ? f.y : f.x;
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            return pair_of(f.x, f.y);
         }
     }
-    // the largest size; NaN if one is NaN
-    __device__ __forceinline__ float top() const {
+    __device__ __forceinline__ float at(int j) const {
+        const float2 f = both_of(two(j >> 1));
+        return j & 1 ? f.y : f.x;
+    }
+    // bits of the largest size, which order as the sizes do, with infinity and NaN above every number
+    __device__ __forceinline__ uint32_t top() const {
         if constexpr (DT == CLEF_FP32) {
-            float m = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = fabsf(__uint_as_float(w[j]));
-                m = v > m || v != v ? v : m;  // once NaN, `v > m` stays false: kept below
-                if (m != m) return m;
-            }
-            return m;
-        } else {
-            // sizes of 16-bit floats order as their bits do, NaN above all
             uint32_t m = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
-            const uint32_t t = max(m & 0xFFFFu, m >> 16);
-            if constexpr (DT == CLEF_BF16) return __uint_as_float(t << 16);
-            else return __half2float(__ushort_as_half(uint16_t(t)));
+            for (int j = 0; j < 16; ++j) m = max(m, w[j] & 0x7FFFFFFFu);
+            return m;
+        } else {
+            const uint32_t m = larger2<DT>(larger2<DT>(larger2<DT>(w[0], w[1]), larger2<DT>(w[2], w[3])),
+                                           larger2<DT>(larger2<DT>(w[4], w[5]), larger2<DT>(w[6], w[7])));
+            const uint32_t t = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
+            if constexpr (DT == CLEF_BF16) return t << 16;
+            else return __float_as_uint(__half2float(__ushort_as_half(uint16_t(t))));
         }
     }
 };
 
-// VEC: every row starts on 16 bytes and has a multiple of 8 values, so a lane's eight are
-// read as whole 16-byte pieces; otherwise value by value.
+// A warp's 512 values from column col0 of a row on, 16 a lane; what lies behind the row reads as 0.
+// VEC: every row starts on 16 bytes and has a multiple of 8 values, so a lane's are read as
+// whole 16-byte pieces.  Otherwise the warp reads 32 neighbours at a time and hands them round
+// through shared memory (3001 x 1111 fp16: 4.3 us; value by value in each lane 7.3).
 template <int DT, bool VEC>
-__device__ __forceinline__ Raw<DT> load8(const void* x, int64_t row0, int col, int cols) {
+__device__ __forceinline__ Raw<DT> load16(const void* x, int64_t row0, int col0, int cols, int lane, uint32_t* stage) {
     Raw<DT> r;
-    constexpr int kWords = DT == CLEF_FP32 ? 8 : 4;
     if constexpr (VEC) {
-        if (col < cols) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) +
-                                                            (row0 + col) * (DT == CLEF_FP32 ? 4 : 2));
+        constexpr int kSize = DT == CLEF_FP32 ? 4 : 2;
+        const int col = col0 + lane * 16;
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + (row0 + col) * kSize);
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = p[i];
-                r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) r.w[i] = 0;
+        for (int i = 0; i < Raw<DT>::kWords / 4; ++i) {
+            const uint4 v = col + i * (16 / kSize) < cols ? p[i] : make_uint4(0, 0, 0, 0);
+            r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
         }
-    } else if constexpr (DT == CLEF_FP32) {
-        const uint32_t* p = static_cast<const uint32_t*>(x) + row0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r.w[j] = col + j < cols ? p[col + j] : 0u;
     } else {
-        const uint16_t* p = static_cast<const uint16_t*>(x) + row0;
+        using T = std::conditional_t<DT == CLEF_FP32, uint32_t, uint16_t>;
+        const T* p = static_cast<const T*>(x) + row0 + col0;
+        T* to = reinterpret_cast<T*>(stage);
+        T v[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = col + 2 * j < cols ? p[col + 2 * j] : 0u;
-            const uint32_t hi = col + 2 * j + 1 < cols ? p[col + 2 * j + 1] : 0u;
-            r.w[j] = lo | hi << 16;
+        for (int j = 0; j < 16; ++j) v[j] = col0 + 32 * j + lane < cols ? p[32 * j + lane] : T(0);
+        __syncwarp();  // the last piece has been read
+#pragma unroll
+        for (int j = 0; j < 16; ++j) to[32 * j + lane] = v[j];
+        __syncwarp();
+        const uint4* own = reinterpret_cast<const uint4*>(stage + lane * Raw<DT>::kWords);
+#pragma unroll
+        for (int i = 0; i < Raw<DT>::kWords / 4; ++i) {
+            const uint4 u = own[i];
+            r.w[4 * i] = u.x; r.w[4 * i + 1] = u.y; r.w[4 * i + 2] = u.z; r.w[4 * i + 3] = u.w;
         }
     }
     return r;
 }
 
-// Sums (or maxima) of a row that W warps share, in one order whatever else the block does.
-template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* red, int W, int warp) {
-    v = MAX ? warp_max(v) : warp_sum(v);
-    if (W == 1) return v;
+// A maximum and a sum over a row that W warps share, in one order whatever else the block does.
+__device__ __forceinline__ void row_reduce(float& most, float& sum, float2* red, int W, int warp) {
+    most = warp_max(most);
+    sum = warp_sum(sum);
+    if (W == 1) return;
     __syncthreads();  // red may still be read from the last call
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(most, sum);
     __syncthreads();
     const int w0 = warp / W * W;
-    v = red[w0];
-    for (int i = 1; i < W; ++i) v = MAX ? fmaxf(v, red[w0 + i]) : v + red[w0 + i];
-    return v;
+    const float2 f = red[w0];
+    most = f.x;
+    sum = f.y;
+    for (int i = 1; i < W; ++i) {
+        const float2 v = red[w0 + i];
+        most = fmaxf(most, v.x);
+        sum += v.y;
+    }
 }
 
-// TILES: 256-value tiles that a lane keeps 8 values of; W warps a row (a power of two), so
-// a row has at most 256 * TILES * W values.
-template <int FMT, int DT, bool VEC, int TILES>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantizeArgs a, int W) {
+// STEPS: 512-value pieces of a row that a warp keeps, 16 values a lane; W warps a row (a power of
+// two), so a row has at most 512 * STEPS * W values.  64 registers a thread, for 32 warps an SM: with 8
+// pieces a warp and half the warps 131072 x 4096 bf16 took 301 us instead of 252.
+template <int FMT, int DT, bool VEC, int STEPS>
+__global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4QuantizeArgs a, int W) {
     constexpr bool NV = FMT == CLEF_NVFP4;
-    __shared__ float red[kThreads / 32];
+    __shared__ float2 red[kThreads / 32];
+    __shared__ __align__(16) uint32_t stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 32 * Raw<DT>::kWords];
     griddep_wait();
     griddep_launch();  // behind the wait: whoever starts early may take what came before us as done
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = int64_t(blockIdx.x) * (kThreads / 32 / W) + warp / W;
     const bool mine = row < a.rows;  // warps behind the last row still meet the barriers
     const int part = warp % W;
-    const int ktiles = (a.cols + kFp4Tile - 1) / kFp4Tile;
+    const int padded = mine ? (a.cols + kFp4Tile - 1) / kFp4Tile * kFp4Tile : 0;  // columns that have scales
+    const bool stats = a.mean != nullptr;
     const int64_t row0 = row * a.row_stride;
 
-    Raw<DT> raw[TILES];
+    Raw<DT> raw[STEPS];
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) {
-        const int col = ((i * W + part) * 32 + lane) * 8;
-        if (mine) raw[i] = load8<DT, VEC>(a.x, row0, col, a.cols);
+    for (int i = 0; i < STEPS; ++i) {
+        const int col0 = (i * W + part) * 512;
+        if (col0 < padded) raw[i] = load16<DT, VEC>(a.x, row0, col0, a.cols, lane, stage[VEC ? 0 : warp]);
         else raw[i] = Raw<DT>{};
     }
-    // the largest size of every block, and of the row's finite blocks
-    float top[TILES], row_top = 0.f;
+    // the largest size of every block and of the row's finite blocks, and the row's sum
+    float top[STEPS], row_top = 0.f, row_sum = 0.f;
+    uint64_t sum = 0;  // (0, 0)
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) {
-        // bits of sizes order as the sizes do, with infinity and NaN above every number
-        uint32_t t = __float_as_uint(raw[i].top());
-        t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
-        if (!NV) t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    for (int i = 0; i < STEPS; ++i) {
+        uint32_t t = raw[i].top();
+        if (!NV) t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
         top[i] = __uint_as_float(t);
-    }
-    float inv_r = 1.f, r = 1.f;
-    bool tiny = false;
-    if constexpr (NV) {
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
+        if (NV) {
             if (top[i] < INFINITY) row_top = fmaxf(row_top, top[i]);
             else {  // the largest finite size of a block that is not finite
-                const int col = ((i * W + part) * 32 + lane) * 8;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 16; ++j) {
                     const float v = fabsf(raw[i].at(j));
-                    if (col + j < a.cols && v < INFINITY) row_top = fmaxf(row_top, v);
+                    if (v < INFINITY) row_top = fmaxf(row_top, v);
                 }
             }
         }
-        row_top = row_reduce<true>(row_top, red, W, warp);
+        if (stats) {
+            uint64_t t2 = add2(raw[i].two(0), raw[i].two(1));
+#pragma unroll
+            for (int j = 2; j < 8; j += 2) t2 = add2(t2, add2(raw[i].two(j), raw[i].two(j + 1)));
+            sum = add2(sum, t2);
+        }
+    }
+    if (NV || stats) {
+        const float2 s2 = both_of(sum);
+        row_sum = s2.x + s2.y;
+        row_reduce(row_top, row_sum, red, W, warp);
+    }
+    const float mean = row_sum / float(a.cols);
+    float inv_r = 1.f, r = 1.f;
+    bool tiny = false;
+    if constexpr (NV) {
         const int e = max(exponent_of(row_top) - 10, -126);
         r = pow2(e);
         inv_r = pow2(-e);
         tiny = e < -100;  // 1 / (block scale * r) may pass fp32's range: divide in two steps
         if (mine && part == 0 && lane == 0) a.row_scale[row] = r;
     }
-    if (a.mean) {  // the same for every thread
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-            float t = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t += raw[i].at(j);
-            s += t;
-        }
-        const float mean = row_reduce<false>(s, red, W, warp) / float(a.cols);
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-            const int col = ((i * W + part) * 32 + lane) * 8;
-            float t = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = col + j < a.cols ? raw[i].at(j) - mean : 0.f;
-                t = fmaf(d, d, t);
-            }
-            q += t;
-        }
-        const float var = row_reduce<false>(q, red, W, warp) / float(a.cols);
-        if (mine && part == 0 && lane == 0) {
-            a.mean[row] = mean;
-            a.rstd[row] = 1.f / sqrtf(var + 1e-5f);
-        }
-    }
     const int64_t code_stride = int64_t(a.cols + 31) / 32 * 16;
     uint8_t* codes = a.codes + row * code_stride;
-    const int kgroups = ktiles * (NV ? 4 : 2);
-    uint8_t* scales = a.scales + (row / kFp4RowGroup * kgroups) * kFp4ScaleGroup +
+    uint8_t* scales = a.scales + (row / kFp4RowGroup * (padded >> (NV ? 6 : 7))) * kFp4ScaleGroup +
                       (row % 32) * 16 + (row % kFp4RowGroup) / 32 * 4;
-    float total = 0.f;
+    const uint64_t less = pair_of(-mean, -mean);
+    float total = 0.f, squares = 0.f;
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) {
-        const int tile = i * W + part;
-        if (tile >= ktiles || !mine) continue;  // the same for a whole warp
-        const int chunk = tile * 32 + lane;
+    for (int i = 0; i < STEPS; ++i) {
+        if ((i * W + part) * 512 >= padded) continue;  // the same for a whole warp
+        const int col = (i * W + part) * 512 + lane * 16;
+        const int left = a.cols - col;  // values from the lane's first to the row's end
         uint32_t byte;    // the block's scale as stored
         float scale, inv; // what it stands for (without r) and its reciprocal
         const bool bad = !(top[i] < INFINITY);
         if constexpr (NV) {
-            byte = bad ? 0x7Fu : to_e4m3(sixth(top[i] * inv_r));
+            byte = bad ? 0x7Fu : to_e4m3(sixth<DT == CLEF_FP32>(top[i] * inv_r));
             scale = from_e4m3(byte);
-            inv = byte == 0 ? 0.f : __frcp_rn(scale);
+            inv = byte == 0 ? 0.f : reciprocal(scale);
         } else {
             const int e = max(exponent_of(top[i]) - 2, -127);
             byte = bad ? 0xFFu : uint32_t(e + 127);
             scale = __uint_as_float(e == -127 ? 0x00400000u : uint32_t(e + 127) << 23);
             inv = pow2(-e);
         }
-        float v[8];
+        uint64_t x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = raw[i].at(j);
-        if constexpr (DT == CLEF_FP32) {
+        for (int j = 0; j < 8; ++j) x[j] = raw[i].two(j);
+        if (stats) {
+            if (left >= 16) {
+                uint64_t t = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float x = NV ? v[j] * inv_r : v[j] * inv;  // powers of two
-                const float q = (NV ? fmaf(x, inv, kGrid) : x + kGrid) - kGrid;
-                const float rest = NV ? fmaf(-q, scale, x) : x - q;
-                v[j] = inv == 0.f ? 0.f : q + (rest > 0.f ? kAside : rest < 0.f ? -kAside : 0.f);
-            }
-        } else {
-            float by = inv;
-            if constexpr (NV) {
-                if (tiny) {
+                for (int j = 0; j < 8; ++j) {
+                    const uint64_t d = add2(x[j], less);
+                    t = fma2(d, d, t);
+                }
+                const float2 t2 = both_of(t);
+                squares += t2.x + t2.y;
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] *= inv_r;
-                } else {
-                    by *= inv_r;
+                for (int j = 0; j < 16; ++j) {
+                    const float d = j < left ? raw[i].at(j) - mean : 0.f;
+                    squares = fmaf(d, d, squares);
                 }
             }
+        }
+        float v[16];
+        if constexpr (DT == CLEF_FP32) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], by, kGrid) - kGrid;
-        }
-        uint32_t packed = pack_e2m1(v);
-        if (bad) {  // any number: the scale makes it NaN; behind the row's end zeros as ever
-            const int left = a.cols - chunk * 8;
-            packed = left >= 8 ? 0x22222222u : left > 0 ? 0x22222222u >> (32 - 4 * left) : 0u;
-        }
-        if (chunk * 4 < code_stride) *reinterpret_cast<uint32_t*>(codes + chunk * 4) = packed;
-        // four blocks' scales are one word, written by the first lane of theirs
-        uint32_t word = byte << (8 * (NV ? lane >> 1 & 3 : lane >> 2 & 3));
-        if constexpr (NV) {
-            word |= __shfl_xor_sync(0xffffffffu, word, 2);
-            word |= __shfl_xor_sync(0xffffffffu, word, 4);
-            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + int64_t(chunk >> 3) * kFp4ScaleGroup) = word;
+            for (int j = 0; j < 16; ++j) {
+                const float y = raw[i].at(j) * (NV ? inv_r : inv);  // powers of two
+                const float q = (NV ? fmaf(y, inv, kGrid) : y + kGrid) - kGrid;
+                const float rest = NV ? fmaf(-q, scale, y) : y - q;
+                v[j] = inv == 0.f ? 0.f : q + (rest > 0.f ? kAside : rest < 0.f ? -kAside : 0.f);
+            }
+        } else if constexpr (!NV) {  // by a power of two: exact
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 q = both_of(mul2(x[j], pair_of(inv, inv)));
+                v[2 * j] = q.x;
+                v[2 * j + 1] = q.y;
+            }
         } else {
-            word |= __shfl_xor_sync(0xffffffffu, word, 4);
-            word |= __shfl_xor_sync(0xffffffffu, word, 8);
-            if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + int64_t(chunk >> 4) * kFp4ScaleGroup) = word;
+            const uint64_t grid = pair_of(kGrid, kGrid), back = pair_of(-kGrid, -kGrid);
+            float by1 = inv;
+            if (tiny) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], pair_of(inv_r, inv_r));
+            } else {
+                by1 *= inv_r;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 q = both_of(add2(fma2(x[j], pair_of(by1, by1), grid), back));
+                v[2 * j] = q.x;
+                v[2 * j + 1] = q.y;
+            }
         }
+        uint2 packed = make_uint2(pack_e2m1(v), pack_e2m1(v + 8));
+        if (bad) {  // any number: the scale makes it NaN; behind the row's end zeros as ever
+            packed.x = left >= 8 ? 0x22222222u : left > 0 ? 0x22222222u >> (32 - 4 * left) : 0u;
+            packed.y = left >= 16 ? 0x22222222u : left > 8 ? 0x22222222u >> (64 - 4 * left) : 0u;
+        }
+        if (col < 2 * code_stride) *reinterpret_cast<uint2*>(codes + col / 2) = packed;
+        // four blocks' scales are one word, written by the first lane of theirs
+        uint32_t word = byte << (8 * (NV ? lane & 3 : lane >> 1 & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, NV ? 1 : 2);
+        word |= __shfl_xor_sync(0xffffffffu, word, NV ? 2 : 4);
+        if ((lane & (NV ? 3 : 7)) == 0 && col < padded)
+            *reinterpret_cast<uint32_t*>(scales + int64_t(col >> (NV ? 6 : 7)) * kFp4ScaleGroup) = word;
         if (a.sums) {
-            uint32_t h[4];
-            unpack_e2m1(packed, h);
+            uint32_t h[8];
+            unpack_e2m1(packed.x, h);
+            unpack_e2m1(packed.y, h + 4);
             float t = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
                 t += f.x + f.y;
             }
             total = fmaf(t, bad ? __uint_as_float(0x7FC00000u) : scale, total);
         }
     }
-    if (a.sums) {
-        total = row_reduce<false>(total, red, W, warp);
-        if (mine && part == 0 && lane == 0) a.sums[row] = total * r;
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ void store8(void* out, int64_t at, const float (&v)[8], int n, bool vec) {
-    if constexpr (DT == CLEF_FP32) {
-        float* p = static_cast<float*>(out) + at;
-        if (vec) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) p[j] = v[j];
-        }
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == CLEF_BF16) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-            else {
-                const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    if (stats || a.sums) {
+        float unused = 0.f;
+        if (stats) {
+            row_reduce(unused, squares, red, W, warp);
+            if (mine && part == 0 && lane == 0) {
+                a.mean[row] = mean;
+                a.rstd[row] = 1.f / sqrtf(squares / float(a.cols) + 1e-5f);
             }
         }
-        uint16_t* p = static_cast<uint16_t*>(out) + at;
-        if (vec) {
-            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) p[j] = uint16_t(w[j >> 1] >> (16 * (j & 1)));
+        if (a.sums) {
+            row_reduce(unused, total, red, W, warp);
+            if (mine && part == 0 && lane == 0) a.sums[row] = total * r;
         }
     }
 }
 
-// Read back: a thread takes 8 values (4 bytes of codes, one scale).
-template <int FMT, int DT>
-__global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4DequantizeArgs a, int chunks, int64_t total,
-                                                                 int vec) {
+// Read back: a warp takes 1024 values of a row, 4 times 8 a lane (4 bytes of codes, one scale).  VEC: every row
+// of the output starts on 16 bytes and has a multiple of 8 values, so that a lane stores whole
+// 16-byte pieces; otherwise the warp hands the values round and stores 32 neighbours at a time.
+constexpr int kBack = 1024;
+
+template <int FMT, int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4DequantizeArgs a) {
     constexpr bool NV = FMT == CLEF_NVFP4;
+    __shared__ __align__(16) float stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 256];
     griddep_wait();
     griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pieces = (a.cols + kBack - 1) / kBack;
+    const uint64_t item = uint64_t(blockIdx.x) * (kThreads / 32) + warp;
+    const int64_t row = int64_t(item / uint32_t(pieces));
+    if (row >= a.rows) return;
+    const int col0 = int(item - uint64_t(row) * uint32_t(pieces)) * kBack;
     const int64_t code_stride = int64_t(a.cols + 31) / 32 * 16;
     const int kgroups = (a.cols + kFp4Tile - 1) / kFp4Tile * (NV ? 4 : 2);
-    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += int64_t(gridDim.x) * kThreads) {
-        const int64_t row = i / chunks;
-        const int chunk = int(i - row * chunks);
-        const uint32_t codes = reinterpret_cast<const uint32_t*>(a.codes + row * code_stride)[chunk];
-        const int block = NV ? chunk >> 1 : chunk >> 2;
-        const uint32_t byte = a.scales[(row / kFp4RowGroup * kgroups + (block >> 2)) * kFp4ScaleGroup + (row % 32) * 16 +
-                                       (row % kFp4RowGroup) / 32 * 4 + (block & 3)];
-        float scale, r = 1.f;
-        if constexpr (NV) {
-            scale = from_e4m3(byte);
-            r = a.row_scale[row];
-        } else {
-            scale = byte == 0xFFu ? __uint_as_float(0x7FC00000u)
-                                  : __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+    const uint8_t* codes = a.codes + row * code_stride;
+    const uint8_t* scales = a.scales + (row / kFp4RowGroup * kgroups) * kFp4ScaleGroup + (row % 32) * 16 +
+                            (row % kFp4RowGroup) / 32 * 4;
+    const float r = NV ? a.row_scale[row] : 1.f;
+    uint32_t packed[4], byte[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int col = col0 + i * 256 + lane * 8;
+        const int block = NV ? col >> 4 : col >> 5;
+        packed[i] = byte[i] = 0;
+        if (col < a.cols) {
+            packed[i] = *reinterpret_cast<const uint32_t*>(codes + col / 2);
+            byte[i] = scales[int64_t(block >> 2) * kFp4ScaleGroup + (block & 3)];
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int col = col0 + i * 256 + lane * 8;
+        if (col0 + i * 256 >= a.cols) break;  // the same for a whole warp
+        float scale;
+        if constexpr (NV) scale = from_e4m3(byte[i]);
+        else scale = byte[i] == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte[i] == 0 ? 0x00400000u : byte[i] << 23);
         uint32_t h[4];
-        unpack_e2m1(codes, h);
+        unpack_e2m1(packed[i], h);
         float v[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -393,27 +427,61 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
             v[2 * j] = f.x * scale * r;
             v[2 * j + 1] = f.y * scale * r;
         }
-        store8<DT>(a.out, row * a.row_stride + chunk * 8, v, a.cols - chunk * 8, vec != 0);
+        if constexpr (VEC) {
+            if (col >= a.cols) continue;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
+                                                  (row * a.row_stride + col) * (DT == CLEF_FP32 ? 4 : 2));
+            if constexpr (DT == CLEF_FP32) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    out[j] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                        __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (DT == CLEF_BF16) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                    else {
+                        const __half2 p = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+                        w[j] = *reinterpret_cast<const uint32_t*>(&p);
+                    }
+                }
+                *out = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+            float* to = stage[warp];
+            __syncwarp();  // the last values have been read
+            reinterpret_cast<float4*>(to)[2 * lane] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(to)[2 * lane + 1] = make_float4(v[4], v[5], v[6], v[7]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = col0 + i * 256 + j * 32 + lane;
+                if (c >= a.cols) continue;
+                const float y = to[j * 32 + lane];
+                const int64_t at = row * a.row_stride + c;
+                if constexpr (DT == CLEF_FP32) static_cast<float*>(a.out)[at] = y;
+                else if constexpr (DT == CLEF_BF16) static_cast<uint16_t*>(a.out)[at] = float_to_bf16(y);
+                else static_cast<uint16_t*>(a.out)[at] = __half_as_ushort(__float2half_rn(y));
+            }
+        }
     }
 }
 
 template <int FMT, int DT, bool VEC>
 cudaError_t quantize_rows(const Fp4QuantizeArgs& a, cudaStream_t s) {
-    // Few rows: as many warps a row as it has tiles, for latency.  Many: as few as hold the
-    // row in registers (16 tiles of 16-bit values, 8 of fp32), so that more reads are in flight
-    // and no barrier is met.
-    const int ktiles = fp4_ktiles(a.cols);
-    constexpr int kMost = DT == CLEF_FP32 ? 8 : 16;
+    // Few rows: as many warps a row as it has pieces, for latency.  Many: as few as hold the row in
+    // registers (4 pieces of 16-bit values, 2 of fp32).
+    const int pieces = (a.cols + 511) / 512;
+    constexpr int kMost = DT == CLEF_FP32 ? 2 : 4;
     const int64_t warps = int64_t(num_sms()) * 16;
     int W = 1;
-    while (W < 8 && W < ktiles && (ktiles > kMost * W || int64_t(a.rows) * W < warps)) W *= 2;
-    const int tiles = (ktiles + W - 1) / W;
+    while (W < 8 && W < pieces && (pieces > kMost * W || int64_t(a.rows) * W < warps)) W *= 2;
+    const int steps = (pieces + W - 1) / W;
     const dim3 grid(unsigned((int64_t(a.rows) * W + kThreads / 32 - 1) / (kThreads / 32)));
-    if (tiles <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1>, grid, dim3(kThreads), 0, s, a, W);
-    if (tiles <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4>, grid, dim3(kThreads), 0, s, a, W);
-    if (tiles <= 8) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 8>, grid, dim3(kThreads), 0, s, a, W);
-    if constexpr (kMost == 16)
-        if (tiles <= 16) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 16>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 2) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 2>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4>, grid, dim3(kThreads), 0, s, a, W);
     return cudaErrorInvalidValue;
 }
 
@@ -427,12 +495,12 @@ cudaError_t quantize_type(const Fp4QuantizeArgs& a, cudaStream_t s) {
 template <int FMT, int DT>
 cudaError_t dequantize_type(const Fp4DequantizeArgs& a, cudaStream_t s) {
     constexpr int size = DT == CLEF_FP32 ? 4 : 2;
-    const int vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.row_stride * size % 16 == 0 && a.cols % 8 == 0;
-    const int chunks = (a.cols + 7) / 8;
-    const int64_t total = int64_t(a.rows) * chunks;
-    const int64_t blocks = (total + kThreads - 1) / kThreads, most = int64_t(num_sms()) * 32;
-    return launch_pdl(fp4_dequantize_kernel<FMT, DT>, dim3(unsigned(blocks < most ? blocks : most)), dim3(kThreads), 0,
-                      s, a, chunks, total, vec);
+    const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.row_stride * size % 16 == 0 && a.cols % 8 == 0;
+    const int64_t items = int64_t(a.rows) * ((a.cols + kBack - 1) / kBack);
+    const int64_t blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    return launch_pdl(vec ? fp4_dequantize_kernel<FMT, DT, true> : fp4_dequantize_kernel<FMT, DT, false>,
+                      dim3(unsigned(blocks)), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

@@ -125,28 +125,6 @@ __device__ __forceinline__ void put_row_terms(float* terms, int j, float2 t) {
     p[2] = t.y;
 }
 
-// Two fp32 numbers in one register pair, and arithmetic on both at once.
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
-__device__ __forceinline__ float2 both_of(uint64_t p) {
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 // Outputs of one column and two rows from their accumulators.
 __device__ __forceinline__ float2 finish2(float acc0, float acc1, const ColumnTerms& c, const float4& t) {
     const uint64_t acc = mul2(pair_of(acc0, acc1), pair_of(c.scale, c.scale));
