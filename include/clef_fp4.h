@@ -80,6 +80,18 @@ CLEF_API int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float*
                               const float* rstd, const float* sums, int32_t dtype, void* out, int64_t row_stride,
                               int32_t* flags, void* stream);
 
+/* Bytes of scratch that clef_fp4_linear needs for `rows` rows of `cols` values. */
+CLEF_API int clef_fp4_linear_scratch(int32_t format, int32_t rows, int32_t cols, size_t* bytes);
+
+/* A layer with 4-bit weights: clef_fp4_quantize of the `rows` rows x in w's format, then clef_fp4_product with
+ * w, the same numbers by one call.  With `sums` (of w's rows) the rows are normalized as there, and their
+ * mean and rstd ([rows] fp32, both needed then) come back too; without, all three are NULL.
+ * scratch: 256-byte aligned device memory of the call's own until it has run. */
+CLEF_API int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
+                             const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride,
+                             float* mean, float* rstd, void* scratch, size_t scratch_bytes, int32_t* flags,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

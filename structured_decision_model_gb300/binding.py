@@ -25,6 +25,7 @@ EXPORTED = [
     "clef_stream_finish_f16", "clef_cache_size", "clef_cache_plan", "clef_cache_append", "clef_cache_read",
     "clef_cache_attend_workspace", "clef_cache_attend", "clef_cache_status", "clef_memory_store",
     "clef_stream_finish_memory", "clef_fp4_size", "clef_fp4_quantize", "clef_fp4_dequantize", "clef_fp4_product",
+    "clef_fp4_linear_scratch", "clef_fp4_linear",
 ]
 BF16, FP16, FP32 = 0, 1, 2   # clef_dtype
 CACHE_MAX_REQUESTS = 1024
@@ -122,6 +123,8 @@ def load():
     lib.clef_fp4_quantize.argtypes = [fp4, _i32, _vp, _i64, _vp, _vp, _vp, _vp]
     lib.clef_fp4_dequantize.argtypes = [fp4, _i32, _vp, _i64, _vp]
     lib.clef_fp4_product.argtypes = [fp4, fp4, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
+    lib.clef_fp4_linear_scratch.argtypes = [_i32, _i32, _i32, ctypes.POINTER(_sz)]
+    lib.clef_fp4_linear.argtypes = [fp4, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _vp]
     for name in EXPORTED:
         if name not in ("clef_weight_count", "clef_status_string", "clef_kernel_launches"):
             getattr(lib, name).restype = ctypes.c_int
@@ -360,3 +363,15 @@ def clef_fp4_product(x: ClefFp4, w: ClefFp4, bias_ptr, mean_ptr, rstd_ptr, sums_
                      flags_ptr, stream=0):
     _check(load().clef_fp4_product(x, w, bias_ptr, mean_ptr, rstd_ptr, sums_ptr, dtype, out_ptr, row_stride, flags_ptr,
                                    stream), "clef_fp4_product")
+
+
+def clef_fp4_linear_scratch(format, rows, cols):
+    out = _sz(0)
+    _check(load().clef_fp4_linear_scratch(format, rows, cols, ctypes.byref(out)), "clef_fp4_linear_scratch")
+    return out.value
+
+
+def clef_fp4_linear(w: ClefFp4, x_dtype, x_ptr, x_stride, rows, bias_ptr, sums_ptr, dtype, out_ptr, row_stride, mean_ptr,
+                    rstd_ptr, scratch_ptr, scratch_bytes, flags_ptr, stream=0):
+    _check(load().clef_fp4_linear(w, x_dtype, x_ptr, x_stride, rows, bias_ptr, sums_ptr, dtype, out_ptr, row_stride,
+                                  mean_ptr, rstd_ptr, scratch_ptr, scratch_bytes, flags_ptr, stream), "clef_fp4_linear")

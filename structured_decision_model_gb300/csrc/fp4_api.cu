@@ -61,6 +61,64 @@ bool bad_rows(const void* p, int dtype, int64_t stride, int64_t least) {
     return !p || misaligned(p, uintptr_t(size_of(dtype))) || stride < least || stride > (int64_t(1) << 31);
 }
 
+int check_product(const clef_fp4& x, const clef_fp4& w, const float* bias, const float* mean, const float* rstd,
+                  const float* sums, int dtype, const void* out, int64_t row_stride, const int32_t* flags) {
+    if (x.format != w.format || x.cols != w.cols || bad_type(dtype) || bad_rows(out, dtype, row_stride, w.rows) ||
+        !mean != !rstd || !mean != !sums || !flags)
+        return CLEF_ERR_INVALID_ARGUMENT;
+    for (const void* p : {static_cast<const void*>(bias), static_cast<const void*>(mean), static_cast<const void*>(rstd),
+                          static_cast<const void*>(sums), static_cast<const void*>(flags)})
+        if (misaligned(p, 4)) return CLEF_ERR_INVALID_ARGUMENT;
+    // output tiles are counted in 32 bits
+    if ((int64_t(x.rows) + 31) / 32 * ((int64_t(w.rows) + 127) / 128) >= kInt32 / 16) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    const int64_t m4 = int64_t(x.rows) * 4, n4 = int64_t(w.rows) * 4;
+    const Run to = rows_run(out, x.rows, row_stride, w.rows, size_of(dtype));
+    for (const Run& r : {codes_run(x), scales_run(x), row_scale_run(x), codes_run(w), scales_run(w), row_scale_run(w),
+                         Run(bias, n4), Run(mean, m4), Run(rstd, m4), Run(sums, n4), Run(flags, 4)})
+        if (to.meets(r)) return CLEF_ERR_INVALID_ARGUMENT;
+    return CLEF_OK;
+}
+
+// A checked product.  `w_settled`: nothing that may still run on the stream writes w.
+int multiply(const clef_fp4& x, const clef_fp4& w, const float* bias, const float* mean, const float* rstd,
+             const float* sums, int dtype, void* out, int64_t row_stride, int32_t* flags, bool w_settled, void* stream) {
+    Fp4ProductArgs a{};
+    a.x_scale = x.format == CLEF_NVFP4 ? x.row_scale : nullptr;
+    a.w_scale = w.format == CLEF_NVFP4 ? w.row_scale : nullptr;
+    a.bias = bias;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.sums = sums;
+    a.out = out;
+    a.ldo = row_stride;
+    a.flags = flags;
+    a.M = x.rows;
+    a.N = w.rows;
+    a.k64 = (x.cols + 63) / 64;
+    a.kgroups = fp4_kgroups(x.format, x.cols);
+    a.splits = 1;
+    a.paired = dtype != CLEF_FP32 && row_stride % 2 == 0 && w.rows % 2 == 0 && !misaligned(out, 4);
+    a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && !misaligned(out, 16);
+    a.w_settled = w_settled;
+    return launch_fp4_product(x, w, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK : CLEF_ERR_CUDA;
+}
+
+// Where the rows of a layer's call lie in its scratch.
+struct Scratch {
+    size_t scales, row_scale, total;
+    Scratch(int format, int rows, int cols) {
+        const clef_fp4 q{nullptr, nullptr, nullptr, rows, cols, format};
+        scales = (size_t(codes_bytes(q)) + 255) / 256 * 256;
+        row_scale = scales + (size_t(scales_bytes(q)) + 255) / 256 * 256;
+        total = row_scale + (format == CLEF_NVFP4 ? size_t(rows) * 4 : 0);
+    }
+    clef_fp4 matrix(void* base, int format, int rows, int cols) const {
+        uint8_t* b = static_cast<uint8_t*>(base);
+        return clef_fp4{b, b + scales, format == CLEF_NVFP4 ? reinterpret_cast<float*>(b + row_scale) : nullptr, rows, cols,
+                        format};
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -113,39 +171,46 @@ int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, co
                      const float* sums, int32_t dtype, void* out, int64_t row_stride, int32_t* flags, void* stream) {
     int st = check_matrix(x);
     if (st == CLEF_OK) st = check_matrix(w);
+    if (st == CLEF_OK) st = check_product(*x, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags);
     if (st != CLEF_OK) return st;
-    if (x->format != w->format || x->cols != w->cols || bad_type(dtype) || bad_rows(out, dtype, row_stride, w->rows) ||
-        !mean != !rstd || !mean != !sums || !flags)
+    return multiply(*x, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, false, stream);
+}
+
+int clef_fp4_linear_scratch(int32_t format, int32_t rows, int32_t cols, size_t* bytes) {
+    if (!bytes) return CLEF_ERR_INVALID_ARGUMENT;
+    const int st = check_size(format, rows, cols);
+    if (st != CLEF_OK) return st;
+    *bytes = Scratch(format, rows, cols).total;
+    return CLEF_OK;
+}
+
+int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows, const float* bias,
+                    const float* sums, int32_t dtype, void* out, int64_t row_stride, float* mean, float* rstd,
+                    void* scratch, size_t scratch_bytes, int32_t* flags, void* stream) {
+    int st = check_matrix(w);
+    if (st == CLEF_OK) st = check_size(w->format, rows, w->cols);
+    if (st != CLEF_OK) return st;
+    if (bad_type(x_dtype) || bad_rows(x, x_dtype, x_stride, 0) || !scratch || misaligned(scratch, 256))
         return CLEF_ERR_INVALID_ARGUMENT;
-    for (const void* p : {static_cast<const void*>(bias), static_cast<const void*>(mean), static_cast<const void*>(rstd),
-                          static_cast<const void*>(sums), static_cast<const void*>(flags)})
-        if (misaligned(p, 4)) return CLEF_ERR_INVALID_ARGUMENT;
-    // output tiles are counted in 32 bits
-    if ((int64_t(x->rows) + 31) / 32 * ((int64_t(w->rows) + 127) / 128) >= kInt32 / 16) return CLEF_ERR_UNSUPPORTED_CONFIG;
-    const int64_t m4 = int64_t(x->rows) * 4, n4 = int64_t(w->rows) * 4;
-    const Run to = rows_run(out, x->rows, row_stride, w->rows, size_of(dtype));
-    for (const Run& r : {codes_run(*x), scales_run(*x), row_scale_run(*x), codes_run(*w), scales_run(*w),
-                         row_scale_run(*w), Run(bias, n4), Run(mean, m4), Run(rstd, m4), Run(sums, n4), Run(flags, 4)})
-        if (to.meets(r)) return CLEF_ERR_INVALID_ARGUMENT;
-    Fp4ProductArgs a{};
-    a.x_scale = x->format == CLEF_NVFP4 ? x->row_scale : nullptr;
-    a.w_scale = w->format == CLEF_NVFP4 ? w->row_scale : nullptr;
-    a.bias = bias;
-    a.mean = mean;
-    a.rstd = rstd;
-    a.sums = sums;
-    a.out = out;
-    a.ldo = row_stride;
-    a.flags = flags;
-    a.M = x->rows;
-    a.N = w->rows;
-    a.k64 = (x->cols + 63) / 64;
-    a.kgroups = fp4_kgroups(x->format, x->cols);
-    a.splits = 1;
-    a.paired = dtype != CLEF_FP32 && row_stride % 2 == 0 && w->rows % 2 == 0 && !misaligned(out, 4);
-    a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && !misaligned(out, 16);
-    return launch_fp4_product(*x, *w, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
-                                                                                                  : CLEF_ERR_CUDA;
+    const Scratch S(w->format, rows, w->cols);
+    if (scratch_bytes < S.total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+    const clef_fp4 q = S.matrix(scratch, w->format, rows, w->cols);
+    st = check_product(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags);
+    if (st != CLEF_OK) return st;
+    // what is written: the scratch, the statistics and the output, apart from each other and from what is read
+    const int64_t m4 = int64_t(rows) * 4, n4 = int64_t(w->rows) * 4;
+    const Run space(scratch, int64_t(S.total)), in = rows_run(x, rows, x_stride, w->cols, size_of(x_dtype)),
+        to = rows_run(out, rows, row_stride, w->rows, size_of(dtype));
+    const Run reads[] = {in, codes_run(*w), scales_run(*w), row_scale_run(*w), Run(bias, n4), Run(sums, n4), Run(flags, 4)};
+    for (const Run& r : reads)
+        if (r.meets(space) || r.meets(Run(mean, m4)) || r.meets(Run(rstd, m4))) return CLEF_ERR_INVALID_ARGUMENT;
+    if (to.meets(in) || to.meets(space) || space.meets(Run(mean, m4)) || space.meets(Run(rstd, m4)) ||
+        Run(mean, m4).meets(Run(rstd, m4)))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    const Fp4QuantizeArgs a{x, x_stride, static_cast<uint8_t*>(q.codes), static_cast<uint8_t*>(q.scales), q.row_scale,
+                            mean, rstd, nullptr, rows, w->cols};
+    if (launch_fp4_quantize(a, w->format, x_dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CLEF_ERR_CUDA;
+    return multiply(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, true, stream);
 }
 
 }  // extern "C"

@@ -310,24 +310,35 @@ __global__ void __launch_bounds__(kThreads) fp4_tile_kernel(const __grid_constan
     const int wt = tile % n_wt, xt = tile / n_wt;  // w's tiles next to each other share x's rows
     const int ktiles = (args.k64 + 3) / 4;
     const int kt0 = int(int64_t(sp) * ktiles / S), kt1 = int(int64_t(sp + 1) * ktiles / S);
-    griddep_wait();
-    griddep_launch();
-
     if (warp == 0) {
         if (lane == 0) {
+            auto load_w = [&](int kt, int s) {
+                uint8_t* st = smem + s * C::STAGE;
+                tma_load_2d(st, &tmW, kt * kAtomBytes, wt * kWRows, &full[s]);
+                tma_load_2d(st + kWBytes + C::X_BYTES, &tmSW, 0, wt * args.kgroups + kt * C::GROUPS, &full[s]);
+            };
+            // what does not come from the kernel before this one is asked for while that still runs
+            const int ahead = args.w_settled ? min(C::STAGES, kt1 - kt0) : 0;
+            for (int k = 0; k < ahead; ++k) {
+                mbar_arrive_expect_tx(&full[k], C::STAGE);
+                load_w(kt0 + k, k);
+            }
+            griddep_wait();
+            griddep_launch();
             bool ok = true;
             int i = 0, s = 0;  // stages filled so far, and the next one
             uint32_t phase = 1;
             for (int kt = kt0; kt < kt1; ++kt, ++i) {
-                if (!mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags)) {
-                    ok = false;
-                    break;
+                if (i >= ahead) {
+                    if (!mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&full[s], C::STAGE);
+                    load_w(kt, s);
                 }
                 uint8_t* st = smem + s * C::STAGE;
-                mbar_arrive_expect_tx(&full[s], C::STAGE);
-                tma_load_2d(st, &tmW, kt * kAtomBytes, wt * kWRows, &full[s]);
                 tma_load_2d(st + kWBytes, &tmX, kt * kAtomBytes, xt * BN, &full[s]);
-                tma_load_2d(st + kWBytes + C::X_BYTES, &tmSW, 0, wt * args.kgroups + kt * C::GROUPS, &full[s]);
                 // x's scales of the 128-row group that the tile lies in (tiles of fewer rows: the first)
                 tma_load_2d(st + kWBytes + C::X_BYTES + C::S_BYTES, &tmSX, 0,
                             xt * BN / kFp4RowGroup * args.kgroups + kt * C::GROUPS, &full[s]);
@@ -384,6 +395,7 @@ __global__ void __launch_bounds__(kThreads) fp4_tile_kernel(const __grid_constan
         if (!mbar_wait_bounded(done, 0, nullptr, args.flags) || !ok) *abort_flag = 1;
         __syncwarp();
     } else {
+        griddep_wait();  // the row terms may come from the kernel before
         const int t = int(threadIdx.x) - 64;
         const int quarter = warp & 3, half = t >> 7;  // TMEM lanes that this warp may read; its half of the columns
         const int row = quarter * 32 + lane, n = wt * kWRows + row;

@@ -23,9 +23,8 @@ BLOCK = {"mxfp4": 32, "nvfp4": 16}
 _FP32 = torch.float32
 
 
-def _sizes(format: int, rows: int, cols: int) -> Tuple[int, int]:
-    """Bytes of codes and scales (clef_fp4_size, without a call into the library)."""
-    return rows * ((cols + 31) // 32 * 16), (rows + 127) // 128 * ((cols + 255) // 256 * (2048 if format else 1024))
+# (input type, output type asked for): their codes, and the output's type
+_TYPES = {(a, b): (_DTYPES[a], _DTYPES[b or a], b or a) for a in _DTYPES for b in (None, *_DTYPES)}
 
 
 def _up(n: int) -> int:
@@ -48,21 +47,22 @@ class Fp4Matrix:
             _refuse(f"format: one of {sorted(FORMATS)}")
         if not 1 <= rows < 2 ** 31 - 256 or not 1 <= cols <= B.FP4_MAX_COLS:
             _refuse(f"an Fp4Matrix has 1 to 2^31 - 257 rows of 1 to {B.FP4_MAX_COLS} values")
-        codes, scales = _sizes(code, rows, cols)
-        at = _up(codes)
-        size = at + _up(scales) + (4 * rows if code == B.NVFP4 else 0)
+        # codes, scales and row scales, each from 256 bytes on (sizes as clef_fp4_size gives them)
+        scales = _up(rows * ((cols + 31) // 32 * 16))
+        row_scale = scales + (rows + 127) // 128 * ((cols + 255) // 256 * (2048 if code else 1024))
+        size = row_scale + (4 * rows if code else 0)
         if data is None:
             data = torch.empty(size, dtype=torch.uint8, device=device)
         elif data.dtype != torch.uint8 or data.dim() != 1 or data.numel() != size or not data.is_contiguous() or \
                 data.data_ptr() % 256:
             _refuse("Fp4Matrix: data is not a contiguous uint8 vector of size_bytes on 256 bytes")
-        if data.device.type != "cuda":
+        index = data.get_device()
+        if index < 0:
             _refuse("Fp4Matrix: data is not on a GPU")
         base = data.data_ptr()
         self.rows, self.cols, self.format, self.data = rows, cols, format, data
-        self.struct = B.ClefFp4(base, base + at, base + at + _up(scales) if code == B.NVFP4 else None, rows, cols, code)
-        self.device = data.device
-        self._index = data.device.index
+        self.struct = B.ClefFp4(base, base + scales, base + row_scale if code else None, rows, cols, code)
+        self.device, self._index = data.device, index
         self.mean = self.rstd = self.sums = self._flags = None
 
     @property
@@ -78,13 +78,14 @@ class Fp4Matrix:
 
     def dequantize(self, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """What the rows stand for, [rows, cols] in ``dtype`` (bf16, fp16 or fp32), rounded once."""
+        given = out is not None
         out = _out(out, self.rows, self.cols, dtype, self.device)
-        if _overlap(out, self.data):
+        if given and _overlap(out, self.data):
             _refuse("out lies apart from what is read")
         if _current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.dequantize(dtype, out)
-        B.clef_fp4_dequantize(self.struct, _DTYPES[dtype], out.data_ptr(), out.stride(0), _raw_stream(self._index))
+        B.clef_fp4_dequantize(self.struct, _DTYPES[dtype], out.data_ptr(), _row_stride(out), _raw_stream(self._index))
         return out
 
     def device_status(self) -> int:
@@ -112,18 +113,21 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
+_lib = B.load
+
+
 def quantize(x: torch.Tensor, format: str = "nvfp4", stats: bool = False, sums: bool = False,
              out: Optional[Fp4Matrix] = None) -> Fp4Matrix:
     """Rows x [rows, cols] (bf16, fp16 or fp32, any row stride, values contiguous) in 4 bits.
 
     ``stats``: also the rows' ``mean`` and ``rstd`` = 1 / sqrt(variance + 1e-5); ``sums``: also the
     sums of what the rows stand for once kept."""
-    dtype = _DTYPES.get(x.dtype)
-    if dtype is None or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or x.device.type != "cuda":
+    dtype, shape, strides = _DTYPES.get(x.dtype), x.shape, x.stride()
+    if dtype is None or len(shape) != 2 or (strides[1] != 1 and shape[1] > 1) or not x.is_cuda:
         _refuse("x: bf16, fp16 or fp32 [rows, cols], values of a row contiguous, on a GPU")
     if x.requires_grad and torch.is_grad_enabled():
         _refuse("x requires a gradient, which 4-bit rows do not pass on")
-    rows, cols = x.shape
+    rows, cols = shape
     if out is None:
         out = Fp4Matrix(rows, cols, format, x.device)
     elif (out.rows, out.cols, out.format, out.device) != (rows, cols, format, x.device):
@@ -131,15 +135,18 @@ def quantize(x: torch.Tensor, format: str = "nvfp4", stats: bool = False, sums: 
     if _current_device() != out._index:
         with torch.cuda.device(out._index):
             return quantize(x, format, stats, sums, out)
-    out.mean = out.rstd = out.sums = None
-    mean = rstd = total = None
+    out.mean = out.rstd = out.sums = mean = rstd = total = None
     if stats:
-        out.mean, out.rstd = torch.empty((2, rows), dtype=_FP32, device=x.device).unbind(0)
+        out.mean = torch.empty(rows, dtype=_FP32, device=x.device)
+        out.rstd = torch.empty(rows, dtype=_FP32, device=x.device)
         mean, rstd = out.mean.data_ptr(), out.rstd.data_ptr()
     if sums:
         out.sums = torch.empty(rows, dtype=_FP32, device=x.device)
         total = out.sums.data_ptr()
-    B.clef_fp4_quantize(out.struct, dtype, x.data_ptr(), _row_stride(x), mean, rstd, total, _raw_stream(out._index))
+    status = _lib().clef_fp4_quantize(out.struct, dtype, x.data_ptr(), strides[0] if rows > 1 else cols, mean, rstd, total,
+                                      _raw_stream(out._index))
+    if status:
+        raise B.ClefError(status, "clef_fp4_quantize")
     return out
 
 
@@ -189,34 +196,66 @@ class Fp4Linear:
                 _refuse("bias: [outs] on the weight's device")
             bias = bias.detach().to(_FP32).contiguous()
         self.bias = bias
-        weight.flags  # made here, outside of any later capture
+        self._bias = None if bias is None else bias.data_ptr()
+        self._flags = weight.flags.data_ptr()  # made here, outside of any later capture
+        self._device, self._index = weight.device, weight._index
+        self._lib, self._struct = B.load(), weight.struct
+        self._scratch = {}  # scratch bytes of the numbers of rows that the layer has met
 
     def _run(self, x, dtype, normalized):
-        dtype = x.dtype if dtype is None else dtype
-        if x.dim() < 1 or x.shape[-1] != self.cols or x.device != self.weight.device:
+        """Outputs, means and rstds of x's rows (the latter None where not ``normalized``)."""
+        types, shape = _TYPES.get((x.dtype, dtype)), x.shape
+        if types is None:
+            _refuse("inputs and outputs: bf16, fp16 or fp32")
+        if x.get_device() != self._index or not shape or shape[-1] != self.cols:
             _refuse(f"x: [..., {self.cols}] on the weight's device")
-        lead = x.shape[:-1]
-        rows = x if x.dim() == 2 else x.reshape(-1, self.cols)
-        if rows.shape[0] == 0:
-            if dtype not in _DTYPES or x.dtype not in _DTYPES:
-                _refuse("inputs and outputs: bf16, fp16 or fp32")
-            q, y = None, torch.empty((0, self.outs), dtype=dtype, device=x.device)
-        else:
-            q = quantize(rows, self.format, stats=normalized)
-            y = product(q, self.weight, self.bias, dtype, normalized)
-        return q, y if x.dim() == 2 else y.view(*lead, self.outs)
+        if x.requires_grad and torch.is_grad_enabled():
+            _refuse("x requires a gradient, which a 4-bit layer does not pass on")
+        rows = x if len(shape) == 2 else x.reshape(-1, self.cols)
+        stride, step = rows.stride()
+        if step != 1 and self.cols > 1:
+            rows = rows.contiguous()
+            stride = self.cols
+        n = rows.shape[0]
+        x_type, out_type, dtype = types
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self._run(x, dtype, normalized)
+        y = torch.empty((n, self.outs), dtype=dtype, device=self._device)
+        mean = rstd = mean_at = rstd_at = sums_at = None
+        if normalized:
+            if self.weight.sums is None:
+                _refuse("normalized: the weight has no sums")
+            mean = torch.empty(n, dtype=_FP32, device=self._device)
+            rstd = torch.empty(n, dtype=_FP32, device=self._device)
+            mean_at, rstd_at, sums_at = mean.data_ptr(), rstd.data_ptr(), self.weight.sums.data_ptr()
+        if n:
+            # a buffer of the call's own: overlapping calls and captured graphs never share one
+            size = self._scratch.get(n)
+            if size is None:
+                if len(self._scratch) >= 4096:
+                    self._scratch.clear()
+                size = self._scratch[n] = B.clef_fp4_linear_scratch(self.weight.struct.format, n, self.cols)
+            scratch = torch.empty(size, dtype=torch.uint8, device=self._device)
+            status = self._lib.clef_fp4_linear(
+                self._struct, x_type, rows.data_ptr(), stride if n > 1 else self.cols, n, self._bias, sums_at, out_type,
+                y.data_ptr(), self.outs, mean_at, rstd_at, scratch.data_ptr(), size, self._flags,
+                _raw_stream(self._index))
+            if status:
+                raise B.ClefError(status, "clef_fp4_linear")
+        if len(shape) != 2:
+            y = y.view(*shape[:-1], self.outs)
+            if normalized:
+                mean, rstd = mean.view(shape[:-1]), rstd.view(shape[:-1])
+        return y, mean, rstd
 
     def __call__(self, x: torch.Tensor, dtype=None) -> torch.Tensor:
-        """x [..., cols] through the layer: [..., outs] in ``dtype`` (x's own by default)."""
-        return self._run(x, dtype, False)[1]
+        """x [..., cols] (bf16, fp16 or fp32) through the layer: [..., outs] in ``dtype`` (x's own by default)."""
+        return self._run(x, dtype, False)[0]
 
     def normalized(self, x: torch.Tensor, dtype=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """The layer behind a LayerNorm: outputs, and the rows' mean and 1 / sqrt(variance + 1e-5) (fp32 [...])."""
-        q, y = self._run(x, dtype, True)
-        if q is None:
-            mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=_FP32, device=x.device).unbind(0)
-            return y, mean, rstd
-        return y, q.mean.view(x.shape[:-1]), q.rstd.view(x.shape[:-1])
+        return self._run(x, dtype, True)
 
     def device_status(self) -> int:
         """Waits for the current stream, reads and clears what the layer's products reported."""
