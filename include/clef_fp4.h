@@ -92,6 +92,38 @@ CLEF_API int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, 
                              float* mean, float* rstd, void* scratch, size_t scratch_bytes, int32_t* flags,
                              void* stream);
 
+/* ---- the head with its memory K/V projection in 4 bits ---- */
+
+/* The K/V weights of every routing layer (with the memory LayerNorm's weight, as clef_prepare_weights left
+ * them in `prepared`) into w (2 * n_route * width rows of `hidden` values, of either format), and the sums
+ * of w's rows (fp32). */
+CLEF_API int clef_fp4_memory_weights(const clef_config* cfg, const void* prepared, const clef_fp4* w, float* sums,
+                                     void* stream);
+
+/* Bytes of scratch for n_rows streamed rows, and for a whole forward pass of the schema. */
+CLEF_API int clef_stream_rows_fp4_scratch(const clef_config* cfg, int32_t format, int32_t n_rows, size_t* bytes);
+CLEF_API int clef_head_forward_fp4_scratch(const clef_config* cfg, int32_t format, const clef_schema* schema,
+                                           size_t* bytes);
+
+/* clef_stream_rows with the rows and the weights in 4 bits: `hidden` is bf16 or fp16 (quantised as it is), w and
+ * sums come from clef_fp4_memory_weights.  A row's keys and values depend on the row alone, up to the
+ * order in which fp32 sums of other numbers of rows a call are added.  Chunks of a schema may mix
+ * this call and the others; clef_stream_finish and its kin follow as ever. */
+CLEF_API int clef_stream_rows_fp4(const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,
+                                  const clef_schema* schema, const void* hidden, int32_t hidden_dtype, int32_t record,
+                                  int32_t row0, int32_t n_rows, void* workspace, size_t workspace_bytes, void* scratch,
+                                  size_t scratch_bytes, void* stream);
+
+/* The forward pass over such a projection: clef_stream_begin, every record's rows, and the finish in one
+ * call.  Records whose rows lie one after the other without a gap, here and in the workspace, are
+ * projected together. */
+CLEF_API int clef_head_forward_fp4(const clef_config* cfg, const void* const* weights, const void* prepared,
+                                   const clef_fp4* w, const float* sums, const clef_schema* schema, const void* hidden,
+                                   int32_t hidden_dtype, const int32_t* token_ids, const uint16_t* lexical, float* logits,
+                                   float* probs, float* q_value, float* q_conf, int32_t* q_argmax, void* workspace,
+                                   size_t workspace_bytes, void* scratch, size_t scratch_bytes,
+                                   const clef_debug_outputs* debug, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,7 +25,8 @@ EXPORTED = [
     "clef_stream_finish_f16", "clef_cache_size", "clef_cache_plan", "clef_cache_append", "clef_cache_read",
     "clef_cache_attend_workspace", "clef_cache_attend", "clef_cache_status", "clef_memory_store",
     "clef_stream_finish_memory", "clef_fp4_size", "clef_fp4_quantize", "clef_fp4_dequantize", "clef_fp4_product",
-    "clef_fp4_linear_scratch", "clef_fp4_linear",
+    "clef_fp4_linear_scratch", "clef_fp4_linear", "clef_fp4_memory_weights", "clef_stream_rows_fp4_scratch",
+    "clef_head_forward_fp4_scratch", "clef_stream_rows_fp4", "clef_head_forward_fp4",
 ]
 BF16, FP16, FP32 = 0, 1, 2   # clef_dtype
 CACHE_MAX_REQUESTS = 1024
@@ -125,6 +126,13 @@ def load():
     lib.clef_fp4_product.argtypes = [fp4, fp4, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
     lib.clef_fp4_linear_scratch.argtypes = [_i32, _i32, _i32, ctypes.POINTER(_sz)]
     lib.clef_fp4_linear.argtypes = [fp4, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _vp]
+    cfg, schema = ctypes.POINTER(ClefConfig), ctypes.POINTER(ClefSchema)
+    lib.clef_fp4_memory_weights.argtypes = [cfg, _vp, fp4, _vp, _vp]
+    lib.clef_stream_rows_fp4_scratch.argtypes = [cfg, _i32, _i32, ctypes.POINTER(_sz)]
+    lib.clef_head_forward_fp4_scratch.argtypes = [cfg, _i32, schema, ctypes.POINTER(_sz)]
+    lib.clef_stream_rows_fp4.argtypes = [cfg, _vp, fp4, _vp, schema, _vp, _i32, _i32, _i32, _i32, _vp, _sz, _vp, _sz, _vp]
+    lib.clef_head_forward_fp4.argtypes = [cfg, ctypes.POINTER(_vp), _vp, fp4, _vp, schema, _vp, _i32, _vp, _vp, _vp, _vp,
+                                          _vp, _vp, _vp, _vp, _sz, _vp, _sz, ctypes.POINTER(ClefDebugOutputs), _vp]
     for name in EXPORTED:
         if name not in ("clef_weight_count", "clef_status_string", "clef_kernel_launches"):
             getattr(lib, name).restype = ctypes.c_int
@@ -375,3 +383,39 @@ def clef_fp4_linear(w: ClefFp4, x_dtype, x_ptr, x_stride, rows, bias_ptr, sums_p
                     rstd_ptr, scratch_ptr, scratch_bytes, flags_ptr, stream=0):
     _check(load().clef_fp4_linear(w, x_dtype, x_ptr, x_stride, rows, bias_ptr, sums_ptr, dtype, out_ptr, row_stride,
                                   mean_ptr, rstd_ptr, scratch_ptr, scratch_bytes, flags_ptr, stream), "clef_fp4_linear")
+
+
+def clef_fp4_memory_weights(cfg, prepared_ptr, w: ClefFp4, sums_ptr, stream=0):
+    _check(load().clef_fp4_memory_weights(ctypes.byref(cfg), prepared_ptr, w, sums_ptr, stream), "clef_fp4_memory_weights")
+
+
+def clef_stream_rows_fp4_scratch(cfg, format, n_rows):
+    out = _sz(0)
+    _check(load().clef_stream_rows_fp4_scratch(ctypes.byref(cfg), format, n_rows, ctypes.byref(out)),
+           "clef_stream_rows_fp4_scratch")
+    return out.value
+
+
+def clef_head_forward_fp4_scratch(cfg, format, schema: Schema):
+    out = _sz(0)
+    _check(load().clef_head_forward_fp4_scratch(ctypes.byref(cfg), format, ctypes.byref(schema.struct), ctypes.byref(out)),
+           "clef_head_forward_fp4_scratch")
+    return out.value
+
+
+def clef_stream_rows_fp4(cfg, prepared_ptr, w: ClefFp4, sums_ptr, schema: Schema, hidden_ptr, hidden_dtype, record, row0,
+                         n_rows, workspace_ptr, workspace_bytes, scratch_ptr, scratch_bytes, stream=0):
+    _check(load().clef_stream_rows_fp4(ctypes.byref(cfg), prepared_ptr, w, sums_ptr, ctypes.byref(schema.struct), hidden_ptr,
+                                       hidden_dtype, record, row0, n_rows, workspace_ptr, workspace_bytes, scratch_ptr,
+                                       scratch_bytes, stream), "clef_stream_rows_fp4")
+
+
+def clef_head_forward_fp4(cfg, weight_ptrs, prepared_ptr, w: ClefFp4, sums_ptr, schema: Schema, hidden_ptr, hidden_dtype,
+                          token_ids_ptr, lexical_ptr, logits_ptr, probs_ptr, q_value_ptr, q_conf_ptr, q_argmax_ptr,
+                          workspace_ptr, workspace_bytes, scratch_ptr, scratch_bytes, debug=None, stream=0):
+    arr = (_vp * len(weight_ptrs))(*weight_ptrs)
+    dbg = ctypes.byref(debug) if debug is not None else None
+    _check(load().clef_head_forward_fp4(ctypes.byref(cfg), arr, prepared_ptr, w, sums_ptr, ctypes.byref(schema.struct),
+                                        hidden_ptr, hidden_dtype, token_ids_ptr, lexical_ptr, logits_ptr, probs_ptr,
+                                        q_value_ptr, q_conf_ptr, q_argmax_ptr, workspace_ptr, workspace_bytes, scratch_ptr,
+                                        scratch_bytes, dbg, stream), "clef_head_forward_fp4")

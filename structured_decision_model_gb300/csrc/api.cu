@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "../../include/clef_cache.h"
+#include "../../include/clef_fp4.h"
 #include "../../include/clef_head.h"
 #include "common.cuh"
 #include "head_kernels.h"
@@ -1082,6 +1083,141 @@ int clef_stream_finish_memory(const clef_config* cfg, const void* const* weights
     return forward_impl(cfg, weights, prepared, schema, static_cast<const uint16_t*>(hidden), token_ids, lexical, logits,
                         probs, q_value, q_conf, q_argmax, workspace, workspace_bytes, debug, stream, kForwardMemory,
                         hidden_dtype == CLEF_FP16, &mem);
+}
+
+}  // extern "C"
+
+namespace {
+
+// 4-bit K/V weights of this head.
+bool fp4_weights_fit(const clef_config* cfg, const clef_fp4* w, const float* sums) {
+    return w && sums && w->rows == 2 * cfg->n_route * cfg->width && w->cols == cfg->hidden;
+}
+
+int check_fp4_rows(const void* prepared, const void* hidden, int32_t dtype, const void* workspace, const void* scratch) {
+    if (!prepared || !hidden || !workspace || !scratch || (dtype != CLEF_BF16 && dtype != CLEF_FP16) ||
+        ((reinterpret_cast<uintptr_t>(prepared) | reinterpret_cast<uintptr_t>(workspace) |
+          reinterpret_cast<uintptr_t>(scratch)) & 255) || (reinterpret_cast<uintptr_t>(hidden) & 15))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    return CLEF_OK;
+}
+
+// K/V and statistics of `rows` rows of `hidden` from padded row `from` on, into compact rows `to` on.
+int project_fp4(const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,
+                const clef_schema* schema, const WsLayout& L, const void* hidden, int32_t dtype, int64_t from, int64_t to,
+                int64_t rows, void* workspace, void* scratch, size_t scratch_bytes, void* stream) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const PreparedLayout PL(cfg);
+    const int64_t NKV = int64_t(2) * cfg->n_route * cfg->width;
+    const int s = clef_fp4_linear(
+        w, dtype, static_cast<const uint16_t*>(hidden) + from * schema->row_stride, schema->row_stride, int32_t(rows),
+        reinterpret_cast<const float*>(static_cast<const uint8_t*>(prepared) + PL.bkv), sums, CLEF_BF16,
+        reinterpret_cast<uint16_t*>(ws + L.kv) + to * NKV, NKV, reinterpret_cast<float*>(ws + L.mu) + to,
+        reinterpret_cast<float*>(ws + L.rstd) + to, scratch, scratch_bytes, reinterpret_cast<int32_t*>(ws + L.flags), stream);
+    return s;
+}
+
+// Records b .. (the return value) - 1 whose rows follow each other without a gap, in `hidden` and in the
+// workspace, from record b on; *rows of them.
+int fp4_run(const clef_schema* schema, const Plan& p, int b, int64_t* rows) {
+    const int32_t* off = p.blob.data() + p.rec_row_off;
+    *rows = schema->lengths[b];
+    int e = b + 1;
+    while (e < schema->B && schema->lengths[e - 1] == schema->Lpad && off[e] == off[b] + *rows) *rows += schema->lengths[e++];
+    return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+int clef_fp4_memory_weights(const clef_config* cfg, const void* prepared, const clef_fp4* w, float* sums, void* stream) {
+    if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    if (!prepared || (reinterpret_cast<uintptr_t>(prepared) & 255) || !fp4_weights_fit(cfg, w, sums))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    const PreparedLayout PL(cfg);
+    return clef_fp4_quantize(w, CLEF_BF16, static_cast<const uint8_t*>(prepared) + PL.wkv, cfg->hidden, nullptr, nullptr,
+                             sums, stream);
+}
+
+int clef_stream_rows_fp4_scratch(const clef_config* cfg, int32_t format, int32_t n_rows, size_t* bytes) {
+    if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    return clef_fp4_linear_scratch(format, n_rows, cfg->hidden, bytes);
+}
+
+int clef_head_forward_fp4_scratch(const clef_config* cfg, int32_t format, const clef_schema* schema, size_t* bytes) {
+    if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    const Plan* pp = nullptr;
+    const WsLayout* lp = nullptr;
+    const int v = cached_plan(cfg, schema, &pp, &lp);
+    if (v != CLEF_OK) return v;
+    int64_t most = 0, rows = 0;
+    for (int b = 0; b < schema->B;) {
+        b = fp4_run(schema, *pp, b, &rows);
+        most = std::max(most, rows);
+    }
+    return clef_fp4_linear_scratch(format, int32_t(most), cfg->hidden, bytes);
+}
+
+int clef_stream_rows_fp4(const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,
+                         const clef_schema* schema, const void* hidden, int32_t hidden_dtype, int32_t record,
+                         int32_t row0, int32_t n_rows, void* workspace, size_t workspace_bytes, void* scratch,
+                         size_t scratch_bytes, void* stream) {
+    if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    int v = check_fp4_rows(prepared, hidden, hidden_dtype, workspace, scratch);
+    if (v != CLEF_OK) return v;
+    if (!fp4_weights_fit(cfg, w, sums)) return CLEF_ERR_INVALID_ARGUMENT;
+    const Plan* pp = nullptr;
+    const WsLayout* lp = nullptr;
+    v = cached_plan(cfg, schema, &pp, &lp);
+    if (v != CLEF_OK) return v;
+    if (record < 0 || record >= schema->B || row0 < 0 || n_rows < 1 ||
+        int64_t(row0) + n_rows > schema->lengths[record])
+        return CLEF_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < lp->total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+    return project_fp4(cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype, int64_t(record) * schema->Lpad + row0,
+                       pp->blob[pp->rec_row_off + record] + int64_t(row0), n_rows, workspace, scratch, scratch_bytes,
+                       stream);
+}
+
+int clef_head_forward_fp4(const clef_config* cfg, const void* const* weights, const void* prepared, const clef_fp4* w,
+                          const float* sums, const clef_schema* schema, const void* hidden, int32_t hidden_dtype,
+                          const int32_t* token_ids, const uint16_t* lexical, float* logits, float* probs, float* q_value,
+                          float* q_conf, int32_t* q_argmax, void* workspace, size_t workspace_bytes, void* scratch,
+                          size_t scratch_bytes, const clef_debug_outputs* debug, void* stream) {
+    if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    int v = check_fp4_rows(prepared, hidden, hidden_dtype, workspace, scratch);
+    if (v != CLEF_OK) return v;
+    if (!fp4_weights_fit(cfg, w, sums) || !weights || !token_ids || !lexical || !logits || !probs || !q_value || !q_conf ||
+        !q_argmax || (reinterpret_cast<uintptr_t>(lexical) & 15))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    const WIdx wi(cfg);
+    for (int i = 0; i < wi.count(); ++i)
+        if (!weights[i] || (reinterpret_cast<uintptr_t>(weights[i]) & 15)) return CLEF_ERR_INVALID_ARGUMENT;
+    size_t need = 0;
+    v = clef_head_forward_fp4_scratch(cfg, w->format, schema, &need);
+    if (v != CLEF_OK) return v;
+    if (scratch_bytes < need) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+    v = clef_stream_begin(cfg, schema, workspace, workspace_bytes, stream);
+    if (v != CLEF_OK) return v;
+    const Plan* pp = nullptr;
+    const WsLayout* lp = nullptr;
+    v = cached_plan(cfg, schema, &pp, &lp);
+    if (v != CLEF_OK) return v;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    CK(mark(debug, 0, st));
+    for (int b = 0; b < schema->B;) {
+        int64_t rows = 0;
+        const int e = fp4_run(schema, *pp, b, &rows);
+        v = project_fp4(cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype, int64_t(b) * schema->Lpad,
+                        pp->blob[pp->rec_row_off + b], rows, workspace, scratch, scratch_bytes, stream);
+        if (v != CLEF_OK) return v;
+        b = e;
+    }
+    CK(mark(debug, 1, st));
+    return forward_impl(cfg, weights, prepared, schema, static_cast<const uint16_t*>(hidden), token_ids, lexical, logits,
+                        probs, q_value, q_conf, q_argmax, workspace, workspace_bytes, debug, stream, kForwardAfterStream,
+                        hidden_dtype == CLEF_FP16);
 }
 
 int clef_device_status(void* workspace, void* stream) {

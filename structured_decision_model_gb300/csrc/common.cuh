@@ -252,7 +252,8 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
 }
 
 // Store of a box from shared memory (generic writes to it come before a fence_proxy_async_smem and a
-// barrier); elements outside the tensor are left out.  The thread's stores form groups in order.
+// barrier); 16-byte pieces that lie outside the tensor are left out (a row
+// that ends inside one is overrun).  The thread's stores form groups in order.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int32_t x, int32_t y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),

@@ -175,23 +175,35 @@ __device__ __forceinline__ Raw<DT> load16(const void* x, int64_t row0, int col0,
     return r;
 }
 
-// A maximum and a sum over a row that W warps share, in one order whatever else the block does.
-__device__ __forceinline__ void row_reduce(float& most, float& sum, float2* red, int W, int warp) {
-    most = warp_max(most);
-    sum = warp_sum(sum);
-    if (W == 1) return;
+// The largest of a row that W warps share.
+__device__ __forceinline__ float row_max(float v, float* red, int W, int warp) {
+    v = warp_max(v);
+    if (W == 1) return v;
     __syncthreads();  // red may still be read from the last call
-    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(most, sum);
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
     __syncthreads();
     const int w0 = warp / W * W;
-    const float2 f = red[w0];
-    most = f.x;
-    sum = f.y;
-    for (int i = 1; i < W; ++i) {
-        const float2 v = red[w0 + i];
-        most = fmaxf(most, v.x);
-        sum += v.y;
+    for (int i = 0; i < W; ++i) v = fmaxf(v, red[w0 + i]);
+    return v;
+}
+
+// The sum over a row of what lane l has for piece i * W + part in v[i]: pieces in order, then lanes, so that it
+// does not depend on how many warps share the row.
+template <int STEPS>
+__device__ __forceinline__ float row_sum(const float (&v)[STEPS], float (*red)[32], int W, int warp, int lane) {
+    float s = 0.f;
+    if (W == 1) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) s += v[i];
+    } else {
+        float(*mine)[32] = red + warp / W * W * STEPS;  // the row's pieces
+        __syncthreads();  // red may still be read from the last call
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) mine[i * W + warp % W][lane] = v[i];
+        __syncthreads();
+        for (int i = 0; i < STEPS * W; ++i) s += mine[i][lane];
     }
+    return warp_sum(s);
 }
 
 // STEPS: 512-value pieces of a row that a warp keeps, 16 values a lane; W warps a row (a power of
@@ -200,7 +212,8 @@ __device__ __forceinline__ void row_reduce(float& most, float& sum, float2* red,
 template <int FMT, int DT, bool VEC, int STEPS>
 __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4QuantizeArgs a, int W) {
     constexpr bool NV = FMT == CLEF_NVFP4;
-    __shared__ float2 red[kThreads / 32];
+    __shared__ float red[kThreads / 32];
+    __shared__ float partial[kThreads / 32 * STEPS][32];
     __shared__ __align__(16) uint32_t stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 32 * Raw<DT>::kWords];
     griddep_wait();
     griddep_launch();  // behind the wait: whoever starts early may take what came before us as done
@@ -220,8 +233,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
         else raw[i] = Raw<DT>{};
     }
     // the largest size of every block and of the row's finite blocks, and the row's sum
-    float top[STEPS], row_top = 0.f, row_sum = 0.f;
-    uint64_t sum = 0;  // (0, 0)
+    float top[STEPS], sum[STEPS], row_top = 0.f;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         uint32_t t = raw[i].top();
@@ -241,18 +253,15 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
             uint64_t t2 = add2(raw[i].two(0), raw[i].two(1));
 #pragma unroll
             for (int j = 2; j < 8; j += 2) t2 = add2(t2, add2(raw[i].two(j), raw[i].two(j + 1)));
-            sum = add2(sum, t2);
+            const float2 f = both_of(t2);
+            sum[i] = f.x + f.y;
         }
     }
-    if (NV || stats) {
-        const float2 s2 = both_of(sum);
-        row_sum = s2.x + s2.y;
-        row_reduce(row_top, row_sum, red, W, warp);
-    }
-    const float mean = row_sum / float(a.cols);
+    const float mean = stats ? row_sum<STEPS>(sum, partial, W, warp, lane) / float(a.cols) : 0.f;
     float inv_r = 1.f, r = 1.f;
     bool tiny = false;
     if constexpr (NV) {
+        row_top = row_max(row_top, red, W, warp);
         const int e = max(exponent_of(row_top) - 10, -126);
         r = pow2(e);
         inv_r = pow2(-e);
@@ -264,9 +273,10 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
     uint8_t* scales = a.scales + (row / kFp4RowGroup * (padded >> (NV ? 6 : 7))) * kFp4ScaleGroup +
                       (row % 32) * 16 + (row % kFp4RowGroup) / 32 * 4;
     const uint64_t less = pair_of(-mean, -mean);
-    float total = 0.f, squares = 0.f;
+    float total[STEPS], squares[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
+        total[i] = squares[i] = 0.f;
         if ((i * W + part) * 512 >= padded) continue;  // the same for a whole warp
         const int col = (i * W + part) * 512 + lane * 16;
         const int left = a.cols - col;  // values from the lane's first to the row's end
@@ -295,12 +305,12 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
                     t = fma2(d, d, t);
                 }
                 const float2 t2 = both_of(t);
-                squares += t2.x + t2.y;
+                squares[i] = t2.x + t2.y;
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float d = j < left ? raw[i].at(j) - mean : 0.f;
-                    squares = fmaf(d, d, squares);
+                    squares[i] = fmaf(d, d, squares[i]);
                 }
             }
         }
@@ -358,22 +368,19 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
                 t += f.x + f.y;
             }
-            total = fmaf(t, bad ? __uint_as_float(0x7FC00000u) : scale, total);
+            total[i] = t * (bad ? __uint_as_float(0x7FC00000u) : scale);
         }
     }
-    if (stats || a.sums) {
-        float unused = 0.f;
-        if (stats) {
-            row_reduce(unused, squares, red, W, warp);
-            if (mine && part == 0 && lane == 0) {
-                a.mean[row] = mean;
-                a.rstd[row] = 1.f / sqrtf(squares / float(a.cols) + 1e-5f);
-            }
+    if (stats) {
+        const float var = row_sum<STEPS>(squares, partial, W, warp, lane) / float(a.cols);
+        if (mine && part == 0 && lane == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = 1.f / sqrtf(var + 1e-5f);
         }
-        if (a.sums) {
-            row_reduce(unused, total, red, W, warp);
-            if (mine && part == 0 && lane == 0) a.sums[row] = total * r;
-        }
+    }
+    if (a.sums) {
+        const float all = row_sum<STEPS>(total, partial, W, warp, lane);
+        if (mine && part == 0 && lane == 0) a.sums[row] = all * r;
     }
 }
 

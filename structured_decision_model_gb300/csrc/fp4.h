@@ -58,7 +58,7 @@ struct Fp4ProductArgs {
     int splits;            // K parts of a tile (a cluster)
     int paired;            // 16-bit outputs: rows and columns allow stores of two values at a time
     int w_settled;         // no kernel that may still run on the stream writes w: it may be read ahead of them
-    int bulk;              // 16-bit outputs: rows start on 16 bytes, so that TMA can store them
+    int bulk;              // 16-bit outputs: rows start and end on 16 bytes, so that TMA can store them
 };
 cudaError_t launch_fp4_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, int dtype,
                                cudaStream_t s);

@@ -98,7 +98,8 @@ int multiply(const clef_fp4& x, const clef_fp4& w, const float* bias, const floa
     a.kgroups = fp4_kgroups(x.format, x.cols);
     a.splits = 1;
     a.paired = dtype != CLEF_FP32 && row_stride % 2 == 0 && w.rows % 2 == 0 && !misaligned(out, 4);
-    a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && !misaligned(out, 16);
+    // TMA writes whole 16-byte pieces of a row, also where the row ends inside one
+    a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && w.rows % 8 == 0 && !misaligned(out, 16);
     a.w_settled = w_settled;
     return launch_fp4_product(x, w, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK : CLEF_ERR_CUDA;
 }

@@ -481,7 +481,7 @@ struct PairCfg {
     static_assert(4 * GROUPS + 8 * GROUPS <= 64, "scales fit the last columns");
 };
 
-// BULK: 16-bit outputs whose rows start on 16 bytes, staged in shared memory and stored by TMA.
+// BULK: 16-bit outputs whose rows start and end on 16 bytes, staged in shared memory and stored by TMA.
 template <int FMT, int OUT, bool BULK>
 __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                    const __grid_constant__ CUtensorMap tmX,

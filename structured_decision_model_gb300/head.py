@@ -12,6 +12,7 @@ import torch
 
 from . import binding as B
 from .memory import MemoryCache, stream_handle
+from .microscaled import Fp4Matrix
 
 
 def weight_order(H, D, heads, F, n_route, n_joint):
@@ -51,8 +52,11 @@ class Outputs:
 
 
 class ClefHead:
+    """``memory_format`` ("nvfp4" or "mxfp4"): ``forward`` and ``stream_rows`` project the memory rows to keys and values
+    with rows and weights in 4 bits (see ``microscaled``); None: in bf16."""
+
     def __init__(self, weights: dict, H=4096, D=1024, heads=16, F=4096, n_route=2, n_joint=4, vocab=248320,
-                 device="cuda"):
+                 device="cuda", memory_format: Optional[str] = None):
         self.cfg = B.make_config(H, D, heads, F, n_route, n_joint, vocab)
         self.H, self.D, self.heads, self.F, self.vocab = H, D, heads, F, vocab
         self.device = device
@@ -65,6 +69,17 @@ class ClefHead:
         self.prepared = torch.empty(nbytes, dtype=torch.uint8, device=device)
         B.clef_prepare_weights(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), nbytes, stream_handle())
         self._ws = None
+        self.memory_weights = None
+        if memory_format is not None:
+            w = Fp4Matrix(2 * n_route * D, H, memory_format, device)
+            w.sums = torch.empty(w.rows, dtype=torch.float32, device=w.device)
+            B.clef_fp4_memory_weights(self.cfg, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), stream_handle())
+            self.memory_weights = w
+
+    def _scratch(self, n_bytes, stream):
+        """A buffer of a call's own, on the call's stream."""
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            return torch.empty(n_bytes, dtype=torch.uint8, device=self.device)
 
     def workspace(self, schema: B.Schema) -> torch.Tensor:
         n = B.clef_workspace_size(self.cfg, schema)
@@ -84,6 +99,16 @@ class ClefHead:
                 out: Optional[Outputs] = None, debug=None, stream=None, check=True) -> Outputs:
         ws = self.workspace(schema)
         out = out if out is not None else self.alloc_outputs(schema)
+        if self.memory_weights is not None:
+            w = self.memory_weights
+            n = B.clef_head_forward_fp4_scratch(self.cfg, w.struct.format, schema)
+            space = self._scratch(n, stream)
+            B.clef_head_forward_fp4(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), schema,
+                                    hidden.data_ptr(), B.FP16 if hidden.dtype == torch.float16 else B.BF16,
+                                    token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(),
+                                    out.q_value.data_ptr(), out.q_conf.data_ptr(), out.q_argmax.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), space.data_ptr(), n, debug=debug, stream=stream_handle(stream))
+            return out
         B.clef_head_forward(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), schema, hidden.data_ptr(),
                             token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(),
                             out.q_value.data_ptr(), out.q_conf.data_ptr(), out.q_argmax.data_ptr(), ws.data_ptr(),
@@ -98,6 +123,14 @@ class ClefHead:
         """Statistics and K/V of rows [row0, row0 + n_rows) of ``record``; ``hidden`` is
         bf16 or fp16 (fp16 rows are rounded to bf16 where the head reads them)."""
         ws = self._ws
+        if self.memory_weights is not None:
+            w = self.memory_weights
+            n = B.clef_stream_rows_fp4_scratch(self.cfg, w.struct.format, n_rows)
+            space = self._scratch(n, stream)
+            B.clef_stream_rows_fp4(self.cfg, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), schema, hidden.data_ptr(),
+                                   B.FP16 if hidden.dtype == torch.float16 else B.BF16, record, row0, n_rows, ws.data_ptr(),
+                                   ws.numel(), space.data_ptr(), n, stream_handle(stream))
+            return
         fn = B.clef_stream_rows_f16 if hidden.dtype == torch.float16 else B.clef_stream_rows
         fn(self.cfg, self.prepared.data_ptr(), schema, hidden.data_ptr(), record, row0, n_rows, ws.data_ptr(),
            ws.numel(), stream_handle(stream))

@@ -1,0 +1,136 @@
+"""The microscaled 4-bit entry points on the host (no GPU): sizes and refusals, all before any CUDA call."""
+import numpy as np
+import pytest
+
+import synth
+from fp4_support import E4M3, LEVELS, kept
+from structured_decision_model_gb300 import binding as B
+from structured_decision_model_gb300.build import build_library
+
+P = 1 << 20  # a well-aligned address that is never read
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build_library()
+    return B.load()
+
+
+def refused(status, f, *args):
+    with pytest.raises(B.ClefError) as e:
+        f(*args)
+    assert e.value.status == status
+
+
+def changed(args, i, v):
+    return [*args[:i], v, *args[i + 1:]]
+
+
+def matrix(at=P, rows=10, cols=100, form=B.NVFP4, **over):
+    d = dict(codes=at, scales=at + (1 << 16), row_scale=at + (2 << 16) if form == B.NVFP4 else None)
+    d.update(over)
+    return B.ClefFp4(d["codes"], d["scales"], d["row_scale"], rows, cols, form)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (128, 256), (129, 257), (1000, 16384)])
+def test_sizes(rows, cols):
+    for form, each in ((B.MXFP4, 1024), (B.NVFP4, 2048)):
+        codes, scales = B.clef_fp4_size(form, rows, cols)
+        assert codes == rows * (-(-cols // 32) * 16)
+        assert scales == -(-rows // 128) * -(-cols // 256) * each
+        up = lambda n: -(-n // 256) * 256
+        assert B.clef_fp4_linear_scratch(form, rows, cols) == up(codes) + up(scales) + (4 * rows if form else 0)
+
+
+@pytest.mark.parametrize("form,rows,cols", [(2, 1, 1), (-1, 1, 1), (0, 0, 1), (1, 1, 0), (1, 1, 16385), (0, 2 ** 31 - 256, 1),
+                                            (1, 2 ** 31 - 300, 16384)])
+def test_unsupported_sizes(form, rows, cols):
+    refused(3, B.clef_fp4_size, form, rows, cols)
+    refused(3, B.clef_fp4_linear_scratch, form, rows, cols)
+
+
+def test_matrices_are_checked():
+    good = [matrix(), B.BF16, 8 * P, 100, None, None, None]
+    for bad in (matrix(codes=None), matrix(scales=None), matrix(row_scale=None), matrix(codes=P + 128), matrix(scales=2 * P + 16),
+                matrix(row_scale=2 * P + 2)):
+        refused(1, B.clef_fp4_quantize, *changed(good, 0, bad))
+    refused(3, B.clef_fp4_quantize, *changed(good, 0, matrix(form=3)))
+    refused(3, B.clef_fp4_quantize, *changed(good, 0, matrix(rows=0)))
+
+
+def test_quantize_refusals():
+    good = [matrix(), B.BF16, 8 * P, 100, 9 * P, 10 * P, 11 * P]
+    for i, v in ((1, 3), (1, -1), (2, None), (2, 8 * P + 1), (3, -1), (3, 2 ** 31 + 1), (4, None), (5, None), (4, 9 * P + 2), (6, 11 * P + 1),
+                 (4, 10 * P),                    # mean and rstd in one place
+                 (4, P + 64), (6, 8 * P + 40),   # outputs inside the codes, inside x
+                 (2, P + 16)):                   # x inside the codes
+        refused(1, B.clef_fp4_quantize, *changed(good, i, v))
+
+
+def test_dequantize_refusals():
+    good = [matrix(), B.FP32, 8 * P, 100]
+    for i, v in ((1, 7), (2, None), (2, 8 * P + 2), (3, 99), (2, P + 4 * 100)):
+        refused(1, B.clef_fp4_dequantize, *changed(good, i, v))
+
+
+def test_product_refusals():
+    x, w = matrix(), matrix(at=4 * P, rows=20)
+    good = [x, w, 12 * P, 13 * P, 14 * P, 15 * P, B.BF16, 8 * P, 20, 16 * P]
+    for i, v in ((1, matrix(at=4 * P, rows=20, form=B.MXFP4)), (1, matrix(at=4 * P, rows=20, cols=101)), (2, 12 * P + 2),
+                 (3, None), (4, None), (5, None), (6, 3), (7, None), (7, 8 * P + 1), (8, 19), (9, None), (9, 16 * P + 1),
+                 (7, P), (7, 4 * P + (1 << 16)), (7, 12 * P), (7, 16 * P)):  # out over x, w's scales, bias, flags
+        refused(1, B.clef_fp4_product, *changed(good, i, v))
+    big = matrix(at=1 << 44, rows=2 ** 30, cols=16, scales=1 << 45, row_scale=1 << 46)
+    refused(3, B.clef_fp4_product, big, matrix(at=4 * P, rows=2 ** 20, cols=16, scales=1 << 47), *changed(good[2:], 6, 2 ** 20))
+
+
+def test_layer_refusals():
+    w = matrix(at=4 * P, rows=20)
+    size = B.clef_fp4_linear_scratch(B.NVFP4, 10, 100)
+    good = [w, B.BF16, 8 * P, 100, 10, 12 * P, 15 * P, B.BF16, 9 * P, 20, 13 * P, 14 * P, 20 * P, size, 16 * P]
+    for i, v in ((1, 5), (2, None), (3, -1), (5, 12 * P + 1), (6, None), (7, 9), (8, None), (9, 19), (10, None), (11, None),
+                 (12, None), (12, 20 * P + 8), (14, None),
+                 (8, 8 * P), (8, 20 * P + 512), (10, 20 * P), (10, 14 * P), (12, 8 * P), (12, 4 * P)):
+        refused(1, B.clef_fp4_linear, *changed(good, i, v))
+    refused(2, B.clef_fp4_linear, *changed(good, 13, size - 1))
+    refused(3, B.clef_fp4_linear, *changed(good, 4, 0))
+
+
+def test_head_refusals():
+    cfg = B.make_config()
+    spec = synth.BatchSpec(name="t", B=2, H=4096, vocab=1000, lengths=[256, 300], questions=(2, 2), options=(2, 3))
+    bt = synth.make_batch(spec, seed=2, with_hidden=False)
+    schema = B.Schema(bt.B, bt.Lpad, bt.H, bt.lengths, bt.q_rec, bt.q_type, bt.q_span, bt.q_opt_off, bt.o_span)
+    w = matrix(at=1 << 30, rows=4096, cols=4096, scales=1 << 31, row_scale=1 << 32)
+    for bad in (matrix(), None):
+        refused(1, B.clef_fp4_memory_weights, cfg, P, bad, P)
+    refused(1, B.clef_fp4_memory_weights, cfg, None, w, P)
+    refused(3, B.clef_fp4_memory_weights, B.make_config(H=100), P, w, P)
+    assert B.clef_head_forward_fp4_scratch(cfg, B.NVFP4, schema) == B.clef_stream_rows_fp4_scratch(cfg, B.NVFP4, 300)
+    refused(3, B.clef_stream_rows_fp4_scratch, cfg, 4, 300)
+    ws = B.clef_workspace_size(cfg, schema)
+    rows = [cfg, P, w, P, schema, P, B.BF16, 1, 0, 300, P, ws, P, 1 << 40]
+    for i, v in ((1, None), (2, matrix()), (3, None), (5, P + 8), (6, B.FP32), (7, 2), (7, -1), (8, 1), (9, 0), (9, 301), (10, P + 16),
+                 (12, P + 16)):
+        refused(1, B.clef_stream_rows_fp4, *changed(rows, i, v))
+    refused(2, B.clef_stream_rows_fp4, *changed(rows, 11, ws - 1))
+    n = B.clef_weight_count(cfg)
+    forward = [cfg, [P] * n, P, w, P, schema, P, B.BF16, P, P, P, P, P, P, P, P, ws, P, 1 << 40]
+    for i, v in ((1, [P + 2] * n), (6, None), (7, B.FP32), (8, None), (9, P + 2), (14, None)):
+        refused(1, B.clef_head_forward_fp4, *changed(forward, i, v))
+    refused(2, B.clef_head_forward_fp4, *changed(forward, 18, 16))
+    refused(2, B.clef_head_forward_fp4, *changed(forward, 16, ws - 1))
+
+
+def test_the_oracle_of_the_tests():
+    """The 64-bit form by hand: a block of each format whose quotients are known."""
+    assert len(LEVELS) == 8 and len(E4M3) == 127 and E4M3[-1] == 448 and E4M3[8] == 2.0 ** -6
+    x = np.zeros((1, 32))
+    x[0, :10] = [7.9, 0.25, 0.75, -1.25, 1.75, 2.5, -3.5, 5.0, 0.2501, 4.9]
+    codes, byte, _, values = kept(x, "mxfp4")
+    assert byte[0, 0] == 127
+    np.testing.assert_array_equal(values[0, :10], [6, 0, 1, -1, 2, 2, -4, 4, 0.5, 4])
+    assert codes[0, 3] == 8 + 2
+    codes, byte, r, values = kept(x / 7.9 * 6, "nvfp4")
+    # amax 6: r = 2^-8, quotient 1 / r = 256 = 2^8, so the scale is 1 again
+    assert r[0] == 2.0 ** -8 and E4M3[byte[0, 0]] == 256 and values[0, 0] == 6

@@ -178,3 +178,195 @@ def test_normalized_product(form, m, n, k):
     check_product(x, w, form, torch.float32, None, True, y)
     m_ = quantize(x, form, stats=True)
     assert torch.equal(m_.mean, mean) and torch.equal(m_.rstd, rstd)
+
+
+# ------------------------------------------------- what a serving program meets
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("m", [3, 70, 600])
+def test_rows_of_no_numbers_stay_by_themselves(form, m):
+    """NaN and infinity in a row of x, or of w, make that row's (column's) outputs NaN and no others."""
+    x, w = rows_of(m, 300, torch.bfloat16, 1, 0.3), rows_of(140, 300, torch.bfloat16, 2, 0.3)
+    clean = Fp4Linear(w, None, form)(x, torch.float32)
+    x2, w2 = x.clone(), w.clone()
+    x2[1, 299], w2[139, 0], w2[5, 77] = float("nan"), float("inf"), float("-inf")
+    y = Fp4Linear(w2, None, form)(x2, torch.float32)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[1], bad[:, 139], bad[:, 5] = True, True, True
+    assert y[bad].isnan().all()
+    # the other values of a row that holds one keep their scales, so the other outputs are as they were
+    assert torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("m", [1, 40, 100, 700])
+def test_outputs_stay_inside_their_rows(dtype, m):
+    """Row strides of every alignment; what lies between the rows and behind the last is left as it was."""
+    t = TYPES[dtype]
+    x, w = quantize(rows_of(m, 200, torch.bfloat16, 3), "nvfp4"), quantize(rows_of(131, 200, torch.bfloat16, 4), "nvfp4")
+    want = product(x, w, None, t)
+    for stride, first in ((131, 0), (132, 0), (136, 0), (137, 3), (144, 8), (140, 2)):
+        wide = torch.full((m + 2, stride), 9.0, dtype=t, device="cuda")
+        out = wide.view(-1)[first:first + m * stride].view(m, stride)[:, :131]
+        assert torch.equal(product(x, w, None, t, out=out), want)
+        left = wide.clone()
+        left.view(-1)[first:first + m * stride].view(m, stride)[:, :131] = 9.0
+        assert (left == 9).all()
+
+
+def test_a_row_depends_on_itself_alone():
+    """The same row among others of any size: equal codes, and equal outputs in calls of one shape."""
+    x = rows_of(300, 1000, torch.bfloat16, 5)
+    layer = Fp4Linear(rows_of(256, 1000, torch.bfloat16, 6))
+    y = layer(x)
+    x2 = x.clone()
+    x2[1:] *= 1e20
+    assert torch.equal(layer(x2)[0], y[0])
+
+
+def test_statistics_do_not_depend_on_the_number_of_rows():
+    """Few rows are shared among more warps than many: the same sums in the same order."""
+    for cols in (1000, 4096, 16384):
+        x = rows_of(2600, cols, torch.bfloat16, cols, 0.3) + 0.25
+        many = quantize(x, stats=True, sums=True)
+        for n in (1, 7, 400):
+            few = quantize(x[:n], stats=True, sums=True)
+            for a, b in ((few.mean, many.mean), (few.rstd, many.rstd), (few.sums, many.sums)):
+                assert torch.equal(a, b[:n])
+
+
+def test_more_tiles_than_the_card_holds():
+    """Pairs of CTAs walk several tiles of 256 x 256: the accumulators in turn, each output type."""
+    x, w = quantize(rows_of(3000, 512, torch.bfloat16, 1, 0.3)), quantize(rows_of(4104, 512, torch.bfloat16, 2, 0.3))
+    a, b = x.dequantize(torch.float32).double(), w.dequantize(torch.float32).double()
+    want, room = a @ b.T, a.abs() @ b.abs().T
+    for out in TYPES.values():
+        off = (product(x, w, None, out).double() - want).abs()
+        # as in check_product: 8 MMAs, 50 roundings, the output's own
+        assert (off <= room * (8 * 2.0 ** -23 + 50 * 2.0 ** -24) + want.abs() * torch.finfo(out).eps / 2).all()
+
+
+def test_long_rows_and_many_tiles():
+    for m, n, k in ((1, 300, 16384), (300, 260, 8200), (2100, 1100, 260)):
+        x, w = rows_of(m, k, torch.bfloat16, m, 0.5), rows_of(n, k, torch.bfloat16, n, 0.5)
+        check_product(x, w, "nvfp4", torch.bfloat16, y=Fp4Linear(w)(x))
+        check_product(x, w, "mxfp4", torch.float32, y=Fp4Linear(w, None, "mxfp4")(x, torch.float32))
+
+
+def test_values_of_any_size():
+    """Rows and weights far from 1: the row scales keep both inside e4m3's range."""
+    for power in (-100, -30, 60):
+        x = rows_of(40, 512, torch.float32, 8, 0.5) * 2.0 ** power
+        w = rows_of(200, 512, torch.float32, 9, 0.5) * 2.0 ** -power
+        for form in FORMATS:
+            check_product(x, w, form, torch.float32, y=Fp4Linear(w, None, form)(x))
+
+
+def test_leading_dimensions_and_empty_batches():
+    layer = Fp4Linear(rows_of(96, 160, torch.bfloat16, 1), torch.randn(96, device="cuda"))
+    x = rows_of(24, 160, torch.bfloat16, 2)
+    y = layer(x)
+    assert torch.equal(layer(x.view(2, 3, 4, 160)), y.view(2, 3, 4, 96))
+    assert torch.equal(layer(x[0]), layer(x[:1])[0])
+    assert torch.equal(layer(x.t().contiguous().t()), y)
+    assert torch.equal(layer(torch.cat([x, x], 1)[:, :160]), y)
+    a, mean, rstd = layer.normalized(x.view(2, 12, 160))
+    assert a.shape == (2, 12, 96) and mean.shape == rstd.shape == (2, 12)
+    assert layer(x[:0]).shape == (0, 96)
+    a, mean, rstd = layer.normalized(x[:0])
+    assert a.shape == (0, 96) and mean.shape == rstd.shape == (0,)
+
+
+def test_the_layer_is_its_steps():
+    w, bias = rows_of(520, 640, torch.bfloat16, 1), torch.randn(520, device="cuda")
+    for m in (1, 64, 300):
+        x = rows_of(m, 640, torch.float16, m)
+        layer = Fp4Linear(w, bias, "mxfp4")
+        q = quantize(x, "mxfp4", stats=True)
+        assert torch.equal(layer(x), product(q, layer.weight, layer.bias, torch.float16))
+        y, mean, rstd = layer.normalized(x)
+        assert torch.equal(y, product(q, layer.weight, layer.bias, torch.float16, normalized=True))
+        assert torch.equal(mean, q.mean) and torch.equal(rstd, q.rstd)
+    kept_data = Fp4Matrix(520, 640, "mxfp4", data=layer.weight.data.clone())
+    assert torch.equal(Fp4Linear(kept_data, bias, "mxfp4")(x), layer(x))
+
+
+def test_streams_and_graphs():
+    """Calls on two streams at once, and two captured graphs of one layer replayed in turn on new inputs."""
+    layer = Fp4Linear(rows_of(1024, 512, torch.bfloat16, 1), torch.randn(1024, device="cuda"))
+    xs = [rows_of(m, 512, torch.bfloat16, m) for m in (1, 64, 600)]
+    want = [layer(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append([layer(x) for x in xs])
+    torch.cuda.synchronize()
+    for ys in got:
+        for y, v in zip(ys, want):
+            assert torch.equal(y, v)
+    graphs, feeds, outs = [], [x.clone() for x in xs], []
+    for f in feeds:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer.normalized(f))
+        graphs.append(g)
+    for turn in range(3):
+        for f, x in zip(feeds, xs):
+            f.copy_(x * (1 + turn))
+        torch.cuda.synchronize()
+        for s, g in zip(streams + streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for f, o in zip(feeds, outs):
+            for a, b in zip(o, layer.normalized(f)):
+                assert torch.equal(a, b)
+    assert layer.device_status() == 0
+
+
+def test_weights_quantised_right_before_their_product():
+    """The product waits for both sides, also when they come from the kernels directly before it."""
+    x, w = rows_of(40, 4096, torch.bfloat16, 1), rows_of(4096, 4096, torch.bfloat16, 2)
+    want = product(quantize(x), quantize(w))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        qx = quantize(x)
+        assert torch.equal(product(qx, quantize(w)), want)
+        layer = Fp4Linear(w)
+        assert torch.equal(layer(x), want)
+
+
+def test_gradients_and_wrong_tensors_are_refused():
+    x = rows_of(4, 64, torch.bfloat16, 1)
+    layer = Fp4Linear(rows_of(32, 64, torch.bfloat16, 2))
+    wanted = x.clone().requires_grad_()
+    with pytest.raises(ClefError):
+        layer(wanted)
+    with pytest.raises(ClefError):
+        quantize(wanted)
+    with torch.no_grad():
+        layer(wanted)
+    for bad in (x[:, :32], x.cpu(), x.double(), x.t()):
+        with pytest.raises(ClefError):
+            layer(bad)
+    q, w = quantize(x), layer.weight
+    with pytest.raises(ClefError):
+        product(q, quantize(x, "mxfp4"))
+    with pytest.raises(ClefError):
+        product(q, w, normalized=True)                      # no statistics
+    with pytest.raises(ClefError):
+        product(q, w, torch.zeros(31, device="cuda"))
+    with pytest.raises(ClefError):
+        product(q, w, out=torch.empty(4, 32, device="cuda", dtype=torch.float16))
+    with pytest.raises(ClefError):
+        product(q, w, out=q.data.view(torch.bfloat16)[:128].view(4, 32))
+    with pytest.raises(ClefError):
+        quantize(x, "fp4")
+    with pytest.raises(ClefError):
+        quantize(x, out=Fp4Matrix(5, 64))
+    with pytest.raises(ClefError):
+        Fp4Matrix(4, 64, data=torch.empty(7, dtype=torch.uint8, device="cuda"))
