@@ -138,11 +138,12 @@ struct Raw {
     }
 };
 
-// A warp's 512 values from column col0 of a row on, 16 a lane; what lies behind the row reads as 0.
+// LANES lanes' 16 values each from column col0 of a row on, `lane` the one's place among them; what lies
+// behind the row reads as 0.
 // VEC: every row starts on 16 bytes and has a multiple of 8 values, so a lane's are read as
-// whole 16-byte pieces.  Otherwise the warp reads 32 neighbours at a time and hands them round
+// whole 16-byte pieces.  Otherwise neighbours are read side by side and handed round
 // through shared memory (3001 x 1111 fp16: 4.3 us; value by value in each lane 7.3).
-template <int DT, bool VEC>
+template <int DT, bool VEC, int LANES>
 __device__ __forceinline__ Raw<DT> load16(const void* x, int64_t row0, int col0, int cols, int lane, uint32_t* stage) {
     Raw<DT> r;
     if constexpr (VEC) {
@@ -160,10 +161,10 @@ __device__ __forceinline__ Raw<DT> load16(const void* x, int64_t row0, int col0,
         T* to = reinterpret_cast<T*>(stage);
         T v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = col0 + 32 * j + lane < cols ? p[32 * j + lane] : T(0);
+        for (int j = 0; j < 16; ++j) v[j] = col0 + LANES * j + lane < cols ? p[LANES * j + lane] : T(0);
         __syncwarp();  // the last piece has been read
 #pragma unroll
-        for (int j = 0; j < 16; ++j) to[32 * j + lane] = v[j];
+        for (int j = 0; j < 16; ++j) to[LANES * j + lane] = v[j];
         __syncwarp();
         const uint4* own = reinterpret_cast<const uint4*>(stage + lane * Raw<DT>::kWords);
 #pragma unroll
@@ -175,10 +176,25 @@ __device__ __forceinline__ Raw<DT> load16(const void* x, int64_t row0, int col0,
     return r;
 }
 
-// The largest of a row that W warps share.
+// Over the LANES lanes of an aligned group.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// The largest of a row that W warps share (a half of a warp has W = 1).
+template <int LANES>
 __device__ __forceinline__ float row_max(float v, float* red, int W, int warp) {
-    v = warp_max(v);
-    if (W == 1) return v;
+    v = lanes_max<LANES>(v);
+    if (LANES < 32 || W == 1) return v;
     __syncthreads();  // red may still be read from the last call
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     __syncthreads();
@@ -189,10 +205,10 @@ __device__ __forceinline__ float row_max(float v, float* red, int W, int warp) {
 
 // The sum over a row of what lane l has for piece i * W + part in v[i]: pieces in order, then lanes, so that it
 // does not depend on how many warps share the row.
-template <int STEPS>
+template <int STEPS, int LANES>
 __device__ __forceinline__ float row_sum(const float (&v)[STEPS], float (*red)[32], int W, int warp, int lane) {
     float s = 0.f;
-    if (W == 1) {
+    if (LANES < 32 || W == 1) {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) s += v[i];
     } else {
@@ -203,24 +219,27 @@ __device__ __forceinline__ float row_sum(const float (&v)[STEPS], float (*red)[3
         __syncthreads();
         for (int i = 0; i < STEPS * W; ++i) s += mine[i][lane];
     }
-    return warp_sum(s);
+    return lanes_sum<LANES>(s);
 }
 
 // STEPS: 512-value pieces of a row that a warp keeps, 16 values a lane; W warps a row (a power of
-// two), so a row has at most 512 * STEPS * W values.  64 registers a thread, for 32 warps an SM: with 8
-// pieces a warp and half the warps 131072 x 4096 bf16 took 301 us instead of 252.
-template <int FMT, int DT, bool VEC, int STEPS>
-__global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4QuantizeArgs a, int W) {
+// two), so a row has at most 512 * STEPS * W values.  LANES 16: rows of up to 256 values, two a warp.
+// 64 registers a thread, for 32 warps an SM: with 8 pieces a warp and half the warps 131072 x 4096 bf16 took 301 us
+// instead of 252.
+template <int FMT, int DT, bool VEC, int STEPS, int LANES>
+__global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 4) fp4_quantize_kernel(const Fp4QuantizeArgs a, int W) {
     constexpr bool NV = FMT == CLEF_NVFP4;
     __shared__ float red[kThreads / 32];
     __shared__ float partial[kThreads / 32 * STEPS][32];
     __shared__ __align__(16) uint32_t stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 32 * Raw<DT>::kWords];
     griddep_wait();
     griddep_launch();  // behind the wait: whoever starts early may take what came before us as done
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * (kThreads / 32 / W) + warp / W;
-    const bool mine = row < a.rows;  // warps behind the last row still meet the barriers
-    const int part = warp % W;
+    static_assert(LANES == 32 || STEPS == 1, "a half of a warp keeps one tile of a row");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x % LANES;
+    const int64_t row = LANES == 32 ? int64_t(blockIdx.x) * (kThreads / 32 / W) + warp / W
+                                    : int64_t(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
+    const bool mine = row < a.rows;  // threads behind the last row still meet the barriers and shuffles
+    const int part = LANES == 32 ? warp % W : 0;
     const int padded = mine ? (a.cols + kFp4Tile - 1) / kFp4Tile * kFp4Tile : 0;  // columns that have scales
     const bool stats = a.mean != nullptr;
     const int64_t row0 = row * a.row_stride;
@@ -229,7 +248,9 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const int col0 = (i * W + part) * 512;
-        if (col0 < padded) raw[i] = load16<DT, VEC>(a.x, row0, col0, a.cols, lane, stage[VEC ? 0 : warp]);
+        uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
+        if (LANES < 32 || col0 < padded)
+            raw[i] = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
         else raw[i] = Raw<DT>{};
     }
     // the largest size of every block and of the row's finite blocks, and the row's sum
@@ -257,11 +278,11 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
             sum[i] = f.x + f.y;
         }
     }
-    const float mean = stats ? row_sum<STEPS>(sum, partial, W, warp, lane) / float(a.cols) : 0.f;
+    const float mean = stats ? row_sum<STEPS, LANES>(sum, partial, W, warp, lane) / float(a.cols) : 0.f;
     float inv_r = 1.f, r = 1.f;
     bool tiny = false;
     if constexpr (NV) {
-        row_top = row_max(row_top, red, W, warp);
+        row_top = row_max<LANES>(row_top, red, W, warp);
         const int e = max(exponent_of(row_top) - 10, -126);
         r = pow2(e);
         inv_r = pow2(-e);
@@ -277,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         total[i] = squares[i] = 0.f;
-        if ((i * W + part) * 512 >= padded) continue;  // the same for a whole warp
+        if (LANES == 32 && (i * W + part) * 512 >= padded) continue;  // the same for a whole warp
         const int col = (i * W + part) * 512 + lane * 16;
         const int left = a.cols - col;  // values from the lane's first to the row's end
         uint32_t byte;    // the block's scale as stored
@@ -351,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
             packed.x = left >= 8 ? 0x22222222u : left > 0 ? 0x22222222u >> (32 - 4 * left) : 0u;
             packed.y = left >= 16 ? 0x22222222u : left > 8 ? 0x22222222u >> (64 - 4 * left) : 0u;
         }
-        if (col < 2 * code_stride) *reinterpret_cast<uint2*>(codes + col / 2) = packed;
+        if (mine && col < 2 * code_stride) *reinterpret_cast<uint2*>(codes + col / 2) = packed;
         // four blocks' scales are one word, written by the first lane of theirs
         uint32_t word = byte << (8 * (NV ? lane & 3 : lane >> 1 & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, NV ? 1 : 2);
@@ -372,21 +393,21 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_quantize_kernel(const Fp4Quan
         }
     }
     if (stats) {
-        const float var = row_sum<STEPS>(squares, partial, W, warp, lane) / float(a.cols);
+        const float var = row_sum<STEPS, LANES>(squares, partial, W, warp, lane) / float(a.cols);
         if (mine && part == 0 && lane == 0) {
             a.mean[row] = mean;
             a.rstd[row] = 1.f / sqrtf(var + 1e-5f);
         }
     }
     if (a.sums) {
-        const float all = row_sum<STEPS>(total, partial, W, warp, lane);
+        const float all = row_sum<STEPS, LANES>(total, partial, W, warp, lane);
         if (mine && part == 0 && lane == 0) a.sums[row] = all * r;
     }
 }
 
 // Read back: a warp takes 1024 values of a row, 4 times 8 a lane (4 bytes of codes, one scale).  VEC: every row
-// of the output starts on 16 bytes and has a multiple of 8 values, so that a lane stores whole
-// 16-byte pieces; otherwise the warp hands the values round and stores 32 neighbours at a time.
+// of the output starts on a multiple of 8 values' bytes and has a multiple of 8 values, so that a lane
+// stores its 8 at once; otherwise the warp hands the values round and stores 32 neighbours at a time.
 constexpr int kBack = 1024;
 
 template <int FMT, int DT, bool VEC>
@@ -439,10 +460,10 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
                                                   (row * a.row_stride + col) * (DT == CLEF_FP32 ? 4 : 2));
             if constexpr (DT == CLEF_FP32) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    out[j] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                        __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+                // one whole 32-byte sector a lane
+                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0]), "f"(v[1]),
+                             "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                             : "memory");
             } else {
                 uint32_t w[4];
 #pragma unroll
@@ -484,11 +505,14 @@ cudaError_t quantize_rows(const Fp4QuantizeArgs& a, cudaStream_t s) {
     const int64_t warps = int64_t(num_sms()) * 16;
     int W = 1;
     while (W < 8 && W < pieces && (pieces > kMost * W || int64_t(a.rows) * W < warps)) W *= 2;
+    if (a.cols <= 256)
+        return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 16>, dim3(unsigned((int64_t(a.rows) + 15) / 16)),
+                          dim3(kThreads), 0, s, a, 1);
     const int steps = (pieces + W - 1) / W;
     const dim3 grid(unsigned((int64_t(a.rows) * W + kThreads / 32 - 1) / (kThreads / 32)));
-    if (steps <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1>, grid, dim3(kThreads), 0, s, a, W);
-    if (steps <= 2) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 2>, grid, dim3(kThreads), 0, s, a, W);
-    if (steps <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 32>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 2) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 2, 32>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4, 32>, grid, dim3(kThreads), 0, s, a, W);
     return cudaErrorInvalidValue;
 }
 
@@ -502,7 +526,8 @@ cudaError_t quantize_type(const Fp4QuantizeArgs& a, cudaStream_t s) {
 template <int FMT, int DT>
 cudaError_t dequantize_type(const Fp4DequantizeArgs& a, cudaStream_t s) {
     constexpr int size = DT == CLEF_FP32 ? 4 : 2;
-    const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.row_stride * size % 16 == 0 && a.cols % 8 == 0;
+    constexpr int piece = 8 * size;
+    const bool vec = reinterpret_cast<uintptr_t>(a.out) % piece == 0 && a.row_stride * size % piece == 0 && a.cols % 8 == 0;
     const int64_t items = int64_t(a.rows) * ((a.cols + kBack - 1) / kBack);
     const int64_t blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;

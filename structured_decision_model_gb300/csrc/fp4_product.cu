@@ -125,7 +125,22 @@ __device__ __forceinline__ void put_row_terms(float* terms, int j, float2 t) {
     p[2] = t.y;
 }
 
-// Outputs of one column and two rows from their accumulators.
+// Two 16-bit values in one word, the first in its low half.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack_two(float lo, float hi) {
+    if constexpr (OUT == CLEF_FP16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        return pack_bf16(lo, hi);
+    }
+}
+
+// An output from its accumulator; finish2: of one column and two rows.
+__device__ __forceinline__ float finish(float acc, const ColumnTerms& c, float f, float h) {
+    return fmaf(acc * c.scale, f, fmaf(h, c.sum, c.bias));
+}
+
 __device__ __forceinline__ float2 finish2(float acc0, float acc1, const ColumnTerms& c, const float4& t) {
     const uint64_t acc = mul2(pair_of(acc0, acc1), pair_of(c.scale, c.scale));
     const uint64_t add = fma2(pair_of(t.z, t.w), pair_of(c.sum, c.sum), pair_of(c.bias, c.bias));
@@ -177,13 +192,7 @@ __device__ __forceinline__ void emit(const Fp4ProductArgs& a, const uint32_t (&r
 #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {
             const float2 v = finish2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), col, t4[j]);
-            uint32_t w;
-            if constexpr (OUT == CLEF_FP16) {
-                const __half2 h = __floats2half2_rn(v.x, v.y);
-                w = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-                w = pack_bf16(v.x, v.y);
-            }
+            const uint32_t w = pack_two<OUT>(v.x, v.y);
             const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
             if (j < most) *out = __byte_perm(w, other, pick);
             out += step;
@@ -220,12 +229,7 @@ __device__ __forceinline__ void stage16(uint32_t saddr, const uint32_t (&lo)[32]
         for (int i = 0; i < 4; ++i) {
             const uint32_t* r = (i < 2 ? lo : hi) + FROM + 4 * g + 2 * (i & 1);
             const float2 v = finish2(__uint_as_float(r[0]), __uint_as_float(r[1]), col[i], t);
-            if constexpr (OUT == CLEF_FP16) {
-                const __half2 h = __floats2half2_rn(v.x, v.y);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-                w[i] = pack_bf16(v.x, v.y);
-            }
+            w[i] = pack_two<OUT>(v.x, v.y);
         }
         stmatrix_x4_trans(saddr + g * 1024, w);
     }
@@ -265,10 +269,57 @@ struct TileCfg {
     static_assert(STAGE % 1024 == 0 && X_BYTES % 1024 == 0, "swizzle atoms start on 1024 bytes");
 };
 
-constexpr int kMaxSplits = 8;
+
+// The S parts of a tile, staged [rows][LD] at `staged` in every CTA of the cluster, added up in order: CTA sp
+// finishes rows sp, sp + S, ..., a warp a row, four columns a lane, with 8 remote reads under way at
+// once (a column a thread and a row at a time, this took longer than the products: 128 rows x 4096
+// x 4096 in two parts 12.5 us, now 8.3).
+template <int OUT, int S, int LD>
+__device__ __forceinline__ void join_parts(const Fp4ProductArgs& args, uint32_t staged, const float* terms, int m0,
+                                           int rows, int n_tile, int sp, int warp, int lane) {
+    constexpr int Q = 8 / S;
+    const int step = S * (kEpilogue / 32), n0 = n_tile + lane * 4;
+    ColumnTerms col[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) col[e] = column_terms(args, n0 + e);
+    for (int j0 = sp + S * warp; j0 < rows; j0 += Q * step) {
+        float4 v[Q][S];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            // rows past the tile's last are read from where the last is
+            const uint32_t at = staged + uint32_t(lane * 16 + min(j0 + q * step, rows - 1) * LD * 4);
+#pragma unroll
+            for (int i = 0; i < S; ++i) v[q][i] = ld_cluster_f4(cluster_map(at, uint32_t(i)));
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int j = j0 + q * step;
+            if (j >= rows) break;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                acc[0] += v[q][i].x; acc[1] += v[q][i].y;
+                acc[2] += v[q][i].z; acc[3] += v[q][i].w;
+            }
+            const float* t = terms + (j >> 1) * 4 + (j & 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = finish(acc[e], col[e], t[0], t[2]);
+            const int64_t at = int64_t(m0 + j) * args.ldo + n0;
+            if (OUT != CLEF_FP32 && args.paired) {
+                uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.out) + at);
+                if (n0 < args.N) out[0] = pack_two<OUT>(acc[0], acc[1]);
+                if (n0 + 2 < args.N) out[1] = pack_two<OUT>(acc[2], acc[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n0 + e < args.N) store_value<OUT>(args.out, at + e, acc[e]);
+            }
+        }
+    }
+}
 
 template <int FMT, int BN, int OUT>
-__global__ void __launch_bounds__(kThreads) fp4_tile_kernel(const __grid_constant__ CUtensorMap tmW,
+__global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                 const __grid_constant__ CUtensorMap tmX,
                                                                 const __grid_constant__ CUtensorMap tmSW,
                                                                 const __grid_constant__ CUtensorMap tmSX,
@@ -426,29 +477,10 @@ __global__ void __launch_bounds__(kThreads) fp4_tile_kernel(const __grid_constan
     if (S > 1) {
         cluster_sync();  // every thread of every CTA of the cluster, on every path
         if (warp >= 2 && !*abort_flag) {
-            const int t = int(threadIdx.x) - 64;
-            const int row = t & (kWRows - 1), n = wt * kWRows + row;
-            const ColumnTerms col = column_terms(args, n);
             const int rows = min(BN, args.M - xt * BN);
-            const uint32_t red0 = smem_u32(smem);
-            // row j of the tile is added up by CTA j % S, each row by 128 neighbouring threads
-            for (int j = sp + S * (t / kWRows); j < rows; j += S * (kEpilogue / kWRows)) {
-                const uint32_t at = red0 + uint32_t((j * C::LD + row) * 4);
-                float v[kMaxSplits];
-#pragma unroll
-                for (int i = 0; i < kMaxSplits; ++i) {
-                    if (i < S)
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[i]) : "r"(cluster_map(at, uint32_t(i))));
-                }
-                float acc = 0.f;
-#pragma unroll
-                for (int i = 0; i < kMaxSplits; ++i)
-                    if (i < S) acc += v[i];
-                const float4 pair = reinterpret_cast<const float4*>(terms)[j >> 1];
-                const float2 y = finish2(acc, acc, col, pair);
-                if (n < args.N)
-                    store_value<OUT>(args.out, int64_t(xt * BN + j) * args.ldo + n, j & 1 ? y.y : y.x);
-            }
+            if (S == 2) join_parts<OUT, 2, C::LD>(args, smem_u32(smem), terms, xt * BN, rows, wt * kWRows, sp, warp - 2, lane);
+            else if (S == 4) join_parts<OUT, 4, C::LD>(args, smem_u32(smem), terms, xt * BN, rows, wt * kWRows, sp, warp - 2, lane);
+            else join_parts<OUT, 8, C::LD>(args, smem_u32(smem), terms, xt * BN, rows, wt * kWRows, sp, warp - 2, lane);
         }
         cluster_sync();  // no CTA leaves while another may still read its shared memory
     }
@@ -790,10 +822,21 @@ cudaError_t launch_tile(const clef_fp4& x, const clef_fp4& w, Fp4ProductArgs a, 
         !scales_map(&maps[3], x))
         return cudaErrorInvalidValue;
     const int tiles = (a.N + kWRows - 1) / kWRows * ((a.M + BN - 1) / BN);
-    // as many K parts as fill the SMs twice, each with a K tile at least
-    a.splits = 1;
+    // K parts of a tile.  A K tile takes a CTA about 0.29 us, joining the parts 0.5 us for one row and 1.3 to 1.5
+    // us for more, however many parts; CTAs beyond one an SM gain nothing (4096 x 4096, one row: 6.8, 5.2, 4.2,
+    // 4.7 us in 1, 2, 4, 8 parts; 4096 x 1024, 32 rows: 3.4, 4.0, 4.3 us in 1, 2, 4), nor do more than 4 parts of
+    // tiles of 128 rows (1024 x 4096, 256 rows: 6.4 us in 4, 8.6 in 8).
     const int ktiles = fp4_ktiles(x.cols);
-    while (a.splits < kMaxSplits && 2 * a.splits <= ktiles && tiles * a.splits * 2 <= 2 * num_sms()) a.splits *= 2;
+    const double join = a.M == 1 ? 0.5 : a.M <= 32 ? 1.3 : 1.5;
+    double best = ktiles * 0.29;
+    a.splits = 1;
+    for (int S = 2; S <= (BN == 128 ? 4 : 8) && S <= ktiles && tiles * S <= num_sms(); S *= 2) {
+        const double t = (ktiles + S - 1) / S * 0.29 + join;
+        if (t < best) {
+            best = t;
+            a.splits = S;
+        }
+    }
     return launch_clusters(fp4_tile_kernel<FMT, BN, OUT>, tiles * a.splits, a.splits, kThreads, C::SMEM, s, maps, a);
 }
 
@@ -843,7 +886,13 @@ cudaError_t launch_pair(const clef_fp4& x, const clef_fp4& w, const Fp4ProductAr
 
 template <int FMT, int OUT>
 cudaError_t launch_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, cudaStream_t s) {
-    if (a.M > 256) {
+    // Tiles of 128 x 128 while two of them at most fall to an SM (one, where K is long: then pairs, which load
+    // half as much, win); measured on both sides at N 1024 to 16384, K 512 to 16384:
+    //   4096 x 4096, 1024 rows (256 tiles): tiles 11.0 us, pairs 11.3; 1536 rows (384): 20.7, 16.8
+    //   4096 x 1024, 1024 rows: 6.2, 7.3; 1536 rows: 10.9, 10.0
+    //   4096 x 16384, 512 rows (128 tiles): 22.7, 25.5; 768 rows (192): 29.1, 26.4
+    const int64_t tiles = int64_t((a.N + kWRows - 1) / kWRows) * ((a.M + 127) / 128);
+    if (a.M > 64 && tiles > (fp4_ktiles(x.cols) > 16 ? 1 : 2) * num_sms()) {
         if constexpr (OUT != CLEF_FP32)
             if (a.bulk) return launch_pair<FMT, OUT, true>(x, w, a, s);
         return launch_pair<FMT, OUT, false>(x, w, a, s);

@@ -78,7 +78,9 @@ class ClefHead:
 
     def _scratch(self, n_bytes, stream):
         """A buffer of a call's own, on the call's stream."""
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        if stream is None:
+            return torch.empty(n_bytes, dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(stream):
             return torch.empty(n_bytes, dtype=torch.uint8, device=self.device)
 
     def workspace(self, schema: B.Schema) -> torch.Tensor:
