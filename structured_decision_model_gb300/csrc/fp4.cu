@@ -1,8 +1,7 @@
 // Rows into microscaled 4-bit form and back.
 //
 // Quantise.  A row belongs to one or more whole warps and stays in their registers: its
-// largest sizes, its mean and variance (two passes over registers, so exact to fp32
-// rounding) and its codes come from one read of memory.  A lane holds 8 consecutive values of
+// largest sizes, its mean and variance and its codes come from one read of memory.  A lane holds 8 consecutive values of
 // every 256-value tile (one 16-byte read, one 4-byte write: both whole lines a warp), so a
 // block of 16 or 32 values is 2 or 4 neighbouring lanes.
 //
@@ -203,34 +202,36 @@ __device__ __forceinline__ float row_max(float v, float* red, int W, int warp) {
     return v;
 }
 
-// The sum over a row of what lane l has for piece i * W + part in v[i]: pieces in order, then lanes, so that it
-// does not depend on how many warps share the row.
-template <int STEPS, int LANES>
-__device__ __forceinline__ float row_sum(const float (&v)[STEPS], float (*red)[32], int W, int warp, int lane) {
-    float s = 0.f;
-    if (LANES < 32 || W == 1) {
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) s += v[i];
-    } else {
-        float(*mine)[32] = red + warp / W * W * STEPS;  // the row's pieces
-        __syncthreads();  // red may still be read from the last call
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) mine[i * W + warp % W][lane] = v[i];
-        __syncthreads();
-        for (int i = 0; i < STEPS * W; ++i) s += mine[i][lane];
+// Sums over a row of what its lanes have for each of its pieces: pieces in order, then lanes, so that a sum
+// does not depend on how many warps share the row.  One warp (or a half) adds up as it goes; several
+// leave what they have in shared memory.
+template <int LANES>
+struct RowSum {
+    float (*all)[32];  // the row's pieces
+    float own = 0.f;
+    __device__ __forceinline__ void add(float v, int W, int piece, int lane) {
+        if (LANES < 32 || W == 1) own += v;
+        else all[piece][lane] = v;
     }
-    return lanes_sum<LANES>(s);
-}
+    __device__ __forceinline__ float get(int W, int pieces, int lane) {
+        if (LANES == 32 && W > 1) {
+            __syncthreads();
+            own = 0.f;
+            for (int i = 0; i < pieces; ++i) own += all[i][lane];
+        }
+        return lanes_sum<LANES>(own);
+    }
+};
 
 // STEPS: 512-value pieces of a row that a warp keeps, 16 values a lane; W warps a row (a power of
 // two), so a row has at most 512 * STEPS * W values.  LANES 16: rows of up to 256 values, two a warp.
-// 64 registers a thread, for 32 warps an SM: with 8 pieces a warp and half the warps 131072 x 4096 bf16 took 301 us
+// EXTRA: statistics or sums are asked for.  64 registers a thread, for 32 warps an SM: with 8 pieces a warp and half the warps 131072 x 4096 bf16 took 301 us
 // instead of 252.
-template <int FMT, int DT, bool VEC, int STEPS, int LANES>
+template <int FMT, int DT, bool VEC, int STEPS, int LANES, bool EXTRA>
 __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 4) fp4_quantize_kernel(const Fp4QuantizeArgs a, int W) {
     constexpr bool NV = FMT == CLEF_NVFP4;
     __shared__ float red[kThreads / 32];
-    __shared__ float partial[kThreads / 32 * STEPS][32];
+    __shared__ float partial[EXTRA ? 3 : 1][EXTRA ? kThreads / 32 * STEPS : 1][32];
     __shared__ __align__(16) uint32_t stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 32 * Raw<DT>::kWords];
     griddep_wait();
     griddep_launch();  // behind the wait: whoever starts early may take what came before us as done
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
     const bool mine = row < a.rows;  // threads behind the last row still meet the barriers and shuffles
     const int part = LANES == 32 ? warp % W : 0;
     const int padded = mine ? (a.cols + kFp4Tile - 1) / kFp4Tile * kFp4Tile : 0;  // columns that have scales
-    const bool stats = a.mean != nullptr;
+    const bool stats = EXTRA && a.mean, sums = EXTRA && a.sums;  // the same for every thread
     const int64_t row0 = row * a.row_stride;
 
     Raw<DT> raw[STEPS];
@@ -253,8 +254,8 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
             raw[i] = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
         else raw[i] = Raw<DT>{};
     }
-    // the largest size of every block and of the row's finite blocks, and the row's sum
-    float top[STEPS], sum[STEPS], row_top = 0.f;
+    // the largest size of every block and of the row's finite blocks
+    float top[STEPS], row_top = 0.f;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         uint32_t t = raw[i].top();
@@ -270,15 +271,7 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
                 }
             }
         }
-        if (stats) {
-            uint64_t t2 = add2(raw[i].two(0), raw[i].two(1));
-#pragma unroll
-            for (int j = 2; j < 8; j += 2) t2 = add2(t2, add2(raw[i].two(j), raw[i].two(j + 1)));
-            const float2 f = both_of(t2);
-            sum[i] = f.x + f.y;
-        }
     }
-    const float mean = stats ? row_sum<STEPS, LANES>(sum, partial, W, warp, lane) / float(a.cols) : 0.f;
     float inv_r = 1.f, r = 1.f;
     bool tiny = false;
     if constexpr (NV) {
@@ -293,11 +286,11 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
     uint8_t* codes = a.codes + row * code_stride;
     uint8_t* scales = a.scales + (row / kFp4RowGroup * (padded >> (NV ? 6 : 7))) * kFp4ScaleGroup +
                       (row % 32) * 16 + (row % kFp4RowGroup) / 32 * 4;
-    const uint64_t less = pair_of(-mean, -mean);
-    float total[STEPS], squares[STEPS];
+    const int first = EXTRA ? warp / W * W * STEPS : 0;  // of the row's pieces among the block's
+    RowSum<LANES> sum{partial[0] + first}, squares{partial[EXTRA ? 1 : 0] + first}, total{partial[EXTRA ? 2 : 0] + first};
+    const int pieces = (a.cols + 511) / 512;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-        total[i] = squares[i] = 0.f;
         if (LANES == 32 && (i * W + part) * 512 >= padded) continue;  // the same for a whole warp
         const int col = (i * W + part) * 512 + lane * 16;
         const int left = a.cols - col;  // values from the lane's first to the row's end
@@ -317,23 +310,16 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
         uint64_t x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = raw[i].two(j);
-        if (stats) {
-            if (left >= 16) {
-                uint64_t t = 0;
+        if (stats) {  // (what lies behind the row's end is 0)
+            uint64_t t = x[0], u = mul2(x[0], x[0]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint64_t d = add2(x[j], less);
-                    t = fma2(d, d, t);
-                }
-                const float2 t2 = both_of(t);
-                squares[i] = t2.x + t2.y;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float d = j < left ? raw[i].at(j) - mean : 0.f;
-                    squares[i] = fmaf(d, d, squares[i]);
-                }
+            for (int j = 1; j < 8; ++j) {
+                t = add2(t, x[j]);
+                u = fma2(x[j], x[j], u);
             }
+            const float2 t2 = both_of(t), u2 = both_of(u);
+            sum.add(t2.x + t2.y, W, i * W + part, lane);
+            squares.add(u2.x + u2.y, W, i * W + part, lane);
         }
         float v[16];
         if constexpr (DT == CLEF_FP32) {
@@ -379,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
         word |= __shfl_xor_sync(0xffffffffu, word, NV ? 2 : 4);
         if ((lane & (NV ? 3 : 7)) == 0 && col < padded)
             *reinterpret_cast<uint32_t*>(scales + int64_t(col >> (NV ? 6 : 7)) * kFp4ScaleGroup) = word;
-        if (a.sums) {
+        if (sums) {
             uint32_t h[8];
             unpack_e2m1(packed.x, h);
             unpack_e2m1(packed.y, h + 4);
@@ -389,18 +375,44 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
                 t += f.x + f.y;
             }
-            total[i] = t * (bad ? __uint_as_float(0x7FC00000u) : scale);
+            total.add(t * (bad ? __uint_as_float(0x7FC00000u) : scale), W, i * W + part, lane);
         }
     }
     if (stats) {
-        const float var = row_sum<STEPS, LANES>(squares, partial, W, warp, lane) / float(a.cols);
+        const float mean = sum.get(W, pieces, lane) / float(a.cols);
+        float var = squares.get(W, pieces, lane) / float(a.cols) - mean * mean;
+        // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows (and those
+        // whose squares pass fp32) are read once more and sum the squares of what is left behind the mean.
+        const bool far = mine && !(mean * mean <= var);
+        if (LANES < 32 || W == 1 ? __any_sync(0xffffffffu, far) : __syncthreads_or(far)) {
+            const uint64_t less = pair_of(-mean, -mean);
+            RowSum<LANES> apart{sum.all};  // every thread is past the sums' barriers, and has read them
+#pragma unroll 1
+            for (int i = 0; i < STEPS; ++i) {
+                if (LANES == 32 && (i * W + part) * 512 >= padded) continue;
+                const int col0 = (i * W + part) * 512;
+                const int left = a.cols - (col0 + lane * 16);  // values from the lane's first to the row's end
+                uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
+                const Raw<DT> again = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
+                float q = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 d = both_of(add2(again.two(j), less));
+                    if (2 * j < left) q = fmaf(d.x, d.x, q);
+                    if (2 * j + 1 < left) q = fmaf(d.y, d.y, q);
+                }
+                apart.add(q, W, i * W + part, lane);
+            }
+            const float v = apart.get(W, pieces, lane) / float(a.cols);
+            if (far) var = v;
+        }
         if (mine && part == 0 && lane == 0) {
             a.mean[row] = mean;
             a.rstd[row] = 1.f / sqrtf(var + 1e-5f);
         }
     }
-    if (a.sums) {
-        const float all = row_sum<STEPS, LANES>(total, partial, W, warp, lane);
+    if (sums) {
+        const float all = total.get(W, pieces, lane);
         if (mine && part == 0 && lane == 0) a.sums[row] = all * r;
     }
 }
@@ -410,39 +422,58 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
 // stores its 8 at once; otherwise the warp hands the values round and stores 32 neighbours at a time.
 constexpr int kBack = 1024;
 
-template <int FMT, int DT, bool VEC>
+// SHORT (VEC only): rows of up to 256 values; a warp takes 128 neighbouring eights of any rows.
+template <int FMT, int DT, bool VEC, bool SHORT>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4DequantizeArgs a) {
     constexpr bool NV = FMT == CLEF_NVFP4;
     __shared__ __align__(16) float stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 256];
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pieces = (a.cols + kBack - 1) / kBack;
     const uint64_t item = uint64_t(blockIdx.x) * (kThreads / 32) + warp;
-    const int64_t row = int64_t(item / uint32_t(pieces));
-    if (row >= a.rows) return;
-    const int col0 = int(item - uint64_t(row) * uint32_t(pieces)) * kBack;
     const int64_t code_stride = int64_t(a.cols + 31) / 32 * 16;
     const int kgroups = (a.cols + kFp4Tile - 1) / kFp4Tile * (NV ? 4 : 2);
-    const uint8_t* codes = a.codes + row * code_stride;
-    const uint8_t* scales = a.scales + (row / kFp4RowGroup * kgroups) * kFp4ScaleGroup + (row % 32) * 16 +
-                            (row % kFp4RowGroup) / 32 * 4;
-    const float r = NV ? a.row_scale[row] : 1.f;
+    int64_t row0;  // the warp's first row, and where in it
+    int at0;       // (SHORT: in eights)
+    const uint32_t per = SHORT ? uint32_t(a.cols) / 8 : uint32_t(a.cols + kBack - 1) / kBack;
+    if constexpr (SHORT) {
+        row0 = int64_t(item * 128 / per);
+        at0 = int(item * 128 - uint64_t(row0) * per);
+    } else {
+        row0 = int64_t(item / per);
+        at0 = int(item - uint64_t(row0) * per) * kBack;
+    }
+    if (row0 >= a.rows) return;
+    int64_t rows[4];
+    int cols[4];
     uint32_t packed[4], byte[4];
+    float r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int col = col0 + i * 256 + lane * 8;
-        const int block = NV ? col >> 4 : col >> 5;
+        if constexpr (SHORT) {
+            const uint32_t t = uint32_t(at0) + i * 32 + lane;
+            rows[i] = row0 + t / per;
+            cols[i] = rows[i] < a.rows ? int(t % per) * 8 : a.cols;
+        } else {
+            rows[i] = row0;
+            cols[i] = at0 + i * 256 + lane * 8;
+        }
+        const int64_t row = rows[i];
+        const int block = NV ? cols[i] >> 4 : cols[i] >> 5;
         packed[i] = byte[i] = 0;
-        if (col < a.cols) {
-            packed[i] = *reinterpret_cast<const uint32_t*>(codes + col / 2);
-            byte[i] = scales[int64_t(block >> 2) * kFp4ScaleGroup + (block & 3)];
+        r[i] = 1.f;
+        if (cols[i] < a.cols) {
+            packed[i] = *reinterpret_cast<const uint32_t*>(a.codes + row * code_stride + cols[i] / 2);
+            byte[i] = a.scales[(row / kFp4RowGroup * kgroups + (block >> 2)) * kFp4ScaleGroup + (row % 32) * 16 +
+                               (row % kFp4RowGroup) / 32 * 4 + (block & 3)];
+            if (NV) r[i] = a.row_scale[row];
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int col = col0 + i * 256 + lane * 8;
-        if (col0 + i * 256 >= a.cols) break;  // the same for a whole warp
+        const int64_t row = rows[i];
+        const int col = cols[i];
+        if (!SHORT && at0 + i * 256 >= a.cols) break;  // the same for a whole warp
         float scale;
         if constexpr (NV) scale = from_e4m3(byte[i]);
         else scale = byte[i] == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte[i] == 0 ? 0x00400000u : byte[i] << 23);
@@ -452,8 +483,8 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-            v[2 * j] = f.x * scale * r;
-            v[2 * j + 1] = f.y * scale * r;
+            v[2 * j] = f.x * scale * r[i];
+            v[2 * j + 1] = f.y * scale * r[i];
         }
         if constexpr (VEC) {
             if (col >= a.cols) continue;
@@ -484,7 +515,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int c = col0 + i * 256 + j * 32 + lane;
+                const int c = at0 + i * 256 + j * 32 + lane;
                 if (c >= a.cols) continue;
                 const float y = to[j * 32 + lane];
                 const int64_t at = row * a.row_stride + c;
@@ -496,7 +527,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
     }
 }
 
-template <int FMT, int DT, bool VEC>
+template <int FMT, int DT, bool VEC, bool EXTRA>
 cudaError_t quantize_rows(const Fp4QuantizeArgs& a, cudaStream_t s) {
     // Few rows: as many warps a row as it has pieces, for latency.  Many: as few as hold the row in
     // registers (4 pieces of 16-bit values, 2 of fp32).
@@ -506,13 +537,13 @@ cudaError_t quantize_rows(const Fp4QuantizeArgs& a, cudaStream_t s) {
     int W = 1;
     while (W < 8 && W < pieces && (pieces > kMost * W || int64_t(a.rows) * W < warps)) W *= 2;
     if (a.cols <= 256)
-        return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 16>, dim3(unsigned((int64_t(a.rows) + 15) / 16)),
+        return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 16, EXTRA>, dim3(unsigned((int64_t(a.rows) + 15) / 16)),
                           dim3(kThreads), 0, s, a, 1);
     const int steps = (pieces + W - 1) / W;
     const dim3 grid(unsigned((int64_t(a.rows) * W + kThreads / 32 - 1) / (kThreads / 32)));
-    if (steps <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 32>, grid, dim3(kThreads), 0, s, a, W);
-    if (steps <= 2) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 2, 32>, grid, dim3(kThreads), 0, s, a, W);
-    if (steps <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4, 32>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 2) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 2, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, W);
     return cudaErrorInvalidValue;
 }
 
@@ -520,7 +551,9 @@ template <int FMT, int DT>
 cudaError_t quantize_type(const Fp4QuantizeArgs& a, cudaStream_t s) {
     constexpr int size = DT == CLEF_FP32 ? 4 : 2;
     const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.row_stride * size % 16 == 0 && a.cols % 8 == 0;
-    return vec ? quantize_rows<FMT, DT, true>(a, s) : quantize_rows<FMT, DT, false>(a, s);
+    const bool extra = a.mean || a.sums;
+    if (vec) return extra ? quantize_rows<FMT, DT, true, true>(a, s) : quantize_rows<FMT, DT, true, false>(a, s);
+    return extra ? quantize_rows<FMT, DT, false, true>(a, s) : quantize_rows<FMT, DT, false, false>(a, s);
 }
 
 template <int FMT, int DT>
@@ -528,10 +561,13 @@ cudaError_t dequantize_type(const Fp4DequantizeArgs& a, cudaStream_t s) {
     constexpr int size = DT == CLEF_FP32 ? 4 : 2;
     constexpr int piece = 8 * size;
     const bool vec = reinterpret_cast<uintptr_t>(a.out) % piece == 0 && a.row_stride * size % piece == 0 && a.cols % 8 == 0;
-    const int64_t items = int64_t(a.rows) * ((a.cols + kBack - 1) / kBack);
+    const bool brief = vec && a.cols <= 256;
+    const int64_t items = brief ? (int64_t(a.rows) * (a.cols / 8) + 127) / 128
+                                : int64_t(a.rows) * ((a.cols + kBack - 1) / kBack);
     const int64_t blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    return launch_pdl(vec ? fp4_dequantize_kernel<FMT, DT, true> : fp4_dequantize_kernel<FMT, DT, false>,
+    return launch_pdl(brief ? fp4_dequantize_kernel<FMT, DT, true, true>
+                      : vec ? fp4_dequantize_kernel<FMT, DT, true, false> : fp4_dequantize_kernel<FMT, DT, false, false>,
                       dim3(unsigned(blocks)), dim3(kThreads), 0, s, a);
 }
 

@@ -224,6 +224,40 @@ def test_a_row_depends_on_itself_alone():
     assert torch.equal(layer(x2)[0], y[0])
 
 
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("cols", [8, 24, 32, 104, 256])
+def test_many_short_rows(form, cols):
+    """Two rows a warp going in, eights of any rows coming back; the last warp is part full."""
+    x = rows_of(1003, cols, torch.bfloat16, cols)
+    m = quantize(x, form, stats=True)
+    values = check_kept(x, form, m)
+    assert torch.equal(m.dequantize(torch.float32).cpu(), torch.from_numpy(values).float())
+    wide = torch.full((1003, cols + 8), 5.0, dtype=torch.bfloat16, device="cuda")
+    m.dequantize(torch.bfloat16, wide[:, :cols])
+    assert torch.equal(wide[:, :cols], m.dequantize()) and (wide[:, cols:] == 5).all()
+    v = x.double()
+    mean = v.mean(1)
+    assert ((m.mean.double() - mean).abs() <= 42 * 2.0 ** -24 * v.abs().mean(1)).all()
+    var = (v - mean[:, None]).square().mean(1)
+    assert ((m.rstd.double() * (var + EPS).sqrt() - 1).abs() <= 30 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(4, 100), (3, 1000), (2500, 4096), (2, 8192)])
+def test_rows_far_from_zero_keep_their_spread(rows, cols):
+    """Means from none to 2000 times the spread, side by side, and rows whose squares pass fp32."""
+    x = rows_of(rows, cols, torch.float32, 11, 0.2)
+    x += torch.tensor([0.0, 2000.0, -30.0, 1.5], device="cuda").repeat(rows)[:rows, None]
+    m = quantize(x, "nvfp4", stats=True)
+    v = x.double()
+    mean = v.mean(1)
+    var = (v - mean[:, None]).square().mean(1)
+    assert ((m.mean.double() - mean).abs() <= 42 * 2.0 ** -24 * v.abs().mean(1)).all()
+    # the mean's own rounding (half a step of 2000) comes in squared, against a spread of about 1
+    assert ((m.rstd.double() * (var + EPS).sqrt() - 1).abs() <= 30 * 2.0 ** -24 + (42 * 2.0 ** -24 * 2000) ** 2).all()
+    y = quantize(x * 1e30, "nvfp4", stats=True)
+    assert (y.rstd == 0).all()
+
+
 def test_statistics_do_not_depend_on_the_number_of_rows():
     """Few rows are shared among more warps than many: the same sums in the same order."""
     for cols in (1000, 4096, 16384):
