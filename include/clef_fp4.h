@@ -44,6 +44,7 @@ extern "C" {
 typedef enum clef_fp4_format { CLEF_MXFP4 = 0, CLEF_NVFP4 = 1 } clef_fp4_format;
 
 #define CLEF_FP4_MAX_COLS 16384
+#define CLEF_FP4_FEW_ROWS 8
 
 /* A matrix of rows kept in 4 bits.  codes and scales: 256-byte aligned device memory of the
  * sizes that clef_fp4_size gives; row_scale: [rows] fp32, NULL for CLEF_MXFP4.
@@ -86,7 +87,9 @@ CLEF_API int clef_fp4_linear_scratch(int32_t format, int32_t rows, int32_t cols,
 /* A layer with 4-bit weights: clef_fp4_quantize of the `rows` rows x in w's format, then clef_fp4_product with
  * w, the same numbers by one call.  With `sums` (of w's rows) the rows are normalized as there, and their
  * mean and rstd ([rows] fp32, both needed then) come back too; without, all three are NULL.
- * scratch: 256-byte aligned device memory of the call's own until it has run. */
+ * scratch: 256-byte aligned device memory of the call's own until it has run.  Up to CLEF_FP4_FEW_ROWS rows whose
+ * values number a multiple of 8 and whose rows start on 16 bytes (one row: x does) are quantised inside the
+ * product, in one launch: scratch is not used then and may be NULL. */
 CLEF_API int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
                              const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride,
                              float* mean, float* rstd, void* scratch, size_t scratch_bytes, int32_t* flags,

@@ -32,6 +32,7 @@ BF16, FP16, FP32 = 0, 1, 2   # clef_dtype
 CACHE_MAX_REQUESTS = 1024
 MXFP4, NVFP4 = 0, 1          # clef_fp4_format
 FP4_MAX_COLS = 16384
+FP4_FEW_ROWS = 8
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 

@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libclef_head.so")
 SOURCES = ["gemm.cu", "attention.cu", "head_kernels.cu", "record_tail.cu", "api.cu", "cache.cu", "cache_attend.cu",
-           "cache_attend_rows.cu", "cache_api.cu", "fp4.cu", "fp4_product.cu", "fp4_api.cu"]
+           "cache_attend_rows.cu", "cache_api.cu", "fp4.cu", "fp4_product.cu", "fp4_few.cu",
+           "fp4_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 

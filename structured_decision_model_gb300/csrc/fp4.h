@@ -57,10 +57,20 @@ struct Fp4ProductArgs {
     int kgroups;           // scale groups of a row group
     int splits;            // K parts of a tile (a cluster)
     int paired;            // 16-bit outputs: rows and columns allow stores of two values at a time
+    const void* x;         // few rows as they come: rows x_stride elements apart, of `cols` values,
+    int64_t x_stride;      // their statistics (with sums: the LayerNorm fold) going out
+    float* mean_out;
+    float* rstd_out;
+    int cols;
     int w_settled;         // no kernel that may still run on the stream writes w: it may be read ahead of them
     int bulk;              // 16-bit outputs: rows start and end on 16 bytes, so that TMA can store them
 };
 cudaError_t launch_fp4_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, int dtype,
                                cudaStream_t s);
+
+
+// Rows that the product quantises itself, in one launch: whether it can, and the launch (a.M rows of type x_dtype).
+bool fp4_few_rows(int rows, int cols, int x_dtype, const void* x, int64_t x_stride);
+cudaError_t launch_fp4_few(const clef_fp4& w, const Fp4ProductArgs& a, int x_dtype, int dtype, cudaStream_t s);
 
 }  // namespace clef

@@ -79,9 +79,9 @@ int check_product(const clef_fp4& x, const clef_fp4& w, const float* bias, const
     return CLEF_OK;
 }
 
-// A checked product.  `w_settled`: nothing that may still run on the stream writes w.
-int multiply(const clef_fp4& x, const clef_fp4& w, const float* bias, const float* mean, const float* rstd,
-             const float* sums, int dtype, void* out, int64_t row_stride, int32_t* flags, bool w_settled, void* stream) {
+// The arguments of a checked product.  `w_settled`: nothing that may still run on the stream writes w.
+Fp4ProductArgs product_args(const clef_fp4& x, const clef_fp4& w, const float* bias, const float* mean, const float* rstd,
+                            const float* sums, int dtype, void* out, int64_t row_stride, int32_t* flags, bool w_settled) {
     Fp4ProductArgs a{};
     a.x_scale = x.format == CLEF_NVFP4 ? x.row_scale : nullptr;
     a.w_scale = w.format == CLEF_NVFP4 ? w.row_scale : nullptr;
@@ -101,8 +101,11 @@ int multiply(const clef_fp4& x, const clef_fp4& w, const float* bias, const floa
     // TMA writes whole 16-byte pieces of a row, also where the row ends inside one
     a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && w.rows % 8 == 0 && !misaligned(out, 16);
     a.w_settled = w_settled;
-    return launch_fp4_product(x, w, a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK : CLEF_ERR_CUDA;
+    a.cols = x.cols;
+    return a;
 }
+
+int status(cudaError_t e) { return e == cudaSuccess ? CLEF_OK : CLEF_ERR_CUDA; }
 
 // Where the rows of a layer's call lie in its scratch.
 struct Scratch {
@@ -151,8 +154,7 @@ int clef_fp4_quantize(const clef_fp4* q, int32_t dtype, const void* x, int64_t r
     }
     const Fp4QuantizeArgs a{x, row_stride, static_cast<uint8_t*>(q->codes), static_cast<uint8_t*>(q->scales),
                             q->row_scale, mean, rstd, sums, q->rows, q->cols};
-    return launch_fp4_quantize(a, q->format, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
-                                                                                                      : CLEF_ERR_CUDA;
+    return status(launch_fp4_quantize(a, q->format, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int clef_fp4_dequantize(const clef_fp4* q, int32_t dtype, void* out, int64_t row_stride, void* stream) {
@@ -164,8 +166,7 @@ int clef_fp4_dequantize(const clef_fp4* q, int32_t dtype, void* out, int64_t row
         return CLEF_ERR_INVALID_ARGUMENT;
     const Fp4DequantizeArgs a{static_cast<const uint8_t*>(q->codes), static_cast<const uint8_t*>(q->scales),
                               q->row_scale, out, row_stride, q->rows, q->cols};
-    return launch_fp4_dequantize(a, q->format, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CLEF_OK
-                                                                                                        : CLEF_ERR_CUDA;
+    return status(launch_fp4_dequantize(a, q->format, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, const float* mean, const float* rstd,
@@ -174,7 +175,8 @@ int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, co
     if (st == CLEF_OK) st = check_matrix(w);
     if (st == CLEF_OK) st = check_product(*x, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags);
     if (st != CLEF_OK) return st;
-    return multiply(*x, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, false, stream);
+    return status(launch_fp4_product(*x, *w, product_args(*x, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, false),
+                                     dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int clef_fp4_linear_scratch(int32_t format, int32_t rows, int32_t cols, size_t* bytes) {
@@ -191,16 +193,20 @@ int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x
     int st = check_matrix(w);
     if (st == CLEF_OK) st = check_size(w->format, rows, w->cols);
     if (st != CLEF_OK) return st;
-    if (bad_type(x_dtype) || bad_rows(x, x_dtype, x_stride, 0) || !scratch || misaligned(scratch, 256))
-        return CLEF_ERR_INVALID_ARGUMENT;
+    if (bad_type(x_dtype) || bad_rows(x, x_dtype, x_stride, 0)) return CLEF_ERR_INVALID_ARGUMENT;
+    const bool few = fp4_few_rows(rows, w->cols, x_dtype, x, x_stride);
     const Scratch S(w->format, rows, w->cols);
-    if (scratch_bytes < S.total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
-    const clef_fp4 q = S.matrix(scratch, w->format, rows, w->cols);
+    clef_fp4 q{nullptr, nullptr, nullptr, rows, w->cols, w->format};
+    if (!few) {
+        if (!scratch || misaligned(scratch, 256)) return CLEF_ERR_INVALID_ARGUMENT;
+        if (scratch_bytes < S.total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+        q = S.matrix(scratch, w->format, rows, w->cols);
+    }
     st = check_product(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags);
     if (st != CLEF_OK) return st;
     // what is written: the scratch, the statistics and the output, apart from each other and from what is read
     const int64_t m4 = int64_t(rows) * 4, n4 = int64_t(w->rows) * 4;
-    const Run space(scratch, int64_t(S.total)), in = rows_run(x, rows, x_stride, w->cols, size_of(x_dtype)),
+    const Run space(few ? nullptr : scratch, int64_t(S.total)), in = rows_run(x, rows, x_stride, w->cols, size_of(x_dtype)),
         to = rows_run(out, rows, row_stride, w->rows, size_of(dtype));
     const Run reads[] = {in, codes_run(*w), scales_run(*w), row_scale_run(*w), Run(bias, n4), Run(sums, n4), Run(flags, 4)};
     for (const Run& r : reads)
@@ -208,10 +214,21 @@ int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x
     if (to.meets(in) || to.meets(space) || space.meets(Run(mean, m4)) || space.meets(Run(rstd, m4)) ||
         Run(mean, m4).meets(Run(rstd, m4)))
         return CLEF_ERR_INVALID_ARGUMENT;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Fp4ProductArgs p = product_args(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, true);
+    if (few) {  // one launch
+        p.x = x;
+        p.x_stride = x_stride;
+        p.x_scale = p.mean = p.rstd = nullptr;
+        p.mean_out = mean;
+        p.rstd_out = rstd;
+        p.w_settled = false;  // the kernel before this one may be w's
+        return status(launch_fp4_few(*w, p, x_dtype, dtype, s));
+    }
     const Fp4QuantizeArgs a{x, x_stride, static_cast<uint8_t*>(q.codes), static_cast<uint8_t*>(q.scales), q.row_scale,
                             mean, rstd, nullptr, rows, w->cols};
-    if (launch_fp4_quantize(a, w->format, x_dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CLEF_ERR_CUDA;
-    return multiply(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, true, stream);
+    const int quantised = status(launch_fp4_quantize(a, w->format, x_dtype, s));
+    return quantised == CLEF_OK ? status(launch_fp4_product(q, *w, p, dtype, s)) : quantised;
 }
 
 }  // extern "C"

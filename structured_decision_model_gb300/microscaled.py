@@ -200,6 +200,7 @@ class Fp4Linear:
         self._flags = weight.flags.data_ptr()  # made here, outside of any later capture
         self._device, self._index = weight.device, weight._index
         self._lib, self._struct = B.load(), weight.struct
+        self._ragged = self.cols % 8 != 0
         self._scratch = {}  # scratch bytes of the numbers of rows that the layer has met
 
     def _run(self, x, dtype, normalized):
@@ -230,17 +231,21 @@ class Fp4Linear:
             rstd = torch.empty(n, dtype=_FP32, device=self._device)
             mean_at, rstd_at, sums_at = mean.data_ptr(), rstd.data_ptr(), self.weight.sums.data_ptr()
         if n:
-            # a buffer of the call's own: overlapping calls and captured graphs never share one
-            size = self._scratch.get(n)
-            if size is None:
-                if len(self._scratch) >= 4096:
-                    self._scratch.clear()
-                size = self._scratch[n] = B.clef_fp4_linear_scratch(self.weight.struct.format, n, self.cols)
-            scratch = torch.empty(size, dtype=torch.uint8, device=self._device)
+            at, size, scratch = rows.data_ptr(), 0, None
+            stride = stride if n > 1 else self.cols
+            # few rows that start on 16 bytes need no scratch; otherwise a buffer of the call's own: overlapping
+            # calls and captured graphs never share one
+            if n > B.FP4_FEW_ROWS or self._ragged or at & 15 or stride * x.element_size() & 15:
+                size = self._scratch.get(n)
+                if size is None:
+                    if len(self._scratch) >= 4096:
+                        self._scratch.clear()
+                    size = self._scratch[n] = B.clef_fp4_linear_scratch(self._struct.format, n, self.cols)
+                space = torch.empty(size, dtype=torch.uint8, device=self._device)
+                scratch = space.data_ptr()
             status = self._lib.clef_fp4_linear(
-                self._struct, x_type, rows.data_ptr(), stride if n > 1 else self.cols, n, self._bias, sums_at, out_type,
-                y.data_ptr(), self.outs, mean_at, rstd_at, scratch.data_ptr(), size, self._flags,
-                _raw_stream(self._index))
+                self._struct, x_type, at, stride, n, self._bias, sums_at, out_type, y.data_ptr(), self.outs, mean_at,
+                rstd_at, scratch, size, self._flags, _raw_stream(self._index))
             if status:
                 raise B.ClefError(status, "clef_fp4_linear")
         if len(shape) != 2:

@@ -86,7 +86,7 @@ def test_product_refusals():
 
 def test_layer_refusals():
     w = matrix(at=4 * P, rows=20)
-    size = B.clef_fp4_linear_scratch(B.NVFP4, 10, 100)
+    size = B.clef_fp4_linear_scratch(B.NVFP4, 10, 100)  # ragged rows: never without scratch
     good = [w, B.BF16, 8 * P, 100, 10, 12 * P, 15 * P, B.BF16, 9 * P, 20, 13 * P, 14 * P, 20 * P, size, 16 * P]
     for i, v in ((1, 5), (2, None), (3, -1), (5, 12 * P + 1), (6, None), (7, 9), (8, None), (9, 19), (10, None), (11, None),
                  (12, None), (12, 20 * P + 8), (14, None),
@@ -94,6 +94,12 @@ def test_layer_refusals():
         refused(1, B.clef_fp4_linear, *changed(good, i, v))
     refused(2, B.clef_fp4_linear, *changed(good, 13, size - 1))
     refused(3, B.clef_fp4_linear, *changed(good, 4, 0))
+    # few rows: without scratch only where each starts on 16 bytes and has a multiple of 8 values
+    w = matrix(at=4 * P, rows=20, cols=104)
+    few = [w, B.BF16, 8 * P, 104, 8, *good[5:12], None, 0, None]
+    for i, v in ((2, 8 * P + 2), (3, 107), (0, matrix(at=4 * P, rows=20, cols=100)), (4, 9)):
+        refused(1, B.clef_fp4_linear, *changed(changed(few, i, v), 14, 16 * P))
+    refused(1, B.clef_fp4_linear, *few)  # no flags
 
 
 def test_head_refusals():

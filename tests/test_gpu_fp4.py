@@ -325,6 +325,32 @@ def test_the_layer_is_its_steps():
     assert torch.equal(Fp4Linear(kept_data, bias, "mxfp4")(x), layer(x))
 
 
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 1, 8), (1, 100, 4096), (2, 300, 264), (5, 128, 1000), (7, 520, 16384), (8, 17000, 1032),
+                                   (8, 777, 5120), (3, 4096, 8192)])
+def test_few_rows_are_quantised_inside_the_product(form, dtype, m, n, k):
+    """One launch gives what the steps give, bit for bit, statistics too; every type in and out."""
+    x = rows_of(m, k, TYPES[dtype], m + k, 0.5) + 0.25
+    if m > 2:
+        x[1] += 500.0                        # far from zero
+        x[2, :k // 2] = 0.0
+        x[m - 1, k - 1] = float("inf")
+    layer = Fp4Linear(rows_of(n, k, torch.bfloat16, n, 0.5), torch.randn(n, device="cuda"), form)
+    q = quantize(x, form, stats=True)
+    for out in TYPES.values():
+        same = lambda a, b: torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+        assert same(layer(x, out), product(q, layer.weight, layer.bias, out))
+        y, mean, rstd = layer.normalized(x, out)
+        assert same(y, product(q, layer.weight, layer.bias, out, normalized=True))
+        assert same(mean, q.mean) and same(rstd, q.rstd)
+    wide = torch.zeros(m, k + 24, dtype=x.dtype, device="cuda")
+    for first in (0, 8, 3):                  # the last starts off 16 bytes: the steps again
+        wide[:, first:first + k] = x
+        assert same(layer(wide[:, first:first + k]), layer(x))
+    assert layer.device_status() == 0
+
+
 def test_streams_and_graphs():
     """Calls on two streams at once, and two captured graphs of one layer replayed in turn on new inputs."""
     layer = Fp4Linear(rows_of(1024, 512, torch.bfloat16, 1), torch.randn(1024, device="cuda"))
