@@ -56,21 +56,23 @@ Run codes_run(const clef_fp4& q) { return Run(q.codes, codes_bytes(q)); }
 Run scales_run(const clef_fp4& q) { return Run(q.scales, scales_bytes(q)); }
 Run row_scale_run(const clef_fp4& q) { return Run(q.format == CLEF_NVFP4 ? q.row_scale : nullptr, int64_t(q.rows) * 4); }
 
-// Rows of `cols` elements at `stride`: aligned to the element, and offsets that 64 bits hold.
-bool bad_rows(const void* p, int dtype, int64_t stride, int64_t least) {
-    return !p || misaligned(p, uintptr_t(size_of(dtype))) || stride < least || stride > (int64_t(1) << 31);
+// `rows` rows `stride` elements apart: aligned to the element, at least `least` apart, and no further from first to
+// last than memory reaches.
+bool bad_rows(const void* p, int dtype, int64_t rows, int64_t stride, int64_t least) {
+    return !p || misaligned(p, uintptr_t(size_of(dtype))) || stride < least || stride > kInt32 ||
+           (rows - 1) * stride > (int64_t(1) << 40);
 }
 
 int check_product(const clef_fp4& x, const clef_fp4& w, const float* bias, const float* mean, const float* rstd,
                   const float* sums, int dtype, const void* out, int64_t row_stride, const int32_t* flags) {
-    if (x.format != w.format || x.cols != w.cols || bad_type(dtype) || bad_rows(out, dtype, row_stride, w.rows) ||
+    // output tiles are counted in 32 bits
+    if ((int64_t(x.rows) + 31) / 32 * ((int64_t(w.rows) + 127) / 128) >= kInt32 / 16) return CLEF_ERR_UNSUPPORTED_CONFIG;
+    if (x.format != w.format || x.cols != w.cols || bad_type(dtype) || bad_rows(out, dtype, x.rows, row_stride, w.rows) ||
         !mean != !rstd || !mean != !sums || !flags)
         return CLEF_ERR_INVALID_ARGUMENT;
     for (const void* p : {static_cast<const void*>(bias), static_cast<const void*>(mean), static_cast<const void*>(rstd),
                           static_cast<const void*>(sums), static_cast<const void*>(flags)})
         if (misaligned(p, 4)) return CLEF_ERR_INVALID_ARGUMENT;
-    // output tiles are counted in 32 bits
-    if ((int64_t(x.rows) + 31) / 32 * ((int64_t(w.rows) + 127) / 128) >= kInt32 / 16) return CLEF_ERR_UNSUPPORTED_CONFIG;
     const int64_t m4 = int64_t(x.rows) * 4, n4 = int64_t(w.rows) * 4;
     const Run to = rows_run(out, x.rows, row_stride, w.rows, size_of(dtype));
     for (const Run& r : {codes_run(x), scales_run(x), row_scale_run(x), codes_run(w), scales_run(w), row_scale_run(w),
@@ -141,7 +143,7 @@ int clef_fp4_quantize(const clef_fp4* q, int32_t dtype, const void* x, int64_t r
                       float* sums, void* stream) {
     const int st = check_matrix(q);
     if (st != CLEF_OK) return st;
-    if (bad_type(dtype) || bad_rows(x, dtype, row_stride, 0) || !mean != !rstd || misaligned(mean, 4) ||
+    if (bad_type(dtype) || bad_rows(x, dtype, q->rows, row_stride, 0) || !mean != !rstd || misaligned(mean, 4) ||
         misaligned(rstd, 4) || misaligned(sums, 4))
         return CLEF_ERR_INVALID_ARGUMENT;
     const int64_t each = int64_t(q->rows) * 4;
@@ -160,7 +162,7 @@ int clef_fp4_quantize(const clef_fp4* q, int32_t dtype, const void* x, int64_t r
 int clef_fp4_dequantize(const clef_fp4* q, int32_t dtype, void* out, int64_t row_stride, void* stream) {
     const int st = check_matrix(q);
     if (st != CLEF_OK) return st;
-    if (bad_type(dtype) || bad_rows(out, dtype, row_stride, q->cols)) return CLEF_ERR_INVALID_ARGUMENT;
+    if (bad_type(dtype) || bad_rows(out, dtype, q->rows, row_stride, q->cols)) return CLEF_ERR_INVALID_ARGUMENT;
     const Run to = rows_run(out, q->rows, row_stride, q->cols, size_of(dtype));
     if (to.meets(codes_run(*q)) || to.meets(scales_run(*q)) || to.meets(row_scale_run(*q)))
         return CLEF_ERR_INVALID_ARGUMENT;
@@ -193,7 +195,7 @@ int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x
     int st = check_matrix(w);
     if (st == CLEF_OK) st = check_size(w->format, rows, w->cols);
     if (st != CLEF_OK) return st;
-    if (bad_type(x_dtype) || bad_rows(x, x_dtype, x_stride, 0)) return CLEF_ERR_INVALID_ARGUMENT;
+    if (bad_type(x_dtype) || bad_rows(x, x_dtype, rows, x_stride, 0)) return CLEF_ERR_INVALID_ARGUMENT;
     const bool few = fp4_few_rows(rows, w->cols, x_dtype, x, x_stride);
     const Scratch S(w->format, rows, w->cols);
     clef_fp4 q{nullptr, nullptr, nullptr, rows, w->cols, w->format};

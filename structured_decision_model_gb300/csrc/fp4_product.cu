@@ -241,10 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(leader_handed);
             if (!epilogue_agrees(got)) break;  // all warps or none; the row terms are there too
+            const int ahead = t + stride < n_tiles ? t + stride : t;
             ColumnTerms next[NCOL];
 #pragma unroll
-            for (int i = 0; i < NCOL; ++i) next[i] = column_terms(args, (t + stride) % n_wt * 2 * kWRows + lane_n + 8 * i);
-            row = row_terms(args, (t + stride) / n_wt * C::ROWS + tid);
+            for (int i = 0; i < NCOL; ++i) next[i] = column_terms(args, ahead % n_wt * 2 * kWRows + lane_n + 8 * i);
+            row = row_terms(args, ahead / n_wt * C::ROWS + tid);
             const int rows = min(C::ROWS, args.M - m0);
 #pragma unroll 1
             for (int c = 0; c < 128; c += 64) {

@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
         }
         __syncwarp();
     } else if (warp == 1) {
+        griddep_wait();  // the time that the kernel before takes does not count against this warp's waits
         const uint32_t sw = tmem + BN, sx = sw + C::S_COLS;
         const uint64_t d0 = smem_desc_sw128(smem_u32(smem)), c0 = scale_desc(smem_u32(smem) + kWBytes + C::X_BYTES);
         bool ok = true;

@@ -67,6 +67,12 @@ def test_quantize_refusals():
         refused(1, B.clef_fp4_quantize, *changed(good, i, v))
 
 
+def test_rows_further_apart_than_memory_reaches():
+    far = [matrix(rows=2 ** 20), B.BF16, 1 << 50, 2 ** 21, None, None, None]
+    refused(1, B.clef_fp4_quantize, *far)
+    refused(1, B.clef_fp4_dequantize, matrix(rows=2 ** 20), B.BF16, 1 << 50, 2 ** 21)
+
+
 def test_dequantize_refusals():
     good = [matrix(), B.FP32, 8 * P, 100]
     for i, v in ((1, 7), (2, None), (2, 8 * P + 2), (3, 99), (2, P + 4 * 100)):

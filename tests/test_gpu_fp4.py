@@ -168,6 +168,24 @@ def test_product(form, out, m, n, k):
     assert layer.device_status() == 0
 
 
+# more 128 x 128 tiles than two an SM (one, where K is long): CTA pairs; odd widths, ragged K, short last tiles
+PAIR_SHAPES = [(5000, 1100, 260), (4000, 1363, 1000), (1400, 1810, 4200), (40000, 24, 64)]
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("m,n,k", PAIR_SHAPES)
+def test_product_by_pairs(form, out, m, n, k):
+    x, w = rows_of(m, k, torch.bfloat16, m, 0.5), rows_of(n, k, torch.bfloat16, k, 0.5)
+    bias = torch.randn(n, device="cuda") * 3
+    layer = Fp4Linear(w, bias, form)
+    check_product(x, w, form, TYPES[out], bias, y=layer(x, TYPES[out]))
+    if out != "fp16":
+        x = x + 0.5
+        check_product(x, w, form, TYPES[out], bias, True, layer.normalized(x, TYPES[out])[0])
+    assert layer.device_status() == 0
+
+
 @pytest.mark.parametrize("form", FORMATS)
 @pytest.mark.parametrize("m,n,k", SHAPES)
 def test_normalized_product(form, m, n, k):
@@ -212,6 +230,23 @@ def test_outputs_stay_inside_their_rows(dtype, m):
         left = wide.clone()
         left.view(-1)[first:first + m * stride].view(m, stride)[:, :131] = 9.0
         assert (left == 9).all()
+
+
+@pytest.mark.parametrize("n", [136, 24, 131])
+def test_outputs_of_many_rows_stay_inside_theirs(n):
+    """The same of the pair kernel, whose outputs TMA stores where rows start and end on 16 bytes."""
+    m = 40100
+    x, w = quantize(rows_of(m, 64, torch.bfloat16, 3)), quantize(rows_of(n, 64, torch.bfloat16, 4))
+    want = x.dequantize(torch.float32) @ w.dequantize(torch.float32).T  # 64 products of 8 bits each: exact but for the sum
+    for t in (torch.bfloat16, torch.float32):
+        y = product(x, w, None, t)
+        assert ((y.float() - want).abs() <= want.abs() * (torch.finfo(t).eps / 2) + 2.0 ** -20 * want.abs().amax(1, keepdim=True)).all()
+        for stride, first in ((n, 0), (n + 8, 8), (n + 16, 0), (n + 1, 3), (n + 2, 2)):
+            wide = torch.full((m + 2, stride), 9.0, dtype=t, device="cuda")
+            out = wide.view(-1)[first:first + m * stride].view(m, stride)[:, :n]
+            assert torch.equal(product(x, w, None, t, out=out), y)
+            wide.view(-1)[first:first + m * stride].view(m, stride)[:, :n] = 9.0
+            assert (wide == 9).all()
 
 
 def test_a_row_depends_on_itself_alone():
@@ -294,6 +329,18 @@ def test_values_of_any_size():
         w = rows_of(200, 512, torch.float32, 9, 0.5) * 2.0 ** -power
         for form in FORMATS:
             check_product(x, w, form, torch.float32, y=Fp4Linear(w, None, form)(x))
+
+
+def test_the_smallest_scales():
+    """Values around 2^-126: mxfp4's least scale is 2^-127 (a byte of 0), nvfp4's rows are held by their row scale."""
+    x = torch.tensor([1.5 * 2.0 ** -126, -2.0 ** -126, 2.0 ** -125, 0.0] * 64, device="cuda").repeat(20, 1)
+    w = rows_of(130, 256, torch.float32, 9, 0.5) * 2.0 ** 100
+    for form in FORMATS:
+        y = Fp4Linear(w, None, form)(x)
+        # 256 products and their sum lie near 2^-24: compared at 1
+        a, b = (torch.from_numpy(kept(t.double().cpu().numpy(), form)[3]).cuda() for t in (x, w))
+        want, room = a @ b.T, a.abs() @ b.abs().T
+        assert ((y.double() - want).abs() <= room * (4 * 2.0 ** -23 + 50 * 2.0 ** -24)).all()
 
 
 def test_leading_dimensions_and_empty_batches():
