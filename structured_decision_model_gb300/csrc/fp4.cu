@@ -29,16 +29,39 @@ __device__ __forceinline__ float lanes_max(float v) {
     return v;
 }
 
-// The largest of a row that W warps share (a half of a warp has W = 1).
+// The 2^shift warps that share a row, and which row of the block and which of its warps this one is.
+struct Share {
+    int shift, slot, part;
+    __device__ __forceinline__ bool alone() const { return shift == 0; }
+};
+
+// Barriers of warps that share a row, so that the block's other rows go their own way; row_any: whether `p` holds
+// in one of their threads.
+__device__ __forceinline__ void row_sync(const Share& w) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + w.slot), "r"(32 << w.shift) : "memory");
+}
+__device__ __forceinline__ bool row_any(bool p, const Share& w) {
+    int any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(int(p)), "r"(1 + w.slot), "r"(32 << w.shift)
+        : "memory");
+    return any != 0;
+}
+
+// The largest of a row (a half of a warp is alone).
 template <int LANES>
-__device__ __forceinline__ float row_max(float v, float* red, int W, int warp) {
+__device__ __forceinline__ float row_max(float v, float* red, const Share& w) {
     v = lanes_max<LANES>(v);
-    if (LANES < 32 || W == 1) return v;
-    __syncthreads();  // red may still be read from the last call
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    const int w0 = warp / W * W;
-    for (int i = 0; i < W; ++i) v = fmaxf(v, red[w0 + i]);
+    if (LANES < 32 || w.alone()) return v;
+    float* mine = red + (w.slot << w.shift);
+    if ((threadIdx.x & 31) == 0) mine[w.part] = v;
+    row_sync(w);
+    for (int i = 0; i < 1 << w.shift; ++i) v = fmaxf(v, mine[i]);
     return v;
 }
 
@@ -49,13 +72,12 @@ template <int LANES>
 struct RowSum {
     float (*all)[32];  // the row's pieces
     float own = 0.f;
-    __device__ __forceinline__ void add(float v, int W, int piece, int lane) {
-        if (LANES < 32 || W == 1) own += v;
+    __device__ __forceinline__ void add(float v, const Share& w, int piece, int lane) {
+        if (LANES < 32 || w.alone()) own += v;
         else all[piece][lane] = v;
     }
-    __device__ __forceinline__ float get(int W, int pieces, int lane) {
-        if (LANES == 32 && W > 1) {
-            __syncthreads();
+    __device__ __forceinline__ float get(const Share& w, int pieces, int lane) {
+        if (LANES == 32 && !w.alone()) {  // behind a barrier
             own = 0.f;
             for (int i = 0; i < pieces; ++i) own += all[i][lane];
         }
@@ -63,33 +85,34 @@ struct RowSum {
     }
 };
 
-// STEPS: 512-value pieces of a row that a warp keeps, 16 values a lane; W warps a row (a power of
-// two), so a row has at most 512 * STEPS * W values.  LANES 16: rows of up to 256 values, two a warp.
+// STEPS: 512-value pieces of a row that a warp keeps, 16 values a lane; W = 2^shift warps a row, so that a row has at
+// most 512 * STEPS * W values.  LANES 16: rows of up to 256 values, two a warp.
 // EXTRA: statistics or sums are asked for.  64 registers a thread, for 32 warps an SM: with 8 pieces a warp and half
 // the warps 131072 x 4096 bf16 took 301 us instead of 252.
 template <int FMT, int DT, bool VEC, int STEPS, int LANES, bool EXTRA>
 __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 4)
-    fp4_quantize_kernel(const Fp4QuantizeArgs a, int W) {
+    fp4_quantize_kernel(const Fp4QuantizeArgs a, int shift) {
     constexpr bool NV = FMT == CLEF_NVFP4;
-    __shared__ float red[kThreads / 32];
+    __shared__ float red[kThreads / 32], means[kThreads / 32];
     __shared__ float partial[EXTRA ? 3 : 1][EXTRA ? kThreads / 32 * STEPS : 1][32];
     __shared__ __align__(16) uint32_t stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 32 * Raw<DT>::kWords];
     griddep_wait();
     griddep_launch();  // behind the wait: whoever starts early may take what came before us as done
     static_assert(LANES == 32 || STEPS == 1, "a half of a warp keeps one tile of a row");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x % LANES;
-    const int64_t row = LANES == 32 ? int64_t(blockIdx.x) * (kThreads / 32 / W) + warp / W
-                                    : int64_t(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
-    const bool mine = row < a.rows;  // threads behind the last row still meet the barriers and shuffles
-    const int part = LANES == 32 ? warp % W : 0;
+    const Share w{shift, LANES == 32 ? warp >> shift : 0, LANES == 32 ? warp & ((1 << shift) - 1) : 0};
+    const uint32_t row = LANES == 32 ? blockIdx.x * uint32_t(kThreads / 32 >> shift) + uint32_t(w.slot)
+                                     : blockIdx.x * uint32_t(kThreads / LANES) + threadIdx.x / LANES;
+    const bool mine = row < uint32_t(a.rows);  // threads behind the last row still meet their row's barriers and shuffles
+    const int part = w.part;
     const int padded = mine ? (a.cols + kFp4Tile - 1) / kFp4Tile * kFp4Tile : 0;  // columns that have scales
     const bool stats = EXTRA && a.mean, sums = EXTRA && a.sums;  // the same for every thread
-    const int64_t row0 = row * a.row_stride;
+    const int64_t row0 = int64_t(row) * a.row_stride;
 
     Raw<DT> raw[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-        const int col0 = (i * W + part) * 512;
+        const int col0 = ((i << shift) + part) * 512;
         uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
         if (LANES < 32 || col0 < padded)
             raw[i] = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
@@ -106,34 +129,34 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
     }
     RowScale rs{1.f, 1.f, false};
     if constexpr (NV) {
-        rs = row_scale_of(row_max<LANES>(row_top, red, W, warp));
+        rs = row_scale_of(row_max<LANES>(row_top, red, w));
         if (mine && part == 0 && lane == 0) a.row_scale[row] = rs.r;
     }
-    const int64_t code_stride = int64_t(a.cols + 31) / 32 * 16;
-    uint8_t* codes = a.codes + row * code_stride;
-    uint8_t* scales = a.scales + (row / kFp4RowGroup * (padded >> (NV ? 6 : 7))) * kFp4ScaleGroup +
-                      (row % 32) * 16 + (row % kFp4RowGroup) / 32 * 4;
-    const int first = EXTRA ? warp / W * W * STEPS : 0;  // of the row's pieces among the block's
+    const uint32_t code_stride = uint32_t(a.cols + 31) / 32 * 16;
+    uint8_t* codes = a.codes + uint64_t(row) * code_stride;
+    uint8_t* scales = a.scales + uint64_t(row / kFp4RowGroup) * uint32_t(padded >> (NV ? 6 : 7)) * kFp4ScaleGroup +
+                      (row % 32) * 16 + row % kFp4RowGroup / 32 * 4;
+    const int first = EXTRA ? (w.slot << shift) * STEPS : 0;  // of the row's pieces among the block's
     RowSum<LANES> sum{partial[0] + first}, squares{partial[EXTRA ? 1 : 0] + first}, total{partial[EXTRA ? 2 : 0] + first};
     const int pieces = (a.cols + 511) / 512;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-        if (LANES == 32 && (i * W + part) * 512 >= padded) continue;  // the same for a whole warp
-        const int col = (i * W + part) * 512 + lane * 16;
+        if (LANES == 32 && ((i << shift) + part) * 512 >= padded) continue;  // the same for a whole warp
+        const int col = ((i << shift) + part) * 512 + lane * 16;
         const int left = a.cols - col;  // values from the lane's first to the row's end
         uint64_t x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = raw[i].two(j);
         if (stats) {
             const float2 m = moments16(x);
-            sum.add(m.x, W, i * W + part, lane);
-            squares.add(m.y, W, i * W + part, lane);
+            sum.add(m.x, w, (i << shift) + part, lane);
+            squares.add(m.y, w, (i << shift) + part, lane);
         }
         const Coded c = encode16<FMT, DT>(x, top[i], rs.inv, rs.tiny, left);
-        if (mine && col < 2 * code_stride) *reinterpret_cast<uint2*>(codes + col / 2) = c.codes;
+        if (mine && col < int(2 * code_stride)) *reinterpret_cast<uint2*>(codes + col / 2) = c.codes;
         uint32_t word;
         if (scale_word<FMT>(c.byte, lane, &word) && col < padded)
-            *reinterpret_cast<uint32_t*>(scales + int64_t(col >> (NV ? 6 : 7)) * kFp4ScaleGroup) = word;
+            *reinterpret_cast<uint32_t*>(scales + uint32_t(col >> (NV ? 6 : 7)) * kFp4ScaleGroup) = word;
         if (sums) {
             uint32_t h[8];
             unpack_e2m1(c.codes.x, h);
@@ -144,36 +167,47 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
                 t += f.x + f.y;
             }
-            total.add(t * c.scale, W, i * W + part, lane);
+            total.add(t * c.scale, w, (i << shift) + part, lane);
         }
     }
     if (stats) {
-        const float mean = sum.get(W, pieces, lane) / float(a.cols);
-        float var = squares.get(W, pieces, lane) / float(a.cols) - mean * mean;
+        // The row's first warp adds up; the others wait for what it finds only where that is far from zero.
+        if (LANES == 32 && !w.alone()) row_sync(w);
+        float mean = 0.f, var = 0.f;
+        if (part == 0) {
+            mean = sum.get(w, pieces, lane) * a.inv_cols;
+            var = squares.get(w, pieces, lane) * a.inv_cols - mean * mean;
+            if (lane == 0 && LANES == 32) means[warp] = mean;
+        }
         // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows (and those
         // whose squares pass fp32) are read once more and sum the squares of what is left behind the mean.
-        const bool far = mine && !(mean * mean <= var);
-        if (LANES < 32 || W == 1 ? __any_sync(0xffffffffu, far) : __syncthreads_or(far)) {
-            RowSum<LANES> apart{sum.all};  // every thread is past the sums' barriers, and has read them
+        const bool far = mine && part == 0 && !(mean * mean <= var);
+        if (LANES < 32 || w.alone() ? __any_sync(0xffffffffu, far) : row_any(far, w)) {
+            if (LANES == 32) mean = means[w.slot << shift];
+            RowSum<LANES> apart{sum.all};  // the sums have been read
 #pragma unroll 1
             for (int i = 0; i < STEPS; ++i) {
-                if (LANES == 32 && (i * W + part) * 512 >= padded) continue;
-                const int col0 = (i * W + part) * 512;
+                if (LANES == 32 && ((i << shift) + part) * 512 >= padded) continue;
+                const int col0 = ((i << shift) + part) * 512;
                 uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
                 const Raw<DT> again = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
                 const float q = squares_apart<DT>(again, mean, a.cols - (col0 + lane * 16));
-                apart.add(q, W, i * W + part, lane);
+                apart.add(q, w, (i << shift) + part, lane);
             }
-            const float v = apart.get(W, pieces, lane) / float(a.cols);
-            if (far) var = v;
+            if (LANES == 32 && !w.alone()) row_sync(w);
+            if (part == 0) {
+                const float v = apart.get(w, pieces, lane) * a.inv_cols;
+                if (far) var = v;
+            }
         }
         if (mine && part == 0 && lane == 0) {
             a.mean[row] = mean;
-            a.rstd[row] = 1.f / sqrtf(var + 1e-5f);
+            a.rstd[row] = rsqrtf(var + 1e-5f);
         }
     }
     if (sums) {
-        const float all = total.get(W, pieces, lane);
+        if (LANES == 32 && !w.alone()) row_sync(w);
+        const float all = part == 0 ? total.get(w, pieces, lane) : 0.f;
         if (mine && part == 0 && lane == 0) a.sums[row] = all * rs.r;
     }
 }
@@ -295,16 +329,16 @@ cudaError_t quantize_rows(const Fp4QuantizeArgs& a, cudaStream_t s) {
     const int pieces = (a.cols + 511) / 512;
     constexpr int kMost = DT == CLEF_FP32 ? 2 : 4;
     const int64_t warps = int64_t(num_sms()) * 16;
-    int W = 1;
-    while (W < 8 && W < pieces && (pieces > kMost * W || int64_t(a.rows) * W < warps)) W *= 2;
+    int W = 1, shift = 0;
+    for (; W < 8 && W < pieces && (pieces > kMost * W || int64_t(a.rows) * W < warps); ++shift) W *= 2;
     if (a.cols <= 256)
         return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 16, EXTRA>, dim3(unsigned((int64_t(a.rows) + 15) / 16)),
-                          dim3(kThreads), 0, s, a, 1);
+                          dim3(kThreads), 0, s, a, 0);
     const int steps = (pieces + W - 1) / W;
     const dim3 grid(unsigned((int64_t(a.rows) * W + kThreads / 32 - 1) / (kThreads / 32)));
-    if (steps <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, W);
-    if (steps <= 2) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 2, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, W);
-    if (steps <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, W);
+    if (steps <= 1) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 1, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, shift);
+    if (steps <= 2) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 2, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, shift);
+    if (steps <= 4) return launch_pdl(fp4_quantize_kernel<FMT, DT, VEC, 4, 32, EXTRA>, grid, dim3(kThreads), 0, s, a, shift);
     return cudaErrorInvalidValue;
 }
 

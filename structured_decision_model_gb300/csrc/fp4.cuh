@@ -270,14 +270,14 @@ __device__ __forceinline__ RowScale row_scale_of(float row_top) {
 
 // Sums of a lane's values and of their squares (what lies behind the row's end is 0).
 __device__ __forceinline__ float2 moments16(const uint64_t (&x)[8]) {
-    uint64_t t = x[0], u = mul2(x[0], x[0]);
+    float t = 0.f, u = 0.f;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) {
-        t = add2(t, x[j]);
-        u = fma2(x[j], x[j], u);
+    for (int j = 0; j < 8; ++j) {
+        const float2 f = both_of(x[j]);
+        t += f.x + f.y;
+        u = fmaf(f.y, f.y, fmaf(f.x, f.x, u));
     }
-    const float2 t2 = both_of(t), u2 = both_of(u);
-    return make_float2(t2.x + t2.y, u2.x + u2.y);
+    return make_float2(t, u);
 }
 
 // The sum of the squares of a lane's values less the mean; `left` as in encode16.

@@ -29,6 +29,7 @@ struct Fp4QuantizeArgs {
     float* rstd;         // with mean
     float* sums;         // optional
     int rows, cols;
+    float inv_cols;      // 1 / cols
 };
 cudaError_t launch_fp4_quantize(const Fp4QuantizeArgs& a, int format, int dtype, cudaStream_t s);
 
@@ -62,6 +63,7 @@ struct Fp4ProductArgs {
     float* mean_out;
     float* rstd_out;
     int cols;
+    float inv_cols;
     int w_settled;         // no kernel that may still run on the stream writes w: it may be read ahead of them
     int bulk;              // 16-bit outputs: rows start and end on 16 bytes, so that TMA can store them
 };

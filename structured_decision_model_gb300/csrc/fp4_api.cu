@@ -104,6 +104,7 @@ Fp4ProductArgs product_args(const clef_fp4& x, const clef_fp4& w, const float* b
     a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && w.rows % 8 == 0 && !misaligned(out, 16);
     a.w_settled = w_settled;
     a.cols = x.cols;
+    a.inv_cols = 1.f / float(x.cols);
     return a;
 }
 
@@ -155,7 +156,7 @@ int clef_fp4_quantize(const clef_fp4* q, int32_t dtype, const void* x, int64_t r
             if (out[i].meets(out[j])) return CLEF_ERR_INVALID_ARGUMENT;
     }
     const Fp4QuantizeArgs a{x, row_stride, static_cast<uint8_t*>(q->codes), static_cast<uint8_t*>(q->scales),
-                            q->row_scale, mean, rstd, sums, q->rows, q->cols};
+                            q->row_scale, mean, rstd, sums, q->rows, q->cols, 1.f / float(q->cols)};
     return status(launch_fp4_quantize(a, q->format, dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -228,7 +229,7 @@ int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x
         return status(launch_fp4_few(*w, p, x_dtype, dtype, s));
     }
     const Fp4QuantizeArgs a{x, x_stride, static_cast<uint8_t*>(q.codes), static_cast<uint8_t*>(q.scales), q.row_scale,
-                            mean, rstd, nullptr, rows, w->cols};
+                            mean, rstd, nullptr, rows, w->cols, 1.f / float(w->cols)};
     const int quantised = status(launch_fp4_quantize(a, w->format, x_dtype, s));
     return quantised == CLEF_OK ? status(launch_fp4_product(q, *w, p, dtype, s)) : quantised;
 }
