@@ -75,7 +75,8 @@ CLEF_API int clef_fp4_dequantize(const clef_fp4* q, int32_t dtype, void* out, in
  * (bf16, fp16 or fp32).  x and w: of one format and one number of columns; bias: [w.rows]
  * fp32 or NULL.  With mean, rstd (of x's rows) and sums (of w's rows) all given, x's rows
  * are taken less their means and times their rstd: rstd[m] (x w^T - mean[m] sums[n]) + bias[n],
- * the layer behind a LayerNorm whose weight w holds already.  out's rows are
+ * the layer behind a LayerNorm whose weight w holds already.  Sums meet w's row scale first and x's (and rstd)
+ * then, in fp32: rows of w above about 2^90 pass its range on the way, whatever x is.  out's rows are
  * `row_stride` elements apart (at least w.rows) and out lies apart from all inputs. */
 CLEF_API int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, const float* mean,
                               const float* rstd, const float* sums, int32_t dtype, void* out, int64_t row_stride,

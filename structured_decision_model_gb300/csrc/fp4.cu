@@ -3,9 +3,10 @@
 // Quantise.  A row belongs to a half, one or more warps and stays in their registers: its largest
 // sizes, its mean and variance and its codes come from one read of memory.  A lane holds 16
 // consecutive values of every 512: a block of 16 is one lane's and one of 32 two neighbours', so
-// that a scale is worked out once or twice, and arithmetic runs on pairs (fma.rn.f32x2).  What bounds it
-// are issue slots and memory alike.  131072 x 4096 bf16 takes 224 us to nvfp4 (6.1 TB/s), 306 with statistics, 195 to
-// mxfp4 (7.0 TB/s, the rate of a plain copy); with eight values a lane it took 409, 470 and 324.
+// that a scale is worked out once or twice, and the codes' arithmetic runs on pairs (fma.rn.f32x2).
+// Memory bounds it, and with statistics issue slots: 131072 x 4096 bf16 takes 208 us to nvfp4 (6.6 TB/s),
+// 189 to mxfp4 (7.2 TB/s; a plain copy 6.8), 294 with statistics.  Eight values a lane took 409, 324
+// and 470; rows of a block tied together by block-wide barriers, and indexes by division, 224, 195 and 306.
 #include "fp4.cuh"
 #include "kernels.h"
 

@@ -70,6 +70,7 @@ class ClefHead:
         B.clef_prepare_weights(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), nbytes, stream_handle())
         self._ws = None
         self.memory_weights = None
+        self._rows_scratch = {}  # scratch bytes of the chunk lengths met
         if memory_format is not None:
             w = Fp4Matrix(2 * n_route * D, H, memory_format, device)
             w.sums = torch.empty(w.rows, dtype=torch.float32, device=w.device)
@@ -127,7 +128,11 @@ class ClefHead:
         ws = self._ws
         if self.memory_weights is not None:
             w = self.memory_weights
-            n = B.clef_stream_rows_fp4_scratch(self.cfg, w.struct.format, n_rows)
+            n = self._rows_scratch.get(n_rows)
+            if n is None:
+                n = B.clef_stream_rows_fp4_scratch(self.cfg, w.struct.format, n_rows)
+                if len(self._rows_scratch) < 4096:
+                    self._rows_scratch[n_rows] = n
             space = self._scratch(n, stream)
             B.clef_stream_rows_fp4(self.cfg, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), schema, hidden.data_ptr(),
                                    B.FP16 if hidden.dtype == torch.float16 else B.BF16, record, row0, n_rows, ws.data_ptr(),

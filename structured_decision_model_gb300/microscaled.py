@@ -181,7 +181,7 @@ class Fp4Linear:
     """A linear layer of 4-bit weights: its inputs are quantised row by row as they come.
 
     ``weight`` [outs, cols] (bf16, fp16 or fp32; or an ``Fp4Matrix``, quantised with ``sums`` where
-    ``normalized`` is to be called) and ``bias`` [outs] are laid out once.  For ``normalized`` the weight
+    ``normalized`` is to be called) and ``bias`` [outs] (kept as it is where it is contiguous fp32) are laid out once.  For ``normalized`` the weight
     holds the LayerNorm's weight (its columns times it) and the bias what the LayerNorm's bias brings."""
 
     def __init__(self, weight, bias: Optional[torch.Tensor] = None, format: str = "nvfp4"):
