@@ -44,7 +44,6 @@ extern "C" {
 typedef enum clef_fp4_format { CLEF_MXFP4 = 0, CLEF_NVFP4 = 1 } clef_fp4_format;
 
 #define CLEF_FP4_MAX_COLS 16384
-#define CLEF_FP4_FEW_ROWS 8
 
 /* A matrix of rows kept in 4 bits.  codes and scales: 256-byte aligned device memory of the
  * sizes that clef_fp4_size gives; row_scale: [rows] fp32, NULL for CLEF_MXFP4.
@@ -76,21 +75,24 @@ CLEF_API int clef_fp4_dequantize(const clef_fp4* q, int32_t dtype, void* out, in
  * fp32 or NULL.  With mean, rstd (of x's rows) and sums (of w's rows) all given, x's rows
  * are taken less their means and times their rstd: rstd[m] (x w^T - mean[m] sums[n]) + bias[n],
  * the layer behind a LayerNorm whose weight w holds already.  Sums meet w's row scale first and x's (and rstd)
- * then, in fp32: rows of w above about 2^90 pass its range on the way, whatever x is.  out's rows are
+ * then, in fp32: rows of w above about 2^90 pass its range on the way, whatever x is.  (Kept rows
+ * are raw ones: a row whose mean is large against its spread spends its codes on the mean.)  out's rows are
  * `row_stride` elements apart (at least w.rows) and out lies apart from all inputs. */
 CLEF_API int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, const float* mean,
                               const float* rstd, const float* sums, int32_t dtype, void* out, int64_t row_stride,
                               int32_t* flags, void* stream);
 
-/* Bytes of scratch that clef_fp4_linear needs for `rows` rows of `cols` values. */
-CLEF_API int clef_fp4_linear_scratch(int32_t format, int32_t rows, int32_t cols, size_t* bytes);
+/* Bytes of scratch that clef_fp4_linear needs for `rows` rows of `cols` values of type x_dtype, with sums
+ * (normalized) or without, whose rows all start on 16 bytes and have a multiple of 8 values (aligned; one row: x
+ * does) or not.  0: few aligned rows are quantised inside the product, in one launch; its scratch may be NULL.
+ * Without `aligned` the size does for any call of so many rows. */
+CLEF_API int clef_fp4_linear_scratch(int32_t format, int32_t x_dtype, int32_t rows, int32_t cols, int32_t normalized,
+                                     int32_t aligned, size_t* bytes);
 
 /* A layer with 4-bit weights: clef_fp4_quantize of the `rows` rows x in w's format, then clef_fp4_product with
  * w, the same numbers by one call.  With `sums` (of w's rows) the rows are normalized as there, and their
  * mean and rstd ([rows] fp32, both needed then) come back too; without, all three are NULL.
- * scratch: 256-byte aligned device memory of the call's own until it has run.  Up to CLEF_FP4_FEW_ROWS rows whose
- * values number a multiple of 8 and whose rows start on 16 bytes (one row: x does) are quantised inside the
- * product, in one launch: scratch is not used then and may be NULL. */
+ * scratch: 256-byte aligned device memory of the call's own until it has run. */
 CLEF_API int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
                              const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride,
                              float* mean, float* rstd, void* scratch, size_t scratch_bytes, int32_t* flags,

@@ -32,7 +32,6 @@ BF16, FP16, FP32 = 0, 1, 2   # clef_dtype
 CACHE_MAX_REQUESTS = 1024
 MXFP4, NVFP4 = 0, 1          # clef_fp4_format
 FP4_MAX_COLS = 16384
-FP4_FEW_ROWS = 8
 
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
@@ -125,7 +124,7 @@ def load():
     lib.clef_fp4_quantize.argtypes = [fp4, _i32, _vp, _i64, _vp, _vp, _vp, _vp]
     lib.clef_fp4_dequantize.argtypes = [fp4, _i32, _vp, _i64, _vp]
     lib.clef_fp4_product.argtypes = [fp4, fp4, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
-    lib.clef_fp4_linear_scratch.argtypes = [_i32, _i32, _i32, ctypes.POINTER(_sz)]
+    lib.clef_fp4_linear_scratch.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]
     lib.clef_fp4_linear.argtypes = [fp4, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _vp]
     cfg, schema = ctypes.POINTER(ClefConfig), ctypes.POINTER(ClefSchema)
     lib.clef_fp4_memory_weights.argtypes = [cfg, _vp, fp4, _vp, _vp]
@@ -374,9 +373,10 @@ def clef_fp4_product(x: ClefFp4, w: ClefFp4, bias_ptr, mean_ptr, rstd_ptr, sums_
                                    stream), "clef_fp4_product")
 
 
-def clef_fp4_linear_scratch(format, rows, cols):
+def clef_fp4_linear_scratch(format, x_dtype, rows, cols, normalized=0, aligned=0):
     out = _sz(0)
-    _check(load().clef_fp4_linear_scratch(format, rows, cols, ctypes.byref(out)), "clef_fp4_linear_scratch")
+    _check(load().clef_fp4_linear_scratch(format, x_dtype, rows, cols, normalized, aligned, ctypes.byref(out)),
+           "clef_fp4_linear_scratch")
     return out.value
 
 

@@ -21,10 +21,14 @@ cudaError_t launch_few_of(const clef_fp4& w, const Fp4ProductArgs& a, int x_dtyp
 
 }  // namespace
 
-bool fp4_few_rows(int rows, int cols, int x_dtype, const void* x, int64_t x_stride) {
-    const int64_t size = x_dtype == CLEF_FP32 ? 4 : 2;
-    return rows <= kFewRows && cols % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
-           (rows == 1 || x_stride * size % 16 == 0);
+// Every CTA reads its K range of the rows itself and, for row scales or statistics, all of them, a row a warp at a time.
+// GPU time against the two launches' (graph, bf16; a call by itself is 5 us shorter in one launch):
+//   4096 x 4096 mxfp4: 1 row 4.7, 5.4 us; 8: 5.2, 5.9; 16: 5.9, 6.3; 32: 7.6, 6.9     16384 columns, 8 rows: 9.6, 9.8; 16: 11.6, 10.1
+//   4096 x 4096 nvfp4: 1 row 6.6, 5.8 us; 8: 7.2, 5.9; 16: 9.3, 6.2                   16384 columns, 1 row: 13.2, 10.3
+bool fp4_few_rows(int format, int x_dtype, int rows, int cols, bool normalized) {
+    const int64_t bytes = int64_t(cols) * (x_dtype == CLEF_FP32 ? 4 : 2);
+    if (format == CLEF_NVFP4 || normalized) return rows <= 8 && bytes <= 12288;
+    return (rows <= 8 && bytes <= 32768) || (rows <= kFp4FewRows && bytes <= 8192);
 }
 
 cudaError_t launch_fp4_few(const clef_fp4& w, const Fp4ProductArgs& a, int x_dtype, int dtype, cudaStream_t s) {

@@ -115,8 +115,7 @@ constexpr int kEpilogue = 256;               // threads of the epilogue: two war
 constexpr int kThreads = 64 + kEpilogue;     // and one warp each for TMA and MMA
 
 constexpr int kKept = -1;
-constexpr int kFewRows = CLEF_FP4_FEW_ROWS;
-static_assert(kFewRows == kEpilogue / 32, "a row for each epilogue warp");
+static_assert(kFp4FewRows <= 32, "few rows are one tile");
 
 // Two 16-bit values in one word, the first in its low half.
 template <int OUT>
@@ -309,55 +308,61 @@ __device__ __forceinline__ void join_parts(const Fp4ProductArgs& args, uint32_t 
     }
 }
 
-// Row `m` of few rows of x by one warp: its scale and statistics from all of it, then its codes and scales of
-// K tiles kt0 .. kt1 - 1 into the operand stages, as TMA would have laid them.  Returns the row's
-// terms.  The numbers are those of the kernel that quantises many rows, in the same order.
+// Few rows of x by the epilogue's warps, rows warp, warp + 8, ... each: a row's scale and statistics from all of
+// it (its terms go to `terms`, its largest size to `tops`), then the rows' codes and scales of K tiles
+// kt0 .. kt1 - 1 into the operand stages, as TMA would have laid them.  The numbers are those of the
+// kernel that quantises many rows, in the same order.
 template <int FMT, int DT, typename C>
-__device__ __forceinline__ float2 few_row(const Fp4ProductArgs& args, uint8_t* smem, uint64_t* full, uint64_t* empty,
-                                          int kt0, int kt1, int m, int lane, volatile int* abort_flag) {
+__device__ __forceinline__ void few_rows(const Fp4ProductArgs& args, uint8_t* smem, float* terms, float* tops,
+                                         uint64_t* full, uint64_t* empty, int kt0, int kt1, int warp, int lane,
+                                         volatile int* abort_flag) {
     constexpr bool NV = FMT == CLEF_NVFP4;
-    const bool mine = m < args.M;
-    const int64_t row0 = int64_t(m) * args.x_stride;
-    const int cols = mine ? args.cols : 0;
-    float2 f = make_float2(1.f, 0.f);
-    RowScale rs{1.f, 1.f, false};
-    if (mine && (NV || args.mean_out)) {
-        float row_top = 0.f, sum = 0.f, squares = 0.f;
+    const int cols = args.cols;
+#pragma unroll 1
+    for (int m = warp; m < args.M; m += kEpilogue / 32) {
+        const int64_t row0 = int64_t(m) * args.x_stride;
+        float2 f = make_float2(1.f, 0.f);
+        if (NV || args.mean_out) {
+            float row_top = 0.f, sum = 0.f, squares = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < cols; c += 512) {
-            const Raw<DT> raw = load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr);
-            if (NV) row_top = fmaxf(row_top, finite_top<DT>(raw, __uint_as_float(raw.top())));
-            if (args.mean_out) {
-                uint64_t x[8];
+            for (int c = 0; c < cols; c += 512) {
+                const Raw<DT> raw = load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr);
+                if (NV) row_top = fmaxf(row_top, finite_top<DT>(raw, __uint_as_float(raw.top())));
+                if (args.mean_out) {
+                    uint64_t x[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = raw.two(j);
-                const float2 v = moments16(x);
-                sum += v.x;
-                squares += v.y;
+                    for (int j = 0; j < 8; ++j) x[j] = raw.two(j);
+                    const float2 v = moments16(x);
+                    sum += v.x;
+                    squares += v.y;
+                }
+            }
+            if (NV) {
+                row_top = warp_max(row_top);
+                f.x = row_scale_of(row_top).r;
+                if (lane == 0) tops[m] = row_top;
+            }
+            if (args.mean_out) {
+                const float mean = warp_sum(sum) * args.inv_cols;
+                float var = warp_sum(squares) * args.inv_cols - mean * mean;
+                if (!(mean * mean <= var)) {  // see the kernel for many rows
+                    float q = 0.f;
+                    for (int c = 0; c < cols; c += 512)
+                        q += squares_apart<DT>(load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr), mean, cols - (c + lane * 16));
+                    var = warp_sum(q) * args.inv_cols;
+                }
+                const float rstd = rsqrtf(var + 1e-5f);
+                f.x *= rstd;
+                f.y = -mean * rstd;
+                if (blockIdx.x == 0 && lane == 0) {
+                    args.mean_out[m] = mean;
+                    args.rstd_out[m] = rstd;
+                }
             }
         }
-        if (NV) {
-            rs = row_scale_of(warp_max(row_top));
-            f.x = rs.r;
-        }
-        if (args.mean_out) {
-            const float mean = warp_sum(sum) * args.inv_cols;
-            float var = warp_sum(squares) * args.inv_cols - mean * mean;
-            if (!(mean * mean <= var)) {  // see the kernel for many rows
-                float q = 0.f;
-                for (int c = 0; c < cols; c += 512)
-                    q += squares_apart<DT>(load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr), mean, cols - (c + lane * 16));
-                var = warp_sum(q) * args.inv_cols;
-            }
-            const float rstd = rsqrtf(var + 1e-5f);
-            f.x *= rstd;
-            f.y = -mean * rstd;
-            if (blockIdx.x == 0 && lane == 0) {
-                args.mean_out[m] = mean;
-                args.rstd_out[m] = rstd;
-            }
-        }
+        if (lane == 0) put_row_terms(terms, m, f);
     }
+    __syncwarp();  // tops
     // two K tiles at a time, 16 values a lane
     int s = 0;
     uint32_t phase = 1;
@@ -368,8 +373,18 @@ __device__ __forceinline__ float2 few_row(const Fp4ProductArgs& args, uint8_t* s
         bool ok = mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags);
         if (tiles == 2) ok = mbar_wait_bounded(&empty[s1], phase1, abort_flag, args.flags) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
-        if (mine) {
-            const Raw<DT> raw = load16<DT, true, 32>(args.x, row0, kt * kFp4Tile, min(cols, (kt + tiles) * kFp4Tile), lane, nullptr);
+        uint8_t* st = smem + (which ? s1 : s) * C::STAGE + kWBytes;
+        const int v = (lane & 15) * 16;  // the first value's place in its K tile
+        auto load = [&](int m) {         // (a row behind the last reads as zeros)
+            return load16<DT, true, 32>(args.x, int64_t(m) * args.x_stride, kt * kFp4Tile,
+                                        m < args.M ? min(cols, (kt + tiles) * kFp4Tile) : 0, lane, nullptr);
+        };
+        Raw<DT> next = load(warp);
+#pragma unroll 1
+        for (int m = warp; m < args.M; m += kEpilogue / 32) {
+            const Raw<DT> raw = next;
+            next = load(m + kEpilogue / 32);  // while this one is worked on
+            const RowScale rs = NV ? row_scale_of(tops[m]) : RowScale{1.f, 1.f, false};
             uint32_t t = raw.top();
             if (!NV) t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
             uint64_t x[8];
@@ -379,15 +394,13 @@ __device__ __forceinline__ float2 few_row(const Fp4ProductArgs& args, uint8_t* s
             uint32_t word;
             const bool writes = scale_word<FMT>(c.byte, lane, &word);
             if (which < tiles) {
-                uint8_t* st = smem + (which ? s1 : s) * C::STAGE + kWBytes;
-                const int v = (lane & 15) * 16;  // the first value's place in its K tile
                 // 16-byte pieces of a row's 128 bytes, swizzled by the row
                 *reinterpret_cast<uint2*>(st + m * kAtomBytes + (((v >> 5) ^ (m & 7)) << 4) + (v >> 4 & 1) * 8) = c.codes;
                 if (writes)
                     *reinterpret_cast<uint32_t*>(st + C::X_BYTES + C::S_BYTES + (v >> (NV ? 6 : 7)) * kFp4ScaleGroup + m * 16) = word;
             }
-            fence_proxy_async_smem();
         }
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&full[s]);
@@ -396,12 +409,11 @@ __device__ __forceinline__ float2 few_row(const Fp4ProductArgs& args, uint8_t* s
         s = tiles == 2 ? (s1 + 1 == C::STAGES ? 0 : s1 + 1) : s1;
         phase = s1 == 0 || (tiles == 2 && s == 0) ? phase ^ 1u : phase;
     }
-    return f;
 }
 
 // XT: x's type.  kKept: x is a 4-bit matrix that TMA loads.  Otherwise rows as they come (at most
-// kFewRows, 16-byte pieces): the epilogue's warps, idle until the products are done, quantise them, a
-// warp a row, straight into the operand stages.  One token then takes one launch and no scratch.
+// kFp4FewRows, 16-byte pieces): the epilogue's warps, idle until the products are done, quantise them
+// straight into the operand stages.  Such a call takes one launch and no scratch.
 template <int FMT, int BN, int OUT, int XT>
 __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                 const __grid_constant__ CUtensorMap tmX,
@@ -410,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
                                                                 const Fp4ProductArgs args) {
     using C = TileCfg<FMT, BN>;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ float tops[XT == kKept ? 1 : kFp4FewRows];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* terms = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
     uint64_t* full = reinterpret_cast<uint64_t*>(terms + 2 * BN);
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full[s], XT == kKept ? 1 : 1 + kFewRows);  // the copies, and the warps that write x
+            mbar_init(&full[s], XT == kKept ? 1 : 1 + kEpilogue / 32);  // the copies, and the warps that write x
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
@@ -542,8 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
         if constexpr (XT == kKept) {
             if (t < BN) put_row_terms(terms, t, row_terms(args, xt * BN + t));
         } else {
-            const float2 f = few_row<FMT, XT, C>(args, smem, full, empty, kt0, kt1, warp - 2, lane, abort_flag);
-            if (lane == 0) put_row_terms(terms, warp - 2, f);
+            few_rows<FMT, XT, C>(args, smem, terms, tops, full, empty, kt0, kt1, warp - 2, lane, abort_flag);
         }
         bool ok = mbar_wait_bounded(done, 0, abort_flag, args.flags) && !*abort_flag;
         ok = epilogue_agrees(ok);  // the row terms are there too

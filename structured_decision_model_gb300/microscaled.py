@@ -200,8 +200,7 @@ class Fp4Linear:
         self._flags = weight.flags.data_ptr()  # made here, outside of any later capture
         self._device, self._index = weight.device, weight._index
         self._lib, self._struct = B.load(), weight.struct
-        self._ragged = self.cols % 8 != 0
-        self._scratch = {}  # scratch bytes of the numbers of rows that the layer has met
+        self._scratch = {}  # scratch bytes of the calls that the layer has met
 
     def _run(self, x, dtype, normalized):
         """Outputs, means and rstds of x's rows (the latter None where not ``normalized``)."""
@@ -231,16 +230,15 @@ class Fp4Linear:
             rstd = torch.empty(n, dtype=_FP32, device=self._device)
             mean_at, rstd_at, sums_at = mean.data_ptr(), rstd.data_ptr(), self.weight.sums.data_ptr()
         if n:
-            at, size, scratch = rows.data_ptr(), 0, None
+            at, scratch = rows.data_ptr(), None
             stride = stride if n > 1 else self.cols
-            # few rows that start on 16 bytes need no scratch; otherwise a buffer of the call's own: overlapping
-            # calls and captured graphs never share one
-            if n > B.FP4_FEW_ROWS or self._ragged or at & 15 or stride * x.element_size() & 15:
-                size = self._scratch.get(n)
-                if size is None:
-                    if len(self._scratch) >= 4096:
-                        self._scratch.clear()
-                    size = self._scratch[n] = B.clef_fp4_linear_scratch(self._struct.format, n, self.cols)
+            key = (n, x_type, normalized, (at | stride * x.element_size()) & 15 == 0)
+            size = self._scratch.get(key)
+            if size is None:
+                if len(self._scratch) >= 4096:
+                    self._scratch.clear()
+                size = self._scratch[key] = B.clef_fp4_linear_scratch(self._struct.format, x_type, n, self.cols, *key[2:])
+            if size:  # a buffer of the call's own: overlapping calls and captured graphs never share one
                 space = torch.empty(size, dtype=torch.uint8, device=self._device)
                 scratch = space.data_ptr()
             status = self._lib.clef_fp4_linear(

@@ -39,14 +39,15 @@ def test_sizes(rows, cols):
         assert codes == rows * (-(-cols // 32) * 16)
         assert scales == -(-rows // 128) * -(-cols // 256) * each
         up = lambda n: -(-n // 256) * 256
-        assert B.clef_fp4_linear_scratch(form, rows, cols) == up(codes) + up(scales) + (4 * rows if form else 0)
+        assert B.clef_fp4_linear_scratch(form, B.BF16, rows, cols) == up(codes) + up(scales) + (4 * rows if form else 0)
 
 
 @pytest.mark.parametrize("form,rows,cols", [(2, 1, 1), (-1, 1, 1), (0, 0, 1), (1, 1, 0), (1, 1, 16385), (0, 2 ** 31 - 256, 1),
                                             (1, 2 ** 31 - 300, 16384)])
 def test_unsupported_sizes(form, rows, cols):
     refused(3, B.clef_fp4_size, form, rows, cols)
-    refused(3, B.clef_fp4_linear_scratch, form, rows, cols)
+    refused(3, B.clef_fp4_linear_scratch, form, B.BF16, rows, cols)
+    refused(1, B.clef_fp4_linear_scratch, B.MXFP4, 3, 1, 1)
 
 
 def test_matrices_are_checked():
@@ -92,7 +93,7 @@ def test_product_refusals():
 
 def test_layer_refusals():
     w = matrix(at=4 * P, rows=20)
-    size = B.clef_fp4_linear_scratch(B.NVFP4, 10, 100)  # ragged rows: never without scratch
+    size = B.clef_fp4_linear_scratch(B.NVFP4, B.BF16, 10, 100)  # ragged rows: never without scratch
     good = [w, B.BF16, 8 * P, 100, 10, 12 * P, 15 * P, B.BF16, 9 * P, 20, 13 * P, 14 * P, 20 * P, size, 16 * P]
     for i, v in ((1, 5), (2, None), (3, -1), (5, 12 * P + 1), (6, None), (7, 9), (8, None), (9, 19), (10, None), (11, None),
                  (12, None), (12, 20 * P + 8), (14, None),
@@ -108,6 +109,15 @@ def test_layer_refusals():
     refused(1, B.clef_fp4_linear, *few)  # no flags
 
 
+def test_few_rows_need_no_scratch():
+    need = lambda *a: B.clef_fp4_linear_scratch(*a) > 0
+    for form in (B.MXFP4, B.NVFP4):
+        assert not need(form, B.BF16, 8, 4096, 0, 1) and not need(form, B.BF16, 8, 4096, 1, 1)
+        assert need(form, B.BF16, 8, 4096, 0, 0) and need(form, B.BF16, 1, 4092, 0, 1) and need(form, B.BF16, 17, 64, 0, 1)
+    assert need(B.NVFP4, B.FP32, 8, 4096, 0, 1) and not need(B.MXFP4, B.FP32, 8, 4096, 0, 1)
+    assert need(B.MXFP4, B.FP32, 8, 4096, 1, 1) and not need(B.MXFP4, B.FP16, 16, 4096, 0, 1)
+
+
 def test_head_refusals():
     cfg = B.make_config()
     spec = synth.BatchSpec(name="t", B=2, H=4096, vocab=1000, lengths=[256, 300], questions=(2, 2), options=(2, 3))
@@ -119,6 +129,11 @@ def test_head_refusals():
     refused(1, B.clef_fp4_memory_weights, cfg, None, w, P)
     refused(3, B.clef_fp4_memory_weights, B.make_config(H=100), P, w, P)
     assert B.clef_head_forward_fp4_scratch(cfg, B.NVFP4, schema) == B.clef_stream_rows_fp4_scratch(cfg, B.NVFP4, 300)
+    for lengths, rows in (([300, 300], 300), ([256, 256], 512)):  # one product where no padding lies between
+        even = synth.make_batch(synth.BatchSpec(name="t", B=2, H=4096, vocab=1000, lengths=lengths, questions=(2, 2),
+                                                options=(2, 3)), seed=2, with_hidden=False)
+        even = B.Schema(even.B, even.Lpad, even.H, even.lengths, even.q_rec, even.q_type, even.q_span, even.q_opt_off, even.o_span)
+        assert B.clef_head_forward_fp4_scratch(cfg, B.MXFP4, even) == B.clef_stream_rows_fp4_scratch(cfg, B.MXFP4, rows)
     refused(3, B.clef_stream_rows_fp4_scratch, cfg, 4, 300)
     ws = B.clef_workspace_size(cfg, schema)
     rows = [cfg, P, w, P, schema, P, B.BF16, 1, 0, 300, P, ws, P, 1 << 40]

@@ -358,6 +358,14 @@ def test_leading_dimensions_and_empty_batches():
     assert a.shape == (0, 96) and mean.shape == rstd.shape == (0,)
 
 
+def test_one_row_for_all_and_a_matrix_with_itself():
+    layer = Fp4Linear(rows_of(96, 160, torch.bfloat16, 1))
+    x = rows_of(1, 160, torch.bfloat16, 2)
+    for n in (5, 40, 900):
+        assert torch.equal(layer(x.expand(n, 160)), layer(x.expand(n, 160).contiguous()))
+    check_product(x.expand(5, 160), x.expand(5, 160), "nvfp4", torch.float32, y=product(*[quantize(x.expand(5, 160))] * 2, None, torch.float32))
+
+
 def test_the_layer_is_its_steps():
     w, bias = rows_of(520, 640, torch.bfloat16, 1), torch.randn(520, device="cuda")
     for m in (1, 64, 300):
@@ -375,7 +383,7 @@ def test_the_layer_is_its_steps():
 @pytest.mark.parametrize("form", FORMATS)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("m,n,k", [(1, 1, 8), (1, 100, 4096), (2, 300, 264), (5, 128, 1000), (7, 520, 16384), (8, 17000, 1032),
-                                   (8, 777, 5120), (3, 4096, 8192)])
+                                   (8, 777, 5120), (3, 4096, 8192), (9, 300, 2048), (16, 1000, 1288), (16, 520, 4096)])
 def test_few_rows_are_quantised_inside_the_product(form, dtype, m, n, k):
     """One launch gives what the steps give, bit for bit, statistics too; every type in and out."""
     x = rows_of(m, k, TYPES[dtype], m + k, 0.5) + 0.25

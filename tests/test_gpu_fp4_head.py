@@ -153,6 +153,20 @@ def test_full_records_are_projected_together():
         np.testing.assert_array_equal(whole[k], single[k])
 
 
+def test_rows_apart_in_memory():
+    """A row stride wider than the rows: the same outputs."""
+    head, _ = fp4_head("narrow", "mxfp4")
+    bt = batch("narrow", [256, 256, 140], 78)
+    vocab = SHAPES["narrow"].vocab
+    want = forward(head, bt, *device_inputs(bt, vocab))
+    hidden, ids, lex = device_inputs(bt, vocab, bt.H + 72)
+    out = head.forward(schema_of(bt, bt.H + 72), hidden, ids, lex)
+    torch.cuda.synchronize()
+    assert head.device_status() == 0
+    for k, v in outputs(out).items():
+        np.testing.assert_array_equal(v, want[k])
+
+
 def test_kept_memory_over_a_4_bit_projection():
     head, _ = fp4_head("pages", "nvfp4")
     bt = batch("pages", [400, 900], 75)
