@@ -30,10 +30,10 @@ namespace {
 // tile's products run beside the rest of it.
 //
 // Shared memory bounds it: of the 512 cycles that a K tile's four MMAs take, TMA's fills need 304 (nvfp4), the tensor
-// cores' reads 256 and the scales' copies 48.  131072 x 4096 x 4096 to bf16 takes 647 to 662 us (6.6 to 6.8 PFLOP/s;
-// mxfp4 626 to 634), 4864 x 4096 x 16384 91 us (7.1); run for seconds, the power cap sets the rate (731 us).  One MMA
-// thread in a diverged warp took 1527 us, a second election a K tile 723, hand-over by a releasing arrival (which
-// waits for the last tile's stores) 10 % more.
+// cores' reads 256 and the scales' copies 48.  131072 x 4096 x 4096 to bf16 takes 645 to 662 us (6.6 to 6.8 PFLOP/s;
+// mxfp4 612), 4864 x 4096 x 16384 89 us (7.3); run for seconds, the power cap sets the rate (731 us).  One MMA
+// thread in a diverged warp took 1527 us, a second election a K tile or a slower producer 715, hand-over by a releasing
+// arrival (which waits for the last tile's stores) 10 % more; a last round in halves of tiles gained nothing.
 template <int FMT>
 struct PairCfg {
     static constexpr int GROUPS = groups_of(FMT);
@@ -104,39 +104,40 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
     griddep_launch();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t leader_full = cluster_map(smem_u32(full), 0);
-            bool ok = true;
-            int i = 0, s = 0;  // stages filled so far, and the next one
-            uint32_t phase = 1;
-            for (int t = first; ok && t < n_tiles; t += stride) {
-                const int w0 = (t % n_wt) * 2 + int(rank);  // 128-row groups: own rows of w,
-                const int x0 = (t / n_wt) * 2;              // the first of x's two
-                for (int kt = 0; kt < ktiles; ++kt, ++i) {
-                    if (!mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = smem + s * C::STAGE_STRIDE;
+        const uint32_t leader_full = cluster_map(smem_u32(full), 0);
+        bool ok = true;
+        int i = 0, s = 0;  // stages filled so far, and the next one
+        uint32_t phase = 1;
+        for (int t = first; ok && t < n_tiles; t += stride) {
+            const int w0 = (t % n_wt) * 2 + int(rank), x0 = (t / n_wt) * 2;  // 128-row groups: own rows of w, x's first
+            int sw = w0 * args.kgroups, sx = x0 * args.kgroups;              // scale groups of the K tile
+            for (int kt = 0; kt < ktiles; ++kt, ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags));
+                if (!ok) break;
+                uint8_t* st = smem + s * C::STAGE_STRIDE;
+                uint8_t* sc = st + kWBytes + C::X_BYTES;
+                const uint32_t bar = leader_full + 8u * uint32_t(s);
+                if (elect_one()) {
                     // rank 0's barrier counts the bytes of both CTAs
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
-                    const uint32_t bar = leader_full + 8u * uint32_t(s);
-                    uint8_t* sc = st + kWBytes + C::X_BYTES;
                     tma_load_2d_pair(st, &tmW, kt * kAtomBytes, w0 * kWRows, bar);
                     tma_load_2d_pair(st + kWBytes, &tmX, kt * kAtomBytes, (x0 + int(rank)) * kFp4RowGroup, bar);
-                    tma_load_2d_pair(sc, &tmSW, 0, w0 * args.kgroups + kt * C::GROUPS, bar);
-                    tma_load_2d_pair(sc + C::S_BYTES, &tmSX, 0, x0 * args.kgroups + kt * C::GROUPS, bar);
-                    tma_load_2d_pair(sc + 2 * C::S_BYTES, &tmSX, 0, (x0 + 1) * args.kgroups + kt * C::GROUPS, bar);
-                    if (++s == C::STAGES) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
+                    tma_load_2d_pair(sc, &tmSW, 0, sw, bar);
+                    tma_load_2d_pair(sc + C::S_BYTES, &tmSX, 0, sx, bar);
+                    tma_load_2d_pair(sc + 2 * C::S_BYTES, &tmSX, 0, sx + args.kgroups, bar);
+                }
+                __syncwarp();
+                sw += C::GROUPS;
+                sx += C::GROUPS;
+                if (++s == C::STAGES) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
-            if (!ok && rank == 0) {  // let every copy that this CTA's barriers count land before it goes
-                for (int j = i < C::STAGES ? 0 : i - C::STAGES; j < i; ++j)
-                    mbar_wait_bounded(&full[j % C::STAGES], uint32_t(j / C::STAGES & 1), nullptr, nullptr);
-            }
+        }
+        if (!ok && rank == 0) {  // let every copy that this CTA's barriers count land before it goes
+            for (int j = i < C::STAGES ? 0 : i - C::STAGES; j < i; ++j)
+                mbar_wait_bounded(&full[j % C::STAGES], uint32_t(j / C::STAGES & 1), nullptr, nullptr);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -139,8 +139,8 @@ __device__ __forceinline__ float2 finish2(float acc0, float acc1, const ColumnTe
     return both_of(fma2(acc, pair_of(t.x, t.y), add));
 }
 
-// True in one thread of a converged warp.  The MMA warps stay converged and pick the issuing thread
-// around each batch of tcgen05 instructions: addresses and descriptors then stay in uniform
+// True in one thread of a converged warp.  The warps that issue TMA and MMA stay converged and pick the
+// issuing thread around each batch of instructions: addresses and descriptors then stay in uniform
 // registers, where the instructions want them.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;

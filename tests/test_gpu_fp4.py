@@ -315,6 +315,26 @@ def test_more_tiles_than_the_card_holds():
         assert (off <= room * (8 * 2.0 ** -23 + 50 * 2.0 ** -24) + want.abs() * torch.finfo(out).eps / 2).all()
 
 
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("m,n", [(4900, 4104), (5003, 4096), (4097, 4099), (20000, 300)])
+def test_last_round_of_tiles(form, m, n):
+    """Tile counts that leave most pairs of CTAs, or few, without a tile in the last round, with ragged rows and columns:
+    each output type, plain and with the normalisation's terms."""
+    x, w = quantize(rows_of(m, 320, torch.bfloat16, 1, 0.3), form, stats=True), quantize(rows_of(n, 320, torch.bfloat16, 2, 0.3), form, sums=True)
+    a, b = x.dequantize(torch.float32).double(), w.dequantize(torch.float32).double()
+    want, room = a @ b.T, a.abs() @ b.abs().T
+    bias = torch.randn(n, device="cuda")
+    folded = x.rstd.double()[:, None] * (want - x.mean.double()[:, None] * b.sum(1)) + bias
+    folded_room = x.rstd.double()[:, None] * (room + x.mean.double().abs()[:, None] * b.abs().sum(1)) + bias.abs()
+    for out in TYPES.values():
+        # as in check_product: 5 MMAs, 50 roundings, the output's own
+        steps = 5 * 2.0 ** -23 + 50 * 2.0 ** -24
+        off = (product(x, w, None, out).double() - want).abs()
+        assert (off <= room * steps + want.abs() * torch.finfo(out).eps / 2).all()
+        off = (product(x, w, bias, out, normalized=True).double() - folded).abs()
+        assert (off <= folded_room * steps + folded.abs() * torch.finfo(out).eps / 2).all()
+
+
 def test_long_rows_and_many_tiles():
     for m, n, k in ((1, 300, 16384), (300, 260, 8200), (2100, 1100, 260)):
         x, w = rows_of(m, k, torch.bfloat16, m, 0.5), rows_of(n, k, torch.bfloat16, n, 0.5)
