@@ -5,8 +5,9 @@
 // consecutive values of every 512: a block of 16 is one lane's and one of 32 two neighbours', so
 // that a scale is worked out once or twice, and the codes' arithmetic runs on pairs (fma.rn.f32x2).
 // Memory bounds it, and with statistics issue slots: 131072 x 4096 bf16 takes 208 us to nvfp4 (6.6 TB/s),
-// 189 to mxfp4 (7.2 TB/s; a plain copy 6.8), 294 with statistics.  Eight values a lane took 409, 324
-// and 470; rows of a block tied together by block-wide barriers, and indexes by division, 224, 195 and 306.
+// 189 to mxfp4 (7.2 TB/s; a plain copy 6.8), 257 and 218 with statistics.  Eight values a lane took 409, 324 and
+// 470 (nvfp4 with statistics); rows of a block tied together by block-wide barriers, and indexes by division, 224, 195
+// and 306; sums and squares apart, and asked for at run time, 294 with statistics.
 #include "fp4.cuh"
 #include "kernels.h"
 
@@ -80,22 +81,52 @@ struct RowSum {
     __device__ __forceinline__ float get(const Share& w, int pieces, int lane) {
         if (LANES == 32 && !w.alone()) {  // behind a barrier
             own = 0.f;
+#pragma unroll 4
             for (int i = 0; i < pieces; ++i) own += all[i][lane];
         }
         return lanes_sum<LANES>(own);
     }
 };
 
+// Two such sums, side by side; each half of the lanes adds up one of them.
+template <int LANES>
+struct RowSums {
+    uint64_t (*all)[32];
+    uint64_t own = 0;
+    __device__ __forceinline__ void add(uint64_t v, const Share& w, int piece, int lane) {
+        if (LANES < 32 || w.alone()) own = add2(own, v);
+        else all[piece][lane] = v;
+    }
+    __device__ __forceinline__ float2 get(const Share& w, int pieces, int lane) {
+        if (LANES == 32 && !w.alone()) {  // behind a barrier
+            own = 0;
+#pragma unroll 4
+            for (int i = 0; i < pieces; ++i) own = add2(own, all[i][lane]);
+        }
+        const float2 f = both_of(own);
+        const bool low = (lane & LANES / 2) == 0;
+        float v = (low ? f.x : f.y) + __shfl_xor_sync(0xffffffffu, low ? f.y : f.x, LANES / 2);
+#pragma unroll
+        for (int o = LANES / 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        const float apart = __shfl_xor_sync(0xffffffffu, v, LANES / 2);
+        return low ? make_float2(v, apart) : make_float2(apart, v);
+    }
+};
+
+// What else is asked for: the statistics; sums of what is kept, and maybe the statistics.
+enum { kNothing, kStats, kSums };
+
 // STEPS: 512-value pieces of a row that a warp keeps, 16 values a lane; W = 2^shift warps a row, so that a row has at
-// most 512 * STEPS * W values.  LANES 16: rows of up to 256 values, two a warp.
-// EXTRA: statistics or sums are asked for.  64 registers a thread, for 32 warps an SM: with 8 pieces a warp and half
-// the warps 131072 x 4096 bf16 took 301 us instead of 252.
-template <int FMT, int DT, bool VEC, int STEPS, int LANES, bool EXTRA>
+// most 512 * STEPS * W values.  LANES 16: rows of up to 256 values, two a warp.  64 registers a thread, for 32 warps
+// an SM: with 8 pieces a warp and half the warps 131072 x 4096 bf16 took 301 us instead of 252.
+template <int FMT, int DT, bool VEC, int STEPS, int LANES, int EXTRA>
 __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 4)
     fp4_quantize_kernel(const Fp4QuantizeArgs a, int shift) {
     constexpr bool NV = FMT == CLEF_NVFP4;
     __shared__ float red[kThreads / 32], means[kThreads / 32];
-    __shared__ float partial[EXTRA ? 3 : 1][EXTRA ? kThreads / 32 * STEPS : 1][32];
+    constexpr int kPieces = kThreads / 32 * STEPS;
+    __shared__ uint64_t moments[EXTRA ? kPieces : 1][32];
+    __shared__ float totals[EXTRA == kSums ? kPieces : 1][32];
     __shared__ __align__(16) uint32_t stage[VEC ? 1 : kThreads / 32][VEC ? 4 : 32 * Raw<DT>::kWords];
     griddep_wait();
     griddep_launch();  // behind the wait: whoever starts early may take what came before us as done
@@ -107,7 +138,8 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
     const bool mine = row < uint32_t(a.rows);  // threads behind the last row still meet their row's barriers and shuffles
     const int part = w.part;
     const int padded = mine ? (a.cols + kFp4Tile - 1) / kFp4Tile * kFp4Tile : 0;  // columns that have scales
-    const bool stats = EXTRA && a.mean, sums = EXTRA && a.sums;  // the same for every thread
+    const bool stats = EXTRA == kStats || (EXTRA == kSums && a.mean);  // the same for every thread
+    constexpr bool sums = EXTRA == kSums;
     const int64_t row0 = int64_t(row) * a.row_stride;
 
     Raw<DT> raw[STEPS];
@@ -138,7 +170,8 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
     uint8_t* scales = a.scales + uint64_t(row / kFp4RowGroup) * uint32_t(padded >> (NV ? 6 : 7)) * kFp4ScaleGroup +
                       (row % 32) * 16 + row % kFp4RowGroup / 32 * 4;
     const int first = EXTRA ? (w.slot << shift) * STEPS : 0;  // of the row's pieces among the block's
-    RowSum<LANES> sum{partial[0] + first}, squares{partial[EXTRA ? 1 : 0] + first}, total{partial[EXTRA ? 2 : 0] + first};
+    RowSums<LANES> both{moments + first};
+    RowSum<LANES> total{totals + (sums ? first : 0)};
     const int pieces = (a.cols + 511) / 512;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
@@ -148,11 +181,7 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
         uint64_t x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = raw[i].two(j);
-        if (stats) {
-            const float2 m = moments16(x);
-            sum.add(m.x, w, (i << shift) + part, lane);
-            squares.add(m.y, w, (i << shift) + part, lane);
-        }
+        if (stats) both.add(moments16(x), w, (i << shift) + part, lane);
         const Coded c = encode16<FMT, DT>(x, top[i], rs.inv, rs.tiny, left);
         if (mine && col < int(2 * code_stride)) *reinterpret_cast<uint2*>(codes + col / 2) = c.codes;
         uint32_t word;
@@ -176,8 +205,9 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
         if (LANES == 32 && !w.alone()) row_sync(w);
         float mean = 0.f, var = 0.f;
         if (part == 0) {
-            mean = sum.get(w, pieces, lane) * a.inv_cols;
-            var = squares.get(w, pieces, lane) * a.inv_cols - mean * mean;
+            const float2 f = both.get(w, pieces, lane);
+            mean = f.x * a.inv_cols;
+            var = f.y * a.inv_cols - mean * mean;
             if (lane == 0 && LANES == 32) means[warp] = mean;
         }
         // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows (and those
@@ -185,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
         const bool far = mine && part == 0 && !(mean * mean <= var);
         if (LANES < 32 || w.alone() ? __any_sync(0xffffffffu, far) : row_any(far, w)) {
             if (LANES == 32) mean = means[w.slot << shift];
-            RowSum<LANES> apart{sum.all};  // the sums have been read
+            RowSum<LANES> apart{reinterpret_cast<float(*)[32]>(both.all)};  // the sums have been read
 #pragma unroll 1
             for (int i = 0; i < STEPS; ++i) {
                 if (LANES == 32 && ((i << shift) + part) * 512 >= padded) continue;
@@ -323,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
     }
 }
 
-template <int FMT, int DT, bool VEC, bool EXTRA>
+template <int FMT, int DT, bool VEC, int EXTRA>
 cudaError_t quantize_rows(const Fp4QuantizeArgs& a, cudaStream_t s) {
     // Few rows: as many warps a row as it has pieces, for latency.  Many: as few as hold the row in
     // registers (4 pieces of 16-bit values, 2 of fp32).
@@ -347,9 +377,12 @@ template <int FMT, int DT>
 cudaError_t quantize_type(const Fp4QuantizeArgs& a, cudaStream_t s) {
     constexpr int size = DT == CLEF_FP32 ? 4 : 2;
     const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.row_stride * size % 16 == 0 && a.cols % 8 == 0;
-    const bool extra = a.mean || a.sums;
-    if (vec) return extra ? quantize_rows<FMT, DT, true, true>(a, s) : quantize_rows<FMT, DT, true, false>(a, s);
-    return extra ? quantize_rows<FMT, DT, false, true>(a, s) : quantize_rows<FMT, DT, false, false>(a, s);
+    if (vec) {
+        if (a.sums) return quantize_rows<FMT, DT, true, kSums>(a, s);
+        return a.mean ? quantize_rows<FMT, DT, true, kStats>(a, s) : quantize_rows<FMT, DT, true, kNothing>(a, s);
+    }
+    if (a.sums) return quantize_rows<FMT, DT, false, kSums>(a, s);
+    return a.mean ? quantize_rows<FMT, DT, false, kStats>(a, s) : quantize_rows<FMT, DT, false, kNothing>(a, s);
 }
 
 template <int FMT, int DT>

@@ -269,15 +269,15 @@ __device__ __forceinline__ RowScale row_scale_of(float row_top) {
 }
 
 // Sums of a lane's values and of their squares (what lies behind the row's end is 0).
-__device__ __forceinline__ float2 moments16(const uint64_t (&x)[8]) {
-    float t = 0.f, u = 0.f;
+__device__ __forceinline__ uint64_t moments16(const uint64_t (&x)[8]) {
+    uint64_t t = x[0], u = mul2(x[0], x[0]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 f = both_of(x[j]);
-        t += f.x + f.y;
-        u = fmaf(f.y, f.y, fmaf(f.x, f.x, u));
+    for (int j = 1; j < 8; ++j) {
+        t = add2(t, x[j]);
+        u = fma2(x[j], x[j], u);
     }
-    return make_float2(t, u);
+    const float2 a = both_of(t), b = both_of(u);
+    return pair_of(a.x + a.y, b.x + b.y);
 }
 
 // The sum of the squares of a lane's values less the mean; `left` as in encode16.

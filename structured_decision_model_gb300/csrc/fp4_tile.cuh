@@ -332,7 +332,7 @@ __device__ __forceinline__ void few_rows(const Fp4ProductArgs& args, uint8_t* sm
                     uint64_t x[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = raw.two(j);
-                    const float2 v = moments16(x);
+                    const float2 v = both_of(moments16(x));
                     sum += v.x;
                     squares += v.y;
                 }
