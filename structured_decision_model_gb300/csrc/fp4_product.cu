@@ -30,8 +30,10 @@ namespace {
 // tile's products run beside the rest of it.
 //
 // Shared memory bounds it: of the 512 cycles that a K tile's four MMAs take, TMA's fills need 304 (nvfp4), the tensor
-// cores' reads 256 and the scales' copies 48.  131072 x 4096 x 4096 to bf16 takes 645 to 662 us (6.6 to 6.8 PFLOP/s;
-// mxfp4 612), 4864 x 4096 x 16384 89 us (7.3); run for seconds, the power cap sets the rate (731 us).  One MMA
+// cores' reads 256 and the scales' copies 48.  An MMA's scales are copied before the MMA that comes before it: the copies
+// run beside that one (all of a K tile's copies before its first MMA left the tensor cores idle: 650 and 609 us instead
+// of 618 and 575; a K tile's last MMA held back behind the next one's first copies: 630 and 588).  131072 x 4096 x 4096
+// to bf16 takes 615 to 622 us (7.1 PFLOP/s; mxfp4 575, 7.65), 4864 x 4096 x 16384 85 us (7.7; mxfp4 80 to 84).  One MMA
 // thread in a diverged warp took 1527 us, a second election a K tile or a slower producer 715, hand-over by a releasing
 // arrival (which waits for the last tile's stores) 10 % more; a last round in halves of tiles gained nothing.
 template <int FMT>
@@ -165,17 +167,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
                     const uint64_t dc = c0 + uint64_t(s * (C::STAGE_STRIDE >> 4));
                     const int nk = min(4, args.k64 - 4 * kt);
                     if (elect_one()) {
-#pragma unroll
-                        for (int g = 0; g < C::GROUPS; ++g) {
+                        constexpr bool MX = FMT == CLEF_MXFP4;
+                        auto copy = [&](uint32_t g) {
                             copy_scales<true>(sw + 4 * g, dc + g * (kFp4ScaleGroup >> 4));
                             copy_scales<true>(sx + 8 * g, dc + (C::GROUPS + g) * (kFp4ScaleGroup >> 4));
                             copy_scales<true>(sx + 8 * g + 4, dc + (2 * C::GROUPS + g) * (kFp4ScaleGroup >> 4));
-                        }
+                        };
+                        copy(0);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if (k >= nk) break;
-                            constexpr bool MX = FMT == CLEF_MXFP4;
-                            const uint32_t g = MX ? k / 2 : k;
+                            const uint32_t g = MX ? k / 2 : k;  // mxfp4: a group holds two MMAs' scales
+                            if (MX ? k == 1 : k < 3) copy(g + 1);
+                            if (k >= nk) continue;
                             mma_fp4<FMT, true>(acc, da + uint64_t(2 * k), db + uint64_t(2 * k),
                                                idesc_fp4(FMT, 2 * kWRows, C::ROWS, MX ? (k & 1) * 2 : 0), sw + 4 * g,
                                                sx + 8 * g, kt > 0 || k > 0 ? 1u : 0u);
