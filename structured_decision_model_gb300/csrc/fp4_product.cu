@@ -351,9 +351,9 @@ template <int FMT, int OUT>
 cudaError_t launch_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, cudaStream_t s) {
     // Tiles of 128 x 128 while two of them at most fall to an SM (one, where K is long: then pairs, which load
     // half as much, win); measured on both sides at N 1024 to 16384, K 512 to 16384:
-    //   4096 x 4096, 1024 rows (256 tiles): tiles 11.0 us, pairs 11.3; 1536 rows (384): 20.7, 16.8
-    //   4096 x 1024, 1024 rows: 6.2, 7.3; 1536 rows: 10.9, 10.0
-    //   4096 x 16384, 512 rows (128 tiles): 22.7, 25.5; 768 rows (192): 29.1, 26.4
+    //   4096 x 4096, 1024 rows (256 tiles): tiles 10.7 us, pairs 10.8; 1280 rows (320): 18.6, 15.3
+    //   4096 x 1024, 1024 rows: 6.2, 7.4; 1280 rows: 10.5, 9.9
+    //   4096 x 16384, 512 rows (128 tiles): 22.9, 23.2; 608 rows (160): 27.6, 23.5
     const int64_t tiles = int64_t((a.N + kWRows - 1) / kWRows) * ((a.M + 127) / 128);
     if (a.M > 64 && tiles > (fp4_ktiles(x.cols) > 16 ? 1 : 2) * num_sms()) {
         if constexpr (OUT != CLEF_FP32)
