@@ -304,6 +304,19 @@ def test_statistics_do_not_depend_on_the_number_of_rows():
                 assert torch.equal(a, b[:n])
 
 
+@pytest.mark.parametrize("form", FORMATS)
+def test_statistics_and_sums_at_once_are_those_apart(form):
+    for rows, cols, dtype in ((5, 200, torch.bfloat16), (300, 1111, torch.float32), (4000, 4096, torch.bfloat16), (40, 9000, torch.float16)):
+        x = rows_of(rows, cols, dtype, rows, 0.5)
+        x[::3] += 20  # their squares' sum tells nothing of the spread: read once more
+        plain, both = quantize(x, form), quantize(x, form, stats=True, sums=True)
+        stats, sums = quantize(x, form, stats=True), quantize(x, form, sums=True)
+        assert torch.equal(both.mean, stats.mean) and torch.equal(both.rstd, stats.rstd)
+        assert torch.equal(both.sums, sums.sums) and sums.mean is None and stats.sums is None
+        for other in (both, stats, sums):
+            assert torch.equal(other.dequantize(dtype), plain.dequantize(dtype))
+
+
 def test_more_tiles_than_the_card_holds():
     """Pairs of CTAs walk several tiles of 256 x 256: the accumulators in turn, each output type."""
     x, w = quantize(rows_of(3000, 512, torch.bfloat16, 1, 0.3)), quantize(rows_of(4104, 512, torch.bfloat16, 2, 0.3))
