@@ -208,13 +208,13 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
             const float2 f = both.get(w, pieces, lane);
             mean = f.x * a.inv_cols;
             var = f.y * a.inv_cols - mean * mean;
-            if (lane == 0 && LANES == 32) means[warp] = mean;
+            if (LANES == 32 && !w.alone() && lane == 0) means[warp] = mean;
         }
         // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows (and those
         // whose squares pass fp32) are read once more and sum the squares of what is left behind the mean.
         const bool far = mine && part == 0 && !(mean * mean <= var);
         if (LANES < 32 || w.alone() ? __any_sync(0xffffffffu, far) : row_any(far, w)) {
-            if (LANES == 32) mean = means[w.slot << shift];
+            if (LANES == 32 && !w.alone()) mean = means[w.slot << shift];  // behind row_any's barrier
             RowSum<LANES> apart{reinterpret_cast<float(*)[32]>(both.all)};  // the sums have been read
 #pragma unroll 1
             for (int i = 0; i < STEPS; ++i) {
