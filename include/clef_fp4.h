@@ -63,7 +63,8 @@ CLEF_API int clef_fp4_size(int32_t format, int32_t rows, int32_t cols, size_t* c
 /* Rows x (dtype bf16, fp16 or fp32, `row_stride` elements apart, the values of a row
  * contiguous) into q.  Optional outputs ([rows] fp32, NULL: not wanted): mean and rstd, the
  * row's mean and 1 / sqrt(variance + 1e-5) of x itself; sums, the sum of what the row
- * stands for once kept. */
+ * stands for once kept.  They are fp32 sums: a row whose values add up past fp32's range has an infinite
+ * mean, and one whose squared distances from the mean do by far (a spread of about 2^96 / sqrt(cols) and more) an rstd of 0. */
 CLEF_API int clef_fp4_quantize(const clef_fp4* q, int32_t dtype, const void* x, int64_t row_stride, float* mean,
                                float* rstd, float* sums, void* stream);
 

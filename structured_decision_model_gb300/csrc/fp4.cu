@@ -123,7 +123,8 @@ template <int FMT, int DT, bool VEC, int STEPS, int LANES, int EXTRA>
 __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 4)
     fp4_quantize_kernel(const Fp4QuantizeArgs a, int shift) {
     constexpr bool NV = FMT == CLEF_NVFP4;
-    __shared__ float red[kThreads / 32], means[kThreads / 32];
+    __shared__ float red[kThreads / 32];
+    __shared__ Spread spreads[EXTRA ? kThreads / 32 : 1];
     constexpr int kPieces = kThreads / 32 * STEPS;
     __shared__ uint64_t moments[EXTRA ? kPieces : 1][32];
     __shared__ float totals[EXTRA == kSums ? kPieces : 1][32];
@@ -204,25 +205,27 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
         // The row's first warp adds up; the others wait for what it finds only where that is far from zero.
         if (LANES == 32 && !w.alone()) row_sync(w);
         float mean = 0.f, var = 0.f;
+        Spread from{0.f, 1.f};
         if (part == 0) {
             const float2 f = both.get(w, pieces, lane);
             mean = f.x * a.inv_cols;
             var = f.y * a.inv_cols - mean * mean;
-            if (LANES == 32 && !w.alone() && lane == 0) means[warp] = mean;
+            from = spread_of(mean, var);
+            if (LANES == 32 && !w.alone() && lane == 0) spreads[warp] = from;
         }
-        // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows (and those
-        // whose squares pass fp32) are read once more and sum the squares of what is left behind the mean.
-        const bool far = mine && part == 0 && !(mean * mean <= var);
+        // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows, and those
+        // whose squares pass fp32, are read once more and sum the squares of what is left behind the mean.
+        const bool far = mine && part == 0 && far_from_zero(mean, var);
         if (LANES < 32 || w.alone() ? __any_sync(0xffffffffu, far) : row_any(far, w)) {
-            if (LANES == 32 && !w.alone()) mean = means[w.slot << shift];  // behind row_any's barrier
-            RowSum<LANES> apart{reinterpret_cast<float(*)[32]>(both.all)};  // the sums have been read
+            if (LANES == 32 && !w.alone()) from = spreads[w.slot << shift];  // behind row_any's barrier
+            RowSum<LANES> apart{reinterpret_cast<float(*)[32]>(both.all)};   // the sums have been read
 #pragma unroll 1
             for (int i = 0; i < STEPS; ++i) {
                 if (LANES == 32 && ((i << shift) + part) * 512 >= padded) continue;
                 const int col0 = ((i << shift) + part) * 512;
                 uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
                 const Raw<DT> again = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
-                const float q = squares_apart<DT>(again, mean, a.cols - (col0 + lane * 16));
+                const float q = squares_apart<DT>(again, from, a.cols - (col0 + lane * 16));
                 apart.add(q, w, (i << shift) + part, lane);
             }
             if (LANES == 32 && !w.alone()) row_sync(w);
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
         }
         if (mine && part == 0 && lane == 0) {
             a.mean[row] = mean;
-            a.rstd[row] = rsqrtf(var + 1e-5f);
+            a.rstd[row] = rstd_of(var, from.by);
         }
     }
     if (sums) {

@@ -280,14 +280,25 @@ __device__ __forceinline__ uint64_t moments16(const uint64_t (&x)[8]) {
     return pair_of(a.x + a.y, b.x + b.y);
 }
 
-// The sum of the squares of a lane's values less the mean; `left` as in encode16.
+// How a row's variance is found from its distances from the mean, where the mean square less the mean's square does not
+// give it.  `by` scales the distances, a power of two: where the mean square passes fp32's range, so may the distances'
+// (those that count are above 2^30 there, steps of values near 2^57 and more).
+struct Spread {
+    float mean, by;
+};
+constexpr float kFar = 2.3283064365386963e-10f;  // 2^-32
+__device__ __forceinline__ Spread spread_of(float mean, float var) { return Spread{mean, var < INFINITY ? 1.f : kFar}; }
+__device__ __forceinline__ bool far_from_zero(float mean, float var) { return !(mean * mean <= var && var < INFINITY); }
+__device__ __forceinline__ float rstd_of(float var, float by) { return rsqrtf(var + 1e-5f * by * by) * by; }
+
+// The sum of the squares of a lane's scaled distances from the mean; `left` as in encode16.
 template <int DT>
-__device__ __forceinline__ float squares_apart(const Raw<DT>& raw, float mean, int left) {
-    const uint64_t less = pair_of(-mean, -mean);
+__device__ __forceinline__ float squares_apart(const Raw<DT>& raw, const Spread& from, int left) {
+    const uint64_t less = pair_of(-from.mean, -from.mean), by = pair_of(from.by, from.by);
     float q = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float2 d = both_of(add2(raw.two(j), less));
+        const float2 d = both_of(mul2(add2(raw.two(j), less), by));
         if (2 * j < left) q = fmaf(d.x, d.x, q);
         if (2 * j + 1 < left) q = fmaf(d.y, d.y, q);
     }

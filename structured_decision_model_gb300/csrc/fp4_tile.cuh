@@ -345,13 +345,14 @@ __device__ __forceinline__ void few_rows(const Fp4ProductArgs& args, uint8_t* sm
             if (args.mean_out) {
                 const float mean = warp_sum(sum) * args.inv_cols;
                 float var = warp_sum(squares) * args.inv_cols - mean * mean;
-                if (!(mean * mean <= var)) {  // see the kernel for many rows
+                const Spread from = spread_of(mean, var);
+                if (far_from_zero(mean, var)) {  // see the kernel for many rows
                     float q = 0.f;
                     for (int c = 0; c < cols; c += 512)
-                        q += squares_apart<DT>(load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr), mean, cols - (c + lane * 16));
+                        q += squares_apart<DT>(load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr), from, cols - (c + lane * 16));
                     var = warp_sum(q) * args.inv_cols;
                 }
-                const float rstd = rsqrtf(var + 1e-5f);
+                const float rstd = rstd_of(var, from.by);
                 f.x *= rstd;
                 f.y = -mean * rstd;
                 if (blockIdx.x == 0 && lane == 0) {
