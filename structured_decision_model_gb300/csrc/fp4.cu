@@ -214,24 +214,34 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
             if (LANES == 32 && !w.alone() && lane == 0) spreads[warp] = from;
         }
         // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows, and those
-        // whose squares pass fp32, are read once more and sum the squares of what is left behind the mean.
+        // whose squares pass fp32, are read twice more, for their mean and for their variance.
         const bool far = mine && part == 0 && far_from_zero(mean, var);
         if (LANES < 32 || w.alone() ? __any_sync(0xffffffffu, far) : row_any(far, w)) {
-            if (LANES == 32 && !w.alone()) from = spreads[w.slot << shift];  // behind row_any's barrier
-            RowSum<LANES> apart{reinterpret_cast<float(*)[32]>(both.all)};   // the sums have been read
+            RowSums<LANES> apart{both.all};  // the sums have been read
 #pragma unroll 1
-            for (int i = 0; i < STEPS; ++i) {
-                if (LANES == 32 && ((i << shift) + part) * 512 >= padded) continue;
-                const int col0 = ((i << shift) + part) * 512;
-                uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
-                const Raw<DT> again = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
-                const float q = squares_apart<DT>(again, from, a.cols - (col0 + lane * 16));
-                apart.add(q, w, (i << shift) + part, lane);
-            }
-            if (LANES == 32 && !w.alone()) row_sync(w);
-            if (part == 0) {
-                const float v = apart.get(w, pieces, lane) * a.inv_cols;
-                if (far) var = v;
+            for (int turn = 0; turn < 2; ++turn) {
+                if (LANES == 32 && !w.alone()) from = spreads[w.slot << shift];  // behind a barrier
+                apart.own = 0;
+#pragma unroll 1
+                for (int i = 0; i < STEPS; ++i) {
+                    if (LANES == 32 && ((i << shift) + part) * 512 >= padded) continue;
+                    const int col0 = ((i << shift) + part) * 512;
+                    uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
+                    const Raw<DT> again = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
+                    apart.add(moments_apart<DT>(again, from, a.cols - (col0 + lane * 16)), w, (i << shift) + part, lane);
+                }
+                if (LANES == 32 && !w.alone()) row_sync(w);
+                if (part == 0) {
+                    const float2 f = apart.get(w, pieces, lane);
+                    const float rest = f.x * a.inv_cols;
+                    if (turn == 0) {
+                        if (far) mean = from.mean = corrected_mean(from, rest);
+                        if (LANES == 32 && !w.alone() && lane == 0) spreads[warp] = from;
+                    } else if (far) {
+                        var = variance_apart(rest, f.y * a.inv_cols);
+                    }
+                }
+                if (LANES == 32 && !w.alone() && turn == 0) row_sync(w);
             }
         }
         if (mine && part == 0 && lane == 0) {

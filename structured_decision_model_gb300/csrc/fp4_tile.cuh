@@ -343,14 +343,23 @@ __device__ __forceinline__ void few_rows(const Fp4ProductArgs& args, uint8_t* sm
                 if (lane == 0) tops[m] = row_top;
             }
             if (args.mean_out) {
-                const float mean = warp_sum(sum) * args.inv_cols;
+                float mean = warp_sum(sum) * args.inv_cols;
                 float var = warp_sum(squares) * args.inv_cols - mean * mean;
-                const Spread from = spread_of(mean, var);
+                Spread from = spread_of(mean, var);
                 if (far_from_zero(mean, var)) {  // see the kernel for many rows
-                    float q = 0.f;
-                    for (int c = 0; c < cols; c += 512)
-                        q += squares_apart<DT>(load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr), from, cols - (c + lane * 16));
-                    var = warp_sum(q) * args.inv_cols;
+#pragma unroll 1
+                    for (int turn = 0; turn < 2; ++turn) {
+                        float d = 0.f, q = 0.f;
+                        for (int c = 0; c < cols; c += 512) {
+                            const Raw<DT> raw = load16<DT, true, 32>(args.x, row0, c, cols, lane, nullptr);
+                            const float2 v = both_of(moments_apart<DT>(raw, from, cols - (c + lane * 16)));
+                            d += v.x;
+                            q += v.y;
+                        }
+                        const float rest = warp_sum(d) * args.inv_cols;
+                        if (turn == 0) mean = from.mean = corrected_mean(from, rest);
+                        else var = variance_apart(rest, warp_sum(q) * args.inv_cols);
+                    }
                 }
                 const float rstd = rstd_of(var, from.by);
                 f.x *= rstd;
