@@ -159,8 +159,8 @@ CLEF_API int clef_cache_attend(const clef_cache* cache, int32_t B, int32_t total
                                int32_t table_stride, const int32_t* lengths, float scale, int32_t causal, void* out,
                                float* lse, int32_t* flags, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Waits for `stream`, then reads and clears `flags`: CLEF_OK, CLEF_ERR_DEVICE_BOUNDS or
- * CLEF_ERR_NO_PAGES (bounds first when both happened). */
+/* Waits for `stream`, then reads and clears `flags`: CLEF_OK, CLEF_ERR_DEVICE_TIMEOUT (a wait of a 4-bit
+ * product, clef_fp4.h, ran out), CLEF_ERR_DEVICE_BOUNDS or CLEF_ERR_NO_PAGES (the first of these that happened). */
 CLEF_API int clef_cache_status(int32_t* flags, void* stream);
 
 /* ---- the head over kept memory.

@@ -30,7 +30,8 @@
  * before any launch, a clef_status from every entry point, all work asynchronous on
  * `stream` of the current device, nothing allocated, every call capturable into a CUDA
  * graph.  `flags` is a device int32 that the caller clears; kernels only set bits in it
- * (clef_cache_status reads and clears it).
+ * (clef_cache_status reads and clears it).  Every wait of the products is bounded: where one
+ * ran out it reports CLEF_ERR_DEVICE_TIMEOUT, and the outputs since it was last read are not to be used.
  */
 #ifndef CLEF_FP4_H
 #define CLEF_FP4_H

@@ -220,6 +220,7 @@ int clef_cache_status(int32_t* flags, void* stream) {
     CKC(cudaMemcpyAsync(&h, flags, 4, cudaMemcpyDeviceToHost, st));
     CKC(cudaStreamSynchronize(st));
     if (h != 0) CKC(cudaMemsetAsync(flags, 0, 4, st));
+    if (h & kFlagTimeout) return CLEF_ERR_DEVICE_TIMEOUT;
     if (h & kFlagBounds) return CLEF_ERR_DEVICE_BOUNDS;
     if (h & kFlagPages) return CLEF_ERR_NO_PAGES;
     return CLEF_OK;
