@@ -6,11 +6,13 @@
 
 and by single steps: ``quantize`` (an ``Fp4Matrix``), ``Fp4Matrix.dequantize`` and ``product``.
 All arithmetic happens in libclef_head.so, on torch's current stream.  Nothing here waits
-for the GPU; ``device_status`` does, and reports what the kernels met.  A value is kept as
+for the GPU but the first matrix on a device, whose words for reports are cleared from the host (and every 2048th
+matrix of weights); ``device_status`` does, and reports what the kernels met.  A value is kept as
 the nearest of 16 numbers times its block's scale: "mxfp4" (blocks of 32, a power of two)
 or "nvfp4" (blocks of 16, three bits behind the point, and a power of two for each row).
 Nothing here passes gradients on: tensors that require one are refused while grad mode is on.
 """
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -29,6 +31,33 @@ _TYPES = {(a, b): (_DTYPES[a], _DTYPES[b or a], b or a) for a in _DTYPES for b i
 
 def _up(n: int) -> int:
     return (n + 255) // 256 * 256
+
+
+# Words that products report in, by device: [cleared ones, how many are taken].  Every matrix takes one at its first
+# product and none is taken twice, so that a word is clear for every stream from the start and no captured graph
+# clears it again.
+_WORDS = 4096
+_words = {}
+_words_lock = threading.Lock()
+
+
+def _cleared_words(index, want):
+    """The device's words with at least ``want`` to take, half of all where no capture keeps new ones from being cleared."""
+    words = _words.get(index)
+    if words is None or words[1] > _WORDS // 2:
+        if not torch.cuda.is_current_stream_capturing():
+            # from the host, which waits for the copy: whatever stream uses a word first comes behind it
+            words = _words[index] = [torch.zeros(_WORDS, dtype=torch.int32).to(torch.device("cuda", index)), 0]
+        elif want and (words is None or words[1] == _WORDS):
+            _refuse("a capture cannot clear flags: ask for the matrix's before it")
+    return words
+
+
+def _flag_word(index):
+    with _words_lock:
+        words = _cleared_words(index, 1)
+        words[1] += 1
+        return words[0][words[1] - 1:words[1]]
 
 
 class Fp4Matrix:
@@ -63,6 +92,9 @@ class Fp4Matrix:
         self.rows, self.cols, self.format, self.data = rows, cols, format, data
         self.struct = B.ClefFp4(base, base + scales, base + row_scale if code else None, rows, cols, code)
         self.device, self._index = data.device, index
+        if index not in _words:  # now, so that a later capture finds some
+            with _words_lock:
+                _cleared_words(index, 0)
         self.mean = self.rstd = self.sums = self._flags = None
 
     @property
@@ -71,9 +103,9 @@ class Fp4Matrix:
 
     @property
     def flags(self) -> torch.Tensor:
-        """What the products with these weights report (int32 [1]); made at the first one."""
+        """What the products with these weights report (int32 [1])."""
         if self._flags is None:
-            self._flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+            self._flags = _flag_word(self._index)
         return self._flags
 
     def dequantize(self, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:

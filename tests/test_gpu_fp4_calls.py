@@ -2,7 +2,9 @@
 import pytest
 import torch
 
-from structured_decision_model_gb300.microscaled import Fp4Linear, quantize
+from structured_decision_model_gb300 import microscaled
+from structured_decision_model_gb300.binding import ClefError
+from structured_decision_model_gb300.microscaled import Fp4Linear, Fp4Matrix, product, quantize
 
 pytestmark = pytest.mark.gpu
 
@@ -11,6 +13,14 @@ BOUNDS, TIMEOUT = 1, 2  # bits that kernels set
 
 def rows_of(rows, cols, seed=0, dtype=torch.bfloat16):
     return torch.randn(rows, cols, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def captured(f):
+    """The graph of one call, and what the call returned."""
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = f()
+    return g, out
 
 
 @pytest.mark.parametrize("bits,status", [(TIMEOUT, 6), (BOUNDS, 5), (TIMEOUT | BOUNDS, 6)])
@@ -24,3 +34,66 @@ def test_a_wait_that_ran_out_is_reported(bits, status):
         layer(rows_of(20, 256, 1))
         assert report() == status
         assert report() == 0
+
+
+def test_the_first_product_of_a_matrix_in_a_graph():
+    """What products report stays through replays until it is read, and is clear before the first one."""
+    x, w = quantize(rows_of(20, 256, 1)), quantize(rows_of(130, 256, 2))
+    junk = torch.full((1 << 16,), -1, dtype=torch.int32, device="cuda")  # memory that a new buffer may be made from
+    del junk
+    g, y = captured(lambda: product(x, w))
+    assert w.device_status() == 0
+    g.replay()
+    assert torch.equal(y, product(x, w))
+    w.flags.fill_(TIMEOUT)                 # as a wait that ran out leaves it
+    g.replay()
+    torch.cuda.synchronize()
+    assert w.device_status() == 6          # CLEF_ERR_DEVICE_TIMEOUT
+    assert w.device_status() == 0
+
+
+def test_matrices_report_apart():
+    a, b = quantize(rows_of(8, 64, 1)), quantize(rows_of(8, 64, 2))
+    a.flags.fill_(TIMEOUT)
+    product(a, b)
+    assert b.device_status() == 0 and a.device_status() == 6
+
+
+def test_the_first_product_on_another_stream():
+    """Flags are clear for every stream, whatever the one that made them still has to do."""
+    x, w = quantize(rows_of(20, 256, 1)), quantize(rows_of(130, 256, 2))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    at = w.flags
+    with torch.cuda.stream(s):
+        at.fill_(TIMEOUT)
+        s.synchronize()
+    torch.cuda.synchronize()
+    assert w.device_status() == 6
+
+
+def test_every_matrix_has_its_own_word():
+    data = torch.empty(256 + 2048 + 4, dtype=torch.uint8, device="cuda")
+    at = [Fp4Matrix(1, 32, data=data).flags.data_ptr() for _ in range(5000)]  # more than are cleared at once
+    assert len(set(at)) == 5000
+
+
+def test_a_capture_without_cleared_words(monkeypatch):
+    """Nothing was made on the device before: rows are captured, a product is refused until there are words."""
+    monkeypatch.setattr(microscaled, "_words", {})
+    x, w = rows_of(20, 256, 1), rows_of(130, 256, 2)
+
+    def steps():
+        a, b = quantize(x), quantize(w)
+        with pytest.raises(ClefError):
+            product(a, b)
+        return a, b
+
+    g, (a, b) = captured(steps)
+    g.replay()
+    want = quantize(w)                     # outside: clears words
+    assert torch.equal(product(a, b), product(quantize(x), want)) and b.device_status() == 0
+    g, y = captured(lambda: product(quantize(x), quantize(w)))
+    g.replay()
+    assert torch.equal(y, product(a, b))
