@@ -84,17 +84,19 @@ CLEF_API int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float*
                               const float* rstd, const float* sums, int32_t dtype, void* out, int64_t row_stride,
                               int32_t* flags, void* stream);
 
-/* Bytes of scratch that clef_fp4_linear needs for `rows` rows of `cols` values of type x_dtype, with sums
- * (normalized) or without, whose rows all start on 16 bytes and have a multiple of 8 values (aligned; one row: x
- * does) or not.  0: few aligned rows are quantised inside the product, in one launch; its scratch may be NULL.
+/* Bytes of scratch to give clef_fp4_linear for `rows` rows of `cols` values of type x_dtype and `outs` rows of weights,
+ * with sums (normalized) or without, whose rows all start on 16 bytes and have a multiple of 8 values (aligned; one
+ * row: x does) or not, in a call by itself or in a captured graph (captured), whose launches cost the host nothing.
+ * 0: the rows are few and best quantised inside the product, in one launch; give NULL.
  * Without `aligned` the size does for any call of so many rows. */
-CLEF_API int clef_fp4_linear_scratch(int32_t format, int32_t x_dtype, int32_t rows, int32_t cols, int32_t normalized,
-                                     int32_t aligned, size_t* bytes);
+CLEF_API int clef_fp4_linear_scratch(int32_t format, int32_t x_dtype, int32_t rows, int32_t cols, int32_t outs,
+                                     int32_t normalized, int32_t aligned, int32_t captured, size_t* bytes);
 
 /* A layer with 4-bit weights: clef_fp4_quantize of the `rows` rows x in w's format, then clef_fp4_product with
  * w, the same numbers by one call.  With `sums` (of w's rows) the rows are normalized as there, and their
  * mean and rstd ([rows] fp32, both needed then) come back too; without, all three are NULL.
- * scratch: 256-byte aligned device memory of the call's own until it has run. */
+ * scratch: 256-byte aligned device memory of the call's own until it has run; NULL, for few aligned rows alone: one
+ * launch, which needs none. */
 CLEF_API int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
                              const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride,
                              float* mean, float* rstd, void* scratch, size_t scratch_bytes, int32_t* flags,

@@ -124,7 +124,7 @@ def load():
     lib.clef_fp4_quantize.argtypes = [fp4, _i32, _vp, _i64, _vp, _vp, _vp, _vp]
     lib.clef_fp4_dequantize.argtypes = [fp4, _i32, _vp, _i64, _vp]
     lib.clef_fp4_product.argtypes = [fp4, fp4, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
-    lib.clef_fp4_linear_scratch.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]
+    lib.clef_fp4_linear_scratch.argtypes = [_i32] * 8 + [ctypes.POINTER(_sz)]
     lib.clef_fp4_linear.argtypes = [fp4, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _vp]
     cfg, schema = ctypes.POINTER(ClefConfig), ctypes.POINTER(ClefSchema)
     lib.clef_fp4_memory_weights.argtypes = [cfg, _vp, fp4, _vp, _vp]
@@ -373,10 +373,10 @@ def clef_fp4_product(x: ClefFp4, w: ClefFp4, bias_ptr, mean_ptr, rstd_ptr, sums_
                                    stream), "clef_fp4_product")
 
 
-def clef_fp4_linear_scratch(format, x_dtype, rows, cols, normalized=0, aligned=0):
+def clef_fp4_linear_scratch(format, x_dtype, rows, cols, normalized=0, aligned=0, outs=1, captured=0):
     out = _sz(0)
-    _check(load().clef_fp4_linear_scratch(format, x_dtype, rows, cols, normalized, aligned, ctypes.byref(out)),
-           "clef_fp4_linear_scratch")
+    _check(load().clef_fp4_linear_scratch(format, x_dtype, rows, cols, outs, normalized, aligned, captured,
+                                          ctypes.byref(out)), "clef_fp4_linear_scratch")
     return out.value
 
 

@@ -1142,7 +1142,7 @@ int clef_fp4_memory_weights(const clef_config* cfg, const void* prepared, const 
 
 int clef_stream_rows_fp4_scratch(const clef_config* cfg, int32_t format, int32_t n_rows, size_t* bytes) {
     if (!config_ok(cfg)) return CLEF_ERR_UNSUPPORTED_CONFIG;
-    return clef_fp4_linear_scratch(format, CLEF_BF16, n_rows, cfg->hidden, 1, 0, bytes);
+    return clef_fp4_linear_scratch(format, CLEF_BF16, n_rows, cfg->hidden, 1, 1, 0, 0, bytes);
 }
 
 int clef_head_forward_fp4_scratch(const clef_config* cfg, int32_t format, const clef_schema* schema, size_t* bytes) {
@@ -1156,7 +1156,7 @@ int clef_head_forward_fp4_scratch(const clef_config* cfg, int32_t format, const 
         b = fp4_run(schema, *pp, b, &rows);
         most = std::max(most, rows);
     }
-    return clef_fp4_linear_scratch(format, CLEF_BF16, int32_t(most), cfg->hidden, 1, 0, bytes);
+    return clef_fp4_linear_scratch(format, CLEF_BF16, int32_t(most), cfg->hidden, 1, 1, 0, 0, bytes);
 }
 
 int clef_stream_rows_fp4(const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,

@@ -71,10 +71,11 @@ cudaError_t launch_fp4_product(const clef_fp4& x, const clef_fp4& w, const Fp4Pr
                                cudaStream_t s);
 
 
-// Rows that the product quantises itself, in one launch: whether it should, and the launch (a.M rows of type x_dtype
-// that start on 16 bytes, cols a multiple of 8).
+// Rows that the product quantises itself, in one launch: whether it can, whether that pays, and the launch (a.M rows
+// of type x_dtype that start on 16 bytes, cols a multiple of 8).
 constexpr int kFp4FewRows = 16;
 bool fp4_few_rows(int format, int x_dtype, int rows, int cols, bool normalized);
+bool fp4_few_pays(int format, int x_dtype, int rows, int cols, int outs, bool normalized, bool captured);
 cudaError_t launch_fp4_few(const clef_fp4& w, const Fp4ProductArgs& a, int x_dtype, int dtype, cudaStream_t s);
 
 }  // namespace clef

@@ -182,12 +182,13 @@ int clef_fp4_product(const clef_fp4* x, const clef_fp4* w, const float* bias, co
                                      dtype, static_cast<cudaStream_t>(stream)));
 }
 
-int clef_fp4_linear_scratch(int32_t format, int32_t x_dtype, int32_t rows, int32_t cols, int32_t normalized,
-                            int32_t aligned, size_t* bytes) {
-    if (!bytes || bad_type(x_dtype)) return CLEF_ERR_INVALID_ARGUMENT;
+int clef_fp4_linear_scratch(int32_t format, int32_t x_dtype, int32_t rows, int32_t cols, int32_t outs, int32_t normalized,
+                            int32_t aligned, int32_t captured, size_t* bytes) {
+    if (!bytes || bad_type(x_dtype) || outs < 1) return CLEF_ERR_INVALID_ARGUMENT;
     const int st = check_size(format, rows, cols);
     if (st != CLEF_OK) return st;
-    const bool few = aligned && cols % 8 == 0 && fp4_few_rows(format, x_dtype, rows, cols, normalized != 0);
+    const bool few = aligned && fp4_few_rows(format, x_dtype, rows, cols, normalized != 0) &&
+                     fp4_few_pays(format, x_dtype, rows, cols, outs, normalized != 0, captured != 0);
     *bytes = few ? 0 : Scratch(format, rows, cols).total;
     return CLEF_OK;
 }
@@ -200,14 +201,12 @@ int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x
     if (st != CLEF_OK) return st;
     if (bad_type(x_dtype) || bad_rows(x, x_dtype, rows, x_stride, 0)) return CLEF_ERR_INVALID_ARGUMENT;
     const bool aligned = !misaligned(x, 16) && (rows == 1 || x_stride * size_of(x_dtype) % 16 == 0);
-    size_t need = 0;
-    clef_fp4_linear_scratch(w->format, x_dtype, rows, w->cols, sums != nullptr, aligned, &need);
-    const bool few = need == 0;
+    const bool few = !scratch && aligned && fp4_few_rows(w->format, x_dtype, rows, w->cols, sums != nullptr);
     const Scratch S(w->format, rows, w->cols);
     clef_fp4 q{nullptr, nullptr, nullptr, rows, w->cols, w->format};
     if (!few) {
         if (!scratch || misaligned(scratch, 256)) return CLEF_ERR_INVALID_ARGUMENT;
-        if (scratch_bytes < need) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+        if (scratch_bytes < S.total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
         q = S.matrix(scratch, w->format, rows, w->cols);
     }
     st = check_product(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags);

@@ -23,6 +23,7 @@ from .memory import _DTYPES, _current_device, _overlap, _raw_stream, _refuse
 FORMATS = {"mxfp4": B.MXFP4, "nvfp4": B.NVFP4}
 BLOCK = {"mxfp4": 32, "nvfp4": 16}
 _FP32 = torch.float32
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 # (input type, output type asked for): their codes, and the output's type
@@ -45,7 +46,7 @@ def _cleared_words(index, want):
     """The device's words with at least ``want`` to take, half of all where no capture keeps new ones from being cleared."""
     words = _words.get(index)
     if words is None or words[1] > _WORDS // 2:
-        if not torch.cuda.is_current_stream_capturing():
+        if not _capturing():
             # from the host, which waits for the copy: whatever stream uses a word first comes behind it
             words = _words[index] = [torch.zeros(_WORDS, dtype=torch.int32).to(torch.device("cuda", index)), 0]
         elif want and (words is None or words[1] == _WORDS):
@@ -264,12 +265,14 @@ class Fp4Linear:
         if n:
             at, scratch = rows.data_ptr(), None
             stride = stride if n > 1 else self.cols
-            key = (n, x_type, normalized, (at | stride * x.element_size()) & 15 == 0)
+            few = n <= 16  # may go in one launch, which depends on whether a graph is being captured
+            key = (n, x_type, normalized, (at | stride * x.element_size()) & 15 == 0, few and _capturing())
             size = self._scratch.get(key)
             if size is None:
                 if len(self._scratch) >= 4096:
                     self._scratch.clear()
-                size = self._scratch[key] = B.clef_fp4_linear_scratch(self._struct.format, x_type, n, self.cols, *key[2:])
+                size = self._scratch[key] = B.clef_fp4_linear_scratch(self._struct.format, x_type, n, self.cols, *key[2:4],
+                                                                      self.outs, key[4])
             if size:  # a buffer of the call's own: overlapping calls and captured graphs never share one
                 space = torch.empty(size, dtype=torch.uint8, device=self._device)
                 scratch = space.data_ptr()

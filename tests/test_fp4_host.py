@@ -161,3 +161,18 @@ def test_the_oracle_of_the_tests():
     codes, byte, r, values = kept(x / 7.9 * 6, "nvfp4")
     # amax 6: r = 2^-8, quotient 1 / r = 256 = 2^8, so the scale is 1 again
     assert r[0] == 2.0 ** -8 and E4M3[byte[0, 0]] == 256 and values[0, 0] == 6
+
+
+def test_few_rows_by_the_outputs_and_the_capture():
+    """One launch while a call by itself is host time; in a graph where the GPU takes less, and never for a vocabulary."""
+    one = lambda form, rows, cols, norm, outs, captured, t=B.BF16: \
+        B.clef_fp4_linear_scratch(form, t, rows, cols, norm, 1, outs, captured) == 0
+    for form in (B.MXFP4, B.NVFP4):
+        for norm in (0, 1):
+            for rows in (1, 8):
+                assert one(form, rows, 4096, norm, 32768, 0) and not one(form, rows, 4096, norm, 32769, 0)
+                assert one(form, rows, 1024, norm, 4096, 1) and not one(form, rows, 1024, norm, 131072, 1)
+    assert one(B.MXFP4, 8, 4096, 0, 4096, 1) and not one(B.MXFP4, 16, 4096, 0, 4096, 1) and one(B.MXFP4, 16, 4096, 0, 4096, 0)
+    for form, norm in ((B.NVFP4, 0), (B.NVFP4, 1), (B.MXFP4, 1)):
+        assert not one(form, 1, 4096, norm, 4096, 1) and not one(form, 8, 4096, norm, 20000, 1) and one(form, 4, 4096, norm, 20000, 1)
+    refused(1, B.clef_fp4_linear_scratch, B.MXFP4, B.BF16, 1, 8, 0, 1, 0)

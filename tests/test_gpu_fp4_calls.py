@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from structured_decision_model_gb300 import microscaled
+from structured_decision_model_gb300 import binding as B, microscaled
 from structured_decision_model_gb300.binding import ClefError
 from structured_decision_model_gb300.microscaled import Fp4Linear, Fp4Matrix, product, quantize
 
@@ -97,3 +97,26 @@ def test_a_capture_without_cleared_words(monkeypatch):
     g, y = captured(lambda: product(quantize(x), quantize(w)))
     g.replay()
     assert torch.equal(y, product(a, b))
+
+
+@pytest.mark.parametrize("form", ["mxfp4", "nvfp4"])
+def test_few_rows_in_one_launch_or_two(form):
+    """By the number of outputs, and by whether a graph is being captured; the same numbers either way."""
+    def launches(f):
+        before = B.clef_kernel_launches()
+        out = f()
+        return B.clef_kernel_launches() - before, out
+
+    x = rows_of(2, 4096, 1)
+    for outs, eager, in_graph in ((256, 1, 2 if form == "nvfp4" else 1), (33000, 2, 2)):
+        layer = Fp4Linear(rows_of(outs, 4096, 2), None, form)
+        n, y = launches(lambda: layer(x))
+        assert n == eager
+        counts = []
+        g, got = captured(lambda: [counts.append(launches(lambda: layer(x))) or counts[-1][1] for _ in range(2)])
+        assert [n for n, _ in counts] == [in_graph] * 2
+        g.replay()
+        assert torch.equal(got[0], y) and torch.equal(got[1], y)
+        assert launches(lambda: layer(x))[0] == eager  # behind the capture as before it
+        assert torch.equal(y, product(quantize(x, form), layer.weight))
+        assert layer.device_status() == 0
