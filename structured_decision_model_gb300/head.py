@@ -11,7 +11,7 @@ import numpy as np
 import torch
 
 from . import binding as B
-from .memory import MemoryCache, stream_handle
+from .memory import _ROW_DTYPES, MemoryCache, stream_handle
 from .microscaled import Fp4Matrix
 
 
@@ -77,6 +77,14 @@ class ClefHead:
             B.clef_fp4_memory_weights(self.cfg, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), stream_handle())
             self.memory_weights = w
 
+    @staticmethod
+    def _row_type(hidden):
+        """The code of the type of rows that are quantised as they are."""
+        code = _ROW_DTYPES.get(hidden.dtype)
+        if code is None or not hidden.is_cuda:
+            raise B.ClefError(1, "hidden: bf16 or fp16 rows on the GPU")
+        return code
+
     def _scratch(self, n_bytes, stream):
         """A buffer of a call's own, on the call's stream."""
         if stream is None:
@@ -103,14 +111,14 @@ class ClefHead:
         ws = self.workspace(schema)
         out = out if out is not None else self.alloc_outputs(schema)
         if self.memory_weights is not None:
-            w = self.memory_weights
+            w, rows = self.memory_weights, self._row_type(hidden)
             n = B.clef_head_forward_fp4_scratch(self.cfg, w.struct.format, schema)
             space = self._scratch(n, stream)
             B.clef_head_forward_fp4(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), schema,
-                                    hidden.data_ptr(), B.FP16 if hidden.dtype == torch.float16 else B.BF16,
-                                    token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(),
-                                    out.q_value.data_ptr(), out.q_conf.data_ptr(), out.q_argmax.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), space.data_ptr(), n, debug=debug, stream=stream_handle(stream))
+                                    hidden.data_ptr(), rows, token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(),
+                                    out.probs.data_ptr(), out.q_value.data_ptr(), out.q_conf.data_ptr(),
+                                    out.q_argmax.data_ptr(), ws.data_ptr(), ws.numel(), space.data_ptr(), n, debug=debug,
+                                    stream=stream_handle(stream))
             return out
         B.clef_head_forward(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), schema, hidden.data_ptr(),
                             token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(),
@@ -127,7 +135,7 @@ class ClefHead:
         bf16 or fp16 (fp16 rows are rounded to bf16 where the head reads them)."""
         ws = self._ws
         if self.memory_weights is not None:
-            w = self.memory_weights
+            w, rows = self.memory_weights, self._row_type(hidden)
             n = self._rows_scratch.get(n_rows)
             if n is None:
                 n = B.clef_stream_rows_fp4_scratch(self.cfg, w.struct.format, n_rows)
@@ -135,8 +143,7 @@ class ClefHead:
                     self._rows_scratch[n_rows] = n
             space = self._scratch(n, stream)
             B.clef_stream_rows_fp4(self.cfg, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), schema, hidden.data_ptr(),
-                                   B.FP16 if hidden.dtype == torch.float16 else B.BF16, record, row0, n_rows, ws.data_ptr(),
-                                   ws.numel(), space.data_ptr(), n, stream_handle(stream))
+                                   rows, record, row0, n_rows, ws.data_ptr(), ws.numel(), space.data_ptr(), n, stream_handle(stream))
             return
         fn = B.clef_stream_rows_f16 if hidden.dtype == torch.float16 else B.clef_stream_rows
         fn(self.cfg, self.prepared.data_ptr(), schema, hidden.data_ptr(), record, row0, n_rows, ws.data_ptr(),
