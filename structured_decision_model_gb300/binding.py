@@ -413,10 +413,13 @@ def clef_stream_rows_fp4(cfg, prepared_ptr, w: ClefFp4, sums_ptr, schema: Schema
 
 def clef_head_forward_fp4(cfg, weight_ptrs, prepared_ptr, w: ClefFp4, sums_ptr, schema: Schema, hidden_ptr, hidden_dtype,
                           token_ids_ptr, lexical_ptr, logits_ptr, probs_ptr, q_value_ptr, q_conf_ptr, q_argmax_ptr,
-                          workspace_ptr, workspace_bytes, scratch_ptr, scratch_bytes, debug=None, stream=0):
+                          workspace_ptr, workspace_bytes, scratch_ptr, scratch_bytes, debug=None, stream=0, check=True):
     arr = (_vp * len(weight_ptrs))(*weight_ptrs)
     dbg = ctypes.byref(debug) if debug is not None else None
-    _check(load().clef_head_forward_fp4(ctypes.byref(cfg), arr, prepared_ptr, w, sums_ptr, ctypes.byref(schema.struct),
-                                        hidden_ptr, hidden_dtype, token_ids_ptr, lexical_ptr, logits_ptr, probs_ptr,
-                                        q_value_ptr, q_conf_ptr, q_argmax_ptr, workspace_ptr, workspace_bytes, scratch_ptr,
-                                        scratch_bytes, dbg, stream), "clef_head_forward_fp4")
+    st = load().clef_head_forward_fp4(ctypes.byref(cfg), arr, prepared_ptr, w, sums_ptr, ctypes.byref(schema.struct),
+                                      hidden_ptr, hidden_dtype, token_ids_ptr, lexical_ptr, logits_ptr, probs_ptr,
+                                      q_value_ptr, q_conf_ptr, q_argmax_ptr, workspace_ptr, workspace_bytes, scratch_ptr,
+                                      scratch_bytes, dbg, stream)
+    if check:
+        _check(st, "clef_head_forward_fp4")
+    return st

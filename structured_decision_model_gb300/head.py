@@ -118,7 +118,7 @@ class ClefHead:
                                     hidden.data_ptr(), rows, token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(),
                                     out.probs.data_ptr(), out.q_value.data_ptr(), out.q_conf.data_ptr(),
                                     out.q_argmax.data_ptr(), ws.data_ptr(), ws.numel(), space.data_ptr(), n, debug=debug,
-                                    stream=stream_handle(stream))
+                                    stream=stream_handle(stream), check=check)
             return out
         B.clef_head_forward(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), schema, hidden.data_ptr(),
                             token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(),
