@@ -10,6 +10,7 @@
 #include "../../include/clef_fp4.h"
 #include "../../include/clef_head.h"
 #include "common.cuh"
+#include "fp4.h"
 #include "head_kernels.h"
 #include "kernels.h"
 
@@ -1102,19 +1103,18 @@ int check_fp4_rows(const void* prepared, const void* hidden, int32_t dtype, cons
     return CLEF_OK;
 }
 
-// K/V and statistics of `rows` rows of `hidden` from padded row `from` on, into compact rows `to` on.
-int project_fp4(const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,
+// K/V and statistics of `rows` rows of `hidden` from padded row `from` on, into compact rows `to` on; or only the checks.
+int project_fp4(bool launch, const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,
                 const clef_schema* schema, const WsLayout& L, const void* hidden, int32_t dtype, int64_t from, int64_t to,
                 int64_t rows, void* workspace, void* scratch, size_t scratch_bytes, void* stream) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const PreparedLayout PL(cfg);
     const int64_t NKV = int64_t(2) * cfg->n_route * cfg->width;
-    const int s = clef_fp4_linear(
-        w, dtype, static_cast<const uint16_t*>(hidden) + from * schema->row_stride, schema->row_stride, int32_t(rows),
-        reinterpret_cast<const float*>(static_cast<const uint8_t*>(prepared) + PL.bkv), sums, CLEF_BF16,
-        reinterpret_cast<uint16_t*>(ws + L.kv) + to * NKV, NKV, reinterpret_cast<float*>(ws + L.mu) + to,
-        reinterpret_cast<float*>(ws + L.rstd) + to, scratch, scratch_bytes, reinterpret_cast<int32_t*>(ws + L.flags), stream);
-    return s;
+    return fp4_linear(launch, w, dtype, static_cast<const uint16_t*>(hidden) + from * schema->row_stride, schema->row_stride,
+                      int32_t(rows), reinterpret_cast<const float*>(static_cast<const uint8_t*>(prepared) + PL.bkv), sums,
+                      CLEF_BF16, reinterpret_cast<uint16_t*>(ws + L.kv) + to * NKV, NKV,
+                      reinterpret_cast<float*>(ws + L.mu) + to, reinterpret_cast<float*>(ws + L.rstd) + to, scratch,
+                      scratch_bytes, reinterpret_cast<int32_t*>(ws + L.flags), stream);
 }
 
 // Records b .. (the return value) - 1 whose rows follow each other without a gap, in `hidden` and in the
@@ -1175,7 +1175,7 @@ int clef_stream_rows_fp4(const clef_config* cfg, const void* prepared, const cle
         int64_t(row0) + n_rows > schema->lengths[record])
         return CLEF_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < lp->total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
-    return project_fp4(cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype, int64_t(record) * schema->Lpad + row0,
+    return project_fp4(true, cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype, int64_t(record) * schema->Lpad + row0,
                        pp->blob[pp->rec_row_off + record] + int64_t(row0), n_rows, workspace, scratch, scratch_bytes,
                        stream);
 }
@@ -1198,22 +1198,31 @@ int clef_head_forward_fp4(const clef_config* cfg, const void* const* weights, co
     v = clef_head_forward_fp4_scratch(cfg, w->format, schema, &need);
     if (v != CLEF_OK) return v;
     if (scratch_bytes < need) return CLEF_ERR_WORKSPACE_TOO_SMALL;
-    v = clef_stream_begin(cfg, schema, workspace, workspace_bytes, stream);
-    if (v != CLEF_OK) return v;
     const Plan* pp = nullptr;
     const WsLayout* lp = nullptr;
     v = cached_plan(cfg, schema, &pp, &lp);
     if (v != CLEF_OK) return v;
+    if (workspace_bytes < lp->total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+    auto project = [&](bool launch) {
+        for (int b = 0; b < schema->B;) {
+            int64_t rows = 0;
+            const int e = fp4_run(schema, *pp, b, &rows);
+            const int s = project_fp4(launch, cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype,
+                                      int64_t(b) * schema->Lpad, pp->blob[pp->rec_row_off + b], rows, workspace, scratch,
+                                      scratch_bytes, stream);
+            if (s != CLEF_OK) return s;
+            b = e;
+        }
+        return int(CLEF_OK);
+    };
+    v = project(false);  // every refusal comes before the first launch
+    if (v != CLEF_OK) return v;
+    v = clef_stream_begin(cfg, schema, workspace, workspace_bytes, stream);
+    if (v != CLEF_OK) return v;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CK(mark(debug, 0, st));
-    for (int b = 0; b < schema->B;) {
-        int64_t rows = 0;
-        const int e = fp4_run(schema, *pp, b, &rows);
-        v = project_fp4(cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype, int64_t(b) * schema->Lpad,
-                        pp->blob[pp->rec_row_off + b], rows, workspace, scratch, scratch_bytes, stream);
-        if (v != CLEF_OK) return v;
-        b = e;
-    }
+    v = project(true);
+    if (v != CLEF_OK) return v;
     CK(mark(debug, 1, st));
     return forward_impl(cfg, weights, prepared, schema, static_cast<const uint16_t*>(hidden), token_ids, lexical, logits,
                         probs, q_value, q_conf, q_argmax, workspace, workspace_bytes, debug, stream, kForwardAfterStream,

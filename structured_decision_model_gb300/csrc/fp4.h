@@ -78,4 +78,9 @@ bool fp4_few_rows(int format, int x_dtype, int rows, int cols, bool normalized);
 bool fp4_few_pays(int format, int x_dtype, int rows, int cols, int outs, bool normalized, bool captured);
 cudaError_t launch_fp4_few(const clef_fp4& w, const Fp4ProductArgs& a, int x_dtype, int dtype, cudaStream_t s);
 
+// clef_fp4_linear, or only the checks of its arguments.
+int fp4_linear(bool launch, const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
+               const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride, float* mean, float* rstd,
+               void* scratch, size_t scratch_bytes, int32_t* flags, void* stream);
+
 }  // namespace clef

@@ -128,6 +128,56 @@ struct Scratch {
 
 }  // namespace
 
+namespace clef {
+
+int fp4_linear(bool launch, const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
+               const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride, float* mean, float* rstd,
+               void* scratch, size_t scratch_bytes, int32_t* flags, void* stream) {
+    int st = check_matrix(w);
+    if (st == CLEF_OK) st = check_size(w->format, rows, w->cols);
+    if (st != CLEF_OK) return st;
+    if (bad_type(x_dtype) || bad_rows(x, x_dtype, rows, x_stride, 0)) return CLEF_ERR_INVALID_ARGUMENT;
+    const bool aligned = !misaligned(x, 16) && (rows == 1 || x_stride * size_of(x_dtype) % 16 == 0);
+    const bool few = !scratch && aligned && fp4_few_rows(w->format, x_dtype, rows, w->cols, sums != nullptr);
+    const Scratch S(w->format, rows, w->cols);
+    clef_fp4 q{nullptr, nullptr, nullptr, rows, w->cols, w->format};
+    if (!few) {
+        if (!scratch || misaligned(scratch, 256)) return CLEF_ERR_INVALID_ARGUMENT;
+        if (scratch_bytes < S.total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
+        q = S.matrix(scratch, w->format, rows, w->cols);
+    }
+    st = check_product(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags);
+    if (st != CLEF_OK) return st;
+    // what is written: the scratch, the statistics and the output, apart from each other and from what is read
+    const int64_t m4 = int64_t(rows) * 4, n4 = int64_t(w->rows) * 4;
+    const Run space(few ? nullptr : scratch, int64_t(S.total)), in = rows_run(x, rows, x_stride, w->cols, size_of(x_dtype)),
+        to = rows_run(out, rows, row_stride, w->rows, size_of(dtype));
+    const Run reads[] = {in, codes_run(*w), scales_run(*w), row_scale_run(*w), Run(bias, n4), Run(sums, n4), Run(flags, 4)};
+    for (const Run& r : reads)
+        if (r.meets(space) || r.meets(Run(mean, m4)) || r.meets(Run(rstd, m4))) return CLEF_ERR_INVALID_ARGUMENT;
+    if (to.meets(in) || to.meets(space) || space.meets(Run(mean, m4)) || space.meets(Run(rstd, m4)) ||
+        Run(mean, m4).meets(Run(rstd, m4)))
+        return CLEF_ERR_INVALID_ARGUMENT;
+    if (!launch) return CLEF_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Fp4ProductArgs p = product_args(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, true);
+    if (few) {  // one launch
+        p.x = x;
+        p.x_stride = x_stride;
+        p.x_scale = p.mean = p.rstd = nullptr;
+        p.mean_out = mean;
+        p.rstd_out = rstd;
+        p.w_settled = false;  // the kernel before this one may be w's
+        return status(launch_fp4_few(*w, p, x_dtype, dtype, s));
+    }
+    const Fp4QuantizeArgs a{x, x_stride, static_cast<uint8_t*>(q.codes), static_cast<uint8_t*>(q.scales), q.row_scale,
+                            mean, rstd, nullptr, rows, w->cols, 1.f / float(w->cols)};
+    const int quantised = status(launch_fp4_quantize(a, w->format, x_dtype, s));
+    return quantised == CLEF_OK ? status(launch_fp4_product(q, *w, p, dtype, s)) : quantised;
+}
+
+}  // namespace clef
+
 extern "C" {
 
 int clef_fp4_size(int32_t format, int32_t rows, int32_t cols, size_t* codes, size_t* scales) {
@@ -196,46 +246,8 @@ int clef_fp4_linear_scratch(int32_t format, int32_t x_dtype, int32_t rows, int32
 int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows, const float* bias,
                     const float* sums, int32_t dtype, void* out, int64_t row_stride, float* mean, float* rstd,
                     void* scratch, size_t scratch_bytes, int32_t* flags, void* stream) {
-    int st = check_matrix(w);
-    if (st == CLEF_OK) st = check_size(w->format, rows, w->cols);
-    if (st != CLEF_OK) return st;
-    if (bad_type(x_dtype) || bad_rows(x, x_dtype, rows, x_stride, 0)) return CLEF_ERR_INVALID_ARGUMENT;
-    const bool aligned = !misaligned(x, 16) && (rows == 1 || x_stride * size_of(x_dtype) % 16 == 0);
-    const bool few = !scratch && aligned && fp4_few_rows(w->format, x_dtype, rows, w->cols, sums != nullptr);
-    const Scratch S(w->format, rows, w->cols);
-    clef_fp4 q{nullptr, nullptr, nullptr, rows, w->cols, w->format};
-    if (!few) {
-        if (!scratch || misaligned(scratch, 256)) return CLEF_ERR_INVALID_ARGUMENT;
-        if (scratch_bytes < S.total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
-        q = S.matrix(scratch, w->format, rows, w->cols);
-    }
-    st = check_product(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags);
-    if (st != CLEF_OK) return st;
-    // what is written: the scratch, the statistics and the output, apart from each other and from what is read
-    const int64_t m4 = int64_t(rows) * 4, n4 = int64_t(w->rows) * 4;
-    const Run space(few ? nullptr : scratch, int64_t(S.total)), in = rows_run(x, rows, x_stride, w->cols, size_of(x_dtype)),
-        to = rows_run(out, rows, row_stride, w->rows, size_of(dtype));
-    const Run reads[] = {in, codes_run(*w), scales_run(*w), row_scale_run(*w), Run(bias, n4), Run(sums, n4), Run(flags, 4)};
-    for (const Run& r : reads)
-        if (r.meets(space) || r.meets(Run(mean, m4)) || r.meets(Run(rstd, m4))) return CLEF_ERR_INVALID_ARGUMENT;
-    if (to.meets(in) || to.meets(space) || space.meets(Run(mean, m4)) || space.meets(Run(rstd, m4)) ||
-        Run(mean, m4).meets(Run(rstd, m4)))
-        return CLEF_ERR_INVALID_ARGUMENT;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    Fp4ProductArgs p = product_args(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, true);
-    if (few) {  // one launch
-        p.x = x;
-        p.x_stride = x_stride;
-        p.x_scale = p.mean = p.rstd = nullptr;
-        p.mean_out = mean;
-        p.rstd_out = rstd;
-        p.w_settled = false;  // the kernel before this one may be w's
-        return status(launch_fp4_few(*w, p, x_dtype, dtype, s));
-    }
-    const Fp4QuantizeArgs a{x, x_stride, static_cast<uint8_t*>(q.codes), static_cast<uint8_t*>(q.scales), q.row_scale,
-                            mean, rstd, nullptr, rows, w->cols, 1.f / float(w->cols)};
-    const int quantised = status(launch_fp4_quantize(a, w->format, x_dtype, s));
-    return quantised == CLEF_OK ? status(launch_fp4_product(q, *w, p, dtype, s)) : quantised;
+    return fp4_linear(true, w, x_dtype, x, x_stride, rows, bias, sums, dtype, out, row_stride, mean, rstd, scratch,
+                      scratch_bytes, flags, stream);
 }
 
 }  // extern "C"

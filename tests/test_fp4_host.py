@@ -176,3 +176,20 @@ def test_few_rows_by_the_outputs_and_the_capture():
     for form, norm in ((B.NVFP4, 0), (B.NVFP4, 1), (B.MXFP4, 1)):
         assert not one(form, 1, 4096, norm, 4096, 1) and not one(form, 8, 4096, norm, 20000, 1) and one(form, 4, 4096, norm, 20000, 1)
     refused(1, B.clef_fp4_linear_scratch, B.MXFP4, B.BF16, 1, 8, 0, 1, 0)
+
+
+def test_head_refusals_come_before_the_first_launch():
+    """What only the projection's own checks know is refused as an argument, not met behind the plan's upload."""
+    cfg = B.make_config()
+    bt = synth.make_batch(synth.BatchSpec(name="t", B=2, H=4096, vocab=1000, lengths=[256, 300], questions=(2, 2), options=(2, 3)),
+                          seed=2, with_hidden=False)
+    schema = B.Schema(bt.B, bt.Lpad, bt.H, bt.lengths, bt.q_rec, bt.q_type, bt.q_span, bt.q_opt_off, bt.o_span)
+    ws = B.clef_workspace_size(cfg, schema)
+    at = [(i + 1) << 32 for i in range(16)]
+    over = dict(rows=4096, cols=4096, at=at[0], scales=at[1], row_scale=at[2])
+    good = [cfg, [P] * B.clef_weight_count(cfg), at[3], matrix(**over), at[4], schema, at[5], B.BF16, P, P, P, P, P, P, P, at[6], ws,
+            at[7], 1 << 30]
+    for i, v in ((3, matrix(**dict(over, codes=None))), (3, matrix(**dict(over, codes=at[0] + 16))), (3, matrix(**dict(over, scales=None))),
+                 (3, matrix(**dict(over, row_scale=None))), (4, at[4] + 2), (17, at[6]), (17, at[5]), (6, at[7])):
+        refused(1, B.clef_head_forward_fp4, *changed(good, i, v))
+    refused(3, B.clef_head_forward_fp4, *changed(good, 3, matrix(form=2, **over)))
