@@ -35,7 +35,7 @@ def _up(n: int) -> int:
 
 
 # Words that products report in, by device: [cleared ones, how many are taken].  Every matrix takes one at its first
-# product and none is taken twice, so that a word is clear for every stream from the start and no captured graph
+# product, apart from every other matrix's, so that a word is clear for every stream from the start and no captured graph
 # clears it again.
 _WORDS = 4096
 _words = {}

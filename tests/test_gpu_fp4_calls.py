@@ -75,8 +75,8 @@ def test_the_first_product_on_another_stream():
 
 def test_every_matrix_has_its_own_word():
     data = torch.empty(256 + 2048 + 4, dtype=torch.uint8, device="cuda")
-    at = [Fp4Matrix(1, 32, data=data).flags.data_ptr() for _ in range(5000)]  # more than are cleared at once
-    assert len(set(at)) == 5000
+    matrices = [Fp4Matrix(1, 32, data=data) for _ in range(5000)]  # more than are cleared at once
+    assert len({m.flags.data_ptr() for m in matrices}) == 5000
 
 
 def test_a_capture_without_cleared_words(monkeypatch):
