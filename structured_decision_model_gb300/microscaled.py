@@ -10,12 +10,14 @@ for the GPU but the first matrix on a device, whose words for reports are cleare
 matrix of weights); ``device_status`` does, and reports what the kernels met.  A value is kept as
 the nearest of 16 numbers times its block's scale: "mxfp4" (blocks of 32, a power of two)
 or "nvfp4" (blocks of 16, three bits behind the point, and a power of two for each row).
-Nothing here passes gradients on: tensors that require one are refused while grad mode is on.
+Nothing here passes gradients on: tensors that require one are refused while grad mode is on, and dual
+tensors of forward mode always.
 """
 import threading
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 from . import binding as B
 from .memory import _DTYPES, _current_device, _overlap, _raw_stream, _refuse
@@ -28,6 +30,11 @@ _capturing = torch.cuda.is_current_stream_capturing
 
 # (input type, output type asked for): their codes, and the output's type
 _TYPES = {(a, b): (_DTYPES[a], _DTYPES[b or a], b or a) for a in _DTYPES for b in (None, *_DTYPES)}
+
+
+def _dual(t) -> bool:
+    """Whether a tensor carries a tangent of forward-mode differentiation."""
+    return _forward._current_level >= 0 and _forward.unpack_dual(t).tangent is not None
 
 
 def _up(n: int) -> int:
@@ -137,7 +144,7 @@ def _out(out, rows, cols, dtype, device):
     if out.dtype != dtype or out.shape != (rows, cols) or out.device != device or \
             (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
         _refuse(f"out: {dtype} [{rows}, {cols}], values of a row contiguous, rows apart, on {device}")
-    if out.requires_grad and torch.is_grad_enabled():
+    if (out.requires_grad and torch.is_grad_enabled()) or _dual(out):
         _refuse("out requires a gradient")
     return out
 
@@ -158,7 +165,7 @@ def quantize(x: torch.Tensor, format: str = "nvfp4", stats: bool = False, sums: 
     dtype, shape, strides = _DTYPES.get(x.dtype), x.shape, x.stride()
     if dtype is None or len(shape) != 2 or (strides[1] != 1 and shape[1] > 1) or not x.is_cuda:
         _refuse("x: bf16, fp16 or fp32 [rows, cols], values of a row contiguous, on a GPU")
-    if x.requires_grad and torch.is_grad_enabled():
+    if (x.requires_grad and torch.is_grad_enabled()) or _dual(x):
         _refuse("x requires a gradient, which 4-bit rows do not pass on")
     rows, cols = shape
     if out is None:
@@ -192,7 +199,7 @@ def product(x: Fp4Matrix, w: Fp4Matrix, bias: Optional[torch.Tensor] = None, dty
     if x.format != w.format or x.cols != w.cols or x.device != w.device:
         _refuse("product: one format, number of columns and device")
     if bias is not None and (bias.dtype is not _FP32 or bias.shape != (w.rows,) or not bias.is_contiguous() or
-                             bias.device != w.device or (bias.requires_grad and torch.is_grad_enabled())):
+                             bias.device != w.device or (bias.requires_grad and torch.is_grad_enabled()) or _dual(bias)):
         _refuse("bias: contiguous fp32 [w.rows], without a gradient, on the matrices' device")
     if normalized and (x.mean is None or w.sums is None):
         _refuse("normalized: x quantised with stats=True, w with sums=True")
@@ -219,14 +226,16 @@ class Fp4Linear:
 
     def __init__(self, weight, bias: Optional[torch.Tensor] = None, format: str = "nvfp4"):
         if not isinstance(weight, Fp4Matrix):
+            if _dual(weight):
+                _refuse("weight: without a tangent")
             weight = quantize(weight.detach(), format, sums=True)
         elif weight.format != format:
             _refuse("weight: an Fp4Matrix of the format")
         self.weight, self.format = weight, format
         self.cols, self.outs = weight.cols, weight.rows
         if bias is not None:
-            if bias.shape != (self.outs,) or bias.device != weight.device:
-                _refuse("bias: [outs] on the weight's device")
+            if bias.shape != (self.outs,) or bias.device != weight.device or _dual(bias):
+                _refuse("bias: [outs] on the weight's device, without a tangent")
             bias = bias.detach().to(_FP32).contiguous()
         self.bias = bias
         self._bias = None if bias is None else bias.data_ptr()
@@ -242,7 +251,7 @@ class Fp4Linear:
             _refuse("inputs and outputs: bf16, fp16 or fp32")
         if x.get_device() != self._index or not shape or shape[-1] != self.cols:
             _refuse(f"x: [..., {self.cols}] on the weight's device")
-        if x.requires_grad and torch.is_grad_enabled():
+        if (x.requires_grad and torch.is_grad_enabled()) or _dual(x):
             _refuse("x requires a gradient, which a 4-bit layer does not pass on")
         rows = x if len(shape) == 2 else x.reshape(-1, self.cols)
         stride, step = rows.stride()

@@ -1,6 +1,7 @@
 """Calls of the 4-bit operators as programs make them: reports, captures, streams, arguments that change or are refused."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from structured_decision_model_gb300 import binding as B, microscaled
 from structured_decision_model_gb300.binding import ClefError
@@ -120,3 +121,23 @@ def test_few_rows_in_one_launch_or_two(form):
         assert launches(lambda: layer(x))[0] == eager  # behind the capture as before it
         assert torch.equal(y, product(quantize(x, form), layer.weight))
         assert layer.device_status() == 0
+
+
+def test_tangents_are_refused():
+    """Dual tensors of forward-mode differentiation, which require no gradient, also where grad mode is off."""
+    x, w, bias = rows_of(4, 64, 1, torch.float32), rows_of(32, 64, 2), torch.randn(32, device="cuda")
+    layer = Fp4Linear(w, bias)
+    q, y = quantize(x), torch.empty(4, 32, device="cuda")
+    want = layer(x)
+    with forward_ad.dual_level():
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad):
+                for call in (lambda: layer(dual(x)), lambda: layer.normalized(dual(x)), lambda: quantize(dual(x)),
+                             lambda: product(q, layer.weight, dual(bias)), lambda: Fp4Linear(dual(w)), lambda: Fp4Linear(w, dual(bias)),
+                             lambda: product(q, layer.weight, dtype=torch.float32, out=dual(y)),
+                             lambda: layer(dual(x)[:2]), lambda: layer(dual(x.view(2, 2, 64)))):
+                    with pytest.raises(ClefError):
+                        call()
+        assert torch.equal(layer(x), want)  # the others go on as ever
+        assert torch.equal(layer(forward_ad.unpack_dual(dual(x)).primal), want)
