@@ -221,7 +221,8 @@ class Fp4Linear:
     """A linear layer of 4-bit weights: its inputs are quantised row by row as they come.
 
     ``weight`` [outs, cols] (bf16, fp16 or fp32; or an ``Fp4Matrix``, quantised with ``sums`` where
-    ``normalized`` is to be called) and ``bias`` [outs] (kept as it is where it is contiguous fp32) are laid out once.  For ``normalized`` the weight
+    ``normalized`` is to be called) and ``bias`` [outs] (kept as it is where it is contiguous fp32) are laid out once; ``bias``
+    may be set anew, the weight is one for the layer's life.  For ``normalized`` the weight
     holds the LayerNorm's weight (its columns times it) and the bias what the LayerNorm's bias brings."""
 
     def __init__(self, weight, bias: Optional[torch.Tensor] = None, format: str = "nvfp4"):
@@ -231,18 +232,30 @@ class Fp4Linear:
             weight = quantize(weight.detach(), format, sums=True)
         elif weight.format != format:
             _refuse("weight: an Fp4Matrix of the format")
-        self.weight, self.format = weight, format
+        self._weight, self.format = weight, format
         self.cols, self.outs = weight.cols, weight.rows
-        if bias is not None:
-            if bias.shape != (self.outs,) or bias.device != weight.device or _dual(bias):
-                _refuse("bias: [outs] on the weight's device, without a tangent")
-            bias = bias.detach().to(_FP32).contiguous()
-        self.bias = bias
-        self._bias = None if bias is None else bias.data_ptr()
-        self._flags = weight.flags.data_ptr()  # made here, outside of any later capture
         self._device, self._index = weight.device, weight._index
+        self.bias = bias
+        self._flags = weight.flags.data_ptr()  # made here, outside of any later capture
         self._lib, self._struct = B.load(), weight.struct
         self._scratch = {}  # scratch bytes of the calls that the layer has met
+
+    @property
+    def weight(self) -> Fp4Matrix:
+        return self._weight
+
+    @property
+    def bias(self) -> Optional[torch.Tensor]:
+        """fp32 [outs], or None.  May be set, but not for graphs that have been captured: those keep the old one's address."""
+        return self._bias_held
+
+    @bias.setter
+    def bias(self, bias: Optional[torch.Tensor]):
+        if bias is not None:
+            if bias.shape != (self.outs,) or bias.device != self._device or _dual(bias):
+                _refuse("bias: [outs] on the weight's device, without a tangent")
+            bias = bias.detach().to(_FP32).contiguous()
+        self._bias_held, self._bias = bias, None if bias is None else bias.data_ptr()
 
     def _run(self, x, dtype, normalized):
         """Outputs, means and rstds of x's rows (the latter None where not ``normalized``)."""
@@ -266,11 +279,11 @@ class Fp4Linear:
         y = torch.empty((n, self.outs), dtype=dtype, device=self._device)
         mean = rstd = mean_at = rstd_at = sums_at = None
         if normalized:
-            if self.weight.sums is None:
+            if self._weight.sums is None:
                 _refuse("normalized: the weight has no sums")
             mean = torch.empty(n, dtype=_FP32, device=self._device)
             rstd = torch.empty(n, dtype=_FP32, device=self._device)
-            mean_at, rstd_at, sums_at = mean.data_ptr(), rstd.data_ptr(), self.weight.sums.data_ptr()
+            mean_at, rstd_at, sums_at = mean.data_ptr(), rstd.data_ptr(), self._weight.sums.data_ptr()
         if n:
             at, scratch = rows.data_ptr(), None
             stride = stride if n > 1 else self.cols
@@ -306,4 +319,4 @@ class Fp4Linear:
 
     def device_status(self) -> int:
         """Waits for the current stream, reads and clears what the layer's products reported."""
-        return self.weight.device_status()
+        return self._weight.device_status()

@@ -141,3 +141,22 @@ def test_tangents_are_refused():
                         call()
         assert torch.equal(layer(x), want)  # the others go on as ever
         assert torch.equal(layer(forward_ad.unpack_dual(dual(x)).primal), want)
+
+
+def test_the_bias_may_be_set():
+    x, w, bias = rows_of(40, 64, 1), rows_of(32, 64, 2), torch.randn(32, device="cuda")
+    layer = Fp4Linear(w, bias)
+    plain, other = Fp4Linear(w), torch.randn(32, device="cuda").bfloat16()
+    assert layer.bias is not None and torch.equal(layer(x), Fp4Linear(w, bias)(x))
+    layer.bias = other
+    assert torch.equal(layer(x), Fp4Linear(w, other)(x)) and torch.equal(layer.bias, other.float())
+    layer.bias.zero_()
+    assert torch.equal(layer(x), plain(x))
+    layer.bias = None
+    assert layer.bias is None and torch.equal(layer(x), plain(x))
+    for bad in (bias[:31], bias.cpu(), bias[None]):
+        with pytest.raises(ClefError):
+            layer.bias = bad
+    assert torch.equal(layer(x), plain(x))
+    with pytest.raises(AttributeError):
+        layer.weight = plain.weight
