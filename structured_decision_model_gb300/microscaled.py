@@ -10,8 +10,9 @@ for the GPU but the first matrix on a device, whose words for reports are cleare
 matrix of weights); ``device_status`` does, and reports what the kernels met.  A value is kept as
 the nearest of 16 numbers times its block's scale: "mxfp4" (blocks of 32, a power of two)
 or "nvfp4" (blocks of 16, three bits behind the point, and a power of two for each row).
-Nothing here passes gradients on: tensors that require one are refused while grad mode is on, and dual
-tensors of forward mode always.
+Nothing here passes gradients on: inputs, outputs and a product's bias that require one are refused while grad mode
+is on, and dual tensors of forward mode always.  A layer's weight and bias are frozen: taken as numbers, also where they
+are parameters that require a gradient.
 """
 import threading
 from typing import Optional, Tuple
@@ -223,7 +224,8 @@ class Fp4Linear:
     ``weight`` [outs, cols] (bf16, fp16 or fp32; or an ``Fp4Matrix``, quantised with ``sums`` where
     ``normalized`` is to be called) and ``bias`` [outs] (kept as it is where it is contiguous fp32) are laid out once; ``bias``
     may be set anew, the weight is one for the layer's life.  For ``normalized`` the weight
-    holds the LayerNorm's weight (its columns times it) and the bias what the LayerNorm's bias brings."""
+    holds the LayerNorm's weight (its columns times it) and the bias what the LayerNorm's bias brings.
+    Both are frozen: parameters get no gradient through the layer."""
 
     def __init__(self, weight, bias: Optional[torch.Tensor] = None, format: str = "nvfp4"):
         if not isinstance(weight, Fp4Matrix):

@@ -160,3 +160,15 @@ def test_the_bias_may_be_set():
     assert torch.equal(layer(x), plain(x))
     with pytest.raises(AttributeError):
         layer.weight = plain.weight
+
+
+def test_parameters_are_taken_frozen():
+    """A trained layer's parameters: taken as numbers, with grad mode on too; what comes out requires no gradient."""
+    trained = torch.nn.Linear(64, 32, device="cuda")
+    x = rows_of(4, 64, 1, torch.float32)
+    layer = Fp4Linear(trained.weight, trained.bias)
+    y = layer(x)
+    assert not y.requires_grad and not layer.bias.requires_grad and trained.weight.requires_grad
+    assert torch.equal(y, Fp4Linear(trained.weight.detach().clone(), trained.bias.detach().clone())(x))
+    with pytest.raises(ClefError):
+        quantize(trained.weight)               # by itself it is an input
