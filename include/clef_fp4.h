@@ -16,6 +16,9 @@
  *   CLEF_NVFP4  blocks of 16, scale r * e4m3(amax / (6 r)), where r = 2^(floor(log2 a) - 10),
  *               not below 2^-126, a the row's largest finite size: a row stands by itself,
  *               whatever other rows hold
+ * An nvfp4 scale may round up, so that a row's largest value stands for up to 18 / 17 of itself: finite values that
+ * close to a type's largest (65504 in fp16 stands for 67584) read back as infinity in that type.  The largest
+ * number of an mxfp4 block is 1.5 times the power of two at or below its largest size, which every type holds.
  * A block that holds an infinity or a NaN reads as NaN, and so does every product of its row;
  * other rows and blocks are as without it.
  *

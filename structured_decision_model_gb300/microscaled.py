@@ -118,7 +118,9 @@ class Fp4Matrix:
         return self._flags
 
     def dequantize(self, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """What the rows stand for, [rows, cols] in ``dtype`` (bf16, fp16 or fp32), rounded once."""
+        """What the rows stand for, [rows, cols] in ``dtype`` (bf16, fp16 or fp32), rounded once.
+
+        nvfp4 rows may stand for up to 18 / 17 of their largest value, which passes the type's range next to its end."""
         given = out is not None
         out = _out(out, self.rows, self.cols, dtype, self.device)
         if given and _overlap(out, self.data):

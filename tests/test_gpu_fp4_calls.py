@@ -3,6 +3,7 @@ import pytest
 import torch
 from torch.autograd import forward_ad
 
+from fp4_support import kept
 from structured_decision_model_gb300 import binding as B, microscaled
 from structured_decision_model_gb300.binding import ClefError
 from structured_decision_model_gb300.microscaled import Fp4Linear, Fp4Matrix, product, quantize
@@ -172,3 +173,19 @@ def test_parameters_are_taken_frozen():
     assert torch.equal(y, Fp4Linear(trained.weight.detach().clone(), trained.bias.detach().clone())(x))
     with pytest.raises(ClefError):
         quantize(trained.weight)               # by itself it is an input
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_rows_at_the_end_of_their_type(dtype):
+    """What a row's largest value stands for may pass the type's range: rounded once, to infinity in that type."""
+    most = torch.finfo(dtype).max
+    x = torch.tensor([[most, -most] + [most / 8] * 30, [most / 2, most / 4] + [1.0] * 30], dtype=dtype, device="cuda")
+    for form in ("mxfp4", "nvfp4"):
+        m = quantize(x, form)
+        want = torch.from_numpy(kept(x.double().cpu().numpy(), form)[3])
+        assert torch.equal(m.dequantize(dtype).cpu(), want.to(dtype))
+        assert want.abs().max() <= most * 18 / 17 and m.dequantize(dtype)[1].isfinite().all()
+        if form == "mxfp4":
+            assert m.dequantize(dtype).isfinite().all()
+    if dtype == torch.float16:
+        assert m.dequantize(torch.float32)[0, 0] == 67584 and m.dequantize(dtype)[0, 0].isinf()
