@@ -1,10 +1,12 @@
-"""Calls of the head over 4 bits that are refused, or that are made without a check."""
+"""Calls of the head over 4 bits that are refused, or that are made without a check, and the wide head."""
 import pytest
 import torch
 
-from gpu_support import device_inputs, schema_of
+import synth
+from gpu_support import LOGIT_TOL, compare, device_inputs, run_oracle, schema_of
 from structured_decision_model_gb300 import binding as B
-from test_gpu_fp4_head import SHAPES, batch, fp4_head
+from structured_decision_model_gb300.head import ClefHead
+from test_gpu_fp4_head import SHAPES, batch, forward, fp4_head, kept_memory, outputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +38,25 @@ def test_forward_without_a_check_returns():
     assert (out.logits == 9).all()
     with pytest.raises(B.ClefError):
         head.forward(schema_of(bt), hidden.view(-1)[1:], ids, lex, out=out)
+
+
+@pytest.mark.parametrize("form", ["mxfp4", "nvfp4"])
+def test_the_5120_wide_head(form, kept_memory):
+    """Twenty K tiles a row, ragged records, chunks: the same acceptance."""
+    shape = synth.HeadShape(H=5120)
+    w = synth.make_weights(shape, 0)
+    head = ClefHead(w, shape.H, shape.D, shape.heads, shape.F, shape.n_route, shape.n_joint, shape.vocab, memory_format=form)
+    spec = synth.BatchSpec(name="wide", B=3, H=shape.H, vocab=shape.vocab, lengths=[260, 700, 260], questions=(2, 4), options=(2, 5))
+    bt = synth.make_batch(spec, seed=83)
+    hidden, ids, lex = device_inputs(bt, shape.vocab)
+    got = forward(head, bt, hidden, ids, lex)
+    kept_memory(form)
+    compare(got, run_oracle(w, shape, bt), bt)
+    sch = schema_of(bt)
+    head.stream_begin(sch)
+    for b, n in enumerate(bt.lengths):
+        for r in range(0, int(n), 128):
+            head.stream_rows(sch, hidden, b, r, min(128, int(n) - r))
+    streamed = outputs(head.stream_finish(sch, hidden, ids, lex))
+    assert head.device_status() == 0
+    assert abs(streamed["logits"] - got["logits"]).max() <= LOGIT_TOL
