@@ -113,6 +113,45 @@ struct RowSums {
     }
 };
 
+// Mean and 1 / sqrt(variance + eps) of a row from its distances, where its first mean and variance (of part 0) want them
+// (of two rows in a warp, maybe one does).  `spread` holds the first mean for the warps that share the row; the sums in `all`
+// have been read.  Rare and long: kept out of the kernel, which has no register to spare (131072 x 4096 bf16 to nvfp4 with
+// statistics: 256 us, 271 with this within it; where every row wants it 413).
+template <int DT, bool VEC, int STEPS, int LANES>
+__device__ __noinline__ float2 statistics_apart(const void* x, int64_t row0, int cols, float inv_cols, Share w, int lane,
+                                                uint64_t (*all)[32], Spread* spread, uint32_t* own, float2 first) {
+    const bool shared = LANES == 32 && !w.alone(), far = w.part == 0 && far_from_zero(first.x, first.y);
+    const int pieces = (cols + 511) / 512;
+    RowSums<LANES> apart{all};
+    Spread from = spread_of(first.x, first.y);
+    bool wanted = far;  // of the row's first warp
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+        if (shared) from = *spread;  // behind a barrier
+        apart.own = 0;
+#pragma unroll 1
+        for (int i = 0; i < STEPS; ++i) {
+            const int piece = (i << w.shift) + w.part, col0 = piece * 512;
+            if (LANES == 32 && col0 >= cols) continue;
+            const Raw<DT> again = load16<DT, VEC, LANES>(x, row0, col0, cols, lane, own);
+            apart.add(moments_apart<DT>(again, from, cols - (col0 + lane * 16)), w, piece, lane);
+        }
+        if (shared) row_sync(w);
+        if (w.part == 0) {
+            const float2 f = apart.get(w, pieces, lane);
+            const float rest = f.x * inv_cols, square = f.y * inv_cols;
+            if (wanted) {
+                first.y = variance_apart(rest, square);
+                if (turn == 0) first.x = from.mean = corrected_mean(from, rest);
+            }
+            wanted = wanted && mostly_rounding(rest, square);
+            if (shared && lane == 0) *spread = from;
+        }
+        if (turn == 0 && !(shared ? row_any(wanted, w) : __any_sync(0xffffffffu, wanted))) break;
+    }
+    return make_float2(first.x, rstd_of(first.y, from.by));
+}
+
 // What else is asked for: the statistics; sums of what is kept, and maybe the statistics.
 enum { kNothing, kStats, kSums };
 
@@ -204,49 +243,26 @@ __global__ void __launch_bounds__(kThreads, DT == CLEF_FP32 && STEPS == 4 ? 2 : 
     if (stats) {
         // The row's first warp adds up; the others wait for what it finds only where that is far from zero.
         if (LANES == 32 && !w.alone()) row_sync(w);
-        float mean = 0.f, var = 0.f;
-        Spread from{0.f, 1.f};
+        float2 found = make_float2(0.f, 0.f);  // mean and variance, then mean and 1 / sqrt(variance + eps)
         if (part == 0) {
             const float2 f = both.get(w, pieces, lane);
-            mean = f.x * a.inv_cols;
-            var = f.y * a.inv_cols - mean * mean;
-            from = spread_of(mean, var);
-            if (LANES == 32 && !w.alone() && lane == 0) spreads[warp] = from;
+            found.x = f.x * a.inv_cols;
+            found.y = f.y * a.inv_cols - found.x * found.x;
+            if (LANES == 32 && !w.alone() && lane == 0) spreads[warp] = spread_of(found.x, found.y);
         }
         // A mean square less a mean's loses as many bits as the mean exceeds the spread: such rows, and those
-        // whose squares pass fp32, are read twice more, for their mean and for their variance.
-        const bool far = mine && part == 0 && far_from_zero(mean, var);
+        // whose squares pass fp32, are read once or twice more.
+        const bool far = mine && part == 0 && far_from_zero(found.x, found.y);
         if (LANES < 32 || w.alone() ? __any_sync(0xffffffffu, far) : row_any(far, w)) {
-            RowSums<LANES> apart{both.all};  // the sums have been read
-#pragma unroll 1
-            for (int turn = 0; turn < 2; ++turn) {
-                if (LANES == 32 && !w.alone()) from = spreads[w.slot << shift];  // behind a barrier
-                apart.own = 0;
-#pragma unroll 1
-                for (int i = 0; i < STEPS; ++i) {
-                    if (LANES == 32 && ((i << shift) + part) * 512 >= padded) continue;
-                    const int col0 = ((i << shift) + part) * 512;
-                    uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
-                    const Raw<DT> again = load16<DT, VEC, LANES>(a.x, mine ? row0 : 0, col0, mine ? a.cols : 0, lane, own);
-                    apart.add(moments_apart<DT>(again, from, a.cols - (col0 + lane * 16)), w, (i << shift) + part, lane);
-                }
-                if (LANES == 32 && !w.alone()) row_sync(w);
-                if (part == 0) {
-                    const float2 f = apart.get(w, pieces, lane);
-                    const float rest = f.x * a.inv_cols;
-                    if (turn == 0) {
-                        if (far) mean = from.mean = corrected_mean(from, rest);
-                        if (LANES == 32 && !w.alone() && lane == 0) spreads[warp] = from;
-                    } else if (far) {
-                        var = variance_apart(rest, f.y * a.inv_cols);
-                    }
-                }
-                if (LANES == 32 && !w.alone() && turn == 0) row_sync(w);
-            }
+            uint32_t* own = stage[VEC ? 0 : warp] + (VEC || LANES == 32 ? 0 : (threadIdx.x & 16) * Raw<DT>::kWords);
+            found = statistics_apart<DT, VEC, STEPS, LANES>(a.x, mine ? row0 : 0, mine ? a.cols : 0, a.inv_cols, w, lane, both.all,
+                                                            &spreads[LANES == 32 ? w.slot << shift : 0], own, found);
+        } else {
+            found.y = rstd_of(found.y, 1.f);
         }
         if (mine && part == 0 && lane == 0) {
-            a.mean[row] = mean;
-            a.rstd[row] = rstd_of(var, from.by);
+            a.mean[row] = found.x;
+            a.rstd[row] = found.y;
         }
     }
     if (sums) {

@@ -309,10 +309,11 @@ __device__ __forceinline__ uint64_t moments_apart(const Raw<DT>& raw, const Spre
     return pair_of(a.x + a.y, b.x + b.y);
 }
 
-// Distances twice: what is left over of the first ones' mean corrects the mean to within half a step, without which a
-// mean of 10^5 is wrong by 0.008 and the variance of a constant row by the square of that, more than 1e-5.
-// The second ones' mean square then holds the variance to all but a bit, since a row that is not constant spreads over at
-// least a step.  (Means and variances that are no numbers stay as they are.)
+// What the distances' mean is corrects the first mean to within half a step, and the distances' mean square less its
+// square is the variance, without the square of the first mean's rounding (0.008 at a mean of 10^5: more than 1e-5 in the
+// variance of a constant row).  Where that square is most of it, distances from the corrected mean are taken: a row that
+// is not constant spreads over at least a step, so that those lose a bit at most.
+// (Means and variances that are no numbers stay as they are.)
 __device__ __forceinline__ float corrected_mean(const Spread& from, float rest) {
     const float m = fmaf(rest, 1.f / from.by, from.mean);
     return fabsf(m) < INFINITY ? m : from.mean;
@@ -320,5 +321,7 @@ __device__ __forceinline__ float corrected_mean(const Spread& from, float rest) 
 __device__ __forceinline__ float variance_apart(float rest, float square) {
     return square < INFINITY ? fmaxf(fmaf(-rest, rest, square), 0.f) : square;
 }
+
+__device__ __forceinline__ bool mostly_rounding(float rest, float square) { return !(4.f * rest * rest <= square); }
 
 }  // namespace clef

@@ -356,9 +356,10 @@ __device__ __forceinline__ void few_rows(const Fp4ProductArgs& args, uint8_t* sm
                             d += v.x;
                             q += v.y;
                         }
-                        const float rest = warp_sum(d) * args.inv_cols;
+                        const float rest = warp_sum(d) * args.inv_cols, square = warp_sum(q) * args.inv_cols;
+                        var = variance_apart(rest, square);
                         if (turn == 0) mean = from.mean = corrected_mean(from, rest);
-                        else var = variance_apart(rest, warp_sum(q) * args.inv_cols);
+                        if (!mostly_rounding(rest, square)) break;
                     }
                 }
                 const float rstd = rstd_of(var, from.by);

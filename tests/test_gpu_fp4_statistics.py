@@ -1,7 +1,7 @@
 """Statistics of rows whose mean is large against their spread, or whose squares pass fp32's range, in 64 bits.
 
-Such rows are read twice more: once for the mean of what lies behind the first mean, which gives the mean to its
-last bit, and once for the spread around that.
+Such rows are read again: the mean of what lies behind the first mean gives the mean to its last bit, and where
+that is most of the spread, they are read once more for the spread around it.
 """
 import pytest
 import torch
