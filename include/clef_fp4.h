@@ -105,6 +105,14 @@ CLEF_API int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, 
                              float* mean, float* rstd, void* scratch, size_t scratch_bytes, int32_t* flags,
                              void* stream);
 
+/* Self-test of the products' wait limits: clef_fp4_linear without bias and sums whose product never loads the last
+ * 256 columns (or fewer, where the row ends), so that the waits for them run out after limit_ns (1 us .. 100 ms)
+ * each.  The kernels then report CLEF_ERR_DEVICE_TIMEOUT in `flags` and return; out is left as it was, or in part
+ * written, and the context stays usable. */
+CLEF_API int clef_fp4_selftest_timeout(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
+                                       int32_t dtype, void* out, int64_t row_stride, void* scratch, size_t scratch_bytes,
+                                       int64_t limit_ns, int32_t* flags, void* stream);
+
 /* ---- the head with its memory K/V projection in 4 bits ---- */
 
 /* The K/V weights of every routing layer (with the memory LayerNorm's weight, as clef_prepare_weights left

@@ -27,6 +27,7 @@ EXPORTED = [
     "clef_stream_finish_memory", "clef_fp4_size", "clef_fp4_quantize", "clef_fp4_dequantize", "clef_fp4_product",
     "clef_fp4_linear_scratch", "clef_fp4_linear", "clef_fp4_memory_weights", "clef_stream_rows_fp4_scratch",
     "clef_head_forward_fp4_scratch", "clef_stream_rows_fp4", "clef_head_forward_fp4",
+    "clef_fp4_selftest_timeout",
 ]
 BF16, FP16, FP32 = 0, 1, 2   # clef_dtype
 CACHE_MAX_REQUESTS = 1024
@@ -126,6 +127,7 @@ def load():
     lib.clef_fp4_product.argtypes = [fp4, fp4, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
     lib.clef_fp4_linear_scratch.argtypes = [_i32] * 8 + [ctypes.POINTER(_sz)]
     lib.clef_fp4_linear.argtypes = [fp4, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _vp]
+    lib.clef_fp4_selftest_timeout.argtypes = [fp4, _i32, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _sz, _i64, _vp, _vp]
     cfg, schema = ctypes.POINTER(ClefConfig), ctypes.POINTER(ClefSchema)
     lib.clef_fp4_memory_weights.argtypes = [cfg, _vp, fp4, _vp, _vp]
     lib.clef_stream_rows_fp4_scratch.argtypes = [cfg, _i32, _i32, ctypes.POINTER(_sz)]
@@ -384,6 +386,12 @@ def clef_fp4_linear(w: ClefFp4, x_dtype, x_ptr, x_stride, rows, bias_ptr, sums_p
                     rstd_ptr, scratch_ptr, scratch_bytes, flags_ptr, stream=0):
     _check(load().clef_fp4_linear(w, x_dtype, x_ptr, x_stride, rows, bias_ptr, sums_ptr, dtype, out_ptr, row_stride,
                                   mean_ptr, rstd_ptr, scratch_ptr, scratch_bytes, flags_ptr, stream), "clef_fp4_linear")
+
+
+def clef_fp4_selftest_timeout(w: ClefFp4, x_dtype, x_ptr, x_stride, rows, dtype, out_ptr, row_stride, scratch_ptr,
+                              scratch_bytes, limit_ns, flags_ptr, stream=0):
+    _check(load().clef_fp4_selftest_timeout(w, x_dtype, x_ptr, x_stride, rows, dtype, out_ptr, row_stride, scratch_ptr,
+                                            scratch_bytes, limit_ns, flags_ptr, stream), "clef_fp4_selftest_timeout")
 
 
 def clef_fp4_memory_weights(cfg, prepared_ptr, w: ClefFp4, sums_ptr, stream=0):

@@ -1104,13 +1104,13 @@ int check_fp4_rows(const void* prepared, const void* hidden, int32_t dtype, cons
 }
 
 // K/V and statistics of `rows` rows of `hidden` from padded row `from` on, into compact rows `to` on; or only the checks.
-int project_fp4(bool launch, const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,
+int project_fp4(Fp4Call call, const clef_config* cfg, const void* prepared, const clef_fp4* w, const float* sums,
                 const clef_schema* schema, const WsLayout& L, const void* hidden, int32_t dtype, int64_t from, int64_t to,
                 int64_t rows, void* workspace, void* scratch, size_t scratch_bytes, void* stream) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const PreparedLayout PL(cfg);
     const int64_t NKV = int64_t(2) * cfg->n_route * cfg->width;
-    return fp4_linear(launch, w, dtype, static_cast<const uint16_t*>(hidden) + from * schema->row_stride, schema->row_stride,
+    return fp4_linear(call, 0, w, dtype, static_cast<const uint16_t*>(hidden) + from * schema->row_stride, schema->row_stride,
                       int32_t(rows), reinterpret_cast<const float*>(static_cast<const uint8_t*>(prepared) + PL.bkv), sums,
                       CLEF_BF16, reinterpret_cast<uint16_t*>(ws + L.kv) + to * NKV, NKV,
                       reinterpret_cast<float*>(ws + L.mu) + to, reinterpret_cast<float*>(ws + L.rstd) + to, scratch,
@@ -1175,7 +1175,7 @@ int clef_stream_rows_fp4(const clef_config* cfg, const void* prepared, const cle
         int64_t(row0) + n_rows > schema->lengths[record])
         return CLEF_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < lp->total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
-    return project_fp4(true, cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype, int64_t(record) * schema->Lpad + row0,
+    return project_fp4(kFp4Run, cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype, int64_t(record) * schema->Lpad + row0,
                        pp->blob[pp->rec_row_off + record] + int64_t(row0), n_rows, workspace, scratch, scratch_bytes,
                        stream);
 }
@@ -1203,11 +1203,11 @@ int clef_head_forward_fp4(const clef_config* cfg, const void* const* weights, co
     v = cached_plan(cfg, schema, &pp, &lp);
     if (v != CLEF_OK) return v;
     if (workspace_bytes < lp->total) return CLEF_ERR_WORKSPACE_TOO_SMALL;
-    auto project = [&](bool launch) {
+    auto project = [&](Fp4Call call) {
         for (int b = 0; b < schema->B;) {
             int64_t rows = 0;
             const int e = fp4_run(schema, *pp, b, &rows);
-            const int s = project_fp4(launch, cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype,
+            const int s = project_fp4(call, cfg, prepared, w, sums, schema, *lp, hidden, hidden_dtype,
                                       int64_t(b) * schema->Lpad, pp->blob[pp->rec_row_off + b], rows, workspace, scratch,
                                       scratch_bytes, stream);
             if (s != CLEF_OK) return s;
@@ -1215,13 +1215,13 @@ int clef_head_forward_fp4(const clef_config* cfg, const void* const* weights, co
         }
         return int(CLEF_OK);
     };
-    v = project(false);  // every refusal comes before the first launch
+    v = project(kFp4Check);  // every refusal comes before the first launch
     if (v != CLEF_OK) return v;
     v = clef_stream_begin(cfg, schema, workspace, workspace_bytes, stream);
     if (v != CLEF_OK) return v;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CK(mark(debug, 0, st));
-    v = project(true);
+    v = project(kFp4Run);
     if (v != CLEF_OK) return v;
     CK(mark(debug, 1, st));
     return forward_impl(cfg, weights, prepared, schema, static_cast<const uint16_t*>(hidden), token_ids, lexical, logits,

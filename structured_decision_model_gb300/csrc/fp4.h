@@ -65,6 +65,8 @@ struct Fp4ProductArgs {
     int cols;
     float inv_cols;
     int w_settled;         // no kernel that may still run on the stream writes w: it may be read ahead of them
+    uint64_t wait_ns;      // limit of a wait
+    int withheld;          // 1: the last K tile is never loaded, so that the waits for it run out (the self-test)
     int bulk;              // 16-bit outputs: rows start and end on 16 bytes, so that TMA can store them
 };
 cudaError_t launch_fp4_product(const clef_fp4& x, const clef_fp4& w, const Fp4ProductArgs& a, int dtype,
@@ -78,8 +80,10 @@ bool fp4_few_rows(int format, int x_dtype, int rows, int cols, bool normalized);
 bool fp4_few_pays(int format, int x_dtype, int rows, int cols, int outs, bool normalized, bool captured);
 cudaError_t launch_fp4_few(const clef_fp4& w, const Fp4ProductArgs& a, int x_dtype, int dtype, cudaStream_t s);
 
-// clef_fp4_linear, or only the checks of its arguments.
-int fp4_linear(bool launch, const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
+// clef_fp4_linear; only the checks of its arguments; or with a product whose last K tile is withheld and whose waits end
+// after starve_ns.
+enum Fp4Call { kFp4Check, kFp4Run, kFp4Starve };
+int fp4_linear(Fp4Call call, uint64_t starve_ns, const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
                const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride, float* mean, float* rstd,
                void* scratch, size_t scratch_bytes, int32_t* flags, void* stream);
 

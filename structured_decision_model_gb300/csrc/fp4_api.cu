@@ -102,6 +102,7 @@ Fp4ProductArgs product_args(const clef_fp4& x, const clef_fp4& w, const float* b
     a.paired = dtype != CLEF_FP32 && row_stride % 2 == 0 && w.rows % 2 == 0 && !misaligned(out, 4);
     // TMA writes whole 16-byte pieces of a row, also where the row ends inside one
     a.bulk = dtype != CLEF_FP32 && row_stride % 8 == 0 && w.rows % 8 == 0 && !misaligned(out, 16);
+    a.wait_ns = kWaitLimitNs;
     a.w_settled = w_settled;
     a.cols = x.cols;
     a.inv_cols = 1.f / float(x.cols);
@@ -130,7 +131,7 @@ struct Scratch {
 
 namespace clef {
 
-int fp4_linear(bool launch, const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
+int fp4_linear(Fp4Call call, uint64_t starve_ns, const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
                const float* bias, const float* sums, int32_t dtype, void* out, int64_t row_stride, float* mean, float* rstd,
                void* scratch, size_t scratch_bytes, int32_t* flags, void* stream) {
     int st = check_matrix(w);
@@ -158,9 +159,13 @@ int fp4_linear(bool launch, const clef_fp4* w, int32_t x_dtype, const void* x, i
     if (to.meets(in) || to.meets(space) || space.meets(Run(mean, m4)) || space.meets(Run(rstd, m4)) ||
         Run(mean, m4).meets(Run(rstd, m4)))
         return CLEF_ERR_INVALID_ARGUMENT;
-    if (!launch) return CLEF_OK;
+    if (call == kFp4Check) return CLEF_OK;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     Fp4ProductArgs p = product_args(q, *w, bias, mean, rstd, sums, dtype, out, row_stride, flags, true);
+    if (call == kFp4Starve) {
+        p.wait_ns = starve_ns;
+        p.withheld = 1;
+    }
     if (few) {  // one launch
         p.x = x;
         p.x_stride = x_stride;
@@ -246,8 +251,16 @@ int clef_fp4_linear_scratch(int32_t format, int32_t x_dtype, int32_t rows, int32
 int clef_fp4_linear(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows, const float* bias,
                     const float* sums, int32_t dtype, void* out, int64_t row_stride, float* mean, float* rstd,
                     void* scratch, size_t scratch_bytes, int32_t* flags, void* stream) {
-    return fp4_linear(true, w, x_dtype, x, x_stride, rows, bias, sums, dtype, out, row_stride, mean, rstd, scratch,
+    return fp4_linear(kFp4Run, 0, w, x_dtype, x, x_stride, rows, bias, sums, dtype, out, row_stride, mean, rstd, scratch,
                       scratch_bytes, flags, stream);
+}
+
+int clef_fp4_selftest_timeout(const clef_fp4* w, int32_t x_dtype, const void* x, int64_t x_stride, int32_t rows,
+                              int32_t dtype, void* out, int64_t row_stride, void* scratch, size_t scratch_bytes,
+                              int64_t limit_ns, int32_t* flags, void* stream) {
+    if (limit_ns < 1000 || limit_ns > 100000000) return CLEF_ERR_INVALID_ARGUMENT;
+    return fp4_linear(kFp4Starve, uint64_t(limit_ns), w, x_dtype, x, x_stride, rows, nullptr, nullptr, dtype, out, row_stride,
+                      nullptr, nullptr, scratch, scratch_bytes, flags, stream);
 }
 
 }  // extern "C"

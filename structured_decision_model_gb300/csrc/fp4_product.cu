@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
         for (int t = first; ok && t < n_tiles; t += stride) {
             const int w0 = (t % n_wt) * 2 + int(rank), x0 = (t / n_wt) * 2;  // 128-row groups: own rows of w, x's first
             int sw = w0 * args.kgroups, sx = x0 * args.kgroups;              // scale groups of the K tile
-            for (int kt = 0; kt < ktiles; ++kt, ++i) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags));
+            for (int kt = 0; kt < ktiles - args.withheld; ++kt, ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags, args.wait_ns));
                 if (!ok) break;
                 uint8_t* st = smem + s * C::STAGE_STRIDE;
                 uint8_t* sc = st + kWBytes + C::X_BYTES;
@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
                     phase ^= 1u;
                 }
             }
+            if (args.withheld) break;
         }
         if (!ok && rank == 0) {  // let every copy that this CTA's barriers count land before it goes
             for (int j = i < C::STAGES ? 0 : i - C::STAGES; j < i; ++j)
@@ -153,13 +154,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
             for (int t = first; ok && t < n_tiles; t += stride, ++j) {
                 const uint32_t acc = tmem + (j & 1 ? C::ACC1 : 0);
                 if (j > 0) {  // the last tile's shared columns: whatever came before it has been read too
-                    ok = mbar_wait_bounded(handed, uint32_t(j - 1) & 1u, abort_flag, args.flags, kWaitLimitNs, true);
+                    ok = mbar_wait_bounded(handed, uint32_t(j - 1) & 1u, abort_flag, args.flags, args.wait_ns, true);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
                 }
                 for (int kt = 0; kt < ktiles; ++kt) {
-                    ok = mbar_wait_bounded(&full[s], phase, abort_flag, args.flags);
+                    ok = mbar_wait_bounded(&full[s], phase, abort_flag, args.flags, args.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -226,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_pair_kernel(const __grid_cons
             const int m0 = t / n_wt * C::ROWS, n0 = t % n_wt * 2 * kWRows + int(rank) * kWRows;
             float* mine = terms + (j & 1) * 2 * C::ROWS;
             put_row_terms(mine, tid, row);
-            const bool got = mbar_wait_bounded(&tfull[j & 1], uint32_t(j >> 1) & 1u, abort_flag, args.flags);
+            const bool got = mbar_wait_bounded(&tfull[j & 1], uint32_t(j >> 1) & 1u, abort_flag, args.flags,
+                                               args.wait_ns);
             tc_fence_after();
             // The accumulators share the last 64 columns of the first and the first 64 of the second: the
             // warps whose half they lie in take them and say so, the others only that they are done with the

@@ -381,8 +381,8 @@ __device__ __forceinline__ void few_rows(const Fp4ProductArgs& args, uint8_t* sm
         const int tiles = min(2, kt1 - kt), which = lane >> 4, col = kt * kFp4Tile + lane * 16;
         const int s1 = s + 1 == C::STAGES ? 0 : s + 1;
         const uint32_t phase1 = s1 == 0 ? phase ^ 1u : phase;
-        bool ok = mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags);
-        if (tiles == 2) ok = mbar_wait_bounded(&empty[s1], phase1, abort_flag, args.flags) && ok;
+        bool ok = mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags, args.wait_ns);
+        if (tiles == 2) ok = mbar_wait_bounded(&empty[s1], phase1, abort_flag, args.flags, args.wait_ns) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
         uint8_t* st = smem + (which ? s1 : s) * C::STAGE + kWBytes;
         const int v = (lane & 15) * 16;  // the first value's place in its K tile
@@ -489,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
         // The first K tiles' stages wait for nobody: their copies are asked for under one election.  Converged, the warp
         // keeps addresses in uniform registers (511 rows x 4096 x 16384 23.9 -> 22.9 us, 511 x 2560 x 640 4.6 -> 4.5;
         // an election for each of the first K tiles as well: 23.2 and 4.6).
-        const int free = min(C::STAGES, kt1 - kt0);
+        const int last = kt1 - args.withheld;  // the K tiles that are loaded end here
+        const int free = min(C::STAGES, last - kt0);
         if (elect_one() && args.w_settled) {
             for (int k = 0; k < free; ++k) load_w(kt0 + k, k);
         }
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
         bool ok = true;
         int i = free, s = 0;  // stages filled so far, and the next one
         uint32_t phase = 0;
-        for (int kt = kt0 + free; kt < kt1; ++kt, ++i) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags));
+        for (int kt = kt0 + free; kt < last; ++kt, ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], phase, abort_flag, args.flags, args.wait_ns));
             if (!ok) break;
             if (elect_one()) {
                 load_w(kt, s);
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
         int s = 0;
         uint32_t phase = 0;
         for (int kt = kt0; kt < kt1; ++kt) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], phase, abort_flag, args.flags));
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], phase, abort_flag, args.flags, args.wait_ns));
             if (!ok) break;
             tc_fence_after();
             const uint64_t da = d0 + uint64_t(s * (C::STAGE >> 4)), db = da + (kWBytes >> 4);
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_tile_kernel(const __grid_cons
         } else {
             few_rows<FMT, XT, C>(args, smem, terms, tops, full, empty, kt0, kt1, warp - 2, lane, abort_flag);
         }
-        bool ok = mbar_wait_bounded(done, 0, abort_flag, args.flags) && !*abort_flag;
+        bool ok = mbar_wait_bounded(done, 0, abort_flag, args.flags, args.wait_ns) && !*abort_flag;
         ok = epilogue_agrees(ok);  // the row terms are there too
         tc_fence_after();
         const int rows = min(BN, args.M - xt * BN);

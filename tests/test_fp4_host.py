@@ -193,3 +193,11 @@ def test_head_refusals_come_before_the_first_launch():
                  (3, matrix(**dict(over, row_scale=None))), (4, at[4] + 2), (17, at[6]), (17, at[5]), (6, at[7])):
         refused(1, B.clef_head_forward_fp4, *changed(good, i, v))
     refused(3, B.clef_head_forward_fp4, *changed(good, 3, matrix(form=2, **over)))
+
+
+def test_selftest_refusals():
+    w = matrix(at=4 * P, rows=20)
+    size = B.clef_fp4_linear_scratch(B.NVFP4, B.BF16, 10, 100)
+    good = [w, B.BF16, 8 * P, 100, 10, B.BF16, 9 * P, 20, 20 * P, size, 1_000_000, 16 * P]
+    for i, v in ((2, None), (6, None), (8, None), (10, 999), (10, 100_000_001), (11, None)):
+        refused(1, B.clef_fp4_selftest_timeout, *changed(good, i, v))

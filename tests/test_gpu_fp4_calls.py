@@ -189,3 +189,28 @@ def test_rows_at_the_end_of_their_type(dtype):
             assert m.dequantize(dtype).isfinite().all()
     if dtype == torch.float16:
         assert m.dequantize(torch.float32)[0, 0] == 67584 and m.dequantize(dtype)[0, 0].isinf()
+
+
+@pytest.mark.parametrize("form", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 4096), (8, 40, 64), (20, 300, 4096), (100, 300, 1000), (40, 40, 64), (5000, 1100, 1000)])
+def test_waits_of_the_products_run_out(form, m, n, k):
+    """A K tile that never comes: few rows, tiles (in parts of K, and whole) and pairs report it and return; what follows
+    is as before."""
+    x, layer = rows_of(m, k, 1), Fp4Linear(rows_of(n, k, 2), None, form)
+    want = layer(x)
+    assert layer.device_status() == 0
+    few = m <= 8
+    size = 0 if few else B.clef_fp4_linear_scratch(layer.weight.struct.format, B.BF16, m, k)
+    space, out = torch.empty(max(size, 256), dtype=torch.uint8, device="cuda"), torch.full((m, n), 9.0, dtype=torch.bfloat16, device="cuda")
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    B.clef_fp4_selftest_timeout(layer.weight.struct, B.BF16, x.data_ptr(), k, m, B.BF16, out.data_ptr(), n,
+                                None if few else space.data_ptr(), size, 5_000_000, layer.weight.flags.data_ptr(),
+                                torch.cuda.current_stream().cuda_stream)
+    end.record()
+    assert layer.device_status() == 6 and layer.device_status() == 0
+    assert begin.elapsed_time(end) >= 5  # ms: a wait did run out
+    assert (out == 9).all()              # every tile gave up
+    for _ in range(3):
+        assert torch.equal(layer(x), want)
+    assert layer.device_status() == 0
