@@ -26,7 +26,7 @@ from .memory import _DTYPES, _current_device, _overlap, _raw_stream, _refuse
 FORMATS = {"mxfp4": B.MXFP4, "nvfp4": B.NVFP4}
 BLOCK = {"mxfp4": 32, "nvfp4": 16}
 _FP32 = torch.float32
-_capturing = torch.cuda.is_current_stream_capturing
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 
 # (input type, output type asked for): their codes, and the output's type
@@ -34,7 +34,7 @@ _TYPES = {(a, b): (_DTYPES[a], _DTYPES[b or a], b or a) for a in _DTYPES for b i
 
 
 def _dual(t) -> bool:
-    """Whether a tensor carries a tangent of forward-mode differentiation."""
+    """Whether a tensor carries a tangent of forward-mode differentiation (asked on every call: no level, no look)."""
     return _forward._current_level >= 0 and _forward.unpack_dual(t).tangent is not None
 
 
