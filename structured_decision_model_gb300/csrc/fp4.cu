@@ -4,8 +4,8 @@
 // sizes, its mean and variance and its codes come from one read of memory.  A lane holds 16
 // consecutive values of every 512: a block of 16 is one lane's and one of 32 two neighbours', so
 // that a scale is worked out once or twice, and the codes' arithmetic runs on pairs (fma.rn.f32x2).
-// Memory bounds it, and with statistics issue slots: 131072 x 4096 bf16 takes 208 us to nvfp4 (6.6 TB/s),
-// 189 to mxfp4 (7.2 TB/s; a plain copy 6.8), 257 and 218 with statistics.  Eight values a lane took 409, 324 and
+// Memory bounds it, and with statistics issue slots: 131072 x 4096 bf16 takes 206 us to nvfp4 (6.6 TB/s),
+// 188 to mxfp4 (7.2 TB/s; a plain copy 6.8), 256 and 216 with statistics, 271 and 228 with sums.  Eight values a lane took 409, 324 and
 // 470 (nvfp4 with statistics); rows of a block tied together by block-wide barriers, and indexes by division, 224, 195
 // and 306; sums and squares apart, and asked for at run time, 294 with statistics.
 #include "fp4.cuh"

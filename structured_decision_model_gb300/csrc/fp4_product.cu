@@ -29,13 +29,16 @@ namespace {
 // The epilogue takes the shared columns first and hands them back at once; from then on the next
 // tile's products run beside the rest of it.
 //
-// Shared memory bounds it: of the 512 cycles that a K tile's four MMAs take, TMA's fills need 304 (nvfp4), the tensor
-// cores' reads 256 and the scales' copies 48.  An MMA's scales are copied before the MMA that comes before it: the copies
+// What bounds it is power, and the MMAs themselves.  Sustained, a K tile takes 613 cycles at 1.62 GHz (nvfp4, K = 16384; mxfp4 597
+// at 1.71), of which its four MMAs are 512; without loads and outputs 595 at 1.96 (578 at 2.07).  Loads cost clock,
+// not cycles: 96.9 us with them, 78.8 without; without outputs 91.4, without copies of scales 96.1 (4864 x 4096 x 16384).
+// An MMA's scales are copied before the MMA that comes before it: the copies
 // run beside that one (all of a K tile's copies before its first MMA left the tensor cores idle: 650 and 609 us instead
 // of 618 and 575; a K tile's last MMA held back behind the next one's first copies: 630 and 588).  131072 x 4096 x 4096
-// to bf16 takes 615 to 622 us (7.1 PFLOP/s; mxfp4 575, 7.65), 4864 x 4096 x 16384 85 us (7.7; mxfp4 80 to 84).  One MMA
+// to bf16 takes 614 to 625 us (7.1 PFLOP/s; mxfp4 578, 7.6), 4864 x 4096 x 16384 89 to 97 us (mxfp4 85 to 89).  One MMA
 // thread in a diverged warp took 1527 us, a second election a K tile or a slower producer 715, hand-over by a releasing
 // arrival (which waits for the last tile's stores) 10 % more; a last round in halves of tiles gained nothing.
+// Outputs of fp32, or of rows that do not start or end on 16 bytes, go out by direct stores (emit).
 template <int FMT>
 struct PairCfg {
     static constexpr int GROUPS = groups_of(FMT);

@@ -241,8 +241,8 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[NC]) {
 // --------------------------------------------------------- one CTA, one tile
 // 128 rows of w x BN rows of x.  Few rows of x leave few tiles, so the K range of a tile is
 // cut among the CTAs of a cluster, which stage their fp32 tiles in their own shared memory
-// and add them in order through distributed shared memory.  Latency bounds it: 4096 x 4096 takes 4.2 us for one
-// row (weights 1.4 us at the copy rate), 5.5 for 64, 6.8 for 128, 7.7 for 256; 16384 x 4096, 24 rows, 7.1 us.
+// and add them in order through distributed shared memory.  Latency bounds it: 4096 x 4096 takes 4.0 us for one
+// row (weights 1.4 us at the copy rate), 5.3 for 64, 6.8 for 128, 7.4 for 256; 16384 x 4096, 24 rows, 6.9 us.
 template <int FMT, int BN>
 struct TileCfg {
     static constexpr int GROUPS = groups_of(FMT);
