@@ -1110,11 +1110,21 @@ int project_fp4(Fp4Call call, const clef_config* cfg, const void* prepared, cons
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const PreparedLayout PL(cfg);
     const int64_t NKV = int64_t(2) * cfg->n_route * cfg->width;
-    return fp4_linear(call, 0, w, dtype, static_cast<const uint16_t*>(hidden) + from * schema->row_stride, schema->row_stride,
-                      int32_t(rows), reinterpret_cast<const float*>(static_cast<const uint8_t*>(prepared) + PL.bkv), sums,
-                      CLEF_BF16, reinterpret_cast<uint16_t*>(ws + L.kv) + to * NKV, NKV,
-                      reinterpret_cast<float*>(ws + L.mu) + to, reinterpret_cast<float*>(ws + L.rstd) + to, scratch,
-                      scratch_bytes, reinterpret_cast<int32_t*>(ws + L.flags), stream);
+    const uint16_t* x = static_cast<const uint16_t*>(hidden) + from * schema->row_stride;
+    if (rows <= kFp4FewRows) {  // in one launch, where that pays
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capture) != cudaSuccess) cudaGetLastError();
+        const bool aligned = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (rows == 1 || schema->row_stride % 8 == 0);
+        size_t need = 1;
+        clef_fp4_linear_scratch(w->format, dtype, int32_t(rows), cfg->hidden, int32_t(NKV), 1, aligned,
+                                capture != cudaStreamCaptureStatusNone, &need);
+        if (need == 0) scratch = nullptr;
+    }
+    return fp4_linear(call, 0, w, dtype, x, schema->row_stride, int32_t(rows),
+                      reinterpret_cast<const float*>(static_cast<const uint8_t*>(prepared) + PL.bkv), sums, CLEF_BF16,
+                      reinterpret_cast<uint16_t*>(ws + L.kv) + to * NKV, NKV, reinterpret_cast<float*>(ws + L.mu) + to,
+                      reinterpret_cast<float*>(ws + L.rstd) + to, scratch, scratch_bytes,
+                      reinterpret_cast<int32_t*>(ws + L.flags), stream);
 }
 
 // Records b .. (the return value) - 1 whose rows follow each other without a gap, in `hidden` and in the

@@ -60,3 +60,36 @@ def test_the_5120_wide_head(form, kept_memory):
     streamed = outputs(head.stream_finish(sch, hidden, ids, lex))
     assert head.device_status() == 0
     assert abs(streamed["logits"] - got["logits"]).max() <= LOGIT_TOL
+
+
+@pytest.mark.parametrize("form", ["mxfp4", "nvfp4"])
+def test_short_chunks_in_one_launch_or_two(form):
+    """A chunk of a few rows by itself goes in one launch, in a graph in two (its rows are long); keys and values are the same."""
+    head, _ = fp4_head("pages", form)
+    bt = batch("pages", [160, 300], 84)
+    hidden, ids, lex = device_inputs(bt, SHAPES["pages"].vocab)
+    sch = schema_of(bt)
+
+    def rows(chunk):
+        before = B.clef_kernel_launches()
+        for b, n in enumerate(bt.lengths):
+            for r in range(0, int(n), chunk):
+                head.stream_rows(sch, hidden, b, r, min(chunk, int(n) - r))
+        return B.clef_kernel_launches() - before
+
+    def finish():
+        out = outputs(head.stream_finish(sch, hidden, ids, lex))
+        assert head.device_status() == 0
+        return out
+
+    head.stream_begin(sch)
+    assert rows(8) == 20 + 38
+    eager = finish()
+    head.stream_begin(sch)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        assert rows(8) == 2 * (20 + 38)
+    g.replay()
+    for k, v in finish().items():
+        assert (v == eager[k]).all()
