@@ -77,12 +77,12 @@ class ClefHead:
             B.clef_fp4_memory_weights(self.cfg, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), stream_handle())
             self.memory_weights = w
 
-    @staticmethod
-    def _row_type(hidden):
-        """The code of the type of rows that are quantised as they are."""
-        code = _ROW_DTYPES.get(hidden.dtype)
-        if code is None or not hidden.is_cuda:
-            raise B.ClefError(1, "hidden: bf16 or fp16 rows on the GPU")
+    def _row_type(self, hidden, half=True):
+        """The code of the rows' type: bf16 (or its bits in integers), or fp16 where ``half``.  Rows that are quantised: on
+        the GPU, and no integers."""
+        code = B.BF16 if not hidden.is_floating_point() and self.memory_weights is None else _ROW_DTYPES.get(hidden.dtype)
+        if code is None or (code == B.FP16 and not half) or (self.memory_weights is not None and not hidden.is_cuda):
+            raise B.ClefError(1, "hidden: bf16 or fp16 rows" if half else "hidden: bf16 rows")
         return code
 
     def _scratch(self, n_bytes, stream):
@@ -120,6 +120,7 @@ class ClefHead:
                                     out.q_argmax.data_ptr(), ws.data_ptr(), ws.numel(), space.data_ptr(), n, debug=debug,
                                     stream=stream_handle(stream), check=check)
             return out
+        self._row_type(hidden, half=False)
         B.clef_head_forward(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), schema, hidden.data_ptr(),
                             token_ids.data_ptr(), lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(),
                             out.q_value.data_ptr(), out.q_conf.data_ptr(), out.q_argmax.data_ptr(), ws.data_ptr(),
@@ -145,7 +146,7 @@ class ClefHead:
             B.clef_stream_rows_fp4(self.cfg, self.prepared.data_ptr(), w.struct, w.sums.data_ptr(), schema, hidden.data_ptr(),
                                    rows, record, row0, n_rows, ws.data_ptr(), ws.numel(), space.data_ptr(), n, stream_handle(stream))
             return
-        fn = B.clef_stream_rows_f16 if hidden.dtype == torch.float16 else B.clef_stream_rows
+        fn = B.clef_stream_rows_f16 if self._row_type(hidden) == B.FP16 else B.clef_stream_rows
         fn(self.cfg, self.prepared.data_ptr(), schema, hidden.data_ptr(), record, row0, n_rows, ws.data_ptr(),
            ws.numel(), stream_handle(stream))
 
@@ -153,7 +154,7 @@ class ClefHead:
                       out: Optional[Outputs] = None, debug=None, stream=None) -> Outputs:
         ws = self._ws
         out = out if out is not None else self.alloc_outputs(schema)
-        fn = B.clef_stream_finish_f16 if hidden.dtype == torch.float16 else B.clef_stream_finish
+        fn = B.clef_stream_finish_f16 if self._row_type(hidden) == B.FP16 else B.clef_stream_finish
         fn(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), schema, hidden.data_ptr(), token_ids.data_ptr(),
            lexical.data_ptr(), out.logits.data_ptr(), out.probs.data_ptr(), out.q_value.data_ptr(),
            out.q_conf.data_ptr(), out.q_argmax.data_ptr(), ws.data_ptr(), ws.numel(), debug=debug,
@@ -191,7 +192,7 @@ class ClefHead:
         with torch.cuda.stream(s):
             n = B.clef_cache_attend_workspace(cache.struct, schema.B, schema.O, self.heads, table.shape[1] * cache.page)
             space = torch.empty(n, dtype=torch.uint8, device=self.device)
-        dtype = B.FP16 if hidden.dtype == torch.float16 else B.BF16
+        dtype = self._row_type(hidden)
         B.clef_stream_finish_memory(self.cfg, self.weight_ptrs, self.prepared.data_ptr(), schema, first_row,
                                     hidden.data_ptr(), dtype, token_ids.data_ptr(), lexical.data_ptr(),
                                     out.logits.data_ptr(), out.probs.data_ptr(), out.q_value.data_ptr(),

@@ -93,3 +93,31 @@ def test_short_chunks_in_one_launch_or_two(form):
     g.replay()
     for k, v in finish().items():
         assert (v == eager[k]).all()
+
+
+@pytest.mark.parametrize("form", [None, "nvfp4"])
+def test_finishing_over_other_types_is_refused(form):
+    """The finish reads rows too, and so does a head in bf16, whose forward pass takes no fp16."""
+    head, _ = fp4_head("narrow", form)
+    bt = batch("narrow", [140, 200], 85)
+    hidden, ids, lex = device_inputs(bt, SHAPES["narrow"].vocab)
+    sch = schema_of(bt)
+    head.stream_begin(sch)
+    for b, n in enumerate(bt.lengths):
+        head.stream_rows(sch, hidden, b, 0, int(n))
+    with pytest.raises(B.ClefError):
+        head.stream_finish(sch, hidden.float(), ids, lex)
+    if form is None:
+        for bad in (hidden.float(), hidden.double(), hidden.half()):
+            with pytest.raises(B.ClefError):
+                head.forward(sch, bad, ids, lex)
+        with pytest.raises(B.ClefError):
+            head.stream_rows(sch, hidden.float(), 0, 0, 10)
+        bits = outputs(head.forward(sch, hidden.view(torch.int16), ids, lex))
+        for k, v in outputs(head.forward(sch, hidden, ids, lex)).items():
+            assert (v == bits[k]).all()
+        head.stream_begin(sch)
+        for b, n in enumerate(bt.lengths):
+            head.stream_rows(sch, hidden, b, 0, int(n))
+    finite = outputs(head.stream_finish(sch, hidden, ids, lex))
+    assert head.device_status() == 0 and abs(finite["logits"]).max() < 100
